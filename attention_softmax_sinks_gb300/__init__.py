@@ -24,7 +24,10 @@ __all__ = [
     "sink_attn_selftest_wait_timeout", "sink_attn_decode_noalloc", "moe_router_topk_softmax",
     "qkv_bias_rope", "qkv_bias_rope_append_paged", "linear_bias", "moe_router", "GPT_OSS_YARN",
     "EXPORTED_SYMBOLS", "qkv_bias_rope_kv", "qkv_bias_rope_append_paged_kv", "sink_attn_prefill_qkv",
-    "sink_attn_prefill_paged_qkv", "sink_attn_decode_qkv",
+    "sink_attn_prefill_paged_qkv", "sink_attn_decode_qkv", "moe_group_rows", "moe_combine",
+    "grouped_linear_bias", "grouped_linear_swiglu", "mxfp4_quantize", "mxfp4_dequantize",
+    "mxfp4_linear_bias", "grouped_mxfp4_linear_bias", "grouped_mxfp4_linear_swiglu",
+    "mxfp4_scale_columns", "GPT_OSS_SWIGLU",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -38,7 +41,9 @@ EXPORTED_SYMBOLS = (
     "sink_attn_decode_noalloc", "moe_router_topk_softmax", "qkv_bias_rope",
     "qkv_bias_rope_append_paged", "linear_bias", "moe_router", "qkv_bias_rope_kv",
     "qkv_bias_rope_append_paged_kv", "sink_attn_prefill_qkv", "sink_attn_prefill_paged_qkv",
-    "sink_attn_decode_qkv",
+    "sink_attn_decode_qkv", "moe_group_rows", "moe_combine",
+    "grouped_linear_bias", "grouped_linear_swiglu", "mxfp4_quantize", "mxfp4_dequantize",
+    "mxfp4_linear_bias", "grouped_mxfp4_linear_bias", "grouped_mxfp4_linear_swiglu",
 )
 
 _p, _i, _f, _d, _ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_double, ctypes.c_longlong
@@ -70,6 +75,15 @@ _SIGNATURES = {
                                          _i, _f, _i, _p, _p, _p]),
     "sink_attn_decode_qkv": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _f, _i, _p, _p,
                                   _p]),
+    "moe_group_rows": (_i, [_p, _i, _i, _i, _p, _p, _p, _p]),
+    "moe_combine": (_i, [_p, _p, _p, _i, _i, _i, _i, _p, _p]),
+    "grouped_linear_bias": (_i, [_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _p, _p]),
+    "grouped_linear_swiglu": (_i, [_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _f, _f, _p, _p]),
+    "mxfp4_quantize": (_i, [_p, _i, _ll, _i, _p, _p, _p]),
+    "mxfp4_dequantize": (_i, [_p, _p, _ll, _i, _p, _p]),
+    "mxfp4_linear_bias": (_i, [_p, _p, _p, _p, _p, _i, _i, _i, _p, _p]),
+    "grouped_mxfp4_linear_bias": (_i, [_p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _p, _p]),
+    "grouped_mxfp4_linear_swiglu": (_i, [_p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _f, _f, _p, _p]),
 }
 
 # YaRN constants of the public GPT-OSS model configuration (the pages name YaRN
@@ -472,6 +486,216 @@ def moe_router(x, w_router, bias, top_k: int, topk_idx=None, topk_weight=None, e
     if expert_counts is not None:
         return topk_idx, topk_weight, expert_counts
     return topk_idx, topk_weight
+
+
+# ----------------------------------------------------------------------------- the expert layer
+# SwiGLU constants of the public GPT-OSS model configuration (the pages name
+# SwiGLU but give no constants).
+GPT_OSS_SWIGLU = dict(alpha=1.702, limit=7.0)
+
+
+def _shape(t, name, *dims):
+    """A tensor of len(dims) dimensions whose sizes equal the dims that are not None."""
+    if t.dim() != len(dims) or any(d is not None and t.shape[i] != d for i, d in enumerate(dims)):
+        want = ", ".join("*" if d is None else str(d) for d in dims)
+        raise ValueError(f"{name} must be [{want}], got {tuple(t.shape)}")
+    return t
+
+
+def moe_group_rows(topk_idx, num_experts: int, expert_offsets=None, row_token=None, pair_row=None,
+                   stream=None):
+    """Sort the (token, expert) pairs of topk_idx [T, k] int32 by expert, stably.
+
+    Returns (expert_offsets int32 [E + 1], row_token int32 [T * k], pair_row int32 [T, k]):
+    expert e owns rows [expert_offsets[e], expert_offsets[e + 1]), row r reads token
+    row_token[r], and pair (t, i) is row pair_row[t, i].  A negative index is a pair without
+    expert (pair_row -1); row_token is -1 behind the last row."""
+    dev, di = _checked((("topk_idx", topk_idx, torch.int32),))
+    _shape(topk_idx, "topk_idx", None, None)
+    t, k = topk_idx.shape
+    e = int(num_experts)
+    expert_offsets = (torch.empty((max(e, 0) + 1,), dtype=torch.int32, device=dev) if expert_offsets is None
+                      else _out(expert_offsets, "expert_offsets", torch.int32, (e + 1,), di))
+    row_token = (torch.empty((t * k,), dtype=torch.int32, device=dev) if row_token is None
+                 else _out(row_token, "row_token", torch.int32, (t * k,), di))
+    pair_row = (torch.empty((t, k), dtype=torch.int32, device=dev) if pair_row is None
+                else _out(pair_row, "pair_row", torch.int32, (t, k), di))
+    st = _call(load_library().moe_group_rows, di, stream, _ptr(topk_idx), t, k, e, _ptr(expert_offsets),
+               _ptr(row_token), _ptr(pair_row))
+    _check(st, "moe_group_rows")
+    return expert_offsets, row_token, pair_row
+
+
+def moe_combine(y, pair_row, topk_weight, out=None, stream=None):
+    """out[t] = sum_i topk_weight[t, i] * y[pair_row[t, i]]: y [R, H] bf16, pair_row [T, k]
+    int32 (-1 adds nothing), topk_weight [T, k] bf16.  Returns out [T, H] bf16."""
+    dev, di = _checked((("y", y, torch.bfloat16), ("pair_row", pair_row, torch.int32),
+                        ("topk_weight", topk_weight, torch.bfloat16)))
+    _same_device(di, ("pair_row", pair_row), ("topk_weight", topk_weight))
+    _shape(y, "y", None, None)
+    _shape(pair_row, "pair_row", None, None)
+    t, k = pair_row.shape
+    _shape(topk_weight, "topk_weight", t, k)
+    r, h = y.shape
+    out = (torch.empty((t, h), dtype=torch.bfloat16, device=dev) if out is None
+           else _out(out, "out", torch.bfloat16, (t, h), di))
+    st = _call(load_library().moe_combine, di, stream, _ptr(y), _ptr(pair_row), _ptr(topk_weight), r, t, k, h,
+               _ptr(out))
+    _check(st, "moe_combine")
+    return out
+
+
+def _given(x_scales):
+    """x_scales, which tells _grouped that the operands are MXFP4."""
+    if x_scales is None:
+        raise TypeError("x_scales must be a CUDA tensor")
+    return x_scales
+
+
+def _grouped(where, x, x_scales, w, w_scales, expert_offsets, bias, row_token, out, stream, act=None):
+    """The grouped products: x [X, K] and w [E, N, K] in bf16, or as MXFP4 codes and scales."""
+    mx = x_scales is not None
+    dt = torch.uint8 if mx else torch.bfloat16
+    named = [("x_codes", x, dt), ("x_scales", x_scales, dt), ("w_codes", w, dt), ("w_scales", w_scales, dt)] \
+        if mx else [("x", x, dt), ("w", w, dt)]
+    named.append(("expert_offsets", expert_offsets, torch.int32))
+    dev, di = _checked(named)
+    _opt((("bias", bias, torch.bfloat16), ("row_token", row_token, torch.int32)))
+    _same_device(di, *[(name, t) for name, t, _ in named], ("bias", bias), ("row_token", row_token))
+    _shape(x, named[0][0], None, None)
+    x_rows, kx = x.shape
+    _shape(w, "w_codes" if mx else "w", None, None, kx)
+    e, n, _ = w.shape
+    k = 2 * kx if mx else kx
+    if mx:
+        s = mxfp4_scale_columns(k)
+        _shape(x_scales, "x_scales", x_rows, s)
+        _shape(w_scales, "w_scales", e, n, s)
+    _shape(expert_offsets, "expert_offsets", e + 1)
+    if bias is not None:
+        _shape(bias, "bias", e, n)
+    if row_token is not None:
+        _shape(row_token, "row_token", None)
+    rows = x_rows if row_token is None else row_token.shape[0]
+    n_out = n if act is None else n // 2
+    out = (torch.empty((rows, n_out), dtype=torch.bfloat16, device=dev) if out is None
+           else _out(out, "out", torch.bfloat16, (rows, n_out), di))
+    operands = (_ptr(x), _ptr(x_scales), _ptr(w), _ptr(w_scales)) if mx else (_ptr(x), _ptr(w))
+    st = _call(getattr(load_library(), where), di, stream, *operands, _ptr(bias), _ptr(expert_offsets),
+               _ptr(row_token), x_rows, rows, e, n, k, *(act or ()), _ptr(out))
+    _check(st, where)
+    return out
+
+
+def grouped_linear_bias(x, w, expert_offsets, bias=None, row_token=None, out=None, stream=None):
+    """One linear layer per expert on its ragged group of rows, on the tcgen05 tensor cores.
+
+    x [X, K] bf16, w [E, N, K] bf16, expert_offsets [E + 1] int32, bias [E, N] bf16 or None;
+    row r of expert e gives out[r] = x[row_token[r]] @ w[e]^T + bias[e] (row_token None: x[r]).
+    Returns out [R, N] bf16; rows outside every group are left as they were (uninitialised
+    when ``out`` is not given)."""
+    return _grouped("grouped_linear_bias", x, None, w, None, expert_offsets, bias, row_token, out, stream)
+
+
+def grouped_linear_swiglu(x, w, expert_offsets, bias=None, row_token=None,
+                          alpha: float = GPT_OSS_SWIGLU["alpha"], limit: float = GPT_OSS_SWIGLU["limit"],
+                          out=None, stream=None):
+    """grouped_linear_bias followed by the clamped SwiGLU on interleaved gate (even) and up
+    (odd) features, before the one rounding to bf16: g * sigmoid(alpha g) * (u + 1) with
+    g = min(gate, limit), u = clamp(up, -limit, limit).  Returns out [R, N / 2] bf16."""
+    return _grouped("grouped_linear_swiglu", x, None, w, None, expert_offsets, bias, row_token, out, stream,
+                    act=(float(alpha), float(limit)))
+
+
+# ----------------------------------------------------------------------------- MXFP4
+def mxfp4_scale_columns(k: int) -> int:
+    """Scale bytes per row of a K-wide MXFP4 matrix: K / 32 rounded up to a multiple of 16."""
+    return (int(k) // 32 + 15) // 16 * 16
+
+
+def mxfp4_quantize(x, codes=None, scales=None, stream=None):
+    """Quantise x [..., K] (bf16 or fp32, K a multiple of 32) to MXFP4: blocks of 32 values
+    share the scale 2^(floor(log2 max|x|) - 2), values round to the nearest E2M1 (ties to
+    even, at most 6).  Returns (codes uint8 [..., K / 2], scales uint8
+    [..., mxfp4_scale_columns(K)])."""
+    dev, di = _checked((("x", x, torch.float32 if isinstance(x, torch.Tensor) and x.dtype == torch.float32
+                         else torch.bfloat16),))
+    if x.dim() < 1:
+        raise ValueError("x must have at least one dimension")
+    k = x.shape[-1]
+    lead = tuple(x.shape[:-1])
+    rows = 1
+    for d in lead:
+        rows *= d
+    codes = (torch.empty((*lead, k // 2), dtype=torch.uint8, device=dev) if codes is None
+             else _out(codes, "codes", torch.uint8, (*lead, k // 2), di))
+    s = mxfp4_scale_columns(k)
+    scales = (torch.empty((*lead, s), dtype=torch.uint8, device=dev) if scales is None
+              else _out(scales, "scales", torch.uint8, (*lead, s), di))
+    st = _call(load_library().mxfp4_quantize, di, stream, _ptr(x), int(x.dtype == torch.float32), rows, k,
+               _ptr(codes), _ptr(scales))
+    _check(st, "mxfp4_quantize")
+    return codes, scales
+
+
+def mxfp4_dequantize(codes, scales, out=None, stream=None):
+    """The bf16 values [..., K] of MXFP4 codes [..., K / 2] and scales (as mxfp4_quantize
+    returns them)."""
+    dev, di = _checked((("codes", codes, torch.uint8), ("scales", scales, torch.uint8)))
+    _same_device(di, ("scales", scales))
+    if codes.dim() < 1:
+        raise ValueError("codes must have at least one dimension")
+    lead = tuple(codes.shape[:-1])
+    k = 2 * codes.shape[-1]
+    _shape(scales, "scales", *lead, mxfp4_scale_columns(k))
+    rows = 1
+    for d in lead:
+        rows *= d
+    out = (torch.empty((*lead, k), dtype=torch.bfloat16, device=dev) if out is None
+           else _out(out, "out", torch.bfloat16, (*lead, k), di))
+    st = _call(load_library().mxfp4_dequantize, di, stream, _ptr(codes), _ptr(scales), rows, k, _ptr(out))
+    _check(st, "mxfp4_dequantize")
+    return out
+
+
+def mxfp4_linear_bias(x_codes, x_scales, w_codes, w_scales, bias=None, out=None, stream=None):
+    """linear_bias with both operands in MXFP4 (block-scaled tcgen05 products): x [M, K] and
+    w [N, K] as codes [., K / 2] and scales, bias [N] bf16 or None.  Returns [M, N] bf16."""
+    dev, di = _checked((("x_codes", x_codes, torch.uint8), ("x_scales", x_scales, torch.uint8),
+                        ("w_codes", w_codes, torch.uint8), ("w_scales", w_scales, torch.uint8)))
+    _opt((("bias", bias, torch.bfloat16),))
+    _same_device(di, ("x_scales", x_scales), ("w_codes", w_codes), ("w_scales", w_scales), ("bias", bias))
+    _shape(x_codes, "x_codes", None, None)
+    m, half = x_codes.shape
+    _shape(w_codes, "w_codes", None, half)
+    n, k = w_codes.shape[0], 2 * half
+    s = mxfp4_scale_columns(k)
+    _shape(x_scales, "x_scales", m, s)
+    _shape(w_scales, "w_scales", n, s)
+    if bias is not None:
+        _shape(bias, "bias", n)
+    out = (torch.empty((m, n), dtype=torch.bfloat16, device=dev) if out is None
+           else _out(out, "out", torch.bfloat16, (m, n), di))
+    st = _call(load_library().mxfp4_linear_bias, di, stream, _ptr(x_codes), _ptr(x_scales), _ptr(w_codes),
+               _ptr(w_scales), _ptr(bias), m, n, k, _ptr(out))
+    _check(st, "mxfp4_linear_bias")
+    return out
+
+
+def grouped_mxfp4_linear_bias(x_codes, x_scales, w_codes, w_scales, expert_offsets, bias=None, row_token=None,
+                              out=None, stream=None):
+    """grouped_linear_bias with both operands in MXFP4: x [X, K] and w [E, N, K] as codes
+    [., K / 2] and scales (row_token gathers rows of both)."""
+    return _grouped("grouped_mxfp4_linear_bias", x_codes, _given(x_scales), w_codes, w_scales, expert_offsets, bias,
+                    row_token, out, stream)
+
+
+def grouped_mxfp4_linear_swiglu(x_codes, x_scales, w_codes, w_scales, expert_offsets, bias=None, row_token=None,
+                                alpha: float = GPT_OSS_SWIGLU["alpha"], limit: float = GPT_OSS_SWIGLU["limit"],
+                                out=None, stream=None):
+    """grouped_linear_swiglu with both operands in MXFP4."""
+    return _grouped("grouped_mxfp4_linear_swiglu", x_codes, _given(x_scales), w_codes, w_scales, expert_offsets,
+                    bias, row_token, out, stream, act=(float(alpha), float(limit)))
 
 
 # ----------------------------------------------------------------------------- q rotated on chip

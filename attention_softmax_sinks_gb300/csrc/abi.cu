@@ -13,7 +13,9 @@
 #include <cuda_runtime.h>
 
 #include "../../include/linear_bias.h"
+#include "../../include/moe_experts.h"
 #include "../../include/moe_router.h"
+#include "../../include/mxfp4.h"
 #include "../../include/qkv_rope.h"
 #include "../../include/sink_attn.h"
 #include "internal.h"
@@ -92,6 +94,43 @@ sa_status map_matrix(CUtensorMap* m, const void* base, long long rows, long long
   CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides,
                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? SA_OK : SA_ERR_CUDA;
+}
+
+// Expert weights [experts, n, row_bytes] read in boxes of 128 bytes x 128 features; `pair` of
+// them interleaved (2: gate and up features of one output, addressed by the second coordinate).
+sa_status map_experts(CUtensorMap* m, const void* base, long long experts, long long n, long long row_bytes,
+                      int pair, bool bytes) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc;
+  if (sa_status s = encoder(&enc)) return s;
+  const int size = bytes ? 1 : 2;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(row_bytes / size), static_cast<cuuint64_t>(pair),
+                        static_cast<cuuint64_t>(n / pair), static_cast<cuuint64_t>(experts)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(row_bytes) * pair,
+                           static_cast<cuuint64_t>(row_bytes) * n};
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(128 / size), 1, sa::kGroupedFeatures, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = enc(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                   const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? SA_OK : SA_ERR_CUDA;
+}
+
+// Rows [rows, row_bytes] read in boxes of 128 bytes x box_rows (1 for gathers of single rows).
+sa_status map_rows(CUtensorMap* m, const void* base, long long rows, long long row_bytes, int box_rows,
+                   bool bytes) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc;
+  if (sa_status s = encoder(&enc)) return s;
+  const int size = bytes ? 1 : 2;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes / size), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / size), static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = enc(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                   const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? SA_OK : SA_ERR_CUDA;
 }
 
@@ -245,6 +284,74 @@ sa_status rope_common(const void* qkv, const void* bias, const int32_t* cu_q, co
   a.status = status;
   a.timeout_ns = g_timeout_ns;
   return sa::launch_rope(a, stream) == cudaSuccess ? SA_OK : SA_ERR_LAUNCH;
+}
+
+struct GroupedCall {
+  const void *x, *x_scales, *w, *w_scales, *bias;  // scales: MXFP4 only
+  const int32_t *offsets, *row_token;
+  int x_rows, rows, experts, n, k;
+  void* out;
+  bool mxfp4, grouped, swiglu;
+  float alpha, limit;
+};
+
+// Row stride of MXFP4 scales: one byte per 32 values, rows padded to 16 bytes.
+int mxfp4_scale_stride(int k) { return (k / 32 + 15) / 16 * 16; }
+
+sa_status grouped_common(const GroupedCall& c, cudaStream_t stream) {
+  if (c.rows < 0 || c.x_rows < 0 || c.n <= 0 || c.k <= 0 || c.n > (1 << 30) || c.k > (1 << 30))
+    return SA_ERR_SHAPE;
+  if (c.experts < 1 || c.experts > sa::kMaxExperts) return SA_ERR_SHAPE;
+  if (c.swiglu && (c.n % 2 != 0 || !std::isfinite(c.alpha) || !(c.limit > 0.0f))) return SA_ERR_SHAPE;
+  if (c.k % (c.mxfp4 ? 32 : 8) != 0) return SA_ERR_UNSUPPORTED;
+  if (c.rows == 0) return SA_OK;
+  if (!c.x || !c.w || !c.out || (c.grouped && !c.offsets)) return SA_ERR_NULL;
+  if (c.mxfp4 && (!c.x_scales || !c.w_scales)) return SA_ERR_NULL;
+  if (c.row_token ? c.x_rows == 0 : c.x_rows != c.rows) return SA_ERR_SHAPE;
+  if (!aligned16(c.x) || !aligned16(c.w) || !aligned16(c.x_scales) || !aligned16(c.w_scales) ||
+      (reinterpret_cast<uintptr_t>(c.bias) & 1u) || (reinterpret_cast<uintptr_t>(c.out) & 1u))
+    return SA_ERR_ALIGNMENT;
+  sa::GroupedArgs a{};
+  a.n_out = c.swiglu ? c.n / 2 : c.n;
+  const long long blocks_f = (static_cast<long long>(a.n_out) + sa::kGroupedFeatures - 1) / sa::kGroupedFeatures;
+  if ((c.rows / 96LL + c.experts + 1) * blocks_f >= (1LL << 30)) return SA_ERR_SHAPE;
+  const int sms = sm_count();
+  const long long groups = c.experts < c.rows ? c.experts : c.rows;
+  const long long most_rows = c.rows / sa::grouped_tile_rows(c.mxfp4) + groups;
+  // two plain sub-tiles per tile, unless that leaves SMs without a tile
+  a.subs = c.swiglu || most_rows * ((blocks_f + 1) / 2) >= sms ? 2 : 1;
+  a.tiles_f = static_cast<int>(c.swiglu ? blocks_f : (blocks_f + a.subs - 1) / a.subs);
+  unsigned* status = nullptr;
+  if (sa_status s = status_ptr(&status)) return s;
+  a.bias = static_cast<const uint16_t*>(c.bias);
+  a.out = static_cast<uint16_t*>(c.out);
+  a.offsets = c.offsets;
+  a.row_token = c.row_token;
+  a.x_scales = static_cast<const uint8_t*>(c.x_scales);
+  a.w_scales = static_cast<const uint8_t*>(c.w_scales);
+  a.scale_stride = mxfp4_scale_stride(c.k);
+  a.x_rows = c.x_rows;
+  a.rows = c.rows;
+  a.num_experts = c.experts;
+  a.N = c.n;
+  a.K = c.k;
+  a.swiglu = c.swiglu ? 1 : 0;
+  a.alpha = c.alpha;
+  a.limit = c.limit;
+  a.status = status;
+  a.timeout_ns = g_timeout_ns;
+  const long long row_bytes = c.mxfp4 ? c.k / 2 : 2LL * c.k;
+  CUtensorMap wm, xm;
+  if (sa_status s = map_experts(&wm, c.w, c.experts, c.n, row_bytes, c.swiglu ? 2 : 1, c.mxfp4)) return s;
+  if (sa_status s = map_rows(&xm, c.x, c.x_rows, row_bytes, c.row_token ? 1 : 16, c.mxfp4)) return s;
+  return sa::launch_grouped(wm, xm, a, c.mxfp4, sms, stream) == cudaSuccess ? SA_OK : SA_ERR_LAUNCH;
+}
+
+sa_status check_mxfp4(long long rows, int k) {
+  if (rows < 0 || k <= 0 || k > (1 << 30)) return SA_ERR_SHAPE;
+  if (k % 32 != 0) return SA_ERR_UNSUPPORTED;
+  if (rows >= (1LL << 40) / k) return SA_ERR_SHAPE;
+  return SA_OK;
 }
 
 }  // namespace
@@ -672,6 +779,111 @@ sa_status qkv_bias_rope_append_paged_kv(const void* qkv, const void* bias,
                      num_kv_heads, head_dim, rope_base, factor, orig_len, beta_fast, beta_slow,
                      nullptr, paged_k, paged_v, page_table, max_pages, num_pages, true, stream, true,
                      rope_table);
+}
+
+sa_status moe_group_rows(const int32_t* topk_idx, int num_tokens, int top_k, int num_experts,
+                         int32_t* expert_offsets, int32_t* row_token, int32_t* pair_row,
+                         cudaStream_t stream) {
+  if (num_tokens < 0 || num_experts < 1 || num_experts > sa::kMaxExperts) return SA_ERR_SHAPE;
+  if (top_k < 1 || top_k > 8) return SA_ERR_SHAPE;
+  if (static_cast<long long>(num_tokens) * top_k > (1LL << 30)) return SA_ERR_SHAPE;
+  if (!expert_offsets) return SA_ERR_NULL;
+  if (num_tokens > 0 && (!topk_idx || !row_token || !pair_row)) return SA_ERR_NULL;
+  unsigned* status = nullptr;
+  if (sa_status s = status_ptr(&status)) return s;
+  sa::GroupRowsArgs a{topk_idx, expert_offsets, row_token, pair_row, num_tokens * top_k, top_k, num_experts, status};
+  return sa::launch_group_rows(a, stream) == cudaSuccess ? SA_OK : SA_ERR_LAUNCH;
+}
+
+sa_status moe_combine(const void* y, const int32_t* pair_row, const void* topk_weight,
+                      int num_rows, int num_tokens, int top_k, int hidden, void* out,
+                      cudaStream_t stream) {
+  if (num_tokens < 0 || num_rows < 0 || hidden <= 0 || hidden > (1 << 30)) return SA_ERR_SHAPE;
+  if (top_k < 1 || top_k > 8) return SA_ERR_SHAPE;
+  if (static_cast<long long>(num_tokens) * hidden >= (1LL << 40)) return SA_ERR_SHAPE;
+  if (hidden % 8 != 0) return SA_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return SA_OK;
+  if ((!y && num_rows > 0) || !pair_row || !topk_weight || !out) return SA_ERR_NULL;
+  if (!aligned16(y) || !aligned16(out)) return SA_ERR_ALIGNMENT;
+  unsigned* status = nullptr;
+  if (sa_status s = status_ptr(&status)) return s;
+  sa::CombineArgs a{static_cast<const uint16_t*>(y), pair_row, static_cast<const uint16_t*>(topk_weight),
+                    static_cast<uint16_t*>(out), num_rows, num_tokens, top_k, hidden, status};
+  return sa::launch_combine(a, sm_count(), stream) == cudaSuccess ? SA_OK : SA_ERR_LAUNCH;
+}
+
+sa_status grouped_linear_bias(const void* x, const void* w, const void* bias,
+                              const int32_t* expert_offsets, const int32_t* row_token, int x_rows,
+                              int rows, int num_experts, int n, int k, void* out,
+                              cudaStream_t stream) {
+  return grouped_common({x, nullptr, w, nullptr, bias, expert_offsets, row_token, x_rows, rows, num_experts, n, k,
+                         out, false, true, false, 0.0f, 0.0f}, stream);
+}
+
+sa_status grouped_linear_swiglu(const void* x, const void* w, const void* bias,
+                                const int32_t* expert_offsets, const int32_t* row_token,
+                                int x_rows, int rows, int num_experts, int n, int k, float alpha,
+                                float limit, void* out, cudaStream_t stream) {
+  return grouped_common({x, nullptr, w, nullptr, bias, expert_offsets, row_token, x_rows, rows, num_experts, n, k,
+                         out, false, true, true, alpha, limit}, stream);
+}
+
+sa_status mxfp4_quantize(const void* x, int is_fp32, long long rows, int k, void* codes,
+                         void* scales, cudaStream_t stream) {
+  if (sa_status s = check_mxfp4(rows, k)) return s;
+  if (rows == 0) return SA_OK;
+  if (!x || !codes || !scales) return SA_ERR_NULL;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return SA_ERR_ALIGNMENT;
+  sa::Mxfp4Args a{};
+  a.in = x;
+  a.codes = static_cast<uint8_t*>(codes);
+  a.scales = static_cast<uint8_t*>(scales);
+  a.rows = rows;
+  a.k = k;
+  a.stride = mxfp4_scale_stride(k);
+  a.is_fp32 = is_fp32 ? 1 : 0;
+  return sa::launch_mxfp4_quantize(a, sm_count(), stream) == cudaSuccess ? SA_OK : SA_ERR_LAUNCH;
+}
+
+sa_status mxfp4_dequantize(const void* codes, const void* scales, long long rows, int k,
+                           void* out, cudaStream_t stream) {
+  if (sa_status s = check_mxfp4(rows, k)) return s;
+  if (rows == 0) return SA_OK;
+  if (!codes || !scales || !out) return SA_ERR_NULL;
+  if (!aligned16(codes) || !aligned16(scales) || !aligned16(out)) return SA_ERR_ALIGNMENT;
+  sa::Mxfp4Args a{};
+  a.in = codes;
+  a.scales = static_cast<uint8_t*>(const_cast<void*>(scales));
+  a.out = static_cast<uint16_t*>(out);
+  a.rows = rows;
+  a.k = k;
+  a.stride = mxfp4_scale_stride(k);
+  return sa::launch_mxfp4_dequantize(a, sm_count(), stream) == cudaSuccess ? SA_OK : SA_ERR_LAUNCH;
+}
+
+sa_status mxfp4_linear_bias(const void* x_codes, const void* x_scales, const void* w_codes,
+                            const void* w_scales, const void* bias, int m, int n, int k, void* out,
+                            cudaStream_t stream) {
+  return grouped_common({x_codes, x_scales, w_codes, w_scales, bias, nullptr, nullptr, m, m, 1, n, k, out, true,
+                         false, false, 0.0f, 0.0f}, stream);
+}
+
+sa_status grouped_mxfp4_linear_bias(const void* x_codes, const void* x_scales, const void* w_codes,
+                                    const void* w_scales, const void* bias,
+                                    const int32_t* expert_offsets, const int32_t* row_token,
+                                    int x_rows, int rows, int num_experts, int n, int k, void* out,
+                                    cudaStream_t stream) {
+  return grouped_common({x_codes, x_scales, w_codes, w_scales, bias, expert_offsets, row_token, x_rows, rows,
+                         num_experts, n, k, out, true, true, false, 0.0f, 0.0f}, stream);
+}
+
+sa_status grouped_mxfp4_linear_swiglu(const void* x_codes, const void* x_scales,
+                                      const void* w_codes, const void* w_scales, const void* bias,
+                                      const int32_t* expert_offsets, const int32_t* row_token,
+                                      int x_rows, int rows, int num_experts, int n, int k,
+                                      float alpha, float limit, void* out, cudaStream_t stream) {
+  return grouped_common({x_codes, x_scales, w_codes, w_scales, bias, expert_offsets, row_token, x_rows, rows,
+                         num_experts, n, k, out, true, true, true, alpha, limit}, stream);
 }
 
 }  // extern "C"
