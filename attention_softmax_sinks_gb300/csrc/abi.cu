@@ -97,20 +97,18 @@ sa_status map_matrix(CUtensorMap* m, const void* base, long long rows, long long
   return r == CUDA_SUCCESS ? SA_OK : SA_ERR_CUDA;
 }
 
-// Expert weights [experts, n, row_bytes] read in boxes of 128 bytes x 128 features; `pair` of
-// them interleaved (2: gate and up features of one output, addressed by the second coordinate).
+// Expert weights [experts, n, row_bytes] read in boxes of 128 bytes x 128 features.
 sa_status map_experts(CUtensorMap* m, const void* base, long long experts, long long n, long long row_bytes,
-                      int pair, bool bytes) {
+                      bool bytes) {
   PFN_cuTensorMapEncodeTiled_v12000 enc;
   if (sa_status s = encoder(&enc)) return s;
   const int size = bytes ? 1 : 2;
-  cuuint64_t dims[4] = {static_cast<cuuint64_t>(row_bytes / size), static_cast<cuuint64_t>(pair),
-                        static_cast<cuuint64_t>(n / pair), static_cast<cuuint64_t>(experts)};
-  cuuint64_t strides[3] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(row_bytes) * pair,
-                           static_cast<cuuint64_t>(row_bytes) * n};
-  cuuint32_t box[4] = {static_cast<cuuint32_t>(128 / size), 1, sa::kGroupedFeatures, 1};
-  cuuint32_t estr[4] = {1, 1, 1, 1};
-  CUresult r = enc(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(row_bytes / size), static_cast<cuuint64_t>(n),
+                        static_cast<cuuint64_t>(experts)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(row_bytes) * n};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / size), sa::kGroupedFeatures, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
                    const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -313,14 +311,10 @@ sa_status grouped_common(const GroupedCall& c, cudaStream_t stream) {
     return SA_ERR_ALIGNMENT;
   sa::GroupedArgs a{};
   a.n_out = c.swiglu ? c.n / 2 : c.n;
-  const long long blocks_f = (static_cast<long long>(a.n_out) + sa::kGroupedFeatures - 1) / sa::kGroupedFeatures;
-  if ((c.rows / 96LL + c.experts + 1) * blocks_f >= (1LL << 30)) return SA_ERR_SHAPE;
-  const int sms = sm_count();
-  const long long groups = c.experts < c.rows ? c.experts : c.rows;
-  const long long most_rows = c.rows / sa::grouped_tile_rows(c.mxfp4) + groups;
-  // two plain sub-tiles per tile, unless that leaves SMs without a tile
-  a.subs = c.swiglu || most_rows * ((blocks_f + 1) / 2) >= sms ? 2 : 1;
-  a.tiles_f = static_cast<int>(c.swiglu ? blocks_f : (blocks_f + a.subs - 1) / a.subs);
+  a.cap = sa::grouped_tile_rows(c.mxfp4, c.rows, c.experts);
+  const long long tiles_f = (static_cast<long long>(c.n) + sa::kGroupedFeatures - 1) / sa::kGroupedFeatures;
+  if ((c.rows / 64LL + c.experts) * tiles_f >= (1LL << 30)) return SA_ERR_SHAPE;
+  a.tiles_f = static_cast<int>(tiles_f);
   unsigned* status = nullptr;
   if (sa_status s = status_ptr(&status)) return s;
   a.bias = static_cast<const uint16_t*>(c.bias);
@@ -342,9 +336,9 @@ sa_status grouped_common(const GroupedCall& c, cudaStream_t stream) {
   a.timeout_ns = g_timeout_ns;
   const long long row_bytes = c.mxfp4 ? c.k / 2 : 2LL * c.k;
   CUtensorMap wm, xm;
-  if (sa_status s = map_experts(&wm, c.w, c.experts, c.n, row_bytes, c.swiglu ? 2 : 1, c.mxfp4)) return s;
+  if (sa_status s = map_experts(&wm, c.w, c.experts, c.n, row_bytes, c.mxfp4)) return s;
   if (sa_status s = map_rows(&xm, c.x, c.x_rows, row_bytes, c.row_token ? 1 : 16, c.mxfp4)) return s;
-  return sa::launch_grouped(wm, xm, a, c.mxfp4, sms, stream) == cudaSuccess ? SA_OK : SA_ERR_LAUNCH;
+  return sa::launch_grouped(wm, xm, a, c.mxfp4, sm_count(), stream) == cudaSuccess ? SA_OK : SA_ERR_LAUNCH;
 }
 
 sa_status check_mxfp4(long long rows, int k) {

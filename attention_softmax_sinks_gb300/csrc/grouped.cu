@@ -5,23 +5,24 @@
 //
 // Orientation.  The group sizes are ragged and often tiny (a decode step gives an expert one
 // or two rows), while the features are many and fixed, so the weights are the A operand (M =
-// 128 features per MMA) and the rows the B operand, whose N is chosen per tile: a tile of n
-// rows issues MMAs of N = n rounded up to 16 and loads only those rows.  Transposed this way
-// no tensor work is padded beyond 16 rows, and one kernel serves one row and thousands.
+// 128 features) and the rows the B operand, whose N is chosen per tile: a tile of n rows
+// issues MMAs of N = n rounded up to 16 and loads only those rows.  Transposed this way no
+// tensor work is padded beyond 16 rows, and one kernel serves one row and thousands.
 //
-// A tile is two 128-feature sub-tiles (the gate and the up features of the same 128 outputs
-// with SwiGLU: a thread then holds both in its own TMEM lane) by up to kRows rows, so each
-// staged row feeds 256 features.  Persistent kernel, one CTA per SM, 384 threads:
-//   warp 0        producer: the sub-tiles' weight boxes (128 features x 128 bytes) and the
-//                 rows, gathered four per TMA instruction by their indices (a lane keeps the
-//                 four indices it issues) or in boxes of 16 consecutive rows; 128-byte
-//                 swizzle, into a kStages-deep ring
+// A tile is 128 features by up to `cap` rows.  Persistent kernel, one CTA per SM, 512 threads:
+//   warp 0        loads the weights of a ring stage (one box of 128 features x 128 bytes of K,
+//                 128-byte swizzle) when it is free
 //   warp 1        TMEM owner and MMA issuer (one elected thread): 32 bytes of K per MMA
-//   warp 2        MXFP4: reads the scale bytes (16 per row: two stages), writes them into the
-//                 ring in the layout that tcgen05.cp spreads over TMEM (row r of a block of
-//                 128: 4 bytes at 16 (r % 32) + 4 (r / 32), 512 bytes per 128 values of K)
+//   warps 2, 3    MXFP4: scale bytes of the weights (2) and of the rows (3): 16 bytes per row
+//                 serve two stages, written into the ring in the layout that tcgen05.cp
+//                 spreads over TMEM (row r of a block of 128: 4 bytes at 16 (r % 32) + 4 (r / 32),
+//                 512 bytes per 128 values of K)
 //   warps 4..11   epilogue: thread = one feature (TMEM lane), columns = rows; bias and
-//                 activation in fp32, one rounding; a warp writes 64 consecutive bytes per row
+//                 activation in fp32, one rounding; a warp writes 64 consecutive bytes per row.
+//                 SwiGLU: gate and up are neighbouring lanes, which exchange half of their
+//                 columns so that each finishes 16 of every 32
+//   warps 12..15  the rows of a stage: four per TMA gather by their indices (a lane keeps the
+//                 indices it issues), or boxes of 16 consecutive rows
 // Two TMEM accumulators alternate, so the epilogue of a tile overlaps the next tile's MMAs.
 //
 // Tiles are numbered by expert, then feature tile, then row tile: the row tiles of one weight
@@ -39,44 +40,65 @@ namespace {
 
 constexpr int kFeat = kGroupedFeatures;
 constexpr int kStageKBytes = 128;  // bytes of K per ring stage: 64 bf16 or 256 E2M1 values
-constexpr int kThreads = 384;
 constexpr int kEpiWarp0 = 4;
 constexpr int kEpiWarps = 8;
+constexpr int kRowWarp0 = kEpiWarp0 + kEpiWarps;
+constexpr int kRowWarps = 4;
+constexpr int kMaxProducers = 3 + kRowWarps;  // weights, rows, and in MXFP4 two warps of scales
+constexpr int kThreads = 32 * (kRowWarp0 + kRowWarps);
+constexpr int kMaxStages = 8;
+constexpr int kRingBytes = 200 * 1024;
+constexpr int kWBytes = kFeat * kStageKBytes;
+constexpr int kSfBlock = 512;  // scales of 128 rows x 128 values of K
 constexpr unsigned long long kDrainTimeoutNs = 2000000000ull;
 
 template <bool kFp4>
 struct GrpCfg {
-  // 4 accumulators of kRows columns (two buffers of two sub-tiles), MXFP4 scales beside them
-  static constexpr int kRows = kFp4 ? 112 : 128;
-  static constexpr int kSubBytes = kFeat * kStageKBytes;
-  static constexpr int kWBytes = 2 * kSubBytes;
-  static constexpr int kXBytes = kRows * kStageKBytes;
-  static constexpr int kSfBlock = 512;                         // 128 rows x 4 scale bytes
-  static constexpr int kSfBytes = kFp4 ? 2 * 3 * kSfBlock : 0;  // per 128 values of K: two weight blocks, one of rows
-  static constexpr int kStageBytes = kWBytes + kXBytes + kSfBytes;
-  static constexpr int kStages = 4;
+  // two accumulators of kRows columns; in MXFP4 two stages' scales beside them
+  static constexpr int kRows = kFp4 ? 224 : 256;
   static constexpr int kStageK = kFp4 ? 256 : 64;
+  static constexpr int kSfBytes = kFp4 ? 2 * 3 * kSfBlock : 0;  // per 128 values of K: a block of weights, two of rows
+  static constexpr int kSfCols = 24;
   static constexpr int kTmemCols = 512;
-  static_assert(kStageBytes % 1024 == 0 && kXBytes % 1024 == 0, "stages keep the swizzle atom's alignment");
-  static_assert(4 * kRows + (kFp4 ? 2 * 24 : 0) <= kTmemCols, "TMEM holds 512 columns");
+  static constexpr int kProducers = 1 + kRowWarps + (kFp4 ? 2 : 0);
+  static_assert(2 * kRows + (kFp4 ? 2 * kSfCols : 0) <= kTmemCols, "TMEM holds 512 columns");
 };
 
+// A stage holds kWBytes of weights, cap rows of 128 bytes, and the scales.  cap is a multiple
+// of 32, so every part starts on a multiple of 1024 bytes (the swizzle atom) but the scales.
+template <bool kFp4>
+__host__ __device__ constexpr int stage_bytes(int cap) {
+  return (kWBytes + cap * kStageKBytes + GrpCfg<kFp4>::kSfBytes + 1023) / 1024 * 1024;
+}
+template <bool kFp4>
+__host__ __device__ constexpr int stage_count(int cap) {
+  return kRingBytes / stage_bytes<kFp4>(cap) < kMaxStages ? kRingBytes / stage_bytes<kFp4>(cap) : kMaxStages;
+}
+
 struct GrpShared {
-  uint64_t full[8], empty[8], sf_full[8], acc_full[2], acc_empty[2], drain;
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t acc_full[2], acc_empty[2], drain;
   uint32_t tmem_base;
   int abort_flag;
-  int issued;
+  int issued[kMaxProducers];     // stages that each producer warp filled, written when it ends
   int total;                     // row tiles of all experts
   int cum[kMaxExperts + 32];     // row tiles of lower experts (a huge number from E + 1 on)
   int start[kMaxExperts];        // first row
   int rows[kMaxExperts];
 };
+constexpr size_t kSmemBytes = 1024 /*alignment slack*/ + kRingBytes + sizeof(GrpShared);
 
-template <bool kFp4>
-constexpr size_t smem_bytes() {
-  return 1024 /*alignment slack*/ + static_cast<size_t>(GrpCfg<kFp4>::kStages) * GrpCfg<kFp4>::kStageBytes +
-         sizeof(GrpShared);
-}
+// Position in the ring: stage index and the parity of its current round.
+struct RingPos {
+  int stage = 0;
+  uint32_t round = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++stage == stages) {
+      stage = 0;
+      ++round;
+    }
+  }
+};
 
 __device__ __forceinline__ uint64_t sw128_kmajor_desc(uint32_t saddr) {
   uint64_t d = 0;
@@ -103,10 +125,13 @@ __device__ __forceinline__ uint32_t idesc_bf16(int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
          (static_cast<uint32_t>(kFeat >> 4) << 24);
 }
-// kind::mxf4, E2M1 operands, E8M0 scales; `sf`: which scale bytes of a TMEM word (0 or 2).
-__device__ __forceinline__ uint32_t idesc_mxf4(int n, int sf) {
-  return (static_cast<uint32_t>(sf) << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
-         (1u << 23) | (static_cast<uint32_t>(kFeat >> 7) << 27) | (static_cast<uint32_t>(sf) << 29);
+// kind::mxf4, E2M1 operands, E8M0 scales; which two scale bytes of a TMEM word (`sf`: 0 or 2).
+__device__ __forceinline__ uint32_t idesc_mxf4(int n) {
+  return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) |
+         (static_cast<uint32_t>(kFeat >> 7) << 27);
+}
+__device__ __forceinline__ uint32_t idesc_scale_bytes(int sf) {
+  return (static_cast<uint32_t>(sf) << 4) | (static_cast<uint32_t>(sf) << 29);
 }
 
 __device__ __forceinline__ void tc_mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
@@ -123,12 +148,11 @@ __device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint64_t desc) {
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
-__device__ __forceinline__ void tma_load_w(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int e,
-                                           uint32_t bar) {
+__device__ __forceinline__ void tma_load_w(uint32_t dst, const CUtensorMap* map, int x, int f, int e, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(e), "r"(bar)
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(f), "r"(e), "r"(bar)
       : "memory");
 }
 __device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
@@ -148,31 +172,37 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+// Waits of a whole warp; the result is the same in all lanes.
 __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, uint64_t timeout_ns,
                                               volatile int* abort_flag) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   const uint64_t t0 = global_timer_ns();
   for (;;) {
 #pragma unroll 1
     for (int i = 0; i < 64; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
-    if (*abort_flag) return false;
-    if (global_timer_ns() - t0 > timeout_ns) {
+      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
+    if (__any_sync(0xffffffffu, global_timer_ns() - t0 > timeout_ns)) {
       *abort_flag = 1;
       return false;
     }
   }
 }
 
+// One lane of the warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 struct Tile {
-  int e, f0;    // expert; first output feature
-  int r0, n;    // first row, number of rows
-  int subs;     // 128-feature sub-tiles with data
+  int e, f0;  // expert; first feature
+  int r0, n;  // first row, number of rows
 };
 
 // Tile t of the numbering in `sb` (all 32 lanes of a warp call this together).
-__device__ __forceinline__ Tile find_tile(const GrpShared& sb, const GroupedArgs& a, int t, int rows_per_tile,
-                                          int lane) {
+__device__ __forceinline__ Tile find_tile(const GrpShared& sb, const GroupedArgs& a, int t, int lane) {
   const int q = t / a.tiles_f;  // row tiles before it are whole experts' and at most its own expert's
   const unsigned lt = __ballot_sync(0xffffffffu, sb.cum[8 * lane] <= q);
   const int base = 8 * (__popc(lt) - 1);
@@ -181,14 +211,16 @@ __device__ __forceinline__ Tile find_tile(const GrpShared& sb, const GroupedArgs
   r.e = base + __popc(in) - 1;
   const int local = t - sb.cum[r.e] * a.tiles_f;
   const int rows = sb.rows[r.e];
-  const int count = (rows + rows_per_tile - 1) / rows_per_tile;
+  const int count = (rows + a.cap - 1) / a.cap;
   const int ft = local / count, rt = local - ft * count;
   const int per = ((rows + count - 1) / count + 15) & ~15;  // an even split, in multiples of 16
   r.r0 = sb.start[r.e] + rt * per;
   const int left = rows - rt * per;
-  r.n = left < per ? left : per;
-  r.f0 = ft * (a.swiglu ? kFeat : kFeat * a.subs);
-  r.subs = a.swiglu || (a.subs == 2 && r.f0 + kFeat < a.n_out) ? 2 : 1;
+  // through a reduction, whose result the compiler knows to be the same in all lanes
+  r.n = __reduce_min_sync(0xffffffffu, left < per ? left : per);
+  r.r0 = __reduce_min_sync(0xffffffffu, r.r0);
+  r.e = __reduce_min_sync(0xffffffffu, r.e);
+  r.f0 = __reduce_min_sync(0xffffffffu, ft * kFeat);
   return r;
 }
 
@@ -198,23 +230,25 @@ __device__ __forceinline__ float swiglu(float g, float u, float alpha, float lim
   return __fdividef(g, 1.0f + __expf(-alpha * g)) * (u + 1.0f);
 }
 
-template <bool kFp4>
+template <bool kFp4, bool kSwiglu>
 __global__ void __launch_bounds__(kThreads, 1)
 grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                const GroupedArgs a) {
   using C = GrpCfg<kFp4>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  GrpShared& sb = *reinterpret_cast<GrpShared*>(tiles + static_cast<size_t>(C::kStages) * C::kStageBytes);
+  GrpShared& sb = *reinterpret_cast<GrpShared*>(tiles + kRingBytes);
   volatile int* abort_flag = &sb.abort_flag;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int k_steps = (a.K + C::kStageK - 1) / C::kStageK;
+  const int stages = a.stages;
+  const uint32_t ring = smem_u32(tiles);
+  const uint32_t stage_size = stage_bytes<kFp4>(a.cap);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(smem_u32(&sb.full[s]), 1);
-      mbar_init(smem_u32(&sb.sf_full[s]), 1);
+    for (int s = 0; s < kMaxStages; ++s) {
+      mbar_init(smem_u32(&sb.full[s]), C::kProducers);
       mbar_init(smem_u32(&sb.empty[s]), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -223,7 +257,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
     }
     mbar_init(smem_u32(&sb.drain), 1);
     sb.abort_flag = 0;
-    sb.issued = 0;
+    for (int w = 0; w < kMaxProducers; ++w) sb.issued[w] = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -266,7 +300,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
       sb.start[e] = lo;
       sb.rows[e] = hi - lo;
       mine[j] = sum;
-      sum += (hi - lo + C::kRows - 1) / C::kRows;
+      sum += (hi - lo + a.cap - 1) / a.cap;
     }
     int incl = sum;
 #pragma unroll
@@ -289,153 +323,121 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
   const int tiles_total = sb.total * a.tiles_f;
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       tma_prefetch_desc(&wmap);
       tma_prefetch_desc(&xmap);
     }
+    RingPos p;
     int g = 0;
     bool ok = true;
     for (int t = blockIdx.x; t < tiles_total && ok; t += gridDim.x) {
-      const Tile tl = find_tile(sb, a, t, C::kRows, lane);
-      const int n16 = (tl.n + 15) & ~15;
-      int id[4];
-      if (a.row_token) {
-        // rows behind the tile's last one repeat its first: their columns are never stored
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = 4 * lane + j;
-          id[j] = __ldg(a.row_token + tl.r0 + (r < tl.n ? r : 0));
-          if (id[j] < 0 || id[j] >= a.x_rows) {
-            raise_status(a.status, kStatusBadLen);
-            id[j] = 0;
-          }
-        }
-      }
-      for (int kb = 0; kb < k_steps; ++kb, ++g) {
-        const int s = g % C::kStages;
-        const uint32_t bar = smem_u32(&sb.full[s]);
-        const uint32_t dst = smem_u32(tiles + static_cast<size_t>(s) * C::kStageBytes);
-        const int x0 = kb * (kFp4 ? kStageKBytes : kStageKBytes / 2);  // in elements of the maps
-        if (lane == 0) {
-          ok = g < C::kStages ||
-               wait_or_abort(smem_u32(&sb.empty[s]), ((g / C::kStages) - 1) & 1, a.timeout_ns, abort_flag);
-          if (ok) {
-            mbar_arrive_expect_tx(bar, tl.subs * C::kSubBytes + n16 * kStageKBytes);
-            for (int sub = 0; sub < tl.subs; ++sub)  // features past N are zero-filled
-              tma_load_w(dst + sub * C::kSubBytes, &wmap, x0, a.swiglu ? sub : 0,
-                         a.swiglu ? tl.f0 : tl.f0 + sub * kFeat, tl.e, bar);
-          }
-        }
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      const Tile tl = find_tile(sb, a, t, lane);
+      for (int kb = 0; kb < k_steps; ++kb, ++g, p.next(stages)) {
+        if (p.round != 0)
+          ok = wait_or_abort(smem_u32(&sb.empty[p.stage]), (p.round - 1) & 1, a.timeout_ns, abort_flag);
         if (!ok) break;
-        if (a.row_token) {
-          if (4 * lane < n16) tma_gather4(dst + C::kWBytes + lane * 4 * kStageKBytes, &xmap, x0, id, bar);
-        } else {
-          if (16 * lane < n16)
-            tma_load_rows(dst + C::kWBytes + lane * 16 * kStageKBytes, &xmap, x0, tl.r0 + 16 * lane, bar);
+        if (elect_one()) {
+          const uint32_t bar = smem_u32(&sb.full[p.stage]);
+          mbar_arrive_expect_tx(bar, kWBytes);
+          // features past N are zero-filled
+          tma_load_w(ring + p.stage * stage_size, &wmap, kb * (kFp4 ? kStageKBytes : kStageKBytes / 2), tl.f0, tl.e,
+                     bar);
         }
-        __syncwarp();
-        if (lane == 0) sb.issued = g + 1;
       }
     }
-    if (!ok && lane == 0) raise_status(a.status, kStatusTimeout);
+    if (lane == 0) {
+      if (!ok) raise_status(a.status, kStatusTimeout);
+      sb.issued[0] = g;
+    }
   } else if (warp == 1) {
-    int g = 0, i = 0;
+    RingPos p;
+    int i = 0, g = 0;
     bool ok = true;
     for (int t = blockIdx.x; t < tiles_total && ok; t += gridDim.x, ++i) {
-      const Tile tl = find_tile(sb, a, t, C::kRows, lane);
-      if (lane == 0) {
-        const int n16 = (tl.n + 15) & ~15;
-        const int b = i & 1;
-        ok = i < 2 || wait_or_abort(smem_u32(&sb.acc_empty[b]), ((i >> 1) - 1) & 1, a.timeout_ns, abort_flag);
+      const Tile tl = find_tile(sb, a, t, lane);
+      const int n16 = (tl.n + 15) & ~15;
+      const int b = i & 1;
+      if (i >= 2) ok = wait_or_abort(smem_u32(&sb.acc_empty[b]), ((i >> 1) - 1) & 1, a.timeout_ns, abort_flag);
+      tc_fence_after();
+      const uint32_t d = tmem + b * C::kRows;
+      const uint32_t idesc = kFp4 ? idesc_mxf4(n16) : idesc_bf16(n16);
+      for (int kb = 0; kb < k_steps && ok; ++kb, ++g, p.next(stages)) {
+        ok = wait_or_abort(smem_u32(&sb.full[p.stage]), p.round & 1, a.timeout_ns, abort_flag);
+        if (!ok) break;
         tc_fence_after();
-        const uint32_t d = tmem + b * 2 * C::kRows;
-        for (int kb = 0; kb < k_steps && ok; ++kb) {
-          const int s = (g + kb) % C::kStages;
-          const uint32_t parity = ((g + kb) / C::kStages) & 1;
-          ok = wait_or_abort(smem_u32(&sb.full[s]), parity, a.timeout_ns, abort_flag);
-          if (kFp4 && ok) ok = wait_or_abort(smem_u32(&sb.sf_full[s]), parity, a.timeout_ns, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t w_addr = smem_u32(tiles + static_cast<size_t>(s) * C::kStageBytes);
-          const uint32_t x_addr = w_addr + C::kWBytes;
+        const uint32_t w_addr = ring + p.stage * stage_size;
+        const uint32_t x_addr = w_addr + kWBytes;
+        const uint64_t wd = sw128_kmajor_desc(w_addr), xd = sw128_kmajor_desc(x_addr);
+        if (elect_one()) {
           if constexpr (kFp4) {
-            // this stage's scales: per 128 values of K the weight blocks and the rows' block
-            const uint32_t sf = tmem + 4 * C::kRows + ((g + kb) & 1) * 24;
-            const uint32_t sf_addr = x_addr + C::kXBytes;
+            // this stage's scales: per 128 values of K the weights' block and the rows' blocks
+            const uint32_t sf = tmem + 2 * C::kRows + (g & 1) * C::kSfCols;
+            const uint64_t sd = scale_desc(x_addr + a.cap * kStageKBytes);
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-              for (int blk = 0; blk < 3; ++blk)
-                tc_cp_scales(sf + 12 * c + 4 * blk, scale_desc(sf_addr + (3 * c + blk) * C::kSfBlock));
+            for (int c = 0; c < 2; ++c) {
+              tc_cp_scales(sf + 12 * c, sd + (3 * c) * (kSfBlock >> 4));
+              tc_cp_scales(sf + 12 * c + 4, sd + (3 * c + 1) * (kSfBlock >> 4));
+              if (n16 > 128) tc_cp_scales(sf + 12 * c + 8, sd + (3 * c + 2) * (kSfBlock >> 4));
+            }
             const int left = (a.K - kb * C::kStageK + 63) / 64;  // 64-value steps with data
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
-              if (kk >= left) break;
-              const uint32_t sfk = sf + 12 * (kk >> 1);
-              const uint32_t idesc = idesc_mxf4(n16, 2 * (kk & 1));
-              for (int sub = 0; sub < tl.subs; ++sub)
-                tc_mma_mxf4(d + sub * C::kRows, sw128_kmajor_desc(w_addr + sub * C::kSubBytes + kk * 32),
-                            sw128_kmajor_desc(x_addr + kk * 32), idesc, sfk + 4 * sub, sfk + 8, (kb | kk) != 0);
+              if (kk < left)
+                tc_mma_mxf4(d, wd + 2 * kk, xd + 2 * kk, idesc | idesc_scale_bytes(2 * (kk & 1)), sf + 12 * (kk >> 1),
+                            sf + 12 * (kk >> 1) + 4, (kb | kk) != 0);
             }
           } else {
-            const uint32_t idesc = idesc_bf16(n16);
             const int left = (a.K - kb * C::kStageK + 15) / 16;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
-              if (kk >= left) break;
-              for (int sub = 0; sub < tl.subs; ++sub)
-                tc_mma_ss(d + sub * C::kRows, sw128_kmajor_desc(w_addr + sub * C::kSubBytes + kk * 32),
-                          sw128_kmajor_desc(x_addr + kk * 32), idesc, (kb | kk) != 0);
+              if (kk < left) tc_mma_ss(d, wd + 2 * kk, xd + 2 * kk, idesc, (kb | kk) != 0);
             }
           }
-          tc_commit(smem_u32(&sb.empty[s]));
+          tc_commit(smem_u32(&sb.empty[p.stage]));
+          if (kb == k_steps - 1) tc_commit(smem_u32(&sb.acc_full[b]));
         }
-        if (ok) tc_commit(smem_u32(&sb.acc_full[b]));
       }
-      g += k_steps;
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
     }
-    if (lane == 0) {
+    if (elect_one()) {
       if (!ok) raise_status(a.status, kStatusTimeout);
       // every MMA issued by this thread has finished before TMEM is released
       tc_commit(smem_u32(&sb.drain));
       if (!mbar_wait(smem_u32(&sb.drain), 0, kDrainTimeoutNs)) raise_status(a.status, kStatusTimeout);
     }
     __syncwarp();
-  } else if (kFp4 && warp == 2) {
+  } else if (kFp4 && (warp == 2 || warp == 3)) {
     // Scale bytes: a lane keeps rows lane, lane + 32, lane + 64, lane + 96 of each block of
     // 128; 16 bytes of a row serve two stages, the next 16 are requested one pair ahead.
-    const int blocks = (a.K + 31) / 32;  // scale bytes in use
+    const int used = a.K / 32;  // scale bytes in use
+    RingPos p;
     int g = 0;
     bool ok = true;
     for (int t = blockIdx.x; t < tiles_total && ok; t += gridDim.x) {
-      const Tile tl = find_tile(sb, a, t, C::kRows, lane);
-      const uint8_t* src[3][4];
+      const Tile tl = find_tile(sb, a, t, lane);
+      const int blocks = warp == 2 ? 1 : tl.n > 128 ? 2 : 1;
+      const uint8_t* src[2][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = 32 * j + lane;
+      for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
-        for (int sub = 0; sub < 2; ++sub) {
-          const int f = a.swiglu ? tl.f0 + r : tl.f0 + sub * kFeat + r;  // output feature
-          const bool in = sub < tl.subs && f < a.n_out;
-          const long long row = static_cast<long long>(tl.e) * a.N + (a.swiglu ? 2 * f + sub : f);
-          src[sub][j] = in ? a.w_scales + row * a.scale_stride : nullptr;
-        }
-        src[2][j] = nullptr;
-        if (r < tl.n) {
-          long long row = tl.r0 + r;
-          if (a.row_token) {
-            const int id = __ldg(a.row_token + tl.r0 + r);
-            row = id < 0 || id >= a.x_rows ? 0 : id;  // reported by the producer
+        for (int j = 0; j < 4; ++j) {
+          const int r = 128 * blk + 32 * j + lane;
+          src[blk][j] = nullptr;
+          if (warp == 2) {
+            if (blk == 0 && tl.f0 + r < a.N)
+              src[blk][j] = a.w_scales + (static_cast<long long>(tl.e) * a.N + tl.f0 + r) * a.scale_stride;
+          } else if (r < tl.n) {
+            long long row = tl.r0 + r;
+            if (a.row_token) {
+              const int id = __ldg(a.row_token + tl.r0 + r);
+              row = id < 0 || id >= a.x_rows ? 0 : id;  // reported by the row warps
+            }
+            src[blk][j] = a.x_scales + row * a.scale_stride;
           }
-          src[2][j] = a.x_scales + row * a.scale_stride;
         }
-      }
-      uint4 next[3][4];
+      uint4 next[2][4];
       auto request = [&](int pair) {
 #pragma unroll
-        for (int blk = 0; blk < 3; ++blk)
+        for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             next[blk][j] = make_uint4(0, 0, 0, 0);
@@ -444,16 +446,16 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
       };
       request(0);
       for (int kb = 0; kb < k_steps && ok; kb += 2) {
-        uint4 cur[3][4];
+        uint4 cur[2][4];
         // bytes past K / 32 are padding, whatever they hold
         uint32_t mask[4];
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          const int valid = blocks - 8 * kb - 4 * w;
+          const int valid = used - 8 * kb - 4 * w;
           mask[w] = valid >= 4 ? 0xFFFFFFFFu : valid <= 0 ? 0u : (1u << (8 * valid)) - 1u;
         }
 #pragma unroll
-        for (int blk = 0; blk < 3; ++blk)
+        for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             cur[blk][j] = make_uint4(next[blk][j].x & mask[0], next[blk][j].y & mask[1], next[blk][j].z & mask[2],
@@ -462,72 +464,117 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (kb + h >= k_steps) break;
-          const int gs = g + kb + h, s = gs % C::kStages;
-          if (lane == 0)
-            ok = gs < C::kStages ||
-                 wait_or_abort(smem_u32(&sb.empty[s]), ((gs / C::kStages) - 1) & 1, a.timeout_ns, abort_flag);
-          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          if (p.round != 0)
+            ok = wait_or_abort(smem_u32(&sb.empty[p.stage]), (p.round - 1) & 1, a.timeout_ns, abort_flag);
           if (!ok) break;
-          uint8_t* sf = tiles + static_cast<size_t>(s) * C::kStageBytes + C::kWBytes + C::kXBytes;
+          uint8_t* sf = tiles + p.stage * stage_size + kWBytes + a.cap * kStageKBytes + (warp == 2 ? 0 : kSfBlock);
 #pragma unroll
-          for (int blk = 0; blk < 3; ++blk) {
+          for (int blk = 0; blk < 2; ++blk) {
+            if (blk >= blocks) break;
             const uint4* c = cur[blk];
-            reinterpret_cast<uint4*>(sf + blk * C::kSfBlock)[lane] =
+            reinterpret_cast<uint4*>(sf + blk * kSfBlock)[lane] =
                 h == 0 ? make_uint4(c[0].x, c[1].x, c[2].x, c[3].x) : make_uint4(c[0].z, c[1].z, c[2].z, c[3].z);
-            reinterpret_cast<uint4*>(sf + (3 + blk) * C::kSfBlock)[lane] =
+            reinterpret_cast<uint4*>(sf + (3 + blk) * kSfBlock)[lane] =
                 h == 0 ? make_uint4(c[0].y, c[1].y, c[2].y, c[3].y) : make_uint4(c[0].w, c[1].w, c[2].w, c[3].w);
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sb.sf_full[s]));
+          if (elect_one()) mbar_arrive(smem_u32(&sb.full[p.stage]));
+          ++g;
+          p.next(stages);
         }
       }
-      g += k_steps;
     }
-    if (!ok && lane == 0) raise_status(a.status, kStatusTimeout);
+    if (lane == 0) {
+      if (!ok) raise_status(a.status, kStatusTimeout);
+      sb.issued[1 + kRowWarps + warp - 2] = g;
+    }
+  } else if (warp >= kRowWarp0) {
+    const int wr = warp - kRowWarp0;
+    RingPos p;
+    int g = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < tiles_total && ok; t += gridDim.x) {
+      const Tile tl = find_tile(sb, a, t, lane);
+      const int n16 = (tl.n + 15) & ~15;
+      // units of this warp's lanes: four gathered rows, or a box of 16
+      const int rows = a.row_token ? 4 : 16;
+      const int units = n16 / rows, unit = lane * kRowWarps + wr;
+      const bool mine = unit < units;
+      const int bytes = (units - wr + kRowWarps - 1) / kRowWarps * rows * kStageKBytes;  // of this warp
+      int id[4];
+      if (a.row_token && mine) {
+        // rows behind the tile's last one repeat its first: their columns are never stored
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int r = 4 * unit + j;
+          id[j] = __ldg(a.row_token + tl.r0 + (r < tl.n ? r : 0));
+          if (id[j] < 0 || id[j] >= a.x_rows) {
+            raise_status(a.status, kStatusBadLen);
+            id[j] = 0;
+          }
+        }
+      }
+      for (int kb = 0; kb < k_steps; ++kb, ++g, p.next(stages)) {
+        if (p.round != 0)
+          ok = wait_or_abort(smem_u32(&sb.empty[p.stage]), (p.round - 1) & 1, a.timeout_ns, abort_flag);
+        if (!ok) break;
+        const uint32_t bar = smem_u32(&sb.full[p.stage]);
+        const uint32_t dst = ring + p.stage * stage_size + kWBytes;
+        const int x0 = kb * (kFp4 ? kStageKBytes : kStageKBytes / 2);  // in elements of the map
+        if (elect_one()) mbar_arrive_expect_tx(bar, bytes);
+        if (mine) {
+          if (a.row_token) tma_gather4(dst + unit * 4 * kStageKBytes, &xmap, x0, id, bar);
+          else tma_load_rows(dst + unit * 16 * kStageKBytes, &xmap, x0, tl.r0 + 16 * unit, bar);
+        }
+        __syncwarp();
+      }
+    }
+    if (lane == 0) {
+      if (!ok) raise_status(a.status, kStatusTimeout);
+      sb.issued[1 + wr] = g;
+    }
   } else if (warp >= kEpiWarp0) {
-    const int half = (warp - kEpiWarp0) >> 2;
-    const int q = warp & 3;  // TMEM lane quarter (a warp reaches lanes 32 (warp % 4) ..)
+    const int half = (warp - kEpiWarp0) >> 2;  // the two warps of a lane quarter take turns of 32 columns
+    const int q = warp & 3;                    // TMEM lane quarter (a warp reaches lanes 32 (warp % 4) ..)
     const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
     int i = 0;
     for (int t = blockIdx.x; t < tiles_total; t += gridDim.x, ++i) {
-      const Tile tl = find_tile(sb, a, t, C::kRows, lane);
+      const Tile tl = find_tile(sb, a, t, lane);
       const int b = i & 1;
-      // columns of this warp: with SwiGLU and with one sub-tile the halves take turns of
-      // 16 columns, with two plain sub-tiles each half has one
-      const bool split = a.swiglu || tl.subs == 1;
-      const int sub = split ? 0 : half;
-      const int f = tl.f0 + sub * kFeat + 32 * q + lane;
-      const bool mine = f < a.n_out;
-      float b0 = 0.0f, b1 = 0.0f;
-      if (a.bias && mine) {
-        const uint16_t* bias = a.bias + static_cast<long long>(tl.e) * a.N;
-        if (a.swiglu) {
-          b0 = __uint_as_float(static_cast<uint32_t>(__ldg(bias + 2 * f)) << 16);
-          b1 = __uint_as_float(static_cast<uint32_t>(__ldg(bias + 2 * f + 1)) << 16);
-        } else {
-          b0 = __uint_as_float(static_cast<uint32_t>(__ldg(bias + f)) << 16);
-        }
-      }
-      uint16_t* out = a.out + static_cast<long long>(tl.r0) * a.n_out + f;
-      bool ok = true;
-      if (lane == 0) ok = wait_or_abort(smem_u32(&sb.acc_full[b]), (i >> 1) & 1, a.timeout_ns, abort_flag);
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-      if (!ok) break;
+      const int f = tl.f0 + 32 * q + lane;
+      const bool mine = f < a.N;
+      float bias = 0.0f;
+      if (a.bias && mine)
+        bias = __uint_as_float(static_cast<uint32_t>(__ldg(a.bias + static_cast<long long>(tl.e) * a.N + f)) << 16);
+      uint16_t* out = a.out + static_cast<long long>(tl.r0) * a.n_out + (kSwiglu ? f >> 1 : f);
+      if (!wait_or_abort(smem_u32(&sb.acc_full[b]), (i >> 1) & 1, a.timeout_ns, abort_flag)) break;
       tc_fence_after();
-      const uint32_t acc = tmem + lane_base + b * 2 * C::kRows + sub * C::kRows;
+      const uint32_t acc = tmem + lane_base + b * C::kRows;
 #pragma unroll 1
-      for (int c = split ? 16 * half : 0; c < tl.n; c += split ? 32 : 16) {
-        uint32_t r[16], u[16];
-        tmem_ld16(acc + c, r);
-        if (a.swiglu) tmem_ld16(acc + C::kRows + c, u);
+      for (int c = 32 * half; c < tl.n; c += 64) {
+        uint32_t r[32];
+        tmem_ld32(acc + c, r);
         tc_wait_ld();
+        if constexpr (kSwiglu) {
+          // even lanes hold gates, odd lanes the ups of the same outputs: the even lane takes
+          // columns 0..15, the odd one columns 16..31
+          const bool odd = lane & 1;
+          const int first = c + (odd ? 16 : 0);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          float y = __uint_as_float(r[j]) + b0;
-          if (a.swiglu) y = swiglu(y, __uint_as_float(u[j]) + b1, a.alpha, a.limit);
-          if (mine && c + j < tl.n)
-            out[static_cast<long long>(c + j) * a.n_out] = static_cast<uint16_t>(pack_bf16x2(y, 0.0f) & 0xFFFFu);
+          for (int j = 0; j < 16; ++j) {
+            const float lo = __uint_as_float(r[j]) + bias, hi = __uint_as_float(r[16 + j]) + bias;
+            const float theirs = __shfl_xor_sync(0xffffffffu, odd ? lo : hi, 1);
+            const float y = swiglu(odd ? theirs : lo, odd ? hi : theirs, a.alpha, a.limit);
+            if (mine && first + j < tl.n)
+              out[static_cast<long long>(first + j) * a.n_out] = static_cast<uint16_t>(pack_bf16x2(y, 0.0f) & 0xFFFFu);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (mine && c + j < tl.n)
+              out[static_cast<long long>(c + j) * a.n_out] =
+                  static_cast<uint16_t>(pack_bf16x2(__uint_as_float(r[j]) + bias, 0.0f) & 0xFFFFu);
         }
       }
       tc_fence_before();
@@ -539,12 +586,16 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
   tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0 && *abort_flag) {
-    // copies still in flight land before the shared memory is released
-    const int issued = sb.issued;
-    for (int s = 0; s < C::kStages && s < issued; ++s) {
-      const int last = issued - 1 - ((issued - 1 - s) % C::kStages);
-      if (!mbar_wait(smem_u32(&sb.full[s]), (last / C::kStages) & 1, kDrainTimeoutNs))
-        raise_status(a.status, kStatusTimeout);
+    // Copies still in flight land before the shared memory is released.  A stage completes once
+    // every producer warp has arrived; those that gave up earlier than others are less than
+    // one round of the ring behind, and their arrivals are made up for here.
+    int most = 0;
+    for (int w = 0; w < C::kProducers; ++w) most = sb.issued[w] > most ? sb.issued[w] : most;
+    for (int w = 0; w < C::kProducers; ++w)
+      for (int g = sb.issued[w]; g < most; ++g) mbar_arrive(smem_u32(&sb.full[g % stages]));
+    for (int s = 0; s < stages && s < most; ++s) {
+      const int last = most - 1 - ((most - 1 - s) % stages);
+      if (!mbar_wait(smem_u32(&sb.full[s]), (last / stages) & 1, kDrainTimeoutNs)) raise_status(a.status, kStatusTimeout);
     }
   }
   __syncthreads();
@@ -554,7 +605,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
   }
 }
 
-template <bool kFp4>
+template <bool kFp4, bool kSwiglu>
 cudaError_t launch_grouped_t(const CUtensorMap& wmap, const CUtensorMap& xmap, const GroupedArgs& a, int sms,
                              cudaStream_t stream) {
   // the shared-memory opt-in, once per device (host threads may race here: atomic flags,
@@ -564,28 +615,37 @@ cudaError_t launch_grouped_t(const CUtensorMap& wmap, const CUtensorMap& xmap, c
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !attr_set[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(grouped_kernel<kFp4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem_bytes<kFp4>()));
+    e = cudaFuncSetAttribute(grouped_kernel<kFp4, kSwiglu>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kSmemBytes));
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev].store(true, std::memory_order_release);
   }
+  GroupedArgs b = a;
+  b.stages = stage_count<kFp4>(a.cap);
   // no more CTAs than tiles there can be
-  constexpr int kRows = GrpCfg<kFp4>::kRows;
   const long long groups = a.num_experts < a.rows ? a.num_experts : a.rows;
-  const long long most = (a.rows / kRows + groups) * a.tiles_f;
+  const long long most = (a.rows / a.cap + groups) * a.tiles_f;
   const int grid = static_cast<int>(most < sms ? most : sms);
-  grouped_kernel<kFp4><<<grid, kThreads, smem_bytes<kFp4>(), stream>>>(wmap, xmap, a);
+  grouped_kernel<kFp4, kSwiglu><<<grid, kThreads, kSmemBytes, stream>>>(wmap, xmap, b);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-int grouped_tile_rows(bool mxfp4) { return mxfp4 ? GrpCfg<true>::kRows : GrpCfg<false>::kRows; }
+int grouped_tile_rows(bool mxfp4, int rows, int num_experts) {
+  // 64 while the experts have few rows on average: the ring's stages are then small and many
+  // (8 instead of 4), which keeps more weight bytes in flight
+  const int most = mxfp4 ? GrpCfg<true>::kRows : GrpCfg<false>::kRows;
+  return rows <= 32LL * num_experts ? 64 : most;
+}
 
 cudaError_t launch_grouped(const CUtensorMap& wmap, const CUtensorMap& xmap, const GroupedArgs& a, bool mxfp4,
                            int sms, cudaStream_t stream) {
-  return mxfp4 ? launch_grouped_t<true>(wmap, xmap, a, sms, stream)
-               : launch_grouped_t<false>(wmap, xmap, a, sms, stream);
+  if (mxfp4)
+    return a.swiglu ? launch_grouped_t<true, true>(wmap, xmap, a, sms, stream)
+                    : launch_grouped_t<true, false>(wmap, xmap, a, sms, stream);
+  return a.swiglu ? launch_grouped_t<false, true>(wmap, xmap, a, sms, stream)
+                  : launch_grouped_t<false, false>(wmap, xmap, a, sms, stream);
 }
 
 }  // namespace sa

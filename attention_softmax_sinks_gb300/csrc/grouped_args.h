@@ -8,7 +8,7 @@
 namespace sa {
 
 constexpr int kMaxExperts = 256;
-constexpr int kGroupedFeatures = 128;  // features of one sub-tile (one tcgen05.mma M)
+constexpr int kGroupedFeatures = 128;  // features of one tile (the tcgen05.mma M)
 
 struct GroupedArgs {
   const uint16_t* bias;      // bf16 [E, N] or nullptr
@@ -20,18 +20,20 @@ struct GroupedArgs {
   int scale_stride;
   int x_rows, rows, num_experts, N, K;
   int n_out;    // features written per row: N, or N / 2 with swiglu
-  int subs;     // 128-feature sub-tiles per tile: 2, or 1 when few tiles (always 2 with swiglu)
-  int tiles_f;  // feature tiles
+  int tiles_f;  // feature tiles (of N)
+  int cap;      // most rows of a tile
+  int stages;   // ring stages (set by the launcher)
   int swiglu;
   float alpha, limit;
   unsigned* status;
   unsigned long long timeout_ns;
 };
 
-// Token rows of one tile (the largest MMA N): 128 in bf16, fewer in MXFP4, whose scales take
-// TMEM columns beside the accumulators.
-int grouped_tile_rows(bool mxfp4);
-// wmap: w as {K, gate/up (1 without swiglu), features, E} in boxes of 128 bytes x 1 x 128 x 1;
+// Most rows of one tile (the largest MMA N) for `rows` rows over `num_experts` experts: a
+// multiple of 32, at most 256 (bf16) or 224 (MXFP4, whose scales take TMEM columns beside the
+// accumulators).
+int grouped_tile_rows(bool mxfp4, int rows, int num_experts);
+// wmap: w as {K, N, E} in boxes of 128 bytes x 128 x 1;
 // xmap: x [x_rows, K] in boxes of 128 bytes x 16 rows, or x 1 row when row_token gathers.
 cudaError_t launch_grouped(const CUtensorMap& wmap, const CUtensorMap& xmap, const GroupedArgs& a, bool mxfp4,
                            int sms, cudaStream_t stream);
