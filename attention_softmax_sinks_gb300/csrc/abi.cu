@@ -115,7 +115,7 @@ sa_status map_experts(CUtensorMap* m, const void* base, long long experts, long 
   return r == CUDA_SUCCESS ? SA_OK : SA_ERR_CUDA;
 }
 
-// Rows [rows, row_bytes] read in boxes of 128 bytes x box_rows (1 for gathers of single rows).
+// Rows [rows, row_bytes] read in boxes of 128 bytes x box_rows.
 sa_status map_rows(CUtensorMap* m, const void* base, long long rows, long long row_bytes, int box_rows,
                    bool bytes) {
   PFN_cuTensorMapEncodeTiled_v12000 enc;
@@ -314,7 +314,9 @@ sa_status grouped_common(const GroupedCall& c, cudaStream_t stream) {
   a.cap = sa::grouped_tile_rows(c.mxfp4, c.rows, c.experts);
   const long long tiles_f = (static_cast<long long>(c.n) + sa::kGroupedFeatures - 1) / sa::kGroupedFeatures;
   if ((c.rows / 64LL + c.experts) * tiles_f >= (1LL << 30)) return SA_ERR_SHAPE;
+  a.box_rows = a.cap > 64 ? 32 : 16;
   a.tiles_f = static_cast<int>(tiles_f);
+  a.x = static_cast<const uint8_t*>(c.x);
   unsigned* status = nullptr;
   if (sa_status s = status_ptr(&status)) return s;
   a.bias = static_cast<const uint16_t*>(c.bias);
@@ -337,7 +339,7 @@ sa_status grouped_common(const GroupedCall& c, cudaStream_t stream) {
   const long long row_bytes = c.mxfp4 ? c.k / 2 : 2LL * c.k;
   CUtensorMap wm, xm;
   if (sa_status s = map_experts(&wm, c.w, c.experts, c.n, row_bytes, c.mxfp4)) return s;
-  if (sa_status s = map_rows(&xm, c.x, c.x_rows, row_bytes, c.row_token ? 1 : 16, c.mxfp4)) return s;
+  if (sa_status s = map_rows(&xm, c.x, c.x_rows, row_bytes, a.box_rows, c.mxfp4)) return s;
   return sa::launch_grouped(wm, xm, a, c.mxfp4, sm_count(), stream) == cudaSuccess ? SA_OK : SA_ERR_LAUNCH;
 }
 

@@ -21,8 +21,8 @@
 //                 activation in fp32, one rounding; a warp writes 64 consecutive bytes per row.
 //                 SwiGLU: gate and up are neighbouring lanes, which exchange half of their
 //                 columns so that each finishes 16 of every 32
-//   warps 12..15  the rows of a stage: four per TMA gather by their indices (a lane keeps the
-//                 indices it issues), or boxes of 16 consecutive rows
+//   warps 12..15  the rows of a stage: consecutive rows in TMA boxes, rows gathered by their
+//                 indices with 16-byte asynchronous copies
 // Two TMEM accumulators alternate, so the epilogue of a tile overlaps the next tile's MMAs.
 //
 // Tiles are numbered by expert, then feature tile, then row tile: the row tiles of one weight
@@ -49,6 +49,7 @@ constexpr int kThreads = 32 * (kRowWarp0 + kRowWarps);
 constexpr int kMaxStages = 8;
 constexpr int kRingBytes = 200 * 1024;
 constexpr int kWBytes = kFeat * kStageKBytes;
+constexpr int kLag = 2;        // stages between a gather's request and its hand-over
 constexpr int kSfBlock = 512;  // scales of 128 rows x 128 values of K
 constexpr unsigned long long kDrainTimeoutNs = 2000000000ull;
 
@@ -162,14 +163,14 @@ __device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* m
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
-// Four rows of 128 bytes by their indices (the map's box is one row high).
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int x, const int (&r)[4],
-                                            uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(bar)
-      : "memory");
+// 16 bytes by a thread of its own, or 16 zero bytes.
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src, bool data) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(data ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_async_wait() {  // all but the N newest groups
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // Waits of a whole warp; the result is the same in all lanes.
@@ -494,40 +495,76 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
     RingPos p;
     int g = 0;
     bool ok = true;
-    for (int t = blockIdx.x; t < tiles_total && ok; t += gridDim.x) {
-      const Tile tl = find_tile(sb, a, t, lane);
-      const int n16 = (tl.n + 15) & ~15;
-      // units of this warp's lanes: four gathered rows, or a box of 16
-      const int rows = a.row_token ? 4 : 16;
-      const int units = n16 / rows, unit = lane * kRowWarps + wr;
-      const bool mine = unit < units;
-      const int bytes = (units - wr + kRowWarps - 1) / kRowWarps * rows * kStageKBytes;  // of this warp
-      int id[4];
-      if (a.row_token && mine) {
-        // rows behind the tile's last one repeat its first: their columns are never stored
+    if (a.row_token) {
+      // Gathered rows: eight threads per row copy its 128 bytes, 16 rows at a time, into the
+      // places of the 128-byte swizzle.  A stage is handed over (copies landed, fenced
+      // towards the tensor core's reads) once kLag newer ones have been requested.
+      const int tid = threadIdx.x - 32 * kRowWarp0;
+      const int chunk = tid & 7, row0 = tid >> 3;
+      const long long row_bytes = kFp4 ? a.K / 2 : 2LL * a.K;
+      const uint32_t dst0 = kWBytes + row0 * kStageKBytes + ((chunk ^ (row0 & 7)) << 4);
+      RingPos done;
+      int handed = 0;
+      auto hand_over = [&]() {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (elect_one()) mbar_arrive(smem_u32(&sb.full[done.stage]));
+        ++handed;
+        done.next(stages);
+      };
+      for (int t = blockIdx.x; t < tiles_total && ok; t += gridDim.x) {
+        const Tile tl = find_tile(sb, a, t, lane);
+        const int steps = (tl.n + 15) >> 4;
+        const uint8_t* src[C::kRows / 16];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = 4 * unit + j;
-          id[j] = __ldg(a.row_token + tl.r0 + (r < tl.n ? r : 0));
-          if (id[j] < 0 || id[j] >= a.x_rows) {
-            raise_status(a.status, kStatusBadLen);
-            id[j] = 0;
+        for (int i = 0; i < C::kRows / 16; ++i) {
+          src[i] = nullptr;
+          if (i < steps) {
+            // rows behind the tile's last one repeat its first: their columns are never stored
+            const int r = 16 * i + row0;
+            int id = __ldg(a.row_token + tl.r0 + (r < tl.n ? r : 0));
+            if (id < 0 || id >= a.x_rows) {
+              raise_status(a.status, kStatusBadLen);
+              id = 0;
+            }
+            src[i] = a.x + id * row_bytes + 16 * chunk;
+          }
+        }
+        for (int kb = 0; kb < k_steps; ++kb, ++g, p.next(stages)) {
+          if (p.round != 0)
+            ok = wait_or_abort(smem_u32(&sb.empty[p.stage]), (p.round - 1) & 1, a.timeout_ns, abort_flag);
+          if (!ok) break;
+          const bool data = kb * kStageKBytes + 16 * chunk < row_bytes;  // zeros past the row's end
+          const uint32_t dst = ring + p.stage * stage_size + dst0;
+#pragma unroll
+          for (int i = 0; i < C::kRows / 16; ++i)
+            if (i < steps)
+              copy_async16(dst + i * 16 * kStageKBytes, src[i] + (data ? kb * kStageKBytes : 0), data);
+          copy_async_commit();
+          if (g - handed >= kLag) {
+            copy_async_wait<kLag>();
+            hand_over();
           }
         }
       }
-      for (int kb = 0; kb < k_steps; ++kb, ++g, p.next(stages)) {
-        if (p.round != 0)
-          ok = wait_or_abort(smem_u32(&sb.empty[p.stage]), (p.round - 1) & 1, a.timeout_ns, abort_flag);
-        if (!ok) break;
-        const uint32_t bar = smem_u32(&sb.full[p.stage]);
-        const uint32_t dst = ring + p.stage * stage_size + kWBytes;
-        const int x0 = kb * (kFp4 ? kStageKBytes : kStageKBytes / 2);  // in elements of the map
-        if (elect_one()) mbar_arrive_expect_tx(bar, bytes);
-        if (mine) {
-          if (a.row_token) tma_gather4(dst + unit * 4 * kStageKBytes, &xmap, x0, id, bar);
-          else tma_load_rows(dst + unit * 16 * kStageKBytes, &xmap, x0, tl.r0 + 16 * unit, bar);
+      copy_async_wait<0>();
+      while (handed < g) hand_over();
+    } else {
+      for (int t = blockIdx.x; t < tiles_total && ok; t += gridDim.x) {
+        const Tile tl = find_tile(sb, a, t, lane);
+        const int units = (tl.n + a.box_rows - 1) / a.box_rows, unit = lane * kRowWarps + wr;
+        const int bytes = (units - wr + kRowWarps - 1) / kRowWarps * a.box_rows * kStageKBytes;  // of this warp
+        for (int kb = 0; kb < k_steps; ++kb, ++g, p.next(stages)) {
+          if (p.round != 0)
+            ok = wait_or_abort(smem_u32(&sb.empty[p.stage]), (p.round - 1) & 1, a.timeout_ns, abort_flag);
+          if (!ok) break;
+          const uint32_t bar = smem_u32(&sb.full[p.stage]);
+          if (elect_one()) mbar_arrive_expect_tx(bar, bytes);
+          if (unit < units)
+            tma_load_rows(ring + p.stage * stage_size + kWBytes + unit * a.box_rows * kStageKBytes, &xmap,
+                          kb * (kFp4 ? kStageKBytes : kStageKBytes / 2), tl.r0 + a.box_rows * unit, bar);
+          __syncwarp();
         }
-        __syncwarp();
       }
     }
     if (lane == 0) {

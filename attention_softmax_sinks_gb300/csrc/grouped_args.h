@@ -11,6 +11,7 @@ constexpr int kMaxExperts = 256;
 constexpr int kGroupedFeatures = 128;  // features of one tile (the tcgen05.mma M)
 
 struct GroupedArgs {
+  const uint8_t* x;          // [x_rows, K] bf16 or codes (read directly when rows are gathered)
   const uint16_t* bias;      // bf16 [E, N] or nullptr
   uint16_t* out;             // bf16 [rows, N], or [rows, N / 2] with swiglu
   const int32_t* offsets;    // [E + 1], or nullptr: one group of all rows
@@ -22,6 +23,7 @@ struct GroupedArgs {
   int n_out;    // features written per row: N, or N / 2 with swiglu
   int tiles_f;  // feature tiles (of N)
   int cap;      // most rows of a tile
+  int box_rows; // rows of xmap's boxes: divides cap
   int stages;   // ring stages (set by the launcher)
   int swiglu;
   float alpha, limit;
@@ -34,7 +36,7 @@ struct GroupedArgs {
 // accumulators).
 int grouped_tile_rows(bool mxfp4, int rows, int num_experts);
 // wmap: w as {K, N, E} in boxes of 128 bytes x 128 x 1;
-// xmap: x [x_rows, K] in boxes of 128 bytes x 16 rows, or x 1 row when row_token gathers.
+// xmap: x [x_rows, K] in boxes of 128 bytes x box_rows.
 cudaError_t launch_grouped(const CUtensorMap& wmap, const CUtensorMap& xmap, const GroupedArgs& a, bool mxfp4,
                            int sms, cudaStream_t stream);
 
