@@ -311,12 +311,8 @@ sa_status grouped_common(const GroupedCall& c, cudaStream_t stream) {
     return SA_ERR_ALIGNMENT;
   sa::GroupedArgs a{};
   a.n_out = c.swiglu ? c.n / 2 : c.n;
-  a.cap = sa::grouped_tile_rows(c.mxfp4, c.rows, c.experts);
-  const long long tiles_f = (static_cast<long long>(c.n) + sa::kGroupedFeatures - 1) / sa::kGroupedFeatures;
-  if ((c.rows / 64LL + c.experts) * tiles_f >= (1LL << 30)) return SA_ERR_SHAPE;
-  a.box_rows = a.cap > 64 ? 32 : 16;
-  a.tiles_f = static_cast<int>(tiles_f);
-  a.x = static_cast<const uint8_t*>(c.x);
+  const long long blocks_f = (static_cast<long long>(c.n) + sa::kGroupedFeatures - 1) / sa::kGroupedFeatures;
+  if ((c.rows / 64LL + c.experts) * blocks_f >= (1LL << 30)) return SA_ERR_SHAPE;  // more tiles than are counted
   unsigned* status = nullptr;
   if (sa_status s = status_ptr(&status)) return s;
   a.bias = static_cast<const uint16_t*>(c.bias);
@@ -336,6 +332,8 @@ sa_status grouped_common(const GroupedCall& c, cudaStream_t stream) {
   a.limit = c.limit;
   a.status = status;
   a.timeout_ns = g_timeout_ns;
+  a.x = static_cast<const uint8_t*>(c.x);
+  sa::grouped_plan(a, c.mxfp4);
   const long long row_bytes = c.mxfp4 ? c.k / 2 : 2LL * c.k;
   CUtensorMap wm, xm;
   if (sa_status s = map_experts(&wm, c.w, c.experts, c.n, row_bytes, c.mxfp4)) return s;

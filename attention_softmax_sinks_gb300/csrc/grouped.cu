@@ -47,10 +47,13 @@ constexpr int kRowWarps = 4;
 constexpr int kMaxProducers = 3 + kRowWarps;  // weights, rows, and in MXFP4 two warps of scales
 constexpr int kThreads = 32 * (kRowWarp0 + kRowWarps);
 constexpr int kMaxStages = 8;
-constexpr int kRingBytes = 200 * 1024;
+constexpr int kRingBytes = 198 * 1024;
 constexpr int kWBytes = kFeat * kStageKBytes;
-constexpr int kLag = 2;        // stages between a gather's request and its hand-over
-constexpr int kSfBlock = 512;  // scales of 128 rows x 128 values of K
+constexpr int kLag = 2;         // stages between a gather's request and its hand-over
+constexpr int kBand = 8;        // row tiles of an expert that pass over its features together
+constexpr int kSfBlock = 512;   // scales of 128 rows x 128 values of K
+constexpr int kRawPairs = 3;    // scale bytes on their way: pairs of stages
+constexpr int kRawBlock = 128 * 16;
 constexpr unsigned long long kDrainTimeoutNs = 2000000000ull;
 
 template <bool kFp4>
@@ -59,21 +62,23 @@ struct GrpCfg {
   static constexpr int kRows = kFp4 ? 224 : 256;
   static constexpr int kStageK = kFp4 ? 256 : 64;
   static constexpr int kSfBytes = kFp4 ? 2 * 3 * kSfBlock : 0;  // per 128 values of K: a block of weights, two of rows
+  static constexpr int kRawBytes = kFp4 ? kRawPairs * 3 * kRawBlock : 0;
   static constexpr int kSfCols = 24;
   static constexpr int kTmemCols = 512;
-  static constexpr int kProducers = 1 + kRowWarps + (kFp4 ? 2 : 0);
+  static constexpr int kProducers = 1 + kRowWarps + (kFp4 ? 2 : 0);  // warps that fill a stage, per CTA
   static_assert(2 * kRows + (kFp4 ? 2 * kSfCols : 0) <= kTmemCols, "TMEM holds 512 columns");
 };
 
-// A stage holds kWBytes of weights, cap rows of 128 bytes, and the scales.  cap is a multiple
-// of 32, so every part starts on a multiple of 1024 bytes (the swizzle atom) but the scales.
+// A stage holds kWBytes of weights, `rows` rows of 128 bytes (a CTA of a pair stages half of
+// the tile's), and the scales.  rows is a multiple of 16, so the parts start on multiples of
+// 1024 bytes (the swizzle atom).
 template <bool kFp4>
-__host__ __device__ constexpr int stage_bytes(int cap) {
-  return (kWBytes + cap * kStageKBytes + GrpCfg<kFp4>::kSfBytes + 1023) / 1024 * 1024;
+__host__ __device__ constexpr int stage_bytes(int rows) {
+  return (kWBytes + rows * kStageKBytes + GrpCfg<kFp4>::kSfBytes + 1023) / 1024 * 1024;
 }
 template <bool kFp4>
-__host__ __device__ constexpr int stage_count(int cap) {
-  return kRingBytes / stage_bytes<kFp4>(cap) < kMaxStages ? kRingBytes / stage_bytes<kFp4>(cap) : kMaxStages;
+__host__ __device__ constexpr int stage_count(int rows) {
+  return kRingBytes / stage_bytes<kFp4>(rows) < kMaxStages ? kRingBytes / stage_bytes<kFp4>(rows) : kMaxStages;
 }
 
 struct GrpShared {
@@ -87,9 +92,13 @@ struct GrpShared {
   int start[kMaxExperts];        // first row
   int rows[kMaxExperts];
 };
-constexpr size_t kSmemBytes = 1024 /*alignment slack*/ + kRingBytes + sizeof(GrpShared);
+template <bool kFp4>
+constexpr size_t smem_bytes() {
+  return 1024 /*alignment slack*/ + kRingBytes + GrpCfg<kFp4>::kRawBytes + sizeof(GrpShared);
+}
+static_assert(smem_bytes<true>() <= 227 * 1024, "shared memory of one CTA");
 
-// Position in the ring: stage index and the parity of its current round.
+// Position in the ring: stage index and number of rounds made.
 struct RingPos {
   int stage = 0;
   uint32_t round = 0;
@@ -121,51 +130,147 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
   return d;
 }
 
-// kind::f16, bf16 operands, both K-major, fp32 accumulation.
+// M: 128 features, or 256 of a CTA pair.  kind::f16, bf16 operands, both K-major.
+template <bool kPair>
 __device__ __forceinline__ uint32_t idesc_bf16(int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
-         (static_cast<uint32_t>(kFeat >> 4) << 24);
+         (static_cast<uint32_t>((kPair ? 2 : 1) * kFeat >> 4) << 24);
 }
 // kind::mxf4, E2M1 operands, E8M0 scales; which two scale bytes of a TMEM word (`sf`: 0 or 2).
+template <bool kPair>
 __device__ __forceinline__ uint32_t idesc_mxf4(int n) {
   return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) |
-         (static_cast<uint32_t>(kFeat >> 7) << 27);
+         (static_cast<uint32_t>((kPair ? 2 : 1) * kFeat >> 7) << 27);
 }
 __device__ __forceinline__ uint32_t idesc_scale_bytes(int sf) {
   return (static_cast<uint32_t>(sf) << 4) | (static_cast<uint32_t>(sf) << 29);
 }
 
-__device__ __forceinline__ void tc_mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
-          d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-      : "memory");
+// The tcgen05 instructions for one CTA or for a pair (an M = 256 MMA on both SMs, issued by
+// the leading CTA; operands, scales and accumulator halves lie at the same places in both).
+template <bool kPair>
+__device__ __forceinline__ void grp_tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
+  if constexpr (kPair) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    tmem_alloc(dst_smem, ncols);
+    tmem_relinquish();
+  }
 }
-// 512 bytes (32 rows x 16) to the same four columns of all four lane quarters.
-__device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+template <bool kPair>
+__device__ __forceinline__ void grp_tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+  if constexpr (kPair)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+  else
+    tmem_dealloc(taddr, ncols);
+}
+template <bool kPair>
+__device__ __forceinline__ void grp_mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  if constexpr (kPair)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    tc_mma_ss(d_tmem, a_desc, b_desc, idesc, accumulate);
+}
+template <bool kPair>
+__device__ __forceinline__ void grp_mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  if constexpr (kPair)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+// 512 bytes (32 rows x 16) to the same four columns of all four lane quarters; in a pair both
+// CTAs copy from their own shared memory.
+template <bool kPair>
+__device__ __forceinline__ void grp_cp_scales(uint32_t taddr, uint64_t desc) {
+  if constexpr (kPair)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+// Arrive on `bar` (in a pair: on both CTAs') when all tcgen05 work issued so far is done.
+template <bool kPair>
+__device__ __forceinline__ void grp_commit(uint32_t bar) {
+  if constexpr (kPair)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+  else
+    tc_commit(bar);
 }
 
+// Barriers of the leading CTA: `bar` is a shared::cluster address in a pair, which threads of
+// and TMA copies into either CTA signal.  None of these arrivals publishes memory to the other
+// CTA's threads: copies report themselves, accumulators are handed back by tcgen05 fences, and
+// what threads write into a stage is read only by their own SM's tensor core, after a proxy
+// fence that has put it there.  (At cluster scope, a releasing arrival waits for everything its
+// warp has under way and halves the kernel's speed.)
+template <bool kPair>
+__device__ __forceinline__ void grp_arrive(uint32_t bar) {
+  if constexpr (kPair)
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  else
+    mbar_arrive(bar);
+}
+template <bool kPair>
+__device__ __forceinline__ void grp_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
+  if constexpr (kPair)
+    asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                 : "memory");
+  else
+    mbar_arrive_expect_tx(bar, bytes);
+}
+template <bool kPair>
 __device__ __forceinline__ void tma_load_w(uint32_t dst, const CUtensorMap* map, int x, int f, int e, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(f), "r"(e), "r"(bar)
-      : "memory");
+  if constexpr (kPair)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(f), "r"(e), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(f), "r"(e), "r"(bar)
+        : "memory");
 }
+template <bool kPair>
 __device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-      : "memory");
+  if constexpr (kPair)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
 }
-// 16 bytes by a thread of its own, or 16 zero bytes.
-__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src, bool data) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(data ? 16 : 0) : "memory");
+// 16 bytes by a thread of its own: `bytes` of them from src, zeros behind.
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -202,26 +307,31 @@ struct Tile {
   int r0, n;  // first row, number of rows
 };
 
-// Tile t of the numbering in `sb` (all 32 lanes of a warp call this together).
-__device__ __forceinline__ Tile find_tile(const GrpShared& sb, const GroupedArgs& a, int t, int lane) {
+// Tile t of the numbering in `sb` (all 32 lanes of a warp call this together).  `features`: of
+// one tile; `grain`: its rows are split in multiples of this.
+__device__ __forceinline__ Tile find_tile(const GrpShared& sb, const GroupedArgs& a, int t, int features, int grain,
+                                          int lane) {
   const int q = t / a.tiles_f;  // row tiles before it are whole experts' and at most its own expert's
   const unsigned lt = __ballot_sync(0xffffffffu, sb.cum[8 * lane] <= q);
   const int base = 8 * (__popc(lt) - 1);
   const unsigned in = __ballot_sync(0xffffffffu, lane < 8 && sb.cum[base + (lane & 7)] <= q);
   Tile r;
   r.e = base + __popc(in) - 1;
-  const int local = t - sb.cum[r.e] * a.tiles_f;
   const int rows = sb.rows[r.e];
   const int count = (rows + a.cap - 1) / a.cap;
-  const int ft = local / count, rt = local - ft * count;
-  const int per = ((rows + count - 1) / count + 15) & ~15;  // an even split, in multiples of 16
+  int local = t - sb.cum[r.e] * a.tiles_f;
+  const int band = count <= kBand ? 0 : local / (kBand * a.tiles_f);
+  local -= band * kBand * a.tiles_f;
+  const int wide = min(kBand, count - band * kBand);
+  const int ft = local / wide, rt = band * kBand + local - ft * wide;
+  const int per = (rows + count * grain - 1) / (count * grain) * grain;  // an even split, in multiples of grain
   r.r0 = sb.start[r.e] + rt * per;
   const int left = rows - rt * per;
   // through a reduction, whose result the compiler knows to be the same in all lanes
   r.n = __reduce_min_sync(0xffffffffu, left < per ? left : per);
   r.r0 = __reduce_min_sync(0xffffffffu, r.r0);
   r.e = __reduce_min_sync(0xffffffffu, r.e);
-  r.f0 = __reduce_min_sync(0xffffffffu, ft * kFeat);
+  r.f0 = __reduce_min_sync(0xffffffffu, ft * features);
   return r;
 }
 
@@ -231,30 +341,40 @@ __device__ __forceinline__ float swiglu(float g, float u, float alpha, float lim
   return __fdividef(g, 1.0f + __expf(-alpha * g)) * (u + 1.0f);
 }
 
-template <bool kFp4, bool kSwiglu>
+template <bool kFp4, bool kSwiglu, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
 grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                const GroupedArgs a) {
   using C = GrpCfg<kFp4>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  GrpShared& sb = *reinterpret_cast<GrpShared*>(tiles + kRingBytes);
+  GrpShared& sb = *reinterpret_cast<GrpShared*>(tiles + kRingBytes + C::kRawBytes);
   volatile int* abort_flag = &sb.abort_flag;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int k_steps = (a.K + C::kStageK - 1) / C::kStageK;
   const int stages = a.stages;
   const uint32_t ring = smem_u32(tiles);
-  const uint32_t stage_size = stage_bytes<kFp4>(a.cap);
+  // a pair stages half of a tile's rows in each CTA
+  constexpr int kCtas = kPair ? 2 : 1;
+  constexpr int kGrain = 16 * kCtas;
+  constexpr int kFeatures = kCtas * kFeat;
+  const int stage_rows = a.cap / kCtas;
+  const uint32_t stage_size = stage_bytes<kFp4>(stage_rows);
+  const int rank = kPair ? static_cast<int>(cluster_ctarank()) : 0;
+  const int t_first = blockIdx.x / kCtas, t_step = gridDim.x / kCtas;
+  // the leading CTA's barriers
+  const uint32_t full0 = kPair ? dsmem_addr(smem_u32(&sb.full[0]), 0) : smem_u32(&sb.full[0]);
+  const uint32_t acc_empty0 = kPair ? dsmem_addr(smem_u32(&sb.acc_empty[0]), 0) : smem_u32(&sb.acc_empty[0]);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
-      mbar_init(smem_u32(&sb.full[s]), C::kProducers);
+      mbar_init(smem_u32(&sb.full[s]), kCtas * C::kProducers);
       mbar_init(smem_u32(&sb.empty[s]), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&sb.acc_full[b]), 1);
-      mbar_init(smem_u32(&sb.acc_empty[b]), kEpiWarps);
+      mbar_init(smem_u32(&sb.acc_empty[b]), kCtas * kEpiWarps);
     }
     mbar_init(smem_u32(&sb.drain), 1);
     sb.abort_flag = 0;
@@ -262,8 +382,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
     fence_barrier_init();
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(&sb.tmem_base), C::kTmemCols);
-    tmem_relinquish();
+    grp_tmem_alloc<kPair>(smem_u32(&sb.tmem_base), C::kTmemCols);
   }
   if (warp == 2) {
     // the groups: validated, and their row tiles summed up (8 experts per lane).  A group
@@ -319,6 +438,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (kPair) cluster_sync();  // the other CTA's barriers exist
   tc_fence_after();
   const uint32_t tmem = sb.tmem_base;
   const int tiles_total = sb.total * a.tiles_f;
@@ -331,18 +451,18 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
     RingPos p;
     int g = 0;
     bool ok = true;
-    for (int t = blockIdx.x; t < tiles_total && ok; t += gridDim.x) {
-      const Tile tl = find_tile(sb, a, t, lane);
+    for (int t = t_first; t < tiles_total && ok; t += t_step) {
+      const Tile tl = find_tile(sb, a, t, kFeatures, kGrain, lane);
       for (int kb = 0; kb < k_steps; ++kb, ++g, p.next(stages)) {
         if (p.round != 0)
           ok = wait_or_abort(smem_u32(&sb.empty[p.stage]), (p.round - 1) & 1, a.timeout_ns, abort_flag);
         if (!ok) break;
         if (elect_one()) {
-          const uint32_t bar = smem_u32(&sb.full[p.stage]);
-          mbar_arrive_expect_tx(bar, kWBytes);
+          const uint32_t bar = full0 + 8 * p.stage;
+          grp_arrive_expect_tx<kPair>(bar, kWBytes);
           // features past N are zero-filled
-          tma_load_w(ring + p.stage * stage_size, &wmap, kb * (kFp4 ? kStageKBytes : kStageKBytes / 2), tl.f0, tl.e,
-                     bar);
+          tma_load_w<kPair>(ring + p.stage * stage_size, &wmap, kb * (kFp4 ? kStageKBytes : kStageKBytes / 2),
+                            tl.f0 + rank * kFeat, tl.e, bar);
         }
       }
     }
@@ -350,18 +470,18 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
       if (!ok) raise_status(a.status, kStatusTimeout);
       sb.issued[0] = g;
     }
-  } else if (warp == 1) {
+  } else if (warp == 1 && rank == 0) {
     RingPos p;
     int i = 0, g = 0;
     bool ok = true;
-    for (int t = blockIdx.x; t < tiles_total && ok; t += gridDim.x, ++i) {
-      const Tile tl = find_tile(sb, a, t, lane);
-      const int n16 = (tl.n + 15) & ~15;
+    for (int t = t_first; t < tiles_total && ok; t += t_step, ++i) {
+      const Tile tl = find_tile(sb, a, t, kFeatures, kGrain, lane);
+      const int n16 = (tl.n + kGrain - 1) / kGrain * kGrain;
       const int b = i & 1;
       if (i >= 2) ok = wait_or_abort(smem_u32(&sb.acc_empty[b]), ((i >> 1) - 1) & 1, a.timeout_ns, abort_flag);
       tc_fence_after();
       const uint32_t d = tmem + b * C::kRows;
-      const uint32_t idesc = kFp4 ? idesc_mxf4(n16) : idesc_bf16(n16);
+      const uint32_t idesc = kFp4 ? idesc_mxf4<kPair>(n16) : idesc_bf16<kPair>(n16);
       for (int kb = 0; kb < k_steps && ok; ++kb, ++g, p.next(stages)) {
         ok = wait_or_abort(smem_u32(&sb.full[p.stage]), p.round & 1, a.timeout_ns, abort_flag);
         if (!ok) break;
@@ -373,50 +493,53 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
           if constexpr (kFp4) {
             // this stage's scales: per 128 values of K the weights' block and the rows' blocks
             const uint32_t sf = tmem + 2 * C::kRows + (g & 1) * C::kSfCols;
-            const uint64_t sd = scale_desc(x_addr + a.cap * kStageKBytes);
+            const uint64_t sd = scale_desc(x_addr + stage_rows * kStageKBytes);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              tc_cp_scales(sf + 12 * c, sd + (3 * c) * (kSfBlock >> 4));
-              tc_cp_scales(sf + 12 * c + 4, sd + (3 * c + 1) * (kSfBlock >> 4));
-              if (n16 > 128) tc_cp_scales(sf + 12 * c + 8, sd + (3 * c + 2) * (kSfBlock >> 4));
+              grp_cp_scales<kPair>(sf + 12 * c, sd + (3 * c) * (kSfBlock >> 4));
+              grp_cp_scales<kPair>(sf + 12 * c + 4, sd + (3 * c + 1) * (kSfBlock >> 4));
+              if (n16 > 128) grp_cp_scales<kPair>(sf + 12 * c + 8, sd + (3 * c + 2) * (kSfBlock >> 4));
             }
             const int left = (a.K - kb * C::kStageK + 63) / 64;  // 64-value steps with data
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
               if (kk < left)
-                tc_mma_mxf4(d, wd + 2 * kk, xd + 2 * kk, idesc | idesc_scale_bytes(2 * (kk & 1)), sf + 12 * (kk >> 1),
+                grp_mma_mxf4<kPair>(d, wd + 2 * kk, xd + 2 * kk, idesc | idesc_scale_bytes(2 * (kk & 1)), sf + 12 * (kk >> 1),
                             sf + 12 * (kk >> 1) + 4, (kb | kk) != 0);
             }
           } else {
             const int left = (a.K - kb * C::kStageK + 15) / 16;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
-              if (kk < left) tc_mma_ss(d, wd + 2 * kk, xd + 2 * kk, idesc, (kb | kk) != 0);
+              if (kk < left) grp_mma_bf16<kPair>(d, wd + 2 * kk, xd + 2 * kk, idesc, (kb | kk) != 0);
             }
           }
-          tc_commit(smem_u32(&sb.empty[p.stage]));
-          if (kb == k_steps - 1) tc_commit(smem_u32(&sb.acc_full[b]));
+          grp_commit<kPair>(smem_u32(&sb.empty[p.stage]));
+          if (kb == k_steps - 1) grp_commit<kPair>(smem_u32(&sb.acc_full[b]));
         }
       }
     }
     if (elect_one()) {
       if (!ok) raise_status(a.status, kStatusTimeout);
       // every MMA issued by this thread has finished before TMEM is released
-      tc_commit(smem_u32(&sb.drain));
+      grp_commit<kPair>(smem_u32(&sb.drain));
       if (!mbar_wait(smem_u32(&sb.drain), 0, kDrainTimeoutNs)) raise_status(a.status, kStatusTimeout);
     }
     __syncwarp();
   } else if (kFp4 && (warp == 2 || warp == 3)) {
-    // Scale bytes: a lane keeps rows lane, lane + 32, lane + 64, lane + 96 of each block of
-    // 128; 16 bytes of a row serve two stages, the next 16 are requested one pair ahead.
-    const int used = a.K / 32;  // scale bytes in use
+    // Scale bytes: a lane has rows lane, lane + 32, lane + 64, lane + 96 of each block of 128;
+    // 16 bytes of a row serve two stages.  They travel by asynchronous copies into a place of
+    // the lane's own, requested two pairs of stages ahead, and from there into the ring.
+    const int used = a.K / 32;  // scale bytes in use: zeros stand in for those behind
+    const int pairs = (k_steps + 1) / 2;
+    uint8_t* raw = tiles + kRingBytes + (warp == 2 ? 0 : kRawBlock) + 16 * lane;
     RingPos p;
     int g = 0;
     bool ok = true;
-    for (int t = blockIdx.x; t < tiles_total && ok; t += gridDim.x) {
-      const Tile tl = find_tile(sb, a, t, lane);
+    for (int t = t_first; t < tiles_total && ok; t += t_step) {
+      const Tile tl = find_tile(sb, a, t, kFeatures, kGrain, lane);
       const int blocks = warp == 2 ? 1 : tl.n > 128 ? 2 : 1;
-      const uint8_t* src[2][4];
+      const uint8_t* src[2][4];  // nullptr: no such row, zeros
 #pragma unroll
       for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
@@ -424,8 +547,9 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
           const int r = 128 * blk + 32 * j + lane;
           src[blk][j] = nullptr;
           if (warp == 2) {
-            if (blk == 0 && tl.f0 + r < a.N)
-              src[blk][j] = a.w_scales + (static_cast<long long>(tl.e) * a.N + tl.f0 + r) * a.scale_stride;
+            const int f = tl.f0 + rank * kFeat + r;
+            if (blk == 0 && f < a.N)
+              src[blk][j] = a.w_scales + (static_cast<long long>(tl.e) * a.N + f) * a.scale_stride;
           } else if (r < tl.n) {
             long long row = tl.r0 + r;
             if (a.row_token) {
@@ -435,56 +559,57 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
             src[blk][j] = a.x_scales + row * a.scale_stride;
           }
         }
-      uint4 next[2][4];
       auto request = [&](int pair) {
+        if (pair < pairs) {
+          const uint32_t dst = smem_u32(raw) + (pair % kRawPairs) * 3 * kRawBlock;
+          const int valid = min(16, used - 16 * pair);
 #pragma unroll
-        for (int blk = 0; blk < 2; ++blk)
+          for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            next[blk][j] = make_uint4(0, 0, 0, 0);
-            if (src[blk][j]) next[blk][j] = __ldg(reinterpret_cast<const uint4*>(src[blk][j]) + pair);
-          }
+            for (int j = 0; j < 4; ++j)
+              if (blk < blocks)
+                copy_async16(dst + blk * kRawBlock + 512 * j, src[blk][j] ? src[blk][j] + 16 * pair : a.w_scales,
+                             src[blk][j] ? valid : 0);
+        }
+        copy_async_commit();
       };
       request(0);
-      for (int kb = 0; kb < k_steps && ok; kb += 2) {
-        uint4 cur[2][4];
-        // bytes past K / 32 are padding, whatever they hold
-        uint32_t mask[4];
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const int valid = used - 8 * kb - 4 * w;
-          mask[w] = valid >= 4 ? 0xFFFFFFFFu : valid <= 0 ? 0u : (1u << (8 * valid)) - 1u;
-        }
+      request(1);
+      for (int pair = 0; pair < pairs && ok; ++pair) {
+        request(pair + 2);
+        copy_async_wait<2>();
+        const uint8_t* mine = raw + (pair % kRawPairs) * 3 * kRawBlock;
+        uint4 c[2][4];
 #pragma unroll
         for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            cur[blk][j] = make_uint4(next[blk][j].x & mask[0], next[blk][j].y & mask[1], next[blk][j].z & mask[2],
-                                     next[blk][j].w & mask[3]);
-        if (kb + 2 < k_steps) request((kb + 2) / 2);
+            if (blk < blocks) c[blk][j] = *reinterpret_cast<const uint4*>(mine + blk * kRawBlock + 512 * j);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (kb + h >= k_steps) break;
+          if (2 * pair + h >= k_steps) break;
           if (p.round != 0)
             ok = wait_or_abort(smem_u32(&sb.empty[p.stage]), (p.round - 1) & 1, a.timeout_ns, abort_flag);
           if (!ok) break;
-          uint8_t* sf = tiles + p.stage * stage_size + kWBytes + a.cap * kStageKBytes + (warp == 2 ? 0 : kSfBlock);
+          uint8_t* sf = tiles + p.stage * stage_size + kWBytes + stage_rows * kStageKBytes + (warp == 2 ? 0 : kSfBlock);
 #pragma unroll
           for (int blk = 0; blk < 2; ++blk) {
             if (blk >= blocks) break;
-            const uint4* c = cur[blk];
             reinterpret_cast<uint4*>(sf + blk * kSfBlock)[lane] =
-                h == 0 ? make_uint4(c[0].x, c[1].x, c[2].x, c[3].x) : make_uint4(c[0].z, c[1].z, c[2].z, c[3].z);
+                h == 0 ? make_uint4(c[blk][0].x, c[blk][1].x, c[blk][2].x, c[blk][3].x)
+                       : make_uint4(c[blk][0].z, c[blk][1].z, c[blk][2].z, c[blk][3].z);
             reinterpret_cast<uint4*>(sf + (3 + blk) * kSfBlock)[lane] =
-                h == 0 ? make_uint4(c[0].y, c[1].y, c[2].y, c[3].y) : make_uint4(c[0].w, c[1].w, c[2].w, c[3].w);
+                h == 0 ? make_uint4(c[blk][0].y, c[blk][1].y, c[blk][2].y, c[blk][3].y)
+                       : make_uint4(c[blk][0].w, c[blk][1].w, c[blk][2].w, c[blk][3].w);
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (elect_one()) mbar_arrive(smem_u32(&sb.full[p.stage]));
+          if (elect_one()) grp_arrive<kPair>(full0 + 8 * p.stage);
           ++g;
           p.next(stages);
         }
       }
+      copy_async_wait<0>();
     }
     if (lane == 0) {
       if (!ok) raise_status(a.status, kStatusTimeout);
@@ -492,6 +617,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
     }
   } else if (warp >= kRowWarp0) {
     const int wr = warp - kRowWarp0;
+    constexpr int kSteps = C::kRows / kGrain;
     RingPos p;
     int g = 0;
     bool ok = true;
@@ -508,20 +634,21 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
       auto hand_over = [&]() {
         fence_proxy_async_smem();
         __syncwarp();
-        if (elect_one()) mbar_arrive(smem_u32(&sb.full[done.stage]));
+        if (elect_one()) grp_arrive<kPair>(full0 + 8 * done.stage);
         ++handed;
         done.next(stages);
       };
-      for (int t = blockIdx.x; t < tiles_total && ok; t += gridDim.x) {
-        const Tile tl = find_tile(sb, a, t, lane);
-        const int steps = (tl.n + 15) >> 4;
-        const uint8_t* src[C::kRows / 16];
+      for (int t = t_first; t < tiles_total && ok; t += t_step) {
+        const Tile tl = find_tile(sb, a, t, kFeatures, kGrain, lane);
+        const int half = (tl.n + kGrain - 1) / kGrain * 16;  // rows that this CTA stages
+        const int steps = half >> 4;
+        const uint8_t* src[kSteps];
 #pragma unroll
-        for (int i = 0; i < C::kRows / 16; ++i) {
+        for (int i = 0; i < kSteps; ++i) {
           src[i] = nullptr;
           if (i < steps) {
             // rows behind the tile's last one repeat its first: their columns are never stored
-            const int r = 16 * i + row0;
+            const int r = rank * half + 16 * i + row0;
             int id = __ldg(a.row_token + tl.r0 + (r < tl.n ? r : 0));
             if (id < 0 || id >= a.x_rows) {
               raise_status(a.status, kStatusBadLen);
@@ -537,9 +664,9 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
           const bool data = kb * kStageKBytes + 16 * chunk < row_bytes;  // zeros past the row's end
           const uint32_t dst = ring + p.stage * stage_size + dst0;
 #pragma unroll
-          for (int i = 0; i < C::kRows / 16; ++i)
+          for (int i = 0; i < kSteps; ++i)
             if (i < steps)
-              copy_async16(dst + i * 16 * kStageKBytes, src[i] + (data ? kb * kStageKBytes : 0), data);
+              copy_async16(dst + i * 16 * kStageKBytes, src[i] + (data ? kb * kStageKBytes : 0), data ? 16 : 0);
           copy_async_commit();
           if (g - handed >= kLag) {
             copy_async_wait<kLag>();
@@ -550,19 +677,21 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
       copy_async_wait<0>();
       while (handed < g) hand_over();
     } else {
-      for (int t = blockIdx.x; t < tiles_total && ok; t += gridDim.x) {
-        const Tile tl = find_tile(sb, a, t, lane);
-        const int units = (tl.n + a.box_rows - 1) / a.box_rows, unit = lane * kRowWarps + wr;
+      for (int t = t_first; t < tiles_total && ok; t += t_step) {
+        const Tile tl = find_tile(sb, a, t, kFeatures, kGrain, lane);
+        const int half = (tl.n + kGrain - 1) / kGrain * 16;  // rows that this CTA stages
+        const int units = (half + a.box_rows - 1) / a.box_rows, unit = lane * kRowWarps + wr;
         const int bytes = (units - wr + kRowWarps - 1) / kRowWarps * a.box_rows * kStageKBytes;  // of this warp
         for (int kb = 0; kb < k_steps; ++kb, ++g, p.next(stages)) {
           if (p.round != 0)
             ok = wait_or_abort(smem_u32(&sb.empty[p.stage]), (p.round - 1) & 1, a.timeout_ns, abort_flag);
           if (!ok) break;
-          const uint32_t bar = smem_u32(&sb.full[p.stage]);
-          if (elect_one()) mbar_arrive_expect_tx(bar, bytes);
+          const uint32_t bar = full0 + 8 * p.stage;
+          if (elect_one()) grp_arrive_expect_tx<kPair>(bar, bytes);
           if (unit < units)
-            tma_load_rows(ring + p.stage * stage_size + kWBytes + unit * a.box_rows * kStageKBytes, &xmap,
-                          kb * (kFp4 ? kStageKBytes : kStageKBytes / 2), tl.r0 + a.box_rows * unit, bar);
+            tma_load_rows<kPair>(ring + p.stage * stage_size + kWBytes + unit * a.box_rows * kStageKBytes, &xmap,
+                                 kb * (kFp4 ? kStageKBytes : kStageKBytes / 2),
+                                 tl.r0 + rank * half + a.box_rows * unit, bar);
           __syncwarp();
         }
       }
@@ -576,10 +705,10 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
     const int q = warp & 3;                    // TMEM lane quarter (a warp reaches lanes 32 (warp % 4) ..)
     const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
     int i = 0;
-    for (int t = blockIdx.x; t < tiles_total; t += gridDim.x, ++i) {
-      const Tile tl = find_tile(sb, a, t, lane);
+    for (int t = t_first; t < tiles_total; t += t_step, ++i) {
+      const Tile tl = find_tile(sb, a, t, kFeatures, kGrain, lane);
       const int b = i & 1;
-      const int f = tl.f0 + 32 * q + lane;
+      const int f = tl.f0 + rank * kFeat + 32 * q + lane;
       const bool mine = f < a.N;
       float bias = 0.0f;
       if (a.bias && mine)
@@ -616,35 +745,60 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sb.acc_empty[b]));
+      if (lane == 0) grp_arrive<kPair>(acc_empty0 + 8 * b);
     }
   }
 
   tc_fence_before();
   __syncthreads();
-  if (threadIdx.x == 0 && *abort_flag) {
+  if constexpr (kPair) cluster_sync();
+  if (threadIdx.x == 0 && rank == 0) {
     // Copies still in flight land before the shared memory is released.  A stage completes once
     // every producer warp has arrived; those that gave up earlier than others are less than
     // one round of the ring behind, and their arrivals are made up for here.
-    int most = 0;
-    for (int w = 0; w < C::kProducers; ++w) most = sb.issued[w] > most ? sb.issued[w] : most;
-    for (int w = 0; w < C::kProducers; ++w)
-      for (int g = sb.issued[w]; g < most; ++g) mbar_arrive(smem_u32(&sb.full[g % stages]));
-    for (int s = 0; s < stages && s < most; ++s) {
-      const int last = most - 1 - ((most - 1 - s) % stages);
-      if (!mbar_wait(smem_u32(&sb.full[s]), (last / stages) & 1, kDrainTimeoutNs)) raise_status(a.status, kStatusTimeout);
+    auto peer = [&](const int* v, int cta) {
+      int x;
+      if constexpr (kPair)
+        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(dsmem_addr(smem_u32(v), cta)) : "memory");
+      else
+        x = *const_cast<const volatile int*>(v);
+      return x;
+    };
+    int aborted = 0, most = 0;
+    for (int c = 0; c < kCtas; ++c) {
+      aborted |= peer(&sb.abort_flag, c);
+      for (int w = 0; w < C::kProducers; ++w) most = max(most, peer(&sb.issued[w], c));
+    }
+    if (aborted) {
+      for (int c = 0; c < kCtas; ++c)
+        for (int w = 0; w < C::kProducers; ++w)
+          for (int g = peer(&sb.issued[w], c); g < most; ++g) grp_arrive<kPair>(full0 + 8 * (g % stages));
+      for (int s = 0; s < stages && s < most; ++s) {
+        const int last = most - 1 - ((most - 1 - s) % stages);
+        if (!mbar_wait(smem_u32(&sb.full[s]), (last / stages) & 1, kDrainTimeoutNs))
+          raise_status(a.status, kStatusTimeout);
+      }
     }
   }
-  __syncthreads();
+  if constexpr (kPair) {
+    // the leader's last arrival here is behind all its earlier ones: none is still to come
+    if (threadIdx.x == 0 && rank != 0 && !mbar_wait(smem_u32(&sb.drain), 0, kDrainTimeoutNs))
+      raise_status(a.status, kStatusTimeout);
+    __syncthreads();
+    cluster_sync();
+  } else {
+    __syncthreads();
+  }
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, C::kTmemCols);
+    grp_tmem_dealloc<kPair>(tmem, C::kTmemCols);
   }
 }
 
-template <bool kFp4, bool kSwiglu>
+template <bool kFp4, bool kSwiglu, bool kPair>
 cudaError_t launch_grouped_t(const CUtensorMap& wmap, const CUtensorMap& xmap, const GroupedArgs& a, int sms,
                              cudaStream_t stream) {
+  auto kernel = grouped_kernel<kFp4, kSwiglu, kPair>;
   // the shared-memory opt-in, once per device (host threads may race here: atomic flags,
   // and setting the attribute twice is harmless)
   static std::atomic<bool> attr_set[64];
@@ -652,37 +806,59 @@ cudaError_t launch_grouped_t(const CUtensorMap& wmap, const CUtensorMap& xmap, c
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !attr_set[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(grouped_kernel<kFp4, kSwiglu>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kSmemBytes));
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem_bytes<kFp4>()));
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev].store(true, std::memory_order_release);
   }
+  constexpr int kCtas = kPair ? 2 : 1;
   GroupedArgs b = a;
-  b.stages = stage_count<kFp4>(a.cap);
+  b.stages = stage_count<kFp4>(a.cap / kCtas);
   // no more CTAs than tiles there can be
   const long long groups = a.num_experts < a.rows ? a.num_experts : a.rows;
   const long long most = (a.rows / a.cap + groups) * a.tiles_f;
-  const int grid = static_cast<int>(most < sms ? most : sms);
-  grouped_kernel<kFp4, kSwiglu><<<grid, kThreads, kSmemBytes, stream>>>(wmap, xmap, b);
-  return cudaGetLastError();
+  const int slots = sms / kCtas;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((most < slots ? most : slots) * kCtas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem_bytes<kFp4>();
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kCtas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kPair ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, wmap, xmap, b);
+}
+
+template <bool kFp4>
+cudaError_t launch_grouped_f(const CUtensorMap& wmap, const CUtensorMap& xmap, const GroupedArgs& a, int sms,
+                             cudaStream_t stream) {
+  if (a.pair)
+    return a.swiglu ? launch_grouped_t<kFp4, true, true>(wmap, xmap, a, sms, stream)
+                    : launch_grouped_t<kFp4, false, true>(wmap, xmap, a, sms, stream);
+  return a.swiglu ? launch_grouped_t<kFp4, true, false>(wmap, xmap, a, sms, stream)
+                  : launch_grouped_t<kFp4, false, false>(wmap, xmap, a, sms, stream);
 }
 
 }  // namespace
 
-int grouped_tile_rows(bool mxfp4, int rows, int num_experts) {
-  // 64 while the experts have few rows on average: the ring's stages are then small and many
-  // (8 instead of 4), which keeps more weight bytes in flight
-  const int most = mxfp4 ? GrpCfg<true>::kRows : GrpCfg<false>::kRows;
-  return rows <= 32LL * num_experts ? 64 : most;
+void grouped_plan(GroupedArgs& a, bool mxfp4) {
+  // Few rows per expert on average: single CTAs and at most 64 rows per tile, so the ring's
+  // stages are small and many, which keeps more weight bytes in flight.  More rows: CTA pairs,
+  // which stage a tile's rows once for 256 features.
+  a.pair = a.rows > 32LL * a.num_experts;
+  a.cap = !a.pair ? 64 : mxfp4 ? GrpCfg<true>::kRows : GrpCfg<false>::kRows;
+  a.box_rows = 16;
+  const int features = (a.pair ? 2 : 1) * kFeat;
+  a.tiles_f = static_cast<int>((static_cast<long long>(a.N) + features - 1) / features);
 }
 
 cudaError_t launch_grouped(const CUtensorMap& wmap, const CUtensorMap& xmap, const GroupedArgs& a, bool mxfp4,
                            int sms, cudaStream_t stream) {
-  if (mxfp4)
-    return a.swiglu ? launch_grouped_t<true, true>(wmap, xmap, a, sms, stream)
-                    : launch_grouped_t<true, false>(wmap, xmap, a, sms, stream);
-  return a.swiglu ? launch_grouped_t<false, true>(wmap, xmap, a, sms, stream)
-                  : launch_grouped_t<false, false>(wmap, xmap, a, sms, stream);
+  return mxfp4 ? launch_grouped_f<true>(wmap, xmap, a, sms, stream) : launch_grouped_f<false>(wmap, xmap, a, sms, stream);
 }
 
 }  // namespace sa

@@ -22,8 +22,9 @@ struct GroupedArgs {
   int x_rows, rows, num_experts, N, K;
   int n_out;    // features written per row: N, or N / 2 with swiglu
   int tiles_f;  // feature tiles (of N)
+  int pair;     // tiles of CTA pairs: 256 features (else 128)
   int cap;      // most rows of a tile
-  int box_rows; // rows of xmap's boxes: divides cap
+  int box_rows; // rows of xmap's boxes
   int stages;   // ring stages (set by the launcher)
   int swiglu;
   float alpha, limit;
@@ -31,10 +32,10 @@ struct GroupedArgs {
   unsigned long long timeout_ns;
 };
 
-// Most rows of one tile (the largest MMA N) for `rows` rows over `num_experts` experts: a
-// multiple of 32, at most 256 (bf16) or 224 (MXFP4, whose scales take TMEM columns beside the
+// The tiling (pair, cap, box_rows, tiles_f) for a.rows, a.num_experts and a.N.  cap is at
+// least 64, at most 256 in bf16 and 224 in MXFP4 (whose scales take TMEM columns beside the
 // accumulators).
-int grouped_tile_rows(bool mxfp4, int rows, int num_experts);
+void grouped_plan(GroupedArgs& a, bool mxfp4);
 // wmap: w as {K, N, E} in boxes of 128 bytes x 128 x 1;
 // xmap: x [x_rows, K] in boxes of 128 bytes x box_rows.
 cudaError_t launch_grouped(const CUtensorMap& wmap, const CUtensorMap& xmap, const GroupedArgs& a, bool mxfp4,
