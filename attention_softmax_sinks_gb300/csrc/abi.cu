@@ -97,16 +97,16 @@ sa_status map_matrix(CUtensorMap* m, const void* base, long long rows, long long
   return r == CUDA_SUCCESS ? SA_OK : SA_ERR_CUDA;
 }
 
-// Expert weights [experts, n, row_bytes] read in boxes of 128 bytes x 128 features.
+// Expert weights [experts, n, row_bytes] read in boxes of 128 bytes x box_n features.
 sa_status map_experts(CUtensorMap* m, const void* base, long long experts, long long n, long long row_bytes,
-                      bool bytes) {
+                      int box_n, bool bytes) {
   PFN_cuTensorMapEncodeTiled_v12000 enc;
   if (sa_status s = encoder(&enc)) return s;
   const int size = bytes ? 1 : 2;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(row_bytes / size), static_cast<cuuint64_t>(n),
                         static_cast<cuuint64_t>(experts)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(row_bytes) * n};
-  cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / size), sa::kGroupedFeatures, 1};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / size), static_cast<cuuint32_t>(box_n), 1};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = enc(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
                    const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -311,8 +311,8 @@ sa_status grouped_common(const GroupedCall& c, cudaStream_t stream) {
     return SA_ERR_ALIGNMENT;
   sa::GroupedArgs a{};
   a.n_out = c.swiglu ? c.n / 2 : c.n;
-  const long long blocks_f = (static_cast<long long>(c.n) + sa::kGroupedFeatures - 1) / sa::kGroupedFeatures;
-  if ((c.rows / 64LL + c.experts) * blocks_f >= (1LL << 30)) return SA_ERR_SHAPE;  // more tiles than are counted
+  // more tiles than the kernel counts
+  if ((c.rows / 16LL + c.experts) * (c.n / 64LL + 1) >= (1LL << 30)) return SA_ERR_SHAPE;
   unsigned* status = nullptr;
   if (sa_status s = status_ptr(&status)) return s;
   a.bias = static_cast<const uint16_t*>(c.bias);
@@ -333,12 +333,13 @@ sa_status grouped_common(const GroupedCall& c, cudaStream_t stream) {
   a.status = status;
   a.timeout_ns = g_timeout_ns;
   a.x = static_cast<const uint8_t*>(c.x);
-  sa::grouped_plan(a, c.mxfp4);
+  const int sms = sm_count();
+  sa::grouped_plan(a, c.mxfp4, sms);
   const long long row_bytes = c.mxfp4 ? c.k / 2 : 2LL * c.k;
   CUtensorMap wm, xm;
-  if (sa_status s = map_experts(&wm, c.w, c.experts, c.n, row_bytes, c.mxfp4)) return s;
-  if (sa_status s = map_rows(&xm, c.x, c.x_rows, row_bytes, a.box_rows, c.mxfp4)) return s;
-  return sa::launch_grouped(wm, xm, a, c.mxfp4, sm_count(), stream) == cudaSuccess ? SA_OK : SA_ERR_LAUNCH;
+  if (sa_status s = map_experts(&wm, c.w, c.experts, c.n, row_bytes, a.width, c.mxfp4)) return s;
+  if (sa_status s = map_rows(&xm, c.x, c.x_rows, row_bytes, sa::kBoxRows, c.mxfp4)) return s;
+  return sa::launch_grouped(wm, xm, a, c.mxfp4, sms, stream) == cudaSuccess ? SA_OK : SA_ERR_LAUNCH;
 }
 
 sa_status check_mxfp4(long long rows, int k) {

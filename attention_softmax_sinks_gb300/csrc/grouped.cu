@@ -13,8 +13,7 @@
 //   warp 0        loads the weights of a ring stage (one box of 128 features x 128 bytes of K,
 //                 128-byte swizzle) when it is free
 //   warp 1        TMEM owner and MMA issuer (one elected thread): 32 bytes of K per MMA
-//   warps 2, 3    MXFP4: scale bytes of the weights (2) and of the rows (3): 16 bytes per row
-//                 serve two stages, written into the ring in the layout that tcgen05.cp
+//   warps 2, 3    MXFP4: scale bytes of the weights (2) and of the rows (3), written into the ring in the layout that tcgen05.cp
 //                 spreads over TMEM (row r of a block of 128: 4 bytes at 16 (r % 32) + 4 (r / 32),
 //                 512 bytes per 128 values of K)
 //   warps 4..11   epilogue: thread = one feature (TMEM lane), columns = rows; bias and
@@ -46,9 +45,9 @@ constexpr int kRowWarp0 = kEpiWarp0 + kEpiWarps;
 constexpr int kRowWarps = 4;
 constexpr int kMaxProducers = 3 + kRowWarps;  // weights, rows, and in MXFP4 two warps of scales
 constexpr int kThreads = 32 * (kRowWarp0 + kRowWarps);
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 16;
 constexpr int kRingBytes = 198 * 1024;
-constexpr int kWBytes = kFeat * kStageKBytes;
+constexpr int kMaxSingleRows = 64;  // rows of a single CTA's tile
 constexpr int kLag = 2;         // stages between a gather's request and its hand-over
 constexpr int kBand = 8;        // row tiles of an expert that pass over its features together
 constexpr int kSfBlock = 512;   // scales of 128 rows x 128 values of K
@@ -69,16 +68,20 @@ struct GrpCfg {
   static_assert(2 * kRows + (kFp4 ? 2 * kSfCols : 0) <= kTmemCols, "TMEM holds 512 columns");
 };
 
-// A stage holds kWBytes of weights, `rows` rows of 128 bytes (a CTA of a pair stages half of
-// the tile's), and the scales.  rows is a multiple of 16, so the parts start on multiples of
-// 1024 bytes (the swizzle atom).
+// A stage holds `sub` blocks of kStageKBytes of K: `width` features and `rows` rows of 128 bytes
+// in each (a CTA of a pair stages half of the tile's rows), then the blocks' scales.  width and
+// rows are multiples of 16, so the parts start on multiples of 1024 bytes (the swizzle atom).
 template <bool kFp4>
-__host__ __device__ constexpr int stage_bytes(int rows) {
-  return (kWBytes + rows * kStageKBytes + GrpCfg<kFp4>::kSfBytes + 1023) / 1024 * 1024;
+__host__ __device__ constexpr int stage_bytes(int width, int rows, int sub) {
+  return (sub * ((width + rows) * kStageKBytes + GrpCfg<kFp4>::kSfBytes) + 1023) / 1024 * 1024;
 }
+// An MMA reads 128 features also where the tile has fewer: at the end of the last stage, too,
+// that stays inside the ring (what it reads there goes to accumulator lanes that are never stored).
 template <bool kFp4>
-__host__ __device__ constexpr int stage_count(int rows) {
-  return kRingBytes / stage_bytes<kFp4>(rows) < kMaxStages ? kRingBytes / stage_bytes<kFp4>(rows) : kMaxStages;
+__host__ __device__ constexpr int stage_count(int width, int rows, int sub) {
+  const int size = stage_bytes<kFp4>(width, rows, sub);
+  const int n = (kRingBytes - (kFeat - width) * kStageKBytes) / size;
+  return n < kMaxStages ? n : kMaxStages;
 }
 
 struct GrpShared {
@@ -272,6 +275,10 @@ __device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* m
 __device__ __forceinline__ void copy_async16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+// A piece of memory towards L2 (address and size: multiples of 16).
+__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copy_async_wait() {  // all but the N newest groups
@@ -352,15 +359,19 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
   volatile int* abort_flag = &sb.abort_flag;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int k_steps = (a.K + C::kStageK - 1) / C::kStageK;
+  const int k_blocks = (a.K + C::kStageK - 1) / C::kStageK;  // of kStageKBytes
+  const int sub = kPair ? 1 : a.sub;                         // blocks per stage
+  const int k_steps = (k_blocks + sub - 1) / sub;
   const int stages = a.stages;
   const uint32_t ring = smem_u32(tiles);
   // a pair stages half of a tile's rows in each CTA
   constexpr int kCtas = kPair ? 2 : 1;
   constexpr int kGrain = 16 * kCtas;
-  constexpr int kFeatures = kCtas * kFeat;
   const int stage_rows = a.cap / kCtas;
-  const uint32_t stage_size = stage_bytes<kFp4>(stage_rows);
+  const int width = kPair ? kFeat : a.width;  // features of one CTA's part of a tile
+  const uint32_t w_bytes = width * kStageKBytes;
+  const uint32_t stage_size = stage_bytes<kFp4>(width, stage_rows, sub);
+  const uint32_t x_part = sub * w_bytes, sf_part = x_part + sub * stage_rows * kStageKBytes;  // of a stage
   const int rank = kPair ? static_cast<int>(cluster_ctarank()) : 0;
   const int t_first = blockIdx.x / kCtas, t_step = gridDim.x / kCtas;
   // the leading CTA's barriers
@@ -368,6 +379,8 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
   const uint32_t acc_empty0 = kPair ? dsmem_addr(smem_u32(&sb.acc_empty[0]), 0) : smem_u32(&sb.acc_empty[0]);
 
   if (threadIdx.x == 0) {
+    tma_prefetch_desc(&wmap);
+    tma_prefetch_desc(&xmap);
     for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(smem_u32(&sb.full[s]), kCtas * C::kProducers);
       mbar_init(smem_u32(&sb.empty[s]), 1);
@@ -444,25 +457,23 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
   const int tiles_total = sb.total * a.tiles_f;
 
   if (warp == 0) {
-    if (elect_one()) {
-      tma_prefetch_desc(&wmap);
-      tma_prefetch_desc(&xmap);
-    }
     RingPos p;
     int g = 0;
     bool ok = true;
     for (int t = t_first; t < tiles_total && ok; t += t_step) {
-      const Tile tl = find_tile(sb, a, t, kFeatures, kGrain, lane);
+      const Tile tl = find_tile(sb, a, t, kCtas * width, kGrain, lane);
       for (int kb = 0; kb < k_steps; ++kb, ++g, p.next(stages)) {
         if (p.round != 0)
           ok = wait_or_abort(smem_u32(&sb.empty[p.stage]), (p.round - 1) & 1, a.timeout_ns, abort_flag);
         if (!ok) break;
         if (elect_one()) {
           const uint32_t bar = full0 + 8 * p.stage;
-          grp_arrive_expect_tx<kPair>(bar, kWBytes);
-          // features past N are zero-filled
-          tma_load_w<kPair>(ring + p.stage * stage_size, &wmap, kb * (kFp4 ? kStageKBytes : kStageKBytes / 2),
-                            tl.f0 + rank * kFeat, tl.e, bar);
+          const int blocks = kPair ? 1 : min(sub, k_blocks - kb * sub);
+          grp_arrive_expect_tx<kPair>(bar, blocks * w_bytes);
+          for (int u = 0; u == 0 || (!kPair && u < blocks); ++u)  // features past N are zero-filled
+            tma_load_w<kPair>(ring + p.stage * stage_size + u * w_bytes, &wmap,
+                              (kb * sub + u) * (kFp4 ? kStageKBytes : kStageKBytes / 2), tl.f0 + rank * kFeat, tl.e,
+                              bar);
         }
       }
     }
@@ -472,46 +483,52 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
     }
   } else if (warp == 1 && rank == 0) {
     RingPos p;
-    int i = 0, g = 0;
+    int i = 0, scales = 0;
     bool ok = true;
     for (int t = t_first; t < tiles_total && ok; t += t_step, ++i) {
-      const Tile tl = find_tile(sb, a, t, kFeatures, kGrain, lane);
+      const Tile tl = find_tile(sb, a, t, kCtas * width, kGrain, lane);
       const int n16 = (tl.n + kGrain - 1) / kGrain * kGrain;
       const int b = i & 1;
       if (i >= 2) ok = wait_or_abort(smem_u32(&sb.acc_empty[b]), ((i >> 1) - 1) & 1, a.timeout_ns, abort_flag);
       tc_fence_after();
       const uint32_t d = tmem + b * C::kRows;
       const uint32_t idesc = kFp4 ? idesc_mxf4<kPair>(n16) : idesc_bf16<kPair>(n16);
-      for (int kb = 0; kb < k_steps && ok; ++kb, ++g, p.next(stages)) {
+      for (int kb = 0; kb < k_steps && ok; ++kb, p.next(stages)) {
         ok = wait_or_abort(smem_u32(&sb.full[p.stage]), p.round & 1, a.timeout_ns, abort_flag);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t w_addr = ring + p.stage * stage_size;
-        const uint32_t x_addr = w_addr + kWBytes;
-        const uint64_t wd = sw128_kmajor_desc(w_addr), xd = sw128_kmajor_desc(x_addr);
+        const uint32_t stage = ring + p.stage * stage_size;
+        const int blocks = kPair ? 1 : min(sub, k_blocks - kb * sub);
         if (elect_one()) {
-          if constexpr (kFp4) {
-            // this stage's scales: per 128 values of K the weights' block and the rows' blocks
-            const uint32_t sf = tmem + 2 * C::kRows + (g & 1) * C::kSfCols;
-            const uint64_t sd = scale_desc(x_addr + stage_rows * kStageKBytes);
+#pragma unroll 1
+          for (int u = 0; u == 0 || (!kPair && u < blocks); ++u) {
+            const uint64_t wd = sw128_kmajor_desc(stage + u * w_bytes);
+            const uint64_t xd = sw128_kmajor_desc(stage + x_part + u * stage_rows * kStageKBytes);
+            const int block = kb * sub + u;
+            if constexpr (kFp4) {
+              // this block's scales: per 128 values of K the weights' and the rows'
+              const uint32_t sf = tmem + 2 * C::kRows + (scales & 1) * C::kSfCols;
+              const uint64_t sd = scale_desc(stage + sf_part + u * C::kSfBytes);
+              ++scales;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              grp_cp_scales<kPair>(sf + 12 * c, sd + (3 * c) * (kSfBlock >> 4));
-              grp_cp_scales<kPair>(sf + 12 * c + 4, sd + (3 * c + 1) * (kSfBlock >> 4));
-              if (n16 > 128) grp_cp_scales<kPair>(sf + 12 * c + 8, sd + (3 * c + 2) * (kSfBlock >> 4));
-            }
-            const int left = (a.K - kb * C::kStageK + 63) / 64;  // 64-value steps with data
+              for (int c = 0; c < 2; ++c) {
+                grp_cp_scales<kPair>(sf + 12 * c, sd + (3 * c) * (kSfBlock >> 4));
+                grp_cp_scales<kPair>(sf + 12 * c + 4, sd + (3 * c + 1) * (kSfBlock >> 4));
+                if (n16 > 128) grp_cp_scales<kPair>(sf + 12 * c + 8, sd + (3 * c + 2) * (kSfBlock >> 4));
+              }
+              const int left = (a.K - block * C::kStageK + 63) / 64;  // 64-value steps with data
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              if (kk < left)
-                grp_mma_mxf4<kPair>(d, wd + 2 * kk, xd + 2 * kk, idesc | idesc_scale_bytes(2 * (kk & 1)), sf + 12 * (kk >> 1),
-                            sf + 12 * (kk >> 1) + 4, (kb | kk) != 0);
-            }
-          } else {
-            const int left = (a.K - kb * C::kStageK + 15) / 16;
+              for (int kk = 0; kk < 4; ++kk) {
+                if (kk < left)
+                  grp_mma_mxf4<kPair>(d, wd + 2 * kk, xd + 2 * kk, idesc | idesc_scale_bytes(2 * (kk & 1)),
+                                      sf + 12 * (kk >> 1), sf + 12 * (kk >> 1) + 4, (block | kk) != 0);
+              }
+            } else {
+              const int left = (a.K - block * C::kStageK + 15) / 16;
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              if (kk < left) grp_mma_bf16<kPair>(d, wd + 2 * kk, xd + 2 * kk, idesc, (kb | kk) != 0);
+              for (int kk = 0; kk < 4; ++kk) {
+                if (kk < left) grp_mma_bf16<kPair>(d, wd + 2 * kk, xd + 2 * kk, idesc, (block | kk) != 0);
+              }
             }
           }
           grp_commit<kPair>(smem_u32(&sb.empty[p.stage]));
@@ -528,16 +545,16 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
     __syncwarp();
   } else if (kFp4 && (warp == 2 || warp == 3)) {
     // Scale bytes: a lane has rows lane, lane + 32, lane + 64, lane + 96 of each block of 128;
-    // 16 bytes of a row serve two stages.  They travel by asynchronous copies into a place of
-    // the lane's own, requested two pairs of stages ahead, and from there into the ring.
+    // 16 bytes of a row serve two blocks of K.  They travel by asynchronous copies into a place of
+    // the lane's own, requested two pairs of blocks ahead, and from there into the ring.
     const int used = a.K / 32;  // scale bytes in use: zeros stand in for those behind
-    const int pairs = (k_steps + 1) / 2;
+    const int pairs = (k_blocks + 1) / 2;
     uint8_t* raw = tiles + kRingBytes + (warp == 2 ? 0 : kRawBlock) + 16 * lane;
     RingPos p;
     int g = 0;
     bool ok = true;
     for (int t = t_first; t < tiles_total && ok; t += t_step) {
-      const Tile tl = find_tile(sb, a, t, kFeatures, kGrain, lane);
+      const Tile tl = find_tile(sb, a, t, kCtas * width, kGrain, lane);
       const int blocks = warp == 2 ? 1 : tl.n > 128 ? 2 : 1;
       const uint8_t* src[2][4];  // nullptr: no such row, zeros
 #pragma unroll
@@ -548,7 +565,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
           src[blk][j] = nullptr;
           if (warp == 2) {
             const int f = tl.f0 + rank * kFeat + r;
-            if (blk == 0 && f < a.N)
+            if (blk == 0 && r < width && f < a.N)
               src[blk][j] = a.w_scales + (static_cast<long long>(tl.e) * a.N + f) * a.scale_stride;
           } else if (r < tl.n) {
             long long row = tl.r0 + r;
@@ -573,6 +590,14 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
         }
         copy_async_commit();
       };
+      // The next tile's weight scales are one piece of memory: into L2 with them now, in one
+      // go, instead of 32 bytes per row and request.
+      if (warp == 2 && t + t_step < tiles_total) {
+        const Tile nx = find_tile(sb, a, t + t_step, kCtas * width, kGrain, lane);
+        const int f = nx.f0 + rank * kFeat, rows = min(width, a.N - f);
+        if (rows > 0 && elect_one())
+          prefetch_l2(a.w_scales + (static_cast<long long>(nx.e) * a.N + f) * a.scale_stride, rows * a.scale_stride);
+      }
       request(0);
       request(1);
       for (int pair = 0; pair < pairs && ok; ++pair) {
@@ -587,11 +612,13 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
             if (blk < blocks) c[blk][j] = *reinterpret_cast<const uint4*>(mine + blk * kRawBlock + 512 * j);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (2 * pair + h >= k_steps) break;
-          if (p.round != 0)
+          const int block = 2 * pair + h;
+          if (block >= k_blocks) break;
+          const int u = sub == 2 ? h : 0;
+          if (u == 0 && p.round != 0)
             ok = wait_or_abort(smem_u32(&sb.empty[p.stage]), (p.round - 1) & 1, a.timeout_ns, abort_flag);
           if (!ok) break;
-          uint8_t* sf = tiles + p.stage * stage_size + kWBytes + stage_rows * kStageKBytes + (warp == 2 ? 0 : kSfBlock);
+          uint8_t* sf = tiles + p.stage * stage_size + sf_part + u * C::kSfBytes + (warp == 2 ? 0 : kSfBlock);
 #pragma unroll
           for (int blk = 0; blk < 2; ++blk) {
             if (blk >= blocks) break;
@@ -602,11 +629,13 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
                 h == 0 ? make_uint4(c[blk][0].y, c[blk][1].y, c[blk][2].y, c[blk][3].y)
                        : make_uint4(c[blk][0].w, c[blk][1].w, c[blk][2].w, c[blk][3].w);
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (elect_one()) grp_arrive<kPair>(full0 + 8 * p.stage);
-          ++g;
-          p.next(stages);
+          if (u + 1 == sub || block + 1 == k_blocks) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (elect_one()) grp_arrive<kPair>(full0 + 8 * p.stage);
+            ++g;
+            p.next(stages);
+          }
         }
       }
       copy_async_wait<0>();
@@ -617,7 +646,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
     }
   } else if (warp >= kRowWarp0) {
     const int wr = warp - kRowWarp0;
-    constexpr int kSteps = C::kRows / kGrain;
+    constexpr int kSteps = kPair ? C::kRows / kGrain : kMaxSingleRows / 16;
     RingPos p;
     int g = 0;
     bool ok = true;
@@ -628,7 +657,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
       const int tid = threadIdx.x - 32 * kRowWarp0;
       const int chunk = tid & 7, row0 = tid >> 3;
       const long long row_bytes = kFp4 ? a.K / 2 : 2LL * a.K;
-      const uint32_t dst0 = kWBytes + row0 * kStageKBytes + ((chunk ^ (row0 & 7)) << 4);
+      const uint32_t dst0 = x_part + row0 * kStageKBytes + ((chunk ^ (row0 & 7)) << 4);
       RingPos done;
       int handed = 0;
       auto hand_over = [&]() {
@@ -639,7 +668,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
         done.next(stages);
       };
       for (int t = t_first; t < tiles_total && ok; t += t_step) {
-        const Tile tl = find_tile(sb, a, t, kFeatures, kGrain, lane);
+        const Tile tl = find_tile(sb, a, t, kCtas * width, kGrain, lane);
         const int half = (tl.n + kGrain - 1) / kGrain * 16;  // rows that this CTA stages
         const int steps = half >> 4;
         const uint8_t* src[kSteps];
@@ -661,12 +690,16 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
           if (p.round != 0)
             ok = wait_or_abort(smem_u32(&sb.empty[p.stage]), (p.round - 1) & 1, a.timeout_ns, abort_flag);
           if (!ok) break;
-          const bool data = kb * kStageKBytes + 16 * chunk < row_bytes;  // zeros past the row's end
-          const uint32_t dst = ring + p.stage * stage_size + dst0;
+          const int blocks = kPair ? 1 : min(sub, k_blocks - kb * sub);
+#pragma unroll 1
+          for (int u = 0; u == 0 || (!kPair && u < blocks); ++u) {
+            const int at = (kb * sub + u) * kStageKBytes;
+            const bool data = at + 16 * chunk < row_bytes;  // zeros past the row's end
+            const uint32_t dst = ring + p.stage * stage_size + dst0 + u * stage_rows * kStageKBytes;
 #pragma unroll
-          for (int i = 0; i < kSteps; ++i)
-            if (i < steps)
-              copy_async16(dst + i * 16 * kStageKBytes, src[i] + (data ? kb * kStageKBytes : 0), data ? 16 : 0);
+            for (int i = 0; i < kSteps; ++i)
+              if (i < steps) copy_async16(dst + i * 16 * kStageKBytes, src[i] + (data ? at : 0), data ? 16 : 0);
+          }
           copy_async_commit();
           if (g - handed >= kLag) {
             copy_async_wait<kLag>();
@@ -678,20 +711,24 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
       while (handed < g) hand_over();
     } else {
       for (int t = t_first; t < tiles_total && ok; t += t_step) {
-        const Tile tl = find_tile(sb, a, t, kFeatures, kGrain, lane);
+        const Tile tl = find_tile(sb, a, t, kCtas * width, kGrain, lane);
         const int half = (tl.n + kGrain - 1) / kGrain * 16;  // rows that this CTA stages
-        const int units = (half + a.box_rows - 1) / a.box_rows, unit = lane * kRowWarps + wr;
-        const int bytes = (units - wr + kRowWarps - 1) / kRowWarps * a.box_rows * kStageKBytes;  // of this warp
+        // the boxes of all blocks of a stage, dealt out to the warps
+        const int units = half / kBoxRows, box = lane * kRowWarps + wr;
+        const int u = kPair ? 0 : box / units, unit = box - u * units;
+        const uint32_t dst = ring + x_part + (u * stage_rows + unit * kBoxRows) * kStageKBytes;
+        const int row = tl.r0 + rank * half + kBoxRows * unit;
         for (int kb = 0; kb < k_steps; ++kb, ++g, p.next(stages)) {
           if (p.round != 0)
             ok = wait_or_abort(smem_u32(&sb.empty[p.stage]), (p.round - 1) & 1, a.timeout_ns, abort_flag);
           if (!ok) break;
+          const int boxes = (kPair ? 1 : min(sub, k_blocks - kb * sub)) * units;
           const uint32_t bar = full0 + 8 * p.stage;
-          if (elect_one()) grp_arrive_expect_tx<kPair>(bar, bytes);
-          if (unit < units)
-            tma_load_rows<kPair>(ring + p.stage * stage_size + kWBytes + unit * a.box_rows * kStageKBytes, &xmap,
-                                 kb * (kFp4 ? kStageKBytes : kStageKBytes / 2),
-                                 tl.r0 + rank * half + a.box_rows * unit, bar);
+          if (elect_one())
+            grp_arrive_expect_tx<kPair>(bar, (boxes - wr + kRowWarps - 1) / kRowWarps * kBoxRows * kStageKBytes);
+          if (box < boxes)
+            tma_load_rows<kPair>(dst + p.stage * stage_size, &xmap,
+                                 (kb * sub + u) * (kFp4 ? kStageKBytes : kStageKBytes / 2), row, bar);
           __syncwarp();
         }
       }
@@ -706,10 +743,10 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
     const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
     int i = 0;
     for (int t = t_first; t < tiles_total; t += t_step, ++i) {
-      const Tile tl = find_tile(sb, a, t, kFeatures, kGrain, lane);
+      const Tile tl = find_tile(sb, a, t, kCtas * width, kGrain, lane);
       const int b = i & 1;
       const int f = tl.f0 + rank * kFeat + 32 * q + lane;
-      const bool mine = f < a.N;
+      const bool mine = 32 * q + lane < width && f < a.N;
       float bias = 0.0f;
       if (a.bias && mine)
         bias = __uint_as_float(static_cast<uint32_t>(__ldg(a.bias + static_cast<long long>(tl.e) * a.N + f)) << 16);
@@ -813,7 +850,7 @@ cudaError_t launch_grouped_t(const CUtensorMap& wmap, const CUtensorMap& xmap, c
   }
   constexpr int kCtas = kPair ? 2 : 1;
   GroupedArgs b = a;
-  b.stages = stage_count<kFp4>(a.cap / kCtas);
+  b.stages = stage_count<kFp4>(kPair ? kFeat : a.width, a.cap / kCtas, kPair ? 1 : a.sub);
   // no more CTAs than tiles there can be
   const long long groups = a.num_experts < a.rows ? a.num_experts : a.rows;
   const long long most = (a.rows / a.cap + groups) * a.tiles_f;
@@ -845,14 +882,36 @@ cudaError_t launch_grouped_f(const CUtensorMap& wmap, const CUtensorMap& xmap, c
 
 }  // namespace
 
-void grouped_plan(GroupedArgs& a, bool mxfp4) {
-  // Few rows per expert on average: single CTAs and at most 64 rows per tile, so the ring's
-  // stages are small and many, which keeps more weight bytes in flight.  More rows: CTA pairs,
-  // which stage a tile's rows once for 256 features.
+void grouped_plan(GroupedArgs& a, bool mxfp4, int sms) {
+  // More than 32 rows per expert on average: CTA pairs, which stage a tile's rows once for 256
+  // features.  Fewer: single CTAs and small tiles, so that the ring's stages are small and many
+  // and keep more weight bytes in flight.
   a.pair = a.rows > 32LL * a.num_experts;
-  a.cap = !a.pair ? 64 : mxfp4 ? GrpCfg<true>::kRows : GrpCfg<false>::kRows;
-  a.box_rows = 16;
-  const int features = (a.pair ? 2 : 1) * kFeat;
+  a.cap = a.pair ? (mxfp4 ? GrpCfg<true>::kRows : GrpCfg<false>::kRows) : a.rows > 2LL * a.num_experts ? kMaxSingleRows : 16;
+  a.width = kFeat;
+  a.sub = 1;
+  if (!a.pair) {
+    // The width that lets the last round of tiles end soonest, were every group one row tile;
+    // a tile costs about as much as 48 features more.  (One token, four experts, 2880 -> 5760:
+    // 80 features, 288 tiles in two rounds, instead of 180 tiles of 128 in two.)
+    const long long groups = a.num_experts < a.rows ? a.num_experts : a.rows;
+    long long best = -1;
+    for (int w = kFeat; w >= 64; w -= 16) {
+      const long long tiles = groups * ((static_cast<long long>(a.N) + w - 1) / w);
+      const long long cost = (tiles + sms - 1) / sms * (w + 48);
+      if (best < 0 || cost < best) {
+        best = cost;
+        a.width = w;
+      }
+    }
+    // as many blocks of K per stage as leave four stages: with few rows a stage costs its
+    // barriers (about 0.1 us) more than its MMAs
+    auto count = [&](int sub) {
+      return mxfp4 ? stage_count<true>(a.width, a.cap, sub) : stage_count<false>(a.width, a.cap, sub);
+    };
+    for (const int most = mxfp4 ? 2 : 4; a.sub < most && count(2 * a.sub) >= 4;) a.sub *= 2;
+  }
+  const int features = a.pair ? 2 * kFeat : a.width;
   a.tiles_f = static_cast<int>((static_cast<long long>(a.N) + features - 1) / features);
 }
 

@@ -8,6 +8,7 @@
 namespace sa {
 
 constexpr int kMaxExperts = 256;
+constexpr int kBoxRows = 16;  // rows of one TMA box of x
 constexpr int kGroupedFeatures = 128;  // features of one tile (the tcgen05.mma M)
 
 struct GroupedArgs {
@@ -22,9 +23,10 @@ struct GroupedArgs {
   int x_rows, rows, num_experts, N, K;
   int n_out;    // features written per row: N, or N / 2 with swiglu
   int tiles_f;  // feature tiles (of N)
-  int pair;     // tiles of CTA pairs: 256 features (else 128)
+  int pair;     // tiles of CTA pairs: 2 x 128 features
+  int width;    // features of a single CTA's tile: a multiple of 16, at most 128
   int cap;      // most rows of a tile
-  int box_rows; // rows of xmap's boxes
+  int sub;      // blocks of 128 bytes of K per ring stage (1 with pairs)
   int stages;   // ring stages (set by the launcher)
   int swiglu;
   float alpha, limit;
@@ -32,12 +34,12 @@ struct GroupedArgs {
   unsigned long long timeout_ns;
 };
 
-// The tiling (pair, cap, box_rows, tiles_f) for a.rows, a.num_experts and a.N.  cap is at
-// least 64, at most 256 in bf16 and 224 in MXFP4 (whose scales take TMEM columns beside the
-// accumulators).
-void grouped_plan(GroupedArgs& a, bool mxfp4);
-// wmap: w as {K, N, E} in boxes of 128 bytes x 128 x 1;
-// xmap: x [x_rows, K] in boxes of 128 bytes x box_rows.
+// The tiling (pair, width, cap, sub, tiles_f) for a.rows, a.num_experts and a.N.  cap is
+// 16, 64 or, for pairs, 256 in bf16 and 224 in MXFP4 (whose scales take TMEM columns beside
+// the accumulators).
+void grouped_plan(GroupedArgs& a, bool mxfp4, int sms);
+// wmap: w as {K, N, E} in boxes of 128 bytes x width x 1;
+// xmap: x [x_rows, K] in boxes of 128 bytes x kBoxRows.
 cudaError_t launch_grouped(const CUtensorMap& wmap, const CUtensorMap& xmap, const GroupedArgs& a, bool mxfp4,
                            int sms, cudaStream_t stream);
 
