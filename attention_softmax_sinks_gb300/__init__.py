@@ -169,12 +169,12 @@ def _call(fn, dev, stream, *args):
     device's current stream) as the last argument; the previous current device is restored."""
     if stream is not None and stream.device_index != dev:
         raise ValueError(f"stream is on cuda:{stream.device_index}, the tensors on cuda:{dev}")
+    # the raw handle: a Stream object costs more than the rest of the call
+    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
     if torch.cuda.current_device() == dev:
-        s = torch.cuda.current_stream() if stream is None else stream
-        return fn(*args, s.cuda_stream)
+        return fn(*args, s)
     with torch.cuda.device(dev):
-        s = torch.cuda.current_stream() if stream is None else stream
-        return fn(*args, s.cuda_stream)
+        return fn(*args, s)
 
 
 # ----------------------------------------------------------------------------- entry points
@@ -494,12 +494,40 @@ def moe_router(x, w_router, bias, top_k: int, topk_idx=None, topk_weight=None, e
 GPT_OSS_SWIGLU = dict(alpha=1.702, limit=7.0)
 
 
-def _shape(t, name, *dims):
-    """A tensor of len(dims) dimensions whose sizes equal the dims that are not None."""
-    if t.dim() != len(dims) or any(d is not None and t.shape[i] != d for i, d in enumerate(dims)):
-        want = ", ".join("*" if d is None else str(d) for d in dims)
-        raise ValueError(f"{name} must be [{want}], got {tuple(t.shape)}")
-    return t
+def _inputs(required, optional=()):
+    """Validate (name, tensor, dtype, shape) tuples: CUDA, dtype, contiguous, shape (None: any
+    size), all on the first tensor's device.  Returns that device's index."""
+    di = None
+    for group in (required, optional):
+        for name, t, dt, dims in group:
+            if t is None and group is optional:
+                continue
+            if not isinstance(t, torch.Tensor) or t.dtype is not dt or not t.is_cuda or not t.is_contiguous():
+                _dev(t, name, dt)  # raises
+            d = t.get_device()
+            if di is None:
+                di = d
+            elif d != di:
+                _same_device(di, (name, t))  # raises
+            shape = t.shape
+            if len(shape) == len(dims):
+                for have, want in zip(shape, dims):
+                    if want is not None and have != want:
+                        break
+                else:
+                    continue
+            want = ", ".join("*" if v is None else str(v) for v in dims)
+            raise ValueError(f"{name} must be [{want}], got {tuple(shape)}")
+    return di
+
+
+def _size(t, name, dim):
+    """t.shape[dim], of something that may not be a tensor of that many dimensions."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dim() <= dim:
+        raise ValueError(f"{name} has {t.dim()} dimensions, expected more than {dim}")
+    return t.shape[dim]
 
 
 def moe_group_rows(topk_idx, num_experts: int, expert_offsets=None, row_token=None, pair_row=None,
@@ -510,18 +538,18 @@ def moe_group_rows(topk_idx, num_experts: int, expert_offsets=None, row_token=No
     expert e owns rows [expert_offsets[e], expert_offsets[e + 1]), row r reads token
     row_token[r], and pair (t, i) is row pair_row[t, i].  A negative index is a pair without
     expert (pair_row -1); row_token is -1 behind the last row."""
-    dev, di = _checked((("topk_idx", topk_idx, torch.int32),))
-    _shape(topk_idx, "topk_idx", None, None)
+    di = _inputs((("topk_idx", topk_idx, torch.int32, (None, None)),))
     t, k = topk_idx.shape
     e = int(num_experts)
-    expert_offsets = (torch.empty((max(e, 0) + 1,), dtype=torch.int32, device=dev) if expert_offsets is None
+    dev = topk_idx.device
+    expert_offsets = (torch.empty(max(e, 0) + 1, dtype=torch.int32, device=dev) if expert_offsets is None
                       else _out(expert_offsets, "expert_offsets", torch.int32, (e + 1,), di))
-    row_token = (torch.empty((t * k,), dtype=torch.int32, device=dev) if row_token is None
+    row_token = (torch.empty(t * k, dtype=torch.int32, device=dev) if row_token is None
                  else _out(row_token, "row_token", torch.int32, (t * k,), di))
     pair_row = (torch.empty((t, k), dtype=torch.int32, device=dev) if pair_row is None
                 else _out(pair_row, "pair_row", torch.int32, (t, k), di))
-    st = _call(load_library().moe_group_rows, di, stream, _ptr(topk_idx), t, k, e, _ptr(expert_offsets),
-               _ptr(row_token), _ptr(pair_row))
+    st = _call(load_library().moe_group_rows, di, stream, topk_idx.data_ptr(), t, k, e, expert_offsets.data_ptr(),
+               row_token.data_ptr(), pair_row.data_ptr())
     _check(st, "moe_group_rows")
     return expert_offsets, row_token, pair_row
 
@@ -529,60 +557,34 @@ def moe_group_rows(topk_idx, num_experts: int, expert_offsets=None, row_token=No
 def moe_combine(y, pair_row, topk_weight, out=None, stream=None):
     """out[t] = sum_i topk_weight[t, i] * y[pair_row[t, i]]: y [R, H] bf16, pair_row [T, k]
     int32 (-1 adds nothing), topk_weight [T, k] bf16.  Returns out [T, H] bf16."""
-    dev, di = _checked((("y", y, torch.bfloat16), ("pair_row", pair_row, torch.int32),
-                        ("topk_weight", topk_weight, torch.bfloat16)))
-    _same_device(di, ("pair_row", pair_row), ("topk_weight", topk_weight))
-    _shape(y, "y", None, None)
-    _shape(pair_row, "pair_row", None, None)
-    t, k = pair_row.shape
-    _shape(topk_weight, "topk_weight", t, k)
+    t, k = _size(pair_row, "pair_row", 0), _size(pair_row, "pair_row", 1)
+    di = _inputs((("y", y, torch.bfloat16, (None, None)), ("pair_row", pair_row, torch.int32, (t, k)),
+                  ("topk_weight", topk_weight, torch.bfloat16, (t, k))))
     r, h = y.shape
-    out = (torch.empty((t, h), dtype=torch.bfloat16, device=dev) if out is None
+    out = (torch.empty((t, h), dtype=torch.bfloat16, device=y.device) if out is None
            else _out(out, "out", torch.bfloat16, (t, h), di))
-    st = _call(load_library().moe_combine, di, stream, _ptr(y), _ptr(pair_row), _ptr(topk_weight), r, t, k, h,
-               _ptr(out))
+    st = _call(load_library().moe_combine, di, stream, y.data_ptr(), pair_row.data_ptr(), topk_weight.data_ptr(), r,
+               t, k, h, out.data_ptr())
     _check(st, "moe_combine")
     return out
 
 
-def _given(x_scales):
-    """x_scales, which tells _grouped that the operands are MXFP4."""
-    if x_scales is None:
-        raise TypeError("x_scales must be a CUDA tensor")
-    return x_scales
+def _product_output(out, rows, n, x, di):
+    return (torch.empty((rows, n), dtype=torch.bfloat16, device=x.device) if out is None
+            else _out(out, "out", torch.bfloat16, (rows, n), di))
 
 
-def _grouped(where, x, x_scales, w, w_scales, expert_offsets, bias, row_token, out, stream, act=None):
-    """The grouped products: x [X, K] and w [E, N, K] in bf16, or as MXFP4 codes and scales."""
-    mx = x_scales is not None
-    dt = torch.uint8 if mx else torch.bfloat16
-    named = [("x_codes", x, dt), ("x_scales", x_scales, dt), ("w_codes", w, dt), ("w_scales", w_scales, dt)] \
-        if mx else [("x", x, dt), ("w", w, dt)]
-    named.append(("expert_offsets", expert_offsets, torch.int32))
-    dev, di = _checked(named)
-    _opt((("bias", bias, torch.bfloat16), ("row_token", row_token, torch.int32)))
-    _same_device(di, *[(name, t) for name, t, _ in named], ("bias", bias), ("row_token", row_token))
-    _shape(x, named[0][0], None, None)
-    x_rows, kx = x.shape
-    _shape(w, "w_codes" if mx else "w", None, None, kx)
-    e, n, _ = w.shape
-    k = 2 * kx if mx else kx
-    if mx:
-        s = mxfp4_scale_columns(k)
-        _shape(x_scales, "x_scales", x_rows, s)
-        _shape(w_scales, "w_scales", e, n, s)
-    _shape(expert_offsets, "expert_offsets", e + 1)
-    if bias is not None:
-        _shape(bias, "bias", e, n)
-    if row_token is not None:
-        _shape(row_token, "row_token", None)
+def _grouped(where, x, w, expert_offsets, bias, row_token, out, stream, act=()):
+    """The grouped products on bf16 operands; act: SwiGLU's (alpha, limit) or ()."""
+    e, n, k = _size(w, "w", 0), _size(w, "w", 1), _size(w, "w", 2)
+    di = _inputs((("x", x, torch.bfloat16, (None, k)), ("w", w, torch.bfloat16, (e, n, k)),
+                  ("expert_offsets", expert_offsets, torch.int32, (e + 1,))),
+                 (("bias", bias, torch.bfloat16, (e, n)), ("row_token", row_token, torch.int32, (None,))))
+    x_rows = x.shape[0]
     rows = x_rows if row_token is None else row_token.shape[0]
-    n_out = n if act is None else n // 2
-    out = (torch.empty((rows, n_out), dtype=torch.bfloat16, device=dev) if out is None
-           else _out(out, "out", torch.bfloat16, (rows, n_out), di))
-    operands = (_ptr(x), _ptr(x_scales), _ptr(w), _ptr(w_scales)) if mx else (_ptr(x), _ptr(w))
-    st = _call(getattr(load_library(), where), di, stream, *operands, _ptr(bias), _ptr(expert_offsets),
-               _ptr(row_token), x_rows, rows, e, n, k, *(act or ()), _ptr(out))
+    out = _product_output(out, rows, n // 2 if act else n, x, di)
+    st = _call(getattr(load_library(), where), di, stream, x.data_ptr(), w.data_ptr(), _ptr(bias),
+               expert_offsets.data_ptr(), _ptr(row_token), x_rows, rows, e, n, k, *act, out.data_ptr())
     _check(st, where)
     return out
 
@@ -594,7 +596,7 @@ def grouped_linear_bias(x, w, expert_offsets, bias=None, row_token=None, out=Non
     row r of expert e gives out[r] = x[row_token[r]] @ w[e]^T + bias[e] (row_token None: x[r]).
     Returns out [R, N] bf16; rows outside every group are left as they were (uninitialised
     when ``out`` is not given)."""
-    return _grouped("grouped_linear_bias", x, None, w, None, expert_offsets, bias, row_token, out, stream)
+    return _grouped("grouped_linear_bias", x, w, expert_offsets, bias, row_token, out, stream)
 
 
 def grouped_linear_swiglu(x, w, expert_offsets, bias=None, row_token=None,
@@ -603,8 +605,8 @@ def grouped_linear_swiglu(x, w, expert_offsets, bias=None, row_token=None,
     """grouped_linear_bias followed by the clamped SwiGLU on interleaved gate (even) and up
     (odd) features, before the one rounding to bf16: g * sigmoid(alpha g) * (u + 1) with
     g = min(gate, limit), u = clamp(up, -limit, limit).  Returns out [R, N / 2] bf16."""
-    return _grouped("grouped_linear_swiglu", x, None, w, None, expert_offsets, bias, row_token, out, stream,
-                    act=(float(alpha), float(limit)))
+    return _grouped("grouped_linear_swiglu", x, w, expert_offsets, bias, row_token, out, stream,
+                    (float(alpha), float(limit)))
 
 
 # ----------------------------------------------------------------------------- MXFP4
@@ -618,22 +620,18 @@ def mxfp4_quantize(x, codes=None, scales=None, stream=None):
     share the scale 2^(floor(log2 max|x|) - 2), values round to the nearest E2M1 (ties to
     even, at most 6).  Returns (codes uint8 [..., K / 2], scales uint8
     [..., mxfp4_scale_columns(K)])."""
-    dev, di = _checked((("x", x, torch.float32 if isinstance(x, torch.Tensor) and x.dtype == torch.float32
-                         else torch.bfloat16),))
+    fp32 = isinstance(x, torch.Tensor) and x.dtype is torch.float32
+    _dev(x, "x", torch.float32 if fp32 else torch.bfloat16)
     if x.dim() < 1:
         raise ValueError("x must have at least one dimension")
-    k = x.shape[-1]
-    lead = tuple(x.shape[:-1])
-    rows = 1
-    for d in lead:
-        rows *= d
+    di, dev, lead, k = x.get_device(), x.device, x.shape[:-1], x.shape[-1]
     codes = (torch.empty((*lead, k // 2), dtype=torch.uint8, device=dev) if codes is None
              else _out(codes, "codes", torch.uint8, (*lead, k // 2), di))
     s = mxfp4_scale_columns(k)
     scales = (torch.empty((*lead, s), dtype=torch.uint8, device=dev) if scales is None
               else _out(scales, "scales", torch.uint8, (*lead, s), di))
-    st = _call(load_library().mxfp4_quantize, di, stream, _ptr(x), int(x.dtype == torch.float32), rows, k,
-               _ptr(codes), _ptr(scales))
+    st = _call(load_library().mxfp4_quantize, di, stream, x.data_ptr(), int(fp32), lead.numel(), k,
+               codes.data_ptr(), scales.data_ptr())
     _check(st, "mxfp4_quantize")
     return codes, scales
 
@@ -641,19 +639,14 @@ def mxfp4_quantize(x, codes=None, scales=None, stream=None):
 def mxfp4_dequantize(codes, scales, out=None, stream=None):
     """The bf16 values [..., K] of MXFP4 codes [..., K / 2] and scales (as mxfp4_quantize
     returns them)."""
-    dev, di = _checked((("codes", codes, torch.uint8), ("scales", scales, torch.uint8)))
-    _same_device(di, ("scales", scales))
-    if codes.dim() < 1:
-        raise ValueError("codes must have at least one dimension")
-    lead = tuple(codes.shape[:-1])
-    k = 2 * codes.shape[-1]
-    _shape(scales, "scales", *lead, mxfp4_scale_columns(k))
-    rows = 1
-    for d in lead:
-        rows *= d
-    out = (torch.empty((*lead, k), dtype=torch.bfloat16, device=dev) if out is None
+    half = _size(codes, "codes", -1 if isinstance(codes, torch.Tensor) and codes.dim() else 0)
+    k, lead = 2 * half, codes.shape[:-1]
+    di = _inputs((("codes", codes, torch.uint8, (*lead, half)),
+                  ("scales", scales, torch.uint8, (*lead, mxfp4_scale_columns(k)))))
+    out = (torch.empty((*lead, k), dtype=torch.bfloat16, device=codes.device) if out is None
            else _out(out, "out", torch.bfloat16, (*lead, k), di))
-    st = _call(load_library().mxfp4_dequantize, di, stream, _ptr(codes), _ptr(scales), rows, k, _ptr(out))
+    st = _call(load_library().mxfp4_dequantize, di, stream, codes.data_ptr(), scales.data_ptr(), lead.numel(), k,
+               out.data_ptr())
     _check(st, "mxfp4_dequantize")
     return out
 
@@ -661,24 +654,32 @@ def mxfp4_dequantize(codes, scales, out=None, stream=None):
 def mxfp4_linear_bias(x_codes, x_scales, w_codes, w_scales, bias=None, out=None, stream=None):
     """linear_bias with both operands in MXFP4 (block-scaled tcgen05 products): x [M, K] and
     w [N, K] as codes [., K / 2] and scales, bias [N] bf16 or None.  Returns [M, N] bf16."""
-    dev, di = _checked((("x_codes", x_codes, torch.uint8), ("x_scales", x_scales, torch.uint8),
-                        ("w_codes", w_codes, torch.uint8), ("w_scales", w_scales, torch.uint8)))
-    _opt((("bias", bias, torch.bfloat16),))
-    _same_device(di, ("x_scales", x_scales), ("w_codes", w_codes), ("w_scales", w_scales), ("bias", bias))
-    _shape(x_codes, "x_codes", None, None)
-    m, half = x_codes.shape
-    _shape(w_codes, "w_codes", None, half)
-    n, k = w_codes.shape[0], 2 * half
-    s = mxfp4_scale_columns(k)
-    _shape(x_scales, "x_scales", m, s)
-    _shape(w_scales, "w_scales", n, s)
-    if bias is not None:
-        _shape(bias, "bias", n)
-    out = (torch.empty((m, n), dtype=torch.bfloat16, device=dev) if out is None
-           else _out(out, "out", torch.bfloat16, (m, n), di))
-    st = _call(load_library().mxfp4_linear_bias, di, stream, _ptr(x_codes), _ptr(x_scales), _ptr(w_codes),
-               _ptr(w_scales), _ptr(bias), m, n, k, _ptr(out))
+    m, half, n = _size(x_codes, "x_codes", 0), _size(x_codes, "x_codes", 1), _size(w_codes, "w_codes", 0)
+    s = mxfp4_scale_columns(2 * half)
+    di = _inputs((("x_codes", x_codes, torch.uint8, (m, half)), ("x_scales", x_scales, torch.uint8, (m, s)),
+                  ("w_codes", w_codes, torch.uint8, (n, half)), ("w_scales", w_scales, torch.uint8, (n, s))),
+                 (("bias", bias, torch.bfloat16, (n,)),))
+    out = _product_output(out, m, n, x_codes, di)
+    st = _call(load_library().mxfp4_linear_bias, di, stream, x_codes.data_ptr(), x_scales.data_ptr(),
+               w_codes.data_ptr(), w_scales.data_ptr(), _ptr(bias), m, n, 2 * half, out.data_ptr())
     _check(st, "mxfp4_linear_bias")
+    return out
+
+
+def _grouped_mxfp4(where, x_codes, x_scales, w_codes, w_scales, expert_offsets, bias, row_token, out, stream, act=()):
+    """The grouped products on MXFP4 operands; act: SwiGLU's (alpha, limit) or ()."""
+    e, n, half = (_size(w_codes, "w_codes", i) for i in range(3))
+    x_rows, s = _size(x_codes, "x_codes", 0), mxfp4_scale_columns(2 * half)
+    di = _inputs((("x_codes", x_codes, torch.uint8, (x_rows, half)), ("x_scales", x_scales, torch.uint8, (x_rows, s)),
+                  ("w_codes", w_codes, torch.uint8, (e, n, half)), ("w_scales", w_scales, torch.uint8, (e, n, s)),
+                  ("expert_offsets", expert_offsets, torch.int32, (e + 1,))),
+                 (("bias", bias, torch.bfloat16, (e, n)), ("row_token", row_token, torch.int32, (None,))))
+    rows = x_rows if row_token is None else row_token.shape[0]
+    out = _product_output(out, rows, n // 2 if act else n, x_codes, di)
+    st = _call(getattr(load_library(), where), di, stream, x_codes.data_ptr(), x_scales.data_ptr(),
+               w_codes.data_ptr(), w_scales.data_ptr(), _ptr(bias), expert_offsets.data_ptr(), _ptr(row_token),
+               x_rows, rows, e, n, 2 * half, *act, out.data_ptr())
+    _check(st, where)
     return out
 
 
@@ -686,16 +687,16 @@ def grouped_mxfp4_linear_bias(x_codes, x_scales, w_codes, w_scales, expert_offse
                               out=None, stream=None):
     """grouped_linear_bias with both operands in MXFP4: x [X, K] and w [E, N, K] as codes
     [., K / 2] and scales (row_token gathers rows of both)."""
-    return _grouped("grouped_mxfp4_linear_bias", x_codes, _given(x_scales), w_codes, w_scales, expert_offsets, bias,
-                    row_token, out, stream)
+    return _grouped_mxfp4("grouped_mxfp4_linear_bias", x_codes, x_scales, w_codes, w_scales, expert_offsets, bias,
+                          row_token, out, stream)
 
 
 def grouped_mxfp4_linear_swiglu(x_codes, x_scales, w_codes, w_scales, expert_offsets, bias=None, row_token=None,
                                 alpha: float = GPT_OSS_SWIGLU["alpha"], limit: float = GPT_OSS_SWIGLU["limit"],
                                 out=None, stream=None):
     """grouped_linear_swiglu with both operands in MXFP4."""
-    return _grouped("grouped_mxfp4_linear_swiglu", x_codes, _given(x_scales), w_codes, w_scales, expert_offsets,
-                    bias, row_token, out, stream, act=(float(alpha), float(limit)))
+    return _grouped_mxfp4("grouped_mxfp4_linear_swiglu", x_codes, x_scales, w_codes, w_scales, expert_offsets, bias,
+                          row_token, out, stream, (float(alpha), float(limit)))
 
 
 # ----------------------------------------------------------------------------- q rotated on chip

@@ -51,8 +51,7 @@ constexpr int kMaxSingleRows = 64;  // rows of a single CTA's tile
 constexpr int kLag = 2;         // stages between a gather's request and its hand-over
 constexpr int kBand = 8;        // row tiles of an expert that pass over its features together
 constexpr int kSfBlock = 512;   // scales of 128 rows x 128 values of K
-constexpr int kRawPairs = 3;    // scale bytes on their way: pairs of stages
-constexpr int kRawBlock = 128 * 16;
+constexpr int kRawBlock = 128 * 16;  // scale bytes on their way: 16 per row of a block of 128
 constexpr unsigned long long kDrainTimeoutNs = 2000000000ull;
 
 template <bool kFp4>
@@ -61,7 +60,7 @@ struct GrpCfg {
   static constexpr int kRows = kFp4 ? 224 : 256;
   static constexpr int kStageK = kFp4 ? 256 : 64;
   static constexpr int kSfBytes = kFp4 ? 2 * 3 * kSfBlock : 0;  // per 128 values of K: a block of weights, two of rows
-  static constexpr int kRawBytes = kFp4 ? kRawPairs * 3 * kRawBlock : 0;
+  static constexpr int kRawBytes = kFp4 ? 9 * kRawBlock : 0;  // three pairs' weights and rows, or six of a small tile
   static constexpr int kSfCols = 24;
   static constexpr int kTmemCols = 512;
   static constexpr int kProducers = 1 + kRowWarps + (kFp4 ? 2 : 0);  // warps that fill a stage, per CTA
@@ -274,10 +273,6 @@ __device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* m
 // 16 bytes by a thread of its own: `bytes` of them from src, zeros behind.
 __device__ __forceinline__ void copy_async16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-// A piece of memory towards L2 (address and size: multiples of 16).
-__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -546,9 +541,11 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
   } else if (kFp4 && (warp == 2 || warp == 3)) {
     // Scale bytes: a lane has rows lane, lane + 32, lane + 64, lane + 96 of each block of 128;
     // 16 bytes of a row serve two blocks of K.  They travel by asynchronous copies into a place of
-    // the lane's own, requested two pairs of blocks ahead, and from there into the ring.
+    // the lane's own, requested some pairs of blocks ahead, and from there into the ring.
     const int used = a.K / 32;  // scale bytes in use: zeros stand in for those behind
     const int pairs = (k_blocks + 1) / 2;
+    constexpr int kRawPairs = kPair ? 3 : 6;
+    constexpr int kRawStep = C::kRawBytes / kRawPairs;  // weights, then rows (64 of a small tile)
     uint8_t* raw = tiles + kRingBytes + (warp == 2 ? 0 : kRawBlock) + 16 * lane;
     RingPos p;
     int g = 0;
@@ -556,6 +553,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
     for (int t = t_first; t < tiles_total && ok; t += t_step) {
       const Tile tl = find_tile(sb, a, t, kCtas * width, kGrain, lane);
       const int blocks = warp == 2 ? 1 : tl.n > 128 ? 2 : 1;
+      const int most = kPair || warp == 2 ? kFeat : kMaxSingleRows;  // rows of a block that may have scales
       const uint8_t* src[2][4];  // nullptr: no such row, zeros
 #pragma unroll
       for (int blk = 0; blk < 2; ++blk)
@@ -578,38 +576,32 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
         }
       auto request = [&](int pair) {
         if (pair < pairs) {
-          const uint32_t dst = smem_u32(raw) + (pair % kRawPairs) * 3 * kRawBlock;
+          const uint32_t dst = smem_u32(raw) + (pair % kRawPairs) * kRawStep;
           const int valid = min(16, used - 16 * pair);
 #pragma unroll
           for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              if (blk < blocks)
+              if (blk < blocks && 32 * j < most)
                 copy_async16(dst + blk * kRawBlock + 512 * j, src[blk][j] ? src[blk][j] + 16 * pair : a.w_scales,
                              src[blk][j] ? valid : 0);
         }
         copy_async_commit();
       };
-      // The next tile's weight scales are one piece of memory: into L2 with them now, in one
-      // go, instead of 32 bytes per row and request.
-      if (warp == 2 && t + t_step < tiles_total) {
-        const Tile nx = find_tile(sb, a, t + t_step, kCtas * width, kGrain, lane);
-        const int f = nx.f0 + rank * kFeat, rows = min(width, a.N - f);
-        if (rows > 0 && elect_one())
-          prefetch_l2(a.w_scales + (static_cast<long long>(nx.e) * a.N + f) * a.scale_stride, rows * a.scale_stride);
-      }
-      request(0);
-      request(1);
+#pragma unroll
+      for (int i = 0; i + 1 < kRawPairs; ++i) request(i);
       for (int pair = 0; pair < pairs && ok; ++pair) {
-        request(pair + 2);
-        copy_async_wait<2>();
-        const uint8_t* mine = raw + (pair % kRawPairs) * 3 * kRawBlock;
+        request(pair + kRawPairs - 1);
+        copy_async_wait<kRawPairs - 1>();
+        const uint8_t* mine = raw + (pair % kRawPairs) * kRawStep;
         uint4 c[2][4];
 #pragma unroll
         for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            if (blk < blocks) c[blk][j] = *reinterpret_cast<const uint4*>(mine + blk * kRawBlock + 512 * j);
+            if (blk < blocks)
+              c[blk][j] = 32 * j < most ? *reinterpret_cast<const uint4*>(mine + blk * kRawBlock + 512 * j)
+                                        : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int block = 2 * pair + h;
