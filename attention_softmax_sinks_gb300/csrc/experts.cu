@@ -11,31 +11,35 @@ namespace sa {
 namespace {
 
 // ----------------------------------------------------------------------------- grouping
-// Stable counting sort in one launch: a cluster of CTAs splits the pairs into contiguous
-// ranges, each warp owns a contiguous piece, and the ranges' expert counts are exchanged
-// through distributed shared memory.  A pair's row is (pairs of lower experts) + (pairs of
-// its expert in earlier CTAs, earlier warps, earlier steps of its warp, lower lanes): no
-// counter is shared between warps, so the order never depends on timing.
+// Stable counting sort in one launch.  A pair's row is (pairs of lower experts) + (pairs of its
+// expert in earlier ranges, earlier warps, earlier steps of its warp, lower lanes): no counter
+// is shared between warps that write rows, so the order never depends on timing.
+//
+// Few pairs: one CTA.  Many: 8 clusters of 8 CTAs.  The pairs are cut into 8 segments, one per
+// cluster, and each segment into 8 ranges, one per CTA.  Every cluster counts all pairs (its
+// CTA r counts segment r), so it knows what the segments before its own hold without waiting
+// for another cluster; then each CTA counts its own range per warp, and the ranges' counts are
+// exchanged through distributed shared memory.  The scattered 4-byte writes of row_token, 32
+// sectors per warp, are what takes the time on few SMs: 131072 pairs took 20 us on one cluster.
 constexpr int kGroupThreads = 1024;
 constexpr int kGroupWarps = kGroupThreads / 32;
+constexpr int kGroupCluster = 8;
 constexpr int kBatch = 8;  // index loads in flight per lane
 
 __global__ void __launch_bounds__(kGroupThreads, 1) group_rows_kernel(const GroupRowsArgs a, int cluster, int seg) {
   __shared__ int cnt[kGroupWarps][kMaxExperts];  // per warp: counts, then the next row of each expert
-  __shared__ int tot[kMaxExperts];               // this CTA's counts (read by the cluster)
+  __shared__ int seg_tot[kMaxExperts];           // counts of segment `rank` (read by the cluster)
+  __shared__ int tot[kMaxExperts];               // counts of this CTA's range (read by the cluster)
   __shared__ int scan[kMaxExperts / 32];
   __shared__ int total_rows;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int mine = cluster > 1 ? blockIdx.x / kGroupCluster : 0;  // this cluster's segment
   const int E = a.num_experts;
-  for (int i = threadIdx.x; i < kGroupWarps * kMaxExperts; i += kGroupThreads) (&cnt[0][0])[i] = 0;
-  __syncthreads();
+  const long long range = static_cast<long long>(kGroupWarps) * seg, segment = range * kGroupCluster;
 
-  const long long first = static_cast<long long>(rank * kGroupWarps + warp) * seg;
-  const int begin = static_cast<int>(first < a.pairs ? first : a.pairs);
-  const int end = static_cast<int>(first + seg < a.pairs ? first + seg : a.pairs);
   bool bad = false;
-  auto load = [&](int p0, int (&e)[kBatch]) {  // -1: no pair, or a pair without expert
+  auto load = [&](int p0, int end, int (&e)[kBatch]) {  // -1: no pair, or a pair without expert
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int p = p0 + 32 * i + lane;
@@ -47,39 +51,68 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_rows_kernel(const Grou
       if (e[i] < 0 || e[i] >= E) e[i] = -1;
     }
   };
-
-  for (int p0 = begin; p0 < end; p0 += 32 * kBatch) {
-    int e[kBatch];
-    load(p0, e);
+  auto clip = [&](long long p) { return static_cast<int>(p < a.pairs ? p : a.pairs); };
+  // counts of the pairs [begin, end) in this warp's row
+  auto count = [&](int begin, int end) {
+    for (int p0 = begin; p0 < end; p0 += 32 * kBatch) {
+      int e[kBatch];
+      load(p0, end, e);
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-      if (e[i] >= 0) atomicAdd(&cnt[warp][e[i]], 1);
-  }
-  if (bad) raise_status(a.status, kStatusBadLen);
-  __syncthreads();
-
-  // counts -> exclusive prefix over this CTA's warps, and the CTA's totals
-  int mine = 0;
-  if (threadIdx.x < kMaxExperts) {
+      for (int i = 0; i < kBatch; ++i)
+        if (e[i] >= 0) atomicAdd(&cnt[warp][e[i]], 1);
+    }
+  };
+  auto clear = [&]() {
+    for (int i = threadIdx.x; i < kGroupWarps * kMaxExperts; i += kGroupThreads) (&cnt[0][0])[i] = 0;
+  };
+  // cnt -> exclusive prefix over the warps; returns the sum
+  auto over_warps = [&]() {
+    int sum = 0;
 #pragma unroll 8
     for (int w = 0; w < kGroupWarps; ++w) {
       const int c = cnt[w][threadIdx.x];
-      cnt[w][threadIdx.x] = mine;
-      mine += c;
+      cnt[w][threadIdx.x] = sum;
+      sum += c;
     }
-    tot[threadIdx.x] = mine;
+    return sum;
+  };
+  // v[threadIdx.x] of all CTAs of the cluster
+  auto of_cluster = [&](const int* v, int (&c)[kGroupCluster]) {
+    const uint32_t at = smem_u32(v + threadIdx.x);
+#pragma unroll
+    for (int r = 0; r < kGroupCluster; ++r)
+      asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(c[r]) : "r"(dsmem_addr(at, r)) : "memory");
+  };
+
+  const long long first = mine * segment + rank * range + static_cast<long long>(warp) * seg;
+  const int begin = clip(first), end = clip(first + seg);
+  clear();
+  __syncthreads();
+  int before = 0, all = 0;  // of expert threadIdx.x: pairs ahead of this CTA's range, and pairs in all
+  if (cluster > 1) {
+    const long long piece = segment / kGroupWarps;  // a multiple of 32
+    count(clip(rank * segment + warp * piece), clip(rank * segment + (warp + 1) * piece));
+    __syncthreads();
+    if (threadIdx.x < kMaxExperts) seg_tot[threadIdx.x] = over_warps();
+    __syncthreads();
+    clear();
+    __syncthreads();
   }
-  int before = 0, all = mine;
+  count(begin, end);
+  if (bad) raise_status(a.status, kStatusBadLen);
+  __syncthreads();
+  if (threadIdx.x < kMaxExperts) tot[threadIdx.x] = all = over_warps();
   if (cluster > 1) {
     cluster_sync();
     if (threadIdx.x < kMaxExperts) {
+      int s[kGroupCluster], r[kGroupCluster];
+      of_cluster(seg_tot, s);
+      of_cluster(tot, r);
       all = 0;
-      const uint32_t at = smem_u32(&tot[threadIdx.x]);
-      for (int r = 0; r < cluster; ++r) {
-        int c;
-        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(c) : "r"(dsmem_addr(at, r)) : "memory");
-        if (r < rank) before += c;
-        all += c;
+#pragma unroll
+      for (int i = 0; i < kGroupCluster; ++i) {
+        all += s[i];
+        before += (i < mine ? s[i] : 0) + (i < rank ? r[i] : 0);
       }
     }
   }
@@ -98,10 +131,10 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_rows_kernel(const Grou
     int base = 0;
     for (int w = 0; w < warp; ++w) base += scan[w];
     const int off = base + incl - all;
-    if (rank == 0 && threadIdx.x < E) a.offsets[threadIdx.x] = off;
+    if (blockIdx.x == 0 && threadIdx.x < E) a.offsets[threadIdx.x] = off;
     if (threadIdx.x == kMaxExperts - 1) {
       total_rows = base + incl;
-      if (rank == 0) a.offsets[E] = base + incl;
+      if (blockIdx.x == 0) a.offsets[E] = base + incl;
     }
 #pragma unroll 8
     for (int w = 0; w < kGroupWarps; ++w) cnt[w][threadIdx.x] += off + before;
@@ -111,7 +144,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_rows_kernel(const Grou
   const unsigned below = (1u << lane) - 1u;
   for (int p0 = begin; p0 < end; p0 += 32 * kBatch) {
     int e[kBatch];
-    load(p0, e);
+    load(p0, end, e);
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int p = p0 + 32 * i + lane;
@@ -126,8 +159,8 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_rows_kernel(const Grou
     }
   }
   // rows that no pair has
-  for (long long r = total_rows + static_cast<long long>(rank) * kGroupThreads + threadIdx.x; r < a.pairs;
-       r += static_cast<long long>(cluster) * kGroupThreads)
+  for (long long r = total_rows + static_cast<long long>(blockIdx.x) * kGroupThreads + threadIdx.x; r < a.pairs;
+       r += static_cast<long long>(gridDim.x) * kGroupThreads)
     a.row_token[r] = -1;
   if (cluster > 1) cluster_wait();
 }
@@ -139,10 +172,13 @@ template <int K>
 __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a) {
   const int vecs = a.hidden / 8;
   const long long total = static_cast<long long>(a.num_tokens) * vecs;
-  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-       i += static_cast<long long>(gridDim.x) * blockDim.x) {
-    const long long t = i / vecs;
-    const int c = static_cast<int>(i - t * vecs);
+  const long long step = static_cast<long long>(gridDim.x) * blockDim.x;
+  const long long step_t = step / vecs;
+  const int step_c = static_cast<int>(step - step_t * vecs);
+  long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+  for (GridWalk at(i, vecs); i < total; i += step, at.advance(step_t, step_c, vecs)) {
+    const long long t = at.row;
+    const int c = at.col;
     int row[K];
     float w[K];
     uint4 v[K];
@@ -188,12 +224,12 @@ cudaError_t launch_combine_k(const CombineArgs& a, int sms, cudaStream_t stream)
 }  // namespace
 
 cudaError_t launch_group_rows(const GroupRowsArgs& a, cudaStream_t stream) {
-  // one CTA up to 128 pairs per warp, a cluster of 8 (the portable limit) beyond
-  const int cluster = a.pairs <= 128 * kGroupWarps ? 1 : 8;
-  const long long warps = static_cast<long long>(cluster) * kGroupWarps;
+  // one CTA up to 128 pairs per warp
+  const int cluster = a.pairs <= 128 * kGroupWarps ? 1 : kGroupCluster;
+  const long long warps = static_cast<long long>(cluster) * cluster * kGroupWarps;
   const int seg = static_cast<int>(((a.pairs + warps - 1) / warps + 31) / 32 * 32);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(cluster);
+  cfg.gridDim = dim3(cluster * cluster);
   cfg.blockDim = dim3(kGroupThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -202,7 +238,7 @@ cudaError_t launch_group_rows(const GroupRowsArgs& a, cudaStream_t stream) {
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, group_rows_kernel, a, cluster, seg);
 }
 

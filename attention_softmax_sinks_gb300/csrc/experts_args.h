@@ -6,6 +6,24 @@
 
 namespace sa {
 
+// Position of a thread that walks over [rows, width] elements in steps of a whole grid, without
+// a division per step: `step` = step_row * width + step_col.
+struct GridWalk {
+  long long row;
+  int col;
+#ifdef __CUDACC__
+  __device__ __forceinline__ GridWalk(long long i, int width) : row(i / width), col(static_cast<int>(i - row * width)) {}
+  __device__ __forceinline__ void advance(long long step_row, int step_col, int width) {
+    row += step_row;
+    col += step_col;
+    if (col >= width) {
+      col -= width;
+      ++row;
+    }
+  }
+#endif
+};
+
 struct GroupRowsArgs {
   const int32_t* topk_idx;  // [T, k]
   int32_t* offsets;         // [E + 1]

@@ -45,94 +45,131 @@ __device__ __forceinline__ float half_bits_to_float(uint32_t h) {
   return f;
 }
 
-// Four lanes share a block of 32 (8 values each: 16 bytes of bf16 in, 4 bytes of codes out).
+constexpr int kThreads = 256;
+// Pieces in flight per thread, and resident blocks per SM that the grids count on.
 template <bool kFp32>
-__global__ void __launch_bounds__(256) mxfp4_quantize_kernel(const Mxfp4Args a) {
-  const int vecs = a.k / 8;  // a multiple of 4: a block's lanes are in one quad
-  const long long total = a.rows * vecs;
-  const long long step = static_cast<long long>(gridDim.x) * blockDim.x;
-  for (long long i0 = static_cast<long long>(blockIdx.x) * blockDim.x; i0 < total; i0 += step) {
-    const long long i = i0 + threadIdx.x;
-    const bool in = i < total;
-    float v[8];
-    uint32_t mx = 0;
-    if constexpr (kFp32) {
-      float4 p = make_float4(0, 0, 0, 0), q = p;
-      if (in) {
-        p = __ldcs(reinterpret_cast<const float4*>(a.in) + 2 * i);
-        q = __ldcs(reinterpret_cast<const float4*>(a.in) + 2 * i + 1);
+constexpr int kQuantUnroll = kFp32 ? 1 : 2;
+constexpr int kQuantBlocks = 5;
+constexpr int kUnroll = 4;
+constexpr int kDequantBlocks = 8;
+
+// Two lanes share a block of 32 (16 values each: 32 bytes of bf16 in, 8 bytes of codes out).
+// A row's pieces are even in number and so is the grid's step: blocks stay in their pairs.
+template <bool kFp32>
+__global__ void __launch_bounds__(kThreads, kQuantBlocks) mxfp4_quantize_kernel(const Mxfp4Args a) {
+  constexpr int kUnroll = kQuantUnroll<kFp32>;
+  constexpr int kLoads = kFp32 ? 4 : 2;  // of 16 bytes per piece
+  const int pieces = a.k / 16;
+  const long long total = a.rows * pieces;
+  const long long step = static_cast<long long>(gridDim.x) * kThreads;
+  const long long step_row = step / pieces;
+  const int step_col = static_cast<int>(step - step_row * pieces);
+  long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
+  GridWalk at(i, pieces);
+  // every lane of a warp makes the same number of rounds (the pairs exchange their maxima)
+  for (long long base = i - threadIdx.x % 32; base < total; base += kUnroll * step) {
+    uint4 p[kUnroll][kLoads];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+      for (int l = 0; l < kLoads; ++l) {
+        const long long j = i + u * step;
+        p[u][l] = make_uint4(0, 0, 0, 0);
+        if (j < total) p[u][l] = __ldcs(reinterpret_cast<const uint4*>(a.in) + kLoads * j + l);
       }
-      v[0] = p.x, v[1] = p.y, v[2] = p.z, v[3] = p.w, v[4] = q.x, v[5] = q.y, v[6] = q.z, v[7] = q.w;
-    } else {
-      uint4 p = make_uint4(0, 0, 0, 0);
-      if (in) p = __ldcs(reinterpret_cast<const uint4*>(a.in) + i);
-      const uint32_t u[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[2 * j] = __uint_as_float(u[j] << 16);
-        v[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
+    for (int u = 0; u < kUnroll; ++u, i += step, at.advance(step_row, step_col, pieces)) {
+      float v[2][8];
+#pragma unroll
+      for (int l = 0; l < kLoads; ++l) {
+        const uint32_t w[4] = {p[u][l].x, p[u][l].y, p[u][l].z, p[u][l].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (kFp32) {
+            v[l >> 1][4 * (l & 1) + j] = __uint_as_float(w[j]);
+          } else {
+            v[l][2 * j] = __uint_as_float(w[j] << 16);
+            v[l][2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+          }
+        }
       }
-    }
+      uint32_t mx = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) mx = max(mx, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    const uint32_t field = mx >> 23;
-    const bool finite = field < 255u;
-    const uint32_t byte = finite ? (field > 2u ? field - 2u : 0u) : 255u;
-    const float inv = __uint_as_float((254u - (finite ? byte : 0u)) << 23);  // 2^(127 - byte)
+      for (int j = 0; j < 16; ++j) mx = max(mx, __float_as_uint(v[j >> 3][j & 7]) & 0x7FFFFFFFu);
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      const uint32_t field = mx >> 23;
+      const bool finite = field < 255u;
+      const uint32_t byte = finite ? (field > 2u ? field - 2u : 0u) : 255u;
+      const float inv = __uint_as_float((254u - (finite ? byte : 0u)) << 23);  // 2^(127 - byte)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = finite ? v[j] * inv : 0.0f;
-    if (in) {
-      reinterpret_cast<uint32_t*>(a.codes)[i] = pack_e2m1x8(v);
-      if ((threadIdx.x & 3) == 0) {
-        const long long row = i / vecs;
-        const int b = static_cast<int>(i - row * vecs) / 4;
-        uint8_t* s = a.scales + row * a.stride;
-        s[b] = static_cast<uint8_t>(byte);
-        if (b == a.k / 32 - 1)
-          for (int p = b + 1; p < a.stride; ++p) s[p] = 0;  // padding
+      for (int j = 0; j < 16; ++j) v[j >> 3][j & 7] = finite ? v[j >> 3][j & 7] * inv : 0.0f;
+      if (i < total) {
+        reinterpret_cast<uint2*>(a.codes)[i] = make_uint2(pack_e2m1x8(v[0]), pack_e2m1x8(v[1]));
+        if ((threadIdx.x & 1) == 0) {
+          const int b = at.col / 2;
+          uint8_t* s = a.scales + at.row * a.stride;
+          s[b] = static_cast<uint8_t>(byte);
+          if (b == a.k / 32 - 1)
+            for (int c = b + 1; c < a.stride; ++c) s[c] = 0;  // padding
+        }
       }
     }
   }
 }
 
-__global__ void __launch_bounds__(256) mxfp4_dequantize_kernel(const Mxfp4Args a) {
+__global__ void __launch_bounds__(kThreads, kDequantBlocks) mxfp4_dequantize_kernel(const Mxfp4Args a) {
   const int vecs = a.k / 8;
   const long long total = a.rows * vecs;
-  const long long step = static_cast<long long>(gridDim.x) * blockDim.x;
-  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += step) {
-    const long long row = i / vecs;
-    const int b = static_cast<int>(i - row * vecs) / 4;
-    const uint32_t codes = __ldcs(reinterpret_cast<const uint32_t*>(a.in) + i);
-    const uint32_t byte = __ldg(a.scales + row * a.stride + b);
-    // 2^(byte - 127): byte 0 is a subnormal fp32 number, byte 255 NaN
-    const float scale = __uint_as_float(byte == 255u ? 0x7FC00000u : byte == 0u ? 0x00400000u : byte << 23);
-    uint32_t h[4], o[4];
-    unpack_e2m1x8(codes, h);
+  const long long step = static_cast<long long>(gridDim.x) * kThreads;
+  const long long step_row = step / vecs;
+  const int step_vec = static_cast<int>(step - step_row * vecs);
+  long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
+  GridWalk at(i, vecs);
+  while (i < total) {
+    uint32_t codes[kUnroll], byte[kUnroll];
+    GridWalk ahead = at;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      o[j] = pack_bf16x2(half_bits_to_float(h[j]) * scale, half_bits_to_float(h[j] >> 16) * scale);
-    reinterpret_cast<uint4*>(a.out)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+    for (int u = 0; u < kUnroll; ++u, ahead.advance(step_row, step_vec, vecs)) {
+      codes[u] = byte[u] = 0;
+      if (i + u * step < total) {
+        codes[u] = __ldcs(reinterpret_cast<const uint32_t*>(a.in) + i + u * step);
+        byte[u] = __ldg(a.scales + ahead.row * a.stride + ahead.col / 4);
+      }
+    }
+    at = ahead;
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u, i += step) {
+      if (i >= total) break;
+      // 2^(byte - 127): byte 0 is a subnormal fp32 number, byte 255 NaN
+      const uint32_t bits = byte[u] == 255u ? 0x7FC00000u : byte[u] == 0u ? 0x00400000u : byte[u] << 23;
+      const float scale = __uint_as_float(bits);
+      uint32_t h[4], o[4];
+      unpack_e2m1x8(codes[u], h);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        o[j] = pack_bf16x2(half_bits_to_float(h[j]) * scale, half_bits_to_float(h[j] >> 16) * scale);
+      __stcs(reinterpret_cast<uint4*>(a.out) + i, make_uint4(o[0], o[1], o[2], o[3]));
+    }
   }
 }
 
-int blocks_for(const Mxfp4Args& a, int sms) {
-  const long long blocks = (a.rows * (a.k / 8) + 255) / 256, most = 32LL * sms;
+// A grid that fills the device once, or less for small sizes; `values` per thread and step.
+int blocks_for(const Mxfp4Args& a, int values, int per_sm, int sms) {
+  const long long blocks = (a.rows * (a.k / values) + kThreads - 1) / kThreads, most = static_cast<long long>(per_sm) * sms;
   return static_cast<int>(blocks < most ? blocks : most);
 }
 
 }  // namespace
 
 cudaError_t launch_mxfp4_quantize(const Mxfp4Args& a, int sms, cudaStream_t stream) {
-  const int grid = blocks_for(a, sms);
-  if (a.is_fp32) mxfp4_quantize_kernel<true><<<grid, 256, 0, stream>>>(a);
-  else mxfp4_quantize_kernel<false><<<grid, 256, 0, stream>>>(a);
+  const int grid = blocks_for(a, 16, kQuantBlocks, sms);
+  if (a.is_fp32) mxfp4_quantize_kernel<true><<<grid, kThreads, 0, stream>>>(a);
+  else mxfp4_quantize_kernel<false><<<grid, kThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
 cudaError_t launch_mxfp4_dequantize(const Mxfp4Args& a, int sms, cudaStream_t stream) {
-  mxfp4_dequantize_kernel<<<blocks_for(a, sms), 256, 0, stream>>>(a);
+  mxfp4_dequantize_kernel<<<blocks_for(a, 8, kDequantBlocks, sms), kThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
