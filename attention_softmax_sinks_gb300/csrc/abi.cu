@@ -297,7 +297,8 @@ struct GroupedCall {
 int mxfp4_scale_stride(int k) { return (k / 32 + 15) / 16 * 16; }
 
 sa_status grouped_common(const GroupedCall& c, cudaStream_t stream) {
-  if (c.rows < 0 || c.x_rows < 0 || c.n <= 0 || c.k <= 0 || c.n > (1 << 30) || c.k > (1 << 30))
+  if (c.rows < 0 || c.x_rows < 0 || c.n <= 0 || c.k <= 0 || c.rows > (1 << 30) || c.n > (1 << 30) ||
+      c.k > (1 << 30))
     return SA_ERR_SHAPE;
   if (c.experts < 1 || c.experts > sa::kMaxExperts) return SA_ERR_SHAPE;
   if (c.swiglu && (c.n % 2 != 0 || !std::isfinite(c.alpha) || !(c.limit > 0.0f))) return SA_ERR_SHAPE;

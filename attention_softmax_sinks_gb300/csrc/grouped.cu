@@ -91,8 +91,7 @@ struct GrpShared {
   int issued[kMaxProducers];     // stages that each producer warp filled, written when it ends
   int total;                     // row tiles of all experts
   int cum[kMaxExperts + 32];     // row tiles of lower experts (a huge number from E + 1 on)
-  int start[kMaxExperts];        // first row
-  int rows[kMaxExperts];
+  int4 group[kMaxExperts];       // first row, rows, row tiles, rows per tile
 };
 template <bool kFp4>
 constexpr size_t smem_bytes() {
@@ -309,30 +308,41 @@ struct Tile {
   int r0, n;  // first row, number of rows
 };
 
+// x / tiles_f for 0 <= x < 2^30 (a.f_magic, a.f_shift: set by the launcher).
+__device__ __forceinline__ int over_tiles_f(const GroupedArgs& a, int x) {
+  return static_cast<int>((static_cast<uint64_t>(x) * a.f_magic) >> a.f_shift);
+}
+
 // Tile t of the numbering in `sb` (all 32 lanes of a warp call this together).  `features`: of
-// one tile; `grain`: its rows are split in multiples of this.
-__device__ __forceinline__ Tile find_tile(const GrpShared& sb, const GroupedArgs& a, int t, int features, int grain,
-                                          int lane) {
-  const int q = t / a.tiles_f;  // row tiles before it are whole experts' and at most its own expert's
+// one tile.  Every role does this once per tile, the MMA warp between two tiles' MMAs: no
+// integer division, whose latency would show there.
+__device__ __forceinline__ Tile find_tile(const GrpShared& sb, const GroupedArgs& a, int t, int features, int lane) {
+  const int q = over_tiles_f(a, t);  // row tiles before it are whole experts' and at most its own expert's
   const unsigned lt = __ballot_sync(0xffffffffu, sb.cum[8 * lane] <= q);
   const int base = 8 * (__popc(lt) - 1);
   const unsigned in = __ballot_sync(0xffffffffu, lane < 8 && sb.cum[base + (lane & 7)] <= q);
-  Tile r;
-  r.e = base + __popc(in) - 1;
-  const int rows = sb.rows[r.e];
-  const int count = (rows + a.cap - 1) / a.cap;
-  int local = t - sb.cum[r.e] * a.tiles_f;
-  const int band = count <= kBand ? 0 : local / (kBand * a.tiles_f);
+  const int e = base + __popc(in) - 1;
+  const int4 group = sb.group[e];
+  int local = t - sb.cum[e] * a.tiles_f;
+  const int band = group.z <= kBand ? 0 : over_tiles_f(a, local) / kBand;
   local -= band * kBand * a.tiles_f;
-  const int wide = min(kBand, count - band * kBand);
-  const int ft = local / wide, rt = band * kBand + local - ft * wide;
-  const int per = (rows + count * grain - 1) / (count * grain) * grain;  // an even split, in multiples of grain
-  r.r0 = sb.start[r.e] + rt * per;
-  const int left = rows - rt * per;
+  const int wide = min(kBand, group.z - band * kBand);  // 1..8
+  // local / wide: for x < 2^30 the excess of the factor stays below 2^-4 < 1 / 8
+  const uint64_t factor = wide == 1   ? (1ull << 34)
+                          : wide == 2 ? (1ull << 33)
+                          : wide == 3 ? (1ull << 34) / 3 + 1
+                          : wide == 4 ? (1ull << 32)
+                          : wide == 5 ? (1ull << 34) / 5 + 1
+                          : wide == 6 ? (1ull << 34) / 6 + 1
+                          : wide == 7 ? (1ull << 34) / 7 + 1
+                                      : (1ull << 31);
+  const int ft = static_cast<int>((static_cast<uint64_t>(local) * factor) >> 34);
+  const int rt = band * kBand + local - ft * wide;
   // through a reduction, whose result the compiler knows to be the same in all lanes
-  r.n = __reduce_min_sync(0xffffffffu, left < per ? left : per);
-  r.r0 = __reduce_min_sync(0xffffffffu, r.r0);
-  r.e = __reduce_min_sync(0xffffffffu, r.e);
+  Tile r;
+  r.n = __reduce_min_sync(0xffffffffu, min(group.w, group.y - rt * group.w));
+  r.r0 = __reduce_min_sync(0xffffffffu, group.x + rt * group.w);
+  r.e = __reduce_min_sync(0xffffffffu, e);
   r.f0 = __reduce_min_sync(0xffffffffu, ft * features);
   return r;
 }
@@ -425,10 +435,12 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
         }
         high = max(high, off[j]);
       }
-      sb.start[e] = lo;
-      sb.rows[e] = hi - lo;
+      // row tiles, and an even split of the rows among them in multiples of kGrain
+      const int rows = hi - lo, count = (rows + a.cap - 1) / a.cap;
+      const int per = count ? (rows + count * kGrain - 1) / (count * kGrain) * kGrain : 0;
+      sb.group[e] = make_int4(lo, rows, count, per);
       mine[j] = sum;
-      sum += (hi - lo + a.cap - 1) / a.cap;
+      sum += count;
     }
     int incl = sum;
 #pragma unroll
@@ -456,7 +468,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
     int g = 0;
     bool ok = true;
     for (int t = t_first; t < tiles_total && ok; t += t_step) {
-      const Tile tl = find_tile(sb, a, t, kCtas * width, kGrain, lane);
+      const Tile tl = find_tile(sb, a, t, kCtas * width, lane);
       for (int kb = 0; kb < k_steps; ++kb, ++g, p.next(stages)) {
         if (p.round != 0)
           ok = wait_or_abort(smem_u32(&sb.empty[p.stage]), (p.round - 1) & 1, a.timeout_ns, abort_flag);
@@ -481,7 +493,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
     int i = 0, scales = 0;
     bool ok = true;
     for (int t = t_first; t < tiles_total && ok; t += t_step, ++i) {
-      const Tile tl = find_tile(sb, a, t, kCtas * width, kGrain, lane);
+      const Tile tl = find_tile(sb, a, t, kCtas * width, lane);
       const int n16 = (tl.n + kGrain - 1) / kGrain * kGrain;
       const int b = i & 1;
       if (i >= 2) ok = wait_or_abort(smem_u32(&sb.acc_empty[b]), ((i >> 1) - 1) & 1, a.timeout_ns, abort_flag);
@@ -551,7 +563,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
     int g = 0;
     bool ok = true;
     for (int t = t_first; t < tiles_total && ok; t += t_step) {
-      const Tile tl = find_tile(sb, a, t, kCtas * width, kGrain, lane);
+      const Tile tl = find_tile(sb, a, t, kCtas * width, lane);
       const int blocks = warp == 2 ? 1 : tl.n > 128 ? 2 : 1;
       const int most = kPair || warp == 2 ? kFeat : kMaxSingleRows;  // rows of a block that may have scales
       const uint8_t* src[2][4];  // nullptr: no such row, zeros
@@ -660,7 +672,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
         done.next(stages);
       };
       for (int t = t_first; t < tiles_total && ok; t += t_step) {
-        const Tile tl = find_tile(sb, a, t, kCtas * width, kGrain, lane);
+        const Tile tl = find_tile(sb, a, t, kCtas * width, lane);
         const int half = (tl.n + kGrain - 1) / kGrain * 16;  // rows that this CTA stages
         const int steps = half >> 4;
         const uint8_t* src[kSteps];
@@ -703,7 +715,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
       while (handed < g) hand_over();
     } else {
       for (int t = t_first; t < tiles_total && ok; t += t_step) {
-        const Tile tl = find_tile(sb, a, t, kCtas * width, kGrain, lane);
+        const Tile tl = find_tile(sb, a, t, kCtas * width, lane);
         const int half = (tl.n + kGrain - 1) / kGrain * 16;  // rows that this CTA stages
         // the boxes of all blocks of a stage, dealt out to the warps
         const int units = half / kBoxRows, box = lane * kRowWarps + wr;
@@ -735,7 +747,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
     const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
     int i = 0;
     for (int t = t_first; t < tiles_total; t += t_step, ++i) {
-      const Tile tl = find_tile(sb, a, t, kCtas * width, kGrain, lane);
+      const Tile tl = find_tile(sb, a, t, kCtas * width, lane);
       const int b = i & 1;
       const int f = tl.f0 + rank * kFeat + 32 * q + lane;
       const bool mine = 32 * q + lane < width && f < a.N;
@@ -842,6 +854,12 @@ cudaError_t launch_grouped_t(const CUtensorMap& wmap, const CUtensorMap& xmap, c
   }
   constexpr int kCtas = kPair ? 2 : 1;
   GroupedArgs b = a;
+  // x / tiles_f = x * magic >> shift for 0 <= x < 2^30: the excess of magic over 2^shift / tiles_f
+  // is below 1, so the product is off by less than 2^30 / 2^shift <= 1 / tiles_f
+  int bits = 0;
+  while ((1LL << bits) < a.tiles_f) ++bits;
+  b.f_shift = 30 + bits;
+  b.f_magic = static_cast<uint32_t>((1ull << b.f_shift) / a.tiles_f + 1);
   b.stages = stage_count<kFp4>(kPair ? kFeat : a.width, a.cap / kCtas, kPair ? 1 : a.sub);
   // no more CTAs than tiles there can be
   const long long groups = a.num_experts < a.rows ? a.num_experts : a.rows;

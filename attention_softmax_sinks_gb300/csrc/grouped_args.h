@@ -27,7 +27,10 @@ struct GroupedArgs {
   int width;    // features of a single CTA's tile: a multiple of 16, at most 128
   int cap;      // most rows of a tile
   int sub;      // blocks of 128 bytes of K per ring stage (1 with pairs)
-  int stages;   // ring stages (set by the launcher)
+  // set by the launcher
+  int stages;        // ring stages
+  uint32_t f_magic;  // x / tiles_f = x * f_magic >> f_shift
+  int f_shift;
   int swiglu;
   float alpha, limit;
   unsigned* status;
