@@ -16,10 +16,10 @@
 //   warps 2, 3    MXFP4: scale bytes of the weights (2) and of the rows (3), written into the ring in the layout that tcgen05.cp
 //                 spreads over TMEM (row r of a block of 128: 4 bytes at 16 (r % 32) + 4 (r / 32),
 //                 512 bytes per 128 values of K)
-//   warps 4..11   epilogue: thread = one feature (TMEM lane), columns = rows; bias and
-//                 activation in fp32, one rounding; a warp writes 64 consecutive bytes per row.
-//                 SwiGLU: gate and up are neighbouring lanes, which exchange half of their
-//                 columns so that each finishes 16 of every 32
+//   warps 4..11   epilogue: TMEM lanes are features, columns rows; bias and activation in
+//                 fp32, one rounding, 8 x 8 transpositions through shared memory and 16-byte
+//                 stores, 64 consecutive bytes per row and warp (32 with SwiGLU, whose gate and
+//                 up features are neighbouring lanes)
 //   warps 12..15  the rows of a stage: consecutive rows in TMA boxes, rows gathered by their
 //                 indices with 16-byte asynchronous copies
 // Two TMEM accumulators alternate, so the epilogue of a tile overlaps the next tile's MMAs.
@@ -51,6 +51,7 @@ constexpr int kMaxSingleRows = 64;  // rows of a single CTA's tile
 constexpr int kLag = 2;         // stages between a gather's request and its hand-over
 constexpr int kBand = 8;        // row tiles of an expert that pass over its features together
 constexpr int kSfBlock = 512;   // scales of 128 rows x 128 values of K
+constexpr int kPatchBytes = 512;       // of an epilogue warp
 constexpr int kRawBlock = 128 * 16;  // scale bytes on their way: 16 per row of a block of 128
 constexpr unsigned long long kDrainTimeoutNs = 2000000000ull;
 
@@ -95,7 +96,7 @@ struct GrpShared {
 };
 template <bool kFp4>
 constexpr size_t smem_bytes() {
-  return 1024 /*alignment slack*/ + kRingBytes + GrpCfg<kFp4>::kRawBytes + sizeof(GrpShared);
+  return 1024 /*alignment slack*/ + kRingBytes + GrpCfg<kFp4>::kRawBytes + kEpiWarps * kPatchBytes + sizeof(GrpShared);
 }
 static_assert(smem_bytes<true>() <= 227 * 1024, "shared memory of one CTA");
 
@@ -347,6 +348,24 @@ __device__ __forceinline__ Tile find_tile(const GrpShared& sb, const GroupedArgs
   return r;
 }
 
+// 16 TMEM lanes x 32 columns: thread t gets, for each group i of 8 columns, lane t / 4 (r[4 i],
+// r[4 i + 1]) and lane t / 4 + 8 (r[4 i + 2], r[4 i + 3]) of columns 8 i + 2 (t % 4) + {0, 1}.
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// Four 8 x 8 matrices of 16-bit values, each transposed on its way to shared memory: thread
+// 8 m + t gives the address of row t of matrix m, 16 bytes.
+__device__ __forceinline__ void store_transposed(uint32_t addr, const uint32_t (&m)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(m[0]),
+               "r"(m[1]), "r"(m[2]), "r"(m[3])
+               : "memory");
+}
+
 __device__ __forceinline__ float swiglu(float g, float u, float alpha, float limit) {
   g = g > limit ? limit : g;  // comparisons that let NaN through
   u = u > limit ? limit : (u < -limit ? -limit : u);
@@ -360,7 +379,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
   using C = GrpCfg<kFp4>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  GrpShared& sb = *reinterpret_cast<GrpShared*>(tiles + kRingBytes + C::kRawBytes);
+  GrpShared& sb = *reinterpret_cast<GrpShared*>(tiles + kRingBytes + C::kRawBytes + kEpiWarps * kPatchBytes);
   volatile int* abort_flag = &sb.abort_flag;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -745,43 +764,113 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
     const int half = (warp - kEpiWarp0) >> 2;  // the two warps of a lane quarter take turns of 32 columns
     const int q = warp & 3;                    // TMEM lane quarter (a warp reaches lanes 32 (warp % 4) ..)
     const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
+    // Rows of 16-byte pieces where the output allows them: the fragment's threads hold pairs of
+    // rows (columns) of a feature (lane), an 8 x 8 transposition through this warp's 512 bytes
+    // of shared memory makes eight features of a row of them.
+    uint8_t* patch = tiles + kRingBytes + C::kRawBytes + (warp - kEpiWarp0) * kPatchBytes;
+    const uint32_t patch0 = smem_u32(patch);
+    const int fr = lane >> 2;
+    // pieces of a row in the patch: 4 (2 with SwiGLU), at places that spread over the banks
+    const uint32_t put = kSwiglu ? patch0 + ((lane >> 4) * 8 + (lane & 7)) * 32 +
+                                       ((((lane >> 3) & 1) ^ ((lane >> 2) & 1)) << 4)
+                                 : patch0 + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
+    const uint8_t* get = kSwiglu ? patch + (lane >> 1) * 32 + (((lane & 1) ^ ((lane >> 3) & 1)) << 4)
+                                 : patch + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
+    const bool wide = a.n_out % 8 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0;
     int i = 0;
     for (int t = t_first; t < tiles_total; t += t_step, ++i) {
       const Tile tl = find_tile(sb, a, t, kCtas * width, lane);
       const int b = i & 1;
-      const int f = tl.f0 + rank * kFeat + 32 * q + lane;
-      const bool mine = 32 * q + lane < width && f < a.N;
-      float bias = 0.0f;
-      if (a.bias && mine)
-        bias = __uint_as_float(static_cast<uint32_t>(__ldg(a.bias + static_cast<long long>(tl.e) * a.N + f)) << 16);
-      uint16_t* out = a.out + static_cast<long long>(tl.r0) * a.n_out + (kSwiglu ? f >> 1 : f);
-      if (!wait_or_abort(smem_u32(&sb.acc_full[b]), (i >> 1) & 1, a.timeout_ns, abort_flag)) break;
-      tc_fence_after();
+      const int f0 = tl.f0 + rank * kFeat + 32 * q;  // first feature of this warp
+      const int most = min(width - 32 * q, a.N - f0);  // features that are the tile's and exist
       const uint32_t acc = tmem + lane_base + b * C::kRows;
+      const uint16_t* bias = a.bias ? a.bias + static_cast<long long>(tl.e) * a.N + f0 : nullptr;
+      auto bias_of = [&](int f) {
+        return bias && f < most ? __uint_as_float(static_cast<uint32_t>(__ldg(bias + f)) << 16) : 0.0f;
+      };
+      uint16_t* out = a.out + static_cast<long long>(tl.r0) * a.n_out + (kSwiglu ? f0 >> 1 : f0);
+      if (wide) {
+        const float b0 = bias_of(fr), b1 = bias_of(fr + 8), b2 = bias_of(fr + 16), b3 = bias_of(fr + 24);
+        if (!wait_or_abort(smem_u32(&sb.acc_full[b]), (i >> 1) & 1, a.timeout_ns, abort_flag)) break;
+        tc_fence_after();
 #pragma unroll 1
-      for (int c = 32 * half; c < tl.n; c += 64) {
-        uint32_t r[32];
-        tmem_ld32(acc + c, r);
-        tc_wait_ld();
-        if constexpr (kSwiglu) {
-          // even lanes hold gates, odd lanes the ups of the same outputs: the even lane takes
-          // columns 0..15, the odd one columns 16..31
-          const bool odd = lane & 1;
-          const int first = c + (odd ? 16 : 0);
+        for (int c = 32 * half; c < tl.n; c += 64) {
+          uint32_t lo[16], hi[16];  // features 0..15 and 16..31
+          tmem_ld_16x32(acc + c, lo);
+          tmem_ld_16x32(acc + (16u << 16) + c, hi);
+          tc_wait_ld();
+          if constexpr (kSwiglu) {
+            // Gate and up are neighbouring lanes, threads 4 apart.  The one with gates (even)
+            // finishes the outputs of its lower lane, the other those of its upper lane: of
+            // 8 outputs, thread row fr has number fr / 2 + 4 (fr % 2).
+            const bool odd = fr & 1;
+#pragma unroll
+            for (int i2 = 0; i2 < 2; ++i2) {
+              uint32_t m[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t* v = ((j & 1) ? hi : lo) + 4 * (2 * i2 + (j >> 1));
+                const float bl = (j & 1) ? b2 : b0, bh = (j & 1) ? b3 : b1;
+                float y[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const float l = __uint_as_float(v[k]) + bl, h = __uint_as_float(v[2 + k]) + bh;
+                  const float theirs = __shfl_xor_sync(0xffffffffu, odd ? l : h, 4);
+                  y[k] = swiglu(odd ? theirs : l, odd ? h : theirs, a.alpha, a.limit);
+                }
+                m[j] = pack_bf16x2(y[0], y[1]);
+              }
+              store_transposed(put, m);
+              __syncwarp();
+              const uint4 w = *reinterpret_cast<const uint4*>(get);
+              __syncwarp();
+              const int row = c + 16 * i2 + (lane >> 1), f = 8 * (lane & 1);
+              if (row < tl.n && 2 * f < most)  // outputs 0 4 | 1 5 | 2 6 | 3 7 put in order
+                *reinterpret_cast<uint4*>(out + static_cast<long long>(row) * a.n_out + f) =
+                    make_uint4(__byte_perm(w.x, w.y, 0x5410), __byte_perm(w.z, w.w, 0x5410),
+                               __byte_perm(w.x, w.y, 0x7632), __byte_perm(w.z, w.w, 0x7632));
+            }
+          } else {
+#pragma unroll
+            for (int i4 = 0; i4 < 4; ++i4) {
+              uint32_t m[4];
+              m[0] = pack_bf16x2(__uint_as_float(lo[4 * i4]) + b0, __uint_as_float(lo[4 * i4 + 1]) + b0);
+              m[1] = pack_bf16x2(__uint_as_float(lo[4 * i4 + 2]) + b1, __uint_as_float(lo[4 * i4 + 3]) + b1);
+              m[2] = pack_bf16x2(__uint_as_float(hi[4 * i4]) + b2, __uint_as_float(hi[4 * i4 + 1]) + b2);
+              m[3] = pack_bf16x2(__uint_as_float(hi[4 * i4 + 2]) + b3, __uint_as_float(hi[4 * i4 + 3]) + b3);
+              store_transposed(put, m);
+              __syncwarp();
+              const uint4 w = *reinterpret_cast<const uint4*>(get);
+              __syncwarp();
+              const int row = c + 8 * i4 + (lane >> 2), f = 8 * (lane & 3);
+              if (row < tl.n && f < most)
+                *reinterpret_cast<uint4*>(out + static_cast<long long>(row) * a.n_out + f) = w;
+            }
+          }
+        }
+      } else {
+        // any N and any address: a thread per feature, 2 bytes at a time
+        const bool mine = lane < most;
+        const float b0 = bias_of(lane);
+        out += kSwiglu ? lane >> 1 : lane;
+        if (!wait_or_abort(smem_u32(&sb.acc_full[b]), (i >> 1) & 1, a.timeout_ns, abort_flag)) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 16 * half; c < tl.n; c += 32) {
+          uint32_t r[16];
+          tmem_ld16(acc + c, r);
+          tc_wait_ld();
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const float lo = __uint_as_float(r[j]) + bias, hi = __uint_as_float(r[16 + j]) + bias;
-            const float theirs = __shfl_xor_sync(0xffffffffu, odd ? lo : hi, 1);
-            const float y = swiglu(odd ? theirs : lo, odd ? hi : theirs, a.alpha, a.limit);
-            if (mine && first + j < tl.n)
-              out[static_cast<long long>(first + j) * a.n_out] = static_cast<uint16_t>(pack_bf16x2(y, 0.0f) & 0xFFFFu);
+            float y = __uint_as_float(r[j]) + b0;
+            if constexpr (kSwiglu) {
+              // both lanes of a pair compute the output, the even one stores it
+              const float theirs = __shfl_xor_sync(0xffffffffu, y, 1);
+              y = swiglu((lane & 1) ? theirs : y, (lane & 1) ? y : theirs, a.alpha, a.limit);
+            }
+            if (mine && c + j < tl.n && !(kSwiglu && (lane & 1)))
+              out[static_cast<long long>(c + j) * a.n_out] = static_cast<uint16_t>(pack_bf16x2(y, 0.0f) & 0xFFFFu);
           }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (mine && c + j < tl.n)
-              out[static_cast<long long>(c + j) * a.n_out] =
-                  static_cast<uint16_t>(pack_bf16x2(__uint_as_float(r[j]) + bias, 0.0f) & 0xFFFFu);
         }
       }
       tc_fence_before();
