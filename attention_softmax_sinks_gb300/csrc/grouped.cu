@@ -13,9 +13,10 @@
 //   warp 0        loads the weights of a ring stage (one box of 128 features x 128 bytes of K,
 //                 128-byte swizzle) when it is free
 //   warp 1        TMEM owner and MMA issuer (one elected thread): 32 bytes of K per MMA
-//   warps 2, 3    MXFP4: scale bytes of the weights (2) and of the rows (3), written into the ring in the layout that tcgen05.cp
-//                 spreads over TMEM (row r of a block of 128: 4 bytes at 16 (r % 32) + 4 (r / 32),
-//                 512 bytes per 128 values of K)
+//   warps 2, 3    MXFP4: warp 2 stages the scale bytes of weights and rows, warp 3 writes them
+//                 into the ring in the layout that tcgen05.cp spreads over TMEM (row r of a
+//                 block of 128: 4 bytes at 16 (r % 32) + 4 (r / 32), 512 bytes per 128 values
+//                 of K); warp 3 also reports gathered rows to the tensor core
 //   warps 4..11   epilogue: TMEM lanes are features, columns rows; bias and activation in
 //                 fp32, one rounding, 8 x 8 transpositions through shared memory and 16-byte
 //                 stores, 64 consecutive bytes per row and warp (32 with SwiGLU, whose gate and
@@ -43,12 +44,12 @@ constexpr int kEpiWarp0 = 4;
 constexpr int kEpiWarps = 8;
 constexpr int kRowWarp0 = kEpiWarp0 + kEpiWarps;
 constexpr int kRowWarps = 4;
-constexpr int kMaxProducers = 3 + kRowWarps;  // weights, rows, and in MXFP4 two warps of scales
+constexpr int kMaxProducers = 2 + kRowWarps;  // warp 0, the row warps, warp 3
 constexpr int kThreads = 32 * (kRowWarp0 + kRowWarps);
 constexpr int kMaxStages = 16;
 constexpr int kRingBytes = 198 * 1024;
 constexpr int kMaxSingleRows = 64;  // rows of a single CTA's tile
-constexpr int kLag = 2;         // stages between a gather's request and its hand-over
+constexpr int kMaxRawPairs = 6;
 constexpr int kBand = 8;        // row tiles of an expert that pass over its features together
 constexpr int kSfBlock = 512;   // scales of 128 rows x 128 values of K
 constexpr int kPatchBytes = 512;       // of an epilogue warp
@@ -61,10 +62,10 @@ struct GrpCfg {
   static constexpr int kRows = kFp4 ? 224 : 256;
   static constexpr int kStageK = kFp4 ? 256 : 64;
   static constexpr int kSfBytes = kFp4 ? 2 * 3 * kSfBlock : 0;  // per 128 values of K: a block of weights, two of rows
-  static constexpr int kRawBytes = kFp4 ? 9 * kRawBlock : 0;  // three pairs' weights and rows, or six of a small tile
+  // staged scale bytes of three pairs of blocks (weights and rows), or of six of a small tile
+  static constexpr int kRawBytes = kFp4 ? 9 * kRawBlock : 0;
   static constexpr int kSfCols = 24;
   static constexpr int kTmemCols = 512;
-  static constexpr int kProducers = 1 + kRowWarps + (kFp4 ? 2 : 0);  // warps that fill a stage, per CTA
   static_assert(2 * kRows + (kFp4 ? 2 * kSfCols : 0) <= kTmemCols, "TMEM holds 512 columns");
 };
 
@@ -85,7 +86,8 @@ __host__ __device__ constexpr int stage_count(int width, int rows, int sub) {
 }
 
 struct GrpShared {
-  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t full[kMaxStages], empty[kMaxStages], landed[kMaxStages];
+  uint64_t raw_full[kMaxRawPairs], raw_empty[kMaxRawPairs];
   uint64_t acc_full[2], acc_empty[2], drain;
   uint32_t tmem_base;
   int abort_flag;
@@ -274,11 +276,11 @@ __device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* m
 __device__ __forceinline__ void copy_async16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_async_wait() {  // all but the N newest groups
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// This thread's arrival on `bar` once its copies so far have landed.
+__device__ __forceinline__ void copy_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ void copy_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Waits of a whole warp; the result is the same in all lanes.
 __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, uint64_t timeout_ns,
@@ -391,12 +393,16 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
   // a pair stages half of a tile's rows in each CTA
   constexpr int kCtas = kPair ? 2 : 1;
   constexpr int kGrain = 16 * kCtas;
+  constexpr int kRawPairs = kPair ? 3 : kMaxRawPairs, kRawStep = C::kRawBytes / kRawPairs;
   const int stage_rows = a.cap / kCtas;
   const int width = kPair ? kFeat : a.width;  // features of one CTA's part of a tile
   const uint32_t w_bytes = width * kStageKBytes;
   const uint32_t stage_size = stage_bytes<kFp4>(width, stage_rows, sub);
   const uint32_t x_part = sub * w_bytes, sf_part = x_part + sub * stage_rows * kStageKBytes;  // of a stage
   const int rank = kPair ? static_cast<int>(cluster_ctarank()) : 0;
+  // warps of a CTA that report a stage filled: gathered rows are reported by warp 3
+  const bool gather = a.row_token != nullptr;
+  const int producers = gather ? 2 : 1 + kRowWarps + (kFp4 ? 1 : 0);
   const int t_first = blockIdx.x / kCtas, t_step = gridDim.x / kCtas;
   // the leading CTA's barriers
   const uint32_t full0 = kPair ? dsmem_addr(smem_u32(&sb.full[0]), 0) : smem_u32(&sb.full[0]);
@@ -406,8 +412,13 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
     tma_prefetch_desc(&wmap);
     tma_prefetch_desc(&xmap);
     for (int s = 0; s < kMaxStages; ++s) {
-      mbar_init(smem_u32(&sb.full[s]), kCtas * C::kProducers);
+      mbar_init(smem_u32(&sb.full[s]), kCtas * producers);
+      mbar_init(smem_u32(&sb.landed[s]), 32 * kRowWarps);
       mbar_init(smem_u32(&sb.empty[s]), 1);
+    }
+    for (int r = 0; r < kMaxRawPairs; ++r) {
+      mbar_init(smem_u32(&sb.raw_full[r]), 32);
+      mbar_init(smem_u32(&sb.raw_empty[r]), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&sb.acc_full[b]), 1);
@@ -569,103 +580,115 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
       if (!mbar_wait(smem_u32(&sb.drain), 0, kDrainTimeoutNs)) raise_status(a.status, kStatusTimeout);
     }
     __syncwarp();
-  } else if (kFp4 && (warp == 2 || warp == 3)) {
-    // Scale bytes: a lane has rows lane, lane + 32, lane + 64, lane + 96 of each block of 128;
-    // 16 bytes of a row serve two blocks of K.  They travel by asynchronous copies into a place of
-    // the lane's own, requested some pairs of blocks ahead, and from there into the ring.
+  } else if (kFp4 && warp == 2) {
+    // Scale bytes on their way: a lane has rows lane, lane + 32, lane + 64, lane + 96 of each
+    // block of 128 (weights, rows, rows from 128 on), 16 bytes of a row serve two blocks of K.
+    // They go to a staging place by asynchronous copies, some pairs of blocks ahead.
     const int used = a.K / 32;  // scale bytes in use: zeros stand in for those behind
     const int pairs = (k_blocks + 1) / 2;
-    constexpr int kRawPairs = kPair ? 3 : 6;
-    constexpr int kRawStep = C::kRawBytes / kRawPairs;  // weights, then rows (64 of a small tile)
-    uint8_t* raw = tiles + kRingBytes + (warp == 2 ? 0 : kRawBlock) + 16 * lane;
+    const uint32_t raw = smem_u32(tiles + kRingBytes) + 16 * lane;
     RingPos p;
+    bool ok = true;
+    for (int t = t_first; t < tiles_total && ok; t += t_step) {
+      const Tile tl = find_tile(sb, a, t, kCtas * width, lane);
+      const uint8_t* src[3][4];  // nullptr: no such row, zeros
+#pragma unroll
+      for (int blk = 0; blk < 3; ++blk)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          src[blk][j] = nullptr;
+          if (blk == 0) {
+            const int r = 32 * j + lane, f = tl.f0 + rank * kFeat + r;
+            if (r < width && f < a.N)
+              src[blk][j] = a.w_scales + (static_cast<long long>(tl.e) * a.N + f) * a.scale_stride;
+          } else {
+            const int r = 128 * (blk - 1) + 32 * j + lane;
+            if (r < tl.n) {
+              long long row = tl.r0 + r;
+              if (gather) {
+                const int id = __ldg(a.row_token + tl.r0 + r);
+                row = id < 0 || id >= a.x_rows ? 0 : id;  // reported by the row warps
+              }
+              src[blk][j] = a.x_scales + row * a.scale_stride;
+            }
+          }
+        }
+      const int quarters = 4 + (tl.n + 31) / 32;
+      for (int pair = 0; pair < pairs; ++pair, p.next(kRawPairs)) {
+        if (p.round != 0)
+          ok = wait_or_abort(smem_u32(&sb.raw_empty[p.stage]), (p.round - 1) & 1, a.timeout_ns, abort_flag);
+        if (!ok) break;
+        const uint32_t dst = raw + p.stage * kRawStep;
+        const int valid = min(16, used - 16 * pair);
+#pragma unroll
+        for (int i = 0; i < 12; ++i)
+          if (i < quarters)
+            copy_async16(dst + 512 * i, src[i >> 2][i & 3] ? src[i >> 2][i & 3] + 16 * pair : a.w_scales,
+                         src[i >> 2][i & 3] ? valid : 0);
+        copy_async_arrive(smem_u32(&sb.raw_full[p.stage]));
+      }
+    }
+    copy_async_wait_all();
+    if (lane == 0 && !ok) raise_status(a.status, kStatusTimeout);
+  } else if (warp == 3 && (kFp4 || gather)) {
+    // What threads have brought becomes the tensor core's: scales are put in their layout,
+    // gathered rows have landed; then one proxy fence, by a warp that has no copies under way
+    // (with them, a fence takes as long as they do), and the stage is reported.
+    RingPos p, pr;
     int g = 0;
     bool ok = true;
     for (int t = t_first; t < tiles_total && ok; t += t_step) {
       const Tile tl = find_tile(sb, a, t, kCtas * width, lane);
-      const int blocks = warp == 2 ? 1 : tl.n > 128 ? 2 : 1;
-      const int most = kPair || warp == 2 ? kFeat : kMaxSingleRows;  // rows of a block that may have scales
-      const uint8_t* src[2][4];  // nullptr: no such row, zeros
-#pragma unroll
-      for (int blk = 0; blk < 2; ++blk)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = 128 * blk + 32 * j + lane;
-          src[blk][j] = nullptr;
-          if (warp == 2) {
-            const int f = tl.f0 + rank * kFeat + r;
-            if (blk == 0 && r < width && f < a.N)
-              src[blk][j] = a.w_scales + (static_cast<long long>(tl.e) * a.N + f) * a.scale_stride;
-          } else if (r < tl.n) {
-            long long row = tl.r0 + r;
-            if (a.row_token) {
-              const int id = __ldg(a.row_token + tl.r0 + r);
-              row = id < 0 || id >= a.x_rows ? 0 : id;  // reported by the row warps
-            }
-            src[blk][j] = a.x_scales + row * a.scale_stride;
-          }
-        }
-      auto request = [&](int pair) {
-        if (pair < pairs) {
-          const uint32_t dst = smem_u32(raw) + (pair % kRawPairs) * kRawStep;
-          const int valid = min(16, used - 16 * pair);
-#pragma unroll
-          for (int blk = 0; blk < 2; ++blk)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (blk < blocks && 32 * j < most)
-                copy_async16(dst + blk * kRawBlock + 512 * j, src[blk][j] ? src[blk][j] + 16 * pair : a.w_scales,
-                             src[blk][j] ? valid : 0);
-        }
-        copy_async_commit();
+      auto report = [&]() {
+        if (gather) ok = wait_or_abort(smem_u32(&sb.landed[p.stage]), p.round & 1, a.timeout_ns, abort_flag);
+        if (!ok) return;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (elect_one()) grp_arrive<kPair>(full0 + 8 * p.stage);
+        ++g;
+        p.next(stages);
       };
-#pragma unroll
-      for (int i = 0; i + 1 < kRawPairs; ++i) request(i);
-      for (int pair = 0; pair < pairs && ok; ++pair) {
-        request(pair + kRawPairs - 1);
-        copy_async_wait<kRawPairs - 1>();
-        const uint8_t* mine = raw + (pair % kRawPairs) * kRawStep;
-        uint4 c[2][4];
-#pragma unroll
-        for (int blk = 0; blk < 2; ++blk)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (blk < blocks)
-              c[blk][j] = 32 * j < most ? *reinterpret_cast<const uint4*>(mine + blk * kRawBlock + 512 * j)
-                                        : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int block = 2 * pair + h;
-          if (block >= k_blocks) break;
-          const int u = sub == 2 ? h : 0;
-          if (u == 0 && p.round != 0)
-            ok = wait_or_abort(smem_u32(&sb.empty[p.stage]), (p.round - 1) & 1, a.timeout_ns, abort_flag);
+      if constexpr (!kFp4) {
+        for (int kb = 0; kb < k_steps && ok; ++kb) report();
+      } else {
+        const int quarters = 4 + (tl.n + 31) / 32;
+        const bool two = tl.n > 128;
+        for (int block = 0; block < k_blocks && ok; block += 2, pr.next(kRawPairs)) {
+          ok = wait_or_abort(smem_u32(&sb.raw_full[pr.stage]), pr.round & 1, a.timeout_ns, abort_flag);
           if (!ok) break;
-          uint8_t* sf = tiles + p.stage * stage_size + sf_part + u * C::kSfBytes + (warp == 2 ? 0 : kSfBlock);
+          const uint8_t* raw = tiles + kRingBytes + pr.stage * kRawStep + 16 * lane;
+          uint4 c[12];
 #pragma unroll
-          for (int blk = 0; blk < 2; ++blk) {
-            if (blk >= blocks) break;
-            reinterpret_cast<uint4*>(sf + blk * kSfBlock)[lane] =
-                h == 0 ? make_uint4(c[blk][0].x, c[blk][1].x, c[blk][2].x, c[blk][3].x)
-                       : make_uint4(c[blk][0].z, c[blk][1].z, c[blk][2].z, c[blk][3].z);
-            reinterpret_cast<uint4*>(sf + (3 + blk) * kSfBlock)[lane] =
-                h == 0 ? make_uint4(c[blk][0].y, c[blk][1].y, c[blk][2].y, c[blk][3].y)
-                       : make_uint4(c[blk][0].w, c[blk][1].w, c[blk][2].w, c[blk][3].w);
-          }
-          if (u + 1 == sub || block + 1 == k_blocks) {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (elect_one()) grp_arrive<kPair>(full0 + 8 * p.stage);
-            ++g;
-            p.next(stages);
+          for (int i = 0; i < 12; ++i)
+            c[i] = i < quarters ? *reinterpret_cast<const uint4*>(raw + 512 * i) : make_uint4(0, 0, 0, 0);
+          __syncwarp();
+          if (elect_one()) mbar_arrive(smem_u32(&sb.raw_empty[pr.stage]));
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (block + h >= k_blocks) break;
+            const int u = sub == 2 ? h : 0;
+            if (u == 0 && p.round != 0)
+              ok = wait_or_abort(smem_u32(&sb.empty[p.stage]), (p.round - 1) & 1, a.timeout_ns, abort_flag);
+            if (!ok) break;
+            uint4* sf = reinterpret_cast<uint4*>(tiles + p.stage * stage_size + sf_part + u * C::kSfBytes) + lane;
+#pragma unroll
+            for (int blk = 0; blk < 3; ++blk) {
+              if (blk == 2 && !two) break;
+              const uint4* v = c + 4 * blk;
+              sf[blk * (kSfBlock / 16)] =
+                  h == 0 ? make_uint4(v[0].x, v[1].x, v[2].x, v[3].x) : make_uint4(v[0].z, v[1].z, v[2].z, v[3].z);
+              sf[(3 + blk) * (kSfBlock / 16)] =
+                  h == 0 ? make_uint4(v[0].y, v[1].y, v[2].y, v[3].y) : make_uint4(v[0].w, v[1].w, v[2].w, v[3].w);
+            }
+            if (u + 1 == sub || block + h + 1 == k_blocks) report();
+            if (!ok) break;
           }
         }
       }
-      copy_async_wait<0>();
     }
     if (lane == 0) {
       if (!ok) raise_status(a.status, kStatusTimeout);
-      sb.issued[1 + kRowWarps + warp - 2] = g;
+      sb.issued[1 + kRowWarps] = g;
     }
   } else if (warp >= kRowWarp0) {
     const int wr = warp - kRowWarp0;
@@ -673,23 +696,13 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
     RingPos p;
     int g = 0;
     bool ok = true;
-    if (a.row_token) {
+    if (gather) {
       // Gathered rows: eight threads per row copy its 128 bytes, 16 rows at a time, into the
-      // places of the 128-byte swizzle.  A stage is handed over (copies landed, fenced
-      // towards the tensor core's reads) once kLag newer ones have been requested.
+      // places of the 128-byte swizzle.
       const int tid = threadIdx.x - 32 * kRowWarp0;
       const int chunk = tid & 7, row0 = tid >> 3;
       const long long row_bytes = kFp4 ? a.K / 2 : 2LL * a.K;
       const uint32_t dst0 = x_part + row0 * kStageKBytes + ((chunk ^ (row0 & 7)) << 4);
-      RingPos done;
-      int handed = 0;
-      auto hand_over = [&]() {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (elect_one()) grp_arrive<kPair>(full0 + 8 * done.stage);
-        ++handed;
-        done.next(stages);
-      };
       for (int t = t_first; t < tiles_total && ok; t += t_step) {
         const Tile tl = find_tile(sb, a, t, kCtas * width, lane);
         const int half = (tl.n + kGrain - 1) / kGrain * 16;  // rows that this CTA stages
@@ -723,15 +736,10 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
             for (int i = 0; i < kSteps; ++i)
               if (i < steps) copy_async16(dst + i * 16 * kStageKBytes, src[i] + (data ? at : 0), data ? 16 : 0);
           }
-          copy_async_commit();
-          if (g - handed >= kLag) {
-            copy_async_wait<kLag>();
-            hand_over();
-          }
+          copy_async_arrive(smem_u32(&sb.landed[p.stage]));
         }
       }
-      copy_async_wait<0>();
-      while (handed < g) hand_over();
+      copy_async_wait_all();
     } else {
       for (int t = t_first; t < tiles_total && ok; t += t_step) {
         const Tile tl = find_tile(sb, a, t, kCtas * width, lane);
@@ -894,15 +902,17 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
         x = *const_cast<const volatile int*>(v);
       return x;
     };
+    auto reports = [&](int w) { return w == 0 || (w <= kRowWarps ? !gather : kFp4 || gather); };
     int aborted = 0, most = 0;
     for (int c = 0; c < kCtas; ++c) {
       aborted |= peer(&sb.abort_flag, c);
-      for (int w = 0; w < C::kProducers; ++w) most = max(most, peer(&sb.issued[w], c));
+      for (int w = 0; w < kMaxProducers; ++w)
+        if (reports(w)) most = max(most, peer(&sb.issued[w], c));
     }
     if (aborted) {
       for (int c = 0; c < kCtas; ++c)
-        for (int w = 0; w < C::kProducers; ++w)
-          for (int g = peer(&sb.issued[w], c); g < most; ++g) grp_arrive<kPair>(full0 + 8 * (g % stages));
+        for (int w = 0; w < kMaxProducers; ++w)
+          for (int g = reports(w) ? peer(&sb.issued[w], c) : most; g < most; ++g) grp_arrive<kPair>(full0 + 8 * (g % stages));
       for (int s = 0; s < stages && s < most; ++s) {
         const int last = most - 1 - ((most - 1 - s) % stages);
         if (!mbar_wait(smem_u32(&sb.full[s]), (last / stages) & 1, kDrainTimeoutNs))
