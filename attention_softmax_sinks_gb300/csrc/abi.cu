@@ -132,6 +132,20 @@ sa_status map_rows(CUtensorMap* m, const void* base, long long rows, long long r
   return r == CUDA_SUCCESS ? SA_OK : SA_ERR_CUDA;
 }
 
+// MXFP4 scale bytes [rows, stride] read in boxes of 16 bytes x box_rows.
+sa_status map_scales(CUtensorMap* m, const void* base, long long rows, int stride, int box_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc;
+  if (sa_status s = encoder(&enc)) return s;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(stride), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride)};
+  cuuint32_t box[2] = {16, static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? SA_OK : SA_ERR_CUDA;
+}
+
 // Paged cache [num_pages, hkv, 16, 64] viewed as [num_pages*hkv*16, 64] rows,
 // one box = one (page, kv head) = 16 rows.
 sa_status map_pages(CUtensorMap* m, const void* base, int num_pages, int hkv) {
@@ -302,6 +316,7 @@ sa_status grouped_common(const GroupedCall& c, cudaStream_t stream) {
     return SA_ERR_SHAPE;
   if (c.experts < 1 || c.experts > sa::kMaxExperts) return SA_ERR_SHAPE;
   if (c.swiglu && (c.n % 2 != 0 || !std::isfinite(c.alpha) || !(c.limit > 0.0f))) return SA_ERR_SHAPE;
+  if (static_cast<long long>(c.experts) * c.n >= (1LL << 31)) return SA_ERR_SHAPE;
   if (c.k % (c.mxfp4 ? 32 : 8) != 0) return SA_ERR_UNSUPPORTED;
   if (c.rows == 0) return SA_OK;
   if (!c.x || !c.w || !c.out || (c.grouped && !c.offsets)) return SA_ERR_NULL;
@@ -337,10 +352,15 @@ sa_status grouped_common(const GroupedCall& c, cudaStream_t stream) {
   const int sms = sm_count();
   sa::grouped_plan(a, c.mxfp4, sms);
   const long long row_bytes = c.mxfp4 ? c.k / 2 : 2LL * c.k;
-  CUtensorMap wm, xm;
-  if (sa_status s = map_experts(&wm, c.w, c.experts, c.n, row_bytes, a.width, c.mxfp4)) return s;
-  if (sa_status s = map_rows(&xm, c.x, c.x_rows, row_bytes, sa::kBoxRows, c.mxfp4)) return s;
-  return sa::launch_grouped(wm, xm, a, c.mxfp4, sms, stream) == cudaSuccess ? SA_OK : SA_ERR_LAUNCH;
+  sa::GroupedMaps m{};
+  if (sa_status s = map_experts(&m.w, c.w, c.experts, c.n, row_bytes, a.width, c.mxfp4)) return s;
+  if (sa_status s = map_rows(&m.x, c.x, c.x_rows, row_bytes, sa::kBoxRows, c.mxfp4)) return s;
+  if (c.mxfp4 && a.pair) {
+    const long long w_rows = static_cast<long long>(c.experts) * c.n;
+    if (sa_status s = map_scales(&m.w_scales, c.w_scales, w_rows, a.scale_stride, a.width)) return s;
+    if (sa_status s = map_scales(&m.x_scales, c.x_scales, c.x_rows, a.scale_stride, 32)) return s;
+  }
+  return sa::launch_grouped(m, a, c.mxfp4, sms, stream) == cudaSuccess ? SA_OK : SA_ERR_LAUNCH;
 }
 
 sa_status check_mxfp4(long long rows, int k) {

@@ -44,8 +44,8 @@ constexpr int kEpiWarp0 = 4;
 constexpr int kEpiWarps = 8;
 constexpr int kRowWarp0 = kEpiWarp0 + kEpiWarps;
 constexpr int kRowWarps = 4;
-constexpr int kMaxProducers = 2 + kRowWarps;  // warp 0, the row warps, warp 3
-constexpr int kThreads = 32 * (kRowWarp0 + kRowWarps);
+constexpr int kScaleWarp = kRowWarp0 + kRowWarps;  // MXFP4 in a pair: beside warp 3
+constexpr int kMaxProducers = 3 + kRowWarps;       // warp 0, the row warps, warp 3 and kScaleWarp
 constexpr int kMaxStages = 16;
 constexpr int kRingBytes = 198 * 1024;
 constexpr int kMaxSingleRows = 64;  // rows of a single CTA's tile
@@ -55,6 +55,11 @@ constexpr int kSfBlock = 512;   // scales of 128 rows x 128 values of K
 constexpr int kPatchBytes = 512;       // of an epilogue warp
 constexpr int kRawBlock = 128 * 16;  // scale bytes on their way: 16 per row of a block of 128
 constexpr unsigned long long kDrainTimeoutNs = 2000000000ull;
+
+template <bool kFp4, bool kPair>
+__host__ __device__ constexpr int grp_threads() {
+  return 32 * (kScaleWarp + (kFp4 && kPair ? 1 : 0));
+}
 
 template <bool kFp4>
 struct GrpCfg {
@@ -66,7 +71,7 @@ struct GrpCfg {
   static constexpr int kRawBytes = kFp4 ? 9 * kRawBlock : 0;
   static constexpr int kSfCols = 24;
   static constexpr int kTmemCols = 512;
-  static_assert(2 * kRows + (kFp4 ? 2 * kSfCols : 0) <= kTmemCols, "TMEM holds 512 columns");
+    static_assert(2 * kRows + (kFp4 ? 2 * kSfCols : 0) <= kTmemCols, "TMEM holds 512 columns");
 };
 
 // A stage holds `sub` blocks of kStageKBytes of K: `width` features and `rows` rows of 128 bytes
@@ -92,6 +97,7 @@ struct GrpShared {
   uint32_t tmem_base;
   int abort_flag;
   int issued[kMaxProducers];     // stages that each producer warp filled, written when it ends
+  int raw_issued;                // pairs of scales that warp 2 requested, likewise
   int total;                     // row tiles of all experts
   int cum[kMaxExperts + 32];     // row tiles of lower experts (a huge number from E + 1 on)
   int4 group[kMaxExperts];       // first row, rows, row tiles, rows per tile
@@ -375,8 +381,9 @@ __device__ __forceinline__ float swiglu(float g, float u, float alpha, float lim
 }
 
 template <bool kFp4, bool kSwiglu, bool kPair>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(grp_threads<kFp4, kPair>(), 1)
 grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+               const __grid_constant__ CUtensorMap wsmap, const __grid_constant__ CUtensorMap xsmap,
                const GroupedArgs a) {
   using C = GrpCfg<kFp4>;
   extern __shared__ uint8_t smem_raw[];
@@ -402,7 +409,8 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
   const int rank = kPair ? static_cast<int>(cluster_ctarank()) : 0;
   // warps of a CTA that report a stage filled: gathered rows are reported by warp 3
   const bool gather = a.row_token != nullptr;
-  const int producers = gather ? 2 : 1 + kRowWarps + (kFp4 ? 1 : 0);
+  constexpr int kScaleWarps = kFp4 ? kCtas : 0;
+  const int producers = 1 + (gather ? 0 : kRowWarps) + (kFp4 ? kScaleWarps : gather ? 1 : 0);
   const int t_first = blockIdx.x / kCtas, t_step = gridDim.x / kCtas;
   // the leading CTA's barriers
   const uint32_t full0 = kPair ? dsmem_addr(smem_u32(&sb.full[0]), 0) : smem_u32(&sb.full[0]);
@@ -411,14 +419,18 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&wmap);
     tma_prefetch_desc(&xmap);
+    if (kFp4 && kPair) {
+      tma_prefetch_desc(&wsmap);
+      tma_prefetch_desc(&xsmap);
+    }
     for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(smem_u32(&sb.full[s]), kCtas * producers);
       mbar_init(smem_u32(&sb.landed[s]), 32 * kRowWarps);
       mbar_init(smem_u32(&sb.empty[s]), 1);
     }
-    for (int r = 0; r < kMaxRawPairs; ++r) {
-      mbar_init(smem_u32(&sb.raw_full[r]), 32);
-      mbar_init(smem_u32(&sb.raw_empty[r]), 1);
+    for (int r = 0; kFp4 && r < kMaxRawPairs; ++r) {
+      mbar_init(smem_u32(&sb.raw_full[r]), kPair ? (gather ? 33 : 1) : 32);
+      mbar_init(smem_u32(&sb.raw_empty[r]), kScaleWarps);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&sb.acc_full[b]), 1);
@@ -427,6 +439,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
     mbar_init(smem_u32(&sb.drain), 1);
     sb.abort_flag = 0;
     for (int w = 0; w < kMaxProducers; ++w) sb.issued[w] = 0;
+    sb.raw_issued = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -581,114 +594,166 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
     }
     __syncwarp();
   } else if (kFp4 && warp == 2) {
-    // Scale bytes on their way: a lane has rows lane, lane + 32, lane + 64, lane + 96 of each
-    // block of 128 (weights, rows, rows from 128 on), 16 bytes of a row serve two blocks of K.
-    // They go to a staging place by asynchronous copies, some pairs of blocks ahead.
-    const int used = a.K / 32;  // scale bytes in use: zeros stand in for those behind
-    const int pairs = (k_blocks + 1) / 2;
-    const uint32_t raw = smem_u32(tiles + kRingBytes) + 16 * lane;
-    RingPos p;
-    bool ok = true;
-    for (int t = t_first; t < tiles_total && ok; t += t_step) {
-      const Tile tl = find_tile(sb, a, t, kCtas * width, lane);
-      const uint8_t* src[3][4];  // nullptr: no such row, zeros
+    if constexpr (kFp4) {
+      // Scale bytes on their way, some pairs of blocks of K ahead: 16 bytes of a row serve a pair.
+      // In a pair of CTAs they come in boxes of 16 bytes x rows, but for gathered rows: copies by
+      // threads, 16 bytes from each of 32 rows, keep the load unit as busy as whole lines would,
+      // and there is enough of them to tell.  Small tiles take copies throughout (boxes: 61 tokens
+      // up 166 us instead of 158).
+      const int pairs = (k_blocks + 1) / 2;
+      const uint32_t raw = smem_u32(tiles + kRingBytes);
+      constexpr int kRowQuarters = (kPair ? GrpCfg<true>::kRows : kMaxSingleRows) / 32;
+      RingPos p;
+      bool ok = true;
+      for (int t = t_first; t < tiles_total && ok; t += t_step) {
+        const Tile tl = find_tile(sb, a, t, kCtas * width, lane);
+        const int quarters = (tl.n + 31) / 32;  // of blocks of 128 rows
+        const bool by_threads = !kPair || gather;
+        const uint8_t* src[kRowQuarters];
+        const uint8_t* wsrc[kPair ? 1 : 4];
 #pragma unroll
-      for (int blk = 0; blk < 3; ++blk)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          src[blk][j] = nullptr;
-          if (blk == 0) {
-            const int r = 32 * j + lane, f = tl.f0 + rank * kFeat + r;
-            if (r < width && f < a.N)
-              src[blk][j] = a.w_scales + (static_cast<long long>(tl.e) * a.N + f) * a.scale_stride;
-          } else {
-            const int r = 128 * (blk - 1) + 32 * j + lane;
-            if (r < tl.n) {
-              long long row = tl.r0 + r;
-              if (gather) {
-                const int id = __ldg(a.row_token + tl.r0 + r);
-                row = id < 0 || id >= a.x_rows ? 0 : id;  // reported by the row warps
-              }
-              src[blk][j] = a.x_scales + row * a.scale_stride;
+        for (int j = 0; j < kRowQuarters; ++j) {
+          const int r = 32 * j + lane;
+          src[j] = nullptr;  // behind the tile's last row: zeros
+          if (by_threads && r < tl.n) {
+            long long row = tl.r0 + r;
+            if (gather) {
+              const int id = __ldg(a.row_token + tl.r0 + r);
+              row = id < 0 || id >= a.x_rows ? 0 : id;  // reported by the row warps
             }
+            src[j] = a.x_scales + row * a.scale_stride;
           }
         }
-      const int quarters = 4 + (tl.n + 31) / 32;
-      for (int pair = 0; pair < pairs; ++pair, p.next(kRawPairs)) {
-        if (p.round != 0)
-          ok = wait_or_abort(smem_u32(&sb.raw_empty[p.stage]), (p.round - 1) & 1, a.timeout_ns, abort_flag);
-        if (!ok) break;
-        const uint32_t dst = raw + p.stage * kRawStep;
-        const int valid = min(16, used - 16 * pair);
+        const int f0 = tl.f0 + rank * kFeat;
+        if constexpr (!kPair) {
 #pragma unroll
-        for (int i = 0; i < 12; ++i)
-          if (i < quarters)
-            copy_async16(dst + 512 * i, src[i >> 2][i & 3] ? src[i >> 2][i & 3] + 16 * pair : a.w_scales,
-                         src[i >> 2][i & 3] ? valid : 0);
-        copy_async_arrive(smem_u32(&sb.raw_full[p.stage]));
+          for (int j = 0; j < 4; ++j) {
+            const int r = 32 * j + lane;
+            wsrc[j] = r < width && f0 + r < a.N
+                          ? a.w_scales + (static_cast<long long>(tl.e) * a.N + f0 + r) * a.scale_stride
+                          : nullptr;
+          }
+        }
+        for (int pair = 0; pair < pairs; ++pair, p.next(kRawPairs)) {
+          if (p.round != 0)
+            ok = wait_or_abort(smem_u32(&sb.raw_empty[p.stage]), (p.round - 1) & 1, a.timeout_ns, abort_flag);
+          if (!ok) break;
+          const uint32_t bar = smem_u32(&sb.raw_full[p.stage]);
+          const uint32_t dst = raw + p.stage * kRawStep;
+          if constexpr (kPair) {
+            if (elect_one()) {
+              mbar_arrive_expect_tx(bar, 16 * width + (gather ? 0 : 512 * quarters));
+              tma_load_rows<false>(dst, &wsmap, 16 * pair, tl.e * a.N + f0, bar);  // E N < 2^31
+            }
+            if (!gather && lane < quarters)
+              tma_load_rows<false>(dst + kRawBlock + 512 * lane, &xsmap, 16 * pair, tl.r0 + 32 * lane, bar);
+            __syncwarp();
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (32 * j < width)
+                copy_async16(dst + 512 * j + 16 * lane, wsrc[j] ? wsrc[j] + 16 * pair : a.w_scales, wsrc[j] ? 16 : 0);
+          }
+          if (by_threads) {
+#pragma unroll
+            for (int j = 0; j < kRowQuarters; ++j)
+              if (j < quarters)
+                copy_async16(dst + kRawBlock + 512 * j + 16 * lane, src[j] ? src[j] + 16 * pair : a.x_scales,
+                             src[j] ? 16 : 0);
+            copy_async_arrive(bar);
+          }
+        }
+      }
+      copy_async_wait_all();
+      if (lane == 0) {
+        if (!ok) raise_status(a.status, kStatusTimeout);
+        sb.raw_issued = p.round * kRawPairs + p.stage;
       }
     }
-    copy_async_wait_all();
-    if (lane == 0 && !ok) raise_status(a.status, kStatusTimeout);
-  } else if (warp == 3 && (kFp4 || gather)) {
+  } else if ((warp == 3 && (kFp4 || gather)) || (kFp4 && kPair && warp == kScaleWarp)) {
     // What threads have brought becomes the tensor core's: scales are put in their layout,
     // gathered rows have landed; then one proxy fence, by a warp that has no copies under way
-    // (with them, a fence takes as long as they do), and the stage is reported.
+    // (with them, a fence takes as long as they do), and the stage is reported.  In a pair of
+    // CTAs two warps take turns of one block of K (warp 3 the even ones) and both report every
+    // stage; alone, one warp is faster (61 tokens up: 158 us, with two 164).
+    const int turn = kFp4 && kPair ? (warp == kScaleWarp ? 1 : 0) : -1;  // -1: all blocks
     RingPos p, pr;
     int g = 0;
     bool ok = true;
     for (int t = t_first; t < tiles_total && ok; t += t_step) {
-      const Tile tl = find_tile(sb, a, t, kCtas * width, lane);
-      auto report = [&]() {
-        if (gather) ok = wait_or_abort(smem_u32(&sb.landed[p.stage]), p.round & 1, a.timeout_ns, abort_flag);
-        if (!ok) return;
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (elect_one()) grp_arrive<kPair>(full0 + 8 * p.stage);
-        ++g;
-        p.next(stages);
-      };
       if constexpr (!kFp4) {
-        for (int kb = 0; kb < k_steps && ok; ++kb) report();
+        for (int kb = 0; kb < k_steps; ++kb, ++g, p.next(stages)) {
+          ok = wait_or_abort(smem_u32(&sb.landed[p.stage]), p.round & 1, a.timeout_ns, abort_flag);
+          if (!ok) break;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (elect_one()) grp_arrive<kPair>(full0 + 8 * p.stage);
+        }
       } else {
-        const int quarters = 4 + (tl.n + 31) / 32;
-        const bool two = tl.n > 128;
+        const Tile tl = find_tile(sb, a, t, kCtas * width, lane);
+        const int quarters = (tl.n + 31) / 32;
+        const int used = a.K / 32;  // scale bytes in use: what lies behind is padding
         for (int block = 0; block < k_blocks && ok; block += 2, pr.next(kRawPairs)) {
           ok = wait_or_abort(smem_u32(&sb.raw_full[pr.stage]), pr.round & 1, a.timeout_ns, abort_flag);
           if (!ok) break;
           const uint8_t* raw = tiles + kRingBytes + pr.stage * kRawStep + 16 * lane;
-          uint4 c[12];
+          // A block's 8 bytes of rows lane, lane + 32, lane + 64, lane + 96 of each block of 128.
+          // All that can be there is read, without a branch: what rows behind the tile's last
+          // one (or features behind its width) have there scales columns (lanes) that are never stored.
+          constexpr int kQuarters = 4 + (kPair ? GrpCfg<true>::kRows : kMaxSingleRows) / 32;
+          uint2 c[kPair ? 1 : 2][12];
 #pragma unroll
-          for (int i = 0; i < 12; ++i)
-            c[i] = i < quarters ? *reinterpret_cast<const uint4*>(raw + 512 * i) : make_uint4(0, 0, 0, 0);
+          for (int h = 0; h < (kPair ? 1 : 2); ++h) {
+            const int half = kPair ? turn : h;
+#pragma unroll
+            for (int i = 0; i < 12; ++i)
+              c[h][i] = i < kQuarters ? *reinterpret_cast<const uint2*>(raw + 512 * i + 8 * half) : make_uint2(0, 0);
+            const int valid = used - 8 * (block + half);  // bytes, the rest is padding
+            if (valid < 8) {
+              const uint32_t mask0 = valid >= 4 ? 0xFFFFFFFFu : valid <= 0 ? 0u : (1u << (8 * valid)) - 1u;
+              const uint32_t mask1 = valid <= 4 ? 0u : (1u << (8 * valid - 32)) - 1u;
+#pragma unroll
+              for (int i = 0; i < kQuarters; ++i) c[h][i] = make_uint2(c[h][i].x & mask0, c[h][i].y & mask1);
+            }
+          }
           __syncwarp();
           if (elect_one()) mbar_arrive(smem_u32(&sb.raw_empty[pr.stage]));
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (block + h >= k_blocks) break;
             const int u = sub == 2 ? h : 0;
+            const bool mine = !kPair || h == turn;
             if (u == 0 && p.round != 0)
               ok = wait_or_abort(smem_u32(&sb.empty[p.stage]), (p.round - 1) & 1, a.timeout_ns, abort_flag);
             if (!ok) break;
-            uint4* sf = reinterpret_cast<uint4*>(tiles + p.stage * stage_size + sf_part + u * C::kSfBytes) + lane;
+            if (mine) {
+              uint4* sf = reinterpret_cast<uint4*>(tiles + p.stage * stage_size + sf_part + u * C::kSfBytes) + lane;
 #pragma unroll
-            for (int blk = 0; blk < 3; ++blk) {
-              if (blk == 2 && !two) break;
-              const uint4* v = c + 4 * blk;
-              sf[blk * (kSfBlock / 16)] =
-                  h == 0 ? make_uint4(v[0].x, v[1].x, v[2].x, v[3].x) : make_uint4(v[0].z, v[1].z, v[2].z, v[3].z);
-              sf[(3 + blk) * (kSfBlock / 16)] =
-                  h == 0 ? make_uint4(v[0].y, v[1].y, v[2].y, v[3].y) : make_uint4(v[0].w, v[1].w, v[2].w, v[3].w);
+              for (int blk = 0; blk < 3; ++blk) {
+                if (blk == 2 && quarters <= 4) break;
+                const uint2* v = c[kPair ? 0 : h] + 4 * blk;
+                sf[blk * (kSfBlock / 16)] = make_uint4(v[0].x, v[1].x, v[2].x, v[3].x);
+                sf[(3 + blk) * (kSfBlock / 16)] = make_uint4(v[0].y, v[1].y, v[2].y, v[3].y);
+              }
             }
-            if (u + 1 == sub || block + h + 1 == k_blocks) report();
-            if (!ok) break;
+            if (u + 1 == sub || block + h + 1 == k_blocks) {
+              if (mine) {
+                if (gather) ok = wait_or_abort(smem_u32(&sb.landed[p.stage]), p.round & 1, a.timeout_ns, abort_flag);
+                if (!ok) break;
+                fence_proxy_async_smem();
+                __syncwarp();
+              }
+              if (elect_one()) grp_arrive<kPair>(full0 + 8 * p.stage);
+              ++g;
+              p.next(stages);
+            }
           }
         }
       }
     }
     if (lane == 0) {
       if (!ok) raise_status(a.status, kStatusTimeout);
-      sb.issued[1 + kRowWarps] = g;
+      sb.issued[1 + kRowWarps + (turn > 0)] = g;
     }
   } else if (warp >= kRowWarp0) {
     const int wr = warp - kRowWarp0;
@@ -708,18 +773,19 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
         const int half = (tl.n + kGrain - 1) / kGrain * 16;  // rows that this CTA stages
         const int steps = half >> 4;
         const uint8_t* src[kSteps];
+        uint32_t has = 0;  // zeros behind the tile's last row: no request
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
-          src[i] = nullptr;
-          if (i < steps) {
-            // rows behind the tile's last one repeat its first: their columns are never stored
-            const int r = rank * half + 16 * i + row0;
-            int id = __ldg(a.row_token + tl.r0 + (r < tl.n ? r : 0));
+          const int r = rank * half + 16 * i + row0;
+          src[i] = a.x;
+          if (i < steps && r < tl.n) {
+            int id = __ldg(a.row_token + tl.r0 + r);
             if (id < 0 || id >= a.x_rows) {
               raise_status(a.status, kStatusBadLen);
               id = 0;
             }
-            src[i] = a.x + id * row_bytes + 16 * chunk;
+            src[i] += id * row_bytes + 16 * chunk;
+            has |= 1u << i;
           }
         }
         for (int kb = 0; kb < k_steps; ++kb, ++g, p.next(stages)) {
@@ -734,7 +800,10 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
             const uint32_t dst = ring + p.stage * stage_size + dst0 + u * stage_rows * kStageKBytes;
 #pragma unroll
             for (int i = 0; i < kSteps; ++i)
-              if (i < steps) copy_async16(dst + i * 16 * kStageKBytes, src[i] + (data ? at : 0), data ? 16 : 0);
+              if (i < steps) {
+                const bool read = data && (has >> i & 1);
+                copy_async16(dst + i * 16 * kStageKBytes, src[i] + (read ? at : 0), read ? 16 : 0);
+              }
           }
           copy_async_arrive(smem_u32(&sb.landed[p.stage]));
         }
@@ -889,6 +958,14 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
 
   tc_fence_before();
   __syncthreads();
+  if (kFp4 && threadIdx.x == 0) {
+    // scales that nobody waited for (the last ones of an aborted run)
+    for (int r = 0; r < kRawPairs && r < sb.raw_issued; ++r) {
+      const int last = sb.raw_issued - 1 - ((sb.raw_issued - 1 - r) % kRawPairs);
+      if (!mbar_wait(smem_u32(&sb.raw_full[r]), (last / kRawPairs) & 1, kDrainTimeoutNs))
+        raise_status(a.status, kStatusTimeout);
+    }
+  }
   if constexpr (kPair) cluster_sync();
   if (threadIdx.x == 0 && rank == 0) {
     // Copies still in flight land before the shared memory is released.  A stage completes once
@@ -902,7 +979,9 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
         x = *const_cast<const volatile int*>(v);
       return x;
     };
-    auto reports = [&](int w) { return w == 0 || (w <= kRowWarps ? !gather : kFp4 || gather); };
+    auto reports = [&](int w) {
+      return w == 0 || (w <= kRowWarps ? !gather : w == 1 + kRowWarps ? kFp4 || gather : kScaleWarps == 2);
+    };
     int aborted = 0, most = 0;
     for (int c = 0; c < kCtas; ++c) {
       aborted |= peer(&sb.abort_flag, c);
@@ -936,7 +1015,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
 }
 
 template <bool kFp4, bool kSwiglu, bool kPair>
-cudaError_t launch_grouped_t(const CUtensorMap& wmap, const CUtensorMap& xmap, const GroupedArgs& a, int sms,
+cudaError_t launch_grouped_t(const GroupedMaps& m, const GroupedArgs& a, int sms,
                              cudaStream_t stream) {
   auto kernel = grouped_kernel<kFp4, kSwiglu, kPair>;
   // the shared-memory opt-in, once per device (host threads may race here: atomic flags,
@@ -966,7 +1045,7 @@ cudaError_t launch_grouped_t(const CUtensorMap& wmap, const CUtensorMap& xmap, c
   const int slots = sms / kCtas;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((most < slots ? most : slots) * kCtas));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(grp_threads<kFp4, kPair>());
   cfg.dynamicSmemBytes = smem_bytes<kFp4>();
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -976,17 +1055,17 @@ cudaError_t launch_grouped_t(const CUtensorMap& wmap, const CUtensorMap& xmap, c
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = kPair ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, wmap, xmap, b);
+  return cudaLaunchKernelEx(&cfg, kernel, m.w, m.x, m.w_scales, m.x_scales, b);
 }
 
 template <bool kFp4>
-cudaError_t launch_grouped_f(const CUtensorMap& wmap, const CUtensorMap& xmap, const GroupedArgs& a, int sms,
+cudaError_t launch_grouped_f(const GroupedMaps& m, const GroupedArgs& a, int sms,
                              cudaStream_t stream) {
   if (a.pair)
-    return a.swiglu ? launch_grouped_t<kFp4, true, true>(wmap, xmap, a, sms, stream)
-                    : launch_grouped_t<kFp4, false, true>(wmap, xmap, a, sms, stream);
-  return a.swiglu ? launch_grouped_t<kFp4, true, false>(wmap, xmap, a, sms, stream)
-                  : launch_grouped_t<kFp4, false, false>(wmap, xmap, a, sms, stream);
+    return a.swiglu ? launch_grouped_t<kFp4, true, true>(m, a, sms, stream)
+                    : launch_grouped_t<kFp4, false, true>(m, a, sms, stream);
+  return a.swiglu ? launch_grouped_t<kFp4, true, false>(m, a, sms, stream)
+                  : launch_grouped_t<kFp4, false, false>(m, a, sms, stream);
 }
 
 }  // namespace
@@ -1024,9 +1103,8 @@ void grouped_plan(GroupedArgs& a, bool mxfp4, int sms) {
   a.tiles_f = static_cast<int>((static_cast<long long>(a.N) + features - 1) / features);
 }
 
-cudaError_t launch_grouped(const CUtensorMap& wmap, const CUtensorMap& xmap, const GroupedArgs& a, bool mxfp4,
-                           int sms, cudaStream_t stream) {
-  return mxfp4 ? launch_grouped_f<true>(wmap, xmap, a, sms, stream) : launch_grouped_f<false>(wmap, xmap, a, sms, stream);
+cudaError_t launch_grouped(const GroupedMaps& m, const GroupedArgs& a, bool mxfp4, int sms, cudaStream_t stream) {
+  return mxfp4 ? launch_grouped_f<true>(m, a, sms, stream) : launch_grouped_f<false>(m, a, sms, stream);
 }
 
 }  // namespace sa

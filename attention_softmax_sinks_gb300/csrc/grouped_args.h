@@ -41,9 +41,12 @@ struct GroupedArgs {
 // 16, 64 or, for pairs, 256 in bf16 and 224 in MXFP4 (whose scales take TMEM columns beside
 // the accumulators).
 void grouped_plan(GroupedArgs& a, bool mxfp4, int sms);
-// wmap: w as {K, N, E} in boxes of 128 bytes x width x 1;
-// xmap: x [x_rows, K] in boxes of 128 bytes x kBoxRows.
-cudaError_t launch_grouped(const CUtensorMap& wmap, const CUtensorMap& xmap, const GroupedArgs& a, bool mxfp4,
-                           int sms, cudaStream_t stream);
+// w: {K, N, E} in boxes of 128 bytes x width x 1;  x: [x_rows, K] in boxes of 128 bytes x
+// kBoxRows;  MXFP4 scales, with pairs only: [E N, scale_stride] in boxes of 16 bytes x width and
+// [x_rows, scale_stride] in boxes of 16 bytes x 32.
+struct GroupedMaps {
+  CUtensorMap w, x, w_scales, x_scales;
+};
+cudaError_t launch_grouped(const GroupedMaps& m, const GroupedArgs& a, bool mxfp4, int sms, cudaStream_t stream);
 
 }  // namespace sa
