@@ -316,7 +316,7 @@ sa_status grouped_common(const GroupedCall& c, cudaStream_t stream) {
     return SA_ERR_SHAPE;
   if (c.experts < 1 || c.experts > sa::kMaxExperts) return SA_ERR_SHAPE;
   if (c.swiglu && (c.n % 2 != 0 || !std::isfinite(c.alpha) || !(c.limit > 0.0f))) return SA_ERR_SHAPE;
-  if (static_cast<long long>(c.experts) * c.n >= (1LL << 31)) return SA_ERR_SHAPE;
+  if (static_cast<long long>(c.experts) * c.n > (1LL << 31) - 1024) return SA_ERR_SHAPE;
   if (c.k % (c.mxfp4 ? 32 : 8) != 0) return SA_ERR_UNSUPPORTED;
   if (c.rows == 0) return SA_OK;
   if (!c.x || !c.w || !c.out || (c.grouped && !c.offsets)) return SA_ERR_NULL;

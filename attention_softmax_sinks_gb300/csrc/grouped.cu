@@ -9,26 +9,43 @@
 // issues MMAs of N = n rounded up to 16 and loads only those rows.  Transposed this way no
 // tensor work is padded beyond 16 rows, and one kernel serves one row and thousands.
 //
-// A tile is 128 features by up to `cap` rows.  Persistent kernel, one CTA per SM, 512 threads:
-//   warp 0        loads the weights of a ring stage (one box of 128 features x 128 bytes of K,
-//                 128-byte swizzle) when it is free
+// A tile is 128 features by up to `cap` rows; with more than a few rows per expert two CTAs on
+// neighbouring SMs work as a pair (cta_group::2: one MMA of 256 features on both, each CTA
+// staging half of the rows).  Persistent kernel, one CTA per SM, 16 warps (17 in MXFP4):
+//   warp 0        the weights of a ring stage (boxes of 128 features x 128 bytes of K, 128-byte
+//                 swizzle) when it is free
 //   warp 1        TMEM owner and MMA issuer (one elected thread): 32 bytes of K per MMA
-//   warps 2, 3    MXFP4: warp 2 stages the scale bytes of weights and rows, warp 3 writes them
-//                 into the ring in the layout that tcgen05.cp spreads over TMEM (row r of a
-//                 block of 128: 4 bytes at 16 (r % 32) + 4 (r / 32), 512 bytes per 128 values
-//                 of K); warp 3 also reports gathered rows to the tensor core
+//   warp 2        MXFP4: scale bytes of weights and rows, into a staging place
+//   warps 3, 16   MXFP4: write them into the ring in the layout that tcgen05.cp spreads over
+//                 TMEM (row r of a block of 128: 4 bytes at 16 (r % 32) + 4 (r / 32), 512 bytes
+//                 per 128 values of K); report them, and gathered rows, to the tensor core
 //   warps 4..11   epilogue: TMEM lanes are features, columns rows; bias and activation in
 //                 fp32, one rounding, 8 x 8 transpositions through shared memory and 16-byte
 //                 stores, 64 consecutive bytes per row and warp (32 with SwiGLU, whose gate and
 //                 up features are neighbouring lanes)
 //   warps 12..15  the rows of a stage: consecutive rows in TMA boxes, rows gathered by their
-//                 indices with 16-byte asynchronous copies
+//                 indices with 16-byte asynchronous copies (TMA gathers of four rows cost their
+//                 warp about 90 cycles each: 32768 tokens took 5.3 ms that way, 2.6 this way)
+// What a warp does per stage it does with uniform control flow and one elected lane, so that
+// descriptors and addresses stay in uniform registers (MMAs from a divergent branch: 125 cycles
+// each to issue, twice what they take).
 // Two TMEM accumulators alternate, so the epilogue of a tile overlaps the next tile's MMAs.
 //
 // Tiles are numbered by expert, then feature tile, then row tile: the row tiles of one weight
-// tile run at the same time and share it through L2, so weights come from memory once.  An
+// tile run at the same time and share it through L2, so weights come from memory once; experts
+// of more than 8 row tiles go in bands of 8, whose rows stay in L2 over all features.  An
 // expert's rows are split evenly among its row tiles.  Each CTA derives the numbering from
 // the offsets in device memory (a prefix sum over at most 256 experts).
+//
+// What bounds it, and what it measured (one GB300; 2880 -> 5760 with SwiGLU and gathered rows,
+// 128 experts, top 4, unless stated):
+//   few rows    the weights' way from memory.  61 tokens 0.51 ms in bf16 (7.0 TB/s), 0.15 ms in
+//               MXFP4 (6.4 TB/s); 1 token 25.6 us and 16 us, of which about 6 are launch, first
+//               loads and the last tile's end.
+//   many rows   bf16: the tensor cores; 32768 tokens 2.6 - 2.8 ms (1560 - 1700 TFLOP/s), one
+//               group of 32768 rows x 4096 -> 2880 0.42 ms (1830).  MXFP4: per ring stage the
+//               scales' way through staging, and the rows' copies; 1.09 ms (4.0 PFLOP/s), one
+//               group 0.14 ms (5.4).
 #include <atomic>
 #include <cstdint>
 
@@ -44,22 +61,17 @@ constexpr int kEpiWarp0 = 4;
 constexpr int kEpiWarps = 8;
 constexpr int kRowWarp0 = kEpiWarp0 + kEpiWarps;
 constexpr int kRowWarps = 4;
-constexpr int kScaleWarp = kRowWarp0 + kRowWarps;  // MXFP4 in a pair: beside warp 3
+constexpr int kScaleWarp = kRowWarp0 + kRowWarps;  // MXFP4: takes turns with warp 3
 constexpr int kMaxProducers = 3 + kRowWarps;       // warp 0, the row warps, warp 3 and kScaleWarp
 constexpr int kMaxStages = 16;
 constexpr int kRingBytes = 198 * 1024;
 constexpr int kMaxSingleRows = 64;  // rows of a single CTA's tile
 constexpr int kMaxRawPairs = 6;
-constexpr int kBand = 8;        // row tiles of an expert that pass over its features together
-constexpr int kSfBlock = 512;   // scales of 128 rows x 128 values of K
-constexpr int kPatchBytes = 512;       // of an epilogue warp
+constexpr int kBand = 8;             // row tiles of an expert that pass over its features together
+constexpr int kSfBlock = 512;        // scales of 128 rows x 128 values of K
 constexpr int kRawBlock = 128 * 16;  // scale bytes on their way: 16 per row of a block of 128
+constexpr int kPatchBytes = 512;     // of an epilogue warp
 constexpr unsigned long long kDrainTimeoutNs = 2000000000ull;
-
-template <bool kFp4, bool kPair>
-__host__ __device__ constexpr int grp_threads() {
-  return 32 * (kScaleWarp + (kFp4 && kPair ? 1 : 0));
-}
 
 template <bool kFp4>
 struct GrpCfg {
@@ -71,7 +83,8 @@ struct GrpCfg {
   static constexpr int kRawBytes = kFp4 ? 9 * kRawBlock : 0;
   static constexpr int kSfCols = 24;
   static constexpr int kTmemCols = 512;
-    static_assert(2 * kRows + (kFp4 ? 2 * kSfCols : 0) <= kTmemCols, "TMEM holds 512 columns");
+  static constexpr int kThreads = 32 * (kScaleWarp + (kFp4 ? 1 : 0));
+  static_assert(2 * kRows + (kFp4 ? 2 * kSfCols : 0) <= kTmemCols, "TMEM holds 512 columns");
 };
 
 // A stage holds `sub` blocks of kStageKBytes of K: `width` features and `rows` rows of 128 bytes
@@ -381,7 +394,7 @@ __device__ __forceinline__ float swiglu(float g, float u, float alpha, float lim
 }
 
 template <bool kFp4, bool kSwiglu, bool kPair>
-__global__ void __launch_bounds__(grp_threads<kFp4, kPair>(), 1)
+__global__ void __launch_bounds__(GrpCfg<kFp4>::kThreads, 1)
 grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                const __grid_constant__ CUtensorMap wsmap, const __grid_constant__ CUtensorMap xsmap,
                const GroupedArgs a) {
@@ -409,8 +422,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
   const int rank = kPair ? static_cast<int>(cluster_ctarank()) : 0;
   // warps of a CTA that report a stage filled: gathered rows are reported by warp 3
   const bool gather = a.row_token != nullptr;
-  constexpr int kScaleWarps = kFp4 ? kCtas : 0;
-  const int producers = 1 + (gather ? 0 : kRowWarps) + (kFp4 ? kScaleWarps : gather ? 1 : 0);
+  const int producers = 1 + (gather ? 0 : kRowWarps) + (kFp4 ? 2 : gather ? 1 : 0);
   const int t_first = blockIdx.x / kCtas, t_step = gridDim.x / kCtas;
   // the leading CTA's barriers
   const uint32_t full0 = kPair ? dsmem_addr(smem_u32(&sb.full[0]), 0) : smem_u32(&sb.full[0]);
@@ -430,7 +442,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
     }
     for (int r = 0; kFp4 && r < kMaxRawPairs; ++r) {
       mbar_init(smem_u32(&sb.raw_full[r]), kPair ? (gather ? 33 : 1) : 32);
-      mbar_init(smem_u32(&sb.raw_empty[r]), kScaleWarps);
+      mbar_init(smem_u32(&sb.raw_empty[r]), 2);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&sb.acc_full[b]), 1);
@@ -598,8 +610,8 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
       // Scale bytes on their way, some pairs of blocks of K ahead: 16 bytes of a row serve a pair.
       // In a pair of CTAs they come in boxes of 16 bytes x rows, but for gathered rows: copies by
       // threads, 16 bytes from each of 32 rows, keep the load unit as busy as whole lines would,
-      // and there is enough of them to tell.  Small tiles take copies throughout (boxes: 61 tokens
-      // up 166 us instead of 158).
+      // and there are enough of them to tell.  Small tiles take copies throughout (8 tokens down,
+      // 2880 x 2880: 28 us, with boxes 31).
       const int pairs = (k_blocks + 1) / 2;
       const uint32_t raw = smem_u32(tiles + kRingBytes);
       constexpr int kRowQuarters = (kPair ? GrpCfg<true>::kRows : kMaxSingleRows) / 32;
@@ -670,13 +682,13 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
         sb.raw_issued = p.round * kRawPairs + p.stage;
       }
     }
-  } else if ((warp == 3 && (kFp4 || gather)) || (kFp4 && kPair && warp == kScaleWarp)) {
+  } else if ((warp == 3 && (kFp4 || gather)) || (kFp4 && warp == kScaleWarp)) {
     // What threads have brought becomes the tensor core's: scales are put in their layout,
     // gathered rows have landed; then one proxy fence, by a warp that has no copies under way
-    // (with them, a fence takes as long as they do), and the stage is reported.  In a pair of
-    // CTAs two warps take turns of one block of K (warp 3 the even ones) and both report every
-    // stage; alone, one warp is faster (61 tokens up: 158 us, with two 164).
-    const int turn = kFp4 && kPair ? (warp == kScaleWarp ? 1 : 0) : -1;  // -1: all blocks
+    // (with them, a fence takes as long as they do), and the stage is reported.  In MXFP4 two
+    // warps take turns of one block of K (warp 3 the even ones) and both report every stage (256
+    // tokens up: 180 us, with one warp 194).
+    [[maybe_unused]] const int turn = warp == kScaleWarp ? 1 : 0;
     RingPos p, pr;
     int g = 0;
     bool ok = true;
@@ -701,20 +713,16 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
           // All that can be there is read, without a branch: what rows behind the tile's last
           // one (or features behind its width) have there scales columns (lanes) that are never stored.
           constexpr int kQuarters = 4 + (kPair ? GrpCfg<true>::kRows : kMaxSingleRows) / 32;
-          uint2 c[kPair ? 1 : 2][12];
+          uint2 c[12];
 #pragma unroll
-          for (int h = 0; h < (kPair ? 1 : 2); ++h) {
-            const int half = kPair ? turn : h;
+          for (int i = 0; i < 12; ++i)
+            c[i] = i < kQuarters ? *reinterpret_cast<const uint2*>(raw + 512 * i + 8 * turn) : make_uint2(0, 0);
+          const int valid = used - 8 * (block + turn);  // bytes, the rest is padding
+          if (valid < 8) {
+            const uint32_t mask0 = valid >= 4 ? 0xFFFFFFFFu : valid <= 0 ? 0u : (1u << (8 * valid)) - 1u;
+            const uint32_t mask1 = valid <= 4 ? 0u : (1u << (8 * valid - 32)) - 1u;
 #pragma unroll
-            for (int i = 0; i < 12; ++i)
-              c[h][i] = i < kQuarters ? *reinterpret_cast<const uint2*>(raw + 512 * i + 8 * half) : make_uint2(0, 0);
-            const int valid = used - 8 * (block + half);  // bytes, the rest is padding
-            if (valid < 8) {
-              const uint32_t mask0 = valid >= 4 ? 0xFFFFFFFFu : valid <= 0 ? 0u : (1u << (8 * valid)) - 1u;
-              const uint32_t mask1 = valid <= 4 ? 0u : (1u << (8 * valid - 32)) - 1u;
-#pragma unroll
-              for (int i = 0; i < kQuarters; ++i) c[h][i] = make_uint2(c[h][i].x & mask0, c[h][i].y & mask1);
-            }
+            for (int i = 0; i < kQuarters; ++i) c[i] = make_uint2(c[i].x & mask0, c[i].y & mask1);
           }
           __syncwarp();
           if (elect_one()) mbar_arrive(smem_u32(&sb.raw_empty[pr.stage]));
@@ -722,7 +730,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
           for (int h = 0; h < 2; ++h) {
             if (block + h >= k_blocks) break;
             const int u = sub == 2 ? h : 0;
-            const bool mine = !kPair || h == turn;
+            const bool mine = h == turn;
             if (u == 0 && p.round != 0)
               ok = wait_or_abort(smem_u32(&sb.empty[p.stage]), (p.round - 1) & 1, a.timeout_ns, abort_flag);
             if (!ok) break;
@@ -731,14 +739,15 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
 #pragma unroll
               for (int blk = 0; blk < 3; ++blk) {
                 if (blk == 2 && quarters <= 4) break;
-                const uint2* v = c[kPair ? 0 : h] + 4 * blk;
+                const uint2* v = c + 4 * blk;
                 sf[blk * (kSfBlock / 16)] = make_uint4(v[0].x, v[1].x, v[2].x, v[3].x);
                 sf[(3 + blk) * (kSfBlock / 16)] = make_uint4(v[0].y, v[1].y, v[2].y, v[3].y);
               }
             }
             if (u + 1 == sub || block + h + 1 == k_blocks) {
-              if (mine) {
-                if (gather) ok = wait_or_abort(smem_u32(&sb.landed[p.stage]), p.round & 1, a.timeout_ns, abort_flag);
+              // of a stage of two blocks both warps have written; the rows are the last one's
+              if (mine || sub == 2) {
+                if (gather && mine) ok = wait_or_abort(smem_u32(&sb.landed[p.stage]), p.round & 1, a.timeout_ns, abort_flag);
                 if (!ok) break;
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -753,7 +762,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
     }
     if (lane == 0) {
       if (!ok) raise_status(a.status, kStatusTimeout);
-      sb.issued[1 + kRowWarps + (turn > 0)] = g;
+      sb.issued[1 + kRowWarps + (kFp4 && warp == kScaleWarp)] = g;
     }
   } else if (warp >= kRowWarp0) {
     const int wr = warp - kRowWarp0;
@@ -980,7 +989,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
       return x;
     };
     auto reports = [&](int w) {
-      return w == 0 || (w <= kRowWarps ? !gather : w == 1 + kRowWarps ? kFp4 || gather : kScaleWarps == 2);
+      return w == 0 || (w <= kRowWarps ? !gather : w == 1 + kRowWarps ? kFp4 || gather : kFp4);
     };
     int aborted = 0, most = 0;
     for (int c = 0; c < kCtas; ++c) {
@@ -1045,7 +1054,7 @@ cudaError_t launch_grouped_t(const GroupedMaps& m, const GroupedArgs& a, int sms
   const int slots = sms / kCtas;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((most < slots ? most : slots) * kCtas));
-  cfg.blockDim = dim3(grp_threads<kFp4, kPair>());
+  cfg.blockDim = dim3(GrpCfg<kFp4>::kThreads);
   cfg.dynamicSmemBytes = smem_bytes<kFp4>();
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1071,10 +1080,12 @@ cudaError_t launch_grouped_f(const GroupedMaps& m, const GroupedArgs& a, int sms
 }  // namespace
 
 void grouped_plan(GroupedArgs& a, bool mxfp4, int sms) {
-  // More than 32 rows per expert on average: CTA pairs, which stage a tile's rows once for 256
+  // More than 48 rows per expert on average: CTA pairs, which stage a tile's rows once for 256
   // features.  Fewer: single CTAs and small tiles, so that the ring's stages are small and many
-  // and keep more weight bytes in flight.
-  a.pair = a.rows > 32LL * a.num_experts;
+  // and keep more weight bytes in flight.  (32 equal experts, 2880 -> 5760, us single / pair:
+  // 40 rows bf16 162 / 167, MXFP4 55 / 54; 96 rows, two row tiles of single CTAs, 197 / 172 and
+  // 89 / 57.  Groups of uneven size pass 64 rows, a single CTA's most, before their average does.)
+  a.pair = a.rows > 48LL * a.num_experts;
   a.cap = a.pair ? (mxfp4 ? GrpCfg<true>::kRows : GrpCfg<false>::kRows) : a.rows > 2LL * a.num_experts ? kMaxSingleRows : 16;
   a.width = kFeat;
   a.sub = 1;

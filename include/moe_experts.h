@@ -71,7 +71,7 @@ sa_status moe_group_rows(const int32_t* topk_idx, int num_tokens, int top_k, int
  *  out            bf16 [rows, n]; must not overlap the inputs
  *  k a multiple of 8, x and w 16-byte aligned, 1 <= num_experts <= 256, any
  *  n >= 1, rows >= 0 (0 launches nothing), rows, n and k <= 2^30,
- *  (rows / 16 + num_experts) * (n / 64 + 1) < 2^30.
+ *  num_experts * n <= 2^31 - 1024, (rows / 16 + num_experts) * (n / 64 + 1) < 2^30.
  *  A device wait that runs out of time (sink_attn_set_wait_timeout_ns) ends
  *  the kernel cleanly and sets SA_ERR_TIMEOUT in the device status word.
  */
