@@ -5,10 +5,10 @@ import numpy as np
 import pytest
 import torch
 
-from experts_common import (acc_bound, bf16_normal, check, linear_bound, mxfp4_normal, sizes_to_offsets,
+from experts_common import (bf16_normal, check, linear_bound, mxfp4_normal, sizes_to_offsets,
                             swiglu_bound)
 from gpu_common import dev, host, require_gpu
-from oracle import experts, moe
+from oracle import experts
 
 pytestmark = pytest.mark.gpu
 
@@ -83,6 +83,8 @@ CASES = [  # experts' row counts, features, inputs (bf16, MXFP4)
     ([1, 0, 0, 2, 1, 0, 0, 0], 2880, (2880, 2880)),
     ([700, 5, 1300], 642, (1048, 1056)),
     (list(np.random.default_rng(3).integers(0, 4, 256)), 128, (64, 64)),
+    ([2300, 3, 4700], 300, (72, 96)),           # more than eight row tiles: several bands of them
+    ([49, 51, 33, 64, 65, 40], 1000, (136, 320)),   # about 48 rows per expert: single CTAs, 1 and 2 row tiles
 ]
 
 
@@ -292,6 +294,88 @@ def test_output_at_an_odd_address_and_no_rows():
     assert sa.grouped_linear_swiglu(operands[0], operands[1], dev(np.zeros(3, np.int32)), row_token=token).shape == (0, 48)
 
 
+def test_beyond_32_bit_offsets():
+    """Outputs, weights and gathered sums whose element offsets pass 2^31: the last rows and the
+    last experts, against fp64."""
+    sa = require_gpu()
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rows, n, k = 800_000, 2816, 64                        # out: 2.25e9 elements
+    x = torch.randn(rows, k, generator=g, device="cuda", dtype=torch.bfloat16)
+    w = torch.randn(2, n, k, generator=g, device="cuda", dtype=torch.bfloat16) / 8
+    off = torch.tensor([0, 300_000, rows], dtype=torch.int32, device="cuda")
+    last = slice(rows - 300, rows)
+    y = x[last].double().cpu().numpy() @ w[1].double().cpu().numpy().T
+    mag = x[last].abs().double().cpu().numpy() @ w[1].abs().double().cpu().numpy().T
+    out = sa.grouped_linear_bias(x, w, off)
+    check(host(out[last]), y, linear_bound(y, mag, k), "last rows")
+    pair_row = torch.tensor([[rows - 1, 5], [rows - 2, rows - 3]], dtype=torch.int32, device="cuda")
+    one = torch.ones((2, 2), dtype=torch.bfloat16, device="cuda")
+    sums = out[pair_row.long()].double().sum(1)
+    # two exact products, one fp32 sum, one rounding to bf16
+    assert ((sa.moe_combine(out, pair_row, one).double() - sums).abs() <= (2.0 ** -8 + 2.0 ** -22) * out[
+        pair_row.long()].double().abs().sum(1)).all()
+    codes, scales = sa.mxfp4_quantize(out)
+    tail = [v[last].cpu().numpy() for v in (codes, scales)]
+    ref = experts.mxfp4_quantize(host(out[last]))
+    assert np.array_equal(tail[0], ref[0]) and np.array_equal(tail[1], ref[1])
+    value = experts.mxfp4_dequantize(*ref)
+    assert np.array_equal(host(sa.mxfp4_dequantize(codes, scales)[last]), value)
+    del out, codes, scales
+    e, n, k = 256, 4096, 2112                             # w: 2.2e9 elements
+    w = torch.empty(e, n, k, device="cuda", dtype=torch.bfloat16).normal_(std=k ** -0.5, generator=g)
+    x = torch.randn(5, k, generator=g, device="cuda", dtype=torch.bfloat16)
+    sizes = np.zeros(e, dtype=int)
+    sizes[[7, 254, 255]] = 1, 2, 2
+    off = sizes_to_offsets(sizes)
+    xv = x.double().cpu().numpy()
+    for mx in (False, True):
+        operands = (*sa.mxfp4_quantize(x), *sa.mxfp4_quantize(w)) if mx else (x, w)
+        out = _call(sa, mx, False, operands, dev(off))
+        for i in (7, 254, 255):
+            at = slice(int(off[i]), int(off[i + 1]))
+            xi, wi = xv[at], w[i].double().cpu().numpy()
+            if mx:
+                xi, wi = (experts.mxfp4_dequantize(*experts.mxfp4_quantize(v)) for v in (xi, wi))
+            y, mag = xi @ wi.T, np.abs(xi) @ np.abs(wi).T
+            check(host(out[at]), y, linear_bound(y, mag, k), f"expert {i} mxfp4={mx}")
+    assert sa.sink_attn_device_status(True) == SA_OK
+
+
+def test_shapes_and_layouts_are_checked():
+    sa = require_gpu()
+    bf, i32, u8 = torch.bfloat16, torch.int32, torch.uint8
+    new = lambda *shape, dt=bf: torch.zeros(*shape, dtype=dt, device="cuda")  # noqa: E731
+    x, w, off = new(6, 64), new(3, 32, 64), new(4, dt=i32)
+    xc, xs, wc, ws = new(6, 32, dt=u8), new(6, 16, dt=u8), new(3, 32, 32, dt=u8), new(3, 32, 16, dt=u8)
+    wrong = [
+        lambda: sa.grouped_linear_bias(x[:, :56].contiguous(), w, off), lambda: sa.grouped_linear_bias(x[:, :56], w, off),
+        lambda: sa.grouped_linear_bias(x, w, off[:3]), lambda: sa.grouped_linear_bias(x, w, off, new(3, 31)),
+        lambda: sa.grouped_linear_bias(x, w, off, row_token=new(2, 3, dt=i32)),
+        lambda: sa.grouped_linear_bias(x, w, off, out=new(6, 33)), lambda: sa.grouped_linear_swiglu(x, w, off, out=new(6, 32)),
+        lambda: sa.grouped_linear_bias(x.t(), w, off), lambda: sa.grouped_linear_bias(x.view(-1), w, off),
+        lambda: sa.grouped_mxfp4_linear_bias(xc, xs[:, :2].contiguous(), wc, ws, off),
+        lambda: sa.grouped_mxfp4_linear_bias(xc, xs, wc, ws[:2], off), lambda: sa.mxfp4_linear_bias(xc, xs, wc[0], ws[1, :30]),
+        lambda: sa.mxfp4_linear_bias(xc, xs, wc[0], ws[0], new(31)), lambda: sa.mxfp4_dequantize(xc, xs[:5]),
+        lambda: sa.moe_combine(x, new(2, 3, dt=i32), new(2, 2)), lambda: sa.moe_combine(x, new(2, 3, dt=i32), new(2, 3), out=new(2, 63)),
+        lambda: sa.moe_group_rows(new(5, dt=i32), 4), lambda: sa.moe_group_rows(new(5, 2, dt=i32), 4, expert_offsets=new(4, dt=i32)),
+        lambda: sa.mxfp4_quantize(x, codes=new(6, 31, dt=u8)),
+    ]
+    for i, call in enumerate(wrong):
+        with pytest.raises(ValueError):
+            call()
+            print("accepted:", i)
+    for call in (lambda: sa.grouped_linear_bias(x.float(), w, off), lambda: sa.moe_group_rows(new(5, 2, dt=torch.int64), 4),
+                 lambda: sa.grouped_linear_bias(x, w, off, new(3, 32, dt=torch.float32))):
+        with pytest.raises(TypeError):
+            call()
+    for call in (lambda: sa.moe_group_rows(new(5, 9, dt=i32), 4), lambda: sa.mxfp4_quantize(new(4, 40)),
+                 lambda: sa.moe_combine(new(6, 60), new(2, 3, dt=i32), new(2, 3)),
+                 lambda: sa.grouped_linear_swiglu(x, new(3, 31, 64), off), lambda: sa.grouped_linear_swiglu(x, w, off, limit=0.0)):
+        with pytest.raises(sa.SinkAttnError):
+            call()
+    assert sa.sink_attn_device_status(True) == SA_OK
+
+
 # ----------------------------------------------------------------------------- combine
 @pytest.mark.parametrize("t,k,h", [(1, 1, 8), (1, 4, 2880), (7, 8, 24), (64, 4, 2880), (333, 3, 1000), (3001, 2, 512),
                                    (50, 5, 72), (51, 6, 80), (52, 7, 88)])
@@ -360,8 +444,7 @@ def _layer_inputs(sa, seed, t, hidden, inner, e, k):
 @pytest.mark.parametrize("mx", [False, True], ids=["bf16", "mxfp4"])
 @pytest.mark.parametrize("t", [1, 37, 600])
 def test_layer_from_router_to_combine(t, mx):
-    """Each step against fp64 on the step's own inputs (so the bounds are those of one step),
-    the indices against the router's oracle order."""
+    """Each step against fp64 on the step's own inputs, so the bounds are those of one step."""
     sa = require_gpu()
     sa.sink_attn_device_status(True)
     hidden, inner, e, k = 512, 384, 16, 4
