@@ -216,7 +216,8 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a) {
 template <int K>
 cudaError_t launch_combine_k(const CombineArgs& a, int sms, cudaStream_t stream) {
   const long long total = static_cast<long long>(a.num_tokens) * (a.hidden / 8);
-  const long long blocks = (total + 255) / 256, most = 8LL * sms;
+  // one wave of resident blocks: 5 per SM with the registers of up to five rows, else 4
+  const long long blocks = (total + 255) / 256, most = (K <= 5 ? 5LL : 4LL) * sms;
   combine_kernel<K><<<static_cast<int>(blocks < most ? blocks : most), 256, 0, stream>>>(a);
   return cudaGetLastError();
 }

@@ -93,16 +93,30 @@ __global__ void __launch_bounds__(kThreads, kQuantBlocks) mxfp4_quantize_kernel(
           }
         }
       }
-      uint32_t mx = 0;
+      uint32_t mx = 0;  // bits of the largest magnitude
+      if constexpr (kFp32) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) mx = max(mx, __float_as_uint(v[j >> 3][j & 7]) & 0x7FFFFFFFu);
+        for (int j = 0; j < 16; ++j) mx = max(mx, __float_as_uint(v[j >> 3][j & 7]) & 0x7FFFFFFFu);
+      } else {  // two bf16 values at a time: their order is that of their bits
+#pragma unroll
+        for (int l = 0; l < kLoads; ++l) {
+          const uint32_t w[4] = {p[u][l].x, p[u][l].y, p[u][l].z, p[u][l].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mx = __vmaxu2(mx, w[j] & 0x7FFF7FFFu);
+        }
+        mx = max(mx << 16, mx & 0xFFFF0000u);
+      }
       mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       const uint32_t field = mx >> 23;
       const bool finite = field < 255u;
       const uint32_t byte = finite ? (field > 2u ? field - 2u : 0u) : 255u;
       const float inv = __uint_as_float((254u - (finite ? byte : 0u)) << 23);  // 2^(127 - byte)
 #pragma unroll
-      for (int j = 0; j < 16; ++j) v[j >> 3][j & 7] = finite ? v[j >> 3][j & 7] * inv : 0.0f;
+      for (int j = 0; j < 16; ++j) v[j >> 3][j & 7] *= inv;
+      if (!finite) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j >> 3][j & 7] = 0.0f;
+      }
       if (i < total) {
         reinterpret_cast<uint2*>(a.codes)[i] = make_uint2(pack_e2m1x8(v[0]), pack_e2m1x8(v[1]));
         if ((threadIdx.x & 1) == 0) {
