@@ -494,30 +494,22 @@ def moe_router(x, w_router, bias, top_k: int, topk_idx=None, topk_weight=None, e
 GPT_OSS_SWIGLU = dict(alpha=1.702, limit=7.0)
 
 
-def _inputs(required, optional=()):
-    """Validate (name, tensor, dtype, shape) tuples: CUDA, dtype, contiguous, shape (None: any
-    size), all on the first tensor's device.  Returns that device's index."""
-    di = None
-    for group in (required, optional):
-        for name, t, dt, dims in group:
-            if t is None and group is optional:
-                continue
-            if not isinstance(t, torch.Tensor) or t.dtype is not dt or not t.is_cuda or not t.is_contiguous():
-                _dev(t, name, dt)  # raises
-            d = t.get_device()
-            if di is None:
-                di = d
-            elif d != di:
+def _inputs(*named):
+    """Validate (name, tensor, dtype, shape) tuples: CUDA, dtype, contiguous, shape (an int: any
+    shape of that many dimensions), all on the first tensor's device.  Returns that device's
+    index.  Optional tensors are left out by the caller when they are None."""
+    di = -1
+    for name, t, dt, shape in named:
+        if not isinstance(t, torch.Tensor) or t.dtype is not dt or not t.is_cuda or not t.is_contiguous():
+            _dev(t, name, dt)  # raises
+        d = t.get_device()
+        if d != di:
+            if di >= 0:
                 _same_device(di, (name, t))  # raises
-            shape = t.shape
-            if len(shape) == len(dims):
-                for have, want in zip(shape, dims):
-                    if want is not None and have != want:
-                        break
-                else:
-                    continue
-            want = ", ".join("*" if v is None else str(v) for v in dims)
-            raise ValueError(f"{name} must be [{want}], got {tuple(shape)}")
+            di = d
+        if t.shape != shape and t.dim() != shape:
+            want = f"of {shape} dimensions" if isinstance(shape, int) else list(shape)
+            raise ValueError(f"{name} must be {want}, got {tuple(t.shape)}")
     return di
 
 
@@ -538,7 +530,7 @@ def moe_group_rows(topk_idx, num_experts: int, expert_offsets=None, row_token=No
     expert e owns rows [expert_offsets[e], expert_offsets[e + 1]), row r reads token
     row_token[r], and pair (t, i) is row pair_row[t, i].  A negative index is a pair without
     expert (pair_row -1); row_token is -1 behind the last row."""
-    di = _inputs((("topk_idx", topk_idx, torch.int32, (None, None)),))
+    di = _inputs(("topk_idx", topk_idx, torch.int32, 2))
     t, k = topk_idx.shape
     e = int(num_experts)
     dev = topk_idx.device
@@ -558,8 +550,8 @@ def moe_combine(y, pair_row, topk_weight, out=None, stream=None):
     """out[t] = sum_i topk_weight[t, i] * y[pair_row[t, i]]: y [R, H] bf16, pair_row [T, k]
     int32 (-1 adds nothing), topk_weight [T, k] bf16.  Returns out [T, H] bf16."""
     t, k = _size(pair_row, "pair_row", 0), _size(pair_row, "pair_row", 1)
-    di = _inputs((("y", y, torch.bfloat16, (None, None)), ("pair_row", pair_row, torch.int32, (t, k)),
-                  ("topk_weight", topk_weight, torch.bfloat16, (t, k))))
+    di = _inputs(("y", y, torch.bfloat16, 2), ("pair_row", pair_row, torch.int32, (t, k)),
+                 ("topk_weight", topk_weight, torch.bfloat16, (t, k)))
     r, h = y.shape
     out = (torch.empty((t, h), dtype=torch.bfloat16, device=y.device) if out is None
            else _out(out, "out", torch.bfloat16, (t, h), di))
@@ -577,10 +569,14 @@ def _product_output(out, rows, n, x, di):
 def _grouped(where, x, w, expert_offsets, bias, row_token, out, stream, act=()):
     """The grouped products on bf16 operands; act: SwiGLU's (alpha, limit) or ()."""
     e, n, k = _size(w, "w", 0), _size(w, "w", 1), _size(w, "w", 2)
-    di = _inputs((("x", x, torch.bfloat16, (None, k)), ("w", w, torch.bfloat16, (e, n, k)),
-                  ("expert_offsets", expert_offsets, torch.int32, (e + 1,))),
-                 (("bias", bias, torch.bfloat16, (e, n)), ("row_token", row_token, torch.int32, (None,))))
-    x_rows = x.shape[0]
+    x_rows = _size(x, "x", 0)
+    named = [("x", x, torch.bfloat16, (x_rows, k)), ("w", w, torch.bfloat16, (e, n, k)),
+             ("expert_offsets", expert_offsets, torch.int32, (e + 1,))]
+    if bias is not None:
+        named.append(("bias", bias, torch.bfloat16, (e, n)))
+    if row_token is not None:
+        named.append(("row_token", row_token, torch.int32, 1))
+    di = _inputs(*named)
     rows = x_rows if row_token is None else row_token.shape[0]
     out = _product_output(out, rows, n // 2 if act else n, x, di)
     st = _call(getattr(load_library(), where), di, stream, x.data_ptr(), w.data_ptr(), _ptr(bias),
@@ -641,8 +637,8 @@ def mxfp4_dequantize(codes, scales, out=None, stream=None):
     returns them)."""
     half = _size(codes, "codes", -1 if isinstance(codes, torch.Tensor) and codes.dim() else 0)
     k, lead = 2 * half, codes.shape[:-1]
-    di = _inputs((("codes", codes, torch.uint8, (*lead, half)),
-                  ("scales", scales, torch.uint8, (*lead, mxfp4_scale_columns(k)))))
+    di = _inputs(("codes", codes, torch.uint8, (*lead, half)),
+                 ("scales", scales, torch.uint8, (*lead, mxfp4_scale_columns(k))))
     out = (torch.empty((*lead, k), dtype=torch.bfloat16, device=codes.device) if out is None
            else _out(out, "out", torch.bfloat16, (*lead, k), di))
     st = _call(load_library().mxfp4_dequantize, di, stream, codes.data_ptr(), scales.data_ptr(), lead.numel(), k,
@@ -656,9 +652,11 @@ def mxfp4_linear_bias(x_codes, x_scales, w_codes, w_scales, bias=None, out=None,
     w [N, K] as codes [., K / 2] and scales, bias [N] bf16 or None.  Returns [M, N] bf16."""
     m, half, n = _size(x_codes, "x_codes", 0), _size(x_codes, "x_codes", 1), _size(w_codes, "w_codes", 0)
     s = mxfp4_scale_columns(2 * half)
-    di = _inputs((("x_codes", x_codes, torch.uint8, (m, half)), ("x_scales", x_scales, torch.uint8, (m, s)),
-                  ("w_codes", w_codes, torch.uint8, (n, half)), ("w_scales", w_scales, torch.uint8, (n, s))),
-                 (("bias", bias, torch.bfloat16, (n,)),))
+    named = [("x_codes", x_codes, torch.uint8, (m, half)), ("x_scales", x_scales, torch.uint8, (m, s)),
+             ("w_codes", w_codes, torch.uint8, (n, half)), ("w_scales", w_scales, torch.uint8, (n, s))]
+    if bias is not None:
+        named.append(("bias", bias, torch.bfloat16, (n,)))
+    di = _inputs(*named)
     out = _product_output(out, m, n, x_codes, di)
     st = _call(load_library().mxfp4_linear_bias, di, stream, x_codes.data_ptr(), x_scales.data_ptr(),
                w_codes.data_ptr(), w_scales.data_ptr(), _ptr(bias), m, n, 2 * half, out.data_ptr())
@@ -670,10 +668,14 @@ def _grouped_mxfp4(where, x_codes, x_scales, w_codes, w_scales, expert_offsets, 
     """The grouped products on MXFP4 operands; act: SwiGLU's (alpha, limit) or ()."""
     e, n, half = (_size(w_codes, "w_codes", i) for i in range(3))
     x_rows, s = _size(x_codes, "x_codes", 0), mxfp4_scale_columns(2 * half)
-    di = _inputs((("x_codes", x_codes, torch.uint8, (x_rows, half)), ("x_scales", x_scales, torch.uint8, (x_rows, s)),
-                  ("w_codes", w_codes, torch.uint8, (e, n, half)), ("w_scales", w_scales, torch.uint8, (e, n, s)),
-                  ("expert_offsets", expert_offsets, torch.int32, (e + 1,))),
-                 (("bias", bias, torch.bfloat16, (e, n)), ("row_token", row_token, torch.int32, (None,))))
+    named = [("x_codes", x_codes, torch.uint8, (x_rows, half)), ("x_scales", x_scales, torch.uint8, (x_rows, s)),
+             ("w_codes", w_codes, torch.uint8, (e, n, half)), ("w_scales", w_scales, torch.uint8, (e, n, s)),
+             ("expert_offsets", expert_offsets, torch.int32, (e + 1,))]
+    if bias is not None:
+        named.append(("bias", bias, torch.bfloat16, (e, n)))
+    if row_token is not None:
+        named.append(("row_token", row_token, torch.int32, 1))
+    di = _inputs(*named)
     rows = x_rows if row_token is None else row_token.shape[0]
     out = _product_output(out, rows, n // 2 if act else n, x_codes, di)
     st = _call(getattr(load_library(), where), di, stream, x_codes.data_ptr(), x_scales.data_ptr(),
