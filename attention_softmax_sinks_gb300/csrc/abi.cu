@@ -358,7 +358,7 @@ sa_status grouped_common(const GroupedCall& c, cudaStream_t stream) {
   if (c.mxfp4 && a.pair) {
     const long long w_rows = static_cast<long long>(c.experts) * c.n;
     if (sa_status s = map_scales(&m.w_scales, c.w_scales, w_rows, a.scale_stride, a.width)) return s;
-    if (sa_status s = map_scales(&m.x_scales, c.x_scales, c.x_rows, a.scale_stride, 32)) return s;
+    if (sa_status s = map_scales(&m.x_scales, c.x_scales, c.x_rows, a.scale_stride, sa::kScaleBoxRows)) return s;
   }
   return sa::launch_grouped(m, a, c.mxfp4, sms, stream) == cudaSuccess ? SA_OK : SA_ERR_LAUNCH;
 }

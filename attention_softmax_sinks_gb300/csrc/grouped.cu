@@ -654,12 +654,15 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
           const uint32_t dst = raw + p.stage * kRawStep;
           if constexpr (kPair) {
             if (elect_one()) {
-              mbar_arrive_expect_tx(bar, 16 * width + (gather ? 0 : 512 * quarters));
+              // few and large boxes: each costs its warp about 90 cycles to issue
+              const int boxes = gather ? 0 : tl.n > kScaleBoxRows ? 2 : 1;
+              mbar_arrive_expect_tx(bar, 16 * (width + boxes * kScaleBoxRows));
               tma_load_rows<false>(dst, &wsmap, 16 * pair, tl.e * a.N + f0, bar);  // E N < 2^31
+              for (int i = 0; i < boxes; ++i)
+                tma_load_rows<false>(dst + kRawBlock + 16 * kScaleBoxRows * i, &xsmap, 16 * pair,
+                                     tl.r0 + kScaleBoxRows * i, bar);
             }
-            if (!gather && lane < quarters)
-              tma_load_rows<false>(dst + kRawBlock + 512 * lane, &xsmap, 16 * pair, tl.r0 + 32 * lane, bar);
-            __syncwarp();
+            __syncwarp();  // together again: the copies below are issued once, not once per branch
           } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -700,6 +703,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
           fence_proxy_async_smem();
           __syncwarp();
           if (elect_one()) grp_arrive<kPair>(full0 + 8 * p.stage);
+          __syncwarp();
         }
       } else {
         const Tile tl = find_tile(sb, a, t, kCtas * width, lane);
@@ -726,6 +730,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
           }
           __syncwarp();
           if (elect_one()) mbar_arrive(smem_u32(&sb.raw_empty[pr.stage]));
+          __syncwarp();
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (block + h >= k_blocks) break;
@@ -753,6 +758,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
                 __syncwarp();
               }
               if (elect_one()) grp_arrive<kPair>(full0 + 8 * p.stage);
+              __syncwarp();
               ++g;
               p.next(stages);
             }
@@ -835,6 +841,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
           const uint32_t bar = full0 + 8 * p.stage;
           if (elect_one())
             grp_arrive_expect_tx<kPair>(bar, (boxes - wr + kRowWarps - 1) / kRowWarps * kBoxRows * kStageKBytes);
+          __syncwarp();
           if (box < boxes)
             tma_load_rows<kPair>(dst + p.stage * stage_size, &xmap,
                                  (kb * sub + u) * (kFp4 ? kStageKBytes : kStageKBytes / 2), row, bar);

@@ -9,6 +9,7 @@ namespace sa {
 
 constexpr int kMaxExperts = 256;
 constexpr int kBoxRows = 16;  // rows of one TMA box of x
+constexpr int kScaleBoxRows = 112;  // rows of one TMA box of x's scales: half of a pair's tile
 constexpr int kGroupedFeatures = 128;  // features of one tile (the tcgen05.mma M)
 
 struct GroupedArgs {
@@ -43,7 +44,7 @@ struct GroupedArgs {
 void grouped_plan(GroupedArgs& a, bool mxfp4, int sms);
 // w: {K, N, E} in boxes of 128 bytes x width x 1;  x: [x_rows, K] in boxes of 128 bytes x
 // kBoxRows;  MXFP4 scales, with pairs only: [E N, scale_stride] in boxes of 16 bytes x width and
-// [x_rows, scale_stride] in boxes of 16 bytes x 32.
+// [x_rows, scale_stride] in boxes of 16 bytes x kScaleBoxRows.
 struct GroupedMaps {
   CUtensorMap w, x, w_scales, x_scales;
 };
