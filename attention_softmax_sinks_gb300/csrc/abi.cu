@@ -162,6 +162,8 @@ sa_status map_pages(CUtensorMap* m, const void* base, int num_pages, int hkv) {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
 
 bool good_scale(float s) { return std::isfinite(s) && s > 0.0f; }
 
@@ -323,7 +325,7 @@ sa_status grouped_common(const GroupedCall& c, cudaStream_t stream) {
   if (c.mxfp4 && (!c.x_scales || !c.w_scales)) return SA_ERR_NULL;
   if (c.row_token ? c.x_rows == 0 : c.x_rows != c.rows) return SA_ERR_SHAPE;
   if (!aligned16(c.x) || !aligned16(c.w) || !aligned16(c.x_scales) || !aligned16(c.w_scales) ||
-      (reinterpret_cast<uintptr_t>(c.bias) & 1u) || (reinterpret_cast<uintptr_t>(c.out) & 1u))
+      !aligned2(c.bias) || !aligned2(c.out) || !aligned4(c.offsets) || !aligned4(c.row_token))
     return SA_ERR_ALIGNMENT;
   sa::GroupedArgs a{};
   a.n_out = c.swiglu ? c.n / 2 : c.n;
@@ -805,6 +807,8 @@ sa_status moe_group_rows(const int32_t* topk_idx, int num_tokens, int top_k, int
   if (static_cast<long long>(num_tokens) * top_k > (1LL << 30)) return SA_ERR_SHAPE;
   if (!expert_offsets) return SA_ERR_NULL;
   if (num_tokens > 0 && (!topk_idx || !row_token || !pair_row)) return SA_ERR_NULL;
+  if (!aligned4(topk_idx) || !aligned4(expert_offsets) || !aligned4(row_token) || !aligned4(pair_row))
+    return SA_ERR_ALIGNMENT;
   unsigned* status = nullptr;
   if (sa_status s = status_ptr(&status)) return s;
   sa::GroupRowsArgs a{topk_idx, expert_offsets, row_token, pair_row, num_tokens * top_k, top_k, num_experts, status};
@@ -820,7 +824,7 @@ sa_status moe_combine(const void* y, const int32_t* pair_row, const void* topk_w
   if (hidden % 8 != 0) return SA_ERR_UNSUPPORTED;
   if (num_tokens == 0) return SA_OK;
   if ((!y && num_rows > 0) || !pair_row || !topk_weight || !out) return SA_ERR_NULL;
-  if (!aligned16(y) || !aligned16(out)) return SA_ERR_ALIGNMENT;
+  if (!aligned16(y) || !aligned16(out) || !aligned4(pair_row) || !aligned2(topk_weight)) return SA_ERR_ALIGNMENT;
   unsigned* status = nullptr;
   if (sa_status s = status_ptr(&status)) return s;
   sa::CombineArgs a{static_cast<const uint16_t*>(y), pair_row, static_cast<const uint16_t*>(topk_weight),

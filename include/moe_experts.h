@@ -15,7 +15,9 @@
  *
  * (mxfp4.h has the same products on 4-bit operands.)  The conventions of
  * sink_attn.h apply: device pointers owned by the caller, asynchronous on
- * `stream`, no allocation, no synchronisation, CUDA-graph capturable.
+ * `stream`, no allocation, no synchronisation, CUDA-graph capturable.  Arrays
+ * lie at multiples of their element's size, or of 16 bytes where stated
+ * (SA_ERR_ALIGNMENT otherwise); outputs overlap no input.
  */
 #ifndef MOE_EXPERTS_H
 #define MOE_EXPERTS_H
@@ -68,7 +70,7 @@ sa_status moe_group_rows(const int32_t* topk_idx, int num_tokens, int top_k, int
  *                 its own, x_rows == rows).  Read inside the groups only.  An
  *                 entry outside [0, x_rows) sets SA_ERR_BOUNDS; that row's
  *                 result is unspecified, the others are not affected.
- *  out            bf16 [rows, n]; must not overlap the inputs
+ *  out            bf16 [rows, n]
  *  k a multiple of 8, x and w 16-byte aligned, 1 <= num_experts <= 256, any
  *  n >= 1, rows >= 0 (0 launches nothing), rows, n and k <= 2^30,
  *  num_experts * n <= 2^31 - 1024, (rows / 16 + num_experts) * (n / 64 + 1) < 2^30.
@@ -103,7 +105,7 @@ sa_status grouped_linear_swiglu(const void* x, const void* w, const void* bias,
  *
  *  y           bf16 [num_rows, hidden], 16-byte aligned, hidden a multiple of 8
  *  pair_row    int32 [num_tokens, top_k];  topk_weight bf16 [num_tokens, top_k]
- *  out         bf16 [num_tokens, hidden], 16-byte aligned, not overlapping y
+ *  out         bf16 [num_tokens, hidden], 16-byte aligned
  *  1 <= top_k <= 8, num_tokens * hidden < 2^40.
  */
 sa_status moe_combine(const void* y, const int32_t* pair_row, const void* topk_weight,

@@ -139,3 +139,17 @@ def test_scale_columns():
     for k in (32, 480, 512, 544, 2880, 4096, 5760):
         assert sa.mxfp4_scale_columns(k) == experts.scale_columns(k)
     assert [sa.mxfp4_scale_columns(k) for k in (32, 512, 544, 2880)] == [16, 16, 32, 96]
+
+
+def test_index_arrays_at_odd_addresses_are_refused(lib):
+    """int32 arrays need 4-byte addresses and bf16 weights 2-byte ones: the kernels' loads would fault."""
+    two = ctypes.c_void_p(0x10002)
+    good = (FAKE, 5, 4, 8, FAKE, FAKE, FAKE)
+    for at in (0, 4, 5, 6):
+        assert lib.moe_group_rows(*good[:at], two, *good[at + 1:], None) == SA_ERR_ALIGNMENT
+    assert lib.moe_group_rows(None, 0, 4, 8, two, None, None, None) == SA_ERR_ALIGNMENT
+    assert lib.moe_combine(FAKE, two, FAKE, 8, 2, 4, 64, FAKE, None) == SA_ERR_ALIGNMENT
+    assert lib.moe_combine(FAKE, FAKE, ODD, 8, 2, 4, 64, FAKE, None) == SA_ERR_ALIGNMENT
+    for name in GROUPED:
+        assert _grouped(lib, name, off=two) == SA_ERR_ALIGNMENT
+        assert _grouped(lib, name, tok=two) == SA_ERR_ALIGNMENT
