@@ -494,6 +494,25 @@ def moe_router(x, w_router, bias, top_k: int, topk_idx=None, topk_weight=None, e
 GPT_OSS_SWIGLU = dict(alpha=1.702, limit=7.0)
 
 
+_C_INT = 2 ** 31 - 1
+
+
+def _c_int(v, name):
+    """v, which has to survive the passage through a C int."""
+    if not -_C_INT <= v <= _C_INT:
+        raise ValueError(f"{name} is {v}, beyond 32 bits")
+    return v
+
+
+def _new(shape, dtype, dev, stream):
+    """An output, from the memory of the stream that will write it: the current stream's may
+    still be in use there, or be given out there again while the kernel runs."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def _inputs(*named):
     """Validate (name, tensor, dtype, shape) tuples: CUDA, dtype, contiguous, shape (an int: any
     shape of that many dimensions), all on the first tensor's device.  Returns that device's
@@ -507,6 +526,9 @@ def _inputs(*named):
             if di >= 0:
                 _same_device(di, (name, t))  # raises
             di = d
+        if t.numel() > _C_INT:
+            for v in t.shape:
+                _c_int(v, f"a dimension of {name}")
         if t.shape != shape and t.dim() != shape:
             want = f"of {shape} dimensions" if isinstance(shape, int) else list(shape)
             raise ValueError(f"{name} must be {want}, got {tuple(t.shape)}")
@@ -532,13 +554,13 @@ def moe_group_rows(topk_idx, num_experts: int, expert_offsets=None, row_token=No
     expert (pair_row -1); row_token is -1 behind the last row."""
     di = _inputs(("topk_idx", topk_idx, torch.int32, 2))
     t, k = topk_idx.shape
-    e = int(num_experts)
+    e = _c_int(int(num_experts), "num_experts")
     dev = topk_idx.device
-    expert_offsets = (torch.empty(max(e, 0) + 1, dtype=torch.int32, device=dev) if expert_offsets is None
+    expert_offsets = (_new(max(e, 0) + 1, torch.int32, dev, stream) if expert_offsets is None
                       else _out(expert_offsets, "expert_offsets", torch.int32, (e + 1,), di))
-    row_token = (torch.empty(t * k, dtype=torch.int32, device=dev) if row_token is None
+    row_token = (_new(t * k, torch.int32, dev, stream) if row_token is None
                  else _out(row_token, "row_token", torch.int32, (t * k,), di))
-    pair_row = (torch.empty((t, k), dtype=torch.int32, device=dev) if pair_row is None
+    pair_row = (_new((t, k), torch.int32, dev, stream) if pair_row is None
                 else _out(pair_row, "pair_row", torch.int32, (t, k), di))
     st = _call(load_library().moe_group_rows, di, stream, topk_idx.data_ptr(), t, k, e, expert_offsets.data_ptr(),
                row_token.data_ptr(), pair_row.data_ptr())
@@ -553,7 +575,7 @@ def moe_combine(y, pair_row, topk_weight, out=None, stream=None):
     di = _inputs(("y", y, torch.bfloat16, 2), ("pair_row", pair_row, torch.int32, (t, k)),
                  ("topk_weight", topk_weight, torch.bfloat16, (t, k)))
     r, h = y.shape
-    out = (torch.empty((t, h), dtype=torch.bfloat16, device=y.device) if out is None
+    out = (_new((t, h), torch.bfloat16, y.device, stream) if out is None
            else _out(out, "out", torch.bfloat16, (t, h), di))
     st = _call(load_library().moe_combine, di, stream, y.data_ptr(), pair_row.data_ptr(), topk_weight.data_ptr(), r,
                t, k, h, out.data_ptr())
@@ -561,8 +583,8 @@ def moe_combine(y, pair_row, topk_weight, out=None, stream=None):
     return out
 
 
-def _product_output(out, rows, n, x, di):
-    return (torch.empty((rows, n), dtype=torch.bfloat16, device=x.device) if out is None
+def _product_output(out, rows, n, x, di, stream):
+    return (_new((rows, n), torch.bfloat16, x.device, stream) if out is None
             else _out(out, "out", torch.bfloat16, (rows, n), di))
 
 
@@ -578,7 +600,7 @@ def _grouped(where, x, w, expert_offsets, bias, row_token, out, stream, act=()):
         named.append(("row_token", row_token, torch.int32, 1))
     di = _inputs(*named)
     rows = x_rows if row_token is None else row_token.shape[0]
-    out = _product_output(out, rows, n // 2 if act else n, x, di)
+    out = _product_output(out, rows, n // 2 if act else n, x, di, stream)
     st = _call(getattr(load_library(), where), di, stream, x.data_ptr(), w.data_ptr(), _ptr(bias),
                expert_offsets.data_ptr(), _ptr(row_token), x_rows, rows, e, n, k, *act, out.data_ptr())
     _check(st, where)
@@ -620,11 +642,11 @@ def mxfp4_quantize(x, codes=None, scales=None, stream=None):
     _dev(x, "x", torch.float32 if fp32 else torch.bfloat16)
     if x.dim() < 1:
         raise ValueError("x must have at least one dimension")
-    di, dev, lead, k = x.get_device(), x.device, x.shape[:-1], x.shape[-1]
-    codes = (torch.empty((*lead, k // 2), dtype=torch.uint8, device=dev) if codes is None
+    di, dev, lead, k = x.get_device(), x.device, x.shape[:-1], _c_int(x.shape[-1], "K")
+    codes = (_new((*lead, k // 2), torch.uint8, dev, stream) if codes is None
              else _out(codes, "codes", torch.uint8, (*lead, k // 2), di))
     s = mxfp4_scale_columns(k)
-    scales = (torch.empty((*lead, s), dtype=torch.uint8, device=dev) if scales is None
+    scales = (_new((*lead, s), torch.uint8, dev, stream) if scales is None
               else _out(scales, "scales", torch.uint8, (*lead, s), di))
     st = _call(load_library().mxfp4_quantize, di, stream, x.data_ptr(), int(fp32), lead.numel(), k,
                codes.data_ptr(), scales.data_ptr())
@@ -639,7 +661,7 @@ def mxfp4_dequantize(codes, scales, out=None, stream=None):
     k, lead = 2 * half, codes.shape[:-1]
     di = _inputs(("codes", codes, torch.uint8, (*lead, half)),
                  ("scales", scales, torch.uint8, (*lead, mxfp4_scale_columns(k))))
-    out = (torch.empty((*lead, k), dtype=torch.bfloat16, device=codes.device) if out is None
+    out = (_new((*lead, k), torch.bfloat16, codes.device, stream) if out is None
            else _out(out, "out", torch.bfloat16, (*lead, k), di))
     st = _call(load_library().mxfp4_dequantize, di, stream, codes.data_ptr(), scales.data_ptr(), lead.numel(), k,
                out.data_ptr())
@@ -657,7 +679,7 @@ def mxfp4_linear_bias(x_codes, x_scales, w_codes, w_scales, bias=None, out=None,
     if bias is not None:
         named.append(("bias", bias, torch.bfloat16, (n,)))
     di = _inputs(*named)
-    out = _product_output(out, m, n, x_codes, di)
+    out = _product_output(out, m, n, x_codes, di, stream)
     st = _call(load_library().mxfp4_linear_bias, di, stream, x_codes.data_ptr(), x_scales.data_ptr(),
                w_codes.data_ptr(), w_scales.data_ptr(), _ptr(bias), m, n, 2 * half, out.data_ptr())
     _check(st, "mxfp4_linear_bias")
@@ -677,7 +699,7 @@ def _grouped_mxfp4(where, x_codes, x_scales, w_codes, w_scales, expert_offsets, 
         named.append(("row_token", row_token, torch.int32, 1))
     di = _inputs(*named)
     rows = x_rows if row_token is None else row_token.shape[0]
-    out = _product_output(out, rows, n // 2 if act else n, x_codes, di)
+    out = _product_output(out, rows, n // 2 if act else n, x_codes, di, stream)
     st = _call(getattr(load_library(), where), di, stream, x_codes.data_ptr(), x_scales.data_ptr(),
                w_codes.data_ptr(), w_scales.data_ptr(), _ptr(bias), expert_offsets.data_ptr(), _ptr(row_token),
                x_rows, rows, e, n, 2 * half, *act, out.data_ptr())

@@ -277,6 +277,29 @@ def test_zero_wait_budget_unwinds_cleanly(mx):
     assert sa.sink_attn_device_status(True) == SA_OK
 
 
+@pytest.mark.parametrize("mx", [False, True], ids=["bf16", "mxfp4"])
+@pytest.mark.parametrize("sizes", [[3, 0, 1, 2], [100, 40, 60, 31], [20, 11, 0, 7]], ids=["cap16", "pair", "cap64"])
+def test_zero_wait_budget_with_gathered_rows(sizes, mx):
+    """As above where threads bring the rows, for each kind of tile."""
+    sa = require_gpu()
+    sa.sink_attn_device_status(True)
+    rng = np.random.default_rng(16)
+    offsets = sizes_to_offsets(sizes)
+    operands, xv, wv = _operands(rng, mx, 50, 4, 640, 2080)
+    token = rng.integers(0, 50, int(offsets[-1])).astype(np.int32)
+    try:
+        sa.sink_attn_set_wait_timeout_ns(0)
+        for _ in range(3):
+            _call(sa, mx, False, operands, dev(offsets), row_token=dev(token))
+        assert sa.sink_attn_device_status(True) in (SA_OK, SA_ERR_TIMEOUT)
+    finally:
+        sa.sink_attn_set_wait_timeout_ns(2_000_000_000)
+    out = _call(sa, mx, False, operands, dev(offsets), row_token=dev(token))
+    ref, bound = _reference(xv, wv, None, offsets, token, False, 2080)
+    check(host(out), ref, bound, "after a zero wait budget")
+    assert sa.sink_attn_device_status(True) == SA_OK
+
+
 def test_output_at_an_odd_address_and_no_rows():
     """out needs 2-byte alignment only; no rows at all launch nothing."""
     sa = require_gpu()
@@ -376,6 +399,30 @@ def test_shapes_and_layouts_are_checked():
     assert sa.sink_attn_device_status(True) == SA_OK
 
 
+def test_sizes_past_the_c_interface_are_refused():
+    """Sizes that a C int cannot hold raise instead of arriving as what is left of them (2^32 + 64
+    values per row would be 64)."""
+    sa = require_gpu()
+    far = 2 ** 32 + 64
+    x = torch.zeros((2, 64), dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros((2, 32, 64), dtype=torch.bfloat16, device="cuda")
+    off = torch.zeros(3, dtype=torch.int32, device="cuda")
+    idx = torch.zeros((4, 2), dtype=torch.int32, device="cuda")
+    long8 = torch.empty(far, dtype=torch.uint8, device="cuda")
+    long16 = torch.empty(far, dtype=torch.bfloat16, device="cuda")
+    long32 = torch.empty(far, dtype=torch.int32, device="cuda")
+    out = torch.empty(1, dtype=torch.bfloat16, device="cuda")
+    for call in (lambda: sa.moe_group_rows(idx, 2 ** 32 + 8), lambda: sa.moe_group_rows(idx, 2 ** 31),
+                 lambda: sa.grouped_linear_bias(x, w, off, row_token=long32, out=out),
+                 lambda: sa.moe_combine(x, long32.view(-1, 1), long16.view(-1, 1), out=out),
+                 lambda: sa.mxfp4_quantize(long16.view(1, -1)), lambda: sa.mxfp4_dequantize(long8.view(1, -1), long8)):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(sa.SinkAttnError):
+        sa.moe_group_rows(idx, -5)
+    assert sa.sink_attn_device_status(True) == SA_OK
+
+
 # ----------------------------------------------------------------------------- combine
 @pytest.mark.parametrize("t,k,h", [(1, 1, 8), (1, 4, 2880), (7, 8, 24), (64, 4, 2880), (333, 3, 1000), (3001, 2, 512),
                                    (50, 5, 72), (51, 6, 80), (52, 7, 88)])
@@ -411,6 +458,67 @@ def test_combine_rows_out_of_range_are_reported():
     assert sa.sink_attn_device_status(True) == SA_ERR_BOUNDS
     none = sa.moe_combine(y[:0], dev(np.full((3, 2), -1, dtype=np.int32)), w[:1].repeat(3, 1))
     assert (none == 0).all()
+    assert sa.sink_attn_device_status(True) == SA_OK
+
+
+# ----------------------------------------------------------------------------- streams
+def _stream_of(t):
+    """The stream whose memory pool a tensor's storage belongs to."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+    raise AssertionError("not in any segment")
+
+
+def test_outputs_belong_to_the_stream_that_writes_them():
+    """With ``stream=`` an output's memory comes from that stream's pool: memory of the current
+    stream's pool may still be in use by what runs there, and may be given out there again while
+    the kernel writes."""
+    sa = require_gpu()
+    s = torch.cuda.Stream()
+    d = _layer_inputs(sa, 3, 20, 512, 384, 16, 4)
+    codes, scales = sa.mxfp4_quantize(d["x"])
+    idx, weight = sa.moe_router(d["x"], d["wr"], d["br"], 4)
+    offsets, row_token, pair_row = sa.moe_group_rows(idx, 16)
+    y = torch.zeros((80, 512), dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    outs = [*sa.moe_group_rows(idx, 16, stream=s), sa.moe_combine(y, pair_row, weight, stream=s),
+            sa.grouped_linear_swiglu(d["x"], d["up"], offsets, row_token=row_token, stream=s),
+            sa.grouped_mxfp4_linear_swiglu(codes, scales, *d["up4"], offsets, row_token=row_token, stream=s),
+            sa.mxfp4_linear_bias(codes, scales, d["up4"][0][0], d["up4"][1][0], stream=s),
+            *sa.mxfp4_quantize(d["x"], stream=s), sa.mxfp4_dequantize(codes, scales, stream=s)]
+    assert [_stream_of(t) for t in outs] == [s.cuda_stream] * len(outs)
+    with torch.cuda.stream(s):
+        assert _stream_of(sa.mxfp4_dequantize(codes, scales)) == s.cuda_stream
+    torch.cuda.synchronize()
+    assert sa.sink_attn_device_status(True) == SA_OK
+
+
+@pytest.mark.parametrize("mx", [False, True], ids=["bf16", "mxfp4"])
+def test_two_graphs_in_turn_and_at_once(mx):
+    """Two captured layers of different sizes, replayed in turn and on two streams at once: nothing
+    is shared between them."""
+    sa = require_gpu()
+    d = [_layer_inputs(sa, 60 + t, t, 512, 384, 16, 4) for t in (9, 400)]
+    want = [_layer(sa, v, mx)[-1].clone() for v in d]
+    graphs, outs = [], []
+    for v in d:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(_layer(sa, v, mx)[-1])
+        graphs.append(g)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for at_once in (False, True) * 3:
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+            if not at_once:
+                s.synchronize()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
     assert sa.sink_attn_device_status(True) == SA_OK
 
 
