@@ -132,13 +132,13 @@ sa_status map_rows(CUtensorMap* m, const void* base, long long rows, long long r
   return r == CUDA_SUCCESS ? SA_OK : SA_ERR_CUDA;
 }
 
-// MXFP4 scale bytes [rows, stride] read in boxes of 16 bytes x box_rows.
+// MXFP4 scale bytes [rows, stride] read in boxes of 16 kScaleBoxCols bytes x box_rows.
 sa_status map_scales(CUtensorMap* m, const void* base, long long rows, int stride, int box_rows) {
   PFN_cuTensorMapEncodeTiled_v12000 enc;
   if (sa_status s = encoder(&enc)) return s;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(stride), static_cast<cuuint64_t>(rows)};
   cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride)};
-  cuuint32_t box[2] = {16, static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t box[2] = {16 * sa::kScaleBoxCols, static_cast<cuuint32_t>(box_rows)};
   cuuint32_t estr[2] = {1, 1};
   CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
@@ -356,7 +356,7 @@ sa_status grouped_common(const GroupedCall& c, cudaStream_t stream) {
   const long long row_bytes = c.mxfp4 ? c.k / 2 : 2LL * c.k;
   sa::GroupedMaps m{};
   if (sa_status s = map_experts(&m.w, c.w, c.experts, c.n, row_bytes, a.width, c.mxfp4)) return s;
-  if (sa_status s = map_rows(&m.x, c.x, c.x_rows, row_bytes, sa::kBoxRows, c.mxfp4)) return s;
+  if (sa_status s = map_rows(&m.x, c.x, c.x_rows, row_bytes, a.pair ? a.cap / 4 : sa::kBoxRows, c.mxfp4)) return s;
   if (c.mxfp4 && a.pair) {
     const long long w_rows = static_cast<long long>(c.experts) * c.n;
     if (sa_status s = map_scales(&m.w_scales, c.w_scales, w_rows, a.scale_stride, a.width)) return s;

@@ -11,21 +11,21 @@
 //
 // A tile is 128 features by up to `cap` rows; with more than a few rows per expert two CTAs on
 // neighbouring SMs work as a pair (cta_group::2: one MMA of 256 features on both, each CTA
-// staging half of the rows).  Persistent kernel, one CTA per SM, 16 warps (17 in MXFP4):
+// staging half of the rows).  Persistent kernel, one CTA per SM, 17 warps:
 //   warp 0        the weights of a ring stage (boxes of 128 features x 128 bytes of K, 128-byte
 //                 swizzle) when it is free
 //   warp 1        TMEM owner and MMA issuer (one elected thread): 32 bytes of K per MMA
 //   warp 2        MXFP4: scale bytes of weights and rows, into a staging place
-//   warps 3, 16   MXFP4: write them into the ring in the layout that tcgen05.cp spreads over
-//                 TMEM (row r of a block of 128: 4 bytes at 16 (r % 32) + 4 (r / 32), 512 bytes
-//                 per 128 values of K); report them, and gathered rows, to the tensor core
+//   warps 3, 16   in turns of a stage: write them into the ring in the layout that tcgen05.cp
+//                 spreads over TMEM (row r of a block of 128: 4 bytes at 16 (r % 32) + 4 (r / 32),
+//                 512 bytes per 128 values of K); report them, and gathered rows
 //   warps 4..11   epilogue: TMEM lanes are features, columns rows; bias and activation in
 //                 fp32, one rounding, 8 x 8 transpositions through shared memory and 16-byte
 //                 stores, 64 consecutive bytes per row and warp (32 with SwiGLU, whose gate and
 //                 up features are neighbouring lanes)
-//   warps 12..15  the rows of a stage: consecutive rows in TMA boxes, rows gathered by their
-//                 indices with 16-byte asynchronous copies (TMA gathers of four rows cost their
-//                 warp about 90 cycles each: 32768 tokens took 5.3 ms that way, 2.6 this way)
+//   warps 12..15  the rows: consecutive ones in TMA boxes, in turns of a stage; rows gathered by
+//                 their indices with 16-byte asynchronous copies (TMA gathers of four rows cost
+//                 their warp about 90 cycles each: 32768 tokens took 5.3 ms that way, 2.6 this way)
 // What a warp does per stage it does with uniform control flow and one elected lane, so that
 // descriptors and addresses stay in uniform registers (MMAs from a divergent branch: 125 cycles
 // each to issue, twice what they take).
@@ -40,12 +40,14 @@
 // What bounds it, and what it measured (one GB300; 2880 -> 5760 with SwiGLU and gathered rows,
 // 128 experts, top 4, unless stated):
 //   few rows    the weights' way from memory.  61 tokens 0.51 ms in bf16 (7.0 TB/s), 0.15 ms in
-//               MXFP4 (6.4 TB/s); 1 token 25.6 us and 16 us, of which about 6 are launch, first
+//               MXFP4 (6.5 TB/s); 1 token 25.5 us and 15 us, of which about 6 are launch, first
 //               loads and the last tile's end.
-//   many rows   bf16: the tensor cores; 32768 tokens 2.6 - 2.8 ms (1560 - 1700 TFLOP/s), one
-//               group of 32768 rows x 4096 -> 2880 0.42 ms (1830).  MXFP4: per ring stage the
-//               scales' way through staging, and the rows' copies; 1.09 ms (4.0 PFLOP/s), one
-//               group 0.14 ms (5.4).
+//   many rows   bf16: the tensor cores and the power limit; 32768 tokens 2.6 - 2.8 ms, 3.1 back to
+//               back (1400 - 1650 TFLOP/s), one group of 32768 rows x 4096 -> 2880 0.42 ms (1830).
+//               MXFP4: a stage's way round the ring (free, filled, reported, multiplied) beside an
+//               epilogue that competes for issue slots; 1.10 ms (4.0 PFLOP/s), consecutive rows
+//               0.93, one group 0.138 (5.6).  With nothing loaded the 0.93 stay, without the
+//               epilogue as well 0.70, without the MMAs as well 0.47.
 #include <atomic>
 #include <cstdint>
 
@@ -61,15 +63,18 @@ constexpr int kEpiWarp0 = 4;
 constexpr int kEpiWarps = 8;
 constexpr int kRowWarp0 = kEpiWarp0 + kEpiWarps;
 constexpr int kRowWarps = 4;
-constexpr int kScaleWarp = kRowWarp0 + kRowWarps;  // MXFP4: takes turns with warp 3
-constexpr int kMaxProducers = 3 + kRowWarps;       // warp 0, the row warps, warp 3 and kScaleWarp
+// Warps that take turns of one stage: those that bring rows in boxes, and those that report what
+// threads have brought (warp 3 and kReportWarp1).
+constexpr int kTurns = kRowWarps;
+constexpr int kReportTurns = 2;
+constexpr int kReportWarp1 = kRowWarp0 + kRowWarps;
+constexpr int kThreads = 32 * (kReportWarp1 + 1);
+constexpr int kProducers = 1 + kTurns + kReportTurns;  // warps: weights, rows, reports
 constexpr int kMaxStages = 16;
-constexpr int kRingBytes = 198 * 1024;
 constexpr int kMaxSingleRows = 64;  // rows of a single CTA's tile
-constexpr int kMaxRawPairs = 6;
+constexpr int kMaxRawSlots = 6;
 constexpr int kBand = 8;             // row tiles of an expert that pass over its features together
 constexpr int kSfBlock = 512;        // scales of 128 rows x 128 values of K
-constexpr int kRawBlock = 128 * 16;  // scale bytes on their way: 16 per row of a block of 128
 constexpr int kPatchBytes = 512;     // of an epilogue warp
 constexpr unsigned long long kDrainTimeoutNs = 2000000000ull;
 
@@ -79,12 +84,27 @@ struct GrpCfg {
   static constexpr int kRows = kFp4 ? 224 : 256;
   static constexpr int kStageK = kFp4 ? 256 : 64;
   static constexpr int kSfBytes = kFp4 ? 2 * 3 * kSfBlock : 0;  // per 128 values of K: a block of weights, two of rows
-  // staged scale bytes of three pairs of blocks (weights and rows), or of six of a small tile
-  static constexpr int kRawBytes = kFp4 ? 9 * kRawBlock : 0;
   static constexpr int kSfCols = 24;
   static constexpr int kTmemCols = 512;
-  static constexpr int kThreads = 32 * (kScaleWarp + (kFp4 ? 1 : 0));
   static_assert(2 * kRows + (kFp4 ? 2 * kSfCols : 0) <= kTmemCols, "TMEM holds 512 columns");
+};
+
+// Shared memory: the ring, and places for MXFP4 scale bytes on their way.  A row's 16 bytes serve
+// two blocks of K.  With pairs of CTAs a place takes three times 16 bytes of each of 128 features
+// and 224 rows: to the copy engine a piece of 16 bytes is a request like one of 128, and 16 at a
+// time the scales' requests were 176 a stage beside the operands' 240.  (32768 x 4096 -> 2880: 16
+// bytes and six stages 144 us, 48 and five stages 138.  Gathered rows, whose scales threads copy,
+// prefer the sixth stage by 2 %.)
+template <bool kFp4, bool kPair>
+struct GrpSmem {
+  static constexpr int kRawCols = kPair ? kScaleBoxCols : 1;  // of 16 bytes
+  static constexpr int kRawPitch = 16 * kRawCols;
+  static constexpr int kRawSlots = kPair ? 3 : kMaxRawSlots;
+  static constexpr int kRawRows = kPair ? GrpCfg<true>::kRows : kMaxSingleRows;
+  static constexpr int kRawStep = kRawPitch * (kFeat + kRawRows);
+  static constexpr int kRawBytes = kFp4 ? kRawSlots * kRawStep : 0;
+  static constexpr int kRingBytes = (kFp4 && kPair ? 165 : 198) * 1024;
+  static constexpr size_t kTotal = 1024 /*alignment slack*/ + kRingBytes + kRawBytes + kEpiWarps * kPatchBytes;
 };
 
 // A stage holds `sub` blocks of kStageKBytes of K: `width` features and `rows` rows of 128 bytes
@@ -96,30 +116,31 @@ __host__ __device__ constexpr int stage_bytes(int width, int rows, int sub) {
 }
 // An MMA reads 128 features also where the tile has fewer: at the end of the last stage, too,
 // that stays inside the ring (what it reads there goes to accumulator lanes that are never stored).
-template <bool kFp4>
+template <bool kFp4, bool kPair>
 __host__ __device__ constexpr int stage_count(int width, int rows, int sub) {
   const int size = stage_bytes<kFp4>(width, rows, sub);
-  const int n = (kRingBytes - (kFeat - width) * kStageKBytes) / size;
+  const int n = (GrpSmem<kFp4, kPair>::kRingBytes - (kFeat - width) * kStageKBytes) / size;
   return n < kMaxStages ? n : kMaxStages;
 }
 
 struct GrpShared {
   uint64_t full[kMaxStages], empty[kMaxStages], landed[kMaxStages];
-  uint64_t raw_full[kMaxRawPairs], raw_empty[kMaxRawPairs];
+  uint64_t raw_full[kMaxRawSlots], raw_empty[kMaxRawSlots];
   uint64_t acc_full[2], acc_empty[2], drain;
   uint32_t tmem_base;
   int abort_flag;
-  int issued[kMaxProducers];     // stages that each producer warp filled, written when it ends
-  int raw_issued;                // pairs of scales that warp 2 requested, likewise
+  int issued[kProducers];     // stages that each producer warp filled, written when it ends
+  int raw_issued;                // places of scales that warp 2 requested, likewise
   int total;                     // row tiles of all experts
   int cum[kMaxExperts + 32];     // row tiles of lower experts (a huge number from E + 1 on)
   int4 group[kMaxExperts];       // first row, rows, row tiles, rows per tile
 };
-template <bool kFp4>
+template <bool kFp4, bool kPair>
 constexpr size_t smem_bytes() {
-  return 1024 /*alignment slack*/ + kRingBytes + GrpCfg<kFp4>::kRawBytes + kEpiWarps * kPatchBytes + sizeof(GrpShared);
+  return GrpSmem<kFp4, kPair>::kTotal + sizeof(GrpShared);
 }
-static_assert(smem_bytes<true>() <= 227 * 1024, "shared memory of one CTA");
+static_assert(smem_bytes<true, true>() <= 227 * 1024 && smem_bytes<true, false>() <= 227 * 1024 &&
+              smem_bytes<false, true>() <= 227 * 1024, "shared memory of one CTA");
 
 // Position in the ring: stage index and number of rounds made.
 struct RingPos {
@@ -130,6 +151,9 @@ struct RingPos {
       stage = 0;
       ++round;
     }
+  }
+  __device__ __forceinline__ void skip(int n, int stages) {
+    for (stage += n; stage >= stages; stage -= stages) ++round;
   }
 };
 
@@ -387,21 +411,40 @@ __device__ __forceinline__ void store_transposed(uint32_t addr, const uint32_t (
                : "memory");
 }
 
-__device__ __forceinline__ float swiglu(float g, float u, float alpha, float limit) {
-  g = g > limit ? limit : g;  // comparisons that let NaN through
-  u = u > limit ? limit : (u < -limit ? -limit : u);
-  return __fdividef(g, 1.0f + __expf(-alpha * g)) * (u + 1.0f);
+// Minimum and maximum that let NaN through.
+__device__ __forceinline__ float min_nan(float x, float y) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float x, float y) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
+// g sigmoid(alpha g) (u + 1) of clamped g and u; scale = -alpha log2(e).  The epilogue shares
+// the issue slots with the warps that keep the ring turning, so its instructions count: results
+// of 2^x and of the reciprocal below 2^-126 are taken as 0, which saves their rescaling.
+__device__ __forceinline__ float swiglu(float g, float u, float scale, float limit) {
+  g = min_nan(g, limit);
+  u = max_nan(min_nan(u, limit), -limit);
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * scale));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  g *= r;
+  return fmaf(g, u, g);
 }
 
 template <bool kFp4, bool kSwiglu, bool kPair>
-__global__ void __launch_bounds__(GrpCfg<kFp4>::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
 grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                const __grid_constant__ CUtensorMap wsmap, const __grid_constant__ CUtensorMap xsmap,
                const GroupedArgs a) {
   using C = GrpCfg<kFp4>;
+  using S = GrpSmem<kFp4, kPair>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  GrpShared& sb = *reinterpret_cast<GrpShared*>(tiles + kRingBytes + C::kRawBytes + kEpiWarps * kPatchBytes);
+  GrpShared& sb = *reinterpret_cast<GrpShared*>(tiles + S::kRingBytes + S::kRawBytes + kEpiWarps * kPatchBytes);
   volatile int* abort_flag = &sb.abort_flag;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -413,16 +456,15 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
   // a pair stages half of a tile's rows in each CTA
   constexpr int kCtas = kPair ? 2 : 1;
   constexpr int kGrain = 16 * kCtas;
-  constexpr int kRawPairs = kPair ? 3 : kMaxRawPairs, kRawStep = C::kRawBytes / kRawPairs;
   const int stage_rows = a.cap / kCtas;
   const int width = kPair ? kFeat : a.width;  // features of one CTA's part of a tile
   const uint32_t w_bytes = width * kStageKBytes;
   const uint32_t stage_size = stage_bytes<kFp4>(width, stage_rows, sub);
   const uint32_t x_part = sub * w_bytes, sf_part = x_part + sub * stage_rows * kStageKBytes;  // of a stage
   const int rank = kPair ? static_cast<int>(cluster_ctarank()) : 0;
-  // warps of a CTA that report a stage filled: gathered rows are reported by warp 3
+  // reports of a CTA that a stage is filled: weights, rows in boxes, what threads bring
   const bool gather = a.row_token != nullptr;
-  const int producers = 1 + (gather ? 0 : kRowWarps) + (kFp4 ? 2 : gather ? 1 : 0);
+  const int producers = 1 + (gather ? 0 : 1) + (kFp4 || gather ? 1 : 0);
   const int t_first = blockIdx.x / kCtas, t_step = gridDim.x / kCtas;
   // the leading CTA's barriers
   const uint32_t full0 = kPair ? dsmem_addr(smem_u32(&sb.full[0]), 0) : smem_u32(&sb.full[0]);
@@ -440,9 +482,9 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
       mbar_init(smem_u32(&sb.landed[s]), 32 * kRowWarps);
       mbar_init(smem_u32(&sb.empty[s]), 1);
     }
-    for (int r = 0; kFp4 && r < kMaxRawPairs; ++r) {
+    for (int r = 0; kFp4 && r < kMaxRawSlots; ++r) {
       mbar_init(smem_u32(&sb.raw_full[r]), kPair ? (gather ? 33 : 1) : 32);
-      mbar_init(smem_u32(&sb.raw_empty[r]), 2);
+      mbar_init(smem_u32(&sb.raw_empty[r]), kReportTurns);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&sb.acc_full[b]), 1);
@@ -450,7 +492,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
     }
     mbar_init(smem_u32(&sb.drain), 1);
     sb.abort_flag = 0;
-    for (int w = 0; w < kMaxProducers; ++w) sb.issued[w] = 0;
+    for (int w = 0; w < kProducers; ++w) sb.issued[w] = 0;
     sb.raw_issued = 0;
     fence_barrier_init();
   }
@@ -519,6 +561,8 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
   const int tiles_total = sb.total * a.tiles_f;
 
   if (warp == 0) {
+    // Copies first, then the report: the copies' way is the long one, and a phase of `full` is not
+    // over before all its arrivals, whatever has landed.
     RingPos p;
     int g = 0;
     bool ok = true;
@@ -531,12 +575,13 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
         if (elect_one()) {
           const uint32_t bar = full0 + 8 * p.stage;
           const int blocks = kPair ? 1 : min(sub, k_blocks - kb * sub);
-          grp_arrive_expect_tx<kPair>(bar, blocks * w_bytes);
           for (int u = 0; u == 0 || (!kPair && u < blocks); ++u)  // features past N are zero-filled
             tma_load_w<kPair>(ring + p.stage * stage_size + u * w_bytes, &wmap,
                               (kb * sub + u) * (kFp4 ? kStageKBytes : kStageKBytes / 2), tl.f0 + rank * kFeat, tl.e,
                               bar);
+          grp_arrive_expect_tx<kPair>(bar, blocks * w_bytes);
         }
+        __syncwarp();
       }
     }
     if (lane == 0) {
@@ -607,33 +652,33 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
     __syncwarp();
   } else if (kFp4 && warp == 2) {
     if constexpr (kFp4) {
-      // Scale bytes on their way, some pairs of blocks of K ahead: 16 bytes of a row serve a pair.
-      // In a pair of CTAs they come in boxes of 16 bytes x rows, but for gathered rows: copies by
-      // threads, 16 bytes from each of 32 rows, keep the load unit as busy as whole lines would,
-      // and there are enough of them to tell.  Small tiles take copies throughout (8 tokens down,
+      // Scale bytes on their way, some blocks of K ahead.  In a pair of CTAs they come in boxes of
+      // kRawPitch bytes x rows, but for gathered rows: copies by threads, 16 bytes each,
+      // neighbouring lanes on the same row.  Small tiles take copies throughout (8 tokens down,
       // 2880 x 2880: 28 us, with boxes 31).
-      const int pairs = (k_blocks + 1) / 2;
-      const uint32_t raw = smem_u32(tiles + kRingBytes);
-      constexpr int kRowQuarters = (kPair ? GrpCfg<true>::kRows : kMaxSingleRows) / 32;
+      const int cols = a.scale_stride / 16;
+      const int slots = (k_blocks + 2 * S::kRawCols - 1) / (2 * S::kRawCols);
+      const uint32_t raw = smem_u32(tiles + S::kRingBytes);
+      constexpr int kRowCopies = S::kRawRows * S::kRawCols / 32;
+      constexpr uint32_t kRowPart = kFeat * S::kRawPitch;
       RingPos p;
       bool ok = true;
       for (int t = t_first; t < tiles_total && ok; t += t_step) {
         const Tile tl = find_tile(sb, a, t, kCtas * width, lane);
-        const int quarters = (tl.n + 31) / 32;  // of blocks of 128 rows
+        const int copies = (tl.n * S::kRawCols + 31) / 32;
         const bool by_threads = !kPair || gather;
-        const uint8_t* src[kRowQuarters];
+        int src[kRowCopies];  // row of x of copy j: the piece (32 j + lane) % kRawCols of it
         const uint8_t* wsrc[kPair ? 1 : 4];
 #pragma unroll
-        for (int j = 0; j < kRowQuarters; ++j) {
-          const int r = 32 * j + lane;
-          src[j] = nullptr;  // behind the tile's last row: zeros
+        for (int j = 0; j < kRowCopies; ++j) {
+          const int r = (32 * j + lane) / S::kRawCols;
+          src[j] = -1;  // behind the tile's last row: zeros
           if (by_threads && r < tl.n) {
-            long long row = tl.r0 + r;
+            src[j] = tl.r0 + r;
             if (gather) {
               const int id = __ldg(a.row_token + tl.r0 + r);
-              row = id < 0 || id >= a.x_rows ? 0 : id;  // reported by the row warps
+              src[j] = id < 0 || id >= a.x_rows ? 0 : id;  // reported by the row warps
             }
-            src[j] = a.x_scales + row * a.scale_stride;
           }
         }
         const int f0 = tl.f0 + rank * kFeat;
@@ -646,20 +691,20 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
                           : nullptr;
           }
         }
-        for (int pair = 0; pair < pairs; ++pair, p.next(kRawPairs)) {
+        for (int slot = 0; slot < slots; ++slot, p.next(S::kRawSlots)) {
           if (p.round != 0)
             ok = wait_or_abort(smem_u32(&sb.raw_empty[p.stage]), (p.round - 1) & 1, a.timeout_ns, abort_flag);
           if (!ok) break;
           const uint32_t bar = smem_u32(&sb.raw_full[p.stage]);
-          const uint32_t dst = raw + p.stage * kRawStep;
+          const uint32_t dst = raw + p.stage * S::kRawStep;
           if constexpr (kPair) {
             if (elect_one()) {
               // few and large boxes: each costs its warp about 90 cycles to issue
               const int boxes = gather ? 0 : tl.n > kScaleBoxRows ? 2 : 1;
-              mbar_arrive_expect_tx(bar, 16 * (width + boxes * kScaleBoxRows));
-              tma_load_rows<false>(dst, &wsmap, 16 * pair, tl.e * a.N + f0, bar);  // E N < 2^31
+              mbar_arrive_expect_tx(bar, S::kRawPitch * (width + boxes * kScaleBoxRows));
+              tma_load_rows<false>(dst, &wsmap, S::kRawPitch * slot, tl.e * a.N + f0, bar);  // E N < 2^31
               for (int i = 0; i < boxes; ++i)
-                tma_load_rows<false>(dst + kRawBlock + 16 * kScaleBoxRows * i, &xsmap, 16 * pair,
+                tma_load_rows<false>(dst + kRowPart + S::kRawPitch * kScaleBoxRows * i, &xsmap, S::kRawPitch * slot,
                                      tl.r0 + kScaleBoxRows * i, bar);
             }
             __syncwarp();  // together again: the copies below are issued once, not once per branch
@@ -667,14 +712,18 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               if (32 * j < width)
-                copy_async16(dst + 512 * j + 16 * lane, wsrc[j] ? wsrc[j] + 16 * pair : a.w_scales, wsrc[j] ? 16 : 0);
+                copy_async16(dst + 512 * j + 16 * lane, wsrc[j] ? wsrc[j] + 16 * slot : a.w_scales, wsrc[j] ? 16 : 0);
           }
           if (by_threads) {
 #pragma unroll
-            for (int j = 0; j < kRowQuarters; ++j)
-              if (j < quarters)
-                copy_async16(dst + kRawBlock + 512 * j + 16 * lane, src[j] ? src[j] + 16 * pair : a.x_scales,
-                             src[j] ? 16 : 0);
+            for (int j = 0; j < kRowCopies; ++j)
+              if (j < copies) {
+                const int col = slot * S::kRawCols + (32 * j + lane) % S::kRawCols;
+                const bool read = src[j] >= 0 && col < cols;
+                copy_async16(dst + kRowPart + 512 * j + 16 * lane,
+                             a.x_scales + (read ? static_cast<long long>(src[j]) * a.scale_stride + 16 * col : 0),
+                             read ? 16 : 0);
+              }
             copy_async_arrive(bar);
           }
         }
@@ -682,99 +731,101 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
       copy_async_wait_all();
       if (lane == 0) {
         if (!ok) raise_status(a.status, kStatusTimeout);
-        sb.raw_issued = p.round * kRawPairs + p.stage;
+        sb.raw_issued = p.round * S::kRawSlots + p.stage;
       }
     }
-  } else if ((warp == 3 && (kFp4 || gather)) || (kFp4 && warp == kScaleWarp)) {
+  } else if (warp == 3 || warp == kReportWarp1) {
     // What threads have brought becomes the tensor core's: scales are put in their layout,
     // gathered rows have landed; then one proxy fence, by a warp that has no copies under way
-    // (with them, a fence takes as long as they do), and the stage is reported.  In MXFP4 two
-    // warps take turns of one block of K (warp 3 the even ones) and both report every stage (256
-    // tokens up: 180 us, with one warp 194).
-    [[maybe_unused]] const int turn = warp == kScaleWarp ? 1 : 0;
+    // (with them, a fence takes as long as they do), and the stage is reported.  The two warps take
+    // turns of one stage, counted over all tiles: a wait for a parity is sound only if the phase
+    // before it is known to be over, which a warp that comes back within one round of the ring
+    // knows from its last stage (rows land, and stages become free, in their order).  Four warps
+    // were slower: every warp that waits takes issue slots from those that work (gathered rows,
+    // 32768 tokens up: 1.25 ms, with two 1.12).
+    const int turn = warp == 3 ? 0 : 1;
     RingPos p, pr;
-    int g = 0;
-    bool ok = true;
-    for (int t = t_first; t < tiles_total && ok; t += t_step) {
-      if constexpr (!kFp4) {
-        for (int kb = 0; kb < k_steps; ++kb, ++g, p.next(stages)) {
-          ok = wait_or_abort(smem_u32(&sb.landed[p.stage]), p.round & 1, a.timeout_ns, abort_flag);
-          if (!ok) break;
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (elect_one()) grp_arrive<kPair>(full0 + 8 * p.stage);
-          __syncwarp();
-        }
-      } else {
-        const Tile tl = find_tile(sb, a, t, kCtas * width, lane);
-        const int quarters = (tl.n + 31) / 32;
-        const int used = a.K / 32;  // scale bytes in use: what lies behind is padding
-        for (int block = 0; block < k_blocks && ok; block += 2, pr.next(kRawPairs)) {
+    int base = 0, done = 0;  // stages of earlier tiles; one more than the last stage reported
+    bool ok = kFp4 || gather;
+    for (int t = t_first; t < tiles_total && ok; t += t_step, base += k_steps) {
+      [[maybe_unused]] int quarters = 0, slot = -1;  // of 128 rows; place of scales that is being read
+      if constexpr (kFp4) quarters = (find_tile(sb, a, t, kCtas * width, lane).n + 31) / 32;
+      auto leave = [&]() {
+        __syncwarp();
+        if (elect_one()) mbar_arrive(smem_u32(&sb.raw_empty[pr.stage]));
+        __syncwarp();
+        pr.next(S::kRawSlots);
+      };
+      auto enter = [&](int next) {
+        while (slot < next && ok) {
+          if (slot >= 0) leave();
+          ++slot;
           ok = wait_or_abort(smem_u32(&sb.raw_full[pr.stage]), pr.round & 1, a.timeout_ns, abort_flag);
-          if (!ok) break;
-          const uint8_t* raw = tiles + kRingBytes + pr.stage * kRawStep + 16 * lane;
-          // A block's 8 bytes of rows lane, lane + 32, lane + 64, lane + 96 of each block of 128.
-          // All that can be there is read, without a branch: what rows behind the tile's last
-          // one (or features behind its width) have there scales columns (lanes) that are never stored.
-          constexpr int kQuarters = 4 + (kPair ? GrpCfg<true>::kRows : kMaxSingleRows) / 32;
-          uint2 c[12];
+        }
+      };
+      int at = 0;
+      for (int kb = (turn - base) & (kReportTurns - 1); kb < k_steps; kb += kReportTurns) {
+        p.skip(kb - at, stages);
+        at = kb;
+        if constexpr (kFp4) {
+          const int blocks = kPair ? 1 : min(sub, k_blocks - kb * sub);
+          for (int u = 0; u == 0 || (!kPair && u < blocks); ++u) {
+            const int block = kb * sub + u;
+            enter(block / (2 * S::kRawCols));
+            if (!ok) break;
+            // The block's 8 bytes of rows lane, lane + 32, lane + 64, lane + 96 of each block of
+            // 128.  All that can be there is read, without a branch: what rows behind the tile's last
+            // one (or features behind its width) have there scales columns (lanes) that are never stored.
+            const uint8_t* raw = tiles + S::kRingBytes + pr.stage * S::kRawStep + S::kRawPitch * lane +
+                                 8 * (block - 2 * S::kRawCols * slot);
+            constexpr int kQuarters = (kFeat + S::kRawRows) / 32;
+            uint2 c[12];
 #pragma unroll
-          for (int i = 0; i < 12; ++i)
-            c[i] = i < kQuarters ? *reinterpret_cast<const uint2*>(raw + 512 * i + 8 * turn) : make_uint2(0, 0);
-          const int valid = used - 8 * (block + turn);  // bytes, the rest is padding
-          if (valid < 8) {
-            const uint32_t mask0 = valid >= 4 ? 0xFFFFFFFFu : valid <= 0 ? 0u : (1u << (8 * valid)) - 1u;
-            const uint32_t mask1 = valid <= 4 ? 0u : (1u << (8 * valid - 32)) - 1u;
+            for (int i = 0; i < 12; ++i)
+              c[i] = i < kQuarters ? *reinterpret_cast<const uint2*>(raw + 32 * S::kRawPitch * i) : make_uint2(0, 0);
+            const int valid = a.K / 32 - 8 * block;  // bytes in use, the rest is padding
+            if (valid < 8) {
+              const uint32_t mask0 = valid >= 4 ? 0xFFFFFFFFu : valid <= 0 ? 0u : (1u << (8 * valid)) - 1u;
+              const uint32_t mask1 = valid <= 4 ? 0u : (1u << (8 * valid - 32)) - 1u;
 #pragma unroll
-            for (int i = 0; i < kQuarters; ++i) c[i] = make_uint2(c[i].x & mask0, c[i].y & mask1);
-          }
-          __syncwarp();
-          if (elect_one()) mbar_arrive(smem_u32(&sb.raw_empty[pr.stage]));
-          __syncwarp();
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (block + h >= k_blocks) break;
-            const int u = sub == 2 ? h : 0;
-            const bool mine = h == turn;
+              for (int i = 0; i < kQuarters; ++i) c[i] = make_uint2(c[i].x & mask0, c[i].y & mask1);
+            }
             if (u == 0 && p.round != 0)
               ok = wait_or_abort(smem_u32(&sb.empty[p.stage]), (p.round - 1) & 1, a.timeout_ns, abort_flag);
             if (!ok) break;
-            if (mine) {
-              uint4* sf = reinterpret_cast<uint4*>(tiles + p.stage * stage_size + sf_part + u * C::kSfBytes) + lane;
+            uint4* sf = reinterpret_cast<uint4*>(tiles + p.stage * stage_size + sf_part + u * C::kSfBytes) + lane;
 #pragma unroll
-              for (int blk = 0; blk < 3; ++blk) {
-                if (blk == 2 && quarters <= 4) break;
-                const uint2* v = c + 4 * blk;
-                sf[blk * (kSfBlock / 16)] = make_uint4(v[0].x, v[1].x, v[2].x, v[3].x);
-                sf[(3 + blk) * (kSfBlock / 16)] = make_uint4(v[0].y, v[1].y, v[2].y, v[3].y);
-              }
-            }
-            if (u + 1 == sub || block + h + 1 == k_blocks) {
-              // of a stage of two blocks both warps have written; the rows are the last one's
-              if (mine || sub == 2) {
-                if (gather && mine) ok = wait_or_abort(smem_u32(&sb.landed[p.stage]), p.round & 1, a.timeout_ns, abort_flag);
-                if (!ok) break;
-                fence_proxy_async_smem();
-                __syncwarp();
-              }
-              if (elect_one()) grp_arrive<kPair>(full0 + 8 * p.stage);
-              __syncwarp();
-              ++g;
-              p.next(stages);
+            for (int blk = 0; blk < 3; ++blk) {
+              if (blk == 2 && quarters <= 4) break;
+              const uint2* v = c + 4 * blk;
+              sf[blk * (kSfBlock / 16)] = make_uint4(v[0].x, v[1].x, v[2].x, v[3].x);
+              sf[(3 + blk) * (kSfBlock / 16)] = make_uint4(v[0].y, v[1].y, v[2].y, v[3].y);
             }
           }
         }
+        if (gather && ok) ok = wait_or_abort(smem_u32(&sb.landed[p.stage]), p.round & 1, a.timeout_ns, abort_flag);
+        if (!ok) break;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (elect_one()) grp_arrive<kPair>(full0 + 8 * p.stage);
+        __syncwarp();
+        done = base + kb + 1;
+      }
+      p.skip(k_steps - at, stages);
+      if constexpr (kFp4) {
+        if (ok) enter((k_blocks - 1) / (2 * S::kRawCols));
+        if (ok) leave();
       }
     }
     if (lane == 0) {
-      if (!ok) raise_status(a.status, kStatusTimeout);
-      sb.issued[1 + kRowWarps + (kFp4 && warp == kScaleWarp)] = g;
+      if (!ok && (kFp4 || gather)) raise_status(a.status, kStatusTimeout);
+      sb.issued[1 + kTurns + turn] = done;
     }
   } else if (warp >= kRowWarp0) {
     const int wr = warp - kRowWarp0;
     constexpr int kSteps = kPair ? C::kRows / kGrain : kMaxSingleRows / 16;
     RingPos p;
-    int g = 0;
+    int g = 0, done = 0;  // stages of earlier tiles; one more than the last stage reported
     bool ok = true;
     if (gather) {
       // Gathered rows: eight threads per row copy its 128 bytes, 16 rows at a time, into the
@@ -803,7 +854,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
             has |= 1u << i;
           }
         }
-        for (int kb = 0; kb < k_steps; ++kb, ++g, p.next(stages)) {
+        for (int kb = 0; kb < k_steps; ++kb, p.next(stages)) {
           if (p.round != 0)
             ok = wait_or_abort(smem_u32(&sb.empty[p.stage]), (p.round - 1) & 1, a.timeout_ns, abort_flag);
           if (!ok) break;
@@ -825,33 +876,47 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
       }
       copy_async_wait_all();
     } else {
-      for (int t = t_first; t < tiles_total && ok; t += t_step) {
+      // Boxes of rows, whole stages in turns: a report to the leading CTA's barrier keeps its warp
+      // about 220 cycles, a copy's issue 100 and more.
+      constexpr int kBox = kPair ? C::kRows / 4 : kBoxRows;
+      for (int t = t_first; t < tiles_total && ok; t += t_step, g += k_steps) {
         const Tile tl = find_tile(sb, a, t, kCtas * width, lane);
         const int half = (tl.n + kGrain - 1) / kGrain * 16;  // rows that this CTA stages
-        // the boxes of all blocks of a stage, dealt out to the warps
-        const int units = half / kBoxRows, box = lane * kRowWarps + wr;
-        const int u = kPair ? 0 : box / units, unit = box - u * units;
-        const uint32_t dst = ring + x_part + (u * stage_rows + unit * kBoxRows) * kStageKBytes;
-        const int row = tl.r0 + rank * half + kBoxRows * unit;
-        for (int kb = 0; kb < k_steps; ++kb, ++g, p.next(stages)) {
+        const int units = (half + kBox - 1) / kBox;          // at most 2 in a pair
+        const int u = kPair ? 0 : lane / units, unit = lane - u * units;
+        const int row0 = tl.r0 + rank * half;
+        int at = 0;
+        for (int kb = (wr - g) & (kTurns - 1); kb < k_steps; kb += kTurns) {
+          p.skip(kb - at, stages);
+          at = kb;
           if (p.round != 0)
             ok = wait_or_abort(smem_u32(&sb.empty[p.stage]), (p.round - 1) & 1, a.timeout_ns, abort_flag);
           if (!ok) break;
           const int boxes = (kPair ? 1 : min(sub, k_blocks - kb * sub)) * units;
-          const uint32_t bar = full0 + 8 * p.stage;
-          if (elect_one())
-            grp_arrive_expect_tx<kPair>(bar, (boxes - wr + kRowWarps - 1) / kRowWarps * kBoxRows * kStageKBytes);
+          const uint32_t bar = full0 + 8 * p.stage, dst = ring + p.stage * stage_size + x_part;
+          if constexpr (kPair) {
+            if (elect_one()) {
+              const int x = kb * (kFp4 ? kStageKBytes : kStageKBytes / 2);
+              tma_load_rows<true>(dst, &xmap, x, row0, bar);
+              if (units > 1) tma_load_rows<true>(dst + kBox * kStageKBytes, &xmap, x, row0 + kBox, bar);
+              grp_arrive_expect_tx<true>(bar, boxes * kBox * kStageKBytes);
+            }
+          } else {
+            if (lane < boxes)
+              tma_load_rows<false>(dst + (u * stage_rows + unit * kBox) * kStageKBytes, &xmap,
+                                   (kb * sub + u) * (kFp4 ? kStageKBytes : kStageKBytes / 2), row0 + kBox * unit, bar);
+            __syncwarp();
+            if (elect_one()) grp_arrive_expect_tx<false>(bar, boxes * kBox * kStageKBytes);
+          }
           __syncwarp();
-          if (box < boxes)
-            tma_load_rows<kPair>(dst + p.stage * stage_size, &xmap,
-                                 (kb * sub + u) * (kFp4 ? kStageKBytes : kStageKBytes / 2), row, bar);
-          __syncwarp();
+          done = g + kb + 1;
         }
+        p.skip(k_steps - at, stages);
       }
     }
     if (lane == 0) {
       if (!ok) raise_status(a.status, kStatusTimeout);
-      sb.issued[1 + wr] = g;
+      sb.issued[1 + wr] = done;
     }
   } else if (warp >= kEpiWarp0) {
     const int half = (warp - kEpiWarp0) >> 2;  // the two warps of a lane quarter take turns of 32 columns
@@ -860,7 +925,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
     // Rows of 16-byte pieces where the output allows them: the fragment's threads hold pairs of
     // rows (columns) of a feature (lane), an 8 x 8 transposition through this warp's 512 bytes
     // of shared memory makes eight features of a row of them.
-    uint8_t* patch = tiles + kRingBytes + C::kRawBytes + (warp - kEpiWarp0) * kPatchBytes;
+    uint8_t* patch = tiles + S::kRingBytes + S::kRawBytes + (warp - kEpiWarp0) * kPatchBytes;
     const uint32_t patch0 = smem_u32(patch);
     const int fr = lane >> 2;
     // pieces of a row in the patch: 4 (2 with SwiGLU), at places that spread over the banks
@@ -869,6 +934,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
                                  : patch0 + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
     const uint8_t* get = kSwiglu ? patch + (lane >> 1) * 32 + (((lane & 1) ^ ((lane >> 3) & 1)) << 4)
                                  : patch + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
+    [[maybe_unused]] const float scale = -1.4426950408889634f * a.alpha;
     const bool wide = a.n_out % 8 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0;
     int i = 0;
     for (int t = t_first; t < tiles_total; t += t_step, ++i) {
@@ -909,7 +975,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
                 for (int k = 0; k < 2; ++k) {
                   const float l = __uint_as_float(v[k]) + bl, h = __uint_as_float(v[2 + k]) + bh;
                   const float theirs = __shfl_xor_sync(0xffffffffu, odd ? l : h, 4);
-                  y[k] = swiglu(odd ? theirs : l, odd ? h : theirs, a.alpha, a.limit);
+                  y[k] = swiglu(odd ? theirs : l, odd ? h : theirs, scale, a.limit);
                 }
                 m[j] = pack_bf16x2(y[0], y[1]);
               }
@@ -959,7 +1025,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
             if constexpr (kSwiglu) {
               // both lanes of a pair compute the output, the even one stores it
               const float theirs = __shfl_xor_sync(0xffffffffu, y, 1);
-              y = swiglu((lane & 1) ? theirs : y, (lane & 1) ? y : theirs, a.alpha, a.limit);
+              y = swiglu((lane & 1) ? theirs : y, (lane & 1) ? y : theirs, scale, a.limit);
             }
             if (mine && c + j < tl.n && !(kSwiglu && (lane & 1)))
               out[static_cast<long long>(c + j) * a.n_out] = static_cast<uint16_t>(pack_bf16x2(y, 0.0f) & 0xFFFFu);
@@ -976,9 +1042,9 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
   __syncthreads();
   if (kFp4 && threadIdx.x == 0) {
     // scales that nobody waited for (the last ones of an aborted run)
-    for (int r = 0; r < kRawPairs && r < sb.raw_issued; ++r) {
-      const int last = sb.raw_issued - 1 - ((sb.raw_issued - 1 - r) % kRawPairs);
-      if (!mbar_wait(smem_u32(&sb.raw_full[r]), (last / kRawPairs) & 1, kDrainTimeoutNs))
+    for (int r = 0; r < S::kRawSlots && r < sb.raw_issued; ++r) {
+      const int last = sb.raw_issued - 1 - ((sb.raw_issued - 1 - r) % S::kRawSlots);
+      if (!mbar_wait(smem_u32(&sb.raw_full[r]), (last / S::kRawSlots) & 1, kDrainTimeoutNs))
         raise_status(a.status, kStatusTimeout);
     }
   }
@@ -995,19 +1061,18 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
         x = *const_cast<const volatile int*>(v);
       return x;
     };
-    auto reports = [&](int w) {
-      return w == 0 || (w <= kRowWarps ? !gather : w == 1 + kRowWarps ? kFp4 || gather : kFp4);
-    };
+    auto reports = [&](int w) { return w == 0 || (w <= kTurns ? !gather : kFp4 || gather); };
     int aborted = 0, most = 0;
     for (int c = 0; c < kCtas; ++c) {
       aborted |= peer(&sb.abort_flag, c);
-      for (int w = 0; w < kMaxProducers; ++w)
+      for (int w = 0; w < kProducers; ++w)
         if (reports(w)) most = max(most, peer(&sb.issued[w], c));
     }
     if (aborted) {
       for (int c = 0; c < kCtas; ++c)
-        for (int w = 0; w < kMaxProducers; ++w)
-          for (int g = reports(w) ? peer(&sb.issued[w], c) : most; g < most; ++g) grp_arrive<kPair>(full0 + 8 * (g % stages));
+        for (int w = 0; w < kProducers; ++w)
+          for (int g = reports(w) ? peer(&sb.issued[w], c) : most; g < most; ++g)
+            if (w == 0 || (w <= kTurns ? g % kTurns == w - 1 : g % kReportTurns == w - 1 - kTurns)) grp_arrive<kPair>(full0 + 8 * (g % stages));
       for (int s = 0; s < stages && s < most; ++s) {
         const int last = most - 1 - ((most - 1 - s) % stages);
         if (!mbar_wait(smem_u32(&sb.full[s]), (last / stages) & 1, kDrainTimeoutNs))
@@ -1042,7 +1107,7 @@ cudaError_t launch_grouped_t(const GroupedMaps& m, const GroupedArgs& a, int sms
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !attr_set[dev].load(std::memory_order_acquire)) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem_bytes<kFp4>()));
+                             static_cast<int>(smem_bytes<kFp4, kPair>()));
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev].store(true, std::memory_order_release);
   }
@@ -1054,15 +1119,16 @@ cudaError_t launch_grouped_t(const GroupedMaps& m, const GroupedArgs& a, int sms
   while ((1LL << bits) < a.tiles_f) ++bits;
   b.f_shift = 30 + bits;
   b.f_magic = static_cast<uint32_t>((1ull << b.f_shift) / a.tiles_f + 1);
-  b.stages = stage_count<kFp4>(kPair ? kFeat : a.width, a.cap / kCtas, kPair ? 1 : a.sub);
+  b.stages = stage_count<kFp4, kPair>(kPair ? kFeat : a.width, a.cap / kCtas, kPair ? 1 : a.sub);
+  if (b.stages < kTurns) return cudaErrorInvalidValue;  // not with any tile that grouped_plan makes
   // no more CTAs than tiles there can be
   const long long groups = a.num_experts < a.rows ? a.num_experts : a.rows;
   const long long most = (a.rows / a.cap + groups) * a.tiles_f;
   const int slots = sms / kCtas;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((most < slots ? most : slots) * kCtas));
-  cfg.blockDim = dim3(GrpCfg<kFp4>::kThreads);
-  cfg.dynamicSmemBytes = smem_bytes<kFp4>();
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem_bytes<kFp4, kPair>();
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1113,7 +1179,7 @@ void grouped_plan(GroupedArgs& a, bool mxfp4, int sms) {
     // as many blocks of K per stage as leave four stages: with few rows a stage costs its
     // barriers (about 0.1 us) more than its MMAs
     auto count = [&](int sub) {
-      return mxfp4 ? stage_count<true>(a.width, a.cap, sub) : stage_count<false>(a.width, a.cap, sub);
+      return mxfp4 ? stage_count<true, false>(a.width, a.cap, sub) : stage_count<false, false>(a.width, a.cap, sub);
     };
     for (const int most = mxfp4 ? 2 : 4; a.sub < most && count(2 * a.sub) >= 4;) a.sub *= 2;
   }

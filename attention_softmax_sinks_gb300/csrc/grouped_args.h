@@ -8,8 +8,9 @@
 namespace sa {
 
 constexpr int kMaxExperts = 256;
-constexpr int kBoxRows = 16;  // rows of one TMA box of x
+constexpr int kBoxRows = 16;  // rows of one TMA box of x (cap / 4 with pairs: two make a CTA's half)
 constexpr int kScaleBoxRows = 112;  // rows of one TMA box of x's scales: half of a pair's tile
+constexpr int kScaleBoxCols = 3;    // 16 bytes of a row's scales, so many times, in one TMA box
 constexpr int kGroupedFeatures = 128;  // features of one tile (the tcgen05.mma M)
 
 struct GroupedArgs {
@@ -42,9 +43,9 @@ struct GroupedArgs {
 // 16, 64 or, for pairs, 256 in bf16 and 224 in MXFP4 (whose scales take TMEM columns beside
 // the accumulators).
 void grouped_plan(GroupedArgs& a, bool mxfp4, int sms);
-// w: {K, N, E} in boxes of 128 bytes x width x 1;  x: [x_rows, K] in boxes of 128 bytes x
-// kBoxRows;  MXFP4 scales, with pairs only: [E N, scale_stride] in boxes of 16 bytes x width and
-// [x_rows, scale_stride] in boxes of 16 bytes x kScaleBoxRows.
+// w: {K, N, E} in boxes of 128 bytes x width x 1;  x: [x_rows, K] in boxes of 128 bytes x kBoxRows
+// (cap / 4 with pairs);  MXFP4 scales, with pairs only: [E N, scale_stride] in boxes of
+// 16 kScaleBoxCols bytes x width and [x_rows, scale_stride] in as many bytes x kScaleBoxRows.
 struct GroupedMaps {
   CUtensorMap w, x, w_scales, x_scales;
 };
