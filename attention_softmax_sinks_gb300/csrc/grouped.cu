@@ -934,7 +934,8 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
                                  : patch0 + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
     const uint8_t* get = kSwiglu ? patch + (lane >> 1) * 32 + (((lane & 1) ^ ((lane >> 3) & 1)) << 4)
                                  : patch + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
-    [[maybe_unused]] const float scale = -1.4426950408889634f * a.alpha;
+    // finite, so that a gate of 0 stays one
+    [[maybe_unused]] const float scale = fminf(fmaxf(-1.4426950408889634f * a.alpha, -3.0e38f), 3.0e38f);
     const bool wide = a.n_out % 8 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0;
     int i = 0;
     for (int t = t_first; t < tiles_total; t += t_step, ++i) {

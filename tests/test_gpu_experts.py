@@ -225,6 +225,21 @@ def test_swiglu_clamps_limits_and_infinities():
     assert torch.isnan(sa.grouped_linear_swiglu(x, w, off, nan)).all()
 
 
+@pytest.mark.parametrize("n", [16, 18], ids=["wide", "narrow"])
+def test_swiglu_of_huge_alpha(n):
+    """Any finite alpha: sigmoid becomes a step, and a gate of 0 still gives 0 (0 times an
+    overflowed alpha would be NaN).  With x = 0 the products are the bias: whole numbers, exact."""
+    sa = require_gpu()
+    x = torch.zeros((3, 64), dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros((1, n, 64), dtype=torch.bfloat16, device="cuda")
+    gate = np.resize([0.0, 1.0, -1.0, 2.0], n // 2)
+    bias = torch.from_numpy(np.stack([gate, np.ones(n // 2)], 1).reshape(1, n)).to(torch.bfloat16).cuda()
+    for alpha in (3e38, -3e38, 0.0):
+        out = host(sa.grouped_linear_swiglu(x, w, dev(np.array([0, 3], dtype=np.int32)), bias, alpha=alpha))
+        sigmoid = np.where(gate * alpha > 0, 1.0, np.where(gate * alpha < 0, 0.0, 0.5))
+        assert np.array_equal(out, np.broadcast_to(gate * sigmoid * 2.0, out.shape))
+
+
 @pytest.mark.parametrize("mx", [False, True], ids=["bf16", "mxfp4"])
 def test_bad_groups_and_bad_rows_are_reported_and_skipped(mx):
     sa = require_gpu()
