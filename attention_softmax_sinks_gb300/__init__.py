@@ -171,7 +171,7 @@ def _call(fn, dev, stream, *args):
         raise ValueError(f"stream is on cuda:{stream.device_index}, the tensors on cuda:{dev}")
     # the raw handle: a Stream object costs more than the rest of the call
     s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:  # the tensors are there: CUDA is initialised
         return fn(*args, s)
     with torch.cuda.device(dev):
         return fn(*args, s)
@@ -519,13 +519,15 @@ def _inputs(*named):
     index.  Optional tensors are left out by the caller when they are None."""
     di = -1
     for name, t, dt, shape in named:
-        if not isinstance(t, torch.Tensor) or t.dtype is not dt or not t.is_cuda or not t.is_contiguous():
+        if not isinstance(t, torch.Tensor) or t.dtype is not dt or not t.is_contiguous():
             _dev(t, name, dt)  # raises
-        d = t.get_device()
+        d = t.get_device()  # -1 on the CPU
         if d != di:
             if di >= 0:
                 _same_device(di, (name, t))  # raises
             di = d
+        if d < 0:
+            _dev(t, name, dt)  # raises
         if t.numel() > _C_INT:
             for v in t.shape:
                 _c_int(v, f"a dimension of {name}")
@@ -535,13 +537,13 @@ def _inputs(*named):
     return di
 
 
-def _size(t, name, dim):
-    """t.shape[dim], of something that may not be a tensor of that many dimensions."""
+def _shape(t, name, dims):
+    """The shape of something that may not be a tensor of ``dims`` dimensions."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dim() <= dim:
-        raise ValueError(f"{name} has {t.dim()} dimensions, expected more than {dim}")
-    return t.shape[dim]
+    if t.dim() != dims:
+        raise ValueError(f"{name} must be of {dims} dimensions, got {tuple(t.shape)}")
+    return t.shape
 
 
 def moe_group_rows(topk_idx, num_experts: int, expert_offsets=None, row_token=None, pair_row=None,
@@ -571,7 +573,7 @@ def moe_group_rows(topk_idx, num_experts: int, expert_offsets=None, row_token=No
 def moe_combine(y, pair_row, topk_weight, out=None, stream=None):
     """out[t] = sum_i topk_weight[t, i] * y[pair_row[t, i]]: y [R, H] bf16, pair_row [T, k]
     int32 (-1 adds nothing), topk_weight [T, k] bf16.  Returns out [T, H] bf16."""
-    t, k = _size(pair_row, "pair_row", 0), _size(pair_row, "pair_row", 1)
+    t, k = _shape(pair_row, "pair_row", 2)
     di = _inputs(("y", y, torch.bfloat16, 2), ("pair_row", pair_row, torch.int32, (t, k)),
                  ("topk_weight", topk_weight, torch.bfloat16, (t, k)))
     r, h = y.shape
@@ -590,8 +592,8 @@ def _product_output(out, rows, n, x, di, stream):
 
 def _grouped(where, x, w, expert_offsets, bias, row_token, out, stream, act=()):
     """The grouped products on bf16 operands; act: SwiGLU's (alpha, limit) or ()."""
-    e, n, k = _size(w, "w", 0), _size(w, "w", 1), _size(w, "w", 2)
-    x_rows = _size(x, "x", 0)
+    e, n, k = _shape(w, "w", 3)
+    x_rows = _shape(x, "x", 2)[0]
     named = [("x", x, torch.bfloat16, (x_rows, k)), ("w", w, torch.bfloat16, (e, n, k)),
              ("expert_offsets", expert_offsets, torch.int32, (e + 1,))]
     if bias is not None:
@@ -657,7 +659,11 @@ def mxfp4_quantize(x, codes=None, scales=None, stream=None):
 def mxfp4_dequantize(codes, scales, out=None, stream=None):
     """The bf16 values [..., K] of MXFP4 codes [..., K / 2] and scales (as mxfp4_quantize
     returns them)."""
-    half = _size(codes, "codes", -1 if isinstance(codes, torch.Tensor) and codes.dim() else 0)
+    if not isinstance(codes, torch.Tensor):
+        raise TypeError("codes must be a CUDA tensor")
+    if codes.dim() < 1:
+        raise ValueError("codes must have at least one dimension")
+    half = codes.shape[-1]
     k, lead = 2 * half, codes.shape[:-1]
     di = _inputs(("codes", codes, torch.uint8, (*lead, half)),
                  ("scales", scales, torch.uint8, (*lead, mxfp4_scale_columns(k))))
@@ -672,7 +678,8 @@ def mxfp4_dequantize(codes, scales, out=None, stream=None):
 def mxfp4_linear_bias(x_codes, x_scales, w_codes, w_scales, bias=None, out=None, stream=None):
     """linear_bias with both operands in MXFP4 (block-scaled tcgen05 products): x [M, K] and
     w [N, K] as codes [., K / 2] and scales, bias [N] bf16 or None.  Returns [M, N] bf16."""
-    m, half, n = _size(x_codes, "x_codes", 0), _size(x_codes, "x_codes", 1), _size(w_codes, "w_codes", 0)
+    m, half = _shape(x_codes, "x_codes", 2)
+    n = _shape(w_codes, "w_codes", 2)[0]
     s = mxfp4_scale_columns(2 * half)
     named = [("x_codes", x_codes, torch.uint8, (m, half)), ("x_scales", x_scales, torch.uint8, (m, s)),
              ("w_codes", w_codes, torch.uint8, (n, half)), ("w_scales", w_scales, torch.uint8, (n, s))]
@@ -688,8 +695,8 @@ def mxfp4_linear_bias(x_codes, x_scales, w_codes, w_scales, bias=None, out=None,
 
 def _grouped_mxfp4(where, x_codes, x_scales, w_codes, w_scales, expert_offsets, bias, row_token, out, stream, act=()):
     """The grouped products on MXFP4 operands; act: SwiGLU's (alpha, limit) or ()."""
-    e, n, half = (_size(w_codes, "w_codes", i) for i in range(3))
-    x_rows, s = _size(x_codes, "x_codes", 0), mxfp4_scale_columns(2 * half)
+    e, n, half = _shape(w_codes, "w_codes", 3)
+    x_rows, s = _shape(x_codes, "x_codes", 2)[0], mxfp4_scale_columns(2 * half)
     named = [("x_codes", x_codes, torch.uint8, (x_rows, half)), ("x_scales", x_scales, torch.uint8, (x_rows, s)),
              ("w_codes", w_codes, torch.uint8, (e, n, half)), ("w_scales", w_scales, torch.uint8, (e, n, s)),
              ("expert_offsets", expert_offsets, torch.int32, (e + 1,))]
