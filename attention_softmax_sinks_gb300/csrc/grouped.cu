@@ -422,17 +422,28 @@ __device__ __forceinline__ float max_nan(float x, float y) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
   return r;
 }
-// g sigmoid(alpha g) (u + 1) of clamped g and u; scale = -alpha log2(e).  The epilogue shares
-// the issue slots with the warps that keep the ring turning, so its instructions count: results
-// of 2^x and of the reciprocal below 2^-126 are taken as 0, which saves their rescaling.
-__device__ __forceinline__ float swiglu(float g, float u, float scale, float limit) {
-  g = min_nan(g, limit);
-  u = max_nan(min_nan(u, limit), -limit);
-  float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * scale));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-  g *= r;
-  return fmaf(g, u, g);
+__device__ __forceinline__ float2 f2_unpack(uint64_t v) {
+  float2 r;
+  f2_split(v, r.x, r.y);
+  return r;
+}
+__device__ __forceinline__ float rcp_ftz(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Two of g sigmoid(alpha g) (u + 1) with clamped g and u; scale2 = -alpha log2(e), twice.  The
+// epilogue shares the issue slots with the warps that keep the ring turning, so its instructions
+// count: packed arithmetic, and results of 2^x and of the reciprocal below 2^-126 taken as 0, which
+// saves their rescaling.
+__device__ __forceinline__ uint32_t swiglu2(float g0, float g1, float u0, float u1, uint64_t scale2, float limit) {
+  const uint64_t g = f2(min_nan(g0, limit), min_nan(g1, limit));
+  const uint64_t u = f2(max_nan(min_nan(u0, limit), -limit), max_nan(min_nan(u1, limit), -limit));
+  const float2 x = f2_unpack(f2_mul(g, scale2));
+  const float2 d = f2_unpack(f2_add(f2(ex2(x.x), ex2(x.y)), f2(1.0f, 1.0f)));
+  const uint64_t t = f2_mul(g, f2(rcp_ftz(d.x), rcp_ftz(d.y)));
+  const float2 y = f2_unpack(f2_fma(t, u, t));
+  return pack_bf16x2(y.x, y.y);
 }
 
 template <bool kFp4, bool kSwiglu, bool kPair>
@@ -935,7 +946,11 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
     const uint8_t* get = kSwiglu ? patch + (lane >> 1) * 32 + (((lane & 1) ^ ((lane >> 3) & 1)) << 4)
                                  : patch + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
     // finite, so that a gate of 0 stays one
-    [[maybe_unused]] const float scale = fminf(fmaxf(-1.4426950408889634f * a.alpha, -3.0e38f), 3.0e38f);
+    const float scale = fminf(fmaxf(-1.4426950408889634f * a.alpha, -3.0e38f), 3.0e38f);
+    [[maybe_unused]] const uint64_t scale2 = f2(scale, scale);
+    auto add2 = [](const uint32_t* v, float b) {  // two accumulators of one feature and its bias
+      return f2_unpack(f2_add(f2(__uint_as_float(v[0]), __uint_as_float(v[1])), f2(b, b)));
+    };
     const bool wide = a.n_out % 8 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0;
     int i = 0;
     for (int t = t_first; t < tiles_total; t += t_step, ++i) {
@@ -970,15 +985,10 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 const uint32_t* v = ((j & 1) ? hi : lo) + 4 * (2 * i2 + (j >> 1));
-                const float bl = (j & 1) ? b2 : b0, bh = (j & 1) ? b3 : b1;
-                float y[2];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  const float l = __uint_as_float(v[k]) + bl, h = __uint_as_float(v[2 + k]) + bh;
-                  const float theirs = __shfl_xor_sync(0xffffffffu, odd ? l : h, 4);
-                  y[k] = swiglu(odd ? theirs : l, odd ? h : theirs, scale, a.limit);
-                }
-                m[j] = pack_bf16x2(y[0], y[1]);
+                const float2 l = add2(v, (j & 1) ? b2 : b0), h = add2(v + 2, (j & 1) ? b3 : b1);
+                const float t0 = __shfl_xor_sync(0xffffffffu, odd ? l.x : h.x, 4);
+                const float t1 = __shfl_xor_sync(0xffffffffu, odd ? l.y : h.y, 4);
+                m[j] = swiglu2(odd ? t0 : l.x, odd ? t1 : l.y, odd ? h.x : t0, odd ? h.y : t1, scale2, a.limit);
               }
               store_transposed(put, m);
               __syncwarp();
@@ -994,10 +1004,10 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
 #pragma unroll
             for (int i4 = 0; i4 < 4; ++i4) {
               uint32_t m[4];
-              m[0] = pack_bf16x2(__uint_as_float(lo[4 * i4]) + b0, __uint_as_float(lo[4 * i4 + 1]) + b0);
-              m[1] = pack_bf16x2(__uint_as_float(lo[4 * i4 + 2]) + b1, __uint_as_float(lo[4 * i4 + 3]) + b1);
-              m[2] = pack_bf16x2(__uint_as_float(hi[4 * i4]) + b2, __uint_as_float(hi[4 * i4 + 1]) + b2);
-              m[3] = pack_bf16x2(__uint_as_float(hi[4 * i4 + 2]) + b3, __uint_as_float(hi[4 * i4 + 3]) + b3);
+              const uint32_t *vl = lo + 4 * i4, *vh = hi + 4 * i4;
+              const float2 y[4] = {add2(vl, b0), add2(vl + 2, b1), add2(vh, b2), add2(vh + 2, b3)};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) m[j] = pack_bf16x2(y[j].x, y[j].y);
               store_transposed(put, m);
               __syncwarp();
               const uint4 w = *reinterpret_cast<const uint4*>(get);
@@ -1022,14 +1032,18 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
           tc_wait_ld();
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            float y = __uint_as_float(r[j]) + b0;
+            const float y = __uint_as_float(r[j]) + b0;
+            uint32_t bits;
             if constexpr (kSwiglu) {
               // both lanes of a pair compute the output, the even one stores it
               const float theirs = __shfl_xor_sync(0xffffffffu, y, 1);
-              y = swiglu((lane & 1) ? theirs : y, (lane & 1) ? y : theirs, scale, a.limit);
+              const float g = (lane & 1) ? theirs : y, u = (lane & 1) ? y : theirs;
+              bits = swiglu2(g, g, u, u, scale2, a.limit);
+            } else {
+              bits = pack_bf16x2(y, 0.0f);
             }
             if (mine && c + j < tl.n && !(kSwiglu && (lane & 1)))
-              out[static_cast<long long>(c + j) * a.n_out] = static_cast<uint16_t>(pack_bf16x2(y, 0.0f) & 0xFFFFu);
+              out[static_cast<long long>(c + j) * a.n_out] = static_cast<uint16_t>(bits & 0xFFFFu);
           }
         }
       }
