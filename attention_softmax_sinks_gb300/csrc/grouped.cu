@@ -45,7 +45,7 @@
 //   many rows   bf16: the tensor cores and the power limit; 32768 tokens 2.6 - 2.8 ms, 3.1 back to
 //               back (1400 - 1650 TFLOP/s), one group of 32768 rows x 4096 -> 2880 0.42 ms (1830).
 //               MXFP4: a stage's way round the ring (free, filled, reported, multiplied) beside an
-//               epilogue that competes for issue slots; 1.10 ms (4.0 PFLOP/s), consecutive rows
+//               epilogue that competes for issue slots; 1.08 ms (4.0 PFLOP/s), consecutive rows
 //               0.93, one group 0.138 (5.6).  With nothing loaded the 0.93 stay, without the
 //               epilogue as well 0.70, without the MMAs as well 0.47.
 #include <atomic>
