@@ -11,7 +11,7 @@
 //
 // A tile is 128 features by up to `cap` rows; with more than a few rows per expert two CTAs on
 // neighbouring SMs work as a pair (cta_group::2: one MMA of 256 features on both, each CTA
-// staging half of the rows).  Persistent kernel, one CTA per SM, 17 warps:
+// staging half of the rows).  Persistent kernel, one CTA per SM, 17 warps (21 in bf16):
 //   warp 0        the weights of a ring stage (boxes of 128 features x 128 bytes of K, 128-byte
 //                 swizzle) when it is free
 //   warp 1        TMEM owner and MMA issuer (one elected thread): 32 bytes of K per MMA
@@ -24,8 +24,9 @@
 //                 stores, 64 consecutive bytes per row and warp (32 with SwiGLU, whose gate and
 //                 up features are neighbouring lanes)
 //   warps 12..15  the rows: consecutive ones in TMA boxes, in turns of a stage; rows gathered by
-//                 their indices with 16-byte asynchronous copies (TMA gathers of four rows cost
-//                 their warp about 90 cycles each: 32768 tokens took 5.3 ms that way, 2.6 this way)
+//                 their indices (bf16: warps 17..20 as well) with 16-byte asynchronous copies (TMA
+//                 gathers of four rows cost their warp about 90 cycles each: 32768 tokens took
+//                 5.3 ms that way, 2.6 this way)
 // What a warp does per stage it does with uniform control flow and one elected lane, so that
 // descriptors and addresses stay in uniform registers (MMAs from a divergent branch: 125 cycles
 // each to issue, twice what they take).
@@ -42,7 +43,7 @@
 //   few rows    the weights' way from memory.  61 tokens 0.51 ms in bf16 (7.0 TB/s), 0.15 ms in
 //               MXFP4 (6.5 TB/s); 1 token 25.5 us and 15 us, of which about 6 are launch, first
 //               loads and the last tile's end.
-//   many rows   bf16: the tensor cores and the power limit; 32768 tokens 2.6 - 2.8 ms, 3.1 back to
+//   many rows   bf16: the tensor cores and the power limit; 32768 tokens 2.6 - 2.8 ms, 3.0 back to
 //               back (1400 - 1650 TFLOP/s), one group of 32768 rows x 4096 -> 2880 0.42 ms (1830).
 //               MXFP4: a stage's way round the ring (free, filled, reported, multiplied) beside an
 //               epilogue that competes for issue slots; 1.08 ms (4.0 PFLOP/s), consecutive rows
@@ -68,7 +69,7 @@ constexpr int kRowWarps = 4;
 constexpr int kTurns = kRowWarps;
 constexpr int kReportTurns = 2;
 constexpr int kReportWarp1 = kRowWarp0 + kRowWarps;
-constexpr int kThreads = 32 * (kReportWarp1 + 1);
+constexpr int kGatherWarp1 = kReportWarp1 + 1;  // the first of the warps that help with gathered rows
 constexpr int kProducers = 1 + kTurns + kReportTurns;  // warps: weights, rows, reports
 constexpr int kMaxStages = 16;
 constexpr int kMaxSingleRows = 64;  // rows of a single CTA's tile
@@ -85,6 +86,11 @@ struct GrpCfg {
   static constexpr int kStageK = kFp4 ? 256 : 64;
   static constexpr int kSfBytes = kFp4 ? 2 * 3 * kSfBlock : 0;  // per 128 values of K: a block of weights, two of rows
   static constexpr int kSfCols = 24;
+  // Warps that copy gathered rows: a warp spends about 100 cycles on each of its copies of a stage,
+  // so more of them fill it sooner (32768 tokens up, back to back: bf16 3.09 ms with four, 3.02 with
+  // eight), but they take issue slots, which MXFP4's short stages miss (1.09 ms, 1.19).
+  static constexpr int kGatherWarps = kFp4 ? kRowWarps : 2 * kRowWarps;
+  static constexpr int kThreads = 32 * (kGatherWarp1 + kGatherWarps - kRowWarps);
   static constexpr int kTmemCols = 512;
   static_assert(2 * kRows + (kFp4 ? 2 * kSfCols : 0) <= kTmemCols, "TMEM holds 512 columns");
 };
@@ -447,7 +453,7 @@ __device__ __forceinline__ uint32_t swiglu2(float g0, float g1, float u0, float 
 }
 
 template <bool kFp4, bool kSwiglu, bool kPair>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(GrpCfg<kFp4>::kThreads, 1)
 grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                const __grid_constant__ CUtensorMap wsmap, const __grid_constant__ CUtensorMap xsmap,
                const GroupedArgs a) {
@@ -490,7 +496,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
     }
     for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(smem_u32(&sb.full[s]), kCtas * producers);
-      mbar_init(smem_u32(&sb.landed[s]), 32 * kRowWarps);
+      mbar_init(smem_u32(&sb.landed[s]), 32 * C::kGatherWarps);
       mbar_init(smem_u32(&sb.empty[s]), 1);
     }
     for (int r = 0; kFp4 && r < kMaxRawSlots; ++r) {
@@ -833,29 +839,30 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
       sb.issued[1 + kTurns + turn] = done;
     }
   } else if (warp >= kRowWarp0) {
-    const int wr = warp - kRowWarp0;
-    constexpr int kSteps = kPair ? C::kRows / kGrain : kMaxSingleRows / 16;
+    const int wr = kFp4 || warp < kReportWarp1 ? warp - kRowWarp0 : kRowWarps + warp - kGatherWarp1;
+    constexpr int kStepRows = 4 * C::kGatherWarps;  // rows that one copy by each thread brings
+    constexpr int kSteps = ((kPair ? C::kRows / 2 : kMaxSingleRows) + kStepRows - 1) / kStepRows;
     RingPos p;
     int g = 0, done = 0;  // stages of earlier tiles; one more than the last stage reported
     bool ok = true;
     if (gather) {
-      // Gathered rows: eight threads per row copy its 128 bytes, 16 rows at a time, into the
-      // places of the 128-byte swizzle.
-      const int tid = threadIdx.x - 32 * kRowWarp0;
+      // Gathered rows: eight threads per row copy its 128 bytes into the places of the 128-byte swizzle.
+      const int tid = 32 * wr + lane;
       const int chunk = tid & 7, row0 = tid >> 3;
       const long long row_bytes = kFp4 ? a.K / 2 : 2LL * a.K;
       const uint32_t dst0 = x_part + row0 * kStageKBytes + ((chunk ^ (row0 & 7)) << 4);
       for (int t = t_first; t < tiles_total && ok; t += t_step) {
         const Tile tl = find_tile(sb, a, t, kCtas * width, lane);
         const int half = (tl.n + kGrain - 1) / kGrain * 16;  // rows that this CTA stages
-        const int steps = half >> 4;
+        const int steps = (half + kStepRows - 1) / kStepRows;
+        auto mine = [&](int i) { return i < steps && (kStepRows == 16 || kStepRows * i + row0 < half); };
         const uint8_t* src[kSteps];
         uint32_t has = 0;  // zeros behind the tile's last row: no request
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
-          const int r = rank * half + 16 * i + row0;
+          const int r = rank * half + kStepRows * i + row0;
           src[i] = a.x;
-          if (i < steps && r < tl.n) {
+          if (mine(i) && r < tl.n) {
             int id = __ldg(a.row_token + tl.r0 + r);
             if (id < 0 || id >= a.x_rows) {
               raise_status(a.status, kStatusBadLen);
@@ -877,16 +884,16 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
             const uint32_t dst = ring + p.stage * stage_size + dst0 + u * stage_rows * kStageKBytes;
 #pragma unroll
             for (int i = 0; i < kSteps; ++i)
-              if (i < steps) {
+              if (mine(i)) {
                 const bool read = data && (has >> i & 1);
-                copy_async16(dst + i * 16 * kStageKBytes, src[i] + (read ? at : 0), read ? 16 : 0);
+                copy_async16(dst + i * kStepRows * kStageKBytes, src[i] + (read ? at : 0), read ? 16 : 0);
               }
           }
           copy_async_arrive(smem_u32(&sb.landed[p.stage]));
         }
       }
       copy_async_wait_all();
-    } else {
+    } else if (kFp4 || wr < kRowWarps) {
       // Boxes of rows, whole stages in turns: a report to the leading CTA's barrier keeps its warp
       // about 220 cycles, a copy's issue 100 and more.
       constexpr int kBox = kPair ? C::kRows / 4 : kBoxRows;
@@ -927,7 +934,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
     }
     if (lane == 0) {
       if (!ok) raise_status(a.status, kStatusTimeout);
-      sb.issued[1 + wr] = done;
+      if (kFp4 || wr < kTurns) sb.issued[1 + wr] = done;
     }
   } else if (warp >= kEpiWarp0) {
     const int half = (warp - kEpiWarp0) >> 2;  // the two warps of a lane quarter take turns of 32 columns
@@ -1142,7 +1149,7 @@ cudaError_t launch_grouped_t(const GroupedMaps& m, const GroupedArgs& a, int sms
   const int slots = sms / kCtas;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((most < slots ? most : slots) * kCtas));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(GrpCfg<kFp4>::kThreads);
   cfg.dynamicSmemBytes = smem_bytes<kFp4, kPair>();
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
