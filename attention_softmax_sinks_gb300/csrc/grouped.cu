@@ -448,7 +448,8 @@ __device__ __forceinline__ uint32_t swiglu2(float g0, float g1, float u0, float 
   const float2 x = f2_unpack(f2_mul(g, scale2));
   const float2 d = f2_unpack(f2_add(f2(ex2(x.x), ex2(x.y)), f2(1.0f, 1.0f)));
   const uint64_t t = f2_mul(g, f2(rcp_ftz(d.x), rcp_ftz(d.y)));
-  const float2 y = f2_unpack(f2_fma(t, u, t));
+  // not t u + t, which is NaN for an infinite t and u <= 0
+  const float2 y = f2_unpack(f2_mul(t, f2_add(u, f2(1.0f, 1.0f))));
   return pack_bf16x2(y.x, y.y);
 }
 
