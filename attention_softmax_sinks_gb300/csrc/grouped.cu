@@ -438,14 +438,15 @@ __device__ __forceinline__ float rcp_ftz(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// Two of g sigmoid(alpha g) (u + 1) with clamped g and u; scale2 = -alpha log2(e), twice.  The
-// epilogue shares the issue slots with the warps that keep the ring turning, so its instructions
+// Two of g sigmoid(alpha g) (u + 1) with clamped g and u; minus_alpha2 = -alpha, twice.  The product
+// with log2(e) follows that with g: alpha log2(e) may not fit into fp32, and would make NaN of a
+// gate of 0.  The epilogue shares the issue slots with the warps that keep the ring turning, so its instructions
 // count: packed arithmetic, and results of 2^x and of the reciprocal below 2^-126 taken as 0, which
 // saves their rescaling.
-__device__ __forceinline__ uint32_t swiglu2(float g0, float g1, float u0, float u1, uint64_t scale2, float limit) {
+__device__ __forceinline__ uint32_t swiglu2(float g0, float g1, float u0, float u1, uint64_t minus_alpha2, float limit) {
   const uint64_t g = f2(min_nan(g0, limit), min_nan(g1, limit));
   const uint64_t u = f2(max_nan(min_nan(u0, limit), -limit), max_nan(min_nan(u1, limit), -limit));
-  const float2 x = f2_unpack(f2_mul(g, scale2));
+  const float2 x = f2_unpack(f2_mul(f2_mul(g, minus_alpha2), f2(1.4426950408889634f, 1.4426950408889634f)));
   const float2 d = f2_unpack(f2_add(f2(ex2(x.x), ex2(x.y)), f2(1.0f, 1.0f)));
   const uint64_t t = f2_mul(g, f2(rcp_ftz(d.x), rcp_ftz(d.y)));
   // not t u + t, which is NaN for an infinite t and u <= 0
@@ -953,9 +954,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
                                  : patch0 + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
     const uint8_t* get = kSwiglu ? patch + (lane >> 1) * 32 + (((lane & 1) ^ ((lane >> 3) & 1)) << 4)
                                  : patch + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
-    // finite, so that a gate of 0 stays one
-    const float scale = fminf(fmaxf(-1.4426950408889634f * a.alpha, -3.0e38f), 3.0e38f);
-    [[maybe_unused]] const uint64_t scale2 = f2(scale, scale);
+    [[maybe_unused]] const uint64_t minus_alpha2 = f2(-a.alpha, -a.alpha);
     auto add2 = [](const uint32_t* v, float b) {  // two accumulators of one feature and its bias
       return f2_unpack(f2_add(f2(__uint_as_float(v[0]), __uint_as_float(v[1])), f2(b, b)));
     };
@@ -996,7 +995,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
                 const float2 l = add2(v, (j & 1) ? b2 : b0), h = add2(v + 2, (j & 1) ? b3 : b1);
                 const float t0 = __shfl_xor_sync(0xffffffffu, odd ? l.x : h.x, 4);
                 const float t1 = __shfl_xor_sync(0xffffffffu, odd ? l.y : h.y, 4);
-                m[j] = swiglu2(odd ? t0 : l.x, odd ? t1 : l.y, odd ? h.x : t0, odd ? h.y : t1, scale2, a.limit);
+                m[j] = swiglu2(odd ? t0 : l.x, odd ? t1 : l.y, odd ? h.x : t0, odd ? h.y : t1, minus_alpha2, a.limit);
               }
               store_transposed(put, m);
               __syncwarp();
@@ -1046,7 +1045,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
               // both lanes of a pair compute the output, the even one stores it
               const float theirs = __shfl_xor_sync(0xffffffffu, y, 1);
               const float g = (lane & 1) ? theirs : y, u = (lane & 1) ? y : theirs;
-              bits = swiglu2(g, g, u, u, scale2, a.limit);
+              bits = swiglu2(g, g, u, u, minus_alpha2, a.limit);
             } else {
               bits = pack_bf16x2(y, 0.0f);
             }

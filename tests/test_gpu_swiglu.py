@@ -78,3 +78,16 @@ def test_infinite_gates_and_ups(mx, rows, wide):
         _check(got, ref, g, u, alpha)
     got, ref, g, u = _activation(sa, [INF], [0.0, -0.5, -2.0, -1.0], 1.702, INF, mx, rows, wide)
     assert got[0, :3].tolist() == [INF, INF, -INF] and np.isnan(got[0, 3])
+
+
+@pytest.mark.parametrize("mx,rows,wide", FORMS)
+def test_alpha_at_the_end_of_its_range(mx, rows, wide):
+    """alpha log2(e) does not fit into fp32 although alpha does: gates so small that alpha g is
+    around 1 still see their sigmoid, and a gate of 0 gives 0."""
+    sa = require_gpu()
+    tiny = 2.0 ** -126
+    gates = [0.0, -0.0, tiny, -tiny, 1.5 * tiny, -1.5 * tiny, 8 * tiny, -4 * tiny, 1.0, -1.0]
+    ups = [2.0 ** 90, -2.0 ** 90, 1.0]
+    for alpha in (3.4e38, -3.4e38, 2.3e38, 2.0e38, 1.0):
+        got, ref, g, u = _activation(sa, gates, ups, np.float32(alpha).item(), INF, mx, rows, wide)
+        _check(got, ref, g, u, alpha)
