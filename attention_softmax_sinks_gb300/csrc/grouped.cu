@@ -440,9 +440,10 @@ __device__ __forceinline__ float rcp_ftz(float x) {
 }
 // Two of g sigmoid(alpha g) (u + 1) with clamped g and u; minus_alpha2 = -alpha, twice.  The product
 // with log2(e) follows that with g: alpha log2(e) may not fit into fp32, and would make NaN of a
-// gate of 0.  The epilogue shares the issue slots with the warps that keep the ring turning, so its instructions
-// count: packed arithmetic, and results of 2^x and of the reciprocal below 2^-126 taken as 0, which
-// saves their rescaling.
+// gate of 0.  The epilogue shares the issue slots with the warps that keep the ring turning, so its
+// instructions count: packed arithmetic, and results of 2^x and of the reciprocal below 2^-126 taken
+// as 0, which saves their rescaling.  A sigmoid below 2^-126 is one of these: |g (u + 1)| 2^-126 of
+// the result at most.
 __device__ __forceinline__ uint32_t swiglu2(float g0, float g1, float u0, float u1, uint64_t minus_alpha2, float limit) {
   const uint64_t g = f2(min_nan(g0, limit), min_nan(g1, limit));
   const uint64_t u = f2(max_nan(min_nan(u0, limit), -limit), max_nan(min_nan(u1, limit), -limit));

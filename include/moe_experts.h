@@ -90,7 +90,9 @@ sa_status grouped_linear_bias(const void* x, const void* w, const void* bias,
  *     out[r, i] = g * sigmoid(alpha * g) * (u + 1)
  *
  *  out bf16 [rows, n / 2]; n even; alpha finite; limit > 0 (+infinity: no
- *  clamp).  Everything else as for grouped_linear_bias.
+ *  clamp).  A sigmoid below 2^-126 counts as 0 (with alpha = 1.702 that of
+ *  gates below -51); otherwise infinities and NaN are those of the formula.
+ *  Everything else as for grouped_linear_bias.
  */
 sa_status grouped_linear_swiglu(const void* x, const void* w, const void* bias,
                                 const int32_t* expert_offsets, const int32_t* row_token,

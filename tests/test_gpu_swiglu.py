@@ -81,6 +81,18 @@ def test_infinite_gates_and_ups(mx, rows, wide):
 
 
 @pytest.mark.parametrize("mx,rows,wide", FORMS)
+def test_sigmoids_below_the_range_of_fp32(mx, rows, wide):
+    """Large negative gates under small and ordinary alpha: what is dropped stays below
+    |g (u + 1)| 2^-126, whatever alpha is."""
+    sa = require_gpu()
+    ups = [0.0, 1.0, -1.0, -3.0, 6.0]
+    for alpha, gates in ((1e-30, [-8.8e31, -8.0e31, -1e32, -3e30, 1e31]), (1e-28, [-1e30, -8.6e29, -9e29, 1e30]),
+                         (1.702, [-40.0, -51.0, -52.0, -60.0, -88.0, -300.0, -1e30]), (-0.25, [300.0, 340.0, 360.0, 1e4])):
+        got, ref, g, u = _activation(sa, gates, ups, alpha, INF, mx, rows, wide)
+        _check(got, ref, g, u, alpha)
+
+
+@pytest.mark.parametrize("mx,rows,wide", FORMS)
 def test_alpha_at_the_end_of_its_range(mx, rows, wide):
     """alpha log2(e) does not fit into fp32 although alpha does: gates so small that alpha g is
     around 1 still see their sigmoid, and a gate of 0 gives 0."""
