@@ -126,8 +126,6 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_rows_kernel(const Grou
   }
   if (lane == 31 && warp < kMaxExperts / 32) scan[warp] = incl;
   __syncthreads();
-  // this CTA has its sums (used above, so read): no CTA may leave before all have
-  if (cluster > 1) cluster_arrive_relaxed();
   if (threadIdx.x < kMaxExperts) {
     int base = 0;
     for (int w = 0; w < warp; ++w) base += scan[w];
@@ -141,6 +139,10 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_rows_kernel(const Grou
     for (int w = 0; w < kGroupWarps; ++w) cnt[w][threadIdx.x] += off + before;
   }
   __syncthreads();
+  // Both sums of the other CTAs are in this one's shared memory now, so they have been read: no CTA
+  // may leave before that is so of all.  (An arrival does not wait for loads under way; `before` has
+  // its first use just above.)
+  if (cluster > 1) cluster_arrive_relaxed();
 
   const unsigned below = (1u << lane) - 1u;
   for (int p0 = begin; p0 < end; p0 += 32 * kBatch) {
@@ -163,6 +165,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_rows_kernel(const Grou
   for (long long r = total_rows + static_cast<long long>(blockIdx.x) * kGroupThreads + threadIdx.x; r < a.pairs;
        r += static_cast<long long>(gridDim.x) * kGroupThreads)
     a.row_token[r] = -1;
+  __syncwarp();
   if (cluster > 1) cluster_wait();
 }
 
