@@ -495,6 +495,7 @@ GPT_OSS_SWIGLU = dict(alpha=1.702, limit=7.0)
 
 
 _C_INT = 2 ** 31 - 1
+_MAX_EXPERTS = 256  # of moe_experts.h
 
 
 def _c_int(v, name):
@@ -558,7 +559,8 @@ def moe_group_rows(topk_idx, num_experts: int, expert_offsets=None, row_token=No
     t, k = topk_idx.shape
     e = _c_int(int(num_experts), "num_experts")
     dev = topk_idx.device
-    expert_offsets = (_new(max(e, 0) + 1, torch.int32, dev, stream) if expert_offsets is None
+    # no memory for a number of experts that the call refuses
+    expert_offsets = (_new(min(max(e, 0), _MAX_EXPERTS) + 1, torch.int32, dev, stream) if expert_offsets is None
                       else _out(expert_offsets, "expert_offsets", torch.int32, (e + 1,), di))
     row_token = (_new(t * k, torch.int32, dev, stream) if row_token is None
                  else _out(row_token, "row_token", torch.int32, (t * k,), di))

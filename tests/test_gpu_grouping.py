@@ -40,3 +40,18 @@ def test_ranges_of_clusters_that_are_empty_or_short(pairs, e):
         for out in outs:
             assert all(torch.equal(g, r) for g, r in zip(out, ref))
     assert sa.sink_attn_device_status(True) == 0
+
+
+def test_refused_numbers_of_experts_allocate_nothing():
+    """An argument that the library refuses is refused before memory is asked for in its size."""
+    sa = require_gpu()
+    idx = torch.zeros((4, 2), dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    for e in (257, 2 ** 20, 2 ** 31 - 1, 0, -1, -2 ** 31 + 1):
+        with pytest.raises(sa.SinkAttnError):
+            sa.moe_group_rows(idx, e)
+    assert torch.cuda.max_memory_allocated() - before < 2 ** 16
+    offsets, _, _ = sa.moe_group_rows(idx, 256)
+    assert offsets.tolist() == [0] + [8] * 256
