@@ -661,14 +661,12 @@ def mxfp4_quantize(x, codes=None, scales=None, stream=None):
 def mxfp4_dequantize(codes, scales, out=None, stream=None):
     """The bf16 values [..., K] of MXFP4 codes [..., K / 2] and scales (as mxfp4_quantize
     returns them)."""
-    if not isinstance(codes, torch.Tensor):
-        raise TypeError("codes must be a CUDA tensor")
+    _dev(codes, "codes", torch.uint8)
     if codes.dim() < 1:
         raise ValueError("codes must have at least one dimension")
-    half = codes.shape[-1]
-    k, lead = 2 * half, codes.shape[:-1]
-    di = _inputs(("codes", codes, torch.uint8, (*lead, half)),
-                 ("scales", scales, torch.uint8, (*lead, mxfp4_scale_columns(k))))
+    # as mxfp4_quantize: K passes through a C int, the number of rows does not
+    di, k, lead = codes.get_device(), _c_int(2 * codes.shape[-1], "K"), codes.shape[:-1]
+    _out(scales, "scales", torch.uint8, (*lead, mxfp4_scale_columns(k)), di)
     out = (_new((*lead, k), torch.bfloat16, codes.device, stream) if out is None
            else _out(out, "out", torch.bfloat16, (*lead, k), di))
     st = _call(load_library().mxfp4_dequantize, di, stream, codes.data_ptr(), scales.data_ptr(), lead.numel(), k,
