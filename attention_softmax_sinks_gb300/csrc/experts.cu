@@ -19,9 +19,11 @@ namespace {
 // cluster, and each segment into 8 ranges, one per CTA.  Every cluster counts all pairs (its
 // CTA r counts segment r), so it knows what the segments before its own hold without waiting
 // for another cluster; then each CTA counts its own range per warp, and the ranges' counts are
-// exchanged through distributed shared memory.  The scattered 4-byte writes of row_token, 32
-// sectors per warp, are what takes the time on few SMs: 131072 pairs took 20 us on one cluster,
-// 10 on eight; 256 pairs take 4, most of it the launch.
+// exchanged through distributed shared memory.  131072 pairs take 10 us (20 on one cluster), bound
+// by latency: 6.8 until the counts are exchanged (launch, two passes of counting in shared memory,
+// the clusters' barrier), 3.1 for the rows, of which 0.3 are the scattered 4-byte writes of row_token
+// and 0.6 the rounds of a batch that have no pairs (a warp has 64, a batch 256).  256 pairs take 4,
+// most of it the launch.
 constexpr int kGroupThreads = 1024;
 constexpr int kGroupWarps = kGroupThreads / 32;
 constexpr int kGroupCluster = 8;

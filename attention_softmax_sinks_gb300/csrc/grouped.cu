@@ -6,8 +6,10 @@
 // Orientation.  The group sizes are ragged and often tiny (a decode step gives an expert one
 // or two rows), while the features are many and fixed, so the weights are the A operand (M =
 // 128 features) and the rows the B operand, whose N is chosen per tile: a tile of n rows
-// issues MMAs of N = n rounded up to 16 and loads only those rows.  Transposed this way no
-// tensor work is padded beyond 16 rows, and one kernel serves one row and thousands.
+// issues MMAs of N = n rounded up to 16 (32 in a pair of CTAs, below).  Transposed this way one
+// kernel serves one row and thousands without padding rows to an M of 128.  Gathered rows are
+// loaded one by one; consecutive ones in whole boxes, of 16 rows in a single CTA and of 64 (bf16)
+// or 56 (MXFP4) in each CTA of a pair, with the scales of 112 rows.
 //
 // A tile is 128 features by up to `cap` rows; with more than a few rows per expert two CTAs on
 // neighbouring SMs work as a pair (cta_group::2: one MMA of 256 features on both, each CTA
@@ -46,8 +48,8 @@
 //   many rows   bf16: the tensor cores and the power limit; 32768 tokens 2.6 - 2.8 ms, 3.0 back to
 //               back (1400 - 1650 TFLOP/s), one group of 32768 rows x 4096 -> 2880 0.42 ms (1830).
 //               MXFP4: a stage's way round the ring (free, filled, reported, multiplied) beside an
-//               epilogue that competes for issue slots; 1.08 ms (4.0 PFLOP/s), consecutive rows
-//               0.93, one group 0.138 (5.6).  With nothing loaded the 0.93 stay, without the
+//               epilogue that competes for issue slots; 1.07 - 1.09 ms (4.0 PFLOP/s), consecutive rows
+//               0.88 - 0.93, one group 0.138 (5.6).  With nothing loaded the 0.93 stay, without the
 //               epilogue as well 0.70, without the MMAs as well 0.47.
 #include <atomic>
 #include <cstdint>
@@ -1027,7 +1029,10 @@ grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__
           }
         }
       } else {
-        // any N and any address: a thread per feature, 2 bytes at a time
+        // Any N and any address: a thread per feature, 2 bytes at a time.  With few rows that costs
+        // nothing (61 tokens up: within 3 %), with many what the epilogue's issue slots do: 32768
+        // gathered tokens up, 5758 features beside 5760, SwiGLU 1.36 / 1.07 ms in MXFP4 and 2.79 / 2.54
+        // in bf16, without it 1.16 / 1.10 and 2.64 / 2.59.
         const bool mine = lane < most;
         const float b0 = bias_of(lane);
         out += kSwiglu ? lane >> 1 : lane;
@@ -1181,6 +1186,9 @@ void grouped_plan(GroupedArgs& a, bool mxfp4, int sms) {
   // and keep more weight bytes in flight.  (32 equal experts, 2880 -> 5760, us single / pair:
   // 40 rows bf16 162 / 167, MXFP4 55 / 54; 96 rows, two row tiles of single CTAs, 197 / 172 and
   // 89 / 57.  Groups of uneven size pass 64 rows, a single CTA's most, before their average does.)
+  // The number of tiles is not part of the rule, so few experts leave SMs idle: one matrix of 2880 ->
+  // 5120 in MXFP4 makes 20 pair tiles of 49 to 224 rows, 40 SMs' work (48 rows 9.3 us, 64 rows 10.9,
+  // 224 rows 12.3, 1024 rows 17.6).
   a.pair = a.rows > 48LL * a.num_experts;
   a.cap = a.pair ? (mxfp4 ? GrpCfg<true>::kRows : GrpCfg<false>::kRows) : a.rows > 2LL * a.num_experts ? kMaxSingleRows : 16;
   a.width = kFeat;
