@@ -27,7 +27,7 @@ __all__ = [
     "sink_attn_prefill_paged_qkv", "sink_attn_decode_qkv", "moe_group_rows", "moe_combine",
     "grouped_linear_bias", "grouped_linear_swiglu", "mxfp4_quantize", "mxfp4_dequantize",
     "mxfp4_linear_bias", "grouped_mxfp4_linear_bias", "grouped_mxfp4_linear_swiglu",
-    "mxfp4_scale_columns", "GPT_OSS_SWIGLU",
+    "mxfp4_scale_columns", "GPT_OSS_SWIGLU", "sink_attn_decode_shared", "sink_attn_decode_shared_splits",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -44,6 +44,7 @@ EXPORTED_SYMBOLS = (
     "sink_attn_decode_qkv", "moe_group_rows", "moe_combine",
     "grouped_linear_bias", "grouped_linear_swiglu", "mxfp4_quantize", "mxfp4_dequantize",
     "mxfp4_linear_bias", "grouped_mxfp4_linear_bias", "grouped_mxfp4_linear_swiglu",
+    "sink_attn_decode_shared", "sink_attn_decode_shared_splits",
 )
 
 _p, _i, _f, _d, _ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_double, ctypes.c_longlong
@@ -83,6 +84,9 @@ _SIGNATURES = {
     "mxfp4_dequantize": (_i, [_p, _p, _ll, _i, _p, _p]),
     "mxfp4_linear_bias": (_i, [_p, _p, _p, _p, _p, _i, _i, _i, _p, _p]),
     "grouped_mxfp4_linear_bias": (_i, [_p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _p, _p]),
+    "sink_attn_decode_shared": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _i, _f, _i, _i,
+                                     _p, _p, _p, _p, _p]),
+    "sink_attn_decode_shared_splits": (None, [_i, _i, _i, _i, _i, _i, _i, _p, _p]),
     "grouped_mxfp4_linear_swiglu": (_i, [_p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _f, _f, _p, _p]),
 }
 
@@ -326,6 +330,75 @@ def sink_attn_merge(partial_o, partial_lse, out=None, lse=None, return_lse: bool
                _ptr(partial_o), _ptr(partial_lse), b, s, h, d, _ptr(out), _ptr(lse))
     _check(st, "sink_attn_merge")
     return out, lse
+
+
+def sink_attn_decode_shared(q, paged_k, paged_v, page_table, kv_lens, sinks, group_offsets, shared_pages,
+                            max_shared_pages: int, sm_scale: float, splits=None, workspace=None, out=None,
+                            lse=None, return_lse: bool = True, stream=None):
+    """sink_attn_decode of a batch whose sequences share prompts: the pages that begin several
+    sequences' page tables are read once for all of them.
+
+    q [B, Hq, 64] bf16, paged_k/v [P, Hkv, 16, 64] bf16, page_table [B, max_pages] int32,
+    kv_lens [B] int32 (whole sequences), sinks [Hq] fp32.  group_offsets [G + 1] int32: group g
+    is sequences [group_offsets[g], group_offsets[g + 1]); shared_pages [G] int32: the pages that
+    begin the page tables of all its sequences, at most max_shared_pages.
+    splits: (shared, own) along the keys, default sink_attn_decode_shared_splits.  workspace:
+    (partial_o [B, shared + own, Hq, 64], partial_lse [B, shared + own, Hq]) fp32, allocated when
+    not given.  Returns (out [B, Hq, 64] bf16, lse [B, Hq] fp32 or None)."""
+    b, hq, d = _shape(q, "q", 3)
+    num_pages, hkv, page_size, kd = _shape(paged_k, "paged_k", 4)
+    groups = _shape(shared_pages, "shared_pages", 1)[0]
+    di = _inputs(("q", q, torch.bfloat16, (b, hq, d)), ("paged_k", paged_k, torch.bfloat16, (num_pages, hkv, page_size, d)),
+                 ("paged_v", paged_v, torch.bfloat16, (num_pages, hkv, page_size, d)),
+                 ("page_table", page_table, torch.int32, 2), ("kv_lens", kv_lens, torch.int32, (b,)),
+                 ("sinks", sinks, torch.float32, (hq,)), ("group_offsets", group_offsets, torch.int32, (groups + 1,)),
+                 ("shared_pages", shared_pages, torch.int32, (groups,)))
+    if page_table.shape[0] != b:
+        raise ValueError(f"page_table must have {b} rows, got {tuple(page_table.shape)}")
+    max_pages, dev = page_table.shape[1], q.device
+    most = _c_int(int(max_shared_pages), "max_shared_pages")
+    if splits is None:
+        splits = sink_attn_decode_shared_splits(b, groups, hq, hkv, most, max_pages, _sm_count(di))
+    ss, so = (_c_int(int(v), "splits") for v in splits)
+    if not (1 <= ss <= 255 and 1 <= so <= 256 - ss):  # no memory for what the call refuses
+        raise ValueError(f"splits must be at least 1 each and at most 256 together, got {(ss, so)}")
+    if workspace is None:
+        partial_o = _new((b, ss + so, hq, d), torch.float32, dev, stream)
+        partial_lse = _new((b, ss + so, hq), torch.float32, dev, stream)
+    else:
+        partial_o = _out(workspace[0], "workspace[0]", torch.float32, (b, ss + so, hq, d), di)
+        partial_lse = _out(workspace[1], "workspace[1]", torch.float32, (b, ss + so, hq), di)
+    out = (_new((b, hq, d), torch.bfloat16, dev, stream) if out is None
+           else _out(out, "out", torch.bfloat16, (b, hq, d), di))
+    if lse is None and return_lse:
+        lse = _new((b, hq), torch.float32, dev, stream)
+    elif lse is not None:
+        _out(lse, "lse", torch.float32, (b, hq), di)
+    st = _call(load_library().sink_attn_decode_shared, di, stream, q.data_ptr(), paged_k.data_ptr(), paged_v.data_ptr(),
+               page_table.data_ptr(), kv_lens.data_ptr(), sinks.data_ptr(), group_offsets.data_ptr(),
+               shared_pages.data_ptr(), b, groups, hq, hkv, d, page_size, max_pages, num_pages, most, float(sm_scale),
+               ss, so, partial_o.data_ptr(), partial_lse.data_ptr(), out.data_ptr(), _ptr(lse))
+    _check(st, "sink_attn_decode_shared")
+    return out, lse
+
+
+_sms = {}
+
+
+def _sm_count(di):
+    """Multiprocessors of device ``di``."""
+    if di not in _sms:
+        _sms[di] = torch.cuda.get_device_properties(di).multi_processor_count
+    return _sms[di]
+
+
+def sink_attn_decode_shared_splits(batch: int, num_groups: int, num_qo_heads: int, num_kv_heads: int,
+                                   max_shared_pages: int, max_pages: int, num_sms: int = 0):
+    """(shared, own) split counts for sink_attn_decode_shared; num_sms 0: 152."""
+    s, o = ctypes.c_int(), ctypes.c_int()
+    load_library().sink_attn_decode_shared_splits(batch, num_groups, num_qo_heads, num_kv_heads, max_shared_pages,
+                                                  max_pages, num_sms, ctypes.byref(s), ctypes.byref(o))
+    return s.value, o.value
 
 
 def sink_attn_decode_splits(batch: int, num_kv_heads: int, max_kv_len: int, page_size: int = 16,

@@ -418,6 +418,30 @@ sa_status sink_attn_device_status(int clear) {
   return SA_OK;
 }
 
+void sink_attn_decode_shared_splits(int batch, int num_groups, int num_qo_heads, int num_kv_heads,
+                                    int max_shared_pages, int max_pages, int num_sms, int* shared_splits,
+                                    int* own_splits) {
+  int s = 1, o = 1;
+  if (batch > 0 && num_groups > 0 && num_kv_heads > 0 && num_qo_heads >= num_kv_heads && max_shared_pages >= 0 &&
+      max_pages > 0) {
+    if (num_sms <= 0) num_sms = 152;
+    // shared part: one CTA per SM at a time, so as many splits as fit one wave, at least one tile
+    // of 8 pages each; more than 24 cost more to merge than they gain
+    const long long tiles = (max_shared_pages + 7) / 8;
+    const long long units = sa::shared_row_tiles(batch, num_groups, num_qo_heads / num_kv_heads) * num_kv_heads;
+    long long n = num_sms / units;
+    if (n > tiles) n = tiles;
+    if (n > 24) n = 24;
+    s = n < 1 ? 1 : static_cast<int>(n);
+    // own part: three CTAs per SM, at least 16 pages each, at most 8 splits
+    const long long own_pages = max_pages > max_shared_pages ? max_pages - max_shared_pages : 1;
+    const long long own_units = static_cast<long long>(batch) * num_kv_heads;
+    while (o < 8 && own_units * o < 3LL * num_sms && own_pages / (2 * o) >= 16) o *= 2;
+  }
+  if (shared_splits) *shared_splits = s;
+  if (own_splits) *own_splits = o;
+}
+
 int sink_attn_decode_splits(int batch, int num_kv_heads, int max_kv_len, int page_size,
                             int num_sms) {
   if (batch <= 0 || num_kv_heads <= 0 || max_kv_len <= 0 || page_size <= 0) return 1;
@@ -521,6 +545,81 @@ sa_status sink_attn_decode_qkv(const void* qkv, const void* qkv_bias, const floa
   return decode_common(qkv, paged_k, paged_v, page_table, kv_lens, sinks, batch, num_qo_heads,
                        num_kv_heads, head_dim, page_size, max_pages, num_pages, sm_scale, num_splits,
                        out, lse, stream, rope);
+}
+
+sa_status sink_attn_decode_shared(const void* q, const void* paged_k, const void* paged_v,
+                                  const int32_t* page_table, const int32_t* kv_lens,
+                                  const float* sinks, const int32_t* group_offsets,
+                                  const int32_t* shared_pages, int batch, int num_groups,
+                                  int num_qo_heads, int num_kv_heads, int head_dim, int page_size,
+                                  int max_pages, int num_pages, int max_shared_pages,
+                                  float sm_scale, int shared_splits, int own_splits,
+                                  float* partial_o, float* partial_lse, void* out, float* lse,
+                                  cudaStream_t stream) {
+  if (batch < 0 || batch > 65535 || num_groups <= 0 || max_pages <= 0 || num_pages <= 0) return SA_ERR_SHAPE;
+  if (max_shared_pages < 0 || max_shared_pages > max_pages || max_pages > (1 << 26)) return SA_ERR_SHAPE;
+  if (shared_splits < 1 || own_splits < 1 || shared_splits > 256 || own_splits > 256 || shared_splits + own_splits > 256)
+    return SA_ERR_SHAPE;
+  if (sa_status s = check_heads(num_qo_heads, num_kv_heads, head_dim)) return s;
+  if (page_size != sa::kPageSize) return SA_ERR_UNSUPPORTED;
+  if (!good_scale(sm_scale)) return SA_ERR_SHAPE;
+  if (num_kv_heads > 65535) return SA_ERR_SHAPE;
+  // one row behind the cache still has to be a coordinate
+  if (static_cast<long long>(num_pages) * num_kv_heads * page_size >= (1LL << 31) - 16) return SA_ERR_SHAPE;
+  if (static_cast<long long>(batch) * num_qo_heads >= (1LL << 31)) return SA_ERR_SHAPE;
+  if (batch == 0) return SA_OK;
+  if (!q || !paged_k || !paged_v || !page_table || !kv_lens || !sinks || !group_offsets || !shared_pages ||
+      !partial_o || !partial_lse || !out)
+    return SA_ERR_NULL;
+  if (!aligned16(q) || !aligned16(paged_k) || !aligned16(paged_v) || !aligned16(out) || !aligned16(partial_o) ||
+      !aligned4(page_table) || !aligned4(kv_lens) || !aligned4(sinks) || !aligned4(group_offsets) ||
+      !aligned4(shared_pages) || !aligned4(partial_lse) || !aligned4(lse))
+    return SA_ERR_ALIGNMENT;
+  const int group = num_qo_heads / num_kv_heads;
+  if (sa::shared_row_tiles(batch, num_groups, group) > 65535) return SA_ERR_SHAPE;
+  unsigned* status = nullptr;
+  if (sa_status s = status_ptr(&status)) return s;
+  CUtensorMap km, vm;
+  if (sa_status s = map_pages(&km, paged_k, num_pages, num_kv_heads)) return s;
+  if (sa_status s = map_pages(&vm, paged_v, num_pages, num_kv_heads)) return s;
+  const sa::SharedPlan plan{group_offsets, shared_pages, num_groups, max_shared_pages, shared_splits, own_splits};
+  sa::SharedArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.page_table = page_table;
+  a.partial_o = partial_o;
+  a.partial_lse = partial_lse;
+  a.plan = plan;
+  a.batch = batch;
+  a.hq = num_qo_heads;
+  a.hkv = num_kv_heads;
+  a.group = group;
+  a.max_pages = max_pages;
+  a.num_pages = num_pages;
+  a.scale_log2 = sm_scale * kLog2e;
+  a.status = status;
+  a.timeout_ns = g_timeout_ns;
+  if (sa::launch_shared(km, vm, a, stream) != cudaSuccess) return SA_ERR_LAUNCH;
+  sa::DecodeArgs d{};
+  d.q = q;
+  d.page_table = page_table;
+  d.kv_lens = kv_lens;
+  d.sinks = sinks;
+  d.out = partial_o;
+  d.lse = partial_lse;
+  d.batch = batch;
+  d.hq = num_qo_heads;
+  d.hkv = num_kv_heads;
+  d.group = group;
+  d.max_pages = max_pages;
+  d.num_pages = num_pages;
+  d.num_splits = own_splits;
+  d.cluster = 1;
+  d.scale_log2 = a.scale_log2;
+  d.status = status;
+  d.timeout_ns = g_timeout_ns;
+  if (sa::launch_decode_own(km, vm, d, plan, stream) != cudaSuccess) return SA_ERR_LAUNCH;
+  const sa::MergeArgs m{partial_o, partial_lse, out, lse, batch, shared_splits + own_splits, num_qo_heads};
+  return sa::launch_merge(m, stream) == cudaSuccess ? SA_OK : SA_ERR_LAUNCH;
 }
 
 sa_status sink_attn_merge(const float* partial_o, const float* partial_lse, int batch,

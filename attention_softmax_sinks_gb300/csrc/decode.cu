@@ -35,6 +35,7 @@
 #include "internal.h"
 #include "ptx.cuh"
 #include "rope_math.cuh"
+#include "shared_args.h"
 
 namespace sa {
 namespace {
@@ -141,11 +142,30 @@ __device__ __noinline__ void cluster_combine(uint32_t recv, int csz, void* out_b
   }
 }
 
-template <int NT, bool kRope>
+// The sequence's own pages begin behind the ones that its group shares: their number, found in
+// the plan (groups are consecutive sequences).  A plan that breaks its bounds is reported.
+__device__ __noinline__ int own_first_page(const SharedPlan& plan, int b, int max_pages, unsigned* status) {
+  int lo = 0, hi = plan.num_groups;  // offsets[lo] <= b < offsets[hi], when the offsets are in order
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(plan.group_offsets + mid) <= b) lo = mid; else hi = mid;
+  }
+  const int pages = __ldg(plan.shared_pages + lo);
+  const bool good = __ldg(plan.group_offsets + lo) <= b && b < __ldg(plan.group_offsets + lo + 1) && pages >= 0 &&
+                    pages <= plan.max_shared_pages && pages <= max_pages;
+  if (!good && threadIdx.x == 0) raise_status(status, kStatusBadLen);
+  return good ? pages : 0;
+}
+
+// kShared: the own parts of a batch that shares prompts.  The pages before own_first_page are left
+// to the kernel launched before this one (shared.cu), which let this one start only when every
+// earlier kernel had completed: nothing is waited for here except, by the grid's last CTA at its
+// end, that kernel itself, so that what follows this grid follows both.
+template <int NT, bool kRope, bool kShared>
 __global__ void __launch_bounds__(kWarps * 32)
     sink_decode_kernel(const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap, const DecodeArgs a,
-                       const DecodeRopeArgs rope) {
+                       const DecodeRopeArgs rope, const SharedPlan plan) {
   static_assert(sizeof(MergeArea<NT>) <= kRingBytes, "the merge area must fit in the ring");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>(
@@ -165,13 +185,15 @@ __global__ void __launch_bounds__(kWarps * 32)
   // what is read before the wait below only chooses what to prefetch and which page-table
   // entries to read early (both are read again after the wait and checked).
   const int kvl = a.kv_lens[blockIdx.z];
+  int page0 = 0;  // first page of this kernel's range
+  if constexpr (kShared) page0 = own_first_page(plan, b, a.max_pages, a.status);
   if (lane == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(full_w + 8 * s, 1);
     fence_barrier_init();
     tma_prefetch_desc(&kmap);
     tma_prefetch_desc(&vmap);
     // While the kernel before this one finishes, ask L2 for this warp's first pages.
-    if (kvl > 0 && kvl <= a.max_pages * kPageSize) {
+    if (!kShared && kvl > 0 && kvl <= a.max_pages * kPageSize) {
       const int np = (kvl + kPageSize - 1) / kPageSize;
       const int ns = a.cluster > 1 ? a.cluster : a.num_splits;
       const int per = (np + ns - 1) / ns;
@@ -193,7 +215,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   // Launched with programmatic stream serialisation: the set-up above may overlap
   // the kernel before this one; apart from the prefetch hints above, every read of
   // an input comes after this wait.
-  pdl_wait_primary();
+  if constexpr (!kShared) pdl_wait_primary();
 
   const int cap = a.max_pages * kPageSize;
   const bool clustered = a.cluster > 1;  // splits of one (sequence, KV head) form a cluster
@@ -201,12 +223,14 @@ __global__ void __launch_bounds__(kWarps * 32)
   const int32_t* ptab = a.page_table + static_cast<size_t>(b) * a.max_pages;
   // this warp's pages for a sequence of kv tokens: p_begin + warp + j * kWarps, j < count
   auto warp_pages = [&](int kv, int& first, int& count) {
-    const int np = (kv + kPageSize - 1) / kPageSize;
+    int np = (kv + kPageSize - 1) / kPageSize;
+    if constexpr (kShared) np = max(np - page0, 0);
     const int per = (np + n_split - 1) / n_split;
     const int pb = min(split * per, np);
     const int pe = min(pb + per, np);
     first = pb + warp;
-    count = first < pe ? (pe - first + kWarps - 1) / kWarps : 0;
+    if constexpr (kShared) first += page0;
+    count = pb + warp < pe ? (pe - pb - warp + kWarps - 1) / kWarps : 0;
   };
   // Page ids, 32 of this warp's pages at a time: lane l of ids_cur holds the id of the
   // warp's page 32 w + l (window w holds the page being consumed) and ids_next those of
@@ -226,6 +250,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     if (threadIdx.x == 0) raise_status(a.status, kStatusBadLen);
     kv_len = kv_len < 0 ? 0 : cap;
   }
+  if (kShared && kv_len < page0 * kPageSize && threadIdx.x == 0) raise_status(a.status, kStatusBadLen);
   if (kv_len != kv_early) {
     warp_pages(kv_len, my_first, my_count);
     ids_cur = load_ids(0);
@@ -343,8 +368,10 @@ __global__ void __launch_bounds__(kWarps * 32)
       for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(sc[nt], a0, a1, a2, a3, qf[nt][kk][0], qf[nt][kk][1]);
     }
   };
-  // O^T += V^T P^T for the page in ring slot `slot` (64 dims x 8 heads per tile)
-  auto accumulate = [&](int slot, const uint32_t (&pt)[NT][2]) {
+  // O^T += V^T P^T for the page in ring slot `slot` (64 dims x 8 heads per tile); kShared: whose
+  // first `valid` tokens exist (what the last page holds behind them, possibly not finite, has
+  // weight zero and is dropped before it is multiplied)
+  auto accumulate = [&](int slot, const uint32_t (&pt)[NT][2], int valid) {
     const uint32_t vb = ring_w + slot * kSlotBytes + kPageBytes;
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
@@ -352,6 +379,17 @@ __global__ void __launch_bounds__(kWarps * 32)
       const int chunk = mt * 2 + ((lane >> 3) & 1);
       uint32_t a0, a1, a2, a3;
       ldsm_x4_trans(vb + tok * 128 + ((chunk ^ (tok & 7)) << 4), a0, a1, a2, a3);
+      if constexpr (kShared) {
+        if (valid < kPageSize) {  // the lane holds tokens t, t + 1 (a0, a1) and t + 8, t + 9 (a2, a3)
+          const int t = 2 * (lane & 3);
+          const uint32_t lo = (t < valid ? 0xFFFFu : 0u) | (t + 1 < valid ? 0xFFFF0000u : 0u);
+          const uint32_t hi = (t + 8 < valid ? 0xFFFFu : 0u) | (t + 9 < valid ? 0xFFFF0000u : 0u);
+          a0 &= lo;
+          a1 &= lo;
+          a2 &= hi;
+          a3 &= hi;
+        }
+      }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(o[nt][mt], a0, a1, a2, a3, pt[nt][0], pt[nt][1]);
     }
@@ -429,8 +467,9 @@ __global__ void __launch_bounds__(kWarps * 32)
         ptb[nt][0] = movmatrix_trans(pack_bf16x2(pb0, pb1));
         ptb[nt][1] = movmatrix_trans(pack_bf16x2(pb2, pb3));
       }
-      if (use_a) accumulate(j % kStages, pta);
-      if (use_b) accumulate((j + 1) % kStages, ptb);
+      const int page_a = (my_first + j * kWarps) * kPageSize;  // its first token
+      if (use_a) accumulate(j % kStages, pta, kv_len - page_a);
+      if (use_b) accumulate((j + 1) % kStages, ptb, kv_len - page_a - kWarps * kPageSize);
     }
     __syncwarp();
     const int next_a = id_of(j + kStages, win), next_b = id_of(j + kStages + 1, win);
@@ -520,7 +559,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     const float inv = den > 0.0f ? 1.0f / den : 0.0f;
     const float lse = den > 0.0f ? (M + lg2(den)) * kLn2 : kNegInf;
     const int head = kvh * G + hh;
-    if (a.num_splits == 1) {
+    if (!kShared && a.num_splits == 1) {
       uint16_t* out = static_cast<uint16_t*>(a.out) +
                       (static_cast<size_t>(b) * a.hq + head) * kHeadDim + d0;
       uint2 pk;
@@ -529,12 +568,17 @@ __global__ void __launch_bounds__(kWarps * 32)
       *reinterpret_cast<uint2*>(out) = pk;
       if (a.lse && d0 == 0) a.lse[static_cast<size_t>(b) * a.hq + head] = lse;
     } else {
-      const size_t row = (static_cast<size_t>(b) * a.num_splits + split) * a.hq + head;
+      size_t row = (static_cast<size_t>(b) * a.num_splits + split) * a.hq + head;
+      if constexpr (kShared)
+        row = (static_cast<size_t>(b) * (plan.shared_splits + plan.own_splits) + plan.shared_splits + split) * a.hq + head;
       float* out = static_cast<float*>(a.out) + row * kHeadDim + d0;
       *reinterpret_cast<float4*>(out) = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv,
                                                     acc[3] * inv);
       if (d0 == 0) a.lse[row] = lse;
     }
+  }
+  if constexpr (kShared) {
+    if (blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1) pdl_wait_primary();
   }
   if (!clustered) return;
 
@@ -587,8 +631,8 @@ int cluster16_capacity(Kern kern, int nt_index, cudaStream_t stream) {
 cudaError_t launch_decode(const CUtensorMap& kmap, const CUtensorMap& vmap, const DecodeArgs& args,
                           const DecodeRopeArgs& rope, cudaStream_t stream) {
   const size_t smem = decode_smem_bytes();
-  auto kern = rope.table ? (args.group <= 8 ? sink_decode_kernel<1, true> : sink_decode_kernel<2, true>)
-                         : (args.group <= 8 ? sink_decode_kernel<1, false> : sink_decode_kernel<2, false>);
+  auto kern = rope.table ? (args.group <= 8 ? sink_decode_kernel<1, true, false> : sink_decode_kernel<2, true, false>)
+                         : (args.group <= 8 ? sink_decode_kernel<1, false, false> : sink_decode_kernel<2, false, false>);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   DecodeArgs a = args;
@@ -616,7 +660,28 @@ cudaError_t launch_decode(const CUtensorMap& kmap, const CUtensorMap& vmap, cons
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = clustered ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, kern, kmap, vmap, a, rope);
+  e = cudaLaunchKernelEx(&cfg, kern, kmap, vmap, a, rope, SharedPlan{});
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+cudaError_t launch_decode_own(const CUtensorMap& kmap, const CUtensorMap& vmap, const DecodeArgs& a,
+                              const SharedPlan& plan, cudaStream_t stream) {
+  const size_t smem = decode_smem_bytes();
+  auto kern = a.group <= 8 ? sink_decode_kernel<1, false, true> : sink_decode_kernel<2, false, true>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.num_splits, a.hkv, a.batch);
+  cfg.blockDim = dim3(kWarps * 32, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, kmap, vmap, a, DecodeRopeArgs{}, plan);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

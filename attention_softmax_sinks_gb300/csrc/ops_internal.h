@@ -8,3 +8,4 @@
 #include "linear_args.h"
 #include "rope_args.h"
 #include "router_args.h"
+#include "shared_args.h"

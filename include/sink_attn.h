@@ -134,6 +134,51 @@ sa_status sink_attn_decode(const void* q, const void* paged_k, const void* paged
                            int num_splits, void* out, float* lse, cudaStream_t stream);
 
 /*
+ * Decode of a batch whose sequences share prompts: the pages that begin several sequences'
+ * page tables are read once for all of them.  The result is that of sink_attn_decode with
+ * num_splits == 1 on the same page table and lengths (up to rounding): the keys split into the
+ * shared ones, computed for all rows of a group together on the tensor cores, and each
+ * sequence's own ones, which carry its sink (the page's rule: the sink in one block only).
+ *
+ *  q, paged_k/v, page_table, kv_lens, sinks, out, lse: as for sink_attn_decode, whole
+ *               sequences (kv_lens counts the shared tokens as well)
+ *  group_offsets int32 [num_groups + 1], device: group g is sequences [group_offsets[g],
+ *               group_offsets[g + 1]); non-decreasing from 0 to batch (empty groups allowed)
+ *  shared_pages int32 [num_groups], device: the first shared_pages[g] entries of the page
+ *               tables of group g's sequences are the same (those of its first sequence are
+ *               read); 0 <= shared_pages[g] <= max_shared_pages, and every sequence of the
+ *               group is at least 16 shared_pages[g] tokens long (a shorter one attends to the
+ *               shared pages and its sink, and SA_ERR_BOUNDS is recorded).  A page that is
+ *               shared only in part belongs to the own ones.
+ *  max_shared_pages: at most max_pages
+ *  shared_splits, own_splits >= 1, together at most 256: along the keys of each part; see
+ *               sink_attn_decode_shared_splits
+ *  partial_o    fp32 [batch, shared_splits + own_splits, num_qo_heads, head_dim], 16-byte
+ *               aligned, partial_lse fp32 [batch, shared_splits + own_splits, num_qo_heads]:
+ *               the caller's workspace, overwritten.  Calls that overlap on the GPU, captured
+ *               graphs among them, need workspaces of their own.
+ * A plan that breaks its bounds sets SA_ERR_BOUNDS in the device status word, and the results
+ * of the sequences it concerns are undefined; keys of a page id outside [0, num_pages) read as
+ * zeros (shared) or are skipped (own).  What the last page holds behind kv_lens is never used,
+ * finite or not.
+ */
+sa_status sink_attn_decode_shared(const void* q, const void* paged_k, const void* paged_v,
+                                  const int32_t* page_table, const int32_t* kv_lens,
+                                  const float* sinks, const int32_t* group_offsets,
+                                  const int32_t* shared_pages, int batch, int num_groups,
+                                  int num_qo_heads, int num_kv_heads, int head_dim, int page_size,
+                                  int max_pages, int num_pages, int max_shared_pages,
+                                  float sm_scale, int shared_splits, int own_splits,
+                                  float* partial_o, float* partial_lse, void* out, float* lse,
+                                  cudaStream_t stream);
+
+/* Host-only helper: split counts for sink_attn_decode_shared from what the host knows of the
+ * batch (bounds: max_shared_pages, and max_pages of whole sequences).  num_sms 0: 152.  No CUDA call. */
+void sink_attn_decode_shared_splits(int batch, int num_groups, int num_qo_heads, int num_kv_heads,
+                                    int max_shared_pages, int max_pages, int num_sms,
+                                    int* shared_splits, int* own_splits);
+
+/*
  * The same three calls with q taken straight from the QKV projection output,
  * the query bias added and the YaRN rotation applied on chip (page "GPT-OSS on
  * day 0", model overview list: QKV projections with biases, YaRN positions;

@@ -1,0 +1,254 @@
+"""Decode of a batch that shares prompts, against attention in 64 bits over each whole sequence.
+
+Tolerances.  P is rounded to bf16 before it is multiplied with V and the result once more at the
+end; each rounding is off by at most half a step, 2^-8 of the value.  With A = sum_j p_j |v_j| the
+output is therefore within 2^-8 (A + |out|), plus 2^-13 A for the fp32 scores: 64 products and
+their sum are off by at most 64 * 2^-24 sum |q k| sm_scale < 2^-13.5 for the inputs here, and
+exp2 and the sums add some 2^-20.  lse: the same 2^-13, and 2^-22 |lse|."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+PAGE, DIM, SCALE = 16, 64, 0.125
+NAN, INF = float("nan"), float("inf")
+
+
+def make(groups, own, hq, hkv, seed=0, spare=3, extra_width=2, sink_std=1.0):
+    """groups: (sequences, shared pages) per group; own: tokens of each sequence behind them.
+    Pages that no sequence uses, and what lies behind a sequence's last token, hold NaN."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    n_seq = sum(n for n, _ in groups)
+    assert len(own) == n_seq
+    starts, lens, rows, used = [0], [], [], 0
+    for n, pages in groups:
+        common = list(range(used, used + pages))
+        used += pages
+        for _ in range(n):
+            mine = (own[len(lens)] + PAGE - 1) // PAGE
+            rows.append(common + list(range(used, used + mine)))
+            used += mine
+            lens.append(pages * PAGE + own[len(lens)])
+        starts.append(starts[-1] + n)
+    num_pages = max(used, 1) + spare
+    place = torch.randperm(num_pages, generator=g, device="cuda").to(torch.int32)
+    width = max([len(r) for r in rows] + [1]) + extra_width
+    table = torch.full((n_seq, width), -1, dtype=torch.int32, device="cuda")
+    for b, r in enumerate(rows):
+        if r:
+            table[b, : len(r)] = place[torch.tensor(r, device="cuda")]
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=g, device="cuda").to(torch.bfloat16)
+
+    k, v = normal(num_pages, hkv, PAGE, DIM), normal(num_pages, hkv, PAGE, DIM)
+    for x in (k, v):
+        x[place[used:].long()] = NAN
+        for b, n in enumerate(lens):
+            if n % PAGE:
+                x[table[b, n // PAGE].long(), :, n % PAGE :] = NAN
+    ints = lambda values: torch.tensor(values, dtype=torch.int32, device="cuda")
+    return dict(q=normal(n_seq, hq, DIM), paged_k=k, paged_v=v, page_table=table, kv_lens=ints(lens),
+                sinks=sink_std * torch.randn(hq, generator=g, device="cuda"), group_offsets=ints(starts),
+                shared_pages=ints([p for _, p in groups]), max_shared_pages=max([p for _, p in groups]), sm_scale=SCALE)
+
+
+def reference(a):
+    """out, lse and A = sum p |v| in 64 bits, sequence by sequence."""
+    q = a["q"].double()
+    n_seq, hq, _ = q.shape
+    hkv = a["paged_k"].shape[1]
+    out, lse, mag = torch.zeros_like(q), torch.zeros(n_seq, hq, dtype=torch.float64, device="cuda"), torch.zeros_like(q)
+    for b, n in enumerate(a["kv_lens"].tolist()):
+        ids = a["page_table"][b, : (n + PAGE - 1) // PAGE].long()
+        k = a["paged_k"][ids].double().transpose(0, 1).reshape(hkv, -1, DIM)[:, :n].repeat_interleave(hq // hkv, 0)
+        v = a["paged_v"][ids].double().transpose(0, 1).reshape(hkv, -1, DIM)[:, :n].repeat_interleave(hq // hkv, 0)
+        x = torch.cat([(k @ q[b, :, :, None]).squeeze(2) * a["sm_scale"], a["sinks"].double()[:, None]], 1)
+        lse[b] = torch.logsumexp(x, 1)
+        p = torch.exp(x - torch.where(lse[b].isinf(), 0.0, lse[b])[:, None])[:, None, :n]
+        out[b], mag[b] = (p @ v).squeeze(1), (p @ v.abs()).squeeze(1)
+    return out, lse, mag
+
+
+def check(a, out, lse):
+    ro, rl, mag = reference(a)
+    bound = 2.0 ** -8 * (ro.abs() + mag) + 2.0 ** -13 * mag + 1e-30
+    err = (out.double() - ro).abs()
+    assert bool((err <= bound).all()), f"out: worst error / bound {(err / bound).max().item()}"
+    same = lse.double() == rl  # infinities
+    err = torch.where(same, 0.0, (lse.double() - rl).abs())
+    assert bool((err <= 2.0 ** -13 + 2.0 ** -22 * rl.abs()).all()), f"lse: worst error {err.max().item()}"
+
+
+def call(a, **kw):
+    import attention_softmax_sinks_gb300 as sa
+    sa.sink_attn_device_status(True)
+    out, lse = sa.sink_attn_decode_shared(**a, **kw)
+    torch.cuda.synchronize()
+    assert sa.sink_attn_device_status(True) == 0
+    return out, lse
+
+
+CASES = {
+    "one sequence, one page": ([(1, 1)], [1], 64, 8, None),
+    "one token, nothing shared": ([(1, 0)], [1], 8, 8, None),
+    "own part empty": ([(3, 2)], [0, 0, 5], 8, 1, (2, 1)),
+    "nothing shared anywhere": ([(5, 0)], [1, 16, 17, 100, 33], 16, 2, (3, 2)),
+    "prompt ends inside a tile": ([(4, 13)], [1, 2, 30, 31], 64, 8, (2, 1)),
+    "one tile of keys": ([(4, 8)], [7, 300, 1, 16], 64, 8, (1, 2)),
+    "more slots than tiles": ([(2, 9)], [5, 50], 64, 8, (24, 4)),
+    "two row tiles, odd group of 5": ([(37, 40)], [(i * 13) % 50 + 1 for i in range(37)], 40, 8, (3, 1)),
+    "group of 7, rows end inside a tile": ([(19, 24)], [3 + i for i in range(19)], 28, 4, None),
+    "group of 16": ([(17, 33)], [1 + 9 * i for i in range(17)], 64, 4, (2, 2)),
+    "no grouped heads": ([(130, 17)], [1 + i % 40 for i in range(130)], 4, 4, None),
+    "several row pairs": ([(70, 30)], [1 + (i * 31) % 90 for i in range(70)], 64, 8, (2, 1)),
+    "groups of all kinds": ([(1, 5), (0, 3), (20, 60), (3, 0), (0, 0), (40, 1), (1, 129)],
+                            [1 + (i * 17) % 70 for i in range(65)], 64, 8, None),
+    "long prompt": ([(9, 700)], [1 + i for i in range(9)], 64, 8, None),
+    "long own parts": ([(3, 20)], [4000, 1, 2500], 64, 8, None),
+    "most slots": ([(2, 300)], [2000, 10], 16, 8, (200, 56)),
+}
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_shared_decode(name):
+    groups, own, hq, hkv, splits = CASES[name]
+    a = make(groups, own, hq, hkv, seed=len(name))
+    check(a, *call(a, splits=splits))
+
+
+def test_many_groups():
+    # more groups than a CTA's threads look at in one go, some of them empty
+    groups = [(i % 3, i % 4) for i in range(900)]
+    n = sum(g for g, _ in groups)
+    a = make(groups, [1 + i % 20 for i in range(n)], 8, 2)
+    check(a, *call(a))
+
+
+def test_agrees_with_plain_decode():
+    import attention_softmax_sinks_gb300 as sa
+    a = make([(6, 50), (3, 10)], [1 + 40 * i for i in range(9)], 64, 8)
+    for x in (a["paged_k"], a["paged_v"]):
+        x.copy_(torch.nan_to_num(x))
+    out, lse = call(a)
+    o, l = sa.sink_attn_decode(a["q"], a["paged_k"], a["paged_v"], a["page_table"], a["kv_lens"], a["sinks"], SCALE)
+    mag = reference(a)[2]
+    assert bool(((out.float() - o.float()).abs() <= 2 * (2.0 ** -8 * (o.float().abs() + mag) + 2.0 ** -13 * mag)).all())
+    assert bool(((lse - l).abs() <= 2.0 ** -12).all())
+
+
+@pytest.mark.parametrize("sink", [-INF, -1e30, 80.0, INF])
+def test_sinks_at_the_extremes(sink):
+    a = make([(3, 9)], [1, 0, 20], 16, 2)
+    a["sinks"].fill_(sink)
+    a["sinks"][0] = 0.5
+    out, lse = call(a)
+    if sink == INF:  # the sink takes all the weight
+        assert bool((out[:, 1:] == 0).all()) and bool((lse[:, 1:] == INF).all())
+        a["sinks"][1:] = 0.5
+        ro, rl, mag = reference(a)
+        assert bool(((out[:, :1] - ro[:, :1]).abs() <= 2.0 ** -7 * mag[:, :1] + 2.0 ** -8 * ro[:, :1].abs()).all())
+    else:
+        check(a, out, lse)
+
+
+def test_no_keys_and_no_sink():
+    a = make([(2, 0)], [0, 3], 8, 1)
+    a["sinks"].fill_(-INF)
+    out, lse = call(a)
+    assert bool((out[0] == 0).all()) and bool((lse[0] == -INF).all())
+    check({**a, "q": a["q"][1:], "page_table": a["page_table"][1:], "kv_lens": a["kv_lens"][1:]}, out[1:], lse[1:])
+
+
+def test_scores_far_apart():
+    # keys of very different size: the running maximum grows in several steps, both ways
+    for flip in (False, True):
+        a = make([(5, 64)], [40] * 5, 64, 8)
+        size = torch.linspace(0.05, 6.0, a["paged_k"].shape[0], device="cuda")
+        order = a["page_table"][0, :64].long()
+        size = size.flip(0) if flip else size
+        k = a["paged_k"].float()
+        k[order] = k[order] * size[:64].reshape(-1, 1, 1, 1)
+        a["paged_k"] = k.to(torch.bfloat16)
+        out, lse = call(a)
+        ro, rl, mag = reference(a)
+        # scores of size up to 6 * 64 * 0.125 * ...: their fp32 error is 6 times that of unit keys
+        assert bool(((out - ro).abs() <= 2.0 ** -8 * (ro.abs() + mag) + 2.0 ** -10 * mag).all())
+        assert bool(((lse - rl).abs() <= 2.0 ** -10).all())
+
+
+def test_outputs_workspace_and_stream():
+    import attention_softmax_sinks_gb300 as sa
+    a = make([(4, 10), (2, 3)], [1, 20, 3, 40, 5, 6], 64, 8)
+    want = call(a, splits=(2, 2))
+    ws = (torch.full((6, 4, 64, DIM), NAN, device="cuda"), torch.full((6, 4, 64), NAN, device="cuda"))
+    out = torch.full((8, 64, DIM), 7.0, dtype=torch.bfloat16, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = sa.sink_attn_decode_shared(**a, splits=(2, 2), workspace=ws, out=out[:6], return_lse=False, stream=s)
+    s.synchronize()
+    assert got[1] is None and torch.equal(got[0], want[0]) and bool((out[6:] == 7).all())
+
+
+def test_repeated_calls_and_graph_replay():
+    import attention_softmax_sinks_gb300 as sa
+    a = make([(30, 40), (11, 7)], [1 + (i * 7) % 60 for i in range(41)], 64, 8)
+    want = call(a)
+    for _ in range(5):
+        got = call(a)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        sa.sink_attn_decode_shared(**a)
+    s.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out, lse = sa.sink_attn_decode_shared(**a)
+    other = torch.Generator(device="cuda").manual_seed(5)
+    for name in ("q", "paged_k", "paged_v"):
+        a[name].copy_(torch.randn(a[name].shape, generator=other, device="cuda"))
+    a["kv_lens"][30:] -= 2 * (a["kv_lens"][30:] > 7 * PAGE + 2)  # shorter own parts, same pages
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert sa.sink_attn_device_status(True) == 0
+    check(a, out, lse)
+
+
+def test_device_side_reports():
+    import attention_softmax_sinks_gb300 as sa
+    SA_ERR_BOUNDS = 5
+
+    def status(**change):
+        a = make([(3, 4), (2, 2)], [1, 20, 3, 40, 5], 16, 2)
+        for x in (a["paged_k"], a["paged_v"]):
+            x.copy_(torch.nan_to_num(x))
+        for name, f in change.items():
+            f(a[name])
+        sa.sink_attn_decode_shared(**a)
+        torch.cuda.synchronize()
+        return sa.sink_attn_device_status(True)
+
+    assert status() == 0
+    assert status(group_offsets=lambda t: t.copy_(torch.tensor([0, 3, 4], device="cuda"))) == SA_ERR_BOUNDS
+    assert status(group_offsets=lambda t: t.copy_(torch.tensor([1, 3, 5], device="cuda"))) == SA_ERR_BOUNDS
+    assert status(group_offsets=lambda t: t.copy_(torch.tensor([0, 9, 5], device="cuda"))) == SA_ERR_BOUNDS
+    assert status(group_offsets=lambda t: t.copy_(torch.tensor([0, -3, 5], device="cuda"))) == SA_ERR_BOUNDS
+    assert status(shared_pages=lambda t: t.fill_(5)) == SA_ERR_BOUNDS   # above max_shared_pages
+    assert status(shared_pages=lambda t: t.fill_(-1)) == SA_ERR_BOUNDS
+    assert status(kv_lens=lambda t: t[1:2].fill_(10)) == SA_ERR_BOUNDS  # shorter than its prompt
+    assert status(kv_lens=lambda t: t.fill_(1 << 30)) == SA_ERR_BOUNDS
+    assert status(page_table=lambda t: t[0, 1:2].fill_(10 ** 6)) == SA_ERR_BOUNDS  # a shared page
+    assert status(page_table=lambda t: t[1, 5:6].fill_(-7)) == SA_ERR_BOUNDS      # an own one
+    assert status() == 0
+
+
+def test_shorter_than_its_prompt():
+    import attention_softmax_sinks_gb300 as sa
+    a = make([(3, 4)], [5, 6, 7], 16, 2)
+    a["kv_lens"][1] = 20
+    out, lse = sa.sink_attn_decode_shared(**a)
+    torch.cuda.synchronize()
+    assert sa.sink_attn_device_status(True) == 5
+    a["kv_lens"][1] = 64  # what it attends to: the shared pages and its sink
+    check(a, out, lse)
