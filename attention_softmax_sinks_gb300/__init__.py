@@ -28,6 +28,7 @@ __all__ = [
     "grouped_linear_bias", "grouped_linear_swiglu", "mxfp4_quantize", "mxfp4_dequantize",
     "mxfp4_linear_bias", "grouped_mxfp4_linear_bias", "grouped_mxfp4_linear_swiglu",
     "mxfp4_scale_columns", "GPT_OSS_SWIGLU", "sink_attn_decode_shared", "sink_attn_decode_shared_splits",
+    "lora_linear_bias",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -44,7 +45,7 @@ EXPORTED_SYMBOLS = (
     "sink_attn_decode_qkv", "moe_group_rows", "moe_combine",
     "grouped_linear_bias", "grouped_linear_swiglu", "mxfp4_quantize", "mxfp4_dequantize",
     "mxfp4_linear_bias", "grouped_mxfp4_linear_bias", "grouped_mxfp4_linear_swiglu",
-    "sink_attn_decode_shared", "sink_attn_decode_shared_splits",
+    "sink_attn_decode_shared", "sink_attn_decode_shared_splits", "lora_linear_bias", "lora_workspace_bytes",
 )
 
 _p, _i, _f, _d, _ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_double, ctypes.c_longlong
@@ -87,6 +88,8 @@ _SIGNATURES = {
     "sink_attn_decode_shared": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _i, _f, _i, _i,
                                      _p, _p, _p, _p, _p]),
     "sink_attn_decode_shared_splits": (None, [_i, _i, _i, _i, _i, _i, _i, _p, _p]),
+    "lora_linear_bias": (_i, [_p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _p, _p, _p]),
+    "lora_workspace_bytes": (_ll, [_i, _i, _i]),
     "grouped_mxfp4_linear_swiglu": (_i, [_p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _f, _f, _p, _p]),
 }
 
@@ -529,6 +532,43 @@ def linear_bias(x, w, bias=None, out=None, stream=None):
     _out(out, "out", torch.bfloat16, (m, n), di)
     st = _call(load_library().linear_bias, di, stream, _ptr(x), _ptr(w), _ptr(bias), m, n, k, _ptr(out))
     _check(st, "linear_bias")
+    return out
+
+
+def lora_linear_bias(x, w, lora_a, lora_b, adapter_idx, bias=None, lora_scale=None, out=None, workspace=None,
+                     stream=None):
+    """linear_bias with the low-rank adapters of many requests at once beside it:
+    out[m] = x[m] @ w^T + bias + lora_scale[a] * (x[m] @ lora_a[a]^T) @ lora_b[a]^T for
+    a = adapter_idx[m], without the last term where adapter_idx[m] is negative.
+
+    x [M, K] bf16, w [N, K] bf16, lora_a [L, R, K] bf16, lora_b [L, N, R] bf16 (R a multiple of 8,
+    at most 128; L at most 1024), adapter_idx [M] int32, bias [N] bf16 or None, lora_scale [L]
+    fp32 or None (1).  workspace: a uint8 tensor of at least lora_workspace_bytes(M, K, R) bytes,
+    allocated when not given.  Returns out [M, N] bf16."""
+    n, k = _shape(w, "w", 2)
+    l, r, _ = _shape(lora_a, "lora_a", 3)
+    m = _shape(x, "x", 2)[0]
+    named = [("x", x, torch.bfloat16, (m, k)), ("w", w, torch.bfloat16, (n, k)), ("lora_a", lora_a, torch.bfloat16, (l, r, k)),
+             ("lora_b", lora_b, torch.bfloat16, (l, n, r)), ("adapter_idx", adapter_idx, torch.int32, (m,))]
+    if bias is not None:
+        named.append(("bias", bias, torch.bfloat16, (n,)))
+    if lora_scale is not None:
+        named.append(("lora_scale", lora_scale, torch.float32, (l,)))
+    di = _inputs(*named)
+    lib = load_library()
+    need = lib.lora_workspace_bytes(m, k, r)
+    if workspace is None:
+        workspace = _new(need, torch.uint8, x.device, stream)
+    else:
+        _dev(workspace, "workspace", torch.uint8)
+        _same_device(di, ("workspace", workspace))
+        if workspace.numel() < need:
+            raise ValueError(f"workspace must have at least {need} bytes, got {workspace.numel()}")
+    out = _product_output(out, m, n, x, di, stream)
+    st = _call(lib.lora_linear_bias, di, stream, x.data_ptr(), w.data_ptr(), _ptr(bias), lora_a.data_ptr(),
+               lora_b.data_ptr(), _ptr(lora_scale), adapter_idx.data_ptr(), m, n, k, r, l, workspace.data_ptr(),
+               out.data_ptr())
+    _check(st, "lora_linear_bias")
     return out
 
 

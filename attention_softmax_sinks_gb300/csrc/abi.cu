@@ -146,6 +146,20 @@ sa_status map_scales(CUtensorMap* m, const void* base, long long rows, int strid
   return r == CUDA_SUCCESS ? SA_OK : SA_ERR_CUDA;
 }
 
+// Adapters' second factors [adapters, n, rank] read in boxes of 16 ranks x box_n features.
+sa_status map_adapters(CUtensorMap* m, const void* base, int adapters, int n, int rank, int box_n) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc;
+  if (sa_status s = encoder(&enc)) return s;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(rank), static_cast<cuuint64_t>(n), static_cast<cuuint64_t>(adapters)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(rank) * 2, static_cast<cuuint64_t>(rank) * 2 * n};
+  cuuint32_t box[3] = {16, static_cast<cuuint32_t>(box_n), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? SA_OK : SA_ERR_CUDA;
+}
+
 // Paged cache [num_pages, hkv, 16, 64] viewed as [num_pages*hkv*16, 64] rows,
 // one box = one (page, kv head) = 16 rows.
 sa_status map_pages(CUtensorMap* m, const void* base, int num_pages, int hkv) {
@@ -789,6 +803,59 @@ sa_status linear_bias(const void* x, const void* w, const void* bias, int m, int
   if (sa_status s = map_matrix(&am, x, m, k, 128)) return s;
   if (sa_status s = map_matrix(&bm, w, n, k, a.block_n)) return s;
   return sa::launch_linear(am, bm, a, sms, stream) == cudaSuccess ? SA_OK : SA_ERR_LAUNCH;
+}
+
+long long lora_workspace_bytes(int m, int k, int rank) {
+  if (m <= 0 || k <= 0 || rank <= 0 || rank > sa::kLoraMaxRank) return 0;
+  const long long tiles = (static_cast<long long>(m) + sa::kLoraTileRows - 1) / sa::kLoraTileRows;
+  return tiles * sa::kLoraPlanInts * 4 + 4LL * sa::lora_splits(m, k) * m * rank;
+}
+
+sa_status lora_linear_bias(const void* x, const void* w, const void* bias, const void* lora_a, const void* lora_b,
+                           const float* lora_scale, const int32_t* adapter_idx, int m, int n, int k, int rank,
+                           int num_adapters, void* workspace, void* out, cudaStream_t stream) {
+  if (m < 0 || n <= 0 || k <= 0 || n > (1 << 30) || k > (1 << 30)) return SA_ERR_SHAPE;
+  if (rank <= 0 || num_adapters < 1 || num_adapters > sa::kLoraMaxAdapters) return SA_ERR_SHAPE;
+  if (n % 8 != 0 || k % 8 != 0 || rank % 8 != 0 || rank > sa::kLoraMaxRank) return SA_ERR_UNSUPPORTED;
+  if (m == 0) return SA_OK;
+  if (!x || !w || !lora_a || !lora_b || !adapter_idx || !workspace || !out) return SA_ERR_NULL;
+  if (!aligned16(x) || !aligned16(w) || !aligned16(lora_a) || !aligned16(lora_b) || !aligned16(workspace) ||
+      !aligned16(out) || !aligned2(bias) || !aligned4(lora_scale) || !aligned4(adapter_idx))
+    return SA_ERR_ALIGNMENT;
+  sa::LoraArgs a{};
+  const int sms = sm_count();
+  a.block_n = sa::lora_tile_n(m, n, k, sms);
+  const long long tiles_m = (static_cast<long long>(m) + sa::kLoraTileRows - 1) / sa::kLoraTileRows;
+  const long long tiles_n = (static_cast<long long>(n) + a.block_n - 1) / a.block_n;
+  if (tiles_m > 65535 || tiles_m * tiles_n >= (1LL << 30)) return SA_ERR_SHAPE;
+  unsigned* status = nullptr;
+  if (sa_status s = status_ptr(&status)) return s;
+  a.x = static_cast<const uint16_t*>(x);
+  a.w = static_cast<const uint16_t*>(w);
+  a.lora_a = static_cast<const uint16_t*>(lora_a);
+  a.lora_b = static_cast<const uint16_t*>(lora_b);
+  a.adapter = adapter_idx;
+  a.scale = lora_scale;
+  a.bias = static_cast<const uint16_t*>(bias);
+  a.out = static_cast<uint16_t*>(out);
+  a.plan = static_cast<int32_t*>(workspace);
+  a.t = reinterpret_cast<float*>(a.plan + tiles_m * sa::kLoraPlanInts);
+  a.M = m;
+  a.N = n;
+  a.K = k;
+  a.R = rank;
+  a.num_adapters = num_adapters;
+  a.splits = sa::lora_splits(m, k);
+  a.tiles_m = static_cast<int>(tiles_m);
+  a.tiles_n = static_cast<int>(tiles_n);
+  a.box_rows = m < sa::kLoraTileRows ? (m + 7) / 8 * 8 : sa::kLoraTileRows;
+  a.status = status;
+  a.timeout_ns = g_timeout_ns;
+  CUtensorMap xm, wm, bm;
+  if (sa_status s = map_matrix(&xm, x, m, k, a.box_rows)) return s;
+  if (sa_status s = map_matrix(&wm, w, n, k, a.block_n)) return s;
+  if (sa_status s = map_adapters(&bm, lora_b, num_adapters, n, rank, a.block_n)) return s;
+  return sa::launch_lora(xm, wm, bm, a, sms, stream) == cudaSuccess ? SA_OK : SA_ERR_LAUNCH;
 }
 
 sa_status moe_router(const void* x, const void* w_router, const void* bias, int num_tokens,

@@ -6,6 +6,7 @@
 #include "experts_args.h"
 #include "grouped_args.h"
 #include "linear_args.h"
+#include "lora_args.h"
 #include "rope_args.h"
 #include "router_args.h"
 #include "shared_args.h"

@@ -41,6 +41,37 @@ extern "C" {
 sa_status linear_bias(const void* x, const void* w, const void* bias, int m, int n, int k,
                       void* out, cudaStream_t stream);
 
+/*
+ * The same layer with the low-rank adapters of many requests at once beside it:
+ *
+ *     out[m] = x[m] W^T + bias + s_a (x[m] A_a^T) B_a^T,    a = adapter_idx[m]
+ *
+ * and without the last term where adapter_idx[m] is negative.  x A^T is summed in fp32, times
+ * s_a rounded once to bf16 for the second product; everything adds up in the fp32 accumulator
+ * that starts from the bias, and the result rounds once to bf16.
+ *
+ *  x, w, bias, out, m, n, k: as for linear_bias
+ *  lora_a       bf16 [num_adapters, rank, k], lora_b bf16 [num_adapters, n, rank], 16-byte
+ *               aligned; rank a multiple of 8, at most 128 (adapters of lower rank are padded
+ *               with zeros); num_adapters 1..1024
+ *  lora_scale   fp32 [num_adapters] or NULL (1)
+ *  adapter_idx  int32 [m], device, in any order.  An index >= num_adapters counts as none and
+ *               sets SA_ERR_BOUNDS in the device status word.
+ *  workspace    lora_workspace_bytes(m, k, rank) bytes of device memory, 16-byte aligned,
+ *               overwritten; calls that overlap on the GPU, captured graphs among them, need
+ *               workspaces of their own
+ * Status codes as for linear_bias (SA_ERR_SHAPE also for rank <= 0, num_adapters out of range and
+ * more than 65535 * 128 tokens; SA_ERR_UNSUPPORTED for other ranks).
+ */
+sa_status lora_linear_bias(const void* x, const void* w, const void* bias, const void* lora_a,
+                           const void* lora_b, const float* lora_scale, const int32_t* adapter_idx,
+                           int m, int n, int k, int rank, int num_adapters, void* workspace,
+                           void* out, cudaStream_t stream);
+
+/* Bytes of workspace for lora_linear_bias (0 for sizes that it refuses or does nothing for).
+ * No CUDA call. */
+long long lora_workspace_bytes(int m, int k, int rank);
+
 #ifdef __cplusplus
 }
 #endif
