@@ -28,7 +28,7 @@ __all__ = [
     "grouped_linear_bias", "grouped_linear_swiglu", "mxfp4_quantize", "mxfp4_dequantize",
     "mxfp4_linear_bias", "grouped_mxfp4_linear_bias", "grouped_mxfp4_linear_swiglu",
     "mxfp4_scale_columns", "GPT_OSS_SWIGLU", "sink_attn_decode_shared", "sink_attn_decode_shared_splits",
-    "lora_linear_bias",
+    "lora_linear_bias", "lora_workspace_bytes", "moe_router_scores",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -46,6 +46,7 @@ EXPORTED_SYMBOLS = (
     "grouped_linear_bias", "grouped_linear_swiglu", "mxfp4_quantize", "mxfp4_dequantize",
     "mxfp4_linear_bias", "grouped_mxfp4_linear_bias", "grouped_mxfp4_linear_swiglu",
     "sink_attn_decode_shared", "sink_attn_decode_shared_splits", "lora_linear_bias", "lora_workspace_bytes",
+    "moe_router_scores",
 )
 
 _p, _i, _f, _d, _ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_double, ctypes.c_longlong
@@ -90,6 +91,7 @@ _SIGNATURES = {
     "sink_attn_decode_shared_splits": (None, [_i, _i, _i, _i, _i, _i, _i, _p, _p]),
     "lora_linear_bias": (_i, [_p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _p, _p, _p]),
     "lora_workspace_bytes": (_ll, [_i, _i, _i]),
+    "moe_router_scores": (_i, [_p, _i, _ll, _i, _i, _i, _p, _i, _i, _i, _f, _p, _p, _p, _p]),
     "grouped_mxfp4_linear_swiglu": (_i, [_p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _f, _f, _p, _p]),
 }
 
@@ -535,6 +537,11 @@ def linear_bias(x, w, bias=None, out=None, stream=None):
     return out
 
 
+def lora_workspace_bytes(m: int, k: int, rank: int) -> int:
+    """Bytes of workspace for lora_linear_bias of m tokens."""
+    return load_library().lora_workspace_bytes(_c_int(m, "m"), _c_int(k, "k"), _c_int(rank, "rank"))
+
+
 def lora_linear_bias(x, w, lora_a, lora_b, adapter_idx, bias=None, lora_scale=None, out=None, workspace=None,
                      stream=None):
     """linear_bias with the low-rank adapters of many requests at once beside it:
@@ -596,6 +603,44 @@ def moe_router(x, w_router, bias, top_k: int, topk_idx=None, topk_weight=None, e
     st = _call(load_library().moe_router, di, stream, _ptr(x), _ptr(w_router), _ptr(bias), t, hidden, e, k,
                _ptr(topk_idx), _ptr(topk_weight), _ptr(expert_counts))
     _check(st, "moe_router")
+    if expert_counts is not None:
+        return topk_idx, topk_weight, expert_counts
+    return topk_idx, topk_weight
+
+
+def moe_router_scores(logits, top_k: int, score: str = "softmax", bias=None, num_groups: int = 1, top_groups: int = 1,
+                      renormalize: bool = True, scale: float = 1.0, topk_idx=None, topk_weight=None,
+                      expert_counts=None, return_counts: bool = False, stream=None):
+    """Router by scores: s = softmax or sigmoid of the logits [T, E] (bf16 or fp32) over all experts,
+    the top_k largest s + bias among the top_groups best of num_groups groups of consecutive
+    experts (a group's merit: the sum of its two largest s + bias), largest first, equal values in
+    favour of the lower index; weights scale * s, divided by the sum of the chosen s with
+    renormalize.  bias [E] fp32 or None.  Returns (idx int32 [T, k], weight bf16 [T, k]) and the
+    int32 [E] counts when asked."""
+    if score not in ("softmax", "sigmoid"):
+        raise ValueError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
+    fp32 = isinstance(logits, torch.Tensor) and logits.dtype is torch.float32
+    t, e = _shape(logits, "logits", 2)
+    named = [("logits", logits, torch.float32 if fp32 else torch.bfloat16, (t, e))]
+    if bias is not None:
+        named.append(("bias", bias, torch.float32, (e,)))
+    di, dev = _inputs(*named), logits.device
+    k = _c_int(int(top_k), "top_k")
+    if not 1 <= k <= 8:  # no memory for what the call refuses
+        raise ValueError(f"top_k must be 1 to 8, got {k}")
+    topk_idx = (_new((t, k), torch.int32, dev, stream) if topk_idx is None
+                else _out(topk_idx, "topk_idx", torch.int32, (t, k), di))
+    topk_weight = (_new((t, k), torch.bfloat16, dev, stream) if topk_weight is None
+                   else _out(topk_weight, "topk_weight", torch.bfloat16, (t, k), di))
+    if expert_counts is None and return_counts:
+        expert_counts = _new((e,), torch.int32, dev, stream)
+    elif expert_counts is not None:
+        _out(expert_counts, "expert_counts", torch.int32, (e,), di)
+    st = _call(load_library().moe_router_scores, di, stream, logits.data_ptr(), int(fp32), t, e, k,
+               int(score == "sigmoid"), _ptr(bias), _c_int(int(num_groups), "num_groups"),
+               _c_int(int(top_groups), "top_groups"), int(bool(renormalize)), float(scale), topk_idx.data_ptr(),
+               topk_weight.data_ptr(), _ptr(expert_counts))
+    _check(st, "moe_router_scores")
     if expert_counts is not None:
         return topk_idx, topk_weight, expert_counts
     return topk_idx, topk_weight

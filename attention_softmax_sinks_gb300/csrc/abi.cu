@@ -914,6 +914,43 @@ sa_status moe_router_topk_softmax(const void* logits, long long num_tokens, int 
   return sa::launch_router(a, stream) == cudaSuccess ? SA_OK : SA_ERR_LAUNCH;
 }
 
+sa_status moe_router_scores(const void* logits, int is_fp32, long long num_tokens, int num_experts, int top_k,
+                            int sigmoid, const float* bias, int num_groups, int top_groups, int renormalize,
+                            float scale, int32_t* topk_idx, void* topk_weight, int32_t* expert_counts,
+                            cudaStream_t stream) {
+  if (num_tokens < 0 || num_experts < 1 || num_experts > 256) return SA_ERR_SHAPE;
+  if (num_groups < 1 || num_groups > sa::kRouterMaxGroups || num_experts % num_groups != 0) return SA_ERR_SHAPE;
+  if (top_groups < 1 || top_groups > num_groups) return SA_ERR_SHAPE;
+  if (top_k < 1 || top_k > 8 || top_k > top_groups * (num_experts / num_groups)) return SA_ERR_SHAPE;
+  if (!std::isfinite(scale)) return SA_ERR_SHAPE;
+  if (num_tokens > (1LL << 40) / num_experts) return SA_ERR_SHAPE;
+  if (num_tokens > 0 && (!logits || !topk_idx || !topk_weight)) return SA_ERR_NULL;
+  if ((is_fp32 ? !aligned4(logits) : !aligned2(logits)) || !aligned4(bias) || !aligned4(topk_idx) ||
+      !aligned2(topk_weight) || !aligned4(expert_counts))
+    return SA_ERR_ALIGNMENT;
+  if (expert_counts &&
+      cudaMemsetAsync(expert_counts, 0, sizeof(int32_t) * num_experts, stream) != cudaSuccess)
+    return SA_ERR_CUDA;
+  if (num_tokens == 0) return SA_OK;
+  sa::RouterScoresArgs a{};
+  a.logits = logits;
+  a.bias = bias;
+  a.topk_idx = topk_idx;
+  a.topk_w = static_cast<uint16_t*>(topk_weight);
+  a.counts = expert_counts;
+  a.num_tokens = num_tokens;
+  a.num_experts = num_experts;
+  a.top_k = top_k;
+  a.num_groups = num_groups;
+  a.top_groups = top_groups;
+  a.fp32 = is_fp32 ? 1 : 0;
+  a.sigmoid = sigmoid ? 1 : 0;
+  a.renormalize = renormalize ? 1 : 0;
+  a.vec4 = num_experts % 4 == 0 && reinterpret_cast<uintptr_t>(logits) % (is_fp32 ? 16 : 8) == 0;
+  a.scale = scale;
+  return sa::launch_router_scores(a, sm_count(), stream) == cudaSuccess ? SA_OK : SA_ERR_LAUNCH;
+}
+
 sa_status qkv_bias_rope(const void* qkv, const void* bias, const int32_t* cu_seqlens_q,
                         const int32_t* kv_lens, int batch, int total_tokens, int num_qo_heads,
                         int num_kv_heads, int head_dim, double rope_base, double factor,

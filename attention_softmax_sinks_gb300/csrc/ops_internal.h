@@ -9,4 +9,5 @@
 #include "lora_args.h"
 #include "rope_args.h"
 #include "router_args.h"
+#include "router_scores_args.h"
 #include "shared_args.h"

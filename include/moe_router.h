@@ -63,6 +63,36 @@ sa_status moe_router(const void* x, const void* w_router, const void* bias, int 
                      int hidden, int num_experts, int top_k, int32_t* topk_idx, void* topk_weight,
                      int32_t* expert_counts, cudaStream_t stream);
 
+/*
+ * The other family of routers (which the page sets against its own: the scores of all experts
+ * first, then the choice): per token t with logits x
+ *
+ *     s_e = 1 / (1 + e^-x_e)  (sigmoid != 0)   or   e^x_e / sum_f e^x_f
+ *     v_e = s_e + bias_e                                        (balance; the choice only)
+ *     groups of num_experts / num_groups consecutive experts: the merit of a group is the sum of
+ *     its two largest v (of one expert: its v); the top_groups groups of largest merit are kept
+ *     S   = the top_k experts of the kept groups with the largest v, largest first
+ *     w_r = scale * s_S[r]  (/ sum_r' s_S[r'] with renormalize; 0 where that sum is 0)
+ *
+ * The choice is that of exact arithmetic on the logits and biases as given, equal values in
+ * favour of the lower index; without a bias it is the logits' own order (within the groups kept).
+ * The weights are computed in fp32 and stored as bf16.
+ *
+ *  logits        fp32 (is_fp32 != 0) or bf16 [num_tokens, num_experts], row-major, at least
+ *                aligned to their elements (four logits at a time where rows are aligned to that);
+ *                -inf takes an expert out, NaN not allowed (the experts of such a row are
+ *                some in range)
+ *  bias          fp32 [num_experts] or NULL; -inf puts an expert behind all others
+ *  topk_idx, topk_weight, expert_counts: as for moe_router_topk_softmax
+ *  1 <= num_experts <= 256, 1 <= num_groups <= 32 dividing num_experts, 1 <= top_groups <=
+ *  num_groups, 1 <= top_k <= min(8, experts of top_groups groups), scale finite
+ *  (SA_ERR_SHAPE otherwise).
+ */
+sa_status moe_router_scores(const void* logits, int is_fp32, long long num_tokens, int num_experts,
+                            int top_k, int sigmoid, const float* bias, int num_groups,
+                            int top_groups, int renormalize, float scale, int32_t* topk_idx,
+                            void* topk_weight, int32_t* expert_counts, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,209 @@
+"""Router by scores, groups and balance, against the definition in 64 bits.
+
+The experts have to be equal.  Weights: the score in fp32 is off by less than 2^-19 relative
+(exp2 and reciprocal 2^-22 each, the exponent's rounding 2^-24 |x| for |x| <= 16, sums of 256), the
+sum for renormalising as much again, and the rounding to bf16 by 2^-8: 2^-8 + 2^-17 of the weight."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+INF = float("inf")
+
+
+def make(t, e, dtype="float32", bias=None, std=1.5, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = (std * torch.randn(t, e, generator=g, device="cuda")).to(getattr(torch, dtype))
+    b = None if bias is None else bias * torch.randn(e, generator=g, device="cuda")
+    return x, b
+
+
+def two_sum(x, y):
+    """x + y without rounding, as a sum of two doubles (adding a huge bias must not hide a score)."""
+    s = x + y
+    z = s - x
+    e = (x - (s - z)) + (y - z)
+    return s, torch.where(torch.isfinite(s), e, 0.0)
+
+
+def descending(hi, lo):
+    """Indices of hi + lo, largest first, equal ones in order."""
+    first = lo.sort(dim=-1, descending=True, stable=True).indices
+    return first.gather(-1, hi.gather(-1, first).sort(dim=-1, descending=True, stable=True).indices)
+
+
+def reference(x, k, score, bias, groups, keep, renorm, scale):
+    x = x.double()
+    t, e = x.shape
+    s = torch.sigmoid(x) if score == "sigmoid" else torch.softmax(x, 1)
+    v, v2 = two_sum(s, torch.zeros(e, dtype=torch.float64, device="cuda") if bias is None else bias.double())
+    idx = descending(x, torch.zeros_like(x)) if bias is None else descending(v, v2)  # without bias: the logits' order
+    if keep < groups:
+        g, g2 = v.reshape(t, groups, -1), v2.reshape(t, groups, -1)
+        two = descending(g, g2)[:, :, :2]
+        g, g2 = g.gather(2, two), g2.gather(2, two).sum(2)
+        m, m2 = two_sum(g[:, :, 0], g[:, :, 1]) if two.shape[2] == 2 else (g[:, :, 0], torch.zeros_like(g2))
+        kept = descending(*two_sum(m, m2 + g2))[:, :keep]
+        inside = torch.zeros(t, groups, dtype=torch.bool, device="cuda").scatter_(1, kept, True)
+        out = ~inside.repeat_interleave(e // groups, 1).gather(1, idx)
+        idx = idx.gather(1, out.int().sort(dim=1, stable=True).indices)
+    idx = idx[:, :k]
+    w = s.gather(1, idx)
+    if renorm:
+        total = w.sum(1, keepdim=True)
+        w = torch.where(total > 0, w / total, 0.0)
+    return idx, scale * w
+
+
+def check(x, k, score="softmax", bias=None, groups=1, keep=1, renorm=True, scale=1.0, **kw):
+    import attention_softmax_sinks_gb300 as sa
+    idx, w, counts = sa.moe_router_scores(x, k, score=score, bias=bias, num_groups=groups, top_groups=keep,
+                                          renormalize=renorm, scale=scale, return_counts=True, **kw)
+    ri, rw = reference(x, k, score, bias, groups, keep, renorm, scale)
+    wrong = (idx.long() != ri).any(1)
+    assert not bool(wrong.any()), f"{int(wrong.sum())} tokens differ, first {int(wrong.nonzero()[0])}: {idx[wrong][0].tolist()} {ri[wrong][0].tolist()}"
+    assert bool(((w.double() - rw).abs() <= (2.0 ** -8 + 2.0 ** -17) * rw.abs() + 1e-38).all())
+    assert torch.equal(counts.long(), torch.bincount(ri.reshape(-1), minlength=x.shape[1]))
+
+
+SHAPES = [(1, 256, 8, 8, 4), (3, 1, 1, 1, 1), (64, 256, 8, 8, 4), (5, 7, 3, 1, 1), (130, 100, 6, 4, 2), (33, 160, 6, 8, 3),
+          (1000, 64, 4, 1, 1), (17, 255, 8, 5, 5), (40, 96, 2, 32, 7), (9, 32, 8, 32, 8), (31, 60, 5, 20, 10),
+          (20, 256, 7, 2, 1), (700, 128, 1, 16, 3), (12, 200, 8, 8, 1), (50, 31, 8, 31, 9)]
+
+
+@pytest.mark.parametrize("t,e,k,groups,keep", SHAPES)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("bias", [None, 0.1])
+def test_router_scores(t, e, k, groups, keep, score, dtype, bias):
+    x, b = make(t, e, dtype, bias, seed=e + k)
+    check(x, k, score, b, groups, keep, renorm=(t % 2 == 0), scale=1.0 if t % 3 else 2.5)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,keep", [(1, 1), (8, 4)])
+@pytest.mark.parametrize("bias", [None, 0.05])
+def test_many_tokens(score, groups, keep, bias):
+    # some of 200000 tokens have neighbours that fp32 cannot tell apart
+    x, b = make(200000, 256, "float32", bias, seed=7)
+    check(x, 8, score, b, groups, keep)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_equal_values(score):
+    # bf16 logits from a handful of values, and a bias of few values: ties everywhere
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = (torch.randint(-3, 4, (3000, 128), generator=g, device="cuda") / 2).to(torch.bfloat16)
+    for bias in (None, torch.zeros(128, device="cuda"), torch.randint(0, 2, (128,), generator=g, device="cuda") / 8.0):
+        check(x, 8, score, bias)
+        check(x, 6, score, bias, 8, 3)
+    same = torch.zeros(5, 256, device="cuda")
+    check(same, 8, score, None, 8, 2)
+    check(same, 8, score, torch.zeros(256, device="cuda"), 16, 16)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_neighbouring_floats(score):
+    # logits one step of fp32 apart: no score in 32 bits tells them apart
+    base = torch.tensor(0.7, device="cuda")
+    steps = torch.arange(64, device="cuda", dtype=torch.int32)
+    row = (base.view(torch.int32) + steps).view(torch.float32)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.stack([row[torch.randperm(64, generator=g, device="cuda")] for _ in range(200)])
+    check(x, 8, score)
+    check(x, 8, score, None, 4, 2)
+    check(x, 8, score, 1e-8 * torch.randn(64, generator=g, device="cuda"))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("size", [1e-6, 30.0, 1e4, 1e30])
+def test_biases_of_any_size(score, size):
+    x, b = make(500, 96, "float32", size, seed=5)
+    check(x, 8, score, b)
+    check(x, 4, score, b, 6, 2)
+    check(x, 8, score, torch.full((96,), size, device="cuda"))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_logits_at_the_extremes(score):
+    x, b = make(300, 64, std=3.0, seed=9)
+    x[:, 5] = -INF
+    x[1, :60] = -INF        # four experts left for eight places
+    x[2] = x[2] * 25        # far below the largest: scores that vanish in fp32
+    x[3] = 80 + x[3]        # sigmoids that round to one
+    x[4] = -80 + x[4]
+    for bias in (None, b):
+        check(x[:2], 8, score, bias, renorm=False) if score == "sigmoid" or bias is None else None
+    check(x, 8, score)
+    check(x, 4, score, None, 8, 8)
+    import attention_softmax_sinks_gb300 as sa
+    out = torch.full((3, 64), -INF, device="cuda")  # nothing to choose from: the first experts, without weight
+    idx, w = sa.moe_router_scores(out, 8, score=score)
+    assert torch.equal(idx.cpu(), torch.arange(8, dtype=torch.int32).repeat(3, 1)) and bool((w == 0).all())
+
+
+def test_disabled_experts():
+    x, b = make(100, 64, seed=2)
+    bias = torch.zeros(64, device="cuda")
+    bias[::2] = -INF
+    check(x, 8, "sigmoid", bias)
+    check(x, 8, "softmax", bias, 4, 2)
+
+
+def test_not_a_number_stays_in_range():
+    import attention_softmax_sinks_gb300 as sa
+    x, b = make(64, 256, seed=4)
+    x[::2, ::3] = float("nan")
+    x[1] = float("nan")
+    x[3, :9] = INF
+    for bias in (None, torch.randn(256, device="cuda"), torch.full((256,), float("nan"), device="cuda")):
+        for groups, keep in ((1, 1), (8, 3)):
+            idx, _ = sa.moe_router_scores(x, 8, "sigmoid", bias, groups, keep)
+            assert bool(((idx >= 0) & (idx < 256)).all())
+
+
+def test_unaligned_rows():
+    base = torch.randn(50 * 64 + 3, device="cuda")
+    for off in (1, 2, 3):
+        check(base[off : off + 50 * 64].reshape(50, 64), 4, "sigmoid", None, 4, 2)
+    half = base.to(torch.bfloat16)
+    for off in (1, 2, 3):
+        check(half[off : off + 50 * 64].reshape(50, 64), 4)
+
+
+def test_no_tokens():
+    import attention_softmax_sinks_gb300 as sa
+    idx, w, c = sa.moe_router_scores(torch.empty(0, 64, device="cuda"), 4, return_counts=True)
+    assert idx.shape == (0, 4) and bool((c == 0).all())
+
+
+def test_outputs_stream_and_graph():
+    import attention_softmax_sinks_gb300 as sa
+    x, b = make(500, 256, bias=0.1)
+    args = dict(score="sigmoid", bias=b, num_groups=8, top_groups=4, scale=2.5)
+    want = sa.moe_router_scores(x, 8, **args)
+    idx = torch.full((510, 8), -9, dtype=torch.int32, device="cuda")
+    w = torch.full((510, 8), -9.0, dtype=torch.bfloat16, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    sa.moe_router_scores(x, 8, **args, topk_idx=idx[:500], topk_weight=w[:500], stream=s)
+    s.synchronize()
+    assert torch.equal(idx[:500], want[0]) and torch.equal(w[:500], want[1])
+    assert bool((idx[500:] == -9).all()) and bool((w[500:] == -9).all())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        gi, gw, gc = sa.moe_router_scores(x, 8, **args, return_counts=True)
+    x.copy_(make(500, 256, seed=8)[0])
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    ri, rw = reference(x, 8, "sigmoid", b, 8, 4, True, 2.5)
+    assert torch.equal(gi.long(), ri) and torch.equal(gc.long(), torch.bincount(ri.reshape(-1), minlength=256))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_experts_that_share_a_huge_bias(score):
+    x, _ = make(300, 64, seed=6)
+    bias = torch.zeros(64, device="cuda")
+    bias[7::5] = 1e20
+    check(x, 8, score, bias)
+    check(x, 6, score, bias, 8, 4)
