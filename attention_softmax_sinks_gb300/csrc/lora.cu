@@ -279,6 +279,7 @@ constexpr int kMaxBlockN = 224;
 constexpr int kTCols = 32;      // TMEM columns of a T buffer: 64 values of K, four chunks of 16 ranks
 constexpr int kChunks = 4;      // chunks of 16 ranks per ring stage
 constexpr int kRingBytes = 196 * 1024;
+constexpr int kStageTarget = 24 * 1024;  // bytes of a ring stage, where blocks are smaller
 constexpr uint32_t kTmemCols = 512;
 // An MMA reads 128 rows of x also where a box has fewer: behind the last stage, too, that stays
 // inside the allocation (what it reads there goes to accumulator rows that are never stored).
@@ -375,10 +376,39 @@ __device__ __noinline__ float single_element(const LoraArgs& a, const int32_t* p
   return sum;
 }
 
-__host__ __device__ constexpr int stage_bytes(int box_rows, int bn) { return (box_rows + bn) * kBK * 2; }
+// A ring stage holds `sub` blocks of 64 values of K: small tiles' blocks are a few KB, and a stage's
+// way round the ring costs the same for one as for four.
+__host__ __device__ constexpr int block_bytes(int box_rows, int bn) { return (box_rows + bn) * kBK * 2; }
+__host__ __device__ constexpr int stage_blocks(int box_rows, int bn) {
+  const int n = kStageTarget / block_bytes(box_rows, bn);
+  return n >= 4 ? 4 : n >= 2 ? 2 : 1;
+}
+__host__ __device__ constexpr int stage_bytes(int box_rows, int bn) {
+  return stage_blocks(box_rows, bn) * block_bytes(box_rows, bn);
+}
 __host__ __device__ constexpr int stage_count(int box_rows, int bn) {
   const int n = kRingBytes / stage_bytes(box_rows, bn);
   return n > kMaxStages ? kMaxStages : n;
+}
+
+// Position in the ring: stage index and number of rounds made.
+struct RingPos {
+  int stage = 0;
+  uint32_t round = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++stage == stages) {
+      stage = 0;
+      ++round;
+    }
+  }
+};
+
+// One lane of a converged warp, always the same one: what it issues stays in a warp-uniform region
+// (from a divergent branch an MMA takes about 125 cycles to issue).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 __host__ __device__ constexpr int acc_columns(int bn) { return (bn + 31) / 32 * 32; }
 __host__ __device__ constexpr int t_bufs(int bn) {
@@ -398,9 +428,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = &sb.abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tiles_total = a.tiles_m * a.tiles_n;
-  const int k_steps = (a.K + kBK - 1) / kBK;
   const int bn = a.block_n;
-  const int stages = stage_count(a.box_rows, bn), sbytes = stage_bytes(a.box_rows, bn), xbytes = a.box_rows * kBK * 2;
+  const int sub = stage_blocks(a.box_rows, bn), stages = stage_count(a.box_rows, bn);
+  const int xbytes = a.box_rows * kBK * 2, bbytes = block_bytes(a.box_rows, bn), sbytes = sub * bbytes;
+  const int k_blocks = (a.K + kBK - 1) / kBK, k_stages = (k_blocks + sub - 1) / sub;
   const int tbufs = t_bufs(bn);
   const uint32_t acc_stride = acc_columns(bn), t_col = 2 * acc_stride;
 
@@ -433,106 +464,125 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sb.tmem_base;
-  // Ring stages of a tile behind its k_steps: four chunks of 16 ranks each.  Only these, and
+  const uint32_t ring = smem_u32(tiles);
+  // Ring stages of a tile behind those of K: four chunks of 16 ranks each.  Only these, and
   // whatever is written, wait for the first kernel.
   auto adapter_stages = [&](int slots) { return (slots * RC + kChunks - 1) / kChunks; };
 
   if (warp == 0) {
     // ------------------------------------------------------------------ loads
-    const uint64_t pol_x = l2_policy_evict_last();  // x: read by the CTAs of every column tile
-    const uint64_t pol_w = l2_policy_evict_last();  // W: read again by every row block
-    int g = 0;  // ring stages so far
+    const uint64_t policy = l2_policy_evict_last();  // x is read for every column tile, W for every row block
+    RingPos p;
+    int issued = 0;
     bool ok = true;
+    // the stage is free (all lanes agree)
+    auto free_stage = [&]() {
+      return p.round == 0 || wait_or_abort(smem_u32(&sb.empty[p.stage]), (p.round - 1) & 1, a.timeout_ns, abort_flag);
+    };
     for (int t = blockIdx.x; t < tiles_total && ok; t += gridDim.x) {
       const int mt = t / a.tiles_n;
       const int m0 = mt * kBM, n0 = (t % a.tiles_n) * bn;
-      if (lane == 0) {
-        for (int kb = 0; kb < k_steps; ++kb) {
-          const int gg = g + kb, s = gg % stages;
-          if (gg >= stages && !wait_or_abort(smem_u32(&sb.empty[s]), ((gg / stages) - 1) & 1, a.timeout_ns, abort_flag)) {
-            ok = false;
-            break;
+      for (int ks = 0; ks < k_stages; ++ks, p.next(stages)) {
+        ok = __all_sync(0xffffffffu, free_stage());
+        if (!ok) break;
+        const int blocks = min(sub, k_blocks - ks * sub);
+        if (elect_one()) {
+          const uint32_t bar = smem_u32(&sb.full[p.stage]);
+          mbar_arrive_expect_tx(bar, blocks * bbytes);
+          for (int u = 0; u < blocks; ++u) {
+            const uint32_t dst = ring + p.stage * sbytes + u * bbytes;
+            const int x = (ks * sub + u) * kBK;
+            tma_load_2d(dst, &xmap, x, m0, bar, policy);  // rows past M are zero-filled
+            tma_load_2d(dst + xbytes, &wmap, x, n0, bar, policy);
           }
-          const uint32_t bar = smem_u32(&sb.full[s]);
-          const uint32_t dst = smem_u32(tiles) + s * sbytes;
-          mbar_arrive_expect_tx(bar, sbytes);
-          tma_load_2d(dst, &xmap, kb * kBK, m0, bar, pol_x);  // rows past M are zero-filled
-          tma_load_2d(dst + xbytes, &wmap, kb * kBK, n0, bar, pol_w);
-          sb.issued = gg + 1;
+          sb.issued = ++issued;
         }
       }
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-      g += k_steps;
       if (!ok) break;
       pdl_wait_primary();  // the plan
       const int32_t* plan = a.plan + static_cast<long long>(mt) * kLoraPlanInts;
       const int slots = __ldcg(plan);
       int held = 0;  // adapters of 32 slots, one per lane
-      for (int e = 0; e < adapter_stages(slots) && ok; ++e, ++g) {
-        const int first = e * kChunks, n = min(kChunks, slots * RC - first), s = g % stages;
-        if (e == 0 || (first / RC) % 32 < (first - kChunks) / RC % 32) {  // entering the next 32 slots
-          const int i = (first / RC) / 32 * 32 + lane;
+      for (int e = 0; e < adapter_stages(slots); ++e, p.next(stages)) {
+        const int first = e * kChunks, n = min(kChunks, slots * RC - first);
+        if (first % (32 * RC) == 0) {  // entering the next 32 slots
+          const int i = first / RC + lane;
           held = i < slots ? __ldcg(plan + kLoraPlanList + i) : 0;
         }
-        if (lane == 0) {
-          if (g >= stages && !wait_or_abort(smem_u32(&sb.empty[s]), ((g / stages) - 1) & 1, a.timeout_ns, abort_flag)) ok = false;
-          else mbar_arrive_expect_tx(smem_u32(&sb.full[s]), n * bn * 32);
-        }
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        ok = __all_sync(0xffffffffu, free_stage());
         if (!ok) break;
-        for (int c = 0; c < n; ++c) {
-          const int id = __shfl_sync(0xffffffffu, held, (first + c) / RC % 32);
-          if (lane == 0)
-            tma_load_3d(smem_u32(tiles) + s * sbytes + c * bn * 32, &bmap, (first + c) % RC * 16, n0, id, smem_u32(&sb.full[s]), pol_w);
+        int id[kChunks];
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) id[c] = __shfl_sync(0xffffffffu, held, (first + c) / RC % 32);
+        if (elect_one()) {
+          const uint32_t bar = smem_u32(&sb.full[p.stage]);
+          mbar_arrive_expect_tx(bar, n * bn * 32);
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c)
+            if (c < n)
+              tma_load_3d(ring + p.stage * sbytes + c * bn * 32, &bmap, (first + c) % RC * 16, n0, id[c], bar, policy);
+          sb.issued = ++issued;
         }
-        if (lane == 0) sb.issued = g + 1;
       }
     }
     if (!ok && lane == 0) raise_status(a.status, kStatusTimeout);
   } else if (warp == 1) {
     // ------------------------------------------------------------------ products
-    if (lane == 0) {
-      const uint32_t idesc = idesc_bf16_kk(kBM, bn);
-      int g = 0, i = 0, ge = 0;  // ring stages, tiles, T buffers so far
-      bool ok = true;
-      for (int t = blockIdx.x; t < tiles_total && ok; t += gridDim.x, ++i) {
-        const int b = i & 1;
-        ok = wait_or_abort(smem_u32(&sb.acc_empty[b]), (i >> 1) & 1, a.timeout_ns, abort_flag);
+    const uint32_t idesc = idesc_bf16_kk(kBM, bn);
+    RingPos p, tb;
+    int i = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < tiles_total && ok; t += gridDim.x, ++i) {
+      const int b = i & 1;
+      ok = __all_sync(0xffffffffu, wait_or_abort(smem_u32(&sb.acc_empty[b]), (i >> 1) & 1, a.timeout_ns, abort_flag));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d = tmem + b * acc_stride;
+      for (int ks = 0; ks < k_stages; ++ks, p.next(stages)) {
+        ok = __all_sync(0xffffffffu, wait_or_abort(smem_u32(&sb.full[p.stage]), p.round & 1, a.timeout_ns, abort_flag));
         if (!ok) break;
         tc_fence_after();
-        const uint32_t d = tmem + b * acc_stride;
-        for (int kb = 0; kb < k_steps; ++kb, ++g) {
-          const int s = g % stages;
-          ok = wait_or_abort(smem_u32(&sb.full[s]), (g / stages) & 1, a.timeout_ns, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t x_addr = smem_u32(tiles) + s * sbytes, w_addr = x_addr + xbytes;
+        const uint32_t stage = ring + p.stage * sbytes;
+        const int blocks = min(sub, k_blocks - ks * sub);
+        if (elect_one()) {
+#pragma unroll 1
+          for (int u = 0; u < blocks; ++u) {
+            const uint64_t xd = sw128_kmajor(stage + u * bbytes), wd = sw128_kmajor(stage + u * bbytes + xbytes);
 #pragma unroll
-          for (int kk = 0; kk < kBK / 16; ++kk)
-            tc_mma_ss(d, sw128_kmajor(x_addr + kk * 32), sw128_kmajor(w_addr + kk * 32), idesc, 1u);
-          tc_commit(smem_u32(&sb.empty[s]));
+            for (int kk = 0; kk < kBK / 16; ++kk) tc_mma_ss(d, xd + 2 * kk, wd + 2 * kk, idesc, 1u);
+          }
+          tc_commit(smem_u32(&sb.empty[p.stage]));
         }
-        if (!ok) break;
-        pdl_wait_primary();
-        const int slots = __ldcg(a.plan + static_cast<long long>(t / a.tiles_n) * kLoraPlanInts);
-        for (int e = 0; e < adapter_stages(slots); ++e, ++g, ++ge) {
-          const int n = min(kChunks, slots * RC - e * kChunks), s = g % stages, tb = ge % tbufs;
-          ok = wait_or_abort(smem_u32(&sb.t_full[tb]), (ge / tbufs) & 1, a.timeout_ns, abort_flag) &&
-               wait_or_abort(smem_u32(&sb.full[s]), (g / stages) & 1, a.timeout_ns, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t b_addr = smem_u32(tiles) + s * sbytes, t_addr = tmem + t_col + tb * kTCols;
-          for (int c = 0; c < n; ++c) tc_mma_ts(d, t_addr + c * 8, sw32_kmajor(b_addr + c * bn * 32), idesc, 1u);
-          tc_commit(smem_u32(&sb.t_empty[tb]));
-          tc_commit(smem_u32(&sb.empty[s]));
-        }
-        if (ok) tc_commit(smem_u32(&sb.acc_full[b]));
       }
+      if (!ok) break;
+      pdl_wait_primary();
+      const int slots = __ldcg(a.plan + static_cast<long long>(t / a.tiles_n) * kLoraPlanInts);
+      for (int e = 0; e < adapter_stages(slots); ++e, p.next(stages), tb.next(tbufs)) {
+        const int n = min(kChunks, slots * RC - e * kChunks);
+        ok = wait_or_abort(smem_u32(&sb.t_full[tb.stage]), tb.round & 1, a.timeout_ns, abort_flag) &&
+             wait_or_abort(smem_u32(&sb.full[p.stage]), p.round & 1, a.timeout_ns, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t t_addr = tmem + t_col + tb.stage * kTCols;
+          const uint64_t bd = sw32_kmajor(ring + p.stage * sbytes);
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c)
+            if (c < n) tc_mma_ts(d, t_addr + c * 8, bd + 2 * c * bn, idesc, 1u);
+          tc_commit(smem_u32(&sb.t_empty[tb.stage]));
+          tc_commit(smem_u32(&sb.empty[p.stage]));
+        }
+      }
+      if (ok && elect_one()) tc_commit(smem_u32(&sb.acc_full[b]));
+    }
+    if (elect_one()) {
       if (!ok) raise_status(a.status, kStatusTimeout);
       // every product issued by this thread has finished before TMEM is released
       tc_commit(smem_u32(&sb.drain));
       if (!mbar_wait(smem_u32(&sb.drain), 0, kDrainTimeoutNs)) raise_status(a.status, kStatusTimeout);
     }
+    __syncwarp();
   } else if (warp >= 4) {
     // ------------------------------------------------------------------ T and epilogue
     const int q = warp & 3;  // TMEM lane quarter
@@ -546,7 +596,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(smem_u32(&sb.acc_empty[j]));
     }
     pdl_wait_primary();  // plan and t; and no output before the first kernel's end
-    int i = 0, ge = 0, held_mt = -1, slots = 0, my_slot = -1;
+    RingPos tb;
+    int i = 0, held_mt = -1, slots = 0, my_slot = -1;
     uint32_t tp[8 * RC];  // s t of this thread's row, bf16 pairs
 #pragma unroll
     for (int e = 0; e < 8 * RC; ++e) tp[e] = 0;
@@ -581,12 +632,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      for (int e = 0; e < adapter_stages(slots); ++e, ++ge) {
-        const int tb = ge % tbufs;
-        if (ge >= tbufs && !wait_or_abort(smem_u32(&sb.t_empty[tb]), ((ge / tbufs) - 1) & 1, a.timeout_ns, abort_flag)) {
+      for (int e = 0; e < adapter_stages(slots); ++e, tb.next(tbufs)) {
+        if (tb.round != 0 &&
+            !wait_or_abort(smem_u32(&sb.t_empty[tb.stage]), (tb.round - 1) & 1, a.timeout_ns, abort_flag)) {
           ok = false;
           break;
         }
+        __syncwarp();
         tc_fence_after();
         uint32_t r[32];
         if constexpr (RC <= kChunks) {  // whole slots per buffer
@@ -602,12 +654,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int w = 0; w < 32; ++w) r[w] = own ? (upper ? tp[32 + w] : tp[w]) : 0u;
         }
-        const uint32_t dst = lane_base + t_col + tb * kTCols;
+        const uint32_t dst = lane_base + t_col + tb.stage * kTCols;
         tmem_st16_at<0>(dst, r);
         tmem_st16_at<16>(dst + 16, r);
         tc_wait_st();
         tc_fence_before();
-        mbar_arrive(smem_u32(&sb.t_full[tb]));
+        mbar_arrive(smem_u32(&sb.t_full[tb.stage]));
       }
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;

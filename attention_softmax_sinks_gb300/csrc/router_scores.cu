@@ -8,14 +8,16 @@
 // Which experts are chosen is a question of order, and is answered as in exact arithmetic, equal
 // values in favour of the lower index:
 //  - Eight lanes per token; lane j holds experts 4 (j + 8 i) + c.  What is ordered becomes a
-//    32-bit key: 24 bits of fixed point and 255 - expert.  The fixed point holds x - max x in
-//    [-32, 0] where there is no bias (scores and logits have the same order), else s + bias over
-//    its range.  Keys sort with one min and one max per comparison: sorting networks per lane,
-//    then three rounds of merging between lanes.
-//  - A key is off by a few units from what it stands for.  Where two neighbours among the chosen,
-//    or the last chosen and the first not chosen, or the last group kept and the first dropped are
-//    closer than that and not equal in logit and bias, the token is done once more in fp64, by
-//    the whole warp (one token in some thousands for logits in 32 bits).
+//    32-bit key: 24 bits of fixed point and 255 - expert.  The fixed point holds s + bias over its
+//    range; without bias and groups x - max x in [-32, 0] (scores and logits have the same order).
+//    Keys sort with one min and one max per comparison: sorting networks per lane, then three
+//    rounds of merging between lanes.  (A lane's keys differ from each other without j, which is
+//    added to the few that leave the lane.)
+//  - A key is off by a few units from what it stands for.  Where the last group kept and the first
+//    dropped, or two neighbours among the chosen, or the last chosen and the first not chosen are
+//    closer than that, and not equal in logit and bias, the experts within reach of that border
+//    are compared once more in fp64, a lane for each (two tokens in a thousand for logits in 32
+//    bits, about 2 us for a warp that has one); more than 32 of them by a walk over all experts.
 //
 // What bounds it: at many tokens the instructions (about 1000 per four tokens), not the logits'
 // way from memory; at few the latency of one pass.
@@ -38,14 +40,40 @@ constexpr unsigned kFull = 0xffffffffu;
 // rounded by at most 2^-20 (half a unit), to a unit by another half, for each of the two.  Scores:
 // exp2 and reciprocal err by 2^-22 and 2^-23 relative, the exponent's rounding by 2^-24 |x| e^-|x|;
 // with the sums' roundings at most 2^-21.5 of a range of at least 1, 6 units, for each of the two.
+// A merit is the sum of two.
 constexpr uint32_t kNear = 16;
-// Merits are sums of two scores and biases in fp32: the same errors, relative to their sizes.
-constexpr float kNearMerit = 1.0f / (1 << 19);
+constexpr float kKeyRange = 16777000.0f;  // keys are 1 .. 2^24 - 1
 
 __device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// 24 bits of fixed point of what is ordered: 1 .. 2^24 - 1 (what is not a number becomes 1:
+// conversion to unsigned saturates).  bias_key: 1 + the bias's part.
+template <bool kSigmoid, bool kScored>
+__device__ __forceinline__ uint32_t fixed_point(float x, float ref, float unit, float soft_unit, float bias_key) {
+  if constexpr (!kScored) return __float2uint_rn(fmaxf((x - ref + 32.0f) * 524287.0f, 0.0f) + 1.0f);
+  float f;
+  if constexpr (kSigmoid) f = fmaf(rcp(1.0f + ex2(-x * kLog2e)), unit, bias_key);
+  else f = fmaf(ex2((x - ref) * kLog2e), soft_unit, bias_key);
+  return max(__float2uint_rn(f), 1u);
+}
+
+template <bool kSigmoid>
+__device__ __forceinline__ float weight_of(float x, float ref, float inv_sum) {
+  return kSigmoid ? 1.0f / (1.0f + expf(-x)) : expf(x - ref) * inv_sum;
+}
+
+// The r-th choice of token t: its score and the sum of the chosen ones'.
+__device__ __forceinline__ void write_choice(const RouterScoresArgs& a, int* hist, long long t, int r, int expert, float score,
+                                             float sum) {
+  float w = a.scale * score;
+  if (a.renormalize) w = sum > 0.0f ? a.scale * (score / sum) : 0.0f;
+  a.topk_idx[t * a.top_k + r] = expert;
+  a.topk_w[t * a.top_k + r] = static_cast<uint16_t>(pack_bf16x2(w, 0.0f) & 0xFFFFu);
+  if (a.counts) atomicAdd(&hist[expert], 1);
 }
 
 template <int N>
@@ -114,6 +142,8 @@ struct WarpScratch {
     Wide value[256];  // the whole warp's one token, done again
   };
   Wide merit[kRouterMaxGroups];
+  uint32_t second[kRouterMaxGroups];
+  int list[32];
 };
 
 __device__ __forceinline__ float load_logit(const RouterScoresArgs& a, long long t, int e) {
@@ -129,9 +159,9 @@ __device__ __forceinline__ bool same_inputs(const RouterScoresArgs& a, long long
   return load_logit(a, t, e) == load_logit(a, t, f) && bias_of(a, e) == bias_of(a, f);
 }
 
-// Token t once more, in fp64, by the whole warp.  picked[r] on every lane: the experts (some in
-// range, whatever the logits are: what is not a number counts as -inf).
-__device__ __noinline__ void choose_exactly(const RouterScoresArgs& a, WarpScratch& ws, long long t, int (&picked)[8]) {
+// Token t in fp64 over all experts, by the whole warp.  picked[r] on every lane: the experts (some
+// in range, whatever the logits are: what is not a number counts as -inf).
+__device__ __noinline__ void choose_among_all(const RouterScoresArgs& a, WarpScratch& ws, long long t, int (&picked)[8]) {
   const int lane = threadIdx.x & 31;
   const int E = a.num_experts;
   double top = -__builtin_huge_val(), sum = 0.0;
@@ -218,63 +248,218 @@ __device__ __noinline__ void choose_exactly(const RouterScoresArgs& a, WarpScrat
   __syncwarp();
 }
 
-template <int K, bool kFp32, bool kSigmoid, bool kBias>
+// Expert e's s + bias of token t in fp64 (its logit where that has the same order).
+__device__ __forceinline__ Wide exact_value(const RouterScoresArgs& a, long long t, int e, double top, double sum, bool scored) {
+  const double x = load_logit(a, t, e);
+  if (!scored) return wide_sum(x, 0.0);
+  return wide_sum(a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - top) / sum, bias_of(a, e));
+}
+
+// The token's largest logit and, for scores by softmax, the sum below it.
+__device__ __forceinline__ void exact_sum(const RouterScoresArgs& a, long long t, bool scored, double& top, double& sum) {
+  const int lane = threadIdx.x & 31;
+  top = -__builtin_huge_val();
+  sum = 0.0;
+  if (a.sigmoid || !scored) return;
+  double x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[i] = lane + 32 * i < a.num_experts ? static_cast<double>(load_logit(a, t, lane + 32 * i)) : -__builtin_huge_val();
+    top = fmax(top, x[i]);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) top = fmax(top, __shfl_xor_sync(kFull, top, off));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum += exp(x[i] - top);  // (independent of each other)
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
+}
+
+// Experts whose key (24 bits, in ws.key[0]; 0: not to be chosen) is at least that of their place
+// `floor`, listed in expert order in ws.list.  Returns their number.
+template <typename Floor>
+__device__ __forceinline__ int list_candidates(WarpScratch& ws, int E, Floor floor) {
+  const int lane = threadIdx.x & 31;
+  int n = 0;
+  for (int e0 = 0; e0 < E; e0 += 32) {
+    const int e = e0 + lane;
+    const bool in = e < E && ws.key[0][e] != 0 && ws.key[0][e] >= floor(e);
+    const unsigned m = __ballot_sync(kFull, in);
+    const int at = n + __popc(m & ((1u << lane) - 1));
+    if (in && at < 32) ws.list[at] = e;
+    n += __popc(m);
+  }
+  __syncwarp();
+  return n;
+}
+
+__device__ __forceinline__ Wide from_lane(const Wide& v, int lane) {
+  return {__shfl_sync(kFull, v.hi, lane), __shfl_sync(kFull, v.lo, lane)};
+}
+
+__device__ __forceinline__ uint32_t below_by(uint32_t q, uint32_t d) { return q > d ? q - d : 0u; }
+
+// Token t by the whole warp, with the comparisons that keys cannot settle made in fp64; writes its
+// results.  bias_key, unit: as in the kernel.
+template <bool kSigmoid, bool kScored>
+__device__ __noinline__ void settle(const RouterScoresArgs& a, WarpScratch& ws, int* hist, const float* bias_key, float unit,
+                                    long long t) {
+  const int lane = threadIdx.x & 31;
+  const int E = a.num_experts, k = a.top_k, size = E / a.num_groups;
+  const bool grouped = kScored && a.top_groups < a.num_groups;
+  // ---- the keys once more, in expert order, without the experts' codes
+  float x[8], ref = kNegInf, total = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[i] = lane + 32 * i < E ? load_logit(a, t, lane + 32 * i) : kNegInf;
+    ref = fmaxf(ref, x[i]);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) ref = fmaxf(ref, __shfl_xor_sync(kFull, ref, off));
+  if (ref == kNegInf) ref = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) total += ex2((x[i] - ref) * kLog2e);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(kFull, total, off);
+  const float inv_sum = total > 0.0f ? 1.0f / total : 0.0f;
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int e = lane + 32 * i;
+    if (e < E) ws.key[0][e] = fixed_point<kSigmoid, kScored>(x[i], ref, unit, unit * inv_sum, kScored ? bias_key[e] : 0.0f);
+  }
+  __syncwarp();
+  int picked[8];
+  bool walk = false;
+  // ---- groups: the candidates for the two largest of each
+  if (grouped) {
+    if (lane < a.num_groups) {
+      uint32_t first = 0, second = 0;
+      for (int i = 0; i < size; ++i) {
+        const uint32_t v = ws.key[0][lane * size + i];
+        second = max(second, min(first, v));
+        first = max(first, v);
+      }
+      ws.second[lane] = size > 1 ? second : first;
+    }
+    __syncwarp();
+    const int n = list_candidates(ws, E, [&](int e) { return below_by(ws.second[e / size], kNear); });
+    walk = n > 32;
+    if (!walk) {
+      double top, sum;
+      exact_sum(a, t, true, top, sum);
+      const int e = lane < n ? ws.list[lane] : 0;
+      const Wide v = exact_value(a, t, e, top, sum, true);
+      const int mine = lane < n ? e / size : -1;
+      Wide first = least(), second = least();  // of group `lane`
+      for (int i = 0; i < n; ++i) {
+        const Wide w = from_lane(v, i);
+        if (__shfl_sync(kFull, mine, i) == lane) {
+          if (above(w, first)) {
+            second = first;
+            first = w;
+          } else if (above(w, second)) {
+            second = w;
+          }
+        }
+      }
+      Wide merit = first;
+      if (size > 1) {
+        const Wide s = wide_sum(first.hi, second.hi);
+        merit = wide_sum(s.hi, s.lo + (first.lo + second.lo));
+      }
+      int before = 0;
+      for (int g = 0; g < a.num_groups; ++g) {
+        const Wide w = from_lane(merit, g);
+        before += above(w, merit) || (g < lane && !above(merit, w));
+      }
+      const unsigned kept = __ballot_sync(kFull, lane < a.num_groups && before < a.top_groups);
+      for (int e2 = lane; e2 < E; e2 += 32)
+        if (!(kept >> (e2 / size) & 1)) ws.key[0][e2] = 0;
+      __syncwarp();
+    }
+  }
+  // ---- the k-th largest key, and in fp64 all that are near it or above
+  if (!walk) {
+    uint32_t last = 0xffffffffu;
+    for (int r = 0; r < k; ++r) {
+      uint32_t most = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int e = lane + 32 * i;
+        const uint32_t v = e < E && ws.key[0][e] != 0 ? ws.key[0][e] << 8 | (255 - e) : 0u;
+        if (v < last) most = max(most, v);
+      }
+      last = __reduce_max_sync(kFull, most);
+    }
+    const uint32_t floor = below_by(last >> 8, kNear);
+    const int n = list_candidates(ws, E, [&](int) { return floor; });
+    walk = n > 32;
+    if (!walk) {
+      const bool scored = a.bias != nullptr;  // else the logits' order is the answer
+      double top, sum;
+      exact_sum(a, t, scored, top, sum);
+      const int e = lane < n ? ws.list[lane] : 0;
+      const Wide v = exact_value(a, t, e, top, sum, scored);
+      int rank = 0;
+      for (int i = 0; i < n; ++i) {
+        const Wide w = from_lane(v, i);
+        rank += above(w, v) || (i < lane && !above(v, w));  // candidates are in expert order
+      }
+      if (lane >= n) rank = 32;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const unsigned m = __ballot_sync(kFull, rank == r);
+        picked[r] = __shfl_sync(kFull, e, m ? __ffs(m) - 1 : 0);
+      }
+    }
+  }
+  if (walk) choose_among_all(a, ws, t, picked);
+  int expert = 0;
+#pragma unroll
+  for (int r = 0; r < 8; ++r)
+    if (lane == r) expert = picked[r];
+  float mine = lane < k ? weight_of<kSigmoid>(load_logit(a, t, expert), ref, inv_sum) : 0.0f;
+  float sum = mine;
+#pragma unroll
+  for (int off = 1; off < kLanes; off <<= 1) sum += __shfl_xor_sync(kFull, sum, off);
+  if (lane < k) write_choice(a, hist, t, lane, expert, mine, sum);
+  __syncwarp();
+}
+
+// kScored: keys hold s + bias (0 without one), else x - max x.
+template <int K, bool kFp32, bool kSigmoid, bool kScored>
 __global__ void __launch_bounds__(256, 2) router_scores_kernel(const RouterScoresArgs a) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   __shared__ int hist[256];
-  __shared__ float bias_range[2];  // least finite bias, keys per unit of score
+  __shared__ __align__(16) float bias_key[256];  // 1 + the bias's part of a key
+  __shared__ float key_unit[1];                  // keys per unit of score
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   WarpScratch& ws = reinterpret_cast<WarpScratch*>(smem_raw)[warp];
   const int E = a.num_experts, k = a.top_k;
   const int j = lane % kLanes, tok = lane / kLanes;
-  const bool grouped = a.top_groups < a.num_groups;
+  const bool grouped = kScored && a.top_groups < a.num_groups;
   const int size = E / a.num_groups;
   const int inv_size = (65536 + size - 1) / size;  // e / size == (e * inv_size) >> 16 for e < 256
-  for (int e = threadIdx.x; e < E; e += blockDim.x) hist[e] = 0;
-  if constexpr (kBias) {
-    if (warp == 0) {
-      float lo = __builtin_huge_valf(), hi = kNegInf;
-      for (int e = lane; e < E; e += 32) {
-        const float b = __ldg(a.bias + e);
-        if (fabsf(b) <= 3.4e38f) {
-          lo = fminf(lo, b);
-          hi = fmaxf(hi, b);
-        }
-      }
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) {
-        lo = fminf(lo, __shfl_xor_sync(kFull, lo, off));
-        hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, off));
-      }
-      if (lane == 0) {
-        bias_range[0] = lo <= hi ? lo : 0.0f;
-        bias_range[1] = lo <= hi ? 16777000.0f / (1.0f + (hi - lo)) : 16777000.0f;
-      }
-    }
-  }
-  __syncthreads();
-  const float base = kBias ? bias_range[0] : 0.0f, per_unit = kBias ? bias_range[1] : 0.0f;
   const long long warps = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
   const long long passes = (a.num_tokens + kTokens - 1) / kTokens;
-  for (long long p = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + warp; p < passes; p += warps) {
-    const long long t = p * kTokens + tok;
-    const bool live = t < a.num_tokens;  // the lanes of a token agree
-    const long long tt = live ? t : a.num_tokens - 1;
-    // ---- logits
-    float x[kOwn];
+  long long p = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + warp;
+  auto token_of = [&](long long pass) { return min(pass * kTokens + tok, a.num_tokens - 1); };  // lanes behind: the last one
+  float x[kOwn];
+  auto load = [&](long long t) {
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       const int e = 4 * (j + kLanes * i);
       if (a.vec4) {
         if (kFp32) {
-          const float4 v = e < E ? __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + tt * E + e))
+          const float4 v = e < E ? __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + t * E + e))
                                  : make_float4(kNegInf, kNegInf, kNegInf, kNegInf);
           x[4 * i] = v.x;
           x[4 * i + 1] = v.y;
           x[4 * i + 2] = v.z;
           x[4 * i + 3] = v.w;
         } else {
-          const uint2 v = e < E ? __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.logits) + tt * E + e))
+          const uint2 v = e < E ? __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.logits) + t * E + e))
                                 : make_uint2(0xFF80FF80u, 0xFF80FF80u);
           x[4 * i] = __uint_as_float(v.x << 16);
           x[4 * i + 1] = __uint_as_float(v.x & 0xFFFF0000u);
@@ -283,17 +468,51 @@ __global__ void __launch_bounds__(256, 2) router_scores_kernel(const RouterScore
         }
       } else {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) x[4 * i + c] = e + c < E ? load_logit(a, tt, e + c) : kNegInf;
+        for (int c = 0; c < 4; ++c) x[4 * i + c] = e + c < E ? load_logit(a, t, e + c) : kNegInf;
       }
     }
+  };
+  if (p < passes) load(token_of(p));  // on their way during the set-up
+  for (int e = threadIdx.x; e < 256; e += blockDim.x) hist[e] = 0;
+  if constexpr (kScored) {
+    if (warp == 0) {
+      float b[8], lo = __builtin_huge_valf(), hi = kNegInf;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        b[i] = lane + 32 * i < E ? bias_of(a, lane + 32 * i) : 0.0f;
+        if (lane + 32 * i < E && fabsf(b[i]) <= 3.4e38f) {
+          lo = fminf(lo, b[i]);
+          hi = fmaxf(hi, b[i]);
+        }
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) {
+        lo = fminf(lo, __shfl_xor_sync(kFull, lo, off));
+        hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, off));
+      }
+      if (!(lo <= hi)) lo = hi = 0.0f;
+      const float unit = kKeyRange / (1.0f + (hi - lo));
+      // b - lo first: what is rounded is small beside the range
+#pragma unroll
+      for (int i = 0; i < 8; ++i) bias_key[lane + 32 * i] = fminf(fmaxf((b[i] - lo) * unit, -4e7f), kKeyRange - unit) + 1.0f;
+      if (lane == 0) key_unit[0] = unit;
+    }
+  }
+  __syncthreads();
+  const float unit = kScored ? key_unit[0] : 0.0f;
+  for (; p < passes; p += warps) {
+    const long long t = p * kTokens + tok, tt = token_of(p);
+    const bool live = t < a.num_tokens;  // the lanes of a token agree
     // ---- maximum, and for the softmax the sum
-    float top = x[0];
+    float ref = 0.0f, inv_sum = 1.0f;
+    if constexpr (!kSigmoid || !kScored) {
+      float top = x[0];
 #pragma unroll
-    for (int i = 1; i < kOwn; ++i) top = fmaxf(top, x[i]);
+      for (int i = 1; i < kOwn; ++i) top = fmaxf(top, x[i]);
 #pragma unroll
-    for (int off = 1; off < kLanes; off <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
-    const float ref = top == kNegInf ? 0.0f : top;
-    float inv_sum = 1.0f;
+      for (int off = 1; off < kLanes; off <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+      ref = top == kNegInf ? 0.0f : top;
+    }
     if constexpr (!kSigmoid) {
       float sum = 0.0f;
 #pragma unroll
@@ -302,22 +521,26 @@ __global__ void __launch_bounds__(256, 2) router_scores_kernel(const RouterScore
       for (int off = 1; off < kLanes; off <<= 1) sum += __shfl_xor_sync(kFull, sum, off);
       inv_sum = sum > 0.0f ? 1.0f / sum : 0.0f;
     }
-    auto score = [&](float v) { return kSigmoid ? rcp(1.0f + ex2(-v * kLog2e)) : ex2((v - ref) * kLog2e) * inv_sum; };
-    // ---- keys
+    // ---- keys, without 4 (7 - j): vector i, element c of a lane
     uint32_t key[kOwn];
+    const float soft_unit = unit * inv_sum;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       const int e = 4 * (j + kLanes * i);
+      float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
+      if constexpr (kScored) b = *reinterpret_cast<const float4*>(&bias_key[e]);
+      const float bc[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        float f;
-        if constexpr (kBias) f = (score(x[4 * i + c]) + ((e + c < E ? __ldg(a.bias + e + c) : 0.0f) - base)) * per_unit;
-        else f = (x[4 * i + c] - ref + 32.0f) * 524287.0f;
-        const uint32_t q = __float2uint_rn(fminf(fmaxf(f, 0.0f), 16777214.0f)) + 1;  // 1 .. 2^24 - 1
-        key[4 * i + c] = e + c < E ? (q << 8) | (255u - static_cast<uint32_t>(e + c)) : 0u;
+        const uint32_t q = fixed_point<kSigmoid, kScored>(x[4 * i + c], ref, unit, soft_unit, bc[c]);
+        key[4 * i + c] = (q << 8) + (32 * (kVecs - 1 - i) + 3 - c);
+        if (e + c >= E) key[4 * i + c] = 0;
       }
     }
-    bool doubt = false;  // the order of two groups or experts is not certain
+    if (p + warps < passes) load(token_of(p + warps));
+    const uint32_t lane_code = 4 * (kLanes - 1 - j);
+    auto expert_of = [](uint32_t full_key) { return 255 - static_cast<int>(full_key & 255u); };
+    bool doubt = false;  // some comparison is not certain
     // ---- groups
     if (grouped) {
 #pragma unroll
@@ -325,71 +548,87 @@ __global__ void __launch_bounds__(256, 2) router_scores_kernel(const RouterScore
         *reinterpret_cast<uint4*>(&ws.key[tok][4 * (j + kLanes * i)]) =
             make_uint4(key[4 * i], key[4 * i + 1], key[4 * i + 2], key[4 * i + 3]);
       __syncwarp();
-      // lane j of a token takes groups j, j + 8, ..: their two largest keys, then their merits
-      float merit[kRouterMaxGroups / kLanes];
+      // lane j of a token takes groups j, j + 8, ..: the sum of their two largest keys
+      constexpr int kMine = kRouterMaxGroups / kLanes;
+      uint32_t merit[kMine];
 #pragma unroll
-      for (int n = 0; n < kRouterMaxGroups / kLanes; ++n) {
+      for (int n = 0; n < kMine; ++n) {
         const int g = j + kLanes * n;
-        merit[n] = kNegInf;
+        merit[n] = 0;
         if (g < a.num_groups) {
           uint32_t first = 0, second = 0;
-          int at = (4 * j + tok) % size;  // lanes begin in different banks
-          for (int i = 0; i < size; ++i) {
-            const uint32_t v = ws.key[tok][g * size + at];
+          auto take = [&](uint32_t v) {
             second = max(second, min(first, v));
             first = max(first, v);
-            at = at + 1 == size ? 0 : at + 1;
+          };
+          const uint32_t* from = &ws.key[tok][g * size];
+          if (size % 4 == 0) {
+            int at = 4 * j % size;  // the lanes of a token begin in different banks
+            for (int i = 0; i < size; i += 4) {
+              const uint4 v = *reinterpret_cast<const uint4*>(from + at);
+              take(v.x);
+              take(v.y);
+              take(v.z);
+              take(v.w);
+              at = at + 4 == size ? 0 : at + 4;
+            }
+          } else {
+            for (int i = 0; i < size; ++i) take(from[i]);
           }
-          const int e1 = 255 - static_cast<int>(first & 255u), e2 = 255 - static_cast<int>(second & 255u);
-          merit[n] = score(load_logit(a, tt, e1)) + bias_of(a, e1);
-          if (size > 1) merit[n] += score(load_logit(a, tt, e2)) + bias_of(a, e2);
+          merit[n] = (first >> 8) + (size > 1 ? second >> 8 : 0u);
         }
       }
       // a group is kept if fewer than top_groups come before it
       unsigned kept = 0;
-      float last_kept = __builtin_huge_valf(), first_dropped = kNegInf;
+      uint32_t last_kept = 0xffffffffu, first_dropped = 0;
 #pragma unroll
-      for (int n = 0; n < kRouterMaxGroups / kLanes; ++n) {
-        int before = 0;
+      for (int n = 0; n < kMine; ++n) {
+        if (kLanes * n < a.num_groups) {
+          int before = 0;
 #pragma unroll
-        for (int m = 0; m < kRouterMaxGroups / kLanes; ++m) {
-          if (kLanes * m < a.num_groups) {
+          for (int m = 0; m < kMine; ++m) {
+            if (kLanes * m < a.num_groups) {
 #pragma unroll
-            for (int l = 0; l < kLanes; ++l) {
-              const float other = __shfl_sync(kFull, merit[m], (lane & ~(kLanes - 1)) + l);
-              before += other > merit[n] || (other == merit[n] && l + kLanes * m < j + kLanes * n);
+              for (int l = 0; l < kLanes; ++l) {
+                const uint32_t other = __shfl_sync(kFull, merit[m], (lane & ~(kLanes - 1)) + l);
+                before += other > merit[n] || (other == merit[n] && l + kLanes * m < j + kLanes * n);
+              }
+            }
+          }
+          if (j + kLanes * n < a.num_groups) {
+            if (before < a.top_groups) {
+              kept |= 1u << (j + kLanes * n);
+              last_kept = min(last_kept, merit[n]);
+            } else {
+              first_dropped = max(first_dropped, merit[n]);
             }
           }
         }
-        if (j + kLanes * n < a.num_groups) {
-          if (before < a.top_groups) {
-            kept |= 1u << (j + kLanes * n);
-            last_kept = fminf(last_kept, merit[n]);
-          } else {
-            first_dropped = fmaxf(first_dropped, merit[n]);
-          }
-        }
-        if (kLanes * (n + 1) >= a.num_groups) break;
       }
 #pragma unroll
       for (int off = 1; off < kLanes; off <<= 1) {
         kept |= __shfl_xor_sync(kFull, kept, off);
-        last_kept = fminf(last_kept, __shfl_xor_sync(kFull, last_kept, off));
-        first_dropped = fmaxf(first_dropped, __shfl_xor_sync(kFull, first_dropped, off));
+        last_kept = min(last_kept, __shfl_xor_sync(kFull, last_kept, off));
+        first_dropped = max(first_dropped, __shfl_xor_sync(kFull, first_dropped, off));
       }
-      // (a tie in merit is settled in fp64 as well)
-      float near = kNearMerit * (1.0f + fabsf(last_kept) + fabsf(first_dropped));
-      if constexpr (kBias) near += 4.0f * static_cast<float>(kNear) / per_unit;
-      doubt = !(last_kept - first_dropped > near);
+      doubt = last_kept - first_dropped <= 2 * kNear;  // a tie in merit as well
 #pragma unroll
-      for (int i = 0; i < kOwn; ++i) {
-        const int e = 4 * (j + kLanes * (i >> 2)) + (i & 3);
-        if (!(kept >> ((e * inv_size) >> 16) & 1)) key[i] = 0;
+      for (int i = 0; i < kVecs; ++i) {
+        const int e = 4 * (j + kLanes * i);
+        if (size % 4 == 0) {
+          const uint32_t in = 0u - (kept >> ((e * inv_size) >> 16) & 1);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) key[4 * i + c] &= in;
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (!(kept >> (((e + c) * inv_size) >> 16) & 1)) key[4 * i + c] = 0;
+        }
       }
       __syncwarp();
     }
     // ---- the K largest keys
-    uint32_t best[K];
+    uint32_t best[K], local[K];
 #pragma unroll
     for (int r = 0; r < K; ++r) best[r] = key[r];
     sort_keys<K>(best);
@@ -402,6 +641,11 @@ __global__ void __launch_bounds__(256, 2) router_scores_kernel(const RouterScore
       merge_keys<K>(best, part);
     }
 #pragma unroll
+    for (int r = 0; r < K; ++r) {
+      if (best[r]) best[r] += lane_code;
+      local[r] = best[r];
+    }
+#pragma unroll
     for (int off = 1; off < kLanes; off <<= 1) {
       uint32_t other[K];
 #pragma unroll
@@ -412,9 +656,17 @@ __global__ void __launch_bounds__(256, 2) router_scores_kernel(const RouterScore
 #pragma unroll
     for (int r = 1; r < K; ++r)
       if (r < k) last = best[r];
-    uint32_t next = 0;  // the largest key not chosen
+    // the largest key not chosen: the first of a lane's list below the last chosen
+    uint32_t next = 0;
 #pragma unroll
-    for (int i = 0; i < kOwn; ++i) next = max(next, key[i] < last ? key[i] : 0u);
+    for (int r = 0; r < K; ++r) next = max(next, local[r] < last ? local[r] : 0u);
+    if (__any_sync(kFull, local[K - 1] >= last)) {  // a lane whose whole list was chosen: its other keys
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) {
+        const uint32_t full_key = key[i] ? key[i] + lane_code : 0u;
+        next = max(next, full_key < last ? full_key : 0u);
+      }
+    }
 #pragma unroll
     for (int off = 1; off < kLanes; off <<= 1) next = max(next, __shfl_xor_sync(kFull, next, off));
     // ---- neighbours too close to be certain, unless logit and bias are the same
@@ -424,45 +676,25 @@ __global__ void __launch_bounds__(256, 2) router_scores_kernel(const RouterScore
         uint32_t below = next;
         if constexpr (K > 1)
           if (r + 1 < K && r + 1 < k) below = best[r + 1 < K ? r + 1 : r];
-        if (below != 0 && (best[r] >> 8) - (below >> 8) <= kNear &&
-            !same_inputs(a, tt, 255 - static_cast<int>(best[r] & 255u), 255 - static_cast<int>(below & 255u)))
+        if (below != 0 && (best[r] >> 8) - (below >> 8) <= kNear && !same_inputs(a, tt, expert_of(best[r]), expert_of(below)))
           doubt = true;
       }
     }
-    // ---- experts of the token, on all of its lanes
-    int picked[8];
-#pragma unroll
-    for (int r = 0; r < 8; ++r) picked[r] = r < K ? 255 - static_cast<int>(best[r < K ? r : 0] & 255u) : 0;
-    unsigned again = __ballot_sync(kFull, doubt && live && j == 0);
-    while (again) {
-      const int first = __ffs(again) - 1;  // lane 0 of the token
-      again &= again - 1;
-      int exact[8];
-      choose_exactly(a, ws, p * kTokens + first / kLanes, exact);
-      if (tok == first / kLanes) {
-#pragma unroll
-        for (int r = 0; r < 8; ++r) picked[r] = exact[r];
-      }
-    }
-    // ---- weights: lane j writes the j-th
-    float mine = 0.0f;
+    // ---- lane j of a token: its j-th expert
     int expert = 0;
 #pragma unroll
-    for (int r = 0; r < 8; ++r)
-      if (j == r) expert = picked[r];
-    if (j < k) {
-      const float v = load_logit(a, tt, expert);
-      mine = kSigmoid ? 1.0f / (1.0f + expf(-v)) : expf(v - ref) * inv_sum;
-    }
+    for (int r = 0; r < K; ++r)
+      if (j == r) expert = expert_of(best[r]);
+    const float mine = j < k ? weight_of<kSigmoid>(load_logit(a, tt, expert), ref, inv_sum) : 0.0f;
     float sum = mine;
 #pragma unroll
     for (int off = 1; off < kLanes; off <<= 1) sum += __shfl_xor_sync(kFull, sum, off);
-    if (live && j < k) {
-      float w = a.scale * mine;
-      if (a.renormalize) w = sum > 0.0f ? a.scale * (mine / sum) : 0.0f;
-      a.topk_idx[t * k + j] = expert;
-      a.topk_w[t * k + j] = static_cast<uint16_t>(pack_bf16x2(w, 0.0f) & 0xFFFFu);
-      if (a.counts) atomicAdd(&hist[expert], 1);
+    if (live && !doubt && j < k) write_choice(a, hist, t, j, expert, mine, sum);
+    unsigned again = __ballot_sync(kFull, doubt && live && j == 0);
+    while (again) {
+      const int lead = __ffs(again) - 1;  // lane 0 of the token
+      again &= again - 1;
+      settle<kSigmoid, kScored>(a, ws, hist, bias_key, unit, p * kTokens + lead / kLanes);
     }
   }
   if (a.counts) {
@@ -478,10 +710,11 @@ cudaError_t launch_scores(const RouterScoresArgs& a, int sms, cudaStream_t strea
   const long long passes = (a.num_tokens + kTokens - 1) / kTokens;
   const int warps = passes <= 2LL * sms ? 1 : 8;
   const long long blocks = (passes + warps - 1) / warps;
-  const long long most = 4LL * sms;  // resident ones
+  const long long most = 2LL * sms;  // resident ones
   const int grid = static_cast<int>(blocks < most ? blocks : most);
   const size_t smem = warps * sizeof(WarpScratch);
-  if (a.bias) router_scores_kernel<K, kFp32, kSigmoid, true><<<grid, 32 * warps, smem, stream>>>(a);
+  if (a.bias || a.top_groups < a.num_groups)
+    router_scores_kernel<K, kFp32, kSigmoid, true><<<grid, 32 * warps, smem, stream>>>(a);
   else router_scores_kernel<K, kFp32, kSigmoid, false><<<grid, 32 * warps, smem, stream>>>(a);
   return cudaGetLastError();
 }
@@ -495,8 +728,7 @@ cudaError_t launch_scores_k(const RouterScoresArgs& a, int sms, cudaStream_t str
 }  // namespace
 
 cudaError_t launch_router_scores(const RouterScoresArgs& a, int sms, cudaStream_t stream) {
-  if (a.top_k == 1) return launch_scores_k<1>(a, sms, stream);
-  if (a.top_k == 2) return launch_scores_k<2>(a, sms, stream);
+  if (a.top_k <= 2) return launch_scores_k<2>(a, sms, stream);
   if (a.top_k <= 4) return launch_scores_k<4>(a, sms, stream);
   return launch_scores_k<8>(a, sms, stream);
 }

@@ -84,6 +84,13 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int m, int n, bool b_mn_major)
 constexpr uint32_t kIdescS = idesc_bf16(128, 128, false);
 constexpr uint32_t kIdescPV = idesc_bf16(128, 64, true);
 
+// One lane of a converged warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // Bounded wait that also gives up as soon as another role has aborted.
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint64_t timeout_ns, volatile int* abort_flag) {
   if (mbar_try_wait(bar, parity)) return true;
@@ -279,45 +286,54 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1 || warp == 2) {
       // ------------------------------------------------------------ products
       const int t = warp - 1;
-      if (lane == 0 && t < ntiles) {
+      if (t < ntiles) {
         const uint32_t tmem = tmem_base();
         const uint32_t d_s = tmem + kColS + t * 128, d_o = tmem + kColO + t * 64, a_p = tmem + kColP + t * 64;
-        bool ok = wait_bar(smem_u32(&sm.q_ready[t]), 0, a.timeout_ns, abort_flag);
-        const uint32_t q_addr = smem_u32(sm.q[t]);
+        auto wait = [&](uint64_t& bar, int parity) {
+          return __all_sync(0xffffffffu, wait_bar(smem_u32(&bar), parity & 1, a.timeout_ns, abort_flag)) != 0;
+        };
+        bool ok = wait(sm.q_ready[t], 0);
+        const uint64_t qd = sw128_desc(smem_u32(sm.q[t]));
         auto s_step = [&](int j) {  // S(j) = Q K_j^T
-          ok = wait_bar(smem_u32(&sm.kv_full[j % kStages]), (j / kStages) & 1, a.timeout_ns, abort_flag);
+          ok = wait(sm.kv_full[j % kStages], j / kStages);
           if (!ok) return;
           tc_fence_after();
-          const uint32_t k_addr = smem_u32(sm.k[j % kStages]);
+          if (elect_one()) {
+            const uint64_t kd = sw128_desc(smem_u32(sm.k[j % kStages]));
 #pragma unroll
-          for (int kk = 0; kk < kHeadDim / 16; ++kk)
-            tc_mma_ss(d_s, sw128_desc(q_addr + kk * 32), sw128_desc(k_addr + kk * 32), kIdescS, kk > 0);
-          tc_commit(smem_u32(&sm.s_full[t]));
+            for (int kk = 0; kk < kHeadDim / 16; ++kk) tc_mma_ss(d_s, qd + 2 * kk, kd + 2 * kk, kIdescS, kk > 0);
+            tc_commit(smem_u32(&sm.s_full[t]));
+          }
         };
         auto pv_step = [&](int j) {  // O += P(j) V_j
-          ok = wait_bar(smem_u32(&sm.p_full[t]), j & 1, a.timeout_ns, abort_flag);
+          ok = wait(sm.p_full[t], j);
           if (!ok) return;
           tc_fence_after();
-          const uint32_t v_addr = smem_u32(sm.v[j % kStages]);
+          if (elect_one()) {
+            const uint64_t vd = sw128_desc(smem_u32(sm.v[j % kStages]));
 #pragma unroll
-          for (int kk = 0; kk < kBlockK / 16; ++kk)
-            tc_mma_ts(d_o, a_p + kk * 8, sw128_desc(v_addr + kk * 16 * 128), kIdescPV, (j > 0 || kk > 0) ? 1u : 0u);
-          tc_commit(smem_u32(&sm.pv_done[t]));
-          tc_commit(smem_u32(&sm.kv_empty[j % kStages]));
+            for (int kk = 0; kk < kBlockK / 16; ++kk)
+              tc_mma_ts(d_o, a_p + kk * 8, vd + kk * (16 * 128 / 16), kIdescPV, (j > 0 || kk > 0) ? 1u : 0u);
+            tc_commit(smem_u32(&sm.pv_done[t]));
+            tc_commit(smem_u32(&sm.kv_empty[j % kStages]));
+          }
         };
         if (ok) s_step(0);
         for (int j = 0; j < n_kv && ok; ++j) {
           if (j >= 1) pv_step(j - 1);
           if (ok && j + 1 < n_kv) {
-            ok = wait_bar(smem_u32(&sm.s_free[t]), j & 1, a.timeout_ns, abort_flag);
+            ok = wait(sm.s_free[t], j);
             if (ok) s_step(j + 1);
           }
         }
         if (ok) pv_step(n_kv - 1);
-        if (!ok) raise_status(a.status, kStatusTimeout);
-        // whatever happened, every product issued here is done before TMEM is released
-        tc_commit(smem_u32(&sm.drain[t]));
-        mbar_wait(smem_u32(&sm.drain[t]), 0, kDrainTimeoutNs);
+        if (elect_one()) {
+          if (!ok) raise_status(a.status, kStatusTimeout);
+          // whatever happened, every product issued here is done before TMEM is released
+          tc_commit(smem_u32(&sm.drain[t]));
+          mbar_wait(smem_u32(&sm.drain[t]), 0, kDrainTimeoutNs);
+        }
+        __syncwarp();
       }
     }
   } else {

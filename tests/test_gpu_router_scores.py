@@ -155,7 +155,8 @@ def test_not_a_number_stays_in_range():
     x[::2, ::3] = float("nan")
     x[1] = float("nan")
     x[3, :9] = INF
-    for bias in (None, torch.randn(256, device="cuda"), torch.full((256,), float("nan"), device="cuda")):
+    for bias in (None, torch.randn(256, device="cuda"), torch.full((256,), float("nan"), device="cuda"),
+                 torch.where(torch.arange(256, device="cuda") % 7 == 0, INF, 0.0)):
         for groups, keep in ((1, 1), (8, 3)):
             idx, _ = sa.moe_router_scores(x, 8, "sigmoid", bias, groups, keep)
             assert bool(((idx >= 0) & (idx < 256)).all())
