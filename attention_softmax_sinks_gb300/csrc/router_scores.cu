@@ -33,6 +33,8 @@ constexpr int kLanes = 8;                    // per token
 constexpr int kTokens = 32 / kLanes;         // per warp
 constexpr int kVecs = 256 / (4 * kLanes);    // vectors of four experts per lane
 constexpr int kOwn = 4 * kVecs;
+constexpr int kBlock = 256;
+constexpr int kMaxDoubtful = 64;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr unsigned kFull = 0xffffffffu;
@@ -50,15 +52,13 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
-// 24 bits of fixed point of what is ordered: 1 .. 2^24 - 1 (what is not a number becomes 1:
-// conversion to unsigned saturates).  bias_key: 1 + the bias's part.
+// 24 bits of fixed point of what is ordered, 1 .. 2^24 - 1; 0 for what is not a number and for a
+// bias of -inf (conversion to unsigned saturates).  bias_key: 1 + the bias's part.
 template <bool kSigmoid, bool kScored>
 __device__ __forceinline__ uint32_t fixed_point(float x, float ref, float unit, float soft_unit, float bias_key) {
   if constexpr (!kScored) return __float2uint_rn(fmaxf((x - ref + 32.0f) * 524287.0f, 0.0f) + 1.0f);
-  float f;
-  if constexpr (kSigmoid) f = fmaf(rcp(1.0f + ex2(-x * kLog2e)), unit, bias_key);
-  else f = fmaf(ex2((x - ref) * kLog2e), soft_unit, bias_key);
-  return max(__float2uint_rn(f), 1u);
+  if constexpr (kSigmoid) return __float2uint_rn(fmaf(rcp(1.0f + ex2(-x * kLog2e)), unit, bias_key));
+  return __float2uint_rn(fmaf(ex2((x - ref) * kLog2e), soft_unit, bias_key));
 }
 
 template <bool kSigmoid>
@@ -133,17 +133,34 @@ __device__ __forceinline__ Wide wide_sum(double x, double y) {
   if (s != s) return {-__builtin_huge_val(), 0.0};  // not a number: the least
   return {s, isinf(s) ? 0.0 : e};
 }
-__device__ __forceinline__ bool above(const Wide& v, const Wide& w) { return v.hi > w.hi || (v.hi == w.hi && v.lo > w.lo); }
+// The same as two integers that sort like it: comparisons of doubles take tens of cycles here.
+struct Order {
+  long long hi, lo;
+};
+__device__ __forceinline__ long long order_of(double v) {
+  const long long b = __double_as_longlong(v + 0.0);  // (-0 becomes 0)
+  return b ^ (b >> 63 & 0x7fffffffffffffffll);
+}
+__device__ __forceinline__ Order order_of(const Wide& v) { return {order_of(v.hi), order_of(v.lo)}; }
+__device__ __forceinline__ bool above(const Order& v, const Order& w) { return v.hi > w.hi || (v.hi == w.hi && v.lo > w.lo); }
+__device__ __forceinline__ Order order_from(const Order& v, int lane) {
+  return {__shfl_sync(kFull, v.hi, lane), __shfl_sync(kFull, v.lo, lane)};
+}
 __device__ __forceinline__ Wide least() { return {-__builtin_huge_val(), 0.0}; }
+// Merit of a group from its two largest values.
+__device__ __forceinline__ Wide merit_of(const Wide& first, const Wide& second) {
+  const Wide s = wide_sum(first.hi, second.hi);
+  return wide_sum(s.hi, s.lo + (first.lo + second.lo));
+}
 
 struct WarpScratch {
   union {
     uint32_t key[kTokens][256];
     Wide value[256];  // the whole warp's one token, done again
   };
-  Wide merit[kRouterMaxGroups];
   uint32_t second[kRouterMaxGroups];
   int list[32];
+  uint32_t kept[kTokens][kRouterMaxGroups];  // first experts of the groups kept
 };
 
 __device__ __forceinline__ float load_logit(const RouterScoresArgs& a, long long t, int e) {
@@ -159,55 +176,66 @@ __device__ __forceinline__ bool same_inputs(const RouterScoresArgs& a, long long
   return load_logit(a, t, e) == load_logit(a, t, f) && bias_of(a, e) == bias_of(a, f);
 }
 
+// Expert e's s + bias of token t in fp64 (its logit where that has the same order).
+template <bool kSigmoid>
+__device__ __noinline__ Wide exact_value(const RouterScoresArgs& a, long long t, int e, double top, double sum, bool scored) {
+  const double x = load_logit(a, t, e);
+  if (!scored) return wide_sum(x, 0.0);
+  return wide_sum(kSigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - top) / sum, bias_of(a, e));
+}
+
+// The token's largest logit and, for scores by softmax, the sum below it.
+template <bool kSigmoid>
+__device__ __forceinline__ void exact_sum(const RouterScoresArgs& a, long long t, bool scored, double& top, double& sum) {
+  const int lane = threadIdx.x & 31;
+  top = 0.0;
+  sum = 1.0;
+  if (kSigmoid || !scored) return;
+  float most = kNegInf;
+  for (int e = lane; e < a.num_experts; e += 32) most = fmaxf(most, load_logit(a, t, e));
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(kFull, most, off));
+  top = most;
+  sum = 0.0;
+#pragma unroll 2
+  for (int e = lane; e < a.num_experts; e += 32) sum += exp(static_cast<double>(load_logit(a, t, e)) - top);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
+}
+
 // Token t in fp64 over all experts, by the whole warp.  picked[r] on every lane: the experts (some
 // in range, whatever the logits are: what is not a number counts as -inf).
+template <bool kSigmoid>
 __device__ __noinline__ void choose_among_all(const RouterScoresArgs& a, WarpScratch& ws, long long t, int (&picked)[8]) {
   const int lane = threadIdx.x & 31;
-  const int E = a.num_experts;
-  double top = -__builtin_huge_val(), sum = 0.0;
-  for (int e = lane; e < E; e += 32) top = fmax(top, static_cast<double>(load_logit(a, t, e)));
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) top = fmax(top, __shfl_xor_sync(kFull, top, off));
+  const int E = a.num_experts, size = E / a.num_groups;
   const bool grouped = a.num_groups > a.top_groups;
   const bool scored = a.bias != nullptr || grouped;  // else the logits' order is the answer
-  if (!a.sigmoid && scored) {
-    for (int e = lane; e < E; e += 32) sum += exp(static_cast<double>(load_logit(a, t, e)) - top);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
-  }
+  double top, sum;
+  exact_sum<kSigmoid>(a, t, scored, top, sum);
   __syncwarp();
-  for (int e = lane; e < E; e += 32) {
-    const double x = load_logit(a, t, e);
-    if (scored) ws.value[e] = wide_sum(a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - top) / sum, bias_of(a, e));
-    else ws.value[e] = wide_sum(x, 0.0);
-  }
+  for (int e = lane; e < E; e += 32) ws.value[e] = exact_value<kSigmoid>(a, t, e, top, sum, scored);
   __syncwarp();
   unsigned kept = kFull;
-  const int size = E / a.num_groups;
   if (grouped) {
-    Wide mine = least();
+    Wide first = least(), second = least();
     if (lane < a.num_groups) {
-      Wide first = least(), second = first;
       for (int i = 0; i < size; ++i) {
         const Wide v = ws.value[lane * size + i];
-        if (above(v, first)) {
+        if (above(order_of(v), order_of(first))) {
           second = first;
           first = v;
-        } else if (above(v, second)) {
+        } else if (above(order_of(v), order_of(second))) {
           second = v;
         }
       }
-      mine = first;
-      if (size > 1) {
-        const Wide s = wide_sum(first.hi, second.hi);
-        mine = wide_sum(s.hi, s.lo + (first.lo + second.lo));
-      }
-      ws.merit[lane] = mine;
     }
-    __syncwarp();
+    const Order merit = order_of(size > 1 ? merit_of(first, second) : first);
     int before = 0;
-    if (lane < a.num_groups)
-      for (int g = 0; g < a.num_groups; ++g) before += above(ws.merit[g], mine) || (g < lane && !above(mine, ws.merit[g]));
+    for (int g = 0; g < a.num_groups; ++g) {
+      const Order w = order_from(merit, g);
+      before += above(w, merit) || (g < lane && !above(merit, w));
+    }
     kept = __ballot_sync(kFull, lane < a.num_groups && before < a.top_groups);
   }
   // without a bias the logits decide between experts (scores may round to the same number)
@@ -218,61 +246,35 @@ __device__ __noinline__ void choose_among_all(const RouterScoresArgs& a, WarpScr
   }
   unsigned taken = 0;  // which of this lane's experts (lane + 32 i)
   constexpr int kNone = 1 << 20;
-#pragma unroll
-  for (int r = 0; r < 8; ++r) {
-    if (r >= a.top_k) break;
-    Wide best = least();
+#pragma unroll 1
+  for (int r = 0; r < a.top_k; ++r) {
+    Order best = order_of(least());
     int at = kNone;
     for (int i = 0; i < 8; ++i) {
       const int e = lane + 32 * i;
       if (e < E && !(taken >> i & 1) && (kept >> (grouped ? e / size : 0) & 1)) {
-        const Wide v = ws.value[e];
+        const Order v = order_of(ws.value[e]);
         if (at == kNone || above(v, best)) {
           best = v;
           at = e;
         }
       }
     }
-#pragma unroll
+#pragma unroll 1
     for (int off = 16; off > 0; off >>= 1) {
-      const Wide v = {__shfl_xor_sync(kFull, best.hi, off), __shfl_xor_sync(kFull, best.lo, off)};
+      const Order v = {__shfl_xor_sync(kFull, best.hi, off), __shfl_xor_sync(kFull, best.lo, off)};
       const int f = __shfl_xor_sync(kFull, at, off);
       if (f != kNone && (at == kNone || above(v, best) || (!above(best, v) && f < at))) {
         best = v;
         at = f;
       }
     }
-    picked[r] = at;
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+      if (s == r) picked[s] = at;
     if ((at & 31) == lane) taken |= 1u << (at >> 5);
   }
   __syncwarp();
-}
-
-// Expert e's s + bias of token t in fp64 (its logit where that has the same order).
-__device__ __forceinline__ Wide exact_value(const RouterScoresArgs& a, long long t, int e, double top, double sum, bool scored) {
-  const double x = load_logit(a, t, e);
-  if (!scored) return wide_sum(x, 0.0);
-  return wide_sum(a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - top) / sum, bias_of(a, e));
-}
-
-// The token's largest logit and, for scores by softmax, the sum below it.
-__device__ __forceinline__ void exact_sum(const RouterScoresArgs& a, long long t, bool scored, double& top, double& sum) {
-  const int lane = threadIdx.x & 31;
-  top = -__builtin_huge_val();
-  sum = 0.0;
-  if (a.sigmoid || !scored) return;
-  double x[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[i] = lane + 32 * i < a.num_experts ? static_cast<double>(load_logit(a, t, lane + 32 * i)) : -__builtin_huge_val();
-    top = fmax(top, x[i]);
-  }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) top = fmax(top, __shfl_xor_sync(kFull, top, off));
-#pragma unroll
-  for (int i = 0; i < 8; ++i) sum += exp(x[i] - top);  // (independent of each other)
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
 }
 
 // Experts whose key (24 bits, in ws.key[0]; 0: not to be chosen) is at least that of their place
@@ -291,10 +293,6 @@ __device__ __forceinline__ int list_candidates(WarpScratch& ws, int E, Floor flo
   }
   __syncwarp();
   return n;
-}
-
-__device__ __forceinline__ Wide from_lane(const Wide& v, int lane) {
-  return {__shfl_sync(kFull, v.hi, lane), __shfl_sync(kFull, v.lo, lane)};
 }
 
 __device__ __forceinline__ uint32_t below_by(uint32_t q, uint32_t d) { return q > d ? q - d : 0u; }
@@ -326,7 +324,8 @@ __device__ __noinline__ void settle(const RouterScoresArgs& a, WarpScratch& ws, 
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int e = lane + 32 * i;
-    if (e < E) ws.key[0][e] = fixed_point<kSigmoid, kScored>(x[i], ref, unit, unit * inv_sum, kScored ? bias_key[e] : 0.0f);
+    if (e < E)  // 0 stands for experts of other groups here
+      ws.key[0][e] = max(fixed_point<kSigmoid, kScored>(x[i], ref, unit, unit * inv_sum, kScored ? bias_key[e] : 0.0f), 1u);
   }
   __syncwarp();
   int picked[8];
@@ -347,30 +346,33 @@ __device__ __noinline__ void settle(const RouterScoresArgs& a, WarpScratch& ws, 
     walk = n > 32;
     if (!walk) {
       double top, sum;
-      exact_sum(a, t, true, top, sum);
+      exact_sum<kSigmoid>(a, t, true, top, sum);
       const int e = lane < n ? ws.list[lane] : 0;
-      const Wide v = exact_value(a, t, e, top, sum, true);
-      const int mine = lane < n ? e / size : -1;
-      Wide first = least(), second = least();  // of group `lane`
+      const Wide v = exact_value<kSigmoid>(a, t, e, top, sum, true);
+      const Order mine = order_of(v);
+      const int group = lane < n ? e / size : -1;
+      int first = -1, second = -1;  // the lanes with the two largest of group `lane`
+      Order of_first = order_of(least()), of_second = of_first;
       for (int i = 0; i < n; ++i) {
-        const Wide w = from_lane(v, i);
-        if (__shfl_sync(kFull, mine, i) == lane) {
-          if (above(w, first)) {
+        const Order w = order_from(mine, i);
+        if (__shfl_sync(kFull, group, i) == lane) {
+          if (first < 0 || above(w, of_first)) {
             second = first;
-            first = w;
-          } else if (above(w, second)) {
-            second = w;
+            of_second = of_first;
+            first = i;
+            of_first = w;
+          } else if (second < 0 || above(w, of_second)) {
+            second = i;
+            of_second = w;
           }
         }
       }
-      Wide merit = first;
-      if (size > 1) {
-        const Wide s = wide_sum(first.hi, second.hi);
-        merit = wide_sum(s.hi, s.lo + (first.lo + second.lo));
-      }
+      const Wide v1 = {__shfl_sync(kFull, v.hi, max(first, 0)), __shfl_sync(kFull, v.lo, max(first, 0))};
+      const Wide v2 = {__shfl_sync(kFull, v.hi, max(second, 0)), __shfl_sync(kFull, v.lo, max(second, 0))};
+      const Order merit = order_of(size > 1 ? merit_of(v1, v2) : v1);
       int before = 0;
       for (int g = 0; g < a.num_groups; ++g) {
-        const Wide w = from_lane(merit, g);
+        const Order w = order_from(merit, g);
         before += above(w, merit) || (g < lane && !above(merit, w));
       }
       const unsigned kept = __ballot_sync(kFull, lane < a.num_groups && before < a.top_groups);
@@ -398,13 +400,13 @@ __device__ __noinline__ void settle(const RouterScoresArgs& a, WarpScratch& ws, 
     if (!walk) {
       const bool scored = a.bias != nullptr;  // else the logits' order is the answer
       double top, sum;
-      exact_sum(a, t, scored, top, sum);
+      exact_sum<kSigmoid>(a, t, scored, top, sum);
       const int e = lane < n ? ws.list[lane] : 0;
-      const Wide v = exact_value(a, t, e, top, sum, scored);
+      const Order mine = order_of(exact_value<kSigmoid>(a, t, e, top, sum, scored));
       int rank = 0;
       for (int i = 0; i < n; ++i) {
-        const Wide w = from_lane(v, i);
-        rank += above(w, v) || (i < lane && !above(v, w));  // candidates are in expert order
+        const Order w = order_from(mine, i);
+        rank += above(w, mine) || (i < lane && !above(mine, w));  // candidates are in expert order
       }
       if (lane >= n) rank = 32;
 #pragma unroll
@@ -414,7 +416,7 @@ __device__ __noinline__ void settle(const RouterScoresArgs& a, WarpScratch& ws, 
       }
     }
   }
-  if (walk) choose_among_all(a, ws, t, picked);
+  if (walk) choose_among_all<kSigmoid>(a, ws, t, picked);
   int expert = 0;
 #pragma unroll
   for (int r = 0; r < 8; ++r)
@@ -428,12 +430,16 @@ __device__ __noinline__ void settle(const RouterScoresArgs& a, WarpScratch& ws, 
 }
 
 // kScored: keys hold s + bias (0 without one), else x - max x.
+// The sorting runs over the keys in shared memory, eight at a time in a loop: unrolled over a
+// lane's 32 keys the pass is 27 KB of code, and warps wait for instructions a third of the time.
 template <int K, bool kFp32, bool kSigmoid, bool kScored>
-__global__ void __launch_bounds__(256, 2) router_scores_kernel(const RouterScoresArgs a) {
+__global__ void __launch_bounds__(kBlock, 3) router_scores_kernel(const RouterScoresArgs a) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   __shared__ int hist[256];
   __shared__ __align__(16) float bias_key[256];  // 1 + the bias's part of a key
-  __shared__ float key_unit[1];                  // keys per unit of score
+  __shared__ float key_unit;                     // keys per unit of score
+  __shared__ long long doubtful[kMaxDoubtful];   // tokens left for the end
+  __shared__ int num_doubtful;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   WarpScratch& ws = reinterpret_cast<WarpScratch*>(smem_raw)[warp];
   const int E = a.num_experts, k = a.top_k;
@@ -441,6 +447,7 @@ __global__ void __launch_bounds__(256, 2) router_scores_kernel(const RouterScore
   const bool grouped = kScored && a.top_groups < a.num_groups;
   const int size = E / a.num_groups;
   const int inv_size = (65536 + size - 1) / size;  // e / size == (e * inv_size) >> 16 for e < 256
+  int vecs = (E + 4 * kLanes - 1) / (4 * kLanes);  // vectors of a lane that hold experts
   const long long warps = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
   const long long passes = (a.num_tokens + kTokens - 1) / kTokens;
   long long p = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + warp;
@@ -474,6 +481,7 @@ __global__ void __launch_bounds__(256, 2) router_scores_kernel(const RouterScore
   };
   if (p < passes) load(token_of(p));  // on their way during the set-up
   for (int e = threadIdx.x; e < 256; e += blockDim.x) hist[e] = 0;
+  if (threadIdx.x == 0) num_doubtful = 0;
   if constexpr (kScored) {
     if (warp == 0) {
       float b[8], lo = __builtin_huge_valf(), hi = kNegInf;
@@ -494,12 +502,13 @@ __global__ void __launch_bounds__(256, 2) router_scores_kernel(const RouterScore
       const float unit = kKeyRange / (1.0f + (hi - lo));
       // b - lo first: what is rounded is small beside the range
 #pragma unroll
-      for (int i = 0; i < 8; ++i) bias_key[lane + 32 * i] = fminf(fmaxf((b[i] - lo) * unit, -4e7f), kKeyRange - unit) + 1.0f;
-      if (lane == 0) key_unit[0] = unit;
+      for (int i = 0; i < 8; ++i)
+        bias_key[lane + 32 * i] = fminf(fmaxf((b[i] - lo) * unit, -4e7f), kKeyRange - unit) + 1.0f;
+      if (lane == 0) key_unit = unit;
     }
   }
   __syncthreads();
-  const float unit = kScored ? key_unit[0] : 0.0f;
+  const float unit = kScored ? key_unit : 0.0f;
   for (; p < passes; p += warps) {
     const long long t = p * kTokens + tok, tt = token_of(p);
     const bool live = t < a.num_tokens;  // the lanes of a token agree
@@ -521,8 +530,7 @@ __global__ void __launch_bounds__(256, 2) router_scores_kernel(const RouterScore
       for (int off = 1; off < kLanes; off <<= 1) sum += __shfl_xor_sync(kFull, sum, off);
       inv_sum = sum > 0.0f ? 1.0f / sum : 0.0f;
     }
-    // ---- keys, without 4 (7 - j): vector i, element c of a lane
-    uint32_t key[kOwn];
+    // ---- 24-bit keys into the scratch, by expert (0 behind the last)
     const float soft_unit = unit * inv_sum;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
@@ -530,23 +538,22 @@ __global__ void __launch_bounds__(256, 2) router_scores_kernel(const RouterScore
       float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
       if constexpr (kScored) b = *reinterpret_cast<const float4*>(&bias_key[e]);
       const float bc[4] = {b.x, b.y, b.z, b.w};
+      uint32_t q[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const uint32_t q = fixed_point<kSigmoid, kScored>(x[4 * i + c], ref, unit, soft_unit, bc[c]);
-        key[4 * i + c] = (q << 8) + (32 * (kVecs - 1 - i) + 3 - c);
-        if (e + c >= E) key[4 * i + c] = 0;
+      for (int c = 0; c < 4; ++c) q[c] = fixed_point<kSigmoid, kScored>(x[4 * i + c], ref, unit, soft_unit, bc[c]);
+      if (e + 4 > E) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (e + c >= E) q[c] = 0;
       }
+      *reinterpret_cast<uint4*>(&ws.key[tok][e]) = make_uint4(q[0], q[1], q[2], q[3]);
     }
     if (p + warps < passes) load(token_of(p + warps));
-    const uint32_t lane_code = 4 * (kLanes - 1 - j);
     auto expert_of = [](uint32_t full_key) { return 255 - static_cast<int>(full_key & 255u); };
     bool doubt = false;  // some comparison is not certain
+    unsigned kept = kFull;
     // ---- groups
     if (grouped) {
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i)
-        *reinterpret_cast<uint4*>(&ws.key[tok][4 * (j + kLanes * i)]) =
-            make_uint4(key[4 * i], key[4 * i + 1], key[4 * i + 2], key[4 * i + 3]);
       __syncwarp();
       // lane j of a token takes groups j, j + 8, ..: the sum of their two largest keys
       constexpr int kMine = kRouterMaxGroups / kLanes;
@@ -555,7 +562,7 @@ __global__ void __launch_bounds__(256, 2) router_scores_kernel(const RouterScore
       for (int n = 0; n < kMine; ++n) {
         const int g = j + kLanes * n;
         merit[n] = 0;
-        if (g < a.num_groups) {
+        if (kLanes * n < a.num_groups && g < a.num_groups) {
           uint32_t first = 0, second = 0;
           auto take = [&](uint32_t v) {
             second = max(second, min(first, v));
@@ -564,6 +571,7 @@ __global__ void __launch_bounds__(256, 2) router_scores_kernel(const RouterScore
           const uint32_t* from = &ws.key[tok][g * size];
           if (size % 4 == 0) {
             int at = 4 * j % size;  // the lanes of a token begin in different banks
+#pragma unroll 2
             for (int i = 0; i < size; i += 4) {
               const uint4 v = *reinterpret_cast<const uint4*>(from + at);
               take(v.x);
@@ -573,14 +581,15 @@ __global__ void __launch_bounds__(256, 2) router_scores_kernel(const RouterScore
               at = at + 4 == size ? 0 : at + 4;
             }
           } else {
+#pragma unroll 1
             for (int i = 0; i < size; ++i) take(from[i]);
           }
-          merit[n] = (first >> 8) + (size > 1 ? second >> 8 : 0u);
+          merit[n] = size > 1 ? first + second : first;
         }
       }
       // a group is kept if fewer than top_groups come before it
-      unsigned kept = 0;
       uint32_t last_kept = 0xffffffffu, first_dropped = 0;
+      kept = 0;
 #pragma unroll
       for (int n = 0; n < kMine; ++n) {
         if (kLanes * n < a.num_groups) {
@@ -612,40 +621,61 @@ __global__ void __launch_bounds__(256, 2) router_scores_kernel(const RouterScore
         first_dropped = max(first_dropped, __shfl_xor_sync(kFull, first_dropped, off));
       }
       doubt = last_kept - first_dropped <= 2 * kNear;  // a tie in merit as well
+      if (size % 4 == 0) {  // the kept groups' first experts, in order
 #pragma unroll
-      for (int i = 0; i < kVecs; ++i) {
-        const int e = 4 * (j + kLanes * i);
-        if (size % 4 == 0) {
-          const uint32_t in = 0u - (kept >> ((e * inv_size) >> 16) & 1);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) key[4 * i + c] &= in;
-        } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (!(kept >> (((e + c) * inv_size) >> 16) & 1)) key[4 * i + c] = 0;
+        for (int n = 0; n < kMine; ++n) {
+          const int g = j + kLanes * n;
+          if (kept >> g & 1) ws.kept[tok][__popc(kept & ((1u << g) - 1))] = g * size;
         }
+        vecs = (a.top_groups * size + 4 * kLanes - 1) / (4 * kLanes);
       }
-      __syncwarp();
     }
+    __syncwarp();
+    // this lane's i-th vector of experts that may be chosen, as full keys (0: none)
+    auto load_keys = [&](int i, uint32_t* key) {
+      int e = 4 * (j + kLanes * i);
+      bool in = true;
+      if (grouped && size % 4 == 0) {  // of the kept groups, one behind the other
+        const int nth = (e * inv_size) >> 16;
+        in = nth < a.top_groups;
+        if (in) e += static_cast<int>(ws.kept[tok][nth]) - nth * size;
+      } else {
+        in = i < kVecs;
+      }
+      const uint4 v = in ? *reinterpret_cast<const uint4*>(&ws.key[tok][e]) : make_uint4(0, 0, 0, 0);
+      const uint32_t code = in ? 255u - e : 3u;
+      key[0] = (v.x << 8) + code;
+      key[1] = (v.y << 8) + code - 1;
+      key[2] = (v.z << 8) + code - 2;
+      key[3] = (v.w << 8) + code - 3;
+      if (!in) key[0] = key[1] = key[2] = key[3] = 0;
+      if (grouped && size % 4 != 0) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (!(kept >> (((e + c) * inv_size) >> 16) & 1)) key[c] = 0;
+      }
+    };
     // ---- the K largest keys
     uint32_t best[K], local[K];
 #pragma unroll
-    for (int r = 0; r < K; ++r) best[r] = key[r];
-    sort_keys<K>(best);
+    for (int r = 0; r < K; ++r) best[r] = 0;
+#pragma unroll 1
+    for (int i = 0; i < vecs; i += 2) {
+      uint32_t key[8];
+      load_keys(i, key);
+      load_keys(i + 1, key + 4);
 #pragma unroll
-    for (int i = K; i < kOwn; i += K) {
-      uint32_t part[K];
+      for (int h = 0; h < 8; h += K) {
+        uint32_t part[K];
 #pragma unroll
-      for (int r = 0; r < K; ++r) part[r] = key[i + r];
-      sort_keys<K>(part);
-      merge_keys<K>(best, part);
+        for (int r = 0; r < K; ++r) part[r] = key[h + r];
+        sort_keys<K>(part);
+        merge_keys<K>(best, part);
+      }
     }
 #pragma unroll
-    for (int r = 0; r < K; ++r) {
-      if (best[r]) best[r] += lane_code;
-      local[r] = best[r];
-    }
-#pragma unroll
+    for (int r = 0; r < K; ++r) local[r] = best[r];
+#pragma unroll 1
     for (int off = 1; off < kLanes; off <<= 1) {
       uint32_t other[K];
 #pragma unroll
@@ -661,40 +691,57 @@ __global__ void __launch_bounds__(256, 2) router_scores_kernel(const RouterScore
 #pragma unroll
     for (int r = 0; r < K; ++r) next = max(next, local[r] < last ? local[r] : 0u);
     if (__any_sync(kFull, local[K - 1] >= last)) {  // a lane whose whole list was chosen: its other keys
+#pragma unroll 1
+      for (int i = 0; i < vecs; ++i) {
+        uint32_t key[4];
+        load_keys(i, key);
 #pragma unroll
-      for (int i = 0; i < kOwn; ++i) {
-        const uint32_t full_key = key[i] ? key[i] + lane_code : 0u;
-        next = max(next, full_key < last ? full_key : 0u);
+        for (int c = 0; c < 4; ++c) next = max(next, key[c] < last ? key[c] : 0u);
       }
     }
 #pragma unroll
     for (int off = 1; off < kLanes; off <<= 1) next = max(next, __shfl_xor_sync(kFull, next, off));
-    // ---- neighbours too close to be certain, unless logit and bias are the same
+    // ---- neighbours too close to be certain, unless logit and bias are the same; and lane j of a
+    // token: its j-th expert
+    int expert = 0;
+    uint32_t below = next;  // the neighbour of this lane's
 #pragma unroll
     for (int r = 0; r < K; ++r) {
-      if (r < k) {
-        uint32_t below = next;
-        if constexpr (K > 1)
-          if (r + 1 < K && r + 1 < k) below = best[r + 1 < K ? r + 1 : r];
-        if (below != 0 && (best[r] >> 8) - (below >> 8) <= kNear && !same_inputs(a, tt, expert_of(best[r]), expert_of(below)))
-          doubt = true;
-      }
+      if (j == r) expert = expert_of(best[r]);
+      if (r > 0 && r < k && j == r - 1) below = best[r];
     }
-    // ---- lane j of a token: its j-th expert
-    int expert = 0;
+    uint32_t own = 0;
 #pragma unroll
     for (int r = 0; r < K; ++r)
-      if (j == r) expert = expert_of(best[r]);
+      if (j == r) own = best[r];
+    if (j < k && below >= 256 && (own >> 8) - (below >> 8) <= kNear && !same_inputs(a, tt, expert, expert_of(below))) doubt = true;
+    const unsigned doubts = __ballot_sync(kFull, doubt && live);
+    doubt = (doubts >> (lane & ~(kLanes - 1)) & ((1u << kLanes) - 1)) != 0;
+    // ---- weights
     const float mine = j < k ? weight_of<kSigmoid>(load_logit(a, tt, expert), ref, inv_sum) : 0.0f;
     float sum = mine;
 #pragma unroll
     for (int off = 1; off < kLanes; off <<= 1) sum += __shfl_xor_sync(kFull, sum, off);
     if (live && !doubt && j < k) write_choice(a, hist, t, j, expert, mine, sum);
-    unsigned again = __ballot_sync(kFull, doubt && live && j == 0);
-    while (again) {
-      const int lead = __ffs(again) - 1;  // lane 0 of the token
-      again &= again - 1;
-      settle<kSigmoid, kScored>(a, ws, hist, bias_key, unit, p * kTokens + lead / kLanes);
+    __syncwarp();  // the keys have been read
+    if (doubt && live && j == 0) {  // left for the end: in the list, or marked where it is full
+      const int at = atomicAdd(&num_doubtful, 1);
+      if (at < kMaxDoubtful) doubtful[at] = t;
+      else a.topk_idx[t * k] = -1;
+    }
+  }
+  // the block's doubtful tokens, shared among its warps
+  __syncthreads();
+  const int left = min(num_doubtful, kMaxDoubtful);
+  for (int i = warp; i < left; i += blockDim.x >> 5)
+    settle<kSigmoid, kScored>(a, ws, hist, bias_key, unit, doubtful[i]);
+  if (num_doubtful > kMaxDoubtful) {  // the marked ones, by the warps that met them
+    p = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + warp;
+    for (; p < passes; p += warps) {
+      for (long long t = p * kTokens; t < min((p + 1) * kTokens, a.num_tokens); ++t) {
+        const int first = *const_cast<volatile int32_t*>(a.topk_idx + t * k);
+        if (__shfl_sync(kFull, first, 0) < 0) settle<kSigmoid, kScored>(a, ws, hist, bias_key, unit, t);
+      }
     }
   }
   if (a.counts) {
@@ -708,9 +755,9 @@ template <int K, bool kFp32, bool kSigmoid>
 cudaError_t launch_scores(const RouterScoresArgs& a, int sms, cudaStream_t stream) {
   // few tokens: a warp per block, so that they spread over the SMs; else eight
   const long long passes = (a.num_tokens + kTokens - 1) / kTokens;
-  const int warps = passes <= 2LL * sms ? 1 : 8;
+  const int warps = passes <= 2LL * sms ? 1 : kBlock / 32;
   const long long blocks = (passes + warps - 1) / warps;
-  const long long most = 2LL * sms;  // resident ones
+  const long long most = 3LL * sms;  // resident ones
   const int grid = static_cast<int>(blocks < most ? blocks : most);
   const size_t smem = warps * sizeof(WarpScratch);
   if (a.bias || a.top_groups < a.num_groups)
