@@ -822,14 +822,13 @@ sa_status lora_linear_bias(const void* x, const void* w, const void* bias, const
   if (!aligned16(x) || !aligned16(w) || !aligned16(lora_a) || !aligned16(lora_b) || !aligned16(workspace) ||
       !aligned16(out) || !aligned2(bias) || !aligned4(lora_scale) || !aligned4(adapter_idx))
     return SA_ERR_ALIGNMENT;
-  sa::LoraArgs a{};
-  const int sms = sm_count();
-  a.block_n = sa::lora_tile_n(m, n, k, sms);
   const long long tiles_m = (static_cast<long long>(m) + sa::kLoraTileRows - 1) / sa::kLoraTileRows;
-  const long long tiles_n = (static_cast<long long>(n) + a.block_n - 1) / a.block_n;
-  if (tiles_m > 65535 || tiles_m * tiles_n >= (1LL << 30)) return SA_ERR_SHAPE;
+  if (tiles_m > 65535 || tiles_m * (n / 16LL + 1) >= (1LL << 30)) return SA_ERR_SHAPE;
+  if (static_cast<long long>(num_adapters) * rank * static_cast<long long>(k > n ? k : n) >= (1LL << 40)) return SA_ERR_SHAPE;
   unsigned* status = nullptr;
   if (sa_status s = status_ptr(&status)) return s;
+  sa::LoraArgs a{};
+  const int sms = sm_count();
   a.x = static_cast<const uint16_t*>(x);
   a.w = static_cast<const uint16_t*>(w);
   a.lora_a = static_cast<const uint16_t*>(lora_a);
@@ -846,16 +845,16 @@ sa_status lora_linear_bias(const void* x, const void* w, const void* bias, const
   a.R = rank;
   a.num_adapters = num_adapters;
   a.splits = sa::lora_splits(m, k);
-  a.tiles_m = static_cast<int>(tiles_m);
-  a.tiles_n = static_cast<int>(tiles_n);
-  a.box_rows = m < sa::kLoraTileRows ? (m + 7) / 8 * 8 : sa::kLoraTileRows;
   a.status = status;
   a.timeout_ns = g_timeout_ns;
-  CUtensorMap xm, wm, bm;
-  if (sa_status s = map_matrix(&xm, x, m, k, a.box_rows)) return s;
-  if (sa_status s = map_matrix(&wm, w, n, k, a.block_n)) return s;
-  if (sa_status s = map_adapters(&bm, lora_b, num_adapters, n, rank, a.block_n)) return s;
-  return sa::launch_lora(xm, wm, bm, a, sms, stream) == cudaSuccess ? SA_OK : SA_ERR_LAUNCH;
+  sa::lora_plan(a, sms);
+  const int w_rows = a.block_n / a.plan_tiles;
+  sa::LoraMaps maps{};
+  if (sa_status s = map_matrix(&maps.x, x, m, k, a.box_rows)) return s;
+  if (sa_status s = map_matrix(&maps.w, w, n, k, w_rows)) return s;
+  if (sa_status s = map_matrix(&maps.a, lora_a, static_cast<long long>(num_adapters) * rank, k, rank)) return s;
+  if (sa_status s = map_adapters(&maps.b, lora_b, num_adapters, n, rank, w_rows)) return s;
+  return sa::launch_lora(maps, a, sms, stream) == cudaSuccess ? SA_OK : SA_ERR_LAUNCH;
 }
 
 sa_status moe_router(const void* x, const void* w_router, const void* bias, int num_tokens,

@@ -9,12 +9,12 @@ namespace sa {
 
 constexpr int kLoraMaxRank = 128;
 constexpr int kLoraMaxAdapters = 1024;
-constexpr int kLoraTileRows = 128;  // tokens of an output tile
-// Per 128 tokens: the number of distinct adapters, which ones (ascending), and each token's place
-// among them (-1: none).
-constexpr int kLoraPlanInts = 264;
+constexpr int kLoraTileRows = 128;  // tokens of a CTA's tile
+// Per 128 tokens (256 where CTAs work in pairs): the number of distinct adapters, which ones
+// (ascending), and each token's place among them (-1: none).
 constexpr int kLoraPlanList = 8;
-constexpr int kLoraPlanSlot = kLoraPlanList + kLoraTileRows;
+constexpr int kLoraPlanSlot = kLoraPlanList + 2 * kLoraTileRows;
+constexpr int kLoraPlanInts = kLoraPlanSlot + 2 * kLoraTileRows;
 
 struct LoraArgs {
   const uint16_t* x;         // bf16 [M, K]
@@ -25,23 +25,27 @@ struct LoraArgs {
   const float* scale;        // [L] or nullptr (1)
   const uint16_t* bias;      // bf16 [N] or nullptr
   uint16_t* out;             // bf16 [M, N]
-  int32_t* plan;             // workspace: [tiles_m, kLoraPlanInts]
+  int32_t* plan;             // workspace: [tiles_m, kLoraPlanInts] (half of it used by pairs)
   float* t;                  // workspace: [splits, M, R]
   int M, N, K, R, num_adapters;
   int splits;                // parts of K whose products are added up by their reader
-  int block_n, tiles_m, tiles_n;
+  int block_n, tiles_m, tiles_n;  // tiles_m: of 128 tokens
+  int plan_tiles;            // 128-token tiles per plan and per tile of the product (2: pairs of CTAs)
   int box_rows;              // rows of an x box
   unsigned* status;
   unsigned long long timeout_ns;
 };
 
+// x in boxes of box_rows x 64; W [N, K] in boxes of block_n / plan_tiles rows x 64; lora_a [L R, K] in
+// boxes of R x 64; lora_b [L, N, R] in boxes of 1 x block_n / plan_tiles x 16 (32-byte swizzle).
+struct LoraMaps {
+  CUtensorMap x, w, a, b;
+};
+
 // Parts of K for the adapters' first product (fixed by the sizes: the workspace holds them).
 int lora_splits(int m, int k);
-// Columns of an output tile (a multiple of 16, at most 224).
-int lora_tile_n(int m, int n, int k, int sms);
-// xmap: x in boxes of box_rows x 64; wmap: W [N, K] in boxes of block_n x 64; bmap: lora_b
-// [L, N, R] in boxes of 1 x block_n x 16 (32-byte swizzle).
-cudaError_t launch_lora(const CUtensorMap& xmap, const CUtensorMap& wmap, const CUtensorMap& bmap, const LoraArgs& a,
-                        int sms, cudaStream_t stream);
+// Tiles for the sizes in a: block_n, tiles_m, tiles_n, plan_tiles, box_rows.
+void lora_plan(LoraArgs& a, int sms);
+cudaError_t launch_lora(const LoraMaps& m, const LoraArgs& a, int sms, cudaStream_t stream);
 
 }  // namespace sa

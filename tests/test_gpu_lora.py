@@ -88,6 +88,10 @@ CASES = {
     "tall": (20000, 64, 96, 16, 8, [(i // 999) % 8 for i in range(20000)]),
     "wide": (3, 64, 40000, 16, 2, [0, 1, -1]),
     "decode, 64 tokens": (64, 2880, 5120, 16, 128, mixed(64, 128)),
+    "pairs, runs": (2700, 264, 5120, 64, 5, [(i // 370) % 5 for i in range(2700)]),
+    "pairs, mixed": (2049, 128, 5000, 16, 300, mixed(2049, 300)),
+    "pairs, rank 128": (2304, 200, 4352, 128, 3, mixed(2304, 3)),
+    "pairs, rank 24": (5000, 72, 2880, 24, 40, mixed(5000, 40)),
 }
 
 
