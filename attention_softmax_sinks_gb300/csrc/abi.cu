@@ -807,8 +807,7 @@ sa_status linear_bias(const void* x, const void* w, const void* bias, int m, int
 
 long long lora_workspace_bytes(int m, int k, int rank) {
   if (m <= 0 || k <= 0 || rank <= 0 || rank > sa::kLoraMaxRank) return 0;
-  const long long tiles = (static_cast<long long>(m) + sa::kLoraTileRows - 1) / sa::kLoraTileRows;
-  return tiles * sa::kLoraPlanInts * 4 + 4LL * sa::lora_splits(m, k) * m * rank;
+  return 2LL * m * rank;
 }
 
 sa_status lora_linear_bias(const void* x, const void* w, const void* bias, const void* lora_a, const void* lora_b,
@@ -837,14 +836,12 @@ sa_status lora_linear_bias(const void* x, const void* w, const void* bias, const
   a.scale = lora_scale;
   a.bias = static_cast<const uint16_t*>(bias);
   a.out = static_cast<uint16_t*>(out);
-  a.plan = static_cast<int32_t*>(workspace);
-  a.t = reinterpret_cast<float*>(a.plan + tiles_m * sa::kLoraPlanInts);
+  a.t = static_cast<uint16_t*>(workspace);
   a.M = m;
   a.N = n;
   a.K = k;
   a.R = rank;
   a.num_adapters = num_adapters;
-  a.splits = sa::lora_splits(m, k);
   a.status = status;
   a.timeout_ns = g_timeout_ns;
   sa::lora_plan(a, sms);

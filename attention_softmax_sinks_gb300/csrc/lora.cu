@@ -5,22 +5,23 @@
 // (page "GPT-OSS on day 0": the projections carry bias terms; the adapters are what requests of
 // one server differ in).  Two kernels, in one call:
 //
-// 1. lora_shrink_kernel: t[m] = x[m] A_a^T, fp32, on tcgen05.  A CTA takes 128 tokens, a part of K
+// 1. lora_shrink_kernel: t[m] = s_a x[m] A_a^T, on tcgen05.  A CTA takes 128 tokens, a part of K
 //    and up to 256 columns: the A_a of as many of the tile's distinct adapters as fit, one behind
 //    the other (found by a bit per adapter and population counts).  Every token meets every one
 //    of them, and its row keeps its own adapter's R columns.  That is wasted work for a tile of
 //    many adapters, but the tile is short of nothing else: what bounds it is the operands' way
-//    in, which is A once per tile and x once per 256 columns.  The parts of K are added by the
-//    reader, in order: no atomics.
+//    in, which is A once per tile and x once per 256 columns.  The CTAs of a tile's parts of K are
+//    a cluster: each sends its rows to the one that adds them up, in order, and rounds once to
+//    bf16 for the second product, as x is: a relative error of 2^-8 at most per term of a sum
+//    over the ranks, of the adapters' part only (which the bf16 output rounds once more anyway).
+//    (With fp32 parts added by the second kernel, 8192 tokens of rank 64 took 27 us longer than
+//    without adapters, and of rank 128 115 us: its loads of t were longer than a tile.)
 // 2. lora_linear_kernel: the product with W on tcgen05, tokens x block_n features per tile,
 //    accumulator seeded with the bias, and then on the same accumulator one more product per
 //    adapter of the tile: T_i B_i^T, where T_i holds s t for the tokens of adapter i and zeros for
 //    the others.  T_i is the A operand in TMEM, written by warps of its own (a thread per row),
 //    which run ahead of the product; B_i comes by TMA in boxes of 16 ranks.  So any mix of
 //    adapters in a tile is right, and a tile of one adapter costs R more columns of K.
-//    s t is rounded to bf16 for the tensor core, as x is: a relative error of 2^-8 at most per
-//    term of a sum over the ranks, of the adapters' part only (which the bf16 output rounds once
-//    more anyway).
 //    Zeros do not keep out an infinity or NaN of another request's B_i: an element that comes out
 //    not finite is computed once more by itself, from its own operands only.
 //    Many tokens: pairs of CTAs (cta_group::2, 256 tokens), which stage half of W's columns each.
@@ -101,78 +102,93 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // ------------------------------------------------------------------ which adapters a tile has
-// Rows of a tile sorted by adapter: `slot` of each row among the tile's distinct adapters
-// (ascending), -1 for none.
-template <int kRows>
+// The distinct adapters of a tile's rows, ascending (`slots` of them, slot by slot).
 struct TilePlan {
   uint32_t bits[kLoraMaxAdapters / 32];
   int word_rank[kLoraMaxAdapters / 32];  // adapters in the words before
-  int list[kRows];                       // adapter of a slot
-  int slot[kRows];
+  int list[2 * kBM];                     // adapter of a slot
   int slots;
 };
 
-// All threads of the CTA, of which there are at least kRows.
+__device__ __forceinline__ void plan_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool plan_barrier_and(bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, r;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred r, 1, 128, p;\n\tselp.u32 %0, 1, 0, r;\n\t}"
+      : "=r"(all)
+      : "r"(ok ? 1u : 0u)
+      : "memory");
+  return all != 0;
+}
+
+// By the 128 threads (four warps) that share named barrier 1: thread i brings rows first_row + i
+// and, of 256 rows, first_row + 128 + i; returns the slot of row first_row + own_row + i (own_row
+// 0 or 128), -1 without adapter.  An adapter that does not exist counts as none and is reported.
 template <int kRows>
-__device__ __forceinline__ void make_plan(const LoraArgs& a, TilePlan<kRows>& plan, int first_row) {
-  const int tid = threadIdx.x;
-  if (tid < kLoraMaxAdapters / 32) plan.bits[tid] = 0;
-  int id = -1;
-  if (tid < kRows && first_row + tid < a.M) {
-    id = __ldg(a.adapter + first_row + tid);
-    if (id >= a.num_adapters) {
+__device__ __forceinline__ int make_plan(const LoraArgs& a, TilePlan& plan, int i, int first_row, int own_row) {
+  int id[kRows / 128];
+#pragma unroll
+  for (int h = 0; h < kRows / 128; ++h) {
+    const int row = first_row + 128 * h + i;
+    id[h] = row < a.M ? __ldg(a.adapter + row) : -1;
+    if (id[h] >= a.num_adapters) {
       raise_status(a.status, kStatusBadPage);
-      id = -1;
+      id[h] = -1;
     }
   }
-  __syncthreads();
-  if (id >= 0) atomicOr(&plan.bits[id >> 5], 1u << (id & 31));
-  __syncthreads();
-  if (tid < 32) {
-    const int n = __popc(plan.bits[tid]);
+  if (i < kLoraMaxAdapters / 32) plan.bits[i] = 0;
+  plan_barrier();
+#pragma unroll
+  for (int h = 0; h < kRows / 128; ++h)
+    if (id[h] >= 0) atomicOr(&plan.bits[id[h] >> 5], 1u << (id[h] & 31));
+  plan_barrier();
+  if (i < 32) {
+    const int n = __popc(plan.bits[i]);
     int incl = n;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, incl, off);
-      if (tid >= off) incl += v;
+      if (i >= off) incl += v;
     }
-    plan.word_rank[tid] = incl - n;
-    if (tid == 31) plan.slots = incl;
+    plan.word_rank[i] = incl - n;
+    if (i == 31) plan.slots = incl;
   }
-  __syncthreads();
-  if (tid < kRows) {
-    int slot = -1;
-    if (id >= 0) {
-      slot = plan.word_rank[id >> 5] + __popc(plan.bits[id >> 5] & ((1u << (id & 31)) - 1));
-      plan.list[slot] = id;  // the same value from all of its rows
-    }
-    plan.slot[tid] = slot;
+  plan_barrier();
+  int slot = -1;
+#pragma unroll
+  for (int h = 0; h < kRows / 128; ++h) {
+    if (id[h] < 0) continue;
+    const int s = plan.word_rank[id[h] >> 5] + __popc(plan.bits[id[h] >> 5] & ((1u << (id[h] & 31)) - 1));
+    plan.list[s] = id[h];  // the same value from all of its rows
+    if (128 * h == own_row) slot = s;
   }
-  __syncthreads();
+  return slot;
 }
 
 // ------------------------------------------------------------------ first product
 constexpr int kShrinkThreads = 256;  // loads, products, plan; warps 4..7 epilogue
 constexpr int kShrinkCols = 256;     // columns of an accumulator
-constexpr int kShrinkStages = 4;
+constexpr int kShrinkStages = 3;
 constexpr int kShrinkStageBytes = (kBM + kShrinkCols) * kBK * 2;
-constexpr size_t kShrinkSmem = 1024 + kShrinkStages * kShrinkStageBytes + 8192;
+// rows that this CTA adds up: from each part of K, together 128 rows of up to 128 ranks
+constexpr int kShrinkRecvBytes = kBM * kLoraMaxRank * 4;
+constexpr size_t kShrinkSmem = 1024 + kShrinkStages * kShrinkStageBytes + kShrinkRecvBytes + 4096;
 
 struct ShrinkShared {
   uint64_t full[kShrinkStages], empty[kShrinkStages], acc_full, acc_empty, drain;
   uint32_t tmem_base;
   int abort_flag;
   int issued;
-  TilePlan<kBM> plan;
-  TilePlan<2 * kBM> pair_plan;
+  int slot[kBM];
+  TilePlan plan;
 };
-static_assert(sizeof(ShrinkShared) <= 8192, "fits behind the ring");
+static_assert(sizeof(ShrinkShared) <= 4096, "fits behind the ring");
 
 __global__ void __launch_bounds__(kShrinkThreads, 1)
     lora_shrink_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap amap, const LoraArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  ShrinkShared& sb = *reinterpret_cast<ShrinkShared*>(tiles + kShrinkStages * kShrinkStageBytes);
+  ShrinkShared& sb = *reinterpret_cast<ShrinkShared*>(tiles + kShrinkStages * kShrinkStageBytes + kShrinkRecvBytes);
   volatile int* abort_flag = &sb.abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tile = blockIdx.z, split = blockIdx.y;
@@ -194,27 +210,16 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
   // inputs without waiting for this grid.
   pdl_wait_primary();
   pdl_launch_dependents();
-  make_plan<kBM>(a, sb.plan, tile * kBM);
-  if (blockIdx.x == 0 && split == 0 && tile % a.plan_tiles == 0) {
-    int32_t* plan = a.plan + static_cast<long long>(tile / a.plan_tiles) * kLoraPlanInts;
-    auto write = [&](const auto& from, int rows) {
-      if (threadIdx.x == 0) plan[0] = from.slots;
-      for (int i = threadIdx.x; i < rows; i += kShrinkThreads) {
-        if (i < from.slots) plan[kLoraPlanList + i] = from.list[i];
-        plan[kLoraPlanSlot + i] = from.slot[i];
-      }
-    };
-    if (a.plan_tiles == 2) {
-      make_plan<2 * kBM>(a, sb.pair_plan, tile * kBM);
-      write(sb.pair_plan, 2 * kBM);
-    } else {
-      write(sb.plan, kBM);
-    }
-  }
+  int mine = -1;  // slot of the epilogue thread's row
+  if (warp >= 4) sb.slot[threadIdx.x - 128] = mine = make_plan<kBM>(a, sb.plan, threadIdx.x - 128, tile * kBM, 0);
+  __syncthreads();
   const int slots = sb.plan.slots;
   const int per_pass = kShrinkCols / a.R;  // adapters side by side
   const int passes = (slots + per_pass - 1) / per_pass;
-  if (static_cast<int>(blockIdx.x) >= passes) return;  // uniform, before TMEM is taken
+  if (static_cast<int>(blockIdx.x) >= passes) return;  // the whole cluster, before TMEM is taken
+  cluster_arrive_relaxed();  // waited for before the first store into another CTA
+  const int owner_rows = kBM / a.splits;  // of the tile: CTA `split` adds up [split * owner_rows, ..)
+  float* recv = reinterpret_cast<float*>(tiles + kShrinkStages * kShrinkStageBytes);  // [part][row][R]
   // this CTA's part of K, in steps of 64
   const int steps = (a.K + kBK - 1) / kBK;
   const int k0 = static_cast<int>(static_cast<long long>(steps) * split / a.splits);
@@ -229,6 +234,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
   const uint32_t tmem = sb.tmem_base;
   const uint32_t ring = smem_u32(tiles);
   const int xbytes = a.box_rows * kBK * 2;
+  cluster_wait();  // every CTA of the cluster runs
 
   if (warp == 0) {
     RingPos p;
@@ -283,10 +289,10 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
     }
     __syncwarp();
   } else if (warp >= 4) {
-    const int q = warp & 3, r = 32 * q + lane, row = tile * kBM + r;
+    const int q = warp & 3, r = 32 * q + lane;
     const uint32_t acc = tmem + (static_cast<uint32_t>(32 * q) << 16);
-    const int mine = sb.plan.slot[r];
-    float* out = a.t + (static_cast<long long>(split) * a.M + row) * a.R;
+    const float scale = mine >= 0 && a.scale ? __ldg(a.scale + sb.plan.list[mine]) : 1.0f;
+    const uint32_t out = dsmem_addr(smem_u32(recv + (split * owner_rows + r % owner_rows) * a.R), r / owner_rows);
     int i = 0;
     for (int pass = blockIdx.x; pass < passes; pass += gridDim.x, ++i) {
       const int first = pass * per_pass, n = min(per_pass, slots - first);
@@ -300,8 +306,11 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
           tmem_ld8(acc + s * a.R + c, v);
           tc_wait_ld();
           if (own) {
-            *reinterpret_cast<uint4*>(out + c) = make_uint4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<uint4*>(out + c + 4) = make_uint4(v[4], v[5], v[6], v[7]);
+            float f[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) f[u] = scale * __uint_as_float(v[u]);
+            dsmem_st4(out + 4 * c, f[0], f[1], f[2], f[3]);
+            dsmem_st4(out + 4 * c + 16, f[4], f[5], f[6], f[7]);
           }
         }
       }
@@ -317,6 +326,28 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
       const int last = sb.issued - 1 - ((sb.issued - 1 - s) % kShrinkStages);
       if (!mbar_wait(smem_u32(&sb.full[s]), (last / kShrinkStages) & 1, kDrainTimeoutNs)) raise_status(a.status, kStatusTimeout);
     }
+  }
+  cluster_sync();  // every part of the rows has arrived
+  const int parts = a.splits;
+  for (int i = threadIdx.x; i < owner_rows * (a.R / 8); i += kShrinkThreads) {
+    const int r = i / (a.R / 8), c = i % (a.R / 8) * 8, s = sb.slot[split * owner_rows + r];
+    if (s < 0 || s / per_pass % gridDim.x != blockIdx.x) continue;  // none, or another cluster's
+    float sum[8] = {};
+    for (int p = 0; p < parts; ++p) {
+      const float4* v = reinterpret_cast<const float4*>(recv + (p * owner_rows + r) * a.R + c);
+      const float4 v0 = v[0], v1 = v[1];
+      sum[0] += v0.x;
+      sum[1] += v0.y;
+      sum[2] += v0.z;
+      sum[3] += v0.w;
+      sum[4] += v1.x;
+      sum[5] += v1.y;
+      sum[6] += v1.z;
+      sum[7] += v1.w;
+    }
+    *reinterpret_cast<uint4*>(a.t + static_cast<long long>(tile * kBM + split * owner_rows + r) * a.R + c) =
+        make_uint4(pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3]), pack_bf16x2(sum[4], sum[5]),
+                   pack_bf16x2(sum[6], sum[7]));
   }
   __syncthreads();
   if (warp == 1) {
@@ -337,15 +368,17 @@ constexpr int kStageTarget = 24 * 1024;  // bytes of a ring stage, where blocks 
 constexpr uint32_t kTmemCols = 512;
 // An MMA reads 128 rows of x also where a box has fewer: behind the last stage, too, that stays
 // inside the allocation (what it reads there goes to accumulator rows that are never stored).
-constexpr size_t kSmem = 1024 + kRingBytes + kBM * kBK * 2 + 1024;
+constexpr size_t kSmem = 1024 + kRingBytes + kBM * kBK * 2 + 4096;
 
 struct LoraBarriers {
-  uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], t_full[kMaxTBufs], t_empty[kMaxTBufs], drain;
+  uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], t_full[kMaxTBufs], t_empty[kMaxTBufs];
+  uint64_t plan_full[2], plan_empty[2], drain;
   uint32_t tmem_base;
   int abort_flag;
   int issued;
+  TilePlan plan[2];  // of this tile's tokens and the next's
 };
-static_assert(sizeof(LoraBarriers) <= 1024, "barriers fit");
+static_assert(sizeof(LoraBarriers) <= 4096, "barriers and plans fit");
 
 // The tcgen05 instructions and copies for one CTA or for a pair (an M = 256 MMA on both SMs,
 // issued by the leading CTA; operands and accumulator halves lie at the same places in both).
@@ -434,8 +467,8 @@ __device__ __forceinline__ void seed_bias(uint32_t taddr, const uint16_t* bias, 
 }
 
 // Element (m, n) by itself, from the operands of token m alone: for elements that an adapter of
-// another token in the tile made not finite (0 times infinity).  `slot`: its place in the plan.
-__device__ __noinline__ float single_element(const LoraArgs& a, const int32_t* plan, int m, int n, int slot) {
+// another token in the tile made not finite (0 times infinity).
+__device__ __noinline__ float single_element(const LoraArgs& a, int m, int n) {
   auto dot8 = [](const uint16_t* p, const uint16_t* q, float sum) {
     const uint4 u = __ldg(reinterpret_cast<const uint4*>(p)), v = __ldg(reinterpret_cast<const uint4*>(q));
     const uint32_t us[4] = {u.x, u.y, u.z, u.w}, vs[4] = {v.x, v.y, v.z, v.w};
@@ -449,16 +482,12 @@ __device__ __noinline__ float single_element(const LoraArgs& a, const int32_t* p
   float sum = a.bias ? __uint_as_float(static_cast<uint32_t>(__ldg(a.bias + n)) << 16) : 0.0f;
   for (int k = 0; k < a.K; k += 8)
     sum = dot8(a.x + static_cast<long long>(m) * a.K + k, a.w + static_cast<long long>(n) * a.K + k, sum);
-  if (slot >= 0) {
-    const int id = __ldcg(plan + kLoraPlanList + slot);
-    const float s = a.scale ? __ldg(a.scale + id) : 1.0f;
+  const int id = __ldg(a.adapter + m);
+  if (id >= 0 && id < a.num_adapters) {
     const uint16_t* b = a.lora_b + (static_cast<long long>(id) * a.N + n) * a.R;
-    for (int r = 0; r < a.R; ++r) {
-      float t = 0.0f;
-      for (int p = 0; p < a.splits; ++p) t += __ldcg(a.t + (static_cast<long long>(p) * a.M + m) * a.R + r);
-      const uint32_t st = pack_bf16x2(s * t, 0.0f) << 16;  // rounded as for the tensor core
-      sum = fmaf(__uint_as_float(st), __uint_as_float(static_cast<uint32_t>(__ldg(b + r)) << 16), sum);
-    }
+    for (int r = 0; r < a.R; ++r)
+      sum = fmaf(__uint_as_float(static_cast<uint32_t>(__ldcg(a.t + static_cast<long long>(m) * a.R + r)) << 16),
+                 __uint_as_float(static_cast<uint32_t>(__ldg(b + r)) << 16), sum);
   }
   return sum;
 }
@@ -520,6 +549,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&sb.t_full[b]), 4 * kCtas);
       mbar_init(smem_u32(&sb.t_empty[b]), 1);
     }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&sb.plan_full[b]), 128);
+      mbar_init(smem_u32(&sb.plan_empty[b]), rank == 0 ? 2 : 1);  // the loads, and the products
+    }
     mbar_init(smem_u32(&sb.drain), 1);
     sb.abort_flag = 0;
     sb.issued = 0;
@@ -545,29 +578,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sb.tmem_base;
   const uint32_t ring = smem_u32(tiles);
-  // Ring stages of a tile behind those of K: four chunks of 16 ranks each.  Only these, and
-  // whatever is written, wait for the first kernel.  From the second tile on the roles read the
-  // plan before the product with W, so that it is there behind it.
+  // Ring stages of a tile behind those of K: four chunks of 16 ranks each.
   auto adapter_stages = [&](int slots) { return (slots * RC + kChunks - 1) / kChunks; };
-  auto plan_of = [&](int t) { return a.plan + static_cast<long long>(t / a.tiles_n) * kLoraPlanInts; };
+  // The plans, one per row block that this CTA passes: made by the warps that write T, read by those
+  // that load and multiply, two at a time.
+  struct PlanPos {
+    int mt = -1, n = -1;  // row block; plans so far less one
+  };
+  // the plan of row block mt is there (all lanes agree); releases the one before
+  auto next_plan = [&](PlanPos& p, int mt) {
+    if (p.mt == mt) return true;
+    if (p.n >= 0 && elect_one()) mbar_arrive(smem_u32(&sb.plan_empty[p.n & 1]));
+    __syncwarp();
+    p.mt = mt;
+    ++p.n;
+    return wait_or_abort(smem_u32(&sb.plan_full[p.n & 1]), (p.n >> 1) & 1, a.timeout_ns, abort_flag);
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------------ loads
     const uint64_t policy = l2_policy_evict_last();  // x is read for every column tile, W for every row block
     RingPos p;
     int issued = 0;
-    bool ok = true, waited = false;
+    PlanPos plan;
+    bool ok = true;
     auto free_stage = [&]() {
       return p.round == 0 || wait_or_abort(smem_u32(&sb.empty[p.stage]), (p.round - 1) & 1, a.timeout_ns, abort_flag);
     };
     for (int t = t_first; t < tiles_total && ok; t += t_step) {
       const int m0 = (t / a.tiles_n * kCtas + rank) * kBM, n0 = (t % a.tiles_n) * bn + rank * wrows;
-      int slots = 0, held = 0;  // held: adapters of 32 slots, one per lane
-      auto read_plan = [&]() {
-        slots = __ldcg(plan_of(t));
-        held = __ldcg(plan_of(t) + kLoraPlanList + lane);  // (behind the last: not used)
-      };
-      if (waited) read_plan();
       for (int ks = 0; ks < k_stages; ++ks, p.next(stages)) {
         ok = free_stage();
         if (!ok) break;
@@ -586,22 +625,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
       if (!ok) break;
-      if (!waited) {
-        pdl_wait_primary();
-        waited = true;
-        read_plan();
-      }
+      ok = next_plan(plan, t / a.tiles_n);
+      if (!ok) break;
+      const TilePlan& tp = sb.plan[plan.n & 1];
+      const int slots = tp.slots;
       for (int e = 0; e < adapter_stages(slots); ++e, p.next(stages)) {
         const int first = e * kChunks, n = min(kChunks, slots * RC - first);
-        if (e > 0 && first % (32 * RC) == 0) {  // entering the next 32 slots
-          const int i = first / RC + lane;
-          held = i < slots ? __ldcg(plan_of(t) + kLoraPlanList + i) : 0;
-        }
         ok = free_stage();
         if (!ok) break;
         int id[kChunks];
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) id[c] = __shfl_sync(0xffffffffu, held, (first + c) / RC % 32);
+        for (int c = 0; c < kChunks; ++c) id[c] = tp.list[min((first + c) / RC, slots - 1)];
         if (elect_one()) {
           const uint32_t bar = full0 + 8 * p.stage;
           pair_expect_tx<kPair>(bar, n * wrows * 32);
@@ -620,11 +654,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t idesc = idesc_bf16_kk(kCtas * kBM, bn);
     RingPos p, tb;
     int i = 0;
-    bool ok = true, waited = false;
+    PlanPos plan;
+    bool ok = true;
     for (int t = t_first; t < tiles_total && ok; t += t_step, ++i) {
       const int b = i & 1;
-      int slots = 0;
-      if (waited) slots = __ldcg(plan_of(t));
       ok = wait_or_abort(smem_u32(&sb.acc_empty[b]), (i >> 1) & 1, a.timeout_ns, abort_flag);
       if (!ok) break;
       tc_fence_after();
@@ -646,11 +679,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
-      if (!waited) {
-        pdl_wait_primary();
-        waited = true;
-        slots = __ldcg(plan_of(t));
-      }
+      ok = next_plan(plan, t / a.tiles_n);
+      if (!ok) break;
+      const int slots = sb.plan[plan.n & 1].slots;
       for (int e = 0; e < adapter_stages(slots); ++e, p.next(stages), tb.next(tbufs)) {
         const int n = min(kChunks, slots * RC - e * kChunks);
         ok = wait_or_abort(smem_u32(&sb.t_full[tb.stage]), tb.round & 1, a.timeout_ns, abort_flag) &&
@@ -680,44 +711,44 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------------ T
     const int q = warp & 3;  // TMEM lane quarter
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * q) << 16);
-    pdl_wait_primary();  // plan and t
     RingPos tb;
-    int held_mt = -1, slots = 0, my_slot = -1;
+    int held_mt = -1, plans = 0, slots = 0, my_slot = -1;
     uint32_t tp[8 * RC];  // s t of this thread's row, bf16 pairs
 #pragma unroll
     for (int e = 0; e < 8 * RC; ++e) tp[e] = 0;
+    // A warp that gave up still comes to the next plan's barrier, where all four learn of it: none
+    // is left waiting there.
     bool ok = true;
-    for (int t = t_first; t < tiles_total && ok; t += t_step) {
+    for (int t = t_first; t < tiles_total; t += t_step) {
       const int mt = t / a.tiles_n;
       if (mt != held_mt) {
         held_mt = mt;
-        const int32_t* plan = plan_of(t);
-        const int row = (mt * kCtas + rank) * kBM + 32 * q + lane;
-        slots = __ldcg(plan);
-        my_slot = __ldcg(plan + kLoraPlanSlot + rank * kBM + 32 * q + lane);
+        if (ok && plans >= 2) ok = wait_or_abort(smem_u32(&sb.plan_empty[plans & 1]), ((plans >> 1) - 1) & 1, a.timeout_ns, abort_flag);
+        ok = plan_barrier_and(ok);  // all four warps go on, or none
+        if (!ok) break;
+        TilePlan& plan = sb.plan[plans & 1];
+        const int i = 32 * q + lane, row = (mt * kCtas + rank) * kBM + i;
+        if constexpr (kPair) my_slot = make_plan<2 * kBM>(a, plan, i, mt * 2 * kBM, rank * kBM);
+        else my_slot = make_plan<kBM>(a, plan, i, mt * kBM, 0);
+        plan_barrier();
+        slots = plan.slots;
+        mbar_arrive(smem_u32(&sb.plan_full[plans & 1]));
+        if (plans == 0) pdl_wait_primary();  // t
+        ++plans;
         if (my_slot >= 0) {
-          const float s = a.scale ? __ldg(a.scale + __ldcg(plan + kLoraPlanList + my_slot)) : 1.0f;
-          const float* src = a.t + static_cast<long long>(row) * a.R;
-          const long long part = static_cast<long long>(a.M) * a.R;
+          const uint4* src = reinterpret_cast<const uint4*>(a.t + static_cast<long long>(row) * a.R);
 #pragma unroll
-          for (int c = 0; c < 4 * RC; ++c) {  // four ranks at a time (R is a multiple of 8)
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (4 * c < a.R) {
-              for (int p = 0; p < a.splits; ++p) {
-                const float4 u = __ldcg(reinterpret_cast<const float4*>(src + p * part + 4 * c));
-                v.x += u.x;
-                v.y += u.y;
-                v.z += u.z;
-                v.w += u.w;
-              }
-            }
-            tp[2 * c] = pack_bf16x2(s * v.x, s * v.y);
-            tp[2 * c + 1] = pack_bf16x2(s * v.z, s * v.w);
+          for (int c = 0; c < 2 * RC; ++c) {  // eight ranks at a time (R is a multiple of 8)
+            const uint4 v = 8 * c < a.R ? __ldcg(src + c) : make_uint4(0, 0, 0, 0);
+            tp[4 * c] = v.x;
+            tp[4 * c + 1] = v.y;
+            tp[4 * c + 2] = v.z;
+            tp[4 * c + 3] = v.w;
           }
         }
       }
       for (int e = 0; e < adapter_stages(slots); ++e, tb.next(tbufs)) {
-        if (tb.round != 0) ok = wait_or_abort(smem_u32(&sb.t_empty[tb.stage]), (tb.round - 1) & 1, a.timeout_ns, abort_flag);
+        if (ok && tb.round != 0) ok = wait_or_abort(smem_u32(&sb.t_empty[tb.stage]), (tb.round - 1) & 1, a.timeout_ns, abort_flag);
         if (!ok) break;
         tc_fence_after();
         uint32_t r[32];
@@ -776,14 +807,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int v = 0; v < 16; ++v) odd = fmaf(__uint_as_float(r[v]), 0.0f, odd);
           if (odd != 0.0f && row < a.M) {
-            const int32_t* plan = plan_of(t);
-            if (__ldcg(plan) > 0) {
-              const int slot = __ldcg(plan + kLoraPlanSlot + rank * kBM + 32 * q + lane);
 #pragma unroll
-              for (int v = 0; v < 16; ++v)
-                if (n0 + c + v < a.N && !(fabsf(__uint_as_float(r[v])) <= 3.402823466e38f))
-                  r[v] = __float_as_uint(single_element(a, plan, row, n0 + c + v, slot));
-            }
+            for (int v = 0; v < 16; ++v)
+              if (n0 + c + v < a.N && !(fabsf(__uint_as_float(r[v])) <= 3.402823466e38f))
+                r[v] = __float_as_uint(single_element(a, row, n0 + c + v));
           }
 #pragma unroll
           for (int v = 0; v < 2; ++v) {
@@ -898,15 +925,6 @@ cudaError_t launch_lora_r(const LoraMaps& m, const LoraArgs& a, int sms, cudaStr
 
 }  // namespace
 
-int lora_splits(int m, int k) {
-  // a CTA per SM at 152 SMs, no more than 8 parts and at least two steps of K in each
-  const int tiles = (m + kBM - 1) / kBM, steps = (k + kBK - 1) / kBK;
-  int s = 152 / tiles;
-  if (s > 8) s = 8;
-  if (s > steps / 2) s = steps / 2;
-  return s < 1 ? 1 : s;
-}
-
 void lora_plan(LoraArgs& a, int sms) {
   a.tiles_m = (a.M + kBM - 1) / kBM;
   // the width with the least rounds x (columns + what a tile costs beside its columns)
@@ -943,6 +961,9 @@ void lora_plan(LoraArgs& a, int sms) {
   }
   a.tiles_n = (a.N + a.block_n - 1) / a.block_n;
   a.box_rows = a.M < kBM ? (a.M + 7) / 8 * 8 : kBM;
+  // parts of K for the first product: a CTA per SM, up to 8 parts of at least two steps
+  a.splits = 1;
+  while (a.splits < 8 && 2 * a.splits * a.tiles_m <= sms && 4 * a.splits <= (a.K + kBK - 1) / kBK) a.splits *= 2;
 }
 
 cudaError_t launch_lora(const LoraMaps& m, const LoraArgs& a, int sms, cudaStream_t stream) {
@@ -955,15 +976,19 @@ cudaError_t launch_lora(const LoraMaps& m, const LoraArgs& a, int sms, cudaStrea
   const int per_pass = kShrinkCols / a.R, passes = (most + per_pass - 1) / per_pass;
   const long long room = 2LL * sms / (static_cast<long long>(a.tiles_m) * a.splits);
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = a.splits;
+  attr[1].val.clusterDim.z = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(room < 1 ? 1 : room < passes ? room : passes), a.splits, a.tiles_m);
   cfg.blockDim = dim3(kShrinkThreads, 1, 1);
   cfg.dynamicSmemBytes = kShrinkSmem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, lora_shrink_kernel, m.x, m.a, a);
   if (e != cudaSuccess) return e;
   if (a.R <= 16) return launch_lora_r<1>(m, a, sms, stream);

@@ -10,12 +10,6 @@ namespace sa {
 constexpr int kLoraMaxRank = 128;
 constexpr int kLoraMaxAdapters = 1024;
 constexpr int kLoraTileRows = 128;  // tokens of a CTA's tile
-// Per 128 tokens (256 where CTAs work in pairs): the number of distinct adapters, which ones
-// (ascending), and each token's place among them (-1: none).
-constexpr int kLoraPlanList = 8;
-constexpr int kLoraPlanSlot = kLoraPlanList + 2 * kLoraTileRows;
-constexpr int kLoraPlanInts = kLoraPlanSlot + 2 * kLoraTileRows;
-
 struct LoraArgs {
   const uint16_t* x;         // bf16 [M, K]
   const uint16_t* w;         // bf16 [N, K]
@@ -25,12 +19,11 @@ struct LoraArgs {
   const float* scale;        // [L] or nullptr (1)
   const uint16_t* bias;      // bf16 [N] or nullptr
   uint16_t* out;             // bf16 [M, N]
-  int32_t* plan;             // workspace: [tiles_m, kLoraPlanInts] (half of it used by pairs)
-  float* t;                  // workspace: [splits, M, R]
+  uint16_t* t;               // workspace: bf16 [M, R], s_a x A_a^T
   int M, N, K, R, num_adapters;
-  int splits;                // parts of K whose products are added up by their reader
+  int splits;                // parts of K of the first product (1, 2, 4 or 8)
   int block_n, tiles_m, tiles_n;  // tiles_m: of 128 tokens
-  int plan_tiles;            // 128-token tiles per plan and per tile of the product (2: pairs of CTAs)
+  int plan_tiles;            // 128-token tiles per tile of the product (2: pairs of CTAs)
   int box_rows;              // rows of an x box
   unsigned* status;
   unsigned long long timeout_ns;
@@ -42,9 +35,7 @@ struct LoraMaps {
   CUtensorMap x, w, a, b;
 };
 
-// Parts of K for the adapters' first product (fixed by the sizes: the workspace holds them).
-int lora_splits(int m, int k);
-// Tiles for the sizes in a: block_n, tiles_m, tiles_n, plan_tiles, box_rows.
+// Tiles for the sizes in a: block_n, tiles_m, tiles_n, plan_tiles, box_rows, splits.
 void lora_plan(LoraArgs& a, int sms);
 cudaError_t launch_lora(const LoraMaps& m, const LoraArgs& a, int sms, cudaStream_t stream);
 
