@@ -807,7 +807,7 @@ sa_status linear_bias(const void* x, const void* w, const void* bias, int m, int
 
 long long lora_workspace_bytes(int m, int k, int rank) {
   if (m <= 0 || k <= 0 || rank <= 0 || rank > sa::kLoraMaxRank) return 0;
-  return 2LL * m * rank;
+  return 16LL * m * rank;  // up to four parts in fp32
 }
 
 sa_status lora_linear_bias(const void* x, const void* w, const void* bias, const void* lora_a, const void* lora_b,
@@ -836,7 +836,6 @@ sa_status lora_linear_bias(const void* x, const void* w, const void* bias, const
   a.scale = lora_scale;
   a.bias = static_cast<const uint16_t*>(bias);
   a.out = static_cast<uint16_t*>(out);
-  a.t = static_cast<uint16_t*>(workspace);
   a.M = m;
   a.N = n;
   a.K = k;
@@ -845,6 +844,8 @@ sa_status lora_linear_bias(const void* x, const void* w, const void* bias, const
   a.status = status;
   a.timeout_ns = g_timeout_ns;
   sa::lora_plan(a, sms);
+  a.t = a.plan_tiles == 2 ? static_cast<uint16_t*>(workspace) : nullptr;
+  a.t_parts = static_cast<float*>(workspace);
   const int w_rows = a.block_n / a.plan_tiles;
   sa::LoraMaps maps{};
   if (sa_status s = map_matrix(&maps.x, x, m, k, a.box_rows)) return s;

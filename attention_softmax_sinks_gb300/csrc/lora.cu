@@ -25,6 +25,10 @@
 //    Zeros do not keep out an infinity or NaN of another request's B_i: an element that comes out
 //    not finite is computed once more by itself, from its own operands only.
 //    Many tokens: pairs of CTAs (cta_group::2, 256 tokens), which stage half of W's columns each.
+//    Few tiles: clusters of 2, 4 or 8 CTAs share one tile's K and adapters and add their accumulators
+//    up through each other's shared memory.  What bounds them is not W's way from memory but the
+//    operands' way into an SM (2 cycles per row and 64 values of K) and the tensor core's reading
+//    of 128 rows of x, live or not; larger tiles with a part of K each need less of both.
 //
 // The second kernel starts while the first runs (programmatic dependent launch): the product with
 // W needs nothing from it, and only the roles of the adapters' part wait for it.
@@ -165,7 +169,237 @@ __device__ __forceinline__ int make_plan(const LoraArgs& a, TilePlan& plan, int 
   return slot;
 }
 
-// ------------------------------------------------------------------ first product
+// ------------------------------------------------------------------ first product, few tokens
+// lora_shrink_few_kernel.  A CTA sorts the 128 tokens of a tile by adapter and takes its share of the
+// units (adapter, up to 64 of its tokens) and of K.  Warp-level matrix instructions with the ranks
+// as M = 16 and the tokens as N = 8: a unit of one token costs what its adapter's rows cost to read.
+// Fragments come straight from memory in 16-byte loads: a lane's eight values of K serve two
+// instructions, in the same order for both operands.  It is small enough (20 KB, half of the
+// registers) to run beside the second kernel's CTAs.  The parts of K are added by their reader.
+constexpr int kFewWarps = 8;
+constexpr int kFewThreads = 32 * kFewWarps;
+constexpr int kUnitTokens = 64;
+constexpr int kRed = 6 * 16 * 32;  // floats: partial sums of the warps that do not add up
+
+struct FewSmem {
+  float red[kRed];
+  uint32_t bits[kLoraMaxAdapters / 32];
+  int word_rank[kLoraMaxAdapters / 32];  // adapters in the words before
+  int list[kLoraTileRows];               // adapter of a slot
+  int warp_count[4][kLoraTileRows];      // its tokens among each 32 of the tile
+  int count[kLoraTileRows];              // its tokens
+  int start[kLoraTileRows + 1];          // where they begin in `order`
+  int unit_start[kLoraTileRows + 1];     // units before a slot
+  int order[kLoraTileRows];              // the tile's tokens by slot
+  int slots;
+};
+
+// Sorts the tile's tokens by adapter.  All threads.
+__device__ __forceinline__ void sort_tokens(const LoraArgs& a, FewSmem& sm, int tile) {
+  const int tid = threadIdx.x;
+  const int m = tile * kLoraTileRows + tid;
+  if (tid < kLoraMaxAdapters / 32) sm.bits[tid] = 0;
+  if (tid < kLoraTileRows)
+    for (int w = 0; w < 4; ++w) sm.warp_count[w][tid] = 0;
+  int id = -1;
+  if (tid < kLoraTileRows && m < a.M) {
+    id = __ldg(a.adapter + m);
+    if (id >= a.num_adapters) {
+      raise_status(a.status, kStatusBadPage);
+      id = -1;
+    }
+  }
+  __syncthreads();
+  if (id >= 0) atomicOr(&sm.bits[id >> 5], 1u << (id & 31));
+  __syncthreads();
+  if (tid < 32) {  // ranks of the words
+    const int n = __popc(sm.bits[tid]);
+    int incl = n;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, off);
+      if (tid >= off) incl += v;
+    }
+    sm.word_rank[tid] = incl - n;
+    if (tid == 31) sm.slots = incl;
+  }
+  __syncthreads();
+  int slot = -1, before = 0;
+  if (tid < kLoraTileRows) {
+    if (id >= 0) slot = sm.word_rank[id >> 5] + __popc(sm.bits[id >> 5] & ((1u << (id & 31)) - 1));
+    const unsigned same = __match_any_sync(0xffffffffu, slot);
+    before = __popc(same & ((1u << (tid & 31)) - 1));
+    if (slot >= 0 && before == 0) {  // the first of the warp's tokens with this adapter
+      sm.list[slot] = id;            // the same value from every warp
+      sm.warp_count[tid >> 5][slot] = __popc(same);
+    }
+  }
+  __syncthreads();
+  if (tid < sm.slots) {
+    int n = 0;
+    for (int w = 0; w < 4; ++w) n += sm.warp_count[w][tid];
+    sm.count[tid] = n;
+  }
+  __syncthreads();
+  if (tid < 32) {  // where each slot's tokens and units begin
+    int tokens = 0, units = 0;
+    for (int s0 = 0; s0 < sm.slots; s0 += 32) {
+      const int s = s0 + tid;
+      const int n = s < sm.slots ? sm.count[s] : 0, u = (n + kUnitTokens - 1) / kUnitTokens;
+      int in = n, iu = u;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int vn = __shfl_up_sync(0xffffffffu, in, off), vu = __shfl_up_sync(0xffffffffu, iu, off);
+        if (tid >= off) {
+          in += vn;
+          iu += vu;
+        }
+      }
+      if (s < sm.slots) {
+        sm.start[s] = tokens + in - n;
+        sm.unit_start[s] = units + iu - u;
+      }
+      tokens += __shfl_sync(0xffffffffu, in, 31);
+      units += __shfl_sync(0xffffffffu, iu, 31);
+    }
+    if (tid == 0) {
+      sm.start[sm.slots] = tokens;
+      sm.unit_start[sm.slots] = units;
+    }
+  }
+  __syncthreads();
+  if (slot >= 0) {  // the tokens of a slot in their own order, the same in every CTA
+    for (int w = 0; w < (tid >> 5); ++w) before += sm.warp_count[w][slot];
+    sm.order[sm.start[slot] + before] = m;
+  }
+  __syncthreads();
+}
+
+// t of one unit: `n` tokens (order[0..n)) of one adapter over k in [k0, k1), ranks [r0, r0 + 16 RC).
+// TG token groups of 8 per warp: TG = 1: the eight warps split K; TG = 4: four parts of K times
+// two halves of the tokens.
+template <int RC, int TG>
+__device__ __forceinline__ void few_unit(const LoraArgs& a, FewSmem& sm, const uint16_t* adapter_rows, const int* order,
+                                            int n, int r0, int k0, int k1, float scale, float* out) {
+  constexpr int kParts = TG == 1 ? kFewWarps : kFewWarps / 2;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int part = warp % kParts, half = warp / kParts;
+  const int g = lane >> 2, q = lane & 3;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  // lane's rows: ranks g, g + 8 of each chunk of 16; token g of each group
+  const uint16_t* arow[RC][2];
+  bool aok[RC][2];
+#pragma unroll
+  for (int c = 0; c < RC; ++c)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = r0 + 16 * c + 8 * h + g;
+      aok[c][h] = r < a.R;
+      arow[c][h] = adapter_rows + static_cast<long long>(aok[c][h] ? r : 0) * a.K;
+    }
+  const uint16_t* xrow[TG];
+  bool xok[TG];
+#pragma unroll
+  for (int i = 0; i < TG; ++i) {
+    const int j = (half * TG + i) * 8 + g;
+    xok[i] = j < n;
+    xrow[i] = a.x + static_cast<long long>(order[xok[i] ? j : 0]) * a.K;
+  }
+  float acc[RC][TG][4];
+#pragma unroll
+  for (int c = 0; c < RC; ++c)
+#pragma unroll
+    for (int i = 0; i < TG; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[c][i][e] = 0.0f;
+#pragma unroll 2
+  for (int kb = k0 + 32 * part; kb < k1; kb += 32 * kParts) {
+    const int k = kb + 8 * q;
+    const bool in = k < k1;
+    uint4 av[RC][2], xv[TG];
+#pragma unroll
+    for (int c = 0; c < RC; ++c)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        av[c][h] = in && aok[c][h] ? __ldg(reinterpret_cast<const uint4*>(arow[c][h] + k)) : zero;
+#pragma unroll
+    for (int i = 0; i < TG; ++i) xv[i] = in && xok[i] ? __ldg(reinterpret_cast<const uint4*>(xrow[i] + k)) : zero;
+#pragma unroll
+    for (int c = 0; c < RC; ++c)
+#pragma unroll
+      for (int i = 0; i < TG; ++i) {
+        mma_bf16_16816(acc[c][i], av[c][0].x, av[c][1].x, av[c][0].y, av[c][1].y, xv[i].x, xv[i].y);
+        mma_bf16_16816(acc[c][i], av[c][0].z, av[c][1].z, av[c][0].w, av[c][1].w, xv[i].z, xv[i].w);
+      }
+  }
+  // the parts of K are added in order by the first part's warps, a few chunks at a time
+  constexpr int kWarpFloats = 16 * 8 * TG;  // of one chunk of ranks
+  static_assert((kParts - 1) * (kFewWarps / kParts) * kWarpFloats <= kRed, "partial sums fit");
+#pragma unroll
+  for (int c = 0; c < RC; ++c) {
+    float* mine = sm.red + ((part - 1) * (kFewWarps / kParts) + half) * kWarpFloats;
+    if (part > 0) {
+#pragma unroll
+      for (int i = 0; i < TG; ++i)
+        *reinterpret_cast<float4*>(mine + (i * 32 + lane) * 4) = make_float4(acc[c][i][0], acc[c][i][1], acc[c][i][2], acc[c][i][3]);
+    }
+    __syncthreads();
+    if (part == 0) {
+      for (int p = 0; p < kParts - 1; ++p) {
+        const float* other = sm.red + (p * (kFewWarps / kParts) + half) * kWarpFloats;
+#pragma unroll
+        for (int i = 0; i < TG; ++i) {
+          const float4 v = *reinterpret_cast<const float4*>(other + (i * 32 + lane) * 4);
+          acc[c][i][0] += v.x;
+          acc[c][i][1] += v.y;
+          acc[c][i][2] += v.z;
+          acc[c][i][3] += v.w;
+        }
+      }
+      // accumulator element e: rank g + 8 (e / 2), token 2 q + e % 2
+#pragma unroll
+      for (int i = 0; i < TG; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = r0 + 16 * c + g + 8 * (e >> 1), j = (half * TG + i) * 8 + 2 * q + (e & 1);
+          if (r < a.R && j < n) out[static_cast<long long>(order[j]) * a.R + r] = scale * acc[c][i][e];
+        }
+    }
+    __syncthreads();
+  }
+}
+
+template <int RC>
+__global__ void __launch_bounds__(kFewThreads, 2) lora_shrink_few_kernel(const LoraArgs a) {
+  __shared__ __align__(16) FewSmem sm;
+  const int tile = blockIdx.z, split = blockIdx.y;
+  // The next kernel starts only when every CTA has passed this wait, so it may read the call's
+  // inputs without waiting for this grid.
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  sort_tokens(a, sm, tile);
+  // this CTA's part of K, in steps of 32
+  const int steps = (a.K + 31) / 32;
+  const int k0 = static_cast<int>(static_cast<long long>(steps) * split / a.splits) * 32;
+  const int k1 = min(static_cast<int>(static_cast<long long>(steps) * (split + 1) / a.splits) * 32, a.K);
+  float* out = a.t_parts + static_cast<long long>(split) * a.M * a.R;
+  const int units = sm.unit_start[sm.slots];
+  int s = 0;
+  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    while (sm.unit_start[s + 1] <= u) ++s;  // units ascend
+    const int first = sm.start[s] + (u - sm.unit_start[s]) * kUnitTokens;
+    const int n = min(sm.start[s + 1] - first, kUnitTokens);
+    const int id = sm.list[s];
+    const float scale = a.scale ? __ldg(a.scale + id) : 1.0f;
+    const uint16_t* rows = a.lora_a + static_cast<long long>(id) * a.R * a.K;
+    for (int r0 = 0; r0 < a.R; r0 += 16 * RC) {
+      if (n <= 8) few_unit<RC, 1>(a, sm, rows, sm.order + first, n, r0, k0, k1, scale, out);
+      else few_unit<RC, 4>(a, sm, rows, sm.order + first, n, r0, k0, k1, scale, out);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ first product, many tokens
 constexpr int kShrinkThreads = 256;  // loads, products, plan; warps 4..7 epilogue
 constexpr int kShrinkCols = 256;     // columns of an accumulator
 constexpr int kShrinkStages = 3;
@@ -363,12 +597,15 @@ constexpr int kMaxTBufs = 8;
 constexpr int kMaxBlockN = 224;
 constexpr int kTCols = 32;      // TMEM columns of a T buffer: 64 values of K, four chunks of 16 ranks
 constexpr int kChunks = 4;      // chunks of 16 ranks per ring stage
-constexpr int kRingBytes = 196 * 1024;
 constexpr int kStageTarget = 24 * 1024;  // bytes of a ring stage, where blocks are smaller
 constexpr uint32_t kTmemCols = 512;
+// A tile per CTA (persistent), per pair of CTAs (persistent), per cluster that shares K.
+constexpr int kModeSingle = 0, kModePair = 1, kModeSplit = 2;
+// Pairs have the SM to themselves; the others leave room for the first kernel's CTAs.
+__host__ __device__ constexpr int ring_bytes(int mode) { return (mode == kModePair ? 196 : 176) * 1024; }
 // An MMA reads 128 rows of x also where a box has fewer: behind the last stage, too, that stays
 // inside the allocation (what it reads there goes to accumulator rows that are never stored).
-constexpr size_t kSmem = 1024 + kRingBytes + kBM * kBK * 2 + 4096;
+constexpr size_t smem_bytes(int mode) { return 1024 + ring_bytes(mode) + kBM * kBK * 2 + 4096; }
 
 struct LoraBarriers {
   uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], t_full[kMaxTBufs], t_empty[kMaxTBufs];
@@ -485,9 +722,17 @@ __device__ __noinline__ float single_element(const LoraArgs& a, int m, int n) {
   const int id = __ldg(a.adapter + m);
   if (id >= 0 && id < a.num_adapters) {
     const uint16_t* b = a.lora_b + (static_cast<long long>(id) * a.N + n) * a.R;
-    for (int r = 0; r < a.R; ++r)
-      sum = fmaf(__uint_as_float(static_cast<uint32_t>(__ldcg(a.t + static_cast<long long>(m) * a.R + r)) << 16),
-                 __uint_as_float(static_cast<uint32_t>(__ldg(b + r)) << 16), sum);
+    for (int r = 0; r < a.R; ++r) {
+      uint32_t st;  // as the tensor core gets it
+      if (a.t) {
+        st = __ldcg(a.t + static_cast<long long>(m) * a.R + r);
+      } else {
+        float v = 0.0f;
+        for (int s = 0; s < a.splits; ++s) v += __ldcg(a.t_parts + (static_cast<long long>(s) * a.M + m) * a.R + r);
+        st = pack_bf16x2(v, 0.0f);
+      }
+      sum = fmaf(__uint_as_float(st << 16), __uint_as_float(static_cast<uint32_t>(__ldg(b + r)) << 16), sum);
+    }
   }
   return sum;
 }
@@ -502,34 +747,56 @@ __host__ __device__ constexpr int stage_blocks(int box_rows, int wrows) {
 __host__ __device__ constexpr int stage_bytes(int box_rows, int wrows) {
   return stage_blocks(box_rows, wrows) * block_bytes(box_rows, wrows);
 }
-__host__ __device__ constexpr int stage_count(int box_rows, int wrows) {
-  const int n = kRingBytes / stage_bytes(box_rows, wrows);
+__host__ __device__ constexpr int stage_count(int mode, int box_rows, int wrows) {
+  const int n = ring_bytes(mode) / stage_bytes(box_rows, wrows);
   return n > kMaxStages ? kMaxStages : n;
 }
+// Accumulators r of row m, columns n .. n + 7, to the output (where n < N; N is a multiple of 8).
+__device__ __forceinline__ void store8(const LoraArgs& a, int m, int n, const float (&r)[8]) {
+  float odd = 0.0f;  // NaN if some element is not finite
+#pragma unroll
+  for (int v = 0; v < 8; ++v) odd = fmaf(r[v], 0.0f, odd);
+  float f[8];
+#pragma unroll
+  for (int v = 0; v < 8; ++v) f[v] = r[v];
+  if (odd != 0.0f) {
+#pragma unroll
+    for (int v = 0; v < 8; ++v)
+      if (!(fabsf(f[v]) <= 3.402823466e38f)) f[v] = single_element(a, m, n + v);
+  }
+  *reinterpret_cast<uint4*>(a.out + static_cast<long long>(m) * a.N + n) =
+      make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+}
+
 __host__ __device__ constexpr int acc_columns(int bn) { return (bn + 31) / 32 * 32; }
 __host__ __device__ constexpr int t_bufs(int bn) {
   const int n = (static_cast<int>(kTmemCols) - 2 * acc_columns(bn)) / kTCols;
   return n > kMaxTBufs ? kMaxTBufs : n;
 }
 
-// RC: chunks of 16 ranks (a rank in between counts as the next size: the boxes behind R read zeros)
-template <int RC, bool kPair>
-__global__ void __launch_bounds__(kThreads, 1)
+// RC: chunks of 16 ranks (a rank in between counts as the next size: the boxes behind R read zeros).
+// Outside pairs 80 registers (two blocks' worth), so that a CTA of the first kernel fits beside.
+template <int RC, int kMode>
+__global__ void __launch_bounds__(kThreads, kMode == kModePair || RC > 4 ? 1 : 2)
     lora_linear_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
                        const __grid_constant__ CUtensorMap bmap, const LoraArgs a) {
+  constexpr bool kPair = kMode == kModePair, kSplit = kMode == kModeSplit;
   constexpr int kCtas = kPair ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  LoraBarriers& sb = *reinterpret_cast<LoraBarriers*>(tiles + kRingBytes + kBM * kBK * 2);
+  LoraBarriers& sb = *reinterpret_cast<LoraBarriers*>(tiles + ring_bytes(kMode) + kBM * kBK * 2);
   volatile int* abort_flag = &sb.abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = kPair ? static_cast<int>(cluster_ctarank()) : 0;
   const int tiles_m = (a.tiles_m + kCtas - 1) / kCtas, tiles_total = tiles_m * a.tiles_n;
-  const int t_first = blockIdx.x / kCtas, t_step = gridDim.x / kCtas;
+  // parts of K and of the adapters, and this CTA's (the whole, part 0, without clusters)
+  const int parts = kSplit ? a.k_parts : 1, part = kSplit ? static_cast<int>(cluster_ctarank()) : 0;
+  const int t_first = blockIdx.x / (kCtas * parts), t_step = gridDim.x / (kCtas * parts);
   const int bn = a.block_n, wrows = bn / kCtas;
-  const int sub = stage_blocks(a.box_rows, wrows), stages = stage_count(a.box_rows, wrows);
+  const int sub = stage_blocks(a.box_rows, wrows), stages = stage_count(kMode, a.box_rows, wrows);
   const int xbytes = a.box_rows * kBK * 2, bbytes = block_bytes(a.box_rows, wrows), sbytes = sub * bbytes;
-  const int k_blocks = (a.K + kBK - 1) / kBK, k_stages = (k_blocks + sub - 1) / sub;
+  const int all_blocks = (a.K + kBK - 1) / kBK, k_first = all_blocks * part / parts;
+  const int k_blocks = all_blocks * (part + 1) / parts - k_first, k_stages = (k_blocks + sub - 1) / sub;
   const int tbufs = t_bufs(bn);
   const uint32_t acc_stride = acc_columns(bn), t_col = 2 * acc_stride;
   // the leading CTA's barriers
@@ -578,6 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sb.tmem_base;
   const uint32_t ring = smem_u32(tiles);
+  pdl_launch_dependents();  // (they wait for this grid's end)
   // Ring stages of a tile behind those of K: four chunks of 16 ranks each.
   auto adapter_stages = [&](int slots) { return (slots * RC + kChunks - 1) / kChunks; };
   // The plans, one per row block that this CTA passes: made by the warps that write T, read by those
@@ -616,7 +884,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           pair_expect_tx<kPair>(bar, blocks * bbytes);
           for (int u = 0; u < blocks; ++u) {
             const uint32_t dst = ring + p.stage * sbytes + u * bbytes;
-            const int x = (ks * sub + u) * kBK;
+            const int x = (k_first + ks * sub + u) * kBK;
             pair_load_2d<kPair>(dst, &xmap, x, m0, bar, policy);  // rows past M are zero-filled
             pair_load_2d<kPair>(dst + xbytes, &wmap, x, n0, bar, policy);
           }
@@ -629,7 +897,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       const TilePlan& tp = sb.plan[plan.n & 1];
       const int slots = tp.slots;
-      for (int e = 0; e < adapter_stages(slots); ++e, p.next(stages)) {
+      for (int e = part; e < adapter_stages(slots); e += parts, p.next(stages)) {
         const int first = e * kChunks, n = min(kChunks, slots * RC - first);
         ok = free_stage();
         if (!ok) break;
@@ -682,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = next_plan(plan, t / a.tiles_n);
       if (!ok) break;
       const int slots = sb.plan[plan.n & 1].slots;
-      for (int e = 0; e < adapter_stages(slots); ++e, p.next(stages), tb.next(tbufs)) {
+      for (int e = part; e < adapter_stages(slots); e += parts, p.next(stages), tb.next(tbufs)) {
         const int n = min(kChunks, slots * RC - e * kChunks);
         ok = wait_or_abort(smem_u32(&sb.t_full[tb.stage]), tb.round & 1, a.timeout_ns, abort_flag) &&
              wait_or_abort(smem_u32(&sb.full[p.stage]), p.round & 1, a.timeout_ns, abort_flag);
@@ -736,18 +1004,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (plans == 0) pdl_wait_primary();  // t
         ++plans;
         if (my_slot >= 0) {
-          const uint4* src = reinterpret_cast<const uint4*>(a.t + static_cast<long long>(row) * a.R);
+          if constexpr (kPair) {
+            const uint4* src = reinterpret_cast<const uint4*>(a.t + static_cast<long long>(row) * a.R);
 #pragma unroll
-          for (int c = 0; c < 2 * RC; ++c) {  // eight ranks at a time (R is a multiple of 8)
-            const uint4 v = 8 * c < a.R ? __ldcg(src + c) : make_uint4(0, 0, 0, 0);
-            tp[4 * c] = v.x;
-            tp[4 * c + 1] = v.y;
-            tp[4 * c + 2] = v.z;
-            tp[4 * c + 3] = v.w;
+            for (int c = 0; c < 2 * RC; ++c) {  // eight ranks at a time (R is a multiple of 8)
+              const uint4 v = 8 * c < a.R ? __ldcg(src + c) : make_uint4(0, 0, 0, 0);
+              tp[4 * c] = v.x;
+              tp[4 * c + 1] = v.y;
+              tp[4 * c + 2] = v.z;
+              tp[4 * c + 3] = v.w;
+            }
+          } else {
+            const float* src = a.t_parts + static_cast<long long>(row) * a.R;
+            const long long stride = static_cast<long long>(a.M) * a.R;
+#pragma unroll
+            for (int c = 0; c < 4 * RC; ++c) {  // four ranks at a time
+              float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (4 * c < a.R) {
+                for (int s = 0; s < a.splits; ++s) {
+                  const float4 u = __ldcg(reinterpret_cast<const float4*>(src + s * stride + 4 * c));
+                  v.x += u.x;
+                  v.y += u.y;
+                  v.z += u.z;
+                  v.w += u.w;
+                }
+              }
+              tp[2 * c] = pack_bf16x2(v.x, v.y);
+              tp[2 * c + 1] = pack_bf16x2(v.z, v.w);
+            }
           }
         }
       }
-      for (int e = 0; e < adapter_stages(slots); ++e, tb.next(tbufs)) {
+      for (int e = part; e < adapter_stages(slots); e += parts, tb.next(tbufs)) {
         if (ok && tb.round != 0) ok = wait_or_abort(smem_u32(&sb.t_empty[tb.stage]), (tb.round - 1) & 1, a.timeout_ns, abort_flag);
         if (!ok) break;
         tc_fence_after();
@@ -781,7 +1069,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * q) << 16);
     for (int j = 0; j < 2; ++j) {  // both accumulators start from the bias of this CTA's first tiles
       const int t = t_first + j * t_step;
-      if (t < tiles_total) seed_bias(lane_base + j * acc_stride, a.bias, (t % a.tiles_n) * bn, a.N, bn);
+      if (t < tiles_total) seed_bias(lane_base + j * acc_stride, part == 0 ? a.bias : nullptr, (t % a.tiles_n) * bn, a.N, bn);
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -795,32 +1083,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int row = m0 + 32 * q + lane;
       if (!wait_or_abort(smem_u32(&sb.acc_full[b]), (i >> 1) & 1, a.timeout_ns, abort_flag)) break;
       tc_fence_after();
+      if constexpr (kSplit) break;  // the one tile: added up below
       const uint32_t acc = lane_base + b * acc_stride;
       if (m0 + 32 * q < a.M) {  // some row of this warp exists
-        uint16_t* orow = a.out + static_cast<long long>(row) * a.N;
 #pragma unroll 1
         for (int c = 0; c < bn; c += 16) {
           uint32_t r[16];
           tmem_ld16(acc + c, r);
           tc_wait_ld();
-          float odd = 0.0f;  // NaN if some element is not finite
 #pragma unroll
-          for (int v = 0; v < 16; ++v) odd = fmaf(__uint_as_float(r[v]), 0.0f, odd);
-          if (odd != 0.0f && row < a.M) {
+          for (int h = 0; h < 16; h += 8) {
+            float f[8];
 #pragma unroll
-            for (int v = 0; v < 16; ++v)
-              if (n0 + c + v < a.N && !(fabsf(__uint_as_float(r[v])) <= 3.402823466e38f))
-                r[v] = __float_as_uint(single_element(a, row, n0 + c + v));
-          }
-#pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            const int n = n0 + c + 8 * v;
-            if (row < a.M && n < a.N)
-              *reinterpret_cast<uint4*>(orow + n) =
-                  make_uint4(pack_bf16x2(__uint_as_float(r[8 * v]), __uint_as_float(r[8 * v + 1])),
-                             pack_bf16x2(__uint_as_float(r[8 * v + 2]), __uint_as_float(r[8 * v + 3])),
-                             pack_bf16x2(__uint_as_float(r[8 * v + 4]), __uint_as_float(r[8 * v + 5])),
-                             pack_bf16x2(__uint_as_float(r[8 * v + 6]), __uint_as_float(r[8 * v + 7])));
+            for (int v = 0; v < 8; ++v) f[v] = __uint_as_float(r[h + v]);
+            if (row < a.M && n0 + c + h < a.N) store8(a, row, n0 + c + h, f);
           }
         }
       }
@@ -833,6 +1109,70 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
+  if constexpr (kSplit) {
+    // Part p adds up and stores columns [p cw, (p + 1) cw) of the tile.  The others' go into its
+    // ring, whose operands every CTA has consumed behind the first barrier; warps 4..7 and 8..11
+    // take turns of 8 columns.
+    __syncwarp();
+    cluster_sync();
+    tc_fence_after();
+    const int cw = (bn + 8 * parts - 1) / (8 * parts) * 8;
+    const int q = warp & 3, r = 32 * q + lane, half = warp >= 8 ? 1 : 0;
+    const int mt = t_first / a.tiles_n, n0 = (t_first % a.tiles_n) * bn, row = mt * kBM + r;
+    const uint32_t acc = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    const float* recv = reinterpret_cast<const float*>(tiles);  // [part][row][cw]
+    const bool warp_live = warp >= 4 && mt * kBM + 32 * q < a.M;
+    if (warp_live) {
+#pragma unroll 1
+      for (int c = 8 * half; c < bn; c += 16) {
+        const int owner = c / cw;
+        if (owner == part) continue;
+        uint32_t v[8];
+        tmem_ld8(acc + c, v);
+        tc_wait_ld();
+        if (row < a.M) {
+          const uint32_t to = dsmem_addr(ring + 4 * ((part * kBM + r) * cw + c - owner * cw), owner);
+          dsmem_st4(to, __uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]), __uint_as_float(v[3]));
+          dsmem_st4(to + 16, __uint_as_float(v[4]), __uint_as_float(v[5]), __uint_as_float(v[6]), __uint_as_float(v[7]));
+        }
+      }
+    }
+    __syncwarp();
+    cluster_sync();
+    if (warp_live && !*abort_flag) {
+#pragma unroll 1
+      for (int c = part * cw + 8 * half; c < min((part + 1) * cw, bn); c += 16) {
+        uint32_t v[8];
+        tmem_ld8(acc + c, v);
+        tc_wait_ld();
+        if (row < a.M && n0 + c < a.N) {
+          float sum[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) sum[u] = 0.0f;
+          for (int p = 0; p < parts; ++p) {  // in order, whoever adds
+            float4 lo, hi;
+            if (p == part) {
+              lo = make_float4(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]), __uint_as_float(v[3]));
+              hi = make_float4(__uint_as_float(v[4]), __uint_as_float(v[5]), __uint_as_float(v[6]), __uint_as_float(v[7]));
+            } else {
+              const float4* from = reinterpret_cast<const float4*>(recv + (p * kBM + r) * cw + c - part * cw);
+              lo = from[0];
+              hi = from[1];
+            }
+            sum[0] += lo.x;
+            sum[1] += lo.y;
+            sum[2] += lo.z;
+            sum[3] += lo.w;
+            sum[4] += hi.x;
+            sum[5] += hi.y;
+            sum[6] += hi.z;
+            sum[7] += hi.w;
+          }
+          store8(a, row, n0 + c, sum);
+        }
+      }
+    }
+  }
   tc_fence_before();
   __syncthreads();
   if constexpr (kPair) cluster_sync();
@@ -892,89 +1232,87 @@ cudaError_t opt_in(Kern kern, size_t bytes, std::atomic<bool> (&done)[64]) {
   return e;
 }
 
-template <int RC, bool kPair>
+template <int RC, int kMode>
 cudaError_t launch_lora_t(const LoraMaps& m, const LoraArgs& a, int sms, cudaStream_t stream) {
   static std::atomic<bool> done[64];
-  cudaError_t e = opt_in(lora_linear_kernel<RC, kPair>, kSmem, done);
+  cudaError_t e = opt_in(lora_linear_kernel<RC, kMode>, smem_bytes(kMode), done);
   if (e != cudaSuccess) return e;
-  constexpr int kCtas = kPair ? 2 : 1;
-  const int total = (a.tiles_m + kCtas - 1) / kCtas * a.tiles_n, slots = sms / kCtas;
+  constexpr int kCtas = kMode == kModePair ? 2 : 1;
+  const int cluster = kMode == kModeSplit ? a.k_parts : kCtas;
+  const int total = (a.tiles_m + kCtas - 1) / kCtas * a.tiles_n, slots = kMode == kModeSplit ? total : sms / kCtas;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((total < slots ? total : slots) * kCtas, 1, 1);
+  cfg.gridDim = dim3((total < slots ? total : slots) * cluster, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = kSmem;
+  cfg.dynamicSmemBytes = smem_bytes(kMode);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = kCtas;
+  attr[1].val.clusterDim.x = cluster;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = kPair ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, lora_linear_kernel<RC, kPair>, m.x, m.w, m.b, a);
+  cfg.numAttrs = kMode == kModeSingle ? 1 : 2;
+  e = cudaLaunchKernelEx(&cfg, lora_linear_kernel<RC, kMode>, m.x, m.w, m.b, a);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
 
 template <int RC>
 cudaError_t launch_lora_r(const LoraMaps& m, const LoraArgs& a, int sms, cudaStream_t stream) {
-  return a.plan_tiles == 2 ? launch_lora_t<RC, true>(m, a, sms, stream) : launch_lora_t<RC, false>(m, a, sms, stream);
+  if (a.plan_tiles == 2) return launch_lora_t<RC, kModePair>(m, a, sms, stream);
+  return a.k_parts > 1 ? launch_lora_t<RC, kModeSplit>(m, a, sms, stream) : launch_lora_t<RC, kModeSingle>(m, a, sms, stream);
 }
 
 }  // namespace
 
 void lora_plan(LoraArgs& a, int sms) {
   a.tiles_m = (a.M + kBM - 1) / kBM;
-  // the width with the least rounds x (columns + what a tile costs beside its columns)
-  auto cost_of = [&](int bn, int ctas) {
-    const long long tiles = static_cast<long long>((a.tiles_m + ctas - 1) / ctas) * ((a.N + bn - 1) / bn);
-    return (tiles + sms / ctas - 1) / (sms / ctas) * (bn + 48);
-  };
-  long long best = -1;
-  for (int bn = kMaxBlockN; bn >= 16; bn -= 16) {
-    const long long cost = cost_of(bn, 1);
-    if (best < 0 || cost < best) {
-      best = cost;
-      a.block_n = bn;
-    }
-  }
-  // Pairs of CTAs stage half as much of W for the same product; where there are tiles for all pairs
-  // and the last round of tiles is not much emptier for them
-  a.plan_tiles = 1;
-  if (a.tiles_m >= 2) {
-    int pair_n = kMaxBlockN;
-    long long pair_cost = -1;
-    for (int bn = kMaxBlockN; bn >= 128; bn -= 32) {
-      const long long cost = cost_of(bn, 2);
-      if (pair_cost < 0 || cost < pair_cost) {
-        pair_cost = cost;
-        pair_n = bn;
-      }
-    }
-    const long long pair_tiles = static_cast<long long>((a.tiles_m + 1) / 2) * ((a.N + pair_n - 1) / pair_n);
-    if (pair_tiles >= sms / 2 && 10 * pair_cost <= 11 * best) {
-      a.plan_tiles = 2;
-      a.block_n = pair_n;
-    }
-  }
-  a.tiles_n = (a.N + a.block_n - 1) / a.block_n;
   a.box_rows = a.M < kBM ? (a.M + 7) / 8 * 8 : kBM;
-  // parts of K for the first product: a CTA per SM, up to 8 parts of at least two steps
+  const int k_blocks = (a.K + kBK - 1) / kBK;
+  // Estimated cycles of tiles of bn columns, by single CTAs, by pairs or by clusters that share K.  A
+  // block of 64 values of K takes what is longest: the operands' way in (64 bytes a cycle), the
+  // tensor core's reading (128 bytes a cycle, 128 rows of x whatever their number), its arithmetic.
+  // Clusters add up at the end, and the GPU holds 76, 36 or 15 of them (GPCs of 18 to 20 SMs): a
+  // second round is not considered.  (4096 -> 2880, 1 token: single CTAs 12.7 us, clusters of 4 8.3;
+  // 2880 -> 5120, 64 tokens 19.2 and 13.6.)
+  auto cycles = [&](int bn, int ctas, int parts) {
+    const long long tiles = static_cast<long long>((a.tiles_m + ctas - 1) / ctas) * ((a.N + bn - 1) / bn);
+    const long long slots = parts == 1 ? sms / ctas : parts == 2 ? sms / 2 : parts == 4 ? sms * 36 / 152 : sms * 15 / 152;
+    const long long rounds = (tiles + slots - 1) / slots;
+    if (parts > 1 && rounds > 1) return 1LL << 60;
+    const long long in = 2LL * (a.box_rows + bn / ctas), read = kBM + bn / ctas, mma = 2LL * bn;
+    long long block = in > read ? in : read;
+    if (mma > block) block = mma;
+    return rounds * ((k_blocks + parts - 1) / parts) * block + 8LL * bn + (parts > 1 ? 1500 : 0);
+  };
+  long long least = 1LL << 60;
+  auto offer = [&](int bn, int ctas, int parts) {
+    const long long c = cycles(bn, ctas, parts);
+    if (c >= least) return;
+    least = c;
+    a.block_n = bn;
+    a.plan_tiles = ctas;
+    a.k_parts = parts;
+  };
+  for (int bn = kMaxBlockN; bn >= 16; bn -= 16) offer(bn, 1, 1);
+  if (a.tiles_m >= 2)
+    for (int bn = kMaxBlockN; bn >= 32; bn -= 32) offer(bn, 2, 1);
+  for (int parts = 2; parts <= 8 && 2 * parts <= k_blocks; parts *= 2)
+    for (int bn = kMaxBlockN; bn >= 32; bn -= 16) offer(bn, 1, parts);
+  a.tiles_n = (a.N + a.block_n - 1) / a.block_n;
+  // Parts of K of the first product.  Many tokens: a CTA per SM, clusters of up to 8 parts of at
+  // least two steps; few: a step of K for each of a CTA's eight warps, up to 4 parts.
   a.splits = 1;
-  while (a.splits < 8 && 2 * a.splits * a.tiles_m <= sms && 4 * a.splits <= (a.K + kBK - 1) / kBK) a.splits *= 2;
+  if (a.plan_tiles == 2) {
+    while (a.splits < 8 && 2 * a.splits * a.tiles_m <= sms && 4 * a.splits <= k_blocks) a.splits *= 2;
+  } else {
+    a.splits = (a.K + 255) / 256 < 4 ? (a.K + 255) / 256 : 4;
+  }
 }
 
 cudaError_t launch_lora(const LoraMaps& m, const LoraArgs& a, int sms, cudaStream_t stream) {
-  static std::atomic<bool> done[64];
-  cudaError_t e = opt_in(lora_shrink_kernel, kShrinkSmem, done);
-  if (e != cudaSuccess) return e;
-  // CTAs side by side: as many passes of 256 columns as a tile can have
-  int most = a.M < kBM ? a.M : kBM;
-  if (most > a.num_adapters) most = a.num_adapters;
-  const int per_pass = kShrinkCols / a.R, passes = (most + per_pass - 1) / per_pass;
-  const long long room = 2LL * sms / (static_cast<long long>(a.tiles_m) * a.splits);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -983,13 +1321,33 @@ cudaError_t launch_lora(const LoraMaps& m, const LoraArgs& a, int sms, cudaStrea
   attr[1].val.clusterDim.x = 1;
   attr[1].val.clusterDim.y = a.splits;
   attr[1].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(room < 1 ? 1 : room < passes ? room : passes), a.splits, a.tiles_m);
-  cfg.blockDim = dim3(kShrinkThreads, 1, 1);
-  cfg.dynamicSmemBytes = kShrinkSmem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, lora_shrink_kernel, m.x, m.a, a);
+  int most = a.M < kBM ? a.M : kBM;  // distinct adapters of a tile
+  if (most > a.num_adapters) most = a.num_adapters;
+  const long long room = 2LL * sms / (static_cast<long long>(a.tiles_m) * a.splits);
+  cudaError_t e;
+  if (a.plan_tiles == 2) {
+    static std::atomic<bool> done[64];
+    e = opt_in(lora_shrink_kernel, kShrinkSmem, done);
+    if (e != cudaSuccess) return e;
+    // CTAs side by side: as many passes of 256 columns as a tile can have
+    const int per_pass = kShrinkCols / a.R, passes = (most + per_pass - 1) / per_pass;
+    cfg.gridDim = dim3(static_cast<unsigned>(room < 1 ? 1 : room < passes ? room : passes), a.splits, a.tiles_m);
+    cfg.blockDim = dim3(kShrinkThreads, 1, 1);
+    cfg.dynamicSmemBytes = kShrinkSmem;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, lora_shrink_kernel, m.x, m.a, a);
+  } else {
+    // side by side: the units that a tile can have (a long unit more than its adapters)
+    const int units = most + 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(room < 2 ? 2 : room < units ? room : units), a.splits, a.tiles_m);
+    cfg.blockDim = dim3(kFewThreads, 1, 1);
+    cfg.numAttrs = 1;
+    e = a.R <= 16   ? cudaLaunchKernelEx(&cfg, lora_shrink_few_kernel<1>, a)
+        : a.R <= 32 ? cudaLaunchKernelEx(&cfg, lora_shrink_few_kernel<2>, a)
+                    : cudaLaunchKernelEx(&cfg, lora_shrink_few_kernel<4>, a);
+  }
   if (e != cudaSuccess) return e;
   if (a.R <= 16) return launch_lora_r<1>(m, a, sms, stream);
   if (a.R <= 32) return launch_lora_r<2>(m, a, sms, stream);

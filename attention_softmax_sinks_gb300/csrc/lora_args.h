@@ -19,10 +19,13 @@ struct LoraArgs {
   const float* scale;        // [L] or nullptr (1)
   const uint16_t* bias;      // bf16 [N] or nullptr
   uint16_t* out;             // bf16 [M, N]
-  uint16_t* t;               // workspace: bf16 [M, R], s_a x A_a^T
+  // workspace, s_a x A_a^T: bf16 [M, R] (many tokens, else nullptr), or fp32 parts [splits, M, R]
+  uint16_t* t;
+  float* t_parts;
   int M, N, K, R, num_adapters;
-  int splits;                // parts of K of the first product (1, 2, 4 or 8)
+  int splits;                // parts of K of the first product
   int block_n, tiles_m, tiles_n;  // tiles_m: of 128 tokens
+  int k_parts;               // CTAs of a cluster that share a tile's K (1, 2, 4 or 8)
   int plan_tiles;            // 128-token tiles per tile of the product (2: pairs of CTAs)
   int box_rows;              // rows of an x box
   unsigned* status;
@@ -35,7 +38,7 @@ struct LoraMaps {
   CUtensorMap x, w, a, b;
 };
 
-// Tiles for the sizes in a: block_n, tiles_m, tiles_n, plan_tiles, box_rows, splits.
+// Tiles for the sizes in a: block_n, tiles_m, tiles_n, plan_tiles, k_parts, box_rows, splits.
 void lora_plan(LoraArgs& a, int sms);
 cudaError_t launch_lora(const LoraMaps& m, const LoraArgs& a, int sms, cudaStream_t stream);
 

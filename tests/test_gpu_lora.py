@@ -88,6 +88,10 @@ CASES = {
     "tall": (20000, 64, 96, 16, 8, [(i // 999) % 8 for i in range(20000)]),
     "wide": (3, 64, 40000, 16, 2, [0, 1, -1]),
     "decode, 64 tokens": (64, 2880, 5120, 16, 128, mixed(64, 128)),
+    "clusters, 100 tokens": (100, 2880, 1000, 32, 60, mixed(100, 60)),
+    "clusters, odd sizes": (7, 1032, 4104, 24, 9, mixed(7, 9)),
+    "clusters, two row blocks": (200, 4096, 1032, 64, 90, mixed(200, 90)),
+    "clusters, rank 128": (61, 2880, 2880, 128, 61, list(range(61))),
     "pairs, runs": (2700, 264, 5120, 64, 5, [(i // 370) % 5 for i in range(2700)]),
     "pairs, mixed": (2049, 128, 5000, 16, 300, mixed(2049, 300)),
     "pairs, rank 128": (2304, 200, 4352, 128, 3, mixed(2304, 3)),
@@ -112,7 +116,9 @@ def test_without_bias_or_scale(bias, scale):
 def test_without_adapters_like_linear_bias():
     import attention_softmax_sinks_gb300 as sa
     a = make(333, 1024, 520, 16, 5, [-1] * 333)
-    assert torch.equal(call(a), sa.linear_bias(a["x"], a["w"], a["bias"]))
+    # the sums' order differs (parts of K): each result is within the bound, so they differ by twice it
+    got, want = call(a), sa.linear_bias(a["x"], a["w"], a["bias"])
+    assert bool(((got.double() - want.double()).abs() <= 2 * reference(a)[1]).all())
 
 
 def test_tokens_stand_alone():
