@@ -13,6 +13,7 @@ head's sink is one extra softmax logit that carries no value row.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -363,16 +364,18 @@ def sink_attn_decode_shared(q, paged_k, paged_v, page_table, kv_lens, sinks, gro
     max_pages, dev = page_table.shape[1], q.device
     most = _c_int(int(max_shared_pages), "max_shared_pages")
     if splits is None:
-        splits = sink_attn_decode_shared_splits(b, groups, hq, hkv, most, max_pages, _sm_count(di))
+        splits = _shared_splits(b, groups, hq, hkv, most, max_pages, _sm_count(di))
     ss, so = (_c_int(int(v), "splits") for v in splits)
     if not (1 <= ss <= 255 and 1 <= so <= 256 - ss):  # no memory for what the call refuses
         raise ValueError(f"splits must be at least 1 each and at most 256 together, got {(ss, so)}")
+    scratch, rows = None, b * (ss + so) * hq
     if workspace is None:
-        partial_o = _new((b, ss + so, hq, d), torch.float32, dev, stream)
-        partial_lse = _new((b, ss + so, hq), torch.float32, dev, stream)
+        scratch = _Scratch(4 * rows * (d + 1), di, stream) if rows else None
+        po = scratch.ptr if rows else 0
+        pl = po + 4 * rows * d
     else:
-        partial_o = _out(workspace[0], "workspace[0]", torch.float32, (b, ss + so, hq, d), di)
-        partial_lse = _out(workspace[1], "workspace[1]", torch.float32, (b, ss + so, hq), di)
+        po = _out(workspace[0], "workspace[0]", torch.float32, (b, ss + so, hq, d), di).data_ptr()
+        pl = _out(workspace[1], "workspace[1]", torch.float32, (b, ss + so, hq), di).data_ptr()
     out = (_new((b, hq, d), torch.bfloat16, dev, stream) if out is None
            else _out(out, "out", torch.bfloat16, (b, hq, d), di))
     if lse is None and return_lse:
@@ -382,7 +385,8 @@ def sink_attn_decode_shared(q, paged_k, paged_v, page_table, kv_lens, sinks, gro
     st = _call(load_library().sink_attn_decode_shared, di, stream, q.data_ptr(), paged_k.data_ptr(), paged_v.data_ptr(),
                page_table.data_ptr(), kv_lens.data_ptr(), sinks.data_ptr(), group_offsets.data_ptr(),
                shared_pages.data_ptr(), b, groups, hq, hkv, d, page_size, max_pages, num_pages, most, float(sm_scale),
-               ss, so, partial_o.data_ptr(), partial_lse.data_ptr(), out.data_ptr(), _ptr(lse))
+               ss, so, po, pl, out.data_ptr(), _ptr(lse))
+    del scratch
     _check(st, "sink_attn_decode_shared")
     return out, lse
 
@@ -404,6 +408,9 @@ def sink_attn_decode_shared_splits(batch: int, num_groups: int, num_qo_heads: in
     load_library().sink_attn_decode_shared_splits(batch, num_groups, num_qo_heads, num_kv_heads, max_shared_pages,
                                                   max_pages, num_sms, ctypes.byref(s), ctypes.byref(o))
     return s.value, o.value
+
+
+_shared_splits = functools.lru_cache(maxsize=4096)(sink_attn_decode_shared_splits)
 
 
 def sink_attn_decode_splits(batch: int, num_kv_heads: int, max_kv_len: int, page_size: int = 16,
@@ -542,6 +549,9 @@ def lora_workspace_bytes(m: int, k: int, rank: int) -> int:
     return load_library().lora_workspace_bytes(_c_int(m, "m"), _c_int(k, "k"), _c_int(rank, "rank"))
 
 
+_lora_bytes = functools.lru_cache(maxsize=4096)(lora_workspace_bytes)
+
+
 def lora_linear_bias(x, w, lora_a, lora_b, adapter_idx, bias=None, lora_scale=None, out=None, workspace=None,
                      stream=None):
     """linear_bias with the low-rank adapters of many requests at once beside it:
@@ -563,18 +573,21 @@ def lora_linear_bias(x, w, lora_a, lora_b, adapter_idx, bias=None, lora_scale=No
         named.append(("lora_scale", lora_scale, torch.float32, (l,)))
     di = _inputs(*named)
     lib = load_library()
-    need = lib.lora_workspace_bytes(m, k, r)
+    need, scratch, ws = _lora_bytes(m, k, r), None, 0
     if workspace is None:
-        workspace = _new(need, torch.uint8, x.device, stream)
+        if need:
+            scratch = _Scratch(need, di, stream)
+            ws = scratch.ptr
     else:
         _dev(workspace, "workspace", torch.uint8)
         _same_device(di, ("workspace", workspace))
         if workspace.numel() < need:
             raise ValueError(f"workspace must have at least {need} bytes, got {workspace.numel()}")
+        ws = workspace.data_ptr()
     out = _product_output(out, m, n, x, di, stream)
     st = _call(lib.lora_linear_bias, di, stream, x.data_ptr(), w.data_ptr(), _ptr(bias), lora_a.data_ptr(),
-               lora_b.data_ptr(), _ptr(lora_scale), adapter_idx.data_ptr(), m, n, k, r, l, workspace.data_ptr(),
-               out.data_ptr())
+               lora_b.data_ptr(), _ptr(lora_scale), adapter_idx.data_ptr(), m, n, k, r, l, ws, out.data_ptr())
+    del scratch
     _check(st, "lora_linear_bias")
     return out
 
@@ -672,12 +685,36 @@ def _new(shape, dtype, dev, stream):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
+class _Scratch:
+    """Memory of a call's own, from the memory of the stream that uses it: given back when the call
+    has been enqueued, so that whatever the stream does next may have it (a third of what a tensor
+    costs the host)."""
+    __slots__ = ("ptr",)
+
+    def __init__(self, nbytes, di, stream):
+        s = torch._C._cuda_getCurrentRawStream(di) if stream is None else stream.cuda_stream
+        if torch._C._cuda_getDevice() == di:
+            self.ptr = torch._C._cuda_cudaCachingAllocator_raw_alloc(nbytes, s)
+        else:
+            with torch.cuda.device(di):
+                self.ptr = torch._C._cuda_cudaCachingAllocator_raw_alloc(nbytes, s)
+
+    def __del__(self):
+        if getattr(self, "ptr", 0):
+            torch._C._cuda_cudaCachingAllocator_raw_delete(self.ptr)
+
+
 def _inputs(*named):
     """Validate (name, tensor, dtype, shape) tuples: CUDA, dtype, contiguous, shape (an int: any
     shape of that many dimensions), all on the first tensor's device.  Returns that device's
     index.  Optional tensors are left out by the caller when they are None."""
     di = -1
     for name, t, dt, shape in named:
+        try:  # what a good call's tensors but the first are
+            if t.dtype is dt and t.shape == shape and t.get_device() == di >= 0 and t.is_contiguous() and t.numel() <= _C_INT:
+                continue
+        except AttributeError:
+            pass
         if not isinstance(t, torch.Tensor) or t.dtype is not dt or not t.is_contiguous():
             _dev(t, name, dt)  # raises
         d = t.get_device()  # -1 on the CPU

@@ -31,6 +31,7 @@
 //    after the wait, the warp's first page ids are read in the same round trip
 //    as the sequence length, for the length seen before the wait, and read
 //    again only if the length changed (64 x 4096 step 78.3 -> 78.0 us).
+#include <atomic>
 #include <mutex>
 #include "internal.h"
 #include "ptx.cuh"
@@ -668,9 +669,18 @@ cudaError_t launch_decode(const CUtensorMap& kmap, const CUtensorMap& vmap, cons
 cudaError_t launch_decode_own(const CUtensorMap& kmap, const CUtensorMap& vmap, const DecodeArgs& a,
                               const SharedPlan& plan, cudaStream_t stream) {
   const size_t smem = decode_smem_bytes();
-  auto kern = a.group <= 8 ? sink_decode_kernel<1, false, true> : sink_decode_kernel<2, false, true>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const int tiles = a.group <= 8 ? 0 : 1;
+  auto kern = tiles == 0 ? sink_decode_kernel<1, false, true> : sink_decode_kernel<2, false, true>;
+  // the shared-memory opt-in, once per device and kernel (host threads may race here)
+  static std::atomic<bool> done[64][2];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !done[dev][tiles].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) done[dev][tiles].store(true, std::memory_order_release);
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.num_splits, a.hkv, a.batch);
   cfg.blockDim = dim3(kWarps * 32, 1, 1);

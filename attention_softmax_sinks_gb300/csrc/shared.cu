@@ -26,6 +26,7 @@
 //                 sum takes the weights before that rounding); warps without rows only keep step
 // O is rescaled only when the maximum grows by more than 2^8 (O / d does not change).
 // A slot without keys, or of a group that shares nothing, writes zeros and lse = -inf.
+#include <atomic>
 #include <cstdint>
 
 #include "internal.h"
@@ -513,9 +514,17 @@ long long shared_row_tiles(int batch, int num_groups, int group) {
 
 cudaError_t launch_shared(const CUtensorMap& kmap, const CUtensorMap& vmap, const SharedArgs& a, cudaStream_t stream) {
   const size_t smem = sizeof(SharedSmem) + 1024;
-  cudaError_t e = cudaFuncSetAttribute(shared_prefix_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  // the shared-memory opt-in, once per device (host threads may race here: atomic flags, and
+  // setting the attribute twice is harmless)
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !done[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(shared_prefix_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.plan.shared_splits, a.hkv, static_cast<unsigned>(shared_row_tiles(a.batch, a.plan.num_groups, a.group)));
   cfg.blockDim = dim3(kThreads, 1, 1);
