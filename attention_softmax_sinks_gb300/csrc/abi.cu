@@ -439,14 +439,16 @@ void sink_attn_decode_shared_splits(int batch, int num_groups, int num_qo_heads,
   if (batch > 0 && num_groups > 0 && num_kv_heads > 0 && num_qo_heads >= num_kv_heads && max_shared_pages >= 0 &&
       max_pages > 0) {
     if (num_sms <= 0) num_sms = 152;
-    // shared part: one CTA per SM at a time, so as many splits as fit one wave, at least one tile
-    // of 8 pages each; more than 24 cost more to merge than they gain
+    // shared part: its CTAs' equal runs cut a unit of work into as many parts as it has CTAs, and one
+    // more; more than 24 cost more to merge than they gain
+    const int group = num_qo_heads / num_kv_heads;
     const long long tiles = (max_shared_pages + 7) / 8;
-    const long long units = sa::shared_row_tiles(batch, num_groups, num_qo_heads / num_kv_heads) * num_kv_heads;
-    long long n = num_sms / units;
-    if (n > tiles) n = tiles;
+    const long long units = sa::shared_row_tiles(batch, 1, group) * num_kv_heads;
+    const long long ctas = sa::shared_ctas(batch, num_groups, group, num_kv_heads, max_shared_pages, max_pages, num_sms);
+    long long n = (ctas + units - 1) / units + 1;
+    if (n > tiles + 1) n = tiles + 1;
     if (n > 24) n = 24;
-    s = n < 1 ? 1 : static_cast<int>(n);
+    s = n < 2 ? 2 : static_cast<int>(n);
     // own part: three CTAs per SM, at least 16 pages each, at most 8 splits
     const long long own_pages = max_pages > max_shared_pages ? max_pages - max_shared_pages : 1;
     const long long own_units = static_cast<long long>(batch) * num_kv_heads;
@@ -570,7 +572,7 @@ sa_status sink_attn_decode_shared(const void* q, const void* paged_k, const void
                                   float sm_scale, int shared_splits, int own_splits,
                                   float* partial_o, float* partial_lse, void* out, float* lse,
                                   cudaStream_t stream) {
-  if (batch < 0 || batch > 65535 || num_groups <= 0 || max_pages <= 0 || num_pages <= 0) return SA_ERR_SHAPE;
+  if (batch < 0 || batch > 65535 || num_groups <= 0 || num_groups > 65535 || max_pages <= 0 || num_pages <= 0) return SA_ERR_SHAPE;
   if (max_shared_pages < 0 || max_shared_pages > max_pages || max_pages > (1 << 26)) return SA_ERR_SHAPE;
   if (shared_splits < 1 || own_splits < 1 || shared_splits > 256 || own_splits > 256 || shared_splits + own_splits > 256)
     return SA_ERR_SHAPE;
@@ -590,7 +592,9 @@ sa_status sink_attn_decode_shared(const void* q, const void* paged_k, const void
       !aligned4(shared_pages) || !aligned4(partial_lse) || !aligned4(lse))
     return SA_ERR_ALIGNMENT;
   const int group = num_qo_heads / num_kv_heads;
-  if (sa::shared_row_tiles(batch, num_groups, group) > 65535) return SA_ERR_SHAPE;
+  // tiles of 128 shared keys of all row tiles, counted in 32 bits
+  if (sa::shared_row_tiles(batch, num_groups, group) * num_kv_heads * ((max_shared_pages + 7) / 8) >= (1LL << 30))
+    return SA_ERR_SHAPE;
   unsigned* status = nullptr;
   if (sa_status s = status_ptr(&status)) return s;
   CUtensorMap km, vm;
@@ -609,6 +613,7 @@ sa_status sink_attn_decode_shared(const void* q, const void* paged_k, const void
   a.group = group;
   a.max_pages = max_pages;
   a.num_pages = num_pages;
+  a.ctas = sa::shared_ctas(batch, num_groups, group, num_kv_heads, max_shared_pages, max_pages, sm_count());
   a.scale_log2 = sm_scale * kLog2e;
   a.status = status;
   a.timeout_ns = g_timeout_ns;
@@ -633,7 +638,7 @@ sa_status sink_attn_decode_shared(const void* q, const void* paged_k, const void
   d.timeout_ns = g_timeout_ns;
   if (sa::launch_decode_own(km, vm, d, plan, stream) != cudaSuccess) return SA_ERR_LAUNCH;
   const sa::MergeArgs m{partial_o, partial_lse, out, lse, batch, shared_splits + own_splits, num_qo_heads};
-  return sa::launch_merge(m, stream) == cudaSuccess ? SA_OK : SA_ERR_LAUNCH;
+  return sa::launch_shared_merge(m, stream) == cudaSuccess ? SA_OK : SA_ERR_LAUNCH;
 }
 
 sa_status sink_attn_merge(const float* partial_o, const float* partial_lse, int batch,

@@ -579,6 +579,10 @@ __global__ void __launch_bounds__(kWarps * 32)
     }
   }
   if constexpr (kShared) {
+    // nobody else writes the shared slots of a sequence that shares nothing
+    if (page0 == 0 && split == 0)
+      for (int i = threadIdx.x; i < G * plan.shared_splits; i += kWarps * 32)
+        a.lse[(static_cast<size_t>(b) * (plan.shared_splits + plan.own_splits) + i / G) * a.hq + kvh * G + i % G] = kNegInf;
     if (blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1) pdl_wait_primary();
   }
   if (!clustered) return;

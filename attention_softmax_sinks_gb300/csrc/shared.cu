@@ -15,17 +15,22 @@
 // h G + r % G), so a shared page is read once per 256 rows and the products run on tcgen05 tiles
 // of 128 rows.
 //
-// One CTA per (slot, KV head, pair of row tiles), 12 warps:
+// Work is counted in tiles of 128 keys of a unit (KV head, pair of row tiles), unit behind unit, and
+// dealt out in equal runs: one run per CTA, of a grid that leaves SMs to the own parts, which are
+// bound by memory where this is bound by arithmetic.  A run covers the end of one unit and the
+// beginning of the next, or several; the part of a unit in a run is a slot of its results.  A CTA
+// has 12 warps:
 //   warp 0        pages by TMA, one per lane, into a ring of four stages of 128 keys
 //   warps 1, 2    one elected thread each issues a row tile's products: S = Q K^T (M = 128,
 //                 N = 128, K = 64) and O += P V with P from TMEM (M = 128, N = 64, K = 128)
 //   warps 4..11   four warps per row tile, a thread per row: it copies its row of Q into shared
 //                 memory (any G: rows of neighbouring heads and sequences fill the tiles without
 //                 gaps), then for each tile of keys the running maximum and sum and P in bf16
-//                 (relative error 2^-9 per weight, as in the other attention kernels; the
+//                 (relative error 2^-8 at most per weight, as in the other attention kernels; the
 //                 sum takes the weights before that rounding); warps without rows only keep step
 // O is rescaled only when the maximum grows by more than 2^8 (O / d does not change).
-// A slot without keys, or of a group that shares nothing, writes zeros and lse = -inf.
+// Slots that a unit does not use get lse = -inf and are not read by the merge; those of sequences
+// that share nothing are marked by the own parts' kernel.
 #include <atomic>
 #include <cstdint>
 
@@ -48,6 +53,24 @@ constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr unsigned long long kDrainTimeoutNs = 2000000000ull;
 
+constexpr int kMaxChunks = 176;  // kThreads groups each: up to 65535 groups
+
+// Where a warp is in its CTA's runs.
+struct Walk {
+  int run;       // of the CTA
+  int at, end;   // the rest of the run
+  int in_group;  // work of group g before `at`
+  int g, first_seq, count, pages;
+};
+
+// A unit's part of a run: rows [row0, row0 + rows) of the group that begins with sequence first_seq,
+// KV head kvh, tiles of keys [tile0, tile0 + n_kv) of its n_pages pages.
+struct Segment {
+  int first_seq, row0, rows, n_pages, kvh, tile0, n_kv;
+  int slot;   // where the results go
+  int empty;  // slots behind it that stay empty (the unit's last part)
+};
+
 struct __align__(1024) SharedSmem {
   uint8_t q[2][kTileBytes];
   uint8_t k[kStages][kTileBytes];
@@ -63,9 +86,16 @@ struct __align__(1024) SharedSmem {
   uint32_t tmem_base;
   int abort_flag;
   int issued_kv;
-  int found;                   // group of this CTA, -1: none
-  int first_tile;              // row tile pairs before that group
+  int total;                   // tiles of keys of all units
+  int most;                    // of one unit
+  int quantum;                 // of one run
+  int runs;
+  int each;                    // 0, or a unit's length in runs of one unit each
   int warp_sum[kThreads / 32];
+  int warp_most[kThreads / 32];
+  int chunk[kMaxChunks];       // work before each kThreads groups
+  Walk walk[kThreads / 32];    // of each warp
+  Segment seg[kThreads / 32];
 };
 
 __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
@@ -119,24 +149,73 @@ __device__ __forceinline__ bool group_bounds(const SharedArgs& a, int g, int& fi
   return good;
 }
 
-// Pairs of row tiles of a group of `count` sequences.
+// Pairs of row tiles of a group of `count` sequences, and its tiles of keys.
 __device__ __forceinline__ int row_tile_pairs(const SharedArgs& a, int count) {
   return (count * a.group + 2 * kBlockQ - 1) / (2 * kBlockQ);
 }
+__device__ __forceinline__ int key_tiles(int pages) { return (pages + kPagesPerTile - 1) / kPagesPerTile; }
 
-// Finds the group whose row tiles contain pair `pair` (sm.found, sm.first_tile), by prefix sums
-// over kThreads groups at a time.  All threads; leaves sm.found = -1 behind the last pair.
-__device__ __noinline__ void find_group(const SharedArgs& a, SharedSmem& sm, int pair) {
+// A group's units' length (`each` or, 0, its tiles of keys; 0 if it shares nothing) and number.
+__device__ __forceinline__ int group_work(const SharedArgs& a, int count, int pages, int each, int& len) {
+  const int tiles = count > 0 ? key_tiles(pages) : 0;
+  len = each && tiles ? each : tiles;
+  return row_tile_pairs(a, count) * a.hkv * len;
+}
+
+// Sums up the groups' work, kThreads groups at a time: sm.total, sm.most, sm.chunk.  All threads.
+__device__ __forceinline__ void sum_work(const SharedArgs& a, SharedSmem& sm, int each, bool report) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const bool reporter = pair == 0 && blockIdx.x == 0 && blockIdx.y == 0;  // looks at every group
   int before = 0;
+  int most = 0;
   for (int g0 = 0; g0 < a.plan.num_groups; g0 += kThreads) {
     const int g = g0 + static_cast<int>(threadIdx.x);
     int n = 0;
+    int tiles = 0;
     if (g < a.plan.num_groups) {
       int first, count, pages;
-      if (!group_bounds(a, g, first, count, pages) && reporter) raise_status(a.status, kStatusBadLen);
-      n = row_tile_pairs(a, count);
+      if (!group_bounds(a, g, first, count, pages) && report) raise_status(a.status, kStatusBadLen);
+      int len;
+      n = group_work(a, count, pages, each, len);
+      tiles = len;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      n += __shfl_xor_sync(0xffffffffu, n, off);
+      tiles = max(tiles, __shfl_xor_sync(0xffffffffu, tiles, off));
+    }
+    __syncthreads();  // the last round's sums have been read
+    if (lane == 0) {
+      sm.warp_sum[warp] = n;
+      sm.warp_most[warp] = tiles;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) sm.chunk[g0 / kThreads] = before;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      before += sm.warp_sum[w];
+      most = max(most, sm.warp_most[w]);
+    }
+  }
+  if (threadIdx.x == 0) {
+    sm.total = before;
+    sm.most = most;
+  }
+  __syncthreads();
+}
+
+// The warp's walk stands at position `pos` of the work (below sm.total), for `quantum` of it.  The
+// whole warp.
+__device__ __forceinline__ void seek(const SharedArgs& a, SharedSmem& sm, Walk& walk, int pos, int quantum, int each) {
+  const int lane = threadIdx.x & 31;
+  int c = 0;
+  while ((c + 1) * kThreads < a.plan.num_groups && sm.chunk[c + 1] <= pos) ++c;
+  int before = sm.chunk[c];
+  for (int g0 = c * kThreads; g0 < a.plan.num_groups; g0 += 32) {
+    const int g = g0 + lane;
+    int first = 0, count = 0, pages = 0, len;
+    int n = 0;
+    if (g < a.plan.num_groups) {
+      group_bounds(a, g, first, count, pages);
+      n = group_work(a, count, pages, each, len);
     }
     int incl = n;
 #pragma unroll
@@ -144,22 +223,59 @@ __device__ __noinline__ void find_group(const SharedArgs& a, SharedSmem& sm, int
       const int v = __shfl_up_sync(0xffffffffu, incl, off);
       if (lane >= off) incl += v;
     }
-    __syncthreads();  // the last round's sums have been read
-    if (lane == 31) sm.warp_sum[warp] = incl;
-    __syncthreads();
-    int total = 0, mine = before;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) mine += sm.warp_sum[w];
-      total += sm.warp_sum[w];
+    const int start = before + incl - n;
+    if (n > 0 && pos >= start && pos < start + n) {
+      walk.at = pos;
+      walk.end = quantum < sm.total - pos ? pos + quantum : sm.total;
+      walk.in_group = pos - start;
+      walk.g = g;
+      walk.first_seq = first;
+      walk.count = count;
+      walk.pages = pages;
     }
-    const int start = mine + incl - n;
-    if (n > 0 && pair >= start && pair < start + n) {
-      sm.found = g;
-      sm.first_tile = start;
-    }
-    before += total;
-    if (pair < before && !reporter) break;  // the same for every thread
+    before += __shfl_sync(0xffffffffu, incl, 31);
+    if (pos < before) break;
   }
+  __syncwarp();
+}
+
+// The walk's next part of a unit, if any.  The whole warp.
+__device__ __forceinline__ bool next_segment(const SharedArgs& a, Walk& walk, Segment& seg, int quantum, int each) {
+  Walk w = walk;
+  Segment s{};
+  bool found = false;
+  while (!found && w.at < w.end) {
+    int len;
+    const int work = group_work(a, w.count, w.pages, each, len);
+    if (w.in_group >= work) {  // on to the next group
+      if (++w.g >= a.plan.num_groups) break;
+      w.in_group = 0;
+      group_bounds(a, w.g, w.first_seq, w.count, w.pages);
+      continue;
+    }
+    const int unit = w.in_group / len, off = w.in_group % len;
+    const int n = min(len - off, w.end - w.at);
+    const int unit_start = w.at - off;
+    s.first_seq = w.first_seq;
+    s.row0 = unit / a.hkv * 2 * kBlockQ;
+    s.rows = min(w.count * a.group - s.row0, 2 * kBlockQ);
+    s.n_pages = w.pages;
+    s.kvh = unit % a.hkv;
+    s.tile0 = off;
+    s.n_kv = min(n, key_tiles(w.pages) - off);  // (a unit shorter than `each` leaves the rest idle)
+    s.slot = w.at / quantum - unit_start / quantum;
+    s.empty = off + n == len ? a.plan.shared_splits - 1 - s.slot : 0;
+    w.at += n;
+    w.in_group += n;
+    found = s.n_kv > 0;
+  }
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) {
+    walk = w;
+    seg = s;
+  }
+  __syncwarp();
+  return found;
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -168,11 +284,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   SharedSmem& sm = *reinterpret_cast<SharedSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int split = blockIdx.x, kvh = blockIdx.y, pair = blockIdx.z;
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&kmap);
     tma_prefetch_desc(&vmap);
-    sm.found = -1;
   }
   // Launched with programmatic stream serialisation.  Every CTA lets the next kernel start only
   // after its own wait, so that kernel (the own parts) may read the call's inputs without waiting
@@ -181,38 +295,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
 
   __syncthreads();
-  find_group(a, sm, pair);
-  __syncthreads();
-  const int g = sm.found;
-  if (g < 0) return;  // uniform: no such row tile
-  int first_seq, n_seq, n_pages;
-  group_bounds(a, g, first_seq, n_seq, n_pages);
-  const int row0 = (pair - sm.first_tile) * 2 * kBlockQ;  // first row within the group
-  const int rows = min(n_seq * a.group - row0, 2 * kBlockQ);
-  const int ntiles = rows > kBlockQ ? 2 : 1;
-  // this slot's tiles of keys: an even share of the group's
-  const int all_tiles = (n_pages + kPagesPerTile - 1) / kPagesPerTile;
-  const int splits = a.plan.shared_splits;
-  const int tile0 = static_cast<int>(static_cast<long long>(all_tiles) * split / splits);
-  const int n_kv = static_cast<int>(static_cast<long long>(all_tiles) * (split + 1) / splits) - tile0;
-  const int n_keys = n_pages * kPageSize;
-  const int slots = splits + a.plan.own_splits;
-  // where row r of this CTA goes: its sequence and query head
-  auto row_index = [&](int r, int& seq, int& head) {
-    const int gr = row0 + r;
-    seq = first_seq + gr / a.group;
-    head = kvh * a.group + gr % a.group;
-  };
-
-  if (n_kv == 0) {  // uniform
-    for (int i = threadIdx.x; i < rows * (kHeadDim / 4); i += kThreads) {
-      int seq, head;
-      row_index(i / (kHeadDim / 4), seq, head);
-      const size_t out = (static_cast<size_t>(seq) * slots + split) * a.hq + head;
-      reinterpret_cast<float4*>(a.partial_o)[out * (kHeadDim / 4) + i % (kHeadDim / 4)] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i % (kHeadDim / 4) == 0) a.partial_lse[out] = kNegInf;
-    }
-    return;
+  // Runs of equal length, as long as it takes for the grid to cover the work and for no unit to
+  // have more parts than slots (a unit meets at most one run more than its length holds).  One
+  // slot: a run per unit, all as long as the longest.
+  const int slots = a.plan.shared_splits;
+  sum_work(a, sm, 0, blockIdx.x == 0);
+  const int most = sm.most, each = slots == 1 ? most : 0;
+  if (each) sum_work(a, sm, each, false);
+  const int total = sm.total, grid = gridDim.x;
+  int quantum = each ? each : total / grid + (total % grid != 0);
+  if (!each && quantum < (most + slots - 2) / (slots - 1)) quantum = (most + slots - 2) / (slots - 1);
+  if (quantum < 1) quantum = 1;
+  // this CTA's runs: blockIdx.x, + gridDim.x, ..
+  const int runs = total / quantum + (total % quantum != 0);
+  if (static_cast<int>(blockIdx.x) >= runs) return;  // uniform, before any barrier or TMEM use
+  if (threadIdx.x == 0) {
+    sm.quantum = quantum;
+    sm.runs = runs;
+    sm.each = each;
   }
 
   volatile int* abort_flag = &sm.abort_flag;
@@ -227,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_u32(&sm.kv_full[s]), 1);
-      mbar_init(smem_u32(&sm.kv_empty[s]), ntiles);
+      mbar_init(smem_u32(&sm.kv_empty[s]), 2);
     }
     sm.abort_flag = 0;
     sm.issued_kv = 0;
@@ -242,141 +342,184 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   auto tmem_base = [&]() { return *reinterpret_cast<volatile const uint32_t*>(&sm.tmem_base); };
 
-  // 128 * 56 + 256 * 224 = 384 * 168 registers (the launch's total)
+  const int slot_rows = slots + a.plan.own_splits;  // slots of a sequence's results
+  Segment& seg = sm.seg[warp];  // the warp's present part of a unit
+  // body(tiles of keys of this part, of the parts before) for every part of this CTA's runs, until it
+  // returns false; every warp walks by itself.
+  // (What it needs from part to part stays in shared memory: the softmax warps have no registers left.)
+  auto for_segments = [&](auto&& body) {
+    volatile SharedSmem& vs = sm;
+    if (lane == 0) sm.walk[warp].run = blockIdx.x;
+    __syncwarp();
+    int g = 0;
+    while (vs.walk[warp].run < vs.runs) {
+      seek(a, sm, sm.walk[warp], vs.walk[warp].run * vs.quantum, vs.quantum, vs.each);
+      while (next_segment(a, sm.walk[warp], seg, vs.quantum, vs.each)) {
+        const int n = seg.n_kv;
+        if (!body(n, g)) return;
+        g += n;
+      }
+      __syncwarp();
+      if (lane == 0) sm.walk[warp].run += gridDim.x;
+      __syncwarp();
+    }
+  };
+
+  // 128 * 80 + 256 * 208 registers, of the launch's 384 * 168 (with fewer for the four control warps, what
+  // every role needs of the set-up is spilled)
   if (warp < 4) {
-    regs_dec<56>();
+    regs_dec<80>();
     if (warp == 0) {
       // ------------------------------------------------------------ pages
       const uint64_t policy = l2_policy_evict_last();  // other row tiles read the same pages
-      const int32_t* ptab = a.page_table + static_cast<size_t>(first_seq) * a.max_pages;
       const int no_page = a.num_pages * a.hkv * kPageSize;  // a row behind the cache: reads as zeros
-      auto load_row = [&](int j) {  // first cache row of box `lane` of tile j (lanes < 8)
-        const int lp = (tile0 + j) * kPagesPerTile + lane;
-        if (lane >= kPagesPerTile || lp >= n_pages) return no_page;
-        const int phys = __ldg(ptab + lp);
-        if (phys < 0 || phys >= a.num_pages) {
-          raise_status(a.status, kStatusBadPage);
-          return no_page;
-        }
-        return (phys * a.hkv + kvh) * kPageSize;
-      };
-      int row = load_row(0);
       bool ok = true;
-      for (int j = 0; j < n_kv; ++j) {
-        const int st = j % kStages;
-        const int next = j + 1 < n_kv ? load_row(j + 1) : no_page;  // in flight while tile j is issued
-        if (j >= kStages) {
-          int r = 1;
-          if (lane == 0) r = wait_bar(smem_u32(&sm.kv_empty[st]), ((j / kStages) - 1) & 1, a.timeout_ns, abort_flag) ? 1 : 0;
-          if (!__shfl_sync(0xffffffffu, r, 0)) {
-            ok = false;
-            break;
+      for_segments([&](int n_kv, int g) {
+        const int32_t* ptab = a.page_table + static_cast<size_t>(seg.first_seq) * a.max_pages;
+        const int n_pages = seg.n_pages, tile0 = seg.tile0, kvh = seg.kvh;
+        auto load_row = [&](int j) {  // first cache row of box `lane` of tile j (lanes < 8)
+          const int lp = (tile0 + j) * kPagesPerTile + lane;
+          if (lane >= kPagesPerTile || lp >= n_pages) return no_page;
+          const int phys = __ldg(ptab + lp);
+          if (phys < 0 || phys >= a.num_pages) {
+            raise_status(a.status, kStatusBadPage);
+            return no_page;
           }
+          return (phys * a.hkv + kvh) * kPageSize;
+        };
+        int row = load_row(0);
+        for (int j = 0; j < n_kv; ++j) {
+          const int gg = g + j, st = gg % kStages;
+          const int next = j + 1 < n_kv ? load_row(j + 1) : no_page;  // in flight while tile j is issued
+          if (gg >= kStages) {
+            int r = 1;
+            if (lane == 0) r = wait_bar(smem_u32(&sm.kv_empty[st]), ((gg / kStages) - 1) & 1, a.timeout_ns, abort_flag) ? 1 : 0;
+            if (!__shfl_sync(0xffffffffu, r, 0)) return ok = false;
+          }
+          const uint32_t bar = smem_u32(&sm.kv_full[st]);
+          if (lane == 0) mbar_arrive_expect_tx(bar, 2 * kTileBytes);
+          __syncwarp();
+          if (lane < kPagesPerTile) {
+            tma_load_2d(smem_u32(sm.k[st]) + lane * kPageSize * 128, &kmap, 0, row, bar, policy);
+            tma_load_2d(smem_u32(sm.v[st]) + lane * kPageSize * 128, &vmap, 0, row, bar, policy);
+          }
+          if (lane == 0) sm.issued_kv = gg + 1;
+          row = next;
         }
-        const uint32_t bar = smem_u32(&sm.kv_full[st]);
-        if (lane == 0) mbar_arrive_expect_tx(bar, 2 * kTileBytes);
-        __syncwarp();
-        if (lane < kPagesPerTile) {
-          tma_load_2d(smem_u32(sm.k[st]) + lane * kPageSize * 128, &kmap, 0, row, bar, policy);
-          tma_load_2d(smem_u32(sm.v[st]) + lane * kPageSize * 128, &vmap, 0, row, bar, policy);
-        }
-        if (lane == 0) sm.issued_kv = j + 1;
-        row = next;
-      }
+        return true;
+      });
       if (!ok && lane == 0) raise_status(a.status, kStatusTimeout);
     } else if (warp == 1 || warp == 2) {
       // ------------------------------------------------------------ products
       const int t = warp - 1;
-      if (t < ntiles) {
-        const uint32_t tmem = tmem_base();
-        const uint32_t d_s = tmem + kColS + t * 128, d_o = tmem + kColO + t * 64, a_p = tmem + kColP + t * 64;
-        auto wait = [&](uint64_t& bar, int parity) {
-          return __all_sync(0xffffffffu, wait_bar(smem_u32(&bar), parity & 1, a.timeout_ns, abort_flag)) != 0;
-        };
-        bool ok = wait(sm.q_ready[t], 0);
-        const uint64_t qd = sw128_desc(smem_u32(sm.q[t]));
+      const uint32_t tmem = tmem_base();
+      const uint32_t d_s = tmem + kColS + t * 128, d_o = tmem + kColO + t * 64, a_p = tmem + kColP + t * 64;
+      const uint64_t qd = sw128_desc(smem_u32(sm.q[t]));
+      auto wait = [&](uint64_t& bar, int parity) {
+        return __all_sync(0xffffffffu, wait_bar(smem_u32(&bar), parity & 1, a.timeout_ns, abort_flag)) != 0;
+      };
+      bool ok = true;
+      int steps = 0, parts = 0;  // of this row tile
+      for_segments([&](int n_kv, int g) {
+        if (t * kBlockQ >= seg.rows) {  // no such row tile: the stages are as good as used
+          for (int j = 0; j < n_kv && ok; ++j) {
+            ok = wait(sm.kv_full[(g + j) % kStages], (g + j) / kStages);
+            if (ok && elect_one()) mbar_arrive(smem_u32(&sm.kv_empty[(g + j) % kStages]));
+            __syncwarp();
+          }
+          return ok;
+        }
+        ok = wait(sm.q_ready[t], parts);
         auto s_step = [&](int j) {  // S(j) = Q K_j^T
-          ok = wait(sm.kv_full[j % kStages], j / kStages);
+          ok = wait(sm.kv_full[(g + j) % kStages], (g + j) / kStages);
           if (!ok) return;
           tc_fence_after();
           if (elect_one()) {
-            const uint64_t kd = sw128_desc(smem_u32(sm.k[j % kStages]));
+            const uint64_t kd = sw128_desc(smem_u32(sm.k[(g + j) % kStages]));
 #pragma unroll
             for (int kk = 0; kk < kHeadDim / 16; ++kk) tc_mma_ss(d_s, qd + 2 * kk, kd + 2 * kk, kIdescS, kk > 0);
             tc_commit(smem_u32(&sm.s_full[t]));
           }
         };
         auto pv_step = [&](int j) {  // O += P(j) V_j
-          ok = wait(sm.p_full[t], j);
+          ok = wait(sm.p_full[t], steps + j);
           if (!ok) return;
           tc_fence_after();
           if (elect_one()) {
-            const uint64_t vd = sw128_desc(smem_u32(sm.v[j % kStages]));
+            const uint64_t vd = sw128_desc(smem_u32(sm.v[(g + j) % kStages]));
 #pragma unroll
             for (int kk = 0; kk < kBlockK / 16; ++kk)
               tc_mma_ts(d_o, a_p + kk * 8, vd + kk * (16 * 128 / 16), kIdescPV, (j > 0 || kk > 0) ? 1u : 0u);
             tc_commit(smem_u32(&sm.pv_done[t]));
-            tc_commit(smem_u32(&sm.kv_empty[j % kStages]));
+            tc_commit(smem_u32(&sm.kv_empty[(g + j) % kStages]));
           }
         };
         if (ok) s_step(0);
         for (int j = 0; j < n_kv && ok; ++j) {
           if (j >= 1) pv_step(j - 1);
           if (ok && j + 1 < n_kv) {
-            ok = wait(sm.s_free[t], j);
+            ok = wait(sm.s_free[t], steps + j);
             if (ok) s_step(j + 1);
           }
         }
         if (ok) pv_step(n_kv - 1);
-        if (elect_one()) {
-          if (!ok) raise_status(a.status, kStatusTimeout);
-          // whatever happened, every product issued here is done before TMEM is released
-          tc_commit(smem_u32(&sm.drain[t]));
-          mbar_wait(smem_u32(&sm.drain[t]), 0, kDrainTimeoutNs);
-        }
-        __syncwarp();
+        steps += n_kv;
+        ++parts;
+        return ok;
+      });
+      if (elect_one()) {
+        if (!ok) raise_status(a.status, kStatusTimeout);
+        // whatever happened, every product issued here is done before TMEM is released
+        tc_commit(smem_u32(&sm.drain[t]));
+        mbar_wait(smem_u32(&sm.drain[t]), 0, kDrainTimeoutNs);
       }
+      __syncwarp();
     }
   } else {
-    regs_inc<224>();
+    regs_inc<208>();
     // -------------------------------------------------------------- softmax
     const int t = (warp - 4) >> 2;  // row tile of this warpgroup
     const int qw = warp & 3;        // TMEM lane quarter
-    const int r = qw * 32 + lane;   // row within the tile
-    if (t < ntiles) {
-      const uint32_t lane_base = tmem_base() + (static_cast<uint32_t>(qw * 32) << 16);
-      const uint32_t s_col = lane_base + kColS + t * 128;
-      const uint32_t o_col = lane_base + kColO + t * 64;
-      const uint32_t p_col = lane_base + kColP + t * 64;
-      const bool live = t * kBlockQ + r < rows;
-      const bool warp_live = t * kBlockQ + qw * 32 < rows;
-      int seq, head;
-      row_index(live ? t * kBlockQ + r : 0, seq, head);
+    const int r = t * kBlockQ + qw * 32 + lane;  // row within the unit
+    const uint32_t lane_base = tmem_base() + (static_cast<uint32_t>(qw * 32) << 16);
+    const uint32_t s_col = lane_base + kColS + t * 128;
+    const uint32_t o_col = lane_base + kColO + t * 64;
+    const uint32_t p_col = lane_base + kColP + t * 64;
+    const uint64_t scale2 = f2(a.scale_log2, a.scale_log2);
+    // sequence and query head of a row of the present part
+    auto row_index = [&](int row, int& seq, int& head) {
+      const int gr = seg.row0 + row;
+      seq = seg.first_seq + gr / a.group;
+      head = seg.kvh * a.group + gr % a.group;
+    };
+    bool ok = true;
+    int steps = 0;  // of this row tile
+    for_segments([&](int n_kv, int) {
+      if (t * kBlockQ >= seg.rows) return true;  // no such row tile
+      // read again where it is used, rather than held in registers that the score row needs
+      const volatile Segment& vseg = seg;
+      auto live = [&]() { return r < vseg.rows; };
+      auto warp_live = [&]() { return (r & ~31) < vseg.rows; };
       {
+        // the tile's Q (every product that read the last part's is done: its scores have been waited for)
+        int seq, head;
+        row_index(live() ? r : 0, seq, head);
         const uint4* src = reinterpret_cast<const uint4*>(a.q + (static_cast<size_t>(seq) * a.hq + head) * kHeadDim);
         uint4 x[8];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) x[c] = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-        uint8_t* dst = sm.q[t] + r * 128;
+        for (int c = 0; c < 8; ++c) x[c] = live() ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+        uint8_t* dst = sm.q[t] + (r & 127) * 128;
 #pragma unroll
         for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(dst + ((c ^ (r & 7)) << 4)) = x[c];
         fence_proxy_async_smem();  // the rows are read by the tensor core (async proxy)
         mbar_arrive(smem_u32(&sm.q_ready[t]));
       }
-      const uint64_t scale2 = f2(a.scale_log2, a.scale_log2);
       float m = kNegInf, d = 0.0f;  // running maximum (log2 units) and sum
-      bool ok = true;
       for (int j = 0; j < n_kv; ++j) {
-        if (!wait_bar(smem_u32(&sm.s_full[t]), j & 1, a.timeout_ns, abort_flag)) {
-          ok = false;
-          break;
-        }
-        if (!warp_live) {  // rows that nothing reads: keep step with the others, phase by phase
+        if (!wait_bar(smem_u32(&sm.s_full[t]), (steps + j) & 1, a.timeout_ns, abort_flag)) return ok = false;
+        if (!warp_live()) {  // rows that nothing reads: keep step with the others, phase by phase
           mbar_arrive(smem_u32(&sm.s_free[t]));
-          if (j > 0 && !wait_bar(smem_u32(&sm.pv_done[t]), (j - 1) & 1, a.timeout_ns, abort_flag)) {
-            ok = false;
-            break;
-          }
+          if (j > 0 && !wait_bar(smem_u32(&sm.pv_done[t]), (steps + j - 1) & 1, a.timeout_ns, abort_flag)) return ok = false;
           mbar_arrive(smem_u32(&sm.p_full[t]));
           continue;
         }
@@ -393,8 +536,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         float s[128];
 #pragma unroll
         for (int c = 0; c < 128; ++c) s[c] = __uint_as_float(sr[c]);
-        const int left = n_keys - (tile0 + j) * kBlockK;  // keys from this tile's first on
         float mraw = fmax3(pm0, pm1, fmaxf(pm2, pm3));
+        // keys from this tile's first on
+        const int left = vseg.n_pages * kPageSize - (vseg.tile0 + j) * kBlockK;
         if (left < kBlockK) {  // the prompt ends inside this tile: its missing pages read as zeros
           mraw = kNegInf;
 #pragma unroll
@@ -432,10 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         f2_split(f2_add(f2_add(acc0, acc1), f2_add(acc2, acc3)), r0, r1);
         d += r0 + r1;
         // P and O are in use by the previous product until it is done
-        if (j > 0 && !wait_bar(smem_u32(&sm.pv_done[t]), (j - 1) & 1, a.timeout_ns, abort_flag)) {
-          ok = false;
-          break;
-        }
+        if (j > 0 && !wait_bar(smem_u32(&sm.pv_done[t]), (steps + j - 1) & 1, a.timeout_ns, abort_flag)) return ok = false;
         tc_fence_after();
         if (j > 0 && __any_sync(0xffffffffu, grow)) {
           const uint64_t f22 = f2(factor, factor);
@@ -467,16 +608,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         mbar_arrive(smem_u32(&sm.p_full[t]));
       }
-      if (ok) ok = wait_bar(smem_u32(&sm.pv_done[t]), (n_kv - 1) & 1, a.timeout_ns, abort_flag);
-      if (ok && warp_live) {
+      steps += n_kv;
+      if (!wait_bar(smem_u32(&sm.pv_done[t]), (steps - 1) & 1, a.timeout_ns, abort_flag)) return ok = false;
+      if (warp_live()) {
         tc_fence_after();
         uint32_t ou[2][32];
         tmem_ld32(o_col, ou[0]);
         tmem_ld32(o_col + 32, ou[1]);
         tc_wait_ld();
-        if (live) {
+        tc_fence_before();  // the next part's products may overwrite O once this thread has handed over its P
+        if (live()) {
           const float inv = d > 0.0f ? 1.0f / d : 0.0f;
-          const size_t out = (static_cast<size_t>(seq) * slots + split) * a.hq + head;
+          int seq, head;
+          row_index(r, seq, head);
+          const size_t out = (static_cast<size_t>(seq) * slot_rows + seg.slot) * a.hq + head;
           float4* o = reinterpret_cast<float4*>(a.partial_o + out * kHeadDim);
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
@@ -485,10 +630,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                                __uint_as_float(u[3]) * inv);
           }
           a.partial_lse[out] = d > 0.0f ? (m + lg2(d)) * kLn2 : kNegInf;
+          for (int e = 1; e <= seg.empty; ++e) a.partial_lse[out + static_cast<size_t>(e) * a.hq] = kNegInf;
         }
       }
-      if (!ok && lane == 0) raise_status(a.status, kStatusTimeout);
-    }
+      return true;
+    });
+    if (!ok && lane == 0) raise_status(a.status, kStatusTimeout);
   }
 
   tc_fence_before();
@@ -504,12 +651,92 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem_base(), kTmemCols);
 }
 
+// Adds a row's slots up: lse = ln sum e^lse_s, out = sum e^(lse_s - lse) o_s.  Sixteen lanes per row,
+// four dimensions each; a slot without weight (lse = -inf) is not read.
+constexpr int kMergeThreads = 256;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kPosInf = __builtin_huge_valf();
+
+__global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const MergeArgs a) {
+  // the partial results come from the two kernels before, whose last CTA has waited for both
+  pdl_launch_dependents();
+  pdl_wait_primary();
+  const int lane = threadIdx.x & 15;
+  const long long row = static_cast<long long>(blockIdx.x) * (kMergeThreads / 16) + (threadIdx.x >> 4);
+  if (row >= static_cast<long long>(a.batch) * a.heads) return;
+  const long long b = row / a.heads, h = row % a.heads;
+  const int S = a.num_splits;
+  const float* lse = a.partial_lse + b * S * a.heads + h;
+  const float4* o = reinterpret_cast<const float4*>(a.partial_o + (b * S * a.heads + h) * kHeadDim) + lane;
+  const unsigned half = 0xffffu << (threadIdx.x & 16);
+  float most = kNegInf;
+  for (int s = lane; s < S; s += 16) most = fmaxf(most, lse[static_cast<long long>(s) * a.heads]);
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(half, most, off));
+  float z = 0.0f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < S; s0 += 16) {
+    // this lane's slot's weight: the largest term exactly 1, -inf exactly 0
+    float w = 0.0f;
+    if (s0 + lane < S) {
+      const float l = lse[static_cast<long long>(s0 + lane) * a.heads];
+      w = l == kNegInf ? 0.0f : l == most ? 1.0f : most == kPosInf ? 0.0f : ex2((l - most) * kLog2e);
+    }
+    const int n = min(16, S - s0);
+    for (int i0 = 0; i0 < n; i0 += 8) {  // eight loads on their way at a time
+      float wi[8];
+      float4 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        wi[i] = __shfl_sync(half, w, (threadIdx.x & 16) + i0 + i);  // (0 behind the last slot)
+        v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (wi[i] != 0.0f) v[i] = o[static_cast<long long>(s0 + i0 + i) * a.heads * (kHeadDim / 4)];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        z += wi[i];
+        acc.x = fmaf(wi[i], v[i].x, acc.x);
+        acc.y = fmaf(wi[i], v[i].y, acc.y);
+        acc.z = fmaf(wi[i], v[i].z, acc.z);
+        acc.w = fmaf(wi[i], v[i].w, acc.w);
+      }
+    }
+  }
+  const float inv = z > 0.0f ? 1.0f / z : 0.0f;
+  uint2 pk;
+  pk.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+  pk.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * kHeadDim + 4 * lane) = pk;
+  if (a.lse && lane == 0) a.lse[row] = most == kPosInf ? kPosInf : z > 0.0f ? most + lg2(z) * kLn2 : kNegInf;
+}
+
 }  // namespace
 
 long long shared_row_tiles(int batch, int num_groups, int group) {
   const long long rows = static_cast<long long>(batch) * group, block = 2 * kBlockQ;
   const long long groups = num_groups < batch ? num_groups : batch;  // the ones that can have rows
   return (rows + groups * (block - 1)) / block;
+}
+
+int shared_ctas(int batch, int num_groups, int group, int hkv, int max_shared_pages, int max_pages, int sms) {
+  // Work of the shared part, if every group's prompt is the longest: 1.4 us an SM for a tile of keys
+  // of two row tiles.  Bytes of the own parts, if they are half of what the page table has room
+  // for: 6.6 GB/ms of all SMs, 0.1 of one.  x SMs for the shared part: it ends at work / x, and what
+  // the own parts have left then has all SMs.
+  const double work = 1.4 * shared_row_tiles(batch, num_groups, group) * hkv * ((max_shared_pages + kPagesPerTile - 1) / kPagesPerTile);
+  const double own = 0.5 * (max_pages - max_shared_pages) * kPageSize * 256.0 * hkv * batch / 6.6e6;  // us of all SMs
+  int best = sms;
+  double least = 1e30;
+  for (int x = sms; x >= 8; x -= 4) {
+    const double end = work / x, rate = (sms - x) * 0.1 / 6.6;
+    const double left = own - (rate < 1.0 ? rate : 1.0) * end;
+    const double t = end + (left > 0.0 ? left : 0.0);
+    if (t < 0.999 * least) {
+      least = t;
+      best = x;
+    }
+  }
+  return best < sms ? best : sms;
 }
 
 cudaError_t launch_shared(const CUtensorMap& kmap, const CUtensorMap& vmap, const SharedArgs& a, cudaStream_t stream) {
@@ -526,7 +753,7 @@ cudaError_t launch_shared(const CUtensorMap& kmap, const CUtensorMap& vmap, cons
     if (dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.plan.shared_splits, a.hkv, static_cast<unsigned>(shared_row_tiles(a.batch, a.plan.num_groups, a.group)));
+  cfg.gridDim = dim3(a.ctas, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -536,6 +763,22 @@ cudaError_t launch_shared(const CUtensorMap& kmap, const CUtensorMap& vmap, cons
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, shared_prefix_kernel, kmap, vmap, a);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+cudaError_t launch_shared_merge(const MergeArgs& a, cudaStream_t stream) {
+  const long long rows = static_cast<long long>(a.batch) * a.heads;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + kMergeThreads / 16 - 1) / (kMergeThreads / 16)), 1, 1);
+  cfg.blockDim = dim3(kMergeThreads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, shared_merge_kernel, a);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

@@ -26,19 +26,26 @@ struct SharedArgs {
   float* partial_lse;            // [B, shared_splits + own_splits, Hq]
   SharedPlan plan;
   int batch, hq, hkv, group, max_pages, num_pages;
+  int ctas;                      // of the shared part's grid
   float scale_log2;              // sm_scale * log2(e)
   unsigned* status;
   unsigned long long timeout_ns;
 };
 
-// CTAs along the rows of the shared part: at least the row tiles of any division of the batch
-// into num_groups groups.
+// Pairs of row tiles of the batch per KV head: at most, however it is divided into num_groups groups.
 long long shared_row_tiles(int batch, int num_groups, int group);
-// Attention of every group's rows over its shared pages, into slots [0, shared_splits).
+// CTAs for the shared part, so that it and the own parts (which get the other SMs) end together as
+// far as the bounds on their lengths tell.
+int shared_ctas(int batch, int num_groups, int group, int hkv, int max_shared_pages, int max_pages, int sms);
+// Attention of every group's rows over its shared pages, into slots [0, shared_splits) (slots not
+// used: lse = -inf, the output not written; nothing for groups that share no pages).
 cudaError_t launch_shared(const CUtensorMap& kmap, const CUtensorMap& vmap, const SharedArgs& a, cudaStream_t stream);
 // Every sequence's own pages and its sink, into the slots behind; launched after launch_shared
-// (decode.cu).  a.num_splits = plan.own_splits, a.out and a.lse are the partial results.
+// (decode.cu).  Where a sequence shares nothing, its shared slots get lse = -inf.  a.num_splits = plan.own_splits, a.out and a.lse are the partial results.
 cudaError_t launch_decode_own(const CUtensorMap& kmap, const CUtensorMap& vmap, const DecodeArgs& a,
                               const SharedPlan& plan, cudaStream_t stream);
+
+// Adds the slots up; launched after launch_decode_own.
+cudaError_t launch_shared_merge(const MergeArgs& a, cudaStream_t stream);
 
 }  // namespace sa

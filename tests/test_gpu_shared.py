@@ -105,6 +105,9 @@ CASES = {
                             [1 + (i * 17) % 70 for i in range(65)], 64, 8, None),
     "long prompt": ([(9, 700)], [1 + i for i in range(9)], 64, 8, None),
     "long own parts": ([(3, 20)], [4000, 1, 2500], 64, 8, None),
+    "one slot, more units than SMs": ([(40, 9), (300, 3), (1, 33), (30, 1)], [1 + i % 19 for i in range(371)], 64, 8, (1, 1)),
+    "two slots, uneven groups": ([(40, 90), (3, 300), (60, 7)], [1 + i % 35 for i in range(103)], 64, 8, (2, 1)),
+    "long own parts, few SMs for the shared": ([(60, 130)], [900 + i for i in range(60)], 64, 8, None),
     "most slots": ([(2, 300)], [2000, 10], 16, 8, (200, 56)),
 }
 
