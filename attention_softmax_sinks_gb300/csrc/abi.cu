@@ -439,20 +439,25 @@ void sink_attn_decode_shared_splits(int batch, int num_groups, int num_qo_heads,
   if (batch > 0 && num_groups > 0 && num_kv_heads > 0 && num_qo_heads >= num_kv_heads && max_shared_pages >= 0 &&
       max_pages > 0) {
     if (num_sms <= 0) num_sms = 152;
-    // shared part: its CTAs' equal runs cut a unit of work into as many parts as it has CTAs, and one
-    // more; more than 24 cost more to merge than they gain
-    const int group = num_qo_heads / num_kv_heads;
-    const long long tiles = (max_shared_pages + 7) / 8;
-    const long long units = sa::shared_row_tiles(batch, 1, group) * num_kv_heads;
-    const long long ctas = sa::shared_ctas(batch, num_groups, group, num_kv_heads, max_shared_pages, max_pages, num_sms);
-    long long n = (ctas + units - 1) / units + 1;
-    if (n > tiles + 1) n = tiles + 1;
-    if (n > 24) n = 24;
-    s = n < 2 ? 2 : static_cast<int>(n);
     // own part: three CTAs per SM, at least 16 pages each, at most 8 splits
     const long long own_pages = max_pages > max_shared_pages ? max_pages - max_shared_pages : 1;
     const long long own_units = static_cast<long long>(batch) * num_kv_heads;
     while (o < 8 && own_units * o < 3LL * num_sms && own_pages / (2 * o) >= 16) o *= 2;
+    // shared part: its CTAs' equal runs cut a unit of work into twice as many parts as it has CTAs
+    // (units are of uneven length), and two more, of two slots where units have one row tile; at
+    // most 40, and 96 MB
+    const int group = num_qo_heads / num_kv_heads;
+    const long long tiles = (max_shared_pages + 7) / 8;
+    const long long units = sa::shared_row_tiles(batch, num_groups, group) * num_kv_heads;
+    const long long ctas = sa::shared_ctas(batch, num_groups, group, num_kv_heads, max_shared_pages, max_pages,
+                                           static_cast<int>(own_units * o < (1 << 30) ? own_units * o : 1 << 30), num_sms);
+    long long n = 2 * ctas / units + 2;
+    if (n > tiles + 1) n = tiles + 1;
+    if (static_cast<long long>(batch) * group <= 128LL * num_groups) n = 2 * (n < tiles / 2 + 1 ? n : tiles / 2 + 1);
+    const long long room = (96LL << 20) / (static_cast<long long>(batch) * num_qo_heads * 260);
+    if (n > room) n = room;
+    if (n > 40) n = 40;
+    s = n < 2 ? 2 : static_cast<int>(n);
   }
   if (shared_splits) *shared_splits = s;
   if (own_splits) *own_splits = o;
@@ -613,7 +618,8 @@ sa_status sink_attn_decode_shared(const void* q, const void* paged_k, const void
   a.group = group;
   a.max_pages = max_pages;
   a.num_pages = num_pages;
-  a.ctas = sa::shared_ctas(batch, num_groups, group, num_kv_heads, max_shared_pages, max_pages, sm_count());
+  a.ctas = sa::shared_ctas(batch, num_groups, group, num_kv_heads, max_shared_pages, max_pages,
+                           batch * num_kv_heads * own_splits, sm_count());
   a.scale_log2 = sm_scale * kLog2e;
   a.status = status;
   a.timeout_ns = g_timeout_ns;

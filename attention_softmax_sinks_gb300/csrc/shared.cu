@@ -29,6 +29,8 @@
 //                 (relative error 2^-8 at most per weight, as in the other attention kernels; the
 //                 sum takes the weights before that rounding); warps without rows only keep step
 // O is rescaled only when the maximum grows by more than 2^8 (O / d does not change).
+// A unit of no more than 128 rows has one row tile, whose steps (product, softmax, product) would
+// follow one another: there the two sets of warps take its tiles of keys in turn, as two slots.
 // Slots that a unit does not use get lse = -inf and are not read by the merge; those of sequences
 // that share nothing are marked by the own parts' kernel.
 #include <atomic>
@@ -67,8 +69,9 @@ struct Walk {
 // KV head kvh, tiles of keys [tile0, tile0 + n_kv) of its n_pages pages.
 struct Segment {
   int first_seq, row0, rows, n_pages, kvh, tile0, n_kv;
-  int slot;   // where the results go
-  int empty;  // slots behind it that stay empty (the unit's last part)
+  int slot;   // where the results go (in turn: 2 slot and 2 slot + 1)
+  int turns;  // one row tile, whose tiles of keys both sets of warps take in turn
+  int last;   // the unit's last part: slots behind it stay empty
 };
 
 struct __align__(1024) SharedSmem {
@@ -83,16 +86,18 @@ struct __align__(1024) SharedSmem {
   uint64_t p_full[2];          // P is written and O rescaled                 (128 arrivals)
   uint64_t pv_done[2];         // O += P V is done                            (tcgen05.commit)
   uint64_t drain[2];
+  uint64_t stagger;            // row tile 0 has handed over a part's first P  (1 arrival)
   uint32_t tmem_base;
   int abort_flag;
   int issued_kv;
   int total;                   // tiles of keys of all units
-  int most;                    // of one unit
+  int most[2];                 // of one unit: of one row tile in two slots, others
   int quantum;                 // of one run
   int runs;
+  int turns;                   // units of one row tile have two slots per part
   int each;                    // 0, or a unit's length in runs of one unit each
   int warp_sum[kThreads / 32];
-  int warp_most[kThreads / 32];
+  int warp_most[2][kThreads / 32];
   int chunk[kMaxChunks];       // work before each kThreads groups
   Walk walk[kThreads / 32];    // of each warp
   Segment seg[kThreads / 32];
@@ -165,39 +170,42 @@ __device__ __forceinline__ int group_work(const SharedArgs& a, int count, int pa
 // Sums up the groups' work, kThreads groups at a time: sm.total, sm.most, sm.chunk.  All threads.
 __device__ __forceinline__ void sum_work(const SharedArgs& a, SharedSmem& sm, int each, bool report) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int before = 0;
-  int most = 0;
+  int before = 0, most[2] = {0, 0};
   for (int g0 = 0; g0 < a.plan.num_groups; g0 += kThreads) {
     const int g = g0 + static_cast<int>(threadIdx.x);
-    int n = 0;
-    int tiles = 0;
+    int n = 0, tiles[2] = {0, 0};
     if (g < a.plan.num_groups) {
-      int first, count, pages;
+      int first, count, pages, len;
       if (!group_bounds(a, g, first, count, pages) && report) raise_status(a.status, kStatusBadLen);
-      int len;
       n = group_work(a, count, pages, each, len);
-      tiles = len;
+      const int rows = count * a.group;  // its last unit has one row tile, or two; the others two
+      if ((rows - 1) % (2 * kBlockQ) < kBlockQ) tiles[0] = len;
+      if (rows > kBlockQ) tiles[1] = len;
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
       n += __shfl_xor_sync(0xffffffffu, n, off);
-      tiles = max(tiles, __shfl_xor_sync(0xffffffffu, tiles, off));
+      tiles[0] = max(tiles[0], __shfl_xor_sync(0xffffffffu, tiles[0], off));
+      tiles[1] = max(tiles[1], __shfl_xor_sync(0xffffffffu, tiles[1], off));
     }
     __syncthreads();  // the last round's sums have been read
     if (lane == 0) {
       sm.warp_sum[warp] = n;
-      sm.warp_most[warp] = tiles;
+      sm.warp_most[0][warp] = tiles[0];
+      sm.warp_most[1][warp] = tiles[1];
     }
     __syncthreads();
     if (threadIdx.x == 0) sm.chunk[g0 / kThreads] = before;
     for (int w = 0; w < kThreads / 32; ++w) {
       before += sm.warp_sum[w];
-      most = max(most, sm.warp_most[w]);
+      most[0] = max(most[0], sm.warp_most[0][w]);
+      most[1] = max(most[1], sm.warp_most[1][w]);
     }
   }
   if (threadIdx.x == 0) {
     sm.total = before;
-    sm.most = most;
+    sm.most[0] = most[0];
+    sm.most[1] = most[1];
   }
   __syncthreads();
 }
@@ -240,7 +248,7 @@ __device__ __forceinline__ void seek(const SharedArgs& a, SharedSmem& sm, Walk& 
 }
 
 // The walk's next part of a unit, if any.  The whole warp.
-__device__ __forceinline__ bool next_segment(const SharedArgs& a, Walk& walk, Segment& seg, int quantum, int each) {
+__device__ __forceinline__ bool next_segment(const SharedArgs& a, Walk& walk, Segment& seg, int quantum, int each, bool turns) {
   Walk w = walk;
   Segment s{};
   bool found = false;
@@ -264,7 +272,8 @@ __device__ __forceinline__ bool next_segment(const SharedArgs& a, Walk& walk, Se
     s.tile0 = off;
     s.n_kv = min(n, key_tiles(w.pages) - off);  // (a unit shorter than `each` leaves the rest idle)
     s.slot = w.at / quantum - unit_start / quantum;
-    s.empty = off + n == len ? a.plan.shared_splits - 1 - s.slot : 0;
+    s.turns = turns && s.rows <= kBlockQ;
+    s.last = off + n == len;
     w.at += n;
     w.in_group += n;
     found = s.n_kv > 0;
@@ -300,11 +309,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   // slot: a run per unit, all as long as the longest.
   const int slots = a.plan.shared_splits;
   sum_work(a, sm, 0, blockIdx.x == 0);
-  const int most = sm.most, each = slots == 1 ? most : 0;
+  const int each = slots == 1 ? max(sm.most[0], sm.most[1]) : 0;
   if (each) sum_work(a, sm, each, false);
   const int total = sm.total, grid = gridDim.x;
   int quantum = each ? each : total / grid + (total % grid != 0);
-  if (!each && quantum < (most + slots - 2) / (slots - 1)) quantum = (most + slots - 2) / (slots - 1);
+  bool turns = false;
+  if (!each) {  // (parts in turn have two slots each)
+    quantum = max(quantum, (max(sm.most[0], sm.most[1]) + slots - 2) / (slots - 1));
+    // tiles of keys in turn, where the slots are enough for parts not much longer than that (at
+    // least of a tile for each set of warps)
+    const int parts = slots / 2 - 1, in_turn = parts > 0 ? max((sm.most[0] + parts - 1) / parts, 2) : 0;
+    turns = in_turn > 0 && in_turn <= 2 * quantum;
+    if (turns && sm.most[0] > 0) quantum = max(quantum, in_turn);
+  }
   if (quantum < 1) quantum = 1;
   // this CTA's runs: blockIdx.x, + gridDim.x, ..
   const int runs = total / quantum + (total % quantum != 0);
@@ -312,6 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     sm.quantum = quantum;
     sm.runs = runs;
+    sm.turns = turns;
     sm.each = each;
   }
 
@@ -325,6 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&sm.pv_done[t]), 1);
       mbar_init(smem_u32(&sm.drain[t]), 1);
     }
+    mbar_init(smem_u32(&sm.stagger), 1);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_u32(&sm.kv_full[s]), 1);
       mbar_init(smem_u32(&sm.kv_empty[s]), 2);
@@ -354,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int g = 0;
     while (vs.walk[warp].run < vs.runs) {
       seek(a, sm, sm.walk[warp], vs.walk[warp].run * vs.quantum, vs.quantum, vs.each);
-      while (next_segment(a, sm.walk[warp], seg, vs.quantum, vs.each)) {
+      while (next_segment(a, sm.walk[warp], seg, vs.quantum, vs.each, vs.turns != 0)) {
         const int n = seg.n_kv;
         if (!body(n, g)) return;
         g += n;
@@ -419,9 +438,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         return __all_sync(0xffffffffu, wait_bar(smem_u32(&bar), parity & 1, a.timeout_ns, abort_flag)) != 0;
       };
       bool ok = true;
-      int steps = 0, parts = 0;  // of this row tile
+      int steps = 0, parts = 0, all_parts = 0;  // of this set of warps; of the CTA
       for_segments([&](int n_kv, int g) {
-        if (t * kBlockQ >= seg.rows) {  // no such row tile: the stages are as good as used
+        const int part = all_parts++;
+        const bool turns = seg.turns;
+        if (!turns && t * kBlockQ >= seg.rows) {  // no such row tile: the stages are as good as used
           for (int j = 0; j < n_kv && ok; ++j) {
             ok = wait(sm.kv_full[(g + j) % kStages], (g + j) / kStages);
             if (ok && elect_one()) mbar_arrive(smem_u32(&sm.kv_empty[(g + j) % kStages]));
@@ -429,41 +450,51 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           return ok;
         }
+        // step i works on tile of keys `first + i * stride` of the part
+        const int stride = turns ? 2 : 1, first = turns ? t : 0, n = turns ? (n_kv - t + 1) / 2 : n_kv;
+        if (n == 0) return true;
         ok = wait(sm.q_ready[t], parts);
-        auto s_step = [&](int j) {  // S(j) = Q K_j^T
-          ok = wait(sm.kv_full[(g + j) % kStages], (g + j) / kStages);
+        // Row tile 1 begins a softmax phase behind row tile 0, so that one set of warps computes
+        // while the other loads and stores.  (Parts longer than the ring only: tile 0 cannot be
+        // through with this part, and `stagger` cannot be two phases on, before tile 1 has begun.)
+        if (ok && t == 1 && !turns && n_kv > kStages) ok = wait(sm.stagger, part);
+        auto s_step = [&](int i) {  // S = Q K^T
+          const int j = g + first + i * stride;
+          ok = wait(sm.kv_full[j % kStages], j / kStages);
           if (!ok) return;
           tc_fence_after();
           if (elect_one()) {
-            const uint64_t kd = sw128_desc(smem_u32(sm.k[(g + j) % kStages]));
+            const uint64_t kd = sw128_desc(smem_u32(sm.k[j % kStages]));
 #pragma unroll
             for (int kk = 0; kk < kHeadDim / 16; ++kk) tc_mma_ss(d_s, qd + 2 * kk, kd + 2 * kk, kIdescS, kk > 0);
             tc_commit(smem_u32(&sm.s_full[t]));
           }
         };
-        auto pv_step = [&](int j) {  // O += P(j) V_j
-          ok = wait(sm.p_full[t], steps + j);
+        auto pv_step = [&](int i) {  // O += P V
+          const int j = g + first + i * stride;
+          ok = wait(sm.p_full[t], steps + i);
           if (!ok) return;
           tc_fence_after();
           if (elect_one()) {
-            const uint64_t vd = sw128_desc(smem_u32(sm.v[(g + j) % kStages]));
+            const uint64_t vd = sw128_desc(smem_u32(sm.v[j % kStages]));
 #pragma unroll
             for (int kk = 0; kk < kBlockK / 16; ++kk)
-              tc_mma_ts(d_o, a_p + kk * 8, vd + kk * (16 * 128 / 16), kIdescPV, (j > 0 || kk > 0) ? 1u : 0u);
+              tc_mma_ts(d_o, a_p + kk * 8, vd + kk * (16 * 128 / 16), kIdescPV, (i > 0 || kk > 0) ? 1u : 0u);
             tc_commit(smem_u32(&sm.pv_done[t]));
-            tc_commit(smem_u32(&sm.kv_empty[(g + j) % kStages]));
+            tc_commit(smem_u32(&sm.kv_empty[j % kStages]));
+            if (turns) mbar_arrive(smem_u32(&sm.kv_empty[j % kStages]));  // for the other set of warps
           }
         };
         if (ok) s_step(0);
-        for (int j = 0; j < n_kv && ok; ++j) {
-          if (j >= 1) pv_step(j - 1);
-          if (ok && j + 1 < n_kv) {
-            ok = wait(sm.s_free[t], steps + j);
-            if (ok) s_step(j + 1);
+        for (int i = 0; i < n && ok; ++i) {
+          if (i >= 1) pv_step(i - 1);
+          if (ok && i + 1 < n) {
+            ok = wait(sm.s_free[t], steps + i);
+            if (ok) s_step(i + 1);
           }
         }
-        if (ok) pv_step(n_kv - 1);
-        steps += n_kv;
+        if (ok) pv_step(n - 1);
+        steps += n;
         ++parts;
         return ok;
       });
@@ -480,7 +511,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // -------------------------------------------------------------- softmax
     const int t = (warp - 4) >> 2;  // row tile of this warpgroup
     const int qw = warp & 3;        // TMEM lane quarter
-    const int r = t * kBlockQ + qw * 32 + lane;  // row within the unit
     const uint32_t lane_base = tmem_base() + (static_cast<uint32_t>(qw * 32) << 16);
     const uint32_t s_col = lane_base + kColS + t * 128;
     const uint32_t o_col = lane_base + kColO + t * 64;
@@ -495,12 +525,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int steps = 0;  // of this row tile
     for_segments([&](int n_kv, int) {
-      if (t * kBlockQ >= seg.rows) return true;  // no such row tile
+      if (!seg.turns && t * kBlockQ >= seg.rows) return true;  // no such row tile
+      const int r = (seg.turns ? 0 : t * kBlockQ) + qw * 32 + lane;  // row within the unit
+      const int n = seg.turns ? (n_kv - t + 1) / 2 : n_kv;
       // read again where it is used, rather than held in registers that the score row needs
       const volatile Segment& vseg = seg;
       auto live = [&]() { return r < vseg.rows; };
       auto warp_live = [&]() { return (r & ~31) < vseg.rows; };
-      {
+      if (n > 0) {
         // the tile's Q (every product that read the last part's is done: its scores have been waited for)
         int seq, head;
         row_index(live() ? r : 0, seq, head);
@@ -515,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(smem_u32(&sm.q_ready[t]));
       }
       float m = kNegInf, d = 0.0f;  // running maximum (log2 units) and sum
-      for (int j = 0; j < n_kv; ++j) {
+      for (int j = 0; j < n; ++j) {
         if (!wait_bar(smem_u32(&sm.s_full[t]), (steps + j) & 1, a.timeout_ns, abort_flag)) return ok = false;
         if (!warp_live()) {  // rows that nothing reads: keep step with the others, phase by phase
           mbar_arrive(smem_u32(&sm.s_free[t]));
@@ -538,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 128; ++c) s[c] = __uint_as_float(sr[c]);
         float mraw = fmax3(pm0, pm1, fmaxf(pm2, pm3));
         // keys from this tile's first on
-        const int left = vseg.n_pages * kPageSize - (vseg.tile0 + j) * kBlockK;
+        const int left = vseg.n_pages * kPageSize - (vseg.tile0 + (vseg.turns ? 2 * j + t : j)) * kBlockK;
         if (left < kBlockK) {  // the prompt ends inside this tile: its missing pages read as zeros
           mraw = kNegInf;
 #pragma unroll
@@ -607,9 +639,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_wait_st();
         tc_fence_before();
         mbar_arrive(smem_u32(&sm.p_full[t]));
+        if (j == 0 && warp == 4 && lane == 0) mbar_arrive(smem_u32(&sm.stagger));
       }
-      steps += n_kv;
-      if (!wait_bar(smem_u32(&sm.pv_done[t]), (steps - 1) & 1, a.timeout_ns, abort_flag)) return ok = false;
+      steps += n;
+      if (n > 0 && !wait_bar(smem_u32(&sm.pv_done[t]), (steps - 1) & 1, a.timeout_ns, abort_flag)) return ok = false;
       if (warp_live()) {
         tc_fence_after();
         uint32_t ou[2][32];
@@ -621,16 +654,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float inv = d > 0.0f ? 1.0f / d : 0.0f;
           int seq, head;
           row_index(r, seq, head);
-          const size_t out = (static_cast<size_t>(seq) * slot_rows + seg.slot) * a.hq + head;
-          float4* o = reinterpret_cast<float4*>(a.partial_o + out * kHeadDim);
+          const int slot = seg.turns ? 2 * seg.slot + t : seg.slot;
+          const size_t out = (static_cast<size_t>(seq) * slot_rows + slot) * a.hq + head;
+          if (n > 0) {
+            float4* o = reinterpret_cast<float4*>(a.partial_o + out * kHeadDim);
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const uint32_t* u = ou[c >> 3] + 4 * (c & 7);
-            o[c] = make_float4(__uint_as_float(u[0]) * inv, __uint_as_float(u[1]) * inv, __uint_as_float(u[2]) * inv,
-                               __uint_as_float(u[3]) * inv);
+            for (int c = 0; c < 16; ++c) {
+              const uint32_t* u = ou[c >> 3] + 4 * (c & 7);
+              o[c] = make_float4(__uint_as_float(u[0]) * inv, __uint_as_float(u[1]) * inv, __uint_as_float(u[2]) * inv,
+                                 __uint_as_float(u[3]) * inv);
+            }
           }
           a.partial_lse[out] = d > 0.0f ? (m + lg2(d)) * kLn2 : kNegInf;
-          for (int e = 1; e <= seg.empty; ++e) a.partial_lse[out + static_cast<size_t>(e) * a.hq] = kNegInf;
+          if (seg.last && (t == 0 || !seg.turns)) {  // slots that nothing goes into
+            float* lse = a.partial_lse + static_cast<size_t>(seq) * slot_rows * a.hq + head;
+            for (int e = seg.turns ? 2 * seg.slot + 2 : seg.slot + 1; e < a.plan.shared_splits; ++e) lse[static_cast<size_t>(e) * a.hq] = kNegInf;
+          }
         }
       }
       return true;
@@ -669,36 +708,36 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Merge
   const float* lse = a.partial_lse + b * S * a.heads + h;
   const float4* o = reinterpret_cast<const float4*>(a.partial_o + (b * S * a.heads + h) * kHeadDim) + lane;
   const unsigned half = 0xffffu << (threadIdx.x & 16);
-  float most = kNegInf;
-  for (int s = lane; s < S; s += 16) most = fmaxf(most, lse[static_cast<long long>(s) * a.heads]);
+  // Sixteen slots' values are asked for before any weight is known, so that a row of up to sixteen
+  // costs one way to L2 (a slot that was not written holds anything: it is not multiplied).
+  float4 v[16];
+  auto ask = [&](int s0) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (s0 + i < S) v[i] = o[static_cast<long long>(s0 + i) * a.heads * (kHeadDim / 4)];
+  };
+  const float first = lane < S ? lse[static_cast<long long>(lane) * a.heads] : kNegInf;
+  ask(0);
+  float most = first;
+  for (int s = lane + 16; s < S; s += 16) most = fmaxf(most, lse[static_cast<long long>(s) * a.heads]);
 #pragma unroll
   for (int off = 8; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(half, most, off));
   float z = 0.0f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int s0 = 0; s0 < S; s0 += 16) {
     // this lane's slot's weight: the largest term exactly 1, -inf exactly 0
-    float w = 0.0f;
-    if (s0 + lane < S) {
-      const float l = lse[static_cast<long long>(s0 + lane) * a.heads];
-      w = l == kNegInf ? 0.0f : l == most ? 1.0f : most == kPosInf ? 0.0f : ex2((l - most) * kLog2e);
-    }
-    const int n = min(16, S - s0);
-    for (int i0 = 0; i0 < n; i0 += 8) {  // eight loads on their way at a time
-      float wi[8];
-      float4 v[8];
+    const float l = s0 == 0 ? first : s0 + lane < S ? lse[static_cast<long long>(s0 + lane) * a.heads] : kNegInf;
+    const float w = l == kNegInf ? 0.0f : l == most ? 1.0f : most == kPosInf ? 0.0f : ex2((l - most) * kLog2e);
+    if (s0 > 0) ask(s0);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        wi[i] = __shfl_sync(half, w, (threadIdx.x & 16) + i0 + i);  // (0 behind the last slot)
-        v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (wi[i] != 0.0f) v[i] = o[static_cast<long long>(s0 + i0 + i) * a.heads * (kHeadDim / 4)];
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        z += wi[i];
-        acc.x = fmaf(wi[i], v[i].x, acc.x);
-        acc.y = fmaf(wi[i], v[i].y, acc.y);
-        acc.z = fmaf(wi[i], v[i].z, acc.z);
-        acc.w = fmaf(wi[i], v[i].w, acc.w);
+    for (int i = 0; i < 16; ++i) {
+      const float wi = __shfl_sync(half, w, (threadIdx.x & 16) + i);  // (0 behind the last slot)
+      if (wi != 0.0f) {
+        z += wi;
+        acc.x = fmaf(wi, v[i].x, acc.x);
+        acc.y = fmaf(wi, v[i].y, acc.y);
+        acc.z = fmaf(wi, v[i].z, acc.z);
+        acc.w = fmaf(wi, v[i].w, acc.w);
       }
     }
   }
@@ -712,31 +751,37 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Merge
 
 }  // namespace
 
+static int key_tiles_of(int pages) { return (pages + kPagesPerTile - 1) / kPagesPerTile; }
+
 long long shared_row_tiles(int batch, int num_groups, int group) {
   const long long rows = static_cast<long long>(batch) * group, block = 2 * kBlockQ;
   const long long groups = num_groups < batch ? num_groups : batch;  // the ones that can have rows
   return (rows + groups * (block - 1)) / block;
 }
 
-int shared_ctas(int batch, int num_groups, int group, int hkv, int max_shared_pages, int max_pages, int sms) {
-  // Work of the shared part, if every group's prompt is the longest: 1.4 us an SM for a tile of keys
-  // of two row tiles.  Bytes of the own parts, if they are half of what the page table has room
-  // for: 6.6 GB/ms of all SMs, 0.1 of one.  x SMs for the shared part: it ends at work / x, and what
-  // the own parts have left then has all SMs.
-  const double work = 1.4 * shared_row_tiles(batch, num_groups, group) * hkv * ((max_shared_pages + kPagesPerTile - 1) / kPagesPerTile);
-  const double own = 0.5 * (max_pages - max_shared_pages) * kPageSize * 256.0 * hkv * batch / 6.6e6;  // us of all SMs
+int shared_ctas(int batch, int num_groups, int group, int hkv, int max_shared_pages, int max_pages, int own_ctas, int sms) {
+  // SM time (us) of the shared part, if every group's prompt is the longest: 1.4 for a tile of keys of
+  // two row tiles, 0.8 of one.  Of the own parts, if they are half as long as the page table has
+  // room for: three CTAs of 3 us and 35 KB per us beside one another.
+  const bool one = static_cast<long long>(batch) * group <= static_cast<long long>(kBlockQ) * num_groups;
+  const double tiles = static_cast<double>(shared_row_tiles(batch, num_groups, group)) * hkv * key_tiles_of(max_shared_pages);
+  const double work = tiles * (one ? 0.8 : 1.4);
+  const double own_bytes = 0.5 * (max_pages - max_shared_pages) * kPageSize * 256.0 * hkv * batch;
+  const double cta = 3.0 + own_bytes / own_ctas / 35e3;
+  const double own = own_ctas * cta / 3.0;
+  // x SMs for the shared part: what the own parts have left at its end then has all SMs
   int best = sms;
   double least = 1e30;
   for (int x = sms; x >= 8; x -= 4) {
-    const double end = work / x, rate = (sms - x) * 0.1 / 6.6;
-    const double left = own - (rate < 1.0 ? rate : 1.0) * end;
-    const double t = end + (left > 0.0 ? left : 0.0);
+    const double end = 4.0 + work / x;
+    const double left = own - (sms - x) * end;
+    const double t = end + (left > 0.0 ? left / sms + cta : 0.0);
     if (t < 0.999 * least) {
       least = t;
       best = x;
     }
   }
-  return best < sms ? best : sms;
+  return best;
 }
 
 cudaError_t launch_shared(const CUtensorMap& kmap, const CUtensorMap& vmap, const SharedArgs& a, cudaStream_t stream) {
