@@ -21,6 +21,7 @@
 // beginning of the next, or several; the part of a unit in a run is a slot of its results.  A CTA
 // has 12 warps:
 //   warp 0        pages by TMA, one per lane, into a ring of four stages of 128 keys
+//   warp 3        walks along the run and puts its parts into a ring of four for the other warps
 //   warps 1, 2    one elected thread each issues a row tile's products: S = Q K^T (M = 128,
 //                 N = 128, K = 64) and O += P V with P from TMEM (M = 128, N = 64, K = 128)
 //   warps 4..11   four warps per row tile, a thread per row: it copies its row of Q into shared
@@ -55,11 +56,11 @@ constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr unsigned long long kDrainTimeoutNs = 2000000000ull;
 
+constexpr int kSegments = 4;
 constexpr int kMaxChunks = 176;  // kThreads groups each: up to 65535 groups
 
-// Where a warp is in its CTA's runs.
+// A place in the CTA's run.
 struct Walk {
-  int run;       // of the CTA
   int at, end;   // the rest of the run
   int in_group;  // work of group g before `at`
   int g, first_seq, count, pages;
@@ -86,21 +87,18 @@ struct __align__(1024) SharedSmem {
   uint64_t p_full[2];          // P is written and O rescaled                 (128 arrivals)
   uint64_t pv_done[2];         // O += P V is done                            (tcgen05.commit)
   uint64_t drain[2];
+  uint64_t seg_full[kSegments];   // a part of the run is there               (1 arrival)
+  uint64_t seg_empty[kSegments];  // every warp that reads it is through with it (11 arrivals)
   uint64_t stagger;            // row tile 0 has handed over a part's first P  (1 arrival)
   uint32_t tmem_base;
   int abort_flag;
   int issued_kv;
   int total;                   // tiles of keys of all units
   int most[2];                 // of one unit: of one row tile in two slots, others
-  int quantum;                 // of one run
-  int runs;
-  int turns;                   // units of one row tile have two slots per part
-  int each;                    // 0, or a unit's length in runs of one unit each
   int warp_sum[kThreads / 32];
   int warp_most[2][kThreads / 32];
   int chunk[kMaxChunks];       // work before each kThreads groups
-  Walk walk[kThreads / 32];    // of each warp
-  Segment seg[kThreads / 32];
+  Segment seg[kSegments];      // parts of this CTA's run, in turn; n_kv = 0: its end
 };
 
 __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
@@ -210,8 +208,7 @@ __device__ __forceinline__ void sum_work(const SharedArgs& a, SharedSmem& sm, in
   __syncthreads();
 }
 
-// The warp's walk stands at position `pos` of the work (below sm.total), for `quantum` of it.  The
-// whole warp.
+// The walk stands at position `pos` of the work (below sm.total), for `quantum` of it.  The whole warp.
 __device__ __forceinline__ void seek(const SharedArgs& a, SharedSmem& sm, Walk& walk, int pos, int quantum, int each) {
   const int lane = threadIdx.x & 31;
   int c = 0;
@@ -232,25 +229,24 @@ __device__ __forceinline__ void seek(const SharedArgs& a, SharedSmem& sm, Walk& 
       if (lane >= off) incl += v;
     }
     const int start = before + incl - n;
-    if (n > 0 && pos >= start && pos < start + n) {
+    const unsigned here = __ballot_sync(0xffffffffu, n > 0 && pos >= start && pos < start + n);
+    if (here) {
+      const int l = __ffs(here) - 1;
       walk.at = pos;
       walk.end = quantum < sm.total - pos ? pos + quantum : sm.total;
-      walk.in_group = pos - start;
-      walk.g = g;
-      walk.first_seq = first;
-      walk.count = count;
-      walk.pages = pages;
+      walk.in_group = pos - __shfl_sync(0xffffffffu, start, l);
+      walk.g = g0 + l;
+      walk.first_seq = __shfl_sync(0xffffffffu, first, l);
+      walk.count = __shfl_sync(0xffffffffu, count, l);
+      walk.pages = __shfl_sync(0xffffffffu, pages, l);
+      return;
     }
     before += __shfl_sync(0xffffffffu, incl, 31);
-    if (pos < before) break;
   }
-  __syncwarp();
 }
 
-// The walk's next part of a unit, if any.  The whole warp.
-__device__ __forceinline__ bool next_segment(const SharedArgs& a, Walk& walk, Segment& seg, int quantum, int each, bool turns) {
-  Walk w = walk;
-  Segment s{};
+// The walk's next part of a unit, if any.
+__device__ __forceinline__ bool next_segment(const SharedArgs& a, Walk& w, Segment& s, int quantum, int each, bool turns) {
   bool found = false;
   while (!found && w.at < w.end) {
     int len;
@@ -278,12 +274,6 @@ __device__ __forceinline__ bool next_segment(const SharedArgs& a, Walk& walk, Se
     w.in_group += n;
     found = s.n_kv > 0;
   }
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) {
-    walk = w;
-    seg = s;
-  }
-  __syncwarp();
   return found;
 }
 
@@ -306,13 +296,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   // Runs of equal length, as long as it takes for the grid to cover the work and for no unit to
   // have more parts than slots (a unit meets at most one run more than its length holds).  One
-  // slot: a run per unit, all as long as the longest.
+  // slot: runs of whole units, all as long as the longest.
   const int slots = a.plan.shared_splits;
   sum_work(a, sm, 0, blockIdx.x == 0);
   const int each = slots == 1 ? max(sm.most[0], sm.most[1]) : 0;
   if (each) sum_work(a, sm, each, false);
   const int total = sm.total, grid = gridDim.x;
-  int quantum = each ? each : total / grid + (total % grid != 0);
+  // (whole units)
+  int quantum = each ? each * ((total / each + grid - 1) / grid) : total / grid + (total % grid != 0);
   bool turns = false;
   if (!each) {  // (parts in turn have two slots each)
     quantum = max(quantum, (max(sm.most[0], sm.most[1]) + slots - 2) / (slots - 1));
@@ -323,15 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (turns && sm.most[0] > 0) quantum = max(quantum, in_turn);
   }
   if (quantum < 1) quantum = 1;
-  // this CTA's runs: blockIdx.x, + gridDim.x, ..
-  const int runs = total / quantum + (total % quantum != 0);
-  if (static_cast<int>(blockIdx.x) >= runs) return;  // uniform, before any barrier or TMEM use
-  if (threadIdx.x == 0) {
-    sm.quantum = quantum;
-    sm.runs = runs;
-    sm.turns = turns;
-    sm.each = each;
-  }
+  if (static_cast<int>(blockIdx.x) >= total / quantum + (total % quantum != 0)) return;  // uniform, before any barrier or TMEM use
 
   volatile int* abort_flag = &sm.abort_flag;
   if (threadIdx.x == 0) {
@@ -344,6 +327,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&sm.drain[t]), 1);
     }
     mbar_init(smem_u32(&sm.stagger), 1);
+    for (int i = 0; i < kSegments; ++i) {
+      mbar_init(smem_u32(&sm.seg_full[i]), 1);
+      mbar_init(smem_u32(&sm.seg_empty[i]), 11);
+    }
     for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_u32(&sm.kv_full[s]), 1);
       mbar_init(smem_u32(&sm.kv_empty[s]), 2);
@@ -362,38 +349,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto tmem_base = [&]() { return *reinterpret_cast<volatile const uint32_t*>(&sm.tmem_base); };
 
   const int slot_rows = slots + a.plan.own_splits;  // slots of a sequence's results
-  Segment& seg = sm.seg[warp];  // the warp's present part of a unit
-  // body(tiles of keys of this part, of the parts before) for every part of this CTA's runs, until it
-  // returns false; every warp walks by itself.
-  // (What it needs from part to part stays in shared memory: the softmax warps have no registers left.)
+  // body(part, its tiles of keys, tiles of keys of the parts before) for every part of this CTA's run,
+  // until it returns false.  The whole warp; false when something has been given up.
   auto for_segments = [&](auto&& body) {
-    volatile SharedSmem& vs = sm;
-    if (lane == 0) sm.walk[warp].run = blockIdx.x;
-    __syncwarp();
     int g = 0;
-    while (vs.walk[warp].run < vs.runs) {
-      seek(a, sm, sm.walk[warp], vs.walk[warp].run * vs.quantum, vs.quantum, vs.each);
-      while (next_segment(a, sm.walk[warp], seg, vs.quantum, vs.each, vs.turns != 0)) {
-        const int n = seg.n_kv;
-        if (!body(n, g)) return;
-        g += n;
-      }
-      __syncwarp();
-      if (lane == 0) sm.walk[warp].run += gridDim.x;
-      __syncwarp();
+    for (int it = 0;; ++it) {
+      if (!__all_sync(0xffffffffu, wait_bar(smem_u32(&sm.seg_full[it % kSegments]), (it / kSegments) & 1, a.timeout_ns, abort_flag)))
+        return false;
+      const volatile Segment& seg = sm.seg[it % kSegments];
+      const int n = seg.n_kv;
+      if (n == 0) return true;
+      if (!__all_sync(0xffffffffu, body(seg, n, g))) return false;
+      if (lane == 0) mbar_arrive(smem_u32(&sm.seg_empty[it % kSegments]));
+      g += n;
     }
   };
 
-  // 128 * 80 + 256 * 208 registers, of the launch's 384 * 168 (with fewer for the four control warps, what
-  // every role needs of the set-up is spilled)
+  // 128 * 56 + 256 * 224 = 384 * 168 registers (the launch's total)
   if (warp < 4) {
-    regs_dec<80>();
+    regs_dec<56>();
     if (warp == 0) {
       // ------------------------------------------------------------ pages
       const uint64_t policy = l2_policy_evict_last();  // other row tiles read the same pages
       const int no_page = a.num_pages * a.hkv * kPageSize;  // a row behind the cache: reads as zeros
-      bool ok = true;
-      for_segments([&](int n_kv, int g) {
+      const bool ok = for_segments([&](const volatile Segment& seg, int n_kv, int g) {
         const int32_t* ptab = a.page_table + static_cast<size_t>(seg.first_seq) * a.max_pages;
         const int n_pages = seg.n_pages, tile0 = seg.tile0, kvh = seg.kvh;
         auto load_row = [&](int j) {  // first cache row of box `lane` of tile j (lanes < 8)
@@ -413,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (gg >= kStages) {
             int r = 1;
             if (lane == 0) r = wait_bar(smem_u32(&sm.kv_empty[st]), ((gg / kStages) - 1) & 1, a.timeout_ns, abort_flag) ? 1 : 0;
-            if (!__shfl_sync(0xffffffffu, r, 0)) return ok = false;
+            if (!__shfl_sync(0xffffffffu, r, 0)) return false;
           }
           const uint32_t bar = smem_u32(&sm.kv_full[st]);
           if (lane == 0) mbar_arrive_expect_tx(bar, 2 * kTileBytes);
@@ -428,6 +407,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       });
       if (!ok && lane == 0) raise_status(a.status, kStatusTimeout);
+    } else if (warp == 3) {
+      // ------------------------------------------------------------ the run's parts
+      Walk walk;
+      seek(a, sm, walk, static_cast<int>(blockIdx.x) * quantum, quantum, each);
+      bool more = true;
+      for (int it = 0; more; ++it) {
+        if (it >= kSegments && !__all_sync(0xffffffffu, wait_bar(smem_u32(&sm.seg_empty[it % kSegments]), ((it / kSegments) - 1) & 1,
+                                                                 a.timeout_ns, abort_flag))) {
+          if (lane == 0) raise_status(a.status, kStatusTimeout);
+          break;
+        }
+        Segment s{};
+        more = next_segment(a, walk, s, quantum, each, turns);
+        if (!more) s.n_kv = 0;
+        if (lane == 0) {
+          sm.seg[it % kSegments] = s;  // (n_kv = 0 behind the last)
+          mbar_arrive(smem_u32(&sm.seg_full[it % kSegments]));
+        }
+        __syncwarp();
+      }
     } else if (warp == 1 || warp == 2) {
       // ------------------------------------------------------------ products
       const int t = warp - 1;
@@ -439,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       bool ok = true;
       int steps = 0, parts = 0, all_parts = 0;  // of this set of warps; of the CTA
-      for_segments([&](int n_kv, int g) {
+      const bool walked = for_segments([&](const volatile Segment& seg, int n_kv, int g) {
         const int part = all_parts++;
         const bool turns = seg.turns;
         if (!turns && t * kBlockQ >= seg.rows) {  // no such row tile: the stages are as good as used
@@ -499,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return ok;
       });
       if (elect_one()) {
-        if (!ok) raise_status(a.status, kStatusTimeout);
+        if (!walked) raise_status(a.status, kStatusTimeout);
         // whatever happened, every product issued here is done before TMEM is released
         tc_commit(smem_u32(&sm.drain[t]));
         mbar_wait(smem_u32(&sm.drain[t]), 0, kDrainTimeoutNs);
@@ -507,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
   } else {
-    regs_inc<208>();
+    regs_inc<224>();
     // -------------------------------------------------------------- softmax
     const int t = (warp - 4) >> 2;  // row tile of this warpgroup
     const int qw = warp & 3;        // TMEM lane quarter
@@ -516,26 +515,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t o_col = lane_base + kColO + t * 64;
     const uint32_t p_col = lane_base + kColP + t * 64;
     const uint64_t scale2 = f2(a.scale_log2, a.scale_log2);
-    // sequence and query head of a row of the present part
-    auto row_index = [&](int row, int& seq, int& head) {
+    // sequence and query head of a row of a part
+    auto row_index = [&](const volatile Segment& seg, int row, int& seq, int& head) {
       const int gr = seg.row0 + row;
       seq = seg.first_seq + gr / a.group;
       head = seg.kvh * a.group + gr % a.group;
     };
-    bool ok = true;
-    int steps = 0;  // of this row tile
-    for_segments([&](int n_kv, int) {
+    auto wait = [&](uint64_t& bar, int parity) {  // the same in all lanes: what follows is for the whole warp
+      return __all_sync(0xffffffffu, wait_bar(smem_u32(&bar), parity & 1, a.timeout_ns, abort_flag)) != 0;
+    };
+    int steps = 0;  // of this set of warps
+    const bool ok = for_segments([&](const volatile Segment& seg, int n_kv, int) {
       if (!seg.turns && t * kBlockQ >= seg.rows) return true;  // no such row tile
       const int r = (seg.turns ? 0 : t * kBlockQ) + qw * 32 + lane;  // row within the unit
       const int n = seg.turns ? (n_kv - t + 1) / 2 : n_kv;
       // read again where it is used, rather than held in registers that the score row needs
-      const volatile Segment& vseg = seg;
-      auto live = [&]() { return r < vseg.rows; };
-      auto warp_live = [&]() { return (r & ~31) < vseg.rows; };
+      auto live = [&]() { return r < seg.rows; };
+      auto warp_live = [&]() { return (r & ~31) < seg.rows; };
       if (n > 0) {
         // the tile's Q (every product that read the last part's is done: its scores have been waited for)
         int seq, head;
-        row_index(live() ? r : 0, seq, head);
+        row_index(seg, live() ? r : 0, seq, head);
         const uint4* src = reinterpret_cast<const uint4*>(a.q + (static_cast<size_t>(seq) * a.hq + head) * kHeadDim);
         uint4 x[8];
 #pragma unroll
@@ -548,10 +548,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float m = kNegInf, d = 0.0f;  // running maximum (log2 units) and sum
       for (int j = 0; j < n; ++j) {
-        if (!wait_bar(smem_u32(&sm.s_full[t]), (steps + j) & 1, a.timeout_ns, abort_flag)) return ok = false;
+        if (!wait(sm.s_full[t], steps + j)) return false;
         if (!warp_live()) {  // rows that nothing reads: keep step with the others, phase by phase
           mbar_arrive(smem_u32(&sm.s_free[t]));
-          if (j > 0 && !wait_bar(smem_u32(&sm.pv_done[t]), (steps + j - 1) & 1, a.timeout_ns, abort_flag)) return ok = false;
+          if (j > 0 && !wait(sm.pv_done[t], steps + j - 1)) return false;
           mbar_arrive(smem_u32(&sm.p_full[t]));
           continue;
         }
@@ -570,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 128; ++c) s[c] = __uint_as_float(sr[c]);
         float mraw = fmax3(pm0, pm1, fmaxf(pm2, pm3));
         // keys from this tile's first on
-        const int left = vseg.n_pages * kPageSize - (vseg.tile0 + (vseg.turns ? 2 * j + t : j)) * kBlockK;
+        const int left = seg.n_pages * kPageSize - (seg.tile0 + (seg.turns ? 2 * j + t : j)) * kBlockK;
         if (left < kBlockK) {  // the prompt ends inside this tile: its missing pages read as zeros
           mraw = kNegInf;
 #pragma unroll
@@ -608,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         f2_split(f2_add(f2_add(acc0, acc1), f2_add(acc2, acc3)), r0, r1);
         d += r0 + r1;
         // P and O are in use by the previous product until it is done
-        if (j > 0 && !wait_bar(smem_u32(&sm.pv_done[t]), (steps + j - 1) & 1, a.timeout_ns, abort_flag)) return ok = false;
+        if (j > 0 && !wait(sm.pv_done[t], steps + j - 1)) return false;
         tc_fence_after();
         if (j > 0 && __any_sync(0xffffffffu, grow)) {
           const uint64_t f22 = f2(factor, factor);
@@ -642,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (j == 0 && warp == 4 && lane == 0) mbar_arrive(smem_u32(&sm.stagger));
       }
       steps += n;
-      if (n > 0 && !wait_bar(smem_u32(&sm.pv_done[t]), (steps - 1) & 1, a.timeout_ns, abort_flag)) return ok = false;
+      if (n > 0 && !wait(sm.pv_done[t], steps - 1)) return false;
       if (warp_live()) {
         tc_fence_after();
         uint32_t ou[2][32];
@@ -653,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (live()) {
           const float inv = d > 0.0f ? 1.0f / d : 0.0f;
           int seq, head;
-          row_index(r, seq, head);
+          row_index(seg, r, seq, head);
           const int slot = seg.turns ? 2 * seg.slot + t : seg.slot;
           const size_t out = (static_cast<size_t>(seq) * slot_rows + slot) * a.hq + head;
           if (n > 0) {
