@@ -439,24 +439,28 @@ void sink_attn_decode_shared_splits(int batch, int num_groups, int num_qo_heads,
   if (batch > 0 && num_groups > 0 && num_kv_heads > 0 && num_qo_heads >= num_kv_heads && max_shared_pages >= 0 &&
       max_pages > 0) {
     if (num_sms <= 0) num_sms = 152;
-    // own part: three CTAs per SM, at least 16 pages each, at most 8 splits
+    // own part: a CTA per SM, at least 16 pages each, at most 8 splits
     const long long own_pages = max_pages > max_shared_pages ? max_pages - max_shared_pages : 1;
     const long long own_units = static_cast<long long>(batch) * num_kv_heads;
-    while (o < 8 && own_units * o < 3LL * num_sms && own_pages / (2 * o) >= 16) o *= 2;
-    // shared part: its CTAs' equal runs cut a unit of work into twice as many parts as it has CTAs
-    // (units are of uneven length), and two more, of two slots where units have one row tile; at
-    // most 40, and 96 MB
+    while (o < 8 && own_units * o < num_sms && own_pages / (2 * o) >= 16) o *= 2;
+    // shared part: its CTAs' equal runs cut a unit of work into as many parts as it has CTAs, twice
+    // as many where groups' units may be of uneven length, and two more; two slots each where units
+    // have one row tile.  More than 15, which with an own one the merge asks for at once, are worth
+    // it for few rows and long prompts only: of 64/8 heads, 8 sequences that share 4800 tokens take
+    // 13.3 us with 15 slots and 16.9 with 40, 16 that share 16384 tokens 21 and 26; but 2 sequences
+    // of 16/1 heads that share 32768 tokens 26 and 18.
     const int group = num_qo_heads / num_kv_heads;
     const long long tiles = (max_shared_pages + 7) / 8;
     const long long units = sa::shared_row_tiles(batch, num_groups, group) * num_kv_heads;
     const long long ctas = sa::shared_ctas(batch, num_groups, group, num_kv_heads, max_shared_pages, max_pages,
                                            static_cast<int>(own_units * o < (1 << 30) ? own_units * o : 1 << 30), num_sms);
-    long long n = 2 * ctas / units + 2;
+    long long n = (num_groups == 1 ? 1 : 2) * ctas / units + 2;
     if (n > tiles + 1) n = tiles + 1;
     if (static_cast<long long>(batch) * group <= 128LL * num_groups) n = 2 * (n < tiles / 2 + 1 ? n : tiles / 2 + 1);
+    const long long most = tiles > 64 && units <= 4 ? 40 : 15;
+    if (n > most) n = most;
     const long long room = (96LL << 20) / (static_cast<long long>(batch) * num_qo_heads * 260);
     if (n > room) n = room;
-    if (n > 40) n = 40;
     s = n < 2 ? 2 : static_cast<int>(n);
   }
   if (shared_splits) *shared_splits = s;

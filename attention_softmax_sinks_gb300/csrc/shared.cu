@@ -94,8 +94,10 @@ struct __align__(1024) SharedSmem {
   int abort_flag;
   int issued_kv;
   int total;                   // tiles of keys of all units
+  int units;
   int most[2];                 // of one unit: of one row tile in two slots, others
   int warp_sum[kThreads / 32];
+  int warp_units[kThreads / 32];
   int warp_most[2][kThreads / 32];
   int chunk[kMaxChunks];       // work before each kThreads groups
   Segment seg[kSegments];      // parts of this CTA's run, in turn; n_kv = 0: its end
@@ -158,24 +160,26 @@ __device__ __forceinline__ int row_tile_pairs(const SharedArgs& a, int count) {
 }
 __device__ __forceinline__ int key_tiles(int pages) { return (pages + kPagesPerTile - 1) / kPagesPerTile; }
 
-// A group's units' length (`each` or, 0, its tiles of keys; 0 if it shares nothing) and number.
+// A group's work, and its units' length: its tiles of keys, rounded up to a multiple of `each` if
+// that is not 0; 0 if it shares nothing.
 __device__ __forceinline__ int group_work(const SharedArgs& a, int count, int pages, int each, int& len) {
   const int tiles = count > 0 ? key_tiles(pages) : 0;
-  len = each && tiles ? each : tiles;
+  len = each ? (tiles + each - 1) / each * each : tiles;
   return row_tile_pairs(a, count) * a.hkv * len;
 }
 
-// Sums up the groups' work, kThreads groups at a time: sm.total, sm.most, sm.chunk.  All threads.
+// Sums up the groups' work, kThreads groups at a time: sm.total, sm.units, sm.most, sm.chunk.  All threads.
 __device__ __forceinline__ void sum_work(const SharedArgs& a, SharedSmem& sm, int each, bool report) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int before = 0, most[2] = {0, 0};
+  int before = 0, units = 0, most[2] = {0, 0};
   for (int g0 = 0; g0 < a.plan.num_groups; g0 += kThreads) {
     const int g = g0 + static_cast<int>(threadIdx.x);
-    int n = 0, tiles[2] = {0, 0};
+    int n = 0, u = 0, tiles[2] = {0, 0};
     if (g < a.plan.num_groups) {
       int first, count, pages, len;
       if (!group_bounds(a, g, first, count, pages) && report) raise_status(a.status, kStatusBadLen);
       n = group_work(a, count, pages, each, len);
+      u = n > 0 ? n / len : 0;
       const int rows = count * a.group;  // its last unit has one row tile, or two; the others two
       if ((rows - 1) % (2 * kBlockQ) < kBlockQ) tiles[0] = len;
       if (rows > kBlockQ) tiles[1] = len;
@@ -183,12 +187,14 @@ __device__ __forceinline__ void sum_work(const SharedArgs& a, SharedSmem& sm, in
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
       n += __shfl_xor_sync(0xffffffffu, n, off);
+      u += __shfl_xor_sync(0xffffffffu, u, off);
       tiles[0] = max(tiles[0], __shfl_xor_sync(0xffffffffu, tiles[0], off));
       tiles[1] = max(tiles[1], __shfl_xor_sync(0xffffffffu, tiles[1], off));
     }
     __syncthreads();  // the last round's sums have been read
     if (lane == 0) {
       sm.warp_sum[warp] = n;
+      sm.warp_units[warp] = u;
       sm.warp_most[0][warp] = tiles[0];
       sm.warp_most[1][warp] = tiles[1];
     }
@@ -196,12 +202,14 @@ __device__ __forceinline__ void sum_work(const SharedArgs& a, SharedSmem& sm, in
     if (threadIdx.x == 0) sm.chunk[g0 / kThreads] = before;
     for (int w = 0; w < kThreads / 32; ++w) {
       before += sm.warp_sum[w];
+      units += sm.warp_units[w];
       most[0] = max(most[0], sm.warp_most[0][w]);
       most[1] = max(most[1], sm.warp_most[1][w]);
     }
   }
   if (threadIdx.x == 0) {
     sm.total = before;
+    sm.units = units;
     sm.most[0] = most[0];
     sm.most[1] = most[1];
   }
@@ -295,24 +303,45 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   __syncthreads();
   // Runs of equal length, as long as it takes for the grid to cover the work and for no unit to
-  // have more parts than slots (a unit meets at most one run more than its length holds).  One
-  // slot: runs of whole units, all as long as the longest.
-  const int slots = a.plan.shared_splits;
+  // have more parts than slots.  Where there are at least four CTAs to a unit, units end with a run
+  // (their lengths are rounded up), as a CTA spends 3 to 5 us between two parts (16 sequences that
+  // share 16384 tokens, 64/8 heads: 28 us with runs of 12 tiles across units of 128, 21 in this
+  // way); else a unit meets at most one run more than its length holds.  One slot: runs of whole
+  // units, all as long as the longest.
+  const int slots = a.plan.shared_splits, grid = gridDim.x;
   sum_work(a, sm, 0, blockIdx.x == 0);
-  const int each = slots == 1 ? max(sm.most[0], sm.most[1]) : 0;
-  if (each) sum_work(a, sm, each, false);
-  const int total = sm.total, grid = gridDim.x;
-  // (whole units)
-  int quantum = each ? each * ((total / each + grid - 1) / grid) : total / grid + (total % grid != 0);
+  const int units = sm.units, most1 = sm.most[1], most = max(sm.most[0], most1);
+  const bool aligned = slots > 1 && 4 * units <= grid;
+  int each = slots == 1 ? most : 0, quantum;
   bool turns = false;
-  if (!each) {  // (parts in turn have two slots each)
-    quantum = max(quantum, (max(sm.most[0], sm.most[1]) + slots - 2) / (slots - 1));
-    // tiles of keys in turn, where the slots are enough for parts not much longer than that (at
-    // least of a tile for each set of warps)
-    const int parts = slots / 2 - 1, in_turn = parts > 0 ? max((sm.most[0] + parts - 1) / parts, 2) : 0;
-    turns = in_turn > 0 && in_turn <= 2 * quantum;
-    if (turns && sm.most[0] > 0) quantum = max(quantum, in_turn);
+  if (each) {
+    sum_work(a, sm, each, false);
+    quantum = each * ((units + grid - 1) / grid);
+  } else {
+    const int cover = aligned ? (sm.total - units + grid - units - 1) / (grid - units) : (sm.total + grid - 1) / grid;
+    quantum = max(cover, aligned ? (most + slots - 1) / slots : (most + slots - 2) / (slots - 1));
+    // Units of one row tile: tiles of keys in turn, if the slots (two for each part) are enough for
+    // runs not much longer than that, as a tile then takes 0.75 us instead of 1.2; an even number,
+    // as many for each set of warps.  Units of two row tiles gain nothing by longer runs.
+    const int parts = slots / 2 - (aligned ? 0 : 1);
+    if (parts > 0 && sm.most[0] > 0) {
+      int in_turn = max((sm.most[0] + parts - 1) / parts, 2);
+      if (most1 == 0) in_turn = (max(in_turn, cover) + 1) & ~1;
+      turns = most1 > 0 ? in_turn <= quantum : 5 * in_turn <= 8 * quantum;
+      if (turns) quantum = max(quantum, in_turn);
+    }
+    if (aligned) {
+      each = max(quantum, 1);
+      if (a.plan.num_groups > 1) {
+        sum_work(a, sm, each, false);
+      } else {
+        __syncthreads();
+        if (threadIdx.x == 0) sm.total = units * ((most + each - 1) / each * each);
+        __syncthreads();
+      }
+    }
   }
+  const int total = sm.total;
   if (quantum < 1) quantum = 1;
   if (static_cast<int>(blockIdx.x) >= total / quantum + (total % quantum != 0)) return;  // uniform, before any barrier or TMEM use
 
@@ -760,12 +789,12 @@ long long shared_row_tiles(int batch, int num_groups, int group) {
 }
 
 int shared_ctas(int batch, int num_groups, int group, int hkv, int max_shared_pages, int max_pages, int own_ctas, int sms) {
-  // SM time (us) of the shared part, if every group's prompt is the longest: 1.4 for a tile of keys of
-  // two row tiles, 0.8 of one.  Of the own parts, if they are half as long as the page table has
+  // SM time (us) of the shared part, if every group's prompt is the longest: 1.28 for a tile of keys
+  // of two row tiles, 0.75 of one.  Of the own parts, if they are half as long as the page table has
   // room for: three CTAs of 3 us and 35 KB per us beside one another.
   const bool one = static_cast<long long>(batch) * group <= static_cast<long long>(kBlockQ) * num_groups;
   const double tiles = static_cast<double>(shared_row_tiles(batch, num_groups, group)) * hkv * key_tiles_of(max_shared_pages);
-  const double work = tiles * (one ? 0.8 : 1.4);
+  const double work = tiles * (one ? 0.75 : 1.28);
   const double own_bytes = 0.5 * (max_pages - max_shared_pages) * kPageSize * 256.0 * hkv * batch;
   const double cta = 3.0 + own_bytes / own_ctas / 35e3;
   const double own = own_ctas * cta / 3.0;
@@ -775,7 +804,7 @@ int shared_ctas(int batch, int num_groups, int group, int hkv, int max_shared_pa
   for (int x = sms; x >= 8; x -= 4) {
     const double end = 4.0 + work / x;
     const double left = own - (sms - x) * end;
-    const double t = end + (left > 0.0 ? left / sms + cta : 0.0);
+    const double t = end + (left > 0.0 ? left / sms : 0.0);
     if (t < 0.999 * least) {
       least = t;
       best = x;
