@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
   if (static_cast<int>(blockIdx.x) >= passes) return;  // the whole cluster, before TMEM is taken
   cluster_arrive_relaxed();  // waited for before the first store into another CTA
   const int owner_rows = kBM / a.splits;  // of the tile: CTA `split` adds up [split * owner_rows, ..)
-  float* recv = reinterpret_cast<float*>(tiles + kShrinkStages * kShrinkStageBytes);  // [part][row][R]
+  float* recv = reinterpret_cast<float*>(tiles + kShrinkStages * kShrinkStageBytes);  // [part][R / 4][row], four each
   // this CTA's part of K, in steps of 64
   const int steps = (a.K + kBK - 1) / kBK;
   const int k0 = static_cast<int>(static_cast<long long>(steps) * split / a.splits);
@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
     const int q = warp & 3, r = 32 * q + lane;
     const uint32_t acc = tmem + (static_cast<uint32_t>(32 * q) << 16);
     const float scale = mine >= 0 && a.scale ? __ldg(a.scale + sb.plan.list[mine]) : 1.0f;
-    const uint32_t out = dsmem_addr(smem_u32(recv + (split * owner_rows + r % owner_rows) * a.R), r / owner_rows);
+    const uint32_t out = dsmem_addr(smem_u32(recv + (split * (a.R / 4) * owner_rows + r % owner_rows) * 4), r / owner_rows);
     int i = 0;
     for (int pass = blockIdx.x; pass < passes; pass += gridDim.x, ++i) {
       const int first = pass * per_pass, n = min(per_pass, slots - first);
@@ -543,8 +543,8 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
             float f[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u) f[u] = scale * __uint_as_float(v[u]);
-            dsmem_st4(out + 4 * c, f[0], f[1], f[2], f[3]);
-            dsmem_st4(out + 4 * c + 16, f[4], f[5], f[6], f[7]);
+            dsmem_st4(out + 4 * c * owner_rows, f[0], f[1], f[2], f[3]);
+            dsmem_st4(out + 4 * (c + 4) * owner_rows, f[4], f[5], f[6], f[7]);
           }
         }
       }
@@ -564,12 +564,12 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
   cluster_sync();  // every part of the rows has arrived
   const int parts = a.splits;
   for (int i = threadIdx.x; i < owner_rows * (a.R / 8); i += kShrinkThreads) {
-    const int r = i / (a.R / 8), c = i % (a.R / 8) * 8, s = sb.slot[split * owner_rows + r];
+    const int r = i % owner_rows, c = i / owner_rows * 8, s = sb.slot[split * owner_rows + r];
     if (s < 0 || s / per_pass % gridDim.x != blockIdx.x) continue;  // none, or another cluster's
     float sum[8] = {};
     for (int p = 0; p < parts; ++p) {
-      const float4* v = reinterpret_cast<const float4*>(recv + (p * owner_rows + r) * a.R + c);
-      const float4 v0 = v[0], v1 = v[1];
+      const float4* v = reinterpret_cast<const float4*>(recv) + (p * (a.R / 4) + c / 4) * owner_rows + r;
+      const float4 v0 = v[0], v1 = v[owner_rows];
       sum[0] += v0.x;
       sum[1] += v0.y;
       sum[2] += v0.z;
@@ -773,6 +773,7 @@ __host__ __device__ constexpr int t_bufs(int bn) {
   const int n = (static_cast<int>(kTmemCols) - 2 * acc_columns(bn)) / kTCols;
   return n > kMaxTBufs ? kMaxTBufs : n;
 }
+static_assert(t_bufs(kMaxBlockN) >= 2, "two buffers of T behind the accumulators");
 
 // RC: chunks of 16 ranks (a rank in between counts as the next size: the boxes behind R read zeros).
 // Outside pairs 80 registers (two blocks' worth), so that a CTA of the first kernel fits beside.
@@ -1120,7 +1121,8 @@ __global__ void __launch_bounds__(kThreads, kMode == kModePair || RC > 4 ? 1 : 2
     const int q = warp & 3, r = 32 * q + lane, half = warp >= 8 ? 1 : 0;
     const int mt = t_first / a.tiles_n, n0 = (t_first % a.tiles_n) * bn, row = mt * kBM + r;
     const uint32_t acc = tmem + (static_cast<uint32_t>(32 * q) << 16);
-    const float* recv = reinterpret_cast<const float*>(tiles);  // [part][row][cw]
+    // [part][cw / 4][row], four columns each: a warp's stores are 512 bytes in a row
+    const float4* recv = reinterpret_cast<const float4*>(tiles);
     const bool warp_live = warp >= 4 && mt * kBM + 32 * q < a.M;
     if (warp_live) {
 #pragma unroll 1
@@ -1131,9 +1133,9 @@ __global__ void __launch_bounds__(kThreads, kMode == kModePair || RC > 4 ? 1 : 2
         tmem_ld8(acc + c, v);
         tc_wait_ld();
         if (row < a.M) {
-          const uint32_t to = dsmem_addr(ring + 4 * ((part * kBM + r) * cw + c - owner * cw), owner);
+          const uint32_t to = dsmem_addr(ring + 16 * ((part * (cw / 4) + (c - owner * cw) / 4) * kBM + r), owner);
           dsmem_st4(to, __uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]), __uint_as_float(v[3]));
-          dsmem_st4(to + 16, __uint_as_float(v[4]), __uint_as_float(v[5]), __uint_as_float(v[6]), __uint_as_float(v[7]));
+          dsmem_st4(to + 16 * kBM, __uint_as_float(v[4]), __uint_as_float(v[5]), __uint_as_float(v[6]), __uint_as_float(v[7]));
         }
       }
     }
@@ -1155,9 +1157,9 @@ __global__ void __launch_bounds__(kThreads, kMode == kModePair || RC > 4 ? 1 : 2
               lo = make_float4(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]), __uint_as_float(v[3]));
               hi = make_float4(__uint_as_float(v[4]), __uint_as_float(v[5]), __uint_as_float(v[6]), __uint_as_float(v[7]));
             } else {
-              const float4* from = reinterpret_cast<const float4*>(recv + (p * kBM + r) * cw + c - part * cw);
+              const float4* from = recv + (p * (cw / 4) + (c - part * cw) / 4) * kBM + r;
               lo = from[0];
-              hi = from[1];
+              hi = from[kBM];
             }
             sum[0] += lo.x;
             sum[1] += lo.y;
@@ -1271,21 +1273,41 @@ void lora_plan(LoraArgs& a, int sms) {
   a.tiles_m = (a.M + kBM - 1) / kBM;
   a.box_rows = a.M < kBM ? (a.M + 7) / 8 * 8 : kBM;
   const int k_blocks = (a.K + kBK - 1) / kBK;
-  // Estimated cycles of tiles of bn columns, by single CTAs, by pairs or by clusters that share K.  A
-  // block of 64 values of K takes what is longest: the operands' way in (64 bytes a cycle), the
-  // tensor core's reading (128 bytes a cycle, 128 rows of x whatever their number), its arithmetic.
-  // Clusters add up at the end, and the GPU holds 76, 36 or 15 of them (GPCs of 18 to 20 SMs): a
-  // second round is not considered.  (4096 -> 2880, 1 token: single CTAs 12.7 us, clusters of 4 8.3;
-  // 2880 -> 5120, 64 tokens 19.2 and 13.6.)
+  // Parts of K of the first product.  Pairs (many tokens): a CTA per SM, clusters of up to 8 parts of at
+  // least two steps; else: a step of K for each of a CTA's eight warps, up to 4 parts.
+  int pair_splits = 1;
+  while (pair_splits < 8 && 2 * pair_splits * a.tiles_m <= sms && 4 * pair_splits <= k_blocks) pair_splits *= 2;
+  // As blocks of K: ranks of half the adapters that a tile of tokens can have.
+  const int most = a.M < kBM ? a.M : kBM;
+  const int adapter_blocks = ((a.num_adapters < most ? a.num_adapters : most) * ((a.R + 15) / 16) + 7) / 8;
+  // Estimated cycles of tiles of bn columns, by single CTAs, by pairs or by clusters that share K; the
+  // factors are fitted to times over 27 sizes (1 to 2000 tokens, 4096 -> 2880, 2880 -> 5120 and 640), and
+  // what is chosen took at most 8% more than the best of all.  A block of 64 values of K takes what is
+  // longest: the operands' way in (64 bytes a cycle), the tensor core's reading (128 bytes a cycle, 128
+  // rows of x whatever their number), its arithmetic.  Clusters that share K add up at the end, and the
+  // GPU holds 76, 36 or 15 of them (GPCs of 18 to 20 SMs), fewer beside the first product's CTAs of
+  // more tokens: a second round is not considered.  Pairs need whole SMs: those that the first
+  // product's CTAs leave (if enough for there to be pairs among them), or all when they are through.  Single CTAs and clusters pay more for it.
+  // (4096 -> 2880, 1 token: single CTAs 12.7 us, clusters of 4 11.0; 2880 -> 5120, 64 tokens: 16.4 and,
+  // clusters of 2, 14.0; 512 tokens: 25.2, pairs 23.5.)
   auto cycles = [&](int bn, int ctas, int parts) {
     const long long tiles = static_cast<long long>((a.tiles_m + ctas - 1) / ctas) * ((a.N + bn - 1) / bn);
-    const long long slots = parts == 1 ? sms / ctas : parts == 2 ? sms / 2 : parts == 4 ? sms * 36 / 152 : sms * 15 / 152;
+    const bool few = a.M <= 32;
+    const long long slots = parts == 1   ? sms / ctas
+                            : parts == 2 ? sms * (few ? 76 : 60) / 152
+                            : parts == 4 ? sms * (few ? 36 : 32) / 152
+                                         : sms * 15 / 152;
     const long long rounds = (tiles + slots - 1) / slots;
     if (parts > 1 && rounds > 1) return 1LL << 60;
     const long long in = 2LL * (a.box_rows + bn / ctas), read = kBM + bn / ctas, mma = 2LL * bn;
     long long block = in > read ? in : read;
     if (mma > block) block = mma;
-    return rounds * ((k_blocks + parts - 1) / parts) * block + 8LL * bn + (parts > 1 ? 1500 : 0);
+    long long tile = (k_blocks + adapter_blocks + parts - 1) / parts * (112 + 7 * block / 10) + 53LL * bn;
+    if (parts > 1) tile += 3LL * most * (bn - bn / parts) / 10;
+    if (ctas == 1) return rounds * tile + 12LL * a.M + (parts == 8 ? 2000 : 0);
+    const long long left = sms - static_cast<long long>(pair_splits) * a.tiles_m, beside = 4 * left >= sms ? left / 2 : 0;
+    const long long late = tiles > beside ? 16000 + (tiles - beside + slots - 1) / slots * tile : 0;
+    return rounds * tile > late ? rounds * tile : late;
   };
   long long least = 1LL << 60;
   auto offer = [&](int bn, int ctas, int parts) {
@@ -1302,14 +1324,7 @@ void lora_plan(LoraArgs& a, int sms) {
   for (int parts = 2; parts <= 8 && 2 * parts <= k_blocks; parts *= 2)
     for (int bn = kMaxBlockN; bn >= 32; bn -= 16) offer(bn, 1, parts);
   a.tiles_n = (a.N + a.block_n - 1) / a.block_n;
-  // Parts of K of the first product.  Many tokens: a CTA per SM, clusters of up to 8 parts of at
-  // least two steps; few: a step of K for each of a CTA's eight warps, up to 4 parts.
-  a.splits = 1;
-  if (a.plan_tiles == 2) {
-    while (a.splits < 8 && 2 * a.splits * a.tiles_m <= sms && 4 * a.splits <= k_blocks) a.splits *= 2;
-  } else {
-    a.splits = (a.K + 255) / 256 < 4 ? (a.K + 255) / 256 : 4;
-  }
+  a.splits = a.plan_tiles == 2 ? pair_splits : (a.K + 255) / 256 < 4 ? (a.K + 255) / 256 : 4;
 }
 
 cudaError_t launch_lora(const LoraMaps& m, const LoraArgs& a, int sms, cudaStream_t stream) {
