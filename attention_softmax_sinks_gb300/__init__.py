@@ -91,7 +91,7 @@ _SIGNATURES = {
                                      _p, _p, _p, _p, _p]),
     "sink_attn_decode_shared_splits": (None, [_i, _i, _i, _i, _i, _i, _i, _p, _p]),
     "lora_linear_bias": (_i, [_p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _p, _p, _p]),
-    "lora_workspace_bytes": (_ll, [_i, _i, _i]),
+    "lora_workspace_bytes": (None, [_i, _i, _i, _p]),
     "moe_router_scores": (_i, [_p, _i, _ll, _i, _i, _i, _p, _i, _i, _i, _f, _p, _p, _p, _p]),
     "grouped_mxfp4_linear_swiglu": (_i, [_p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _f, _f, _p, _p]),
 }
@@ -546,7 +546,9 @@ def linear_bias(x, w, bias=None, out=None, stream=None):
 
 def lora_workspace_bytes(m: int, k: int, rank: int) -> int:
     """Bytes of workspace for lora_linear_bias of m tokens."""
-    return load_library().lora_workspace_bytes(_c_int(m, "m"), _c_int(k, "k"), _c_int(rank, "rank"))
+    n = ctypes.c_longlong()
+    load_library().lora_workspace_bytes(_c_int(m, "m"), _c_int(k, "k"), _c_int(rank, "rank"), ctypes.byref(n))
+    return n.value
 
 
 _lora_bytes = functools.lru_cache(maxsize=4096)(lora_workspace_bytes)

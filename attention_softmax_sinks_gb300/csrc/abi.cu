@@ -453,7 +453,7 @@ void sink_attn_decode_shared_splits(int batch, int num_groups, int num_qo_heads,
     const long long tiles = (max_shared_pages + 7) / 8;
     const long long units = sa::shared_row_tiles(batch, num_groups, group) * num_kv_heads;
     const long long ctas = sa::shared_ctas(batch, num_groups, group, num_kv_heads, max_shared_pages, max_pages,
-                                           static_cast<int>(own_units * o < (1 << 30) ? own_units * o : 1 << 30), num_sms);
+                                           own_units * o, num_sms);
     long long n = (num_groups == 1 ? 1 : 2) * ctas / units + 2;
     if (n > tiles + 1) n = tiles + 1;
     if (static_cast<long long>(batch) * group <= 128LL * num_groups) n = 2 * (n < tiles / 2 + 1 ? n : tiles / 2 + 1);
@@ -622,8 +622,8 @@ sa_status sink_attn_decode_shared(const void* q, const void* paged_k, const void
   a.group = group;
   a.max_pages = max_pages;
   a.num_pages = num_pages;
-  a.ctas = sa::shared_ctas(batch, num_groups, group, num_kv_heads, max_shared_pages, max_pages,
-                           batch * num_kv_heads * own_splits, sm_count());
+  const long long own_ctas = static_cast<long long>(batch) * num_kv_heads * own_splits;
+  a.ctas = sa::shared_ctas(batch, num_groups, group, num_kv_heads, max_shared_pages, max_pages, own_ctas, sm_count());
   a.scale_log2 = sm_scale * kLog2e;
   a.status = status;
   a.timeout_ns = g_timeout_ns;
@@ -820,9 +820,10 @@ sa_status linear_bias(const void* x, const void* w, const void* bias, int m, int
   return sa::launch_linear(am, bm, a, sms, stream) == cudaSuccess ? SA_OK : SA_ERR_LAUNCH;
 }
 
-long long lora_workspace_bytes(int m, int k, int rank) {
-  if (m <= 0 || k <= 0 || rank <= 0 || rank > sa::kLoraMaxRank) return 0;
-  return 16LL * m * rank;  // up to four parts in fp32
+void lora_workspace_bytes(int m, int k, int rank, long long* bytes) {
+  if (!bytes) return;
+  const bool none = m <= 0 || k <= 0 || rank <= 0 || rank > sa::kLoraMaxRank;
+  *bytes = none ? 0 : 16LL * m * rank;  // up to four parts in fp32
 }
 
 sa_status lora_linear_bias(const void* x, const void* w, const void* bias, const void* lora_a, const void* lora_b,

@@ -788,7 +788,8 @@ long long shared_row_tiles(int batch, int num_groups, int group) {
   return (rows + groups * (block - 1)) / block;
 }
 
-int shared_ctas(int batch, int num_groups, int group, int hkv, int max_shared_pages, int max_pages, int own_ctas, int sms) {
+int shared_ctas(int batch, int num_groups, int group, int hkv, int max_shared_pages, int max_pages,
+                long long own_ctas, int sms) {
   // SM time (us) of the shared part, if every group's prompt is the longest: 1.28 for a tile of keys
   // of two row tiles, 0.75 of one.  Of the own parts, if they are half as long as the page table has
   // room for: three CTAs of 3 us and 35 KB per us beside one another.

@@ -36,7 +36,8 @@ struct SharedArgs {
 long long shared_row_tiles(int batch, int num_groups, int group);
 // CTAs for the shared part, so that it and the own parts (which get the other SMs) end together as
 // far as the bounds on their lengths tell.
-int shared_ctas(int batch, int num_groups, int group, int hkv, int max_shared_pages, int max_pages, int own_ctas, int sms);
+int shared_ctas(int batch, int num_groups, int group, int hkv, int max_shared_pages, int max_pages,
+                long long own_ctas, int sms);
 // Attention of every group's rows over its shared pages, into slots [0, shared_splits) (slots not
 // used: lse = -inf, the output not written; nothing for groups that share no pages).
 cudaError_t launch_shared(const CUtensorMap& kmap, const CUtensorMap& vmap, const SharedArgs& a, cudaStream_t stream);

@@ -57,7 +57,7 @@ sa_status linear_bias(const void* x, const void* w, const void* bias, int m, int
  *  lora_scale   fp32 [num_adapters] or NULL (1)
  *  adapter_idx  int32 [m], device, in any order.  An index >= num_adapters counts as none and
  *               sets SA_ERR_BOUNDS in the device status word.
- *  workspace    lora_workspace_bytes(m, k, rank) bytes of device memory, 16-byte aligned,
+ *  workspace    as many bytes of device memory as lora_workspace_bytes says, 16-byte aligned,
  *               overwritten; calls that overlap on the GPU, captured graphs among them, need
  *               workspaces of their own
  * Status codes as for linear_bias (SA_ERR_SHAPE also for rank <= 0, num_adapters out of range and
@@ -68,9 +68,9 @@ sa_status lora_linear_bias(const void* x, const void* w, const void* bias, const
                            int m, int n, int k, int rank, int num_adapters, void* workspace,
                            void* out, cudaStream_t stream);
 
-/* Bytes of workspace for lora_linear_bias (0 for sizes that it refuses or does nothing for).
- * No CUDA call. */
-long long lora_workspace_bytes(int m, int k, int rank);
+/* Bytes of workspace for lora_linear_bias into *bytes (0 for sizes that it refuses or does
+ * nothing for).  No CUDA call. */
+void lora_workspace_bytes(int m, int k, int rank, long long* bytes);
 
 #ifdef __cplusplus
 }
