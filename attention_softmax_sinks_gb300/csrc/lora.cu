@@ -402,14 +402,15 @@ __global__ void __launch_bounds__(kFewThreads, 2) lora_shrink_few_kernel(const L
 // ------------------------------------------------------------------ first product, many tokens
 constexpr int kShrinkThreads = 256;  // loads, products, plan; warps 4..7 epilogue
 constexpr int kShrinkCols = 256;     // columns of an accumulator
-constexpr int kShrinkStages = 3;
-constexpr int kShrinkStageBytes = (kBM + kShrinkCols) * kBK * 2;
+constexpr int kShrinkMaxStages = 8;
+// Three stages of all columns, or more of a tile's few adapters: one of 64 ranks (24 KB) has six.
+constexpr int kShrinkRingBytes = 3 * (kBM + kShrinkCols) * kBK * 2;
 // rows that this CTA adds up: from each part of K, together 128 rows of up to 128 ranks
 constexpr int kShrinkRecvBytes = kBM * kLoraMaxRank * 4;
-constexpr size_t kShrinkSmem = 1024 + kShrinkStages * kShrinkStageBytes + kShrinkRecvBytes + 4096;
+constexpr size_t kShrinkSmem = 1024 + kShrinkRingBytes + kShrinkRecvBytes + 4096;
 
 struct ShrinkShared {
-  uint64_t full[kShrinkStages], empty[kShrinkStages], acc_full, acc_empty, drain;
+  uint64_t full[kShrinkMaxStages], empty[kShrinkMaxStages], acc_full, acc_empty, drain;
   uint32_t tmem_base;
   int abort_flag;
   int issued;
@@ -422,14 +423,14 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
     lora_shrink_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap amap, const LoraArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  ShrinkShared& sb = *reinterpret_cast<ShrinkShared*>(tiles + kShrinkStages * kShrinkStageBytes + kShrinkRecvBytes);
+  ShrinkShared& sb = *reinterpret_cast<ShrinkShared*>(tiles + kShrinkRingBytes + kShrinkRecvBytes);
   volatile int* abort_flag = &sb.abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tile = blockIdx.z, split = blockIdx.y;
+  const int tile = blockIdx.x, split = blockIdx.y, side = blockIdx.z;
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&xmap);
     tma_prefetch_desc(&amap);
-    for (int s = 0; s < kShrinkStages; ++s) {
+    for (int s = 0; s < kShrinkMaxStages; ++s) {
       mbar_init(smem_u32(&sb.full[s]), 1);
       mbar_init(smem_u32(&sb.empty[s]), 1);
     }
@@ -450,10 +451,10 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
   const int slots = sb.plan.slots;
   const int per_pass = kShrinkCols / a.R;  // adapters side by side
   const int passes = (slots + per_pass - 1) / per_pass;
-  if (static_cast<int>(blockIdx.x) >= passes) return;  // the whole cluster, before TMEM is taken
+  if (side >= passes) return;  // the whole cluster, before TMEM is taken
   cluster_arrive_relaxed();  // waited for before the first store into another CTA
   const int owner_rows = kBM / a.splits;  // of the tile: CTA `split` adds up [split * owner_rows, ..)
-  float* recv = reinterpret_cast<float*>(tiles + kShrinkStages * kShrinkStageBytes);  // [part][R / 4][row], four each
+  float* recv = reinterpret_cast<float*>(tiles + kShrinkRingBytes);  // [part][R / 4][row], four each
   // this CTA's part of K, in steps of 64
   const int steps = (a.K + kBK - 1) / kBK;
   const int k0 = static_cast<int>(static_cast<long long>(steps) * split / a.splits);
@@ -468,18 +469,21 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
   const uint32_t tmem = sb.tmem_base;
   const uint32_t ring = smem_u32(tiles);
   const int xbytes = a.box_rows * kBK * 2;
+  // (multiples of 1 KB, as the swizzled operands need: rows in eights)
+  const int stage_bytes = kBM * kBK * 2 + min(per_pass, slots) * a.R * kBK * 2;
+  const int stages = min(kShrinkRingBytes / stage_bytes, kShrinkMaxStages);
   cluster_wait();  // every CTA of the cluster runs
 
   if (warp == 0) {
     RingPos p;
     int issued = 0;
     bool ok = true;
-    for (int pass = blockIdx.x; pass < passes && ok; pass += gridDim.x) {
+    for (int pass = side; pass < passes && ok; pass += gridDim.z) {
       const int first = pass * per_pass, n = min(per_pass, slots - first);
-      for (int ks = 0; ks < k_steps; ++ks, p.next(kShrinkStages)) {
+      for (int ks = 0; ks < k_steps; ++ks, p.next(stages)) {
         ok = p.round == 0 || wait_or_abort(smem_u32(&sb.empty[p.stage]), (p.round - 1) & 1, a.timeout_ns, abort_flag);
         if (!ok) break;
-        const uint32_t bar = smem_u32(&sb.full[p.stage]), dst = ring + p.stage * kShrinkStageBytes;
+        const uint32_t bar = smem_u32(&sb.full[p.stage]), dst = ring + p.stage * stage_bytes;
         if (elect_one()) {
           mbar_arrive_expect_tx(bar, xbytes + n * a.R * kBK * 2);
           tma_load_2d(dst, &xmap, (k0 + ks) * kBK, tile * kBM, bar, l2_policy_evict_last());
@@ -496,18 +500,18 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
     RingPos p;
     int i = 0;
     bool ok = true;
-    for (int pass = blockIdx.x; pass < passes && ok; pass += gridDim.x, ++i) {
+    for (int pass = side; pass < passes && ok; pass += gridDim.z, ++i) {
       const int n = min(per_pass, slots - pass * per_pass);
       const uint32_t idesc = idesc_bf16_kk(kBM, (n * a.R + 15) / 16 * 16);
       if (i > 0) ok = wait_or_abort(smem_u32(&sb.acc_empty), (i - 1) & 1, a.timeout_ns, abort_flag);
       if (!ok) break;
       tc_fence_after();
-      for (int ks = 0; ks < k_steps; ++ks, p.next(kShrinkStages)) {
+      for (int ks = 0; ks < k_steps; ++ks, p.next(stages)) {
         ok = wait_or_abort(smem_u32(&sb.full[p.stage]), p.round & 1, a.timeout_ns, abort_flag);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t stage = ring + p.stage * kShrinkStageBytes;
+          const uint32_t stage = ring + p.stage * stage_bytes;
           const uint64_t xd = sw128_kmajor(stage), ad = sw128_kmajor(stage + kBM * kBK * 2);
 #pragma unroll
           for (int kk = 0; kk < kBK / 16; ++kk) tc_mma_ss(tmem, xd + 2 * kk, ad + 2 * kk, idesc, (ks | kk) != 0);
@@ -528,7 +532,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
     const float scale = mine >= 0 && a.scale ? __ldg(a.scale + sb.plan.list[mine]) : 1.0f;
     const uint32_t out = dsmem_addr(smem_u32(recv + (split * (a.R / 4) * owner_rows + r % owner_rows) * 4), r / owner_rows);
     int i = 0;
-    for (int pass = blockIdx.x; pass < passes; pass += gridDim.x, ++i) {
+    for (int pass = side; pass < passes; pass += gridDim.z, ++i) {
       const int first = pass * per_pass, n = min(per_pass, slots - first);
       if (!wait_or_abort(smem_u32(&sb.acc_full), i & 1, a.timeout_ns, abort_flag)) break;
       tc_fence_after();
@@ -556,16 +560,16 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0 && *abort_flag) {  // copies still in flight land before the shared memory is released
-    for (int s = 0; s < kShrinkStages && s < sb.issued; ++s) {
-      const int last = sb.issued - 1 - ((sb.issued - 1 - s) % kShrinkStages);
-      if (!mbar_wait(smem_u32(&sb.full[s]), (last / kShrinkStages) & 1, kDrainTimeoutNs)) raise_status(a.status, kStatusTimeout);
+    for (int s = 0; s < stages && s < sb.issued; ++s) {
+      const int last = sb.issued - 1 - ((sb.issued - 1 - s) % stages);
+      if (!mbar_wait(smem_u32(&sb.full[s]), (last / stages) & 1, kDrainTimeoutNs)) raise_status(a.status, kStatusTimeout);
     }
   }
   cluster_sync();  // every part of the rows has arrived
   const int parts = a.splits;
   for (int i = threadIdx.x; i < owner_rows * (a.R / 8); i += kShrinkThreads) {
     const int r = i % owner_rows, c = i / owner_rows * 8, s = sb.slot[split * owner_rows + r];
-    if (s < 0 || s / per_pass % gridDim.x != blockIdx.x) continue;  // none, or another cluster's
+    if (s < 0 || s / per_pass % static_cast<int>(gridDim.z) != side) continue;  // none, or another cluster's
     float sum[8] = {};
     for (int p = 0; p < parts; ++p) {
       const float4* v = reinterpret_cast<const float4*>(recv) + (p * (a.R / 4) + c / 4) * owner_rows + r;
@@ -1348,7 +1352,8 @@ cudaError_t launch_lora(const LoraMaps& m, const LoraArgs& a, int sms, cudaStrea
     if (e != cudaSuccess) return e;
     // CTAs side by side: as many passes of 256 columns as a tile can have
     const int per_pass = kShrinkCols / a.R, passes = (most + per_pass - 1) / per_pass;
-    cfg.gridDim = dim3(static_cast<unsigned>(room < 1 ? 1 : room < passes ? room : passes), a.splits, a.tiles_m);
+    // (those that a tile of fewer adapters leaves without work come last)
+    cfg.gridDim = dim3(a.tiles_m, a.splits, static_cast<unsigned>(room < 1 ? 1 : room < passes ? room : passes));
     cfg.blockDim = dim3(kShrinkThreads, 1, 1);
     cfg.dynamicSmemBytes = kShrinkSmem;
     cfg.numAttrs = 2;
