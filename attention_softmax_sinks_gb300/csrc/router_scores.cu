@@ -16,11 +16,15 @@
 //  - A key is off by a few units from what it stands for.  Where the last group kept and the first
 //    dropped, or two neighbours among the chosen, or the last chosen and the first not chosen are
 //    closer than that, and not equal in logit and bias, the experts within reach of that border
-//    are compared once more in fp64, a lane for each (two tokens in a thousand for logits in 32
-//    bits, about 2 us for a warp that has one); more than 32 of them by a walk over all experts.
+//    are compared once more, a lane for each: scores by sigmoid in pairs of fp32, and where that
+//    does not settle it, or by softmax, in fp64 (one token in a thousand of 256 experts in 8 groups
+//    with logits in 32 bits); more than 32 of them by a walk over all experts in fp64.
 //
-// What bounds it: at many tokens the instructions (about 1000 per four tokens), not the logits'
-// way from memory; at few the latency of one pass.
+// What bounds it: at many tokens the instructions, some 1600 for four tokens of 256 experts, and
+// behind them the latency of the doubtful tokens, not the logits' way from memory: 32768 tokens of
+// 256 experts in fp32, 8 of them from 4 of 8 groups, take 30.8 us, 22 of them without the doubtful
+// ones, 5.2 for the bytes alone (33.5 with all of the doubtful in fp64; with 32 lanes per token 90).
+// At few tokens the latency of a launch and one pass: 64 tokens 5.9 us.
 #include <cstdint>
 
 #include "ptx.cuh"
@@ -151,6 +155,92 @@ __device__ __forceinline__ Wide least() { return {-__builtin_huge_val(), 0.0}; }
 __device__ __forceinline__ Wide merit_of(const Wide& first, const Wide& second) {
   const Wide s = wide_sum(first.hi, second.hi);
   return wide_sum(s.hi, s.lo + (first.lo + second.lo));
+}
+
+// ---- The same in pairs and triples of fp32 for scores by sigmoid: a step in fp64 takes some 100
+// cycles here, so that exp, the division and the comparisons of one token took 20 us.  A pair holds
+// a number to 2^-46 or so of its value (sum and product of two: Dekker 1971, Knuth's two-sum).
+struct Pair {
+  float hi, lo;
+};
+__device__ __forceinline__ Pair two_sum(float x, float y) {
+  const float s = __fadd_rn(x, y), z = __fsub_rn(s, x);
+  return {s, __fadd_rn(__fsub_rn(x, __fsub_rn(s, z)), __fsub_rn(y, z))};
+}
+__device__ __forceinline__ Pair quick_sum(float x, float y) {  // |x| >= |y|
+  const float s = __fadd_rn(x, y);
+  return {s, __fsub_rn(y, __fsub_rn(s, x))};
+}
+// a b + c
+__device__ __forceinline__ Pair multiply_add(const Pair& a, const Pair& b, const Pair& c) {
+  const float p = __fmul_rn(a.hi, b.hi);
+  const float e = __fmaf_rn(a.lo, b.hi, __fmaf_rn(a.hi, b.lo, __fmaf_rn(a.hi, b.hi, -p)));
+  const Pair s = two_sum(p, c.hi);
+  return quick_sum(s.hi, __fadd_rn(s.lo, __fadd_rn(e, c.lo)));
+}
+__host__ __device__ constexpr Pair pair_of(double v) { return {static_cast<float>(v), static_cast<float>(v - static_cast<float>(v))}; }
+
+// 1 / (1 + e^-x), off by less than 2^-43: e^-x = 2^n e^r with n ln 2 + r = -x, |r| <= 0.35, and
+// the power series of e^r up to r^12 / 12! (2^-47 is left out), from r^8 on in fp32 (2^-27 of the
+// sum, so 2^-50).  Below x = -60 the result is off by its value, 2^-86.
+__device__ __forceinline__ Pair sigmoid_pair(float x) {
+  const float y = fminf(fmaxf(-x, -60.0f), 60.0f);
+  const float n = rintf(y * kLog2e);
+  constexpr double kLn2 = 0.69314718055994530942, kRough = 45426.0 / 65536.0;  // n kRough is exact
+  constexpr Pair rest = pair_of(kLn2 - kRough);
+  const float r0 = __fmaf_rn(-n, static_cast<float>(kRough), y);  // exact as well
+  const float q = __fmul_rn(n, rest.hi);
+  const Pair s = two_sum(r0, -q);
+  const Pair r = quick_sum(s.hi, __fsub_rn(s.lo, __fmaf_rn(n, rest.lo, __fmaf_rn(n, rest.hi, -q))));
+  constexpr double c3 = 0.5 / 3, c4 = c3 / 4, c5 = c4 / 5, c6 = c5 / 6, c7 = c6 / 7, c8 = c7 / 8, c9 = c8 / 9, c10 = c9 / 10,
+                   c11 = c10 / 11, c12 = c11 / 12;
+  float tail = __fmaf_rn(static_cast<float>(c12), r.hi, static_cast<float>(c11));
+  tail = __fmaf_rn(tail, r.hi, static_cast<float>(c10));
+  tail = __fmaf_rn(tail, r.hi, static_cast<float>(c9));
+  tail = __fmaf_rn(tail, r.hi, static_cast<float>(c8));
+  constexpr Pair p3 = pair_of(c3), p4 = pair_of(c4), p5 = pair_of(c5), p6 = pair_of(c6), p7 = pair_of(c7);
+  Pair e = multiply_add({tail, 0.0f}, r, p7);
+  e = multiply_add(e, r, p6);
+  e = multiply_add(e, r, p5);
+  e = multiply_add(e, r, p4);
+  e = multiply_add(e, r, p3);
+  e = multiply_add(e, r, {0.5f, 0.0f});
+  e = multiply_add(e, r, {1.0f, 0.0f});
+  e = multiply_add(e, r, {1.0f, 0.0f});
+  const float scale = __int_as_float((static_cast<int>(n) + 127) << 23);
+  const Pair u = two_sum(1.0f, e.hi * scale);
+  const Pair d = quick_sum(u.hi, __fmaf_rn(e.lo, scale, u.lo));
+  const float inv = __frcp_rn(d.hi);  // one step of Newton's
+  return quick_sum(inv, __fmul_rn(inv, __fmaf_rn(-d.lo, inv, __fmaf_rn(-d.hi, inv, 1.0f))));
+}
+
+// A number as a sum of three, each at most half a step of the one before: s + bias, whatever the
+// bias's size, and the sum of two such.
+struct Triple {
+  float v0, v1, v2;
+};
+__device__ __forceinline__ Triple triple_of(float x0, float x1, float x2) {
+  const Pair a = two_sum(x1, x2), b = two_sum(x0, a.hi), c = two_sum(b.lo, a.lo);
+  return {b.hi, c.hi, c.lo};
+}
+__device__ __forceinline__ Triple triple_of(const Pair& s, float bias) {
+  const Pair a = two_sum(bias, s.hi);
+  return triple_of(a.hi, a.lo, s.lo);
+}
+__device__ __forceinline__ Triple triple_sum(const Triple& a, const Triple& b) {
+  const Pair s = two_sum(a.v0, b.v0), m = two_sum(a.v1, b.v1), n = two_sum(s.lo, m.hi);
+  return triple_of(s.hi, n.hi, __fadd_rn(n.lo, __fadd_rn(m.lo, __fadd_rn(a.v2, b.v2))));
+}
+__device__ __forceinline__ Triple triple_from(const Triple& v, int lane) {
+  return {__shfl_sync(kFull, v.v0, lane), __shfl_sync(kFull, v.v1, lane), __shfl_sync(kFull, v.v2, lane)};
+}
+// v - w, and whether its sign is certain: v and w are off by 2^-42 at most, the difference of the
+// second terms by 2^-24 of itself (that of the first ones is exact where they are near).
+__device__ __forceinline__ float difference(const Triple& v, const Triple& w, bool& certain) {
+  const float d1 = __fsub_rn(v.v1, w.v1);
+  const float d = __fadd_rn(__fadd_rn(__fsub_rn(v.v0, w.v0), d1), __fsub_rn(v.v2, w.v2));
+  certain = fabsf(d) > fmaf(fabsf(d1), 0x1p-20f, 0x1p-40f);  // (not where something is not a number)
+  return d;
 }
 
 struct WarpScratch {
@@ -324,6 +414,7 @@ __device__ __noinline__ void settle(const RouterScoresArgs& a, WarpScratch& ws, 
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int e = lane + 32 * i;
+    if (e < E) ws.key[1][e] = __float_as_uint(x[i]);
     if (e < E)  // 0 stands for experts of other groups here
       ws.key[0][e] = max(fixed_point<kSigmoid, kScored>(x[i], ref, unit, unit * inv_sum, kScored ? bias_key[e] : 0.0f), 1u);
   }
@@ -345,37 +436,55 @@ __device__ __noinline__ void settle(const RouterScoresArgs& a, WarpScratch& ws, 
     const int n = list_candidates(ws, E, [&](int e) { return below_by(ws.second[e / size], kNear); });
     walk = n > 32;
     if (!walk) {
-      double top, sum;
-      exact_sum<kSigmoid>(a, t, true, top, sum);
       const int e = lane < n ? ws.list[lane] : 0;
-      const Wide v = exact_value<kSigmoid>(a, t, e, top, sum, true);
-      const Order mine = order_of(v);
-      const int group = lane < n ? e / size : -1;
-      int first = -1, second = -1;  // the lanes with the two largest of group `lane`
-      Order of_first = order_of(least()), of_second = of_first;
-      for (int i = 0; i < n; ++i) {
-        const Order w = order_from(mine, i);
-        if (__shfl_sync(kFull, group, i) == lane) {
-          if (first < 0 || above(w, of_first)) {
-            second = first;
-            of_second = of_first;
-            first = i;
-            of_first = w;
-          } else if (second < 0 || above(w, of_second)) {
-            second = i;
-            of_second = w;
+      unsigned kept = 0;
+      // scores by sigmoid, two candidates in every group: lanes 2 g and 2 g + 1
+      bool sure = kSigmoid && size > 1 && n == 2 * a.num_groups;
+      if (sure) {
+        const Triple v = triple_of(sigmoid_pair(__uint_as_float(ws.key[1][e])), bias_of(a, e));
+        const Triple merit = triple_sum(triple_from(v, 2 * lane & 31), triple_from(v, (2 * lane & 31) + 1));
+        int before = 0;
+        for (int g = 0; g < a.num_groups; ++g) {
+          bool certain;
+          const float d = difference(triple_from(merit, g), merit, certain);
+          before += d > 0.0f;
+          if (!certain && g != lane && lane < a.num_groups) sure = false;
+        }
+        kept = __ballot_sync(kFull, lane < a.num_groups && before < a.top_groups);
+        sure = __all_sync(kFull, sure);
+      }
+      if (!sure) {
+        double top, sum;
+        exact_sum<kSigmoid>(a, t, true, top, sum);
+        const Wide v = exact_value<kSigmoid>(a, t, e, top, sum, true);
+        const Order mine = order_of(v);
+        const int group = lane < n ? e / size : -1;
+        int first = -1, second = -1;  // the lanes with the two largest of group `lane`
+        Order of_first = order_of(least()), of_second = of_first;
+        for (int i = 0; i < n; ++i) {
+          const Order w = order_from(mine, i);
+          if (__shfl_sync(kFull, group, i) == lane) {
+            if (first < 0 || above(w, of_first)) {
+              second = first;
+              of_second = of_first;
+              first = i;
+              of_first = w;
+            } else if (second < 0 || above(w, of_second)) {
+              second = i;
+              of_second = w;
+            }
           }
         }
+        const Wide v1 = {__shfl_sync(kFull, v.hi, max(first, 0)), __shfl_sync(kFull, v.lo, max(first, 0))};
+        const Wide v2 = {__shfl_sync(kFull, v.hi, max(second, 0)), __shfl_sync(kFull, v.lo, max(second, 0))};
+        const Order merit = order_of(size > 1 ? merit_of(v1, v2) : v1);
+        int before = 0;
+        for (int g = 0; g < a.num_groups; ++g) {
+          const Order w = order_from(merit, g);
+          before += above(w, merit) || (g < lane && !above(merit, w));
+        }
+        kept = __ballot_sync(kFull, lane < a.num_groups && before < a.top_groups);
       }
-      const Wide v1 = {__shfl_sync(kFull, v.hi, max(first, 0)), __shfl_sync(kFull, v.lo, max(first, 0))};
-      const Wide v2 = {__shfl_sync(kFull, v.hi, max(second, 0)), __shfl_sync(kFull, v.lo, max(second, 0))};
-      const Order merit = order_of(size > 1 ? merit_of(v1, v2) : v1);
-      int before = 0;
-      for (int g = 0; g < a.num_groups; ++g) {
-        const Order w = order_from(merit, g);
-        before += above(w, merit) || (g < lane && !above(merit, w));
-      }
-      const unsigned kept = __ballot_sync(kFull, lane < a.num_groups && before < a.top_groups);
       for (int e2 = lane; e2 < E; e2 += 32)
         if (!(kept >> (e2 / size) & 1)) ws.key[0][e2] = 0;
       __syncwarp();
@@ -399,14 +508,31 @@ __device__ __noinline__ void settle(const RouterScoresArgs& a, WarpScratch& ws, 
     walk = n > 32;
     if (!walk) {
       const bool scored = a.bias != nullptr;  // else the logits' order is the answer
-      double top, sum;
-      exact_sum<kSigmoid>(a, t, scored, top, sum);
       const int e = lane < n ? ws.list[lane] : 0;
-      const Order mine = order_of(exact_value<kSigmoid>(a, t, e, top, sum, scored));
       int rank = 0;
-      for (int i = 0; i < n; ++i) {
-        const Order w = order_from(mine, i);
-        rank += above(w, mine) || (i < lane && !above(mine, w));  // candidates are in expert order
+      bool sure = kSigmoid && scored;
+      if (sure) {
+        const float logit = __uint_as_float(ws.key[1][e]), bias = bias_of(a, e);
+        const Triple mine = triple_of(sigmoid_pair(logit), bias);
+        for (int i = 0; i < n; ++i) {
+          bool certain;
+          const float d = difference(triple_from(mine, i), mine, certain);
+          const float its_logit = __shfl_sync(kFull, logit, i), its_bias = __shfl_sync(kFull, bias, i);
+          const bool same = its_logit == logit && its_bias == bias;
+          rank += same ? i < lane : d > 0.0f;
+          if (!certain && !same && lane < n) sure = false;
+        }
+        sure = __all_sync(kFull, sure);
+      }
+      if (!sure) {
+        double top, sum;
+        exact_sum<kSigmoid>(a, t, scored, top, sum);
+        const Order mine = order_of(exact_value<kSigmoid>(a, t, e, top, sum, scored));
+        rank = 0;
+        for (int i = 0; i < n; ++i) {
+          const Order w = order_from(mine, i);
+          rank += above(w, mine) || (i < lane && !above(mine, w));  // candidates are in expert order
+        }
       }
       if (lane >= n) rank = 32;
 #pragma unroll
