@@ -158,7 +158,7 @@ def test_outputs_workspace_and_stream():
     import attention_softmax_sinks_gb300 as sa
     a = make(140, 512, 264, 16, 9, mixed(140, 9))
     want = call(a)
-    need = sa.load_library().lora_workspace_bytes(140, 512, 16)
+    need = sa.lora_workspace_bytes(140, 512, 16)
     ws = torch.full((need + 64,), 255, dtype=torch.uint8, device="cuda")
     out = torch.full((150, 264), 7.0, dtype=torch.bfloat16, device="cuda")
     s = torch.cuda.Stream()

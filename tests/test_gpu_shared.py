@@ -255,3 +255,15 @@ def test_shorter_than_its_prompt():
     assert sa.sink_attn_device_status(True) == 5
     a["kv_lens"][1] = 64  # what it attends to: the shared pages and its sink
     check(a, out, lse)
+
+
+@pytest.mark.parametrize("groups", [[(5, 61)], [(24, 100)], [(3, 40), (30, 9)], [(2, 300), (1, 7), (2, 130)], [(1, 3)], [(9, 8), (9, 8)]])
+@pytest.mark.parametrize("hq,hkv", [(64, 8), (8, 1), (6, 6)])
+def test_any_number_of_slots(groups, hq, hkv):
+    # units whose parts end with a run and across runs, tiles of keys in turn and not, with slots
+    # that nothing goes into: whatever the workspace held before
+    n = sum(c for c, _ in groups)
+    a = make(groups, [1 + 13 * i % 50 for i in range(n)], hq, hkv, seed=hq)
+    for slots in (1, 2, 3, 4, 5, 6, 7, 8, 11, 14, 15, 20, 39, 64):
+        ws = (torch.full((n, slots + 1, hq, DIM), NAN, device="cuda"), torch.full((n, slots + 1, hq), NAN, device="cuda"))
+        check(a, *call(a, splits=(slots, 1), workspace=ws))
