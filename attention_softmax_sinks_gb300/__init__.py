@@ -348,9 +348,9 @@ def sink_attn_decode_shared(q, paged_k, paged_v, page_table, kv_lens, sinks, gro
     kv_lens [B] int32 (whole sequences), sinks [Hq] fp32.  group_offsets [G + 1] int32: group g
     is sequences [group_offsets[g], group_offsets[g + 1]); shared_pages [G] int32: the pages that
     begin the page tables of all its sequences, at most max_shared_pages.
-    splits: (shared, own) along the keys, default sink_attn_decode_shared_splits.  workspace:
-    (partial_o [B, shared + own, Hq, 64], partial_lse [B, shared + own, Hq]) fp32, allocated when
-    not given.  Returns (out [B, Hq, 64] bf16, lse [B, Hq] fp32 or None)."""
+    splits: (shared, own) along the keys, default sink_attn_decode_shared_splits; (0, 1): every
+    sequence reads all its pages for itself, in one launch.  workspace: (partial_o [B, shared + own,
+    Hq, 64], partial_lse [B, shared + own, Hq]) fp32, allocated when not given, not used for (0, 1).  Returns (out [B, Hq, 64] bf16, lse [B, Hq] fp32 or None)."""
     b, hq, d = _shape(q, "q", 3)
     num_pages, hkv, page_size, kd = _shape(paged_k, "paged_k", 4)
     groups = _shape(shared_pages, "shared_pages", 1)[0]
@@ -366,13 +366,15 @@ def sink_attn_decode_shared(q, paged_k, paged_v, page_table, kv_lens, sinks, gro
     if splits is None:
         splits = _shared_splits(b, groups, hq, hkv, most, max_pages, _sm_count(di))
     ss, so = (_c_int(int(v), "splits") for v in splits)
-    if not (1 <= ss <= 255 and 1 <= so <= 256 - ss):  # no memory for what the call refuses
-        raise ValueError(f"splits must be at least 1 each and at most 256 together, got {(ss, so)}")
-    scratch, rows = None, b * (ss + so) * hq
-    if workspace is None:
-        scratch = _Scratch(4 * rows * (d + 1), di, stream) if rows else None
-        po = scratch.ptr if rows else 0
-        pl = po + 4 * rows * d
+    if (ss, so) != (0, 1) and not (1 <= ss <= 255 and 1 <= so <= 256 - ss):  # no memory for what the call refuses
+        raise ValueError(f"splits must be at least 1 each and at most 256 together, or (0, 1), got {(ss, so)}")
+    scratch, rows, po, pl = None, b * (ss + so) * hq, 0, 0
+    if ss == 0:
+        pass  # every sequence by itself, in one launch
+    elif workspace is None:
+        if rows:
+            scratch = _Scratch(4 * rows * (d + 1), di, stream)
+            po, pl = scratch.ptr, scratch.ptr + 4 * rows * d
     else:
         po = _out(workspace[0], "workspace[0]", torch.float32, (b, ss + so, hq, d), di).data_ptr()
         pl = _out(workspace[1], "workspace[1]", torch.float32, (b, ss + so, hq), di).data_ptr()

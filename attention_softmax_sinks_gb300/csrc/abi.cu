@@ -439,6 +439,22 @@ void sink_attn_decode_shared_splits(int batch, int num_groups, int num_qo_heads,
   if (batch > 0 && num_groups > 0 && num_kv_heads > 0 && num_qo_heads >= num_kv_heads && max_shared_pages >= 0 &&
       max_pages > 0) {
     if (num_sms <= 0) num_sms = 152;
+    // Few pages: every sequence by itself, one launch, if that is estimated to be faster.  By itself:
+    // 5.5 us and, for 1000 pages of 8 KV heads, 4.5, or 9 where more than 8 sequences read the same
+    // ones (5 if they are short, too); together: three launches and the run along the prompt, whose
+    // groups follow one another.  (us by itself / together, 64/8 heads, 64 tokens of their own: 4
+    // sequences that share 2048 tokens 8.3 / 11.9, 4096 tokens 10.5 / 12.8, 8192 tokens 14.8 / 14.5;
+    // 16 that share 256 tokens 6.1 / 11.8, 1024 tokens 15.4 / 12.3; 64 in 4 groups 256 tokens 7.5 /
+    // 13.5, 1024 tokens 30 / 17.6; 4 in 4 groups 16384 tokens 22 / 35.)
+    const double kpages = 1e-3 / 8 * batch * num_kv_heads * max_pages;
+    const double alone = 5.5 + kpages * (batch <= 8LL * num_groups ? 4.5 : max_pages < 32 ? 5.0 : 9.0);
+    const double side = num_groups * (num_kv_heads / 8.0);
+    const double together = 10.5 + (batch < 64 ? 0.07 * batch : 4.5) + 6.5e-3 * max_shared_pages * (side > 1.0 ? side : 1.0);
+    if (alone < together) {
+      if (shared_splits) *shared_splits = 0;
+      if (own_splits) *own_splits = 1;
+      return;
+    }
     // own part: a CTA per SM, at least 16 pages each, at most 8 splits
     const long long own_pages = max_pages > max_shared_pages ? max_pages - max_shared_pages : 1;
     const long long own_units = static_cast<long long>(batch) * num_kv_heads;
@@ -583,7 +599,8 @@ sa_status sink_attn_decode_shared(const void* q, const void* paged_k, const void
                                   cudaStream_t stream) {
   if (batch < 0 || batch > 65535 || num_groups <= 0 || num_groups > 65535 || max_pages <= 0 || num_pages <= 0) return SA_ERR_SHAPE;
   if (max_shared_pages < 0 || max_shared_pages > max_pages || max_pages > (1 << 26)) return SA_ERR_SHAPE;
-  if (shared_splits < 1 || own_splits < 1 || shared_splits > 256 || own_splits > 256 || shared_splits + own_splits > 256)
+  if (shared_splits < 0 || own_splits < 1 || shared_splits > 256 || own_splits > 256 || shared_splits + own_splits > 256 ||
+      (shared_splits == 0 && own_splits > 1))
     return SA_ERR_SHAPE;
   if (sa_status s = check_heads(num_qo_heads, num_kv_heads, head_dim)) return s;
   if (page_size != sa::kPageSize) return SA_ERR_UNSUPPORTED;
@@ -593,8 +610,8 @@ sa_status sink_attn_decode_shared(const void* q, const void* paged_k, const void
   if (static_cast<long long>(num_pages) * num_kv_heads * page_size >= (1LL << 31) - 16) return SA_ERR_SHAPE;
   if (static_cast<long long>(batch) * num_qo_heads >= (1LL << 31)) return SA_ERR_SHAPE;
   if (batch == 0) return SA_OK;
-  if (!q || !paged_k || !paged_v || !page_table || !kv_lens || !sinks || !group_offsets || !shared_pages ||
-      !partial_o || !partial_lse || !out)
+  if (!q || !paged_k || !paged_v || !page_table || !kv_lens || !sinks || !group_offsets || !shared_pages || !out ||
+      (shared_splits > 0 && (!partial_o || !partial_lse)))
     return SA_ERR_NULL;
   if (!aligned16(q) || !aligned16(paged_k) || !aligned16(paged_v) || !aligned16(out) || !aligned16(partial_o) ||
       !aligned4(page_table) || !aligned4(kv_lens) || !aligned4(sinks) || !aligned4(group_offsets) ||
@@ -610,6 +627,28 @@ sa_status sink_attn_decode_shared(const void* q, const void* paged_k, const void
   if (sa_status s = map_pages(&km, paged_k, num_pages, num_kv_heads)) return s;
   if (sa_status s = map_pages(&vm, paged_v, num_pages, num_kv_heads)) return s;
   const sa::SharedPlan plan{group_offsets, shared_pages, num_groups, max_shared_pages, shared_splits, own_splits};
+  sa::DecodeArgs d{};
+  d.q = q;
+  d.page_table = page_table;
+  d.kv_lens = kv_lens;
+  d.sinks = sinks;
+  d.batch = batch;
+  d.hq = num_qo_heads;
+  d.hkv = num_kv_heads;
+  d.group = group;
+  d.max_pages = max_pages;
+  d.num_pages = num_pages;
+  d.num_splits = own_splits;
+  d.cluster = 1;
+  d.scale_log2 = sm_scale * kLog2e;
+  d.status = status;
+  d.timeout_ns = g_timeout_ns;
+  if (shared_splits == 0) {  // every sequence by itself
+    d.out = out;
+    d.lse = lse;
+    d.cluster = cluster_split(batch * num_kv_heads, max_pages);
+    return sa::launch_decode(km, vm, d, sa::DecodeRopeArgs{}, stream, &plan) == cudaSuccess ? SA_OK : SA_ERR_LAUNCH;
+  }
   sa::SharedArgs a{};
   a.q = static_cast<const uint16_t*>(q);
   a.page_table = page_table;
@@ -624,28 +663,12 @@ sa_status sink_attn_decode_shared(const void* q, const void* paged_k, const void
   a.num_pages = num_pages;
   const long long own_ctas = static_cast<long long>(batch) * num_kv_heads * own_splits;
   a.ctas = sa::shared_ctas(batch, num_groups, group, num_kv_heads, max_shared_pages, max_pages, own_ctas, sm_count());
-  a.scale_log2 = sm_scale * kLog2e;
+  a.scale_log2 = d.scale_log2;
   a.status = status;
   a.timeout_ns = g_timeout_ns;
   if (sa::launch_shared(km, vm, a, stream) != cudaSuccess) return SA_ERR_LAUNCH;
-  sa::DecodeArgs d{};
-  d.q = q;
-  d.page_table = page_table;
-  d.kv_lens = kv_lens;
-  d.sinks = sinks;
   d.out = partial_o;
   d.lse = partial_lse;
-  d.batch = batch;
-  d.hq = num_qo_heads;
-  d.hkv = num_kv_heads;
-  d.group = group;
-  d.max_pages = max_pages;
-  d.num_pages = num_pages;
-  d.num_splits = own_splits;
-  d.cluster = 1;
-  d.scale_log2 = a.scale_log2;
-  d.status = status;
-  d.timeout_ns = g_timeout_ns;
   if (sa::launch_decode_own(km, vm, d, plan, stream) != cudaSuccess) return SA_ERR_LAUNCH;
   const sa::MergeArgs m{partial_o, partial_lse, out, lse, batch, shared_splits + own_splits, num_qo_heads};
   return sa::launch_shared_merge(m, stream) == cudaSuccess ? SA_OK : SA_ERR_LAUNCH;

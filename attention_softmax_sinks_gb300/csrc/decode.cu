@@ -158,16 +158,19 @@ __device__ __noinline__ int own_first_page(const SharedPlan& plan, int b, int ma
   return good ? pages : 0;
 }
 
-// kShared: the own parts of a batch that shares prompts.  The pages before own_first_page are left
+// kPlan 2: a batch that shares prompts, each sequence by itself: as without a plan, which is only
+// looked over (4 sequences that share 2048 tokens: 8.4 us; shared part, own parts and merge 11.9).
+// kPlan 1: the own parts of a batch that shares prompts.  The pages before own_first_page are left
 // to the kernel launched before this one (shared.cu), which let this one start only when every
 // earlier kernel had completed: nothing is waited for here except, by the grid's last CTA at its
 // end, that kernel itself, so that what follows this grid follows both.
-template <int NT, bool kRope, bool kShared>
+template <int NT, bool kRope, int kPlan>
 __global__ void __launch_bounds__(kWarps * 32)
     sink_decode_kernel(const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap, const DecodeArgs a,
                        const DecodeRopeArgs rope, const SharedPlan plan) {
   static_assert(sizeof(MergeArea<NT>) <= kRingBytes, "the merge area must fit in the ring");
+  constexpr bool kShared = kPlan == 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -285,6 +288,18 @@ __global__ void __launch_bounds__(kWarps * 32)
     if (lane == 0)
       for (int jj = 0; jj < issued; ++jj) issue(jj, first_ids[jj]);
   }
+  // while these are on their way: is the plan one?  (the groups shared out among the sequences)
+  if (kPlan == 2 && split == 0 && kvh == 0) {
+    bool bad = threadIdx.x == 0 && kv_len < own_first_page(plan, b, a.max_pages, a.status) * kPageSize;
+    if (warp == 1)
+      for (long long g = b * 32LL + lane; g < plan.num_groups; g += a.batch * 32LL) {
+        const int first = __ldg(plan.group_offsets + g), end = __ldg(plan.group_offsets + g + 1), pages = __ldg(plan.shared_pages + g);
+        bad |= first < 0 || end < first || end > a.batch || pages < 0 || pages > plan.max_shared_pages ||
+               (g == 0 && first != 0) || (g + 1 == plan.num_groups && end != a.batch);
+      }
+    if (bad) raise_status(a.status, kStatusBadLen);
+    __syncwarp();
+  }
 
   // Q^T fragments (B operand of S^T = K Q^T): lane holds head (lane/4) of each
   // 8-wide tile, dims kk*16 + 2*(lane%4) + {0,1} and +8.
@@ -369,7 +384,7 @@ __global__ void __launch_bounds__(kWarps * 32)
       for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(sc[nt], a0, a1, a2, a3, qf[nt][kk][0], qf[nt][kk][1]);
     }
   };
-  // O^T += V^T P^T for the page in ring slot `slot` (64 dims x 8 heads per tile); kShared: whose
+  // O^T += V^T P^T for the page in ring slot `slot` (64 dims x 8 heads per tile); with a plan: whose
   // first `valid` tokens exist (what the last page holds behind them, possibly not finite, has
   // weight zero and is dropped before it is multiplied)
   auto accumulate = [&](int slot, const uint32_t (&pt)[NT][2], int valid) {
@@ -380,7 +395,7 @@ __global__ void __launch_bounds__(kWarps * 32)
       const int chunk = mt * 2 + ((lane >> 3) & 1);
       uint32_t a0, a1, a2, a3;
       ldsm_x4_trans(vb + tok * 128 + ((chunk ^ (tok & 7)) << 4), a0, a1, a2, a3);
-      if constexpr (kShared) {
+      if constexpr (kPlan != 0) {
         if (valid < kPageSize) {  // the lane holds tokens t, t + 1 (a0, a1) and t + 8, t + 9 (a2, a3)
           const int t = 2 * (lane & 3);
           const uint32_t lo = (t < valid ? 0xFFFFu : 0u) | (t + 1 < valid ? 0xFFFF0000u : 0u);
@@ -603,7 +618,7 @@ __global__ void __launch_bounds__(kWarps * 32)
 // first call: the cache is filled under a mutex.
 template <typename Kern>
 int cluster16_capacity(Kern kern, int nt_index, cudaStream_t stream) {
-  static int known[64][4] = {};  // 0 unknown, else 1 + the number of resident clusters
+  static int known[64][6] = {};  // 0 unknown, else 1 + the number of resident clusters
   static std::mutex known_mutex;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
@@ -634,10 +649,11 @@ int cluster16_capacity(Kern kern, int nt_index, cudaStream_t stream) {
 }
 
 cudaError_t launch_decode(const CUtensorMap& kmap, const CUtensorMap& vmap, const DecodeArgs& args,
-                          const DecodeRopeArgs& rope, cudaStream_t stream) {
+                          const DecodeRopeArgs& rope, cudaStream_t stream, const SharedPlan* plan) {
   const size_t smem = decode_smem_bytes();
-  auto kern = rope.table ? (args.group <= 8 ? sink_decode_kernel<1, true, false> : sink_decode_kernel<2, true, false>)
-                         : (args.group <= 8 ? sink_decode_kernel<1, false, false> : sink_decode_kernel<2, false, false>);
+  auto kern = rope.table ? (args.group <= 8 ? sink_decode_kernel<1, true, 0> : sink_decode_kernel<2, true, 0>)
+              : plan     ? (args.group <= 8 ? sink_decode_kernel<1, false, 2> : sink_decode_kernel<2, false, 2>)
+                         : (args.group <= 8 ? sink_decode_kernel<1, false, 0> : sink_decode_kernel<2, false, 0>);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   DecodeArgs a = args;
@@ -645,7 +661,7 @@ cudaError_t launch_decode(const CUtensorMap& kmap, const CUtensorMap& vmap, cons
   // KV head)); beyond that, waiting clusters cost more than the larger split saves
   if (a.cluster > 8 &&
       static_cast<long long>(a.batch) * a.hkv >
-          cluster16_capacity(kern, (args.group <= 8 ? 0 : 1) + (rope.table ? 2 : 0), stream))
+          cluster16_capacity(kern, (args.group <= 8 ? 0 : 1) + (rope.table ? 2 : plan ? 4 : 0), stream))
     a.cluster = 8;
   const bool clustered = a.cluster > 1;
   const dim3 grid(clustered ? a.cluster : a.num_splits, a.hkv, a.batch);
@@ -665,7 +681,7 @@ cudaError_t launch_decode(const CUtensorMap& kmap, const CUtensorMap& vmap, cons
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = clustered ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, kern, kmap, vmap, a, rope, SharedPlan{});
+  e = cudaLaunchKernelEx(&cfg, kern, kmap, vmap, a, rope, plan ? *plan : SharedPlan{});
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
@@ -674,7 +690,7 @@ cudaError_t launch_decode_own(const CUtensorMap& kmap, const CUtensorMap& vmap, 
                               const SharedPlan& plan, cudaStream_t stream) {
   const size_t smem = decode_smem_bytes();
   const int tiles = a.group <= 8 ? 0 : 1;
-  auto kern = tiles == 0 ? sink_decode_kernel<1, false, true> : sink_decode_kernel<2, false, true>;
+  auto kern = tiles == 0 ? sink_decode_kernel<1, false, 1> : sink_decode_kernel<2, false, 1>;
   // the shared-memory opt-in, once per device and kernel (host threads may race here)
   static std::atomic<bool> done[64][2];
   int dev = 0;

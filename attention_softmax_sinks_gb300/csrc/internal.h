@@ -63,8 +63,10 @@ struct PrefillRopeArgs {
 };
 
 // Tensor maps (TMA descriptors) built on the host by abi.cu.
+struct SharedPlan;
+// plan: of a batch that shares prompts, looked over only (null: none; not with rope)
 cudaError_t launch_decode(const CUtensorMap& kmap, const CUtensorMap& vmap, const DecodeArgs& a,
-                          const DecodeRopeArgs& rope, cudaStream_t stream);
+                          const DecodeRopeArgs& rope, cudaStream_t stream, const SharedPlan* plan = nullptr);
 cudaError_t launch_merge(const MergeArgs& a, cudaStream_t stream);
 // qpmap: Q in boxes of (128 / group tokens, group heads), used for packed short sequences.
 // omap: the output [T, Hq, 64] mapped like qmap (boxes of 128 tokens x 1 head); full query

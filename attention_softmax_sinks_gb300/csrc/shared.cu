@@ -41,8 +41,10 @@
 // beside the own parts on the others; each sequence by itself would read 64 times as much, 4.3 GB).
 // A batch whose own parts are longer than its prompts is bound by memory: 512 sequences in 8 groups,
 // 1.1 GB, take 204 us, 5.5 TB/s.  Few short prompts are bound by latency: 4 sequences that share 2048
-// tokens 11.9 us, of which 2.6 go by before the first part begins and 2.5 in the merge.
-// Kept out, as slower: all SMs for both kernels (37 sequences in 5 groups 33 us against 29), units dealt
+// tokens 11.9 us, of which 2.6 go by before the first part begins and 2.5 in the merge; such batches
+// are left to one launch that reads every sequence's pages (8.4 us).
+// Kept out, as slower: units of up to 64 rows twice in a tile, each copy with half of a tile's keys
+// (4 x 2048 13.1 us, 37 in 5 groups 31.5); all SMs for both kernels (37 sequences in 5 groups 33 us against 29), units dealt
 // out whole (211 us against 203 for 512 sequences), every role walking along the run for itself (its
 // registers spilled: a tile of keys took 1.5 us).
 #include <atomic>

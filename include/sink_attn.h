@@ -147,19 +147,21 @@ sa_status sink_attn_decode(const void* q, const void* paged_k, const void* paged
  *  shared_pages int32 [num_groups], device: the first shared_pages[g] entries of the page
  *               tables of group g's sequences are the same (those of its first sequence are
  *               read); 0 <= shared_pages[g] <= max_shared_pages, and every sequence of the
- *               group is at least 16 shared_pages[g] tokens long (a shorter one attends to the
- *               shared pages and its sink, and SA_ERR_BOUNDS is recorded).  A page that is
- *               shared only in part belongs to the own ones.
+ *               group is at least 16 shared_pages[g] tokens long (a shorter one's result is
+ *               undefined, and SA_ERR_BOUNDS is recorded).  A page that is shared only in part
+ *               belongs to the own ones.
  *  max_shared_pages: at most max_pages
  *  shared_splits, own_splits >= 1, together at most 256: along the keys of each part; see
- *               sink_attn_decode_shared_splits
+ *               sink_attn_decode_shared_splits.  0 and 1: every sequence reads all its pages
+ *               for itself, in one launch (faster for few pages); partial_o and partial_lse are
+ *               not used then and may be NULL.
  *  partial_o    fp32 [batch, shared_splits + own_splits, num_qo_heads, head_dim], 16-byte
  *               aligned, partial_lse fp32 [batch, shared_splits + own_splits, num_qo_heads]:
  *               the caller's workspace, overwritten.  Calls that overlap on the GPU, captured
  *               graphs among them, need workspaces of their own.
  * A plan that breaks its bounds sets SA_ERR_BOUNDS in the device status word, and the results
  * of the sequences it concerns are undefined; keys of a page id outside [0, num_pages) read as
- * zeros (shared) or are skipped (own).  What the last page holds behind kv_lens is never used,
+ * zeros (shared) or are skipped (own, or with shared_splits 0).  What the last page holds behind kv_lens is never used,
  * finite or not.
  */
 sa_status sink_attn_decode_shared(const void* q, const void* paged_k, const void* paged_v,
@@ -173,7 +175,8 @@ sa_status sink_attn_decode_shared(const void* q, const void* paged_k, const void
                                   cudaStream_t stream);
 
 /* Host-only helper: split counts for sink_attn_decode_shared from what the host knows of the
- * batch (bounds: max_shared_pages, and max_pages of whole sequences).  num_sms 0: 152.  No CUDA call. */
+ * batch (bounds: max_shared_pages, and max_pages of whole sequences); 0 and 1 for few pages.
+ * num_sms 0: 152.  No CUDA call. */
 void sink_attn_decode_shared_splits(int batch, int num_groups, int num_qo_heads, int num_kv_heads,
                                     int max_shared_pages, int max_pages, int num_sms,
                                     int* shared_splits, int* own_splits);

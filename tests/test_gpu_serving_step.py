@@ -66,6 +66,7 @@ def same(a, b):
 BATCHES = {
     "three groups": ([(9, 6), (14, 17), (1, 0)], [1 + 37 * i % 300 for i in range(24)]),
     "one token, one sequence": ([(1, 3)], [1]),
+    "one long prompt": ([(40, 300)], [1 + 29 * i % 200 for i in range(40)]),
     "one prompt": ([(70, 40)], [1 + 11 * i % 90 for i in range(70)]),
 }
 

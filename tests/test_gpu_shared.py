@@ -116,7 +116,8 @@ CASES = {
 def test_shared_decode(name):
     groups, own, hq, hkv, splits = CASES[name]
     a = make(groups, own, hq, hkv, seed=len(name))
-    check(a, *call(a, splits=splits))
+    for s in {splits, (5, 2), (0, 1)}:  # .. and every sequence by itself
+        check(a, *call(a, splits=s))
 
 
 def test_many_groups():
@@ -124,7 +125,8 @@ def test_many_groups():
     groups = [(i % 3, i % 4) for i in range(900)]
     n = sum(g for g, _ in groups)
     a = make(groups, [1 + i % 20 for i in range(n)], 8, 2)
-    check(a, *call(a))
+    for splits in (None, (3, 1), (0, 1)):
+        check(a, *call(a, splits=splits))
 
 
 def test_agrees_with_plain_decode():
@@ -132,19 +134,20 @@ def test_agrees_with_plain_decode():
     a = make([(6, 50), (3, 10)], [1 + 40 * i for i in range(9)], 64, 8)
     for x in (a["paged_k"], a["paged_v"]):
         x.copy_(torch.nan_to_num(x))
-    out, lse = call(a)
+    out, lse = call(a, splits=(6, 2))
     o, l = sa.sink_attn_decode(a["q"], a["paged_k"], a["paged_v"], a["page_table"], a["kv_lens"], a["sinks"], SCALE)
     mag = reference(a)[2]
     assert bool(((out.float() - o.float()).abs() <= 2 * (2.0 ** -8 * (o.float().abs() + mag) + 2.0 ** -13 * mag)).all())
     assert bool(((lse - l).abs() <= 2.0 ** -12).all())
 
 
+@pytest.mark.parametrize("splits", [(2, 1), (0, 1)])
 @pytest.mark.parametrize("sink", [-INF, -1e30, 80.0, INF])
-def test_sinks_at_the_extremes(sink):
+def test_sinks_at_the_extremes(sink, splits):
     a = make([(3, 9)], [1, 0, 20], 16, 2)
     a["sinks"].fill_(sink)
     a["sinks"][0] = 0.5
-    out, lse = call(a)
+    out, lse = call(a, splits=splits)
     if sink == INF:  # the sink takes all the weight
         assert bool((out[:, 1:] == 0).all()) and bool((lse[:, 1:] == INF).all())
         a["sinks"][1:] = 0.5
@@ -154,10 +157,11 @@ def test_sinks_at_the_extremes(sink):
         check(a, out, lse)
 
 
-def test_no_keys_and_no_sink():
+@pytest.mark.parametrize("splits", [(2, 1), (0, 1)])
+def test_no_keys_and_no_sink(splits):
     a = make([(2, 0)], [0, 3], 8, 1)
     a["sinks"].fill_(-INF)
-    out, lse = call(a)
+    out, lse = call(a, splits=splits)
     assert bool((out[0] == 0).all()) and bool((lse[0] == -INF).all())
     check({**a, "q": a["q"][1:], "page_table": a["page_table"][1:], "kv_lens": a["kv_lens"][1:]}, out[1:], lse[1:])
 
@@ -172,7 +176,7 @@ def test_scores_far_apart():
         k = a["paged_k"].float()
         k[order] = k[order] * size[:64].reshape(-1, 1, 1, 1)
         a["paged_k"] = k.to(torch.bfloat16)
-        out, lse = call(a)
+        out, lse = call(a, splits=(6, 1))
         ro, rl, mag = reference(a)
         # scores of size up to 6 * 64 * 0.125 * ...: their fp32 error is 6 times that of unit keys
         assert bool(((out - ro).abs() <= 2.0 ** -8 * (ro.abs() + mag) + 2.0 ** -10 * mag).all())
@@ -218,7 +222,8 @@ def test_repeated_calls_and_graph_replay():
     check(a, out, lse)
 
 
-def test_device_side_reports():
+@pytest.mark.parametrize("splits", [(3, 1), (0, 1)])
+def test_device_side_reports(splits):
     import attention_softmax_sinks_gb300 as sa
     SA_ERR_BOUNDS = 5
 
@@ -228,7 +233,7 @@ def test_device_side_reports():
             x.copy_(torch.nan_to_num(x))
         for name, f in change.items():
             f(a[name])
-        sa.sink_attn_decode_shared(**a)
+        sa.sink_attn_decode_shared(**a, splits=splits)
         torch.cuda.synchronize()
         return sa.sink_attn_device_status(True)
 
@@ -246,15 +251,39 @@ def test_device_side_reports():
     assert status() == 0
 
 
-def test_shorter_than_its_prompt():
+@pytest.mark.parametrize("splits", [(3, 1), (0, 1)])
+def test_shorter_than_its_prompt(splits):
     import attention_softmax_sinks_gb300 as sa
     a = make([(3, 4)], [5, 6, 7], 16, 2)
     a["kv_lens"][1] = 20
-    out, lse = sa.sink_attn_decode_shared(**a)
+    out, lse = sa.sink_attn_decode_shared(**a, splits=splits)
     torch.cuda.synchronize()
     assert sa.sink_attn_device_status(True) == 5
-    a["kv_lens"][1] = 64  # what it attends to: the shared pages and its sink
-    check(a, out, lse)
+    for b in (0, 2):  # the others are not touched by it
+        one = {**a, **{n: a[n][b : b + 1] for n in ("q", "page_table", "kv_lens")}}
+        check(one, out[b : b + 1], lse[b : b + 1])
+
+
+def test_by_itself_in_a_graph_and_on_a_stream():
+    import attention_softmax_sinks_gb300 as sa
+    a = make([(4, 10), (2, 3)], [1, 20, 3, 40, 5, 6], 64, 8)
+    assert sa.sink_attn_decode_shared_splits(6, 2, 64, 8, 10, a["page_table"].shape[1]) == (0, 1)
+    want = call(a)
+    out = torch.full((8, 64, DIM), 7.0, dtype=torch.bfloat16, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = sa.sink_attn_decode_shared(**a, out=out[:6], return_lse=False, stream=s)
+    s.synchronize()
+    assert got[1] is None and torch.equal(got[0], want[0]) and bool((out[6:] == 7).all())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o, l = sa.sink_attn_decode_shared(**a)
+    a["q"].copy_(a["q"].flip(0))
+    g.replay()
+    torch.cuda.synchronize()
+    check(a, o, l)
+    with pytest.raises(ValueError):
+        sa.sink_attn_decode_shared(**a, splits=(0, 2))
 
 
 @pytest.mark.parametrize("groups", [[(5, 61)], [(24, 100)], [(3, 40), (30, 9)], [(2, 300), (1, 7), (2, 130)], [(1, 3)], [(9, 8), (9, 8)]])

@@ -36,7 +36,8 @@ def _shared(lib, **kw):
     (dict(max_pages=2 ** 26 + 1), SA_ERR_SHAPE), (dict(hq=0), SA_ERR_SHAPE), (dict(hkv=0), SA_ERR_SHAPE),
     (dict(hq=65), SA_ERR_SHAPE), (dict(hq=17, hkv=1), SA_ERR_UNSUPPORTED), (dict(dim=128), SA_ERR_UNSUPPORTED),
     (dict(page=32), SA_ERR_UNSUPPORTED), (dict(scale=NAN), SA_ERR_SHAPE), (dict(scale=INF), SA_ERR_SHAPE),
-    (dict(ss=0), SA_ERR_SHAPE), (dict(so=0), SA_ERR_SHAPE), (dict(ss=255), SA_ERR_SHAPE),
+    (dict(ss=0), SA_ERR_SHAPE), (dict(ss=-1, so=1), SA_ERR_SHAPE), (dict(so=0), SA_ERR_SHAPE), (dict(ss=0, so=0), SA_ERR_SHAPE),
+    (dict(ss=0, so=1, po=None, pl=None, q=None), SA_ERR_NULL), (dict(ss=0, so=1, po=None, pl=None, out=EIGHT), SA_ERR_ALIGNMENT), (dict(ss=255), SA_ERR_SHAPE),
     (dict(ss=2 ** 31 - 1, so=2 ** 31 - 1), SA_ERR_SHAPE),
     (dict(num_pages=2 ** 24, hkv=8), SA_ERR_SHAPE),                   # rows of the cache beyond 32 bits
     (dict(num_pages=2 ** 24 - 1, hkv=8, q=None), SA_ERR_NULL),        # just within them
@@ -61,13 +62,14 @@ def test_splits_of_shared_prompts():
                 for shared in (0, 1, 7, 128, 4096, 2 ** 26):
                     for own in (0, 1, 100, 4096):
                         s, o = f(batch, groups, hq, hkv, shared, shared + max(own, 1 if shared == 0 else 0))
-                        assert 1 <= s <= 40 and o in (1, 2, 4, 8) and s + o <= 256
+                        assert (s, o) == (0, 1) or 2 <= s <= 40 and o in (1, 2, 4, 8)
                         # memory of the partial results beyond what one slot of each kind takes
                         assert batch * hq * 260 * (s - 2) <= 96 << 20
     for bad in ((0, 1, 64, 8, 4, 8), (4, 0, 64, 8, 4, 8), (4, 1, 8, 64, 4, 8), (4, 1, 64, 0, 4, 8), (4, 1, 64, 8, -1, 8),
                 (4, 1, 64, 8, 0, 0), (-1, -1, -1, -1, -1, -1)):
         assert f(*bad) == (1, 1)
     assert f(64, 1, 64, 8, 2048, 2112) == f(64, 1, 64, 8, 2048, 2112, 152)
+    assert f(4, 1, 64, 8, 16, 20) == (0, 1) and f(64, 1, 64, 8, 2048, 2112)[0] > 0
 
 
 def _lora(lib, **kw):
