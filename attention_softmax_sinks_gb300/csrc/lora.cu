@@ -1292,8 +1292,8 @@ void lora_plan(LoraArgs& a, int sms) {
   const int most = a.M < kBM ? a.M : kBM;
   const int adapter_blocks = ((a.num_adapters < most ? a.num_adapters : most) * ((a.R + 15) / 16) + 7) / 8;
   // Estimated cycles of tiles of bn columns, by single CTAs, by pairs or by clusters that share K; the
-  // factors are fitted to times over 27 sizes (1 to 2000 tokens, 4096 -> 2880, 2880 -> 5120 and 640), and
-  // what is chosen took at most 8% more than the best of all.  A block of 64 values of K takes what is
+  // factors are fitted to times over 27 sizes (1 to 2000 tokens, 4096 -> 2880, 2880 -> 5120 and 640), where
+  // what is chosen took up to 4% more than the best, for six of them 7 to 13%.  A block of 64 values of K takes what is
   // longest: the operands' way in (64 bytes a cycle), the tensor core's reading (128 bytes a cycle, 128
   // rows of x whatever their number), its arithmetic.  Clusters that share K add up at the end, and the
   // GPU holds 76, 36 or 15 of them (GPCs of 18 to 20 SMs), fewer beside the first product's CTAs of
