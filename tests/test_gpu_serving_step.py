@@ -105,7 +105,7 @@ def test_captured_replayed_and_beside_another():
     on two streams, with other tokens in the same places; and from two threads without graphs."""
     import attention_softmax_sinks_gb300 as sa
     sa.sink_attn_device_status(True)
-    ls = [layer(*BATCHES["three groups"], seed=5), layer(*BATCHES["one prompt"], seed=6)]
+    ls = [layer(*BATCHES["three groups"], seed=5), layer(*BATCHES["one long prompt"], seed=6)]
     eager = [{k: v.clone() for k, v in run(sa, l).items()} for l in ls]
     streams = [torch.cuda.Stream() for _ in ls]
     graphs, results = [], []
