@@ -576,6 +576,8 @@ __global__ void __launch_bounds__(kBlock, 3) router_scores_kernel(const RouterSc
   int vecs = (E + 4 * kLanes - 1) / (4 * kLanes);  // vectors of a lane that hold experts
   const long long warps = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
   const long long passes = (a.num_tokens + kTokens - 1) / kTokens;
+  // (the last, partial round by few blocks: the others settle their doubtful tokens meanwhile; spread
+  // over all blocks, 32768 tokens took 33.3 us instead of 30.8)
   long long p = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + warp;
   auto token_of = [&](long long pass) { return min(pass * kTokens + tok, a.num_tokens - 1); };  // lanes behind: the last one
   float x[kOwn];
