@@ -76,6 +76,7 @@ sa_status moe_router(const void* x, const void* w_router, const void* bias, int 
  *
  * The choice is that of exact arithmetic on the logits and biases as given, equal values in
  * favour of the lower index; without a bias it is the logits' own order (within the groups kept).
+ * (Scores are known to about 2^-52 here: values that differ by less are ordered as they round.)
  * The weights are computed in fp32 and stored as bf16.
  *
  *  logits        fp32 (is_fp32 != 0) or bf16 [num_tokens, num_experts], row-major, at least
