@@ -49,6 +49,8 @@ constexpr unsigned kFull = 0xffffffffu;
 // A merit is the sum of two.
 constexpr uint32_t kNear = 16;
 constexpr float kKeyRange = 16777000.0f;  // keys are 1 .. 2^24 - 1
+// Biases that differ by more than this are looked over for masks, which would leave few keys to the scores.
+constexpr float kWideBias = 32.0f;
 
 __device__ __forceinline__ float rcp(float x) {
   float y;
@@ -57,7 +59,7 @@ __device__ __forceinline__ float rcp(float x) {
 }
 
 // 24 bits of fixed point of what is ordered, 1 .. 2^24 - 1; 0 for what is not a number and for a
-// bias of -inf (conversion to unsigned saturates).  bias_key: 1 + the bias's part.
+// masked expert (conversion to unsigned saturates).  bias_key: 1 + the bias's part.
 template <bool kSigmoid, bool kScored>
 __device__ __forceinline__ uint32_t fixed_point(float x, float ref, float unit, float soft_unit, float bias_key) {
   if constexpr (!kScored) return __float2uint_rn(fmaxf((x - ref + 32.0f) * 524287.0f, 0.0f) + 1.0f);
@@ -367,6 +369,58 @@ __device__ __noinline__ void choose_among_all(const RouterScoresArgs& a, WarpScr
   __syncwarp();
 }
 
+__device__ __forceinline__ float warp_min(float v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v = fminf(v, __shfl_xor_sync(kFull, v, off));
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) { return -warp_min(-v); }
+
+// The biases' range [lo, hi] for the keys (a warp; a lane's biases, NaN behind the last expert).  With
+// R = hi - lo, a finite bias is left out, as masked, only below lo - R - 2.  A score adds 0 to 1.  So
+// a masked expert's value is below every other's, and the merit of a group with fewer than two
+// others is below hi + 1 + (lo - R - 2) + 1 = 2 lo, which no group with two others is below: the order
+// of keys with 0 for masked experts and for such groups is certain.  The highest range that leaves
+// at least `need` experts in it is taken, if there is one; it doubles with every second step.
+__device__ __forceinline__ void bias_range(const float (&b)[8], int need, float& lo, float& hi) {
+  constexpr float kMost = 3.402823466e38f;
+  float least = __builtin_huge_valf(), most = kNegInf;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (fabsf(b[i]) <= kMost) {
+      least = fminf(least, b[i]);
+      most = fmaxf(most, b[i]);
+    }
+  }
+  lo = warp_min(least);
+  hi = warp_max(most);
+  if (!(lo <= hi)) lo = hi = 0.0f;  // no finite one
+  if (hi - lo <= kWideBias) return;
+  lo = hi;
+  for (;;) {
+    // in fp64, rounded down: exact enough beside the steps of fp32 at any size
+    const float reach = __double2float_rd(static_cast<double>(lo) - (static_cast<double>(hi) - lo) - 2.0);
+    float within = lo, below = kNegInf;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (fabsf(b[i]) <= kMost) {
+        if (b[i] >= reach) within = fminf(within, b[i]);
+        else below = fmaxf(below, b[i]);
+        n += b[i] >= lo;
+      }
+    }
+    within = warp_min(within);
+    if (within < lo) {
+      lo = within;
+      continue;
+    }
+    below = warp_max(below);
+    if (__reduce_add_sync(kFull, n) >= need || below == kNegInf) return;
+    lo = below;  // too few: with the next ones below
+  }
+}
+
 // Experts whose key (24 bits, in ws.key[0]; 0: not to be chosen) is at least that of their place
 // `floor`, listed in expert order in ws.list.  Returns their number.
 template <typename Floor>
@@ -388,10 +442,10 @@ __device__ __forceinline__ int list_candidates(WarpScratch& ws, int E, Floor flo
 __device__ __forceinline__ uint32_t below_by(uint32_t q, uint32_t d) { return q > d ? q - d : 0u; }
 
 // Token t by the whole warp, with the comparisons that keys cannot settle made in fp64; writes its
-// results.  bias_key, unit: as in the kernel.
+// results.  bias_key, unit, keyless: as in the kernel.
 template <bool kSigmoid, bool kScored>
 __device__ __noinline__ void settle(const RouterScoresArgs& a, WarpScratch& ws, int* hist, const float* bias_key, float unit,
-                                    long long t) {
+                                    bool keyless, long long t) {
   const int lane = threadIdx.x & 31;
   const int E = a.num_experts, k = a.top_k, size = E / a.num_groups;
   const bool grouped = kScored && a.top_groups < a.num_groups;
@@ -415,14 +469,14 @@ __device__ __noinline__ void settle(const RouterScoresArgs& a, WarpScratch& ws, 
   for (int i = 0; i < 8; ++i) {
     const int e = lane + 32 * i;
     if (e < E) ws.key[1][e] = __float_as_uint(x[i]);
-    if (e < E)  // 0 stands for experts of other groups here
+    if (e < E)  // 0 stands for experts of other groups here (masked ones: below or at the others' least)
       ws.key[0][e] = max(fixed_point<kSigmoid, kScored>(x[i], ref, unit, unit * inv_sum, kScored ? bias_key[e] : 0.0f), 1u);
   }
   __syncwarp();
   int picked[8];
-  bool walk = false;
+  bool walk = keyless;
   // ---- groups: the candidates for the two largest of each
-  if (grouped) {
+  if (grouped && !walk) {
     if (lane < a.num_groups) {
       uint32_t first = 0, second = 0;
       for (int i = 0; i < size; ++i) {
@@ -564,6 +618,8 @@ __global__ void __launch_bounds__(kBlock, 3) router_scores_kernel(const RouterSc
   __shared__ int hist[256];
   __shared__ __align__(16) float bias_key[256];  // 1 + the bias's part of a key
   __shared__ float key_unit;                     // keys per unit of score
+  __shared__ bool masks_differ;                  // masked experts have an order of their own
+  __shared__ bool keyless;                       // biases too far apart for keys: every token in fp64
   __shared__ long long doubtful[kMaxDoubtful];   // tokens left for the end
   __shared__ int num_doubtful;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -612,28 +668,28 @@ __global__ void __launch_bounds__(kBlock, 3) router_scores_kernel(const RouterSc
   if (threadIdx.x == 0) num_doubtful = 0;
   if constexpr (kScored) {
     if (warp == 0) {
-      float b[8], lo = __builtin_huge_valf(), hi = kNegInf;
+      float b[8], lo, hi;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        b[i] = lane + 32 * i < E ? bias_of(a, lane + 32 * i) : 0.0f;
-        if (lane + 32 * i < E && fabsf(b[i]) <= 3.4e38f) {
-          lo = fminf(lo, b[i]);
-          hi = fmaxf(hi, b[i]);
-        }
-      }
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) {
-        lo = fminf(lo, __shfl_xor_sync(kFull, lo, off));
-        hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, off));
-      }
-      if (!(lo <= hi)) lo = hi = 0.0f;
+      for (int i = 0; i < 8; ++i) b[i] = lane + 32 * i < E ? bias_of(a, lane + 32 * i) : __int_as_float(0x7fffffff);
+      bias_range(b, grouped ? max(k, 2 * a.top_groups) : k, lo, hi);
       const float unit = kKeyRange / (1.0f + (hi - lo));
+      bool differ = false;
       // b - lo first: what is rounded is small beside the range
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        bias_key[lane + 32 * i] = fminf(fmaxf((b[i] - lo) * unit, -4e7f), kKeyRange - unit) + 1.0f;
-      if (lane == 0) key_unit = unit;
+      for (int i = 0; i < 8; ++i) {
+        const bool in = b[i] >= lo;  // (not a NaN, which counts as -inf)
+        bias_key[lane + 32 * i] = in ? fminf((b[i] - lo) * unit, kKeyRange - unit) + 1.0f : -4e7f;
+        if (b[i] < lo && b[i] != kNegInf) differ = true;
+      }
+      differ = __any_sync(kFull, differ);
+      if (lane == 0) {
+        key_unit = unit;
+        masks_differ = differ;
+        keyless = !(hi - lo <= 1e30f);
+      }
     }
+  } else if (threadIdx.x == 0) {
+    masks_differ = keyless = false;
   }
   __syncthreads();
   const float unit = kScored ? key_unit : 0.0f;
@@ -678,7 +734,7 @@ __global__ void __launch_bounds__(kBlock, 3) router_scores_kernel(const RouterSc
     }
     if (p + warps < passes) load(token_of(p + warps));
     auto expert_of = [](uint32_t full_key) { return 255 - static_cast<int>(full_key & 255u); };
-    bool doubt = false;  // some comparison is not certain
+    bool doubt = kScored && keyless;  // some comparison is not certain
     unsigned kept = kFull;
     // ---- groups
     if (grouped) {
@@ -712,7 +768,7 @@ __global__ void __launch_bounds__(kBlock, 3) router_scores_kernel(const RouterSc
 #pragma unroll 1
             for (int i = 0; i < size; ++i) take(from[i]);
           }
-          merit[n] = size > 1 ? first + second : first;
+          merit[n] = size > 1 && second != 0 ? first + second : size > 1 ? 0 : first;  // 0: masked, or one left
         }
       }
       // a group is kept if fewer than top_groups come before it
@@ -748,7 +804,8 @@ __global__ void __launch_bounds__(kBlock, 3) router_scores_kernel(const RouterSc
         last_kept = min(last_kept, __shfl_xor_sync(kFull, last_kept, off));
         first_dropped = max(first_dropped, __shfl_xor_sync(kFull, first_dropped, off));
       }
-      doubt = last_kept - first_dropped <= 2 * kNear;  // a tie in merit as well
+      // a tie in merit as well; of 0 only if the masks make a difference
+      doubt |= last_kept - first_dropped <= 2 * kNear && (last_kept != 0 || masks_differ);
       if (size % 4 == 0) {  // the kept groups' first experts, in order
 #pragma unroll
         for (int n = 0; n < kMine; ++n) {
@@ -843,6 +900,7 @@ __global__ void __launch_bounds__(kBlock, 3) router_scores_kernel(const RouterSc
     for (int r = 0; r < K; ++r)
       if (j == r) own = best[r];
     if (j < k && below >= 256 && (own >> 8) - (below >> 8) <= kNear && !same_inputs(a, tt, expert, expert_of(below))) doubt = true;
+    if (kScored && j < k && own < 256 && masks_differ) doubt = true;  // a masked expert among the chosen
     const unsigned doubts = __ballot_sync(kFull, doubt && live);
     doubt = (doubts >> (lane & ~(kLanes - 1)) & ((1u << kLanes) - 1)) != 0;
     // ---- weights
@@ -862,13 +920,13 @@ __global__ void __launch_bounds__(kBlock, 3) router_scores_kernel(const RouterSc
   __syncthreads();
   const int left = min(num_doubtful, kMaxDoubtful);
   for (int i = warp; i < left; i += blockDim.x >> 5)
-    settle<kSigmoid, kScored>(a, ws, hist, bias_key, unit, doubtful[i]);
+    settle<kSigmoid, kScored>(a, ws, hist, bias_key, unit, keyless, doubtful[i]);
   if (num_doubtful > kMaxDoubtful) {  // the marked ones, by the warps that met them
     p = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + warp;
     for (; p < passes; p += warps) {
       for (long long t = p * kTokens; t < min((p + 1) * kTokens, a.num_tokens); ++t) {
         const int first = *const_cast<volatile int32_t*>(a.topk_idx + t * k);
-        if (__shfl_sync(kFull, first, 0) < 0) settle<kSigmoid, kScored>(a, ws, hist, bias_key, unit, t);
+        if (__shfl_sync(kFull, first, 0) < 0) settle<kSigmoid, kScored>(a, ws, hist, bias_key, unit, keyless, t);
       }
     }
   }

@@ -208,3 +208,45 @@ def test_experts_that_share_a_huge_bias(score):
     bias[7::5] = 1e20
     check(x, 8, score, bias)
     check(x, 6, score, bias, 8, 4)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("mask", [-INF, torch.finfo(torch.float32).min, -3e38, -1e9, -1e4])
+def test_groups_with_one_expert_left(score, mask):
+    # a merit is the sum of two values: a masked one takes it below those of groups with two others
+    x = torch.tensor([[3.0, 3.0, -1.0, -1.0]], device="cuda")
+    check(x, 1, score, torch.tensor([0.0, mask, 0.0, 0.0], device="cuda"), 2, 1)
+    x, bias = make(400, 64, bias=0.1, seed=21)
+    e = torch.arange(64, device="cuda")
+    for size in (2, 4, 8):
+        group = e // size
+        masked = ((group % 3 == 0) & (e % size > 0)) | (group % 5 == 1)  # one left of some groups, none of others
+        b = torch.where(masked, mask, bias)
+        groups = 64 // size
+        for keep in (1, groups // 3, groups // 2, groups - 1):  # the last: groups with one or none are kept, too
+            check(x, min(6, keep * size), score, b, groups, keep)
+    # groups of one expert
+    x, e, bias = x[:, :32].contiguous(), e[:32], bias[:32]
+    check(x, 5, score, torch.where(e % 2 == 0, mask, bias), 32, 7)
+    check(x, 8, score, torch.where(e % 4 != 0, mask, bias), 32, 9)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_masked_experts_are_ordered_as_well(score):
+    # fewer experts left than places: the masked ones follow by their values, equal ones by index
+    x, bias = make(200, 64, bias=0.1, seed=22)
+    e = torch.arange(64, device="cuda")
+    low = torch.finfo(torch.float32).min
+    for mask in (low, -1e9, -1e4, -INF):
+        check(x, 8, score, torch.where(e % 13 == 5, bias, mask))
+        check(x, 8, score, torch.where(e % 9 == 0, bias, mask), 8, 2)
+    mixed = torch.where(e % 4 == 0, -INF, torch.where(e % 4 == 1, low, torch.where(e % 4 == 2, -1e5, bias)))
+    check(x, 8, score, mixed)
+    check(x, 8, score, torch.where(e > 20, mixed.clamp(max=-1e5), bias))
+    check(x, 6, score, mixed, 16, 5)
+    check(x, 8, score, mixed.roll(3), 8, 3)
+    check(x, 8, score, torch.full((64,), low, device="cuda"))
+    check(x, 8, score, torch.where(e == 9, 1e4, bias))          # one far above the others
+    check(x, 4, score, torch.where(e == 9, 1e4, bias), 8, 3)
+    check(x, 8, score, torch.where(e < 9, 3e38, -3e38))         # their distance is beyond fp32
+    check(x, 4, score, torch.where(e % 2 == 0, 3e38, -3e38), 8, 3)
