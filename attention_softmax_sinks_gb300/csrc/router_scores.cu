@@ -619,7 +619,7 @@ __global__ void __launch_bounds__(kBlock, 3) router_scores_kernel(const RouterSc
   __shared__ __align__(16) float bias_key[256];  // 1 + the bias's part of a key
   __shared__ float key_unit;                     // keys per unit of score
   __shared__ bool masks_differ;                  // masked experts have an order of their own
-  __shared__ bool keyless;                       // biases too far apart for keys: every token in fp64
+  __shared__ bool keyless;                       // biases too far apart for keys, or +inf: every token in fp64
   __shared__ long long doubtful[kMaxDoubtful];   // tokens left for the end
   __shared__ int num_doubtful;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -673,19 +673,21 @@ __global__ void __launch_bounds__(kBlock, 3) router_scores_kernel(const RouterSc
       for (int i = 0; i < 8; ++i) b[i] = lane + 32 * i < E ? bias_of(a, lane + 32 * i) : __int_as_float(0x7fffffff);
       bias_range(b, grouped ? max(k, 2 * a.top_groups) : k, lo, hi);
       const float unit = kKeyRange / (1.0f + (hi - lo));
-      bool differ = false;
+      bool differ = false, pinned = false;
       // b - lo first: what is rounded is small beside the range
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const bool in = b[i] >= lo;  // (not a NaN, which counts as -inf)
         bias_key[lane + 32 * i] = in ? fminf((b[i] - lo) * unit, kKeyRange - unit) + 1.0f : -4e7f;
         if (b[i] < lo && b[i] != kNegInf) differ = true;
+        if (b[i] == -kNegInf) pinned = true;
       }
       differ = __any_sync(kFull, differ);
+      pinned = __any_sync(kFull, pinned);
       if (lane == 0) {
         key_unit = unit;
         masks_differ = differ;
-        keyless = !(hi - lo <= 1e30f);
+        keyless = pinned || !(hi - lo <= 1e30f);
       }
     }
   } else if (threadIdx.x == 0) {

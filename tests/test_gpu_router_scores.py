@@ -250,3 +250,20 @@ def test_masked_experts_are_ordered_as_well(score):
     check(x, 4, score, torch.where(e == 9, 1e4, bias), 8, 3)
     check(x, 8, score, torch.where(e < 9, 3e38, -3e38))         # their distance is beyond fp32
     check(x, 4, score, torch.where(e % 2 == 0, 3e38, -3e38), 8, 3)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_experts_pinned_by_an_infinite_bias(score):
+    x, bias = make(200, 64, bias=0.1, seed=23)
+    x[:, 9] = -4.0  # not for its score
+    bias[9] = INF
+    check(x, 1, score, bias)
+    check(x, 8, score, bias)
+    check(x, 8, score, bias, 8, 3)
+    bias[[2, 40, 41]] = INF
+    check(x, 3, score, bias)
+    check(x, 6, score, bias, 16, 5)
+    bias[20:40] = -INF
+    check(x, 8, score, bias)
+    check(x, 8, score, bias, 8, 7)
+    check(x, 8, score, torch.full((64,), INF, device="cuda"))
