@@ -42,13 +42,22 @@ constexpr int kMaxDoubtful = 64;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr unsigned kFull = 0xffffffffu;
-// Distance of two keys' 24-bit parts above which their order is certain.  Logits: x - max is
-// rounded by at most 2^-20 (half a unit), to a unit by another half, for each of the two.  Scores:
-// exp2 and reciprocal err by 2^-22 and 2^-23 relative, the exponent's rounding by 2^-24 |x| e^-|x|;
-// with the sums' roundings at most 2^-21.5 of a range of at least 1, 6 units, for each of the two.
+// Distance of two keys' 24-bit parts above which their order is certain.  Logits: the key never falls
+// where the logit grows, only equal keys are uncertain.  Scores, with R the range of the biases, in steps
+// of a key, 2^-24 (1 + R):
+//  - the bias's part (none where R = 0): b - lo by R / (1 + R), its product and the 1 added by 1/2 each;
+//    the sum with the score and the conversion by 1/2 each.  2 R / (1 + R) + 4 for two keys.
+//  - sigmoid: the exponent by 0.3 (|x| s (1 - s) <= 0.224), exp2 (2^-22) by 1, 1 + e^-x by 1, the reciprocal
+//    by 2.  8.6 / (1 + R) for two; with the above most near R = 0, 12.6.
+//  - softmax: exp2 by 4 s, but not at the maximum, the exponent by 2.25 s |x - max| <= 0.63.  4 / (1 + R)
+//    for two, whose scores are 1 together at most.  The sum's relative error counts with the difference of
+//    the two scores, which is that of their biases: at most min(R, 1) times 10, for the 8 roundings of
+//    exp_sum and between lanes, the reciprocal and a product; and for its terms 4.2 at most (1 of exp2;
+//    3.2 of the exponents, for 255 of the same).  With the above most at R = 1, 14.1.
+//    (Terms added one behind the other, 34 roundings, took it to 27.)
 // A merit is the sum of two.
 constexpr uint32_t kNear = 16;
-constexpr float kKeyRange = 16777000.0f;  // keys are 1 .. 2^24 - 1
+constexpr float kKeyRange = 16777000.0f;  // keys are 1 .. 2^24 - 1, with room for what they are off by
 // Biases that differ by more than this are looked over for masks, which would leave few keys to the scores.
 constexpr float kWideBias = 32.0f;
 
@@ -70,6 +79,13 @@ __device__ __forceinline__ uint32_t fixed_point(float x, float ref, float unit, 
 template <bool kSigmoid>
 __device__ __forceinline__ float weight_of(float x, float ref, float inv_sum) {
   return kSigmoid ? 1.0f / (1.0f + expf(-x)) : expf(x - ref) * inv_sum;
+}
+
+// sum exp(x - ref), added in pairs: a term is rounded log2(N) times.
+template <int N>
+__device__ __forceinline__ float exp_sum(const float* x, float ref) {
+  if constexpr (N == 1) return ex2((x[0] - ref) * kLog2e);
+  else return exp_sum<N / 2>(x, ref) + exp_sum<N / 2>(x + N / 2, ref);
 }
 
 // The r-th choice of token t: its score and the sum of the chosen ones'.
@@ -450,7 +466,7 @@ __device__ __noinline__ void settle(const RouterScoresArgs& a, WarpScratch& ws, 
   const int E = a.num_experts, k = a.top_k, size = E / a.num_groups;
   const bool grouped = kScored && a.top_groups < a.num_groups;
   // ---- the keys once more, in expert order, without the experts' codes
-  float x[8], ref = kNegInf, total = 0.0f;
+  float x[8], ref = kNegInf;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     x[i] = lane + 32 * i < E ? load_logit(a, t, lane + 32 * i) : kNegInf;
@@ -459,8 +475,7 @@ __device__ __noinline__ void settle(const RouterScoresArgs& a, WarpScratch& ws, 
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) ref = fmaxf(ref, __shfl_xor_sync(kFull, ref, off));
   if (ref == kNegInf) ref = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) total += ex2((x[i] - ref) * kLog2e);
+  float total = exp_sum<8>(x, ref);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(kFull, total, off);
   const float inv_sum = total > 0.0f ? 1.0f / total : 0.0f;
@@ -678,7 +693,7 @@ __global__ void __launch_bounds__(kBlock, 3) router_scores_kernel(const RouterSc
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const bool in = b[i] >= lo;  // (not a NaN, which counts as -inf)
-        bias_key[lane + 32 * i] = in ? fminf((b[i] - lo) * unit, kKeyRange - unit) + 1.0f : -4e7f;
+        bias_key[lane + 32 * i] = in ? (b[i] - lo) * unit + 1.0f : -4e7f;
         if (b[i] < lo && b[i] != kNegInf) differ = true;
         if (b[i] == -kNegInf) pinned = true;
       }
@@ -709,9 +724,7 @@ __global__ void __launch_bounds__(kBlock, 3) router_scores_kernel(const RouterSc
       ref = top == kNegInf ? 0.0f : top;
     }
     if constexpr (!kSigmoid) {
-      float sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kOwn; ++i) sum += ex2((x[i] - ref) * kLog2e);
+      float sum = exp_sum<kOwn>(x, ref);
 #pragma unroll
       for (int off = 1; off < kLanes; off <<= 1) sum += __shfl_xor_sync(kFull, sum, off);
       inv_sum = sum > 0.0f ? 1.0f / sum : 0.0f;

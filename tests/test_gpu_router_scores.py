@@ -267,3 +267,22 @@ def test_experts_pinned_by_an_infinite_bias(score):
     check(x, 8, score, bias)
     check(x, 8, score, bias, 8, 7)
     check(x, 8, score, torch.full((64,), INF, device="cuda"))
+
+
+@pytest.mark.parametrize("lanes", [1, 2, 8])
+def test_sum_of_many_small_exponentials(lanes):
+    # Terms of the softmax's sum that are each below half a step of the largest one, but not together:
+    # the largest score and another expert's bias are the same to within a few 2^-24.
+    x = torch.full((512, 256), -100.0, device="cuda")
+    small = [4 * (j + 8 * i) + c for j in range(lanes) for i in range(8) for c in range(4)]
+    small += [e for e in (5, 9, 17) if e not in small]
+    small = [e for e in small if e not in (0, 23)]
+    x[:, small] = torch.linspace(-16.6362, -16.8, 512, device="cuda")[:, None]
+    x[:, 0] = 0.0
+    exact = torch.softmax(x.double(), 1)[:, 0]
+    for at in (0, 100, 300, 511):
+        for away in range(-4, 5):
+            bias = torch.zeros(256, device="cuda")
+            bias[23] = exact[at] + away * 2.0 ** -25
+            check(x, 1, "softmax", bias)
+            check(x, 2, "softmax", bias, renorm=False)
