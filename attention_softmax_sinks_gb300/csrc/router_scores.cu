@@ -15,7 +15,8 @@
 //    added to the few that leave the lane.)
 //  - A key is off by a few units from what it stands for.  Where the last group kept and the first
 //    dropped, or two neighbours among the chosen, or the last chosen and the first not chosen are
-//    closer than that, and not equal in logit and bias, the experts within reach of that border
+//    closer than that, and not equal in logit and bias (nor, behind an equal one not chosen, any
+//    other as close), the experts within reach of that border
 //    are compared once more, a lane for each: scores by sigmoid in pairs of fp32, and where that
 //    does not settle it, or by softmax, in fp64 (one token in a thousand of 256 experts in 8 groups
 //    with logits in 32 bits); more than 32 of them by a walk over all experts in fp64.
@@ -914,7 +915,26 @@ __global__ void __launch_bounds__(kBlock, 3) router_scores_kernel(const RouterSc
 #pragma unroll
     for (int r = 0; r < K; ++r)
       if (j == r) own = best[r];
-    if (j < k && below >= 256 && (own >> 8) - (below >> 8) <= kNear && !same_inputs(a, tt, expert, expert_of(below))) doubt = true;
+    const bool near = j < k && below >= 256 && (own >> 8) - (below >> 8) <= kNear;
+    const bool same = near && same_inputs(a, tt, expert, expert_of(below));
+    if (near && !same) doubt = true;
+    // At the border only the first behind it has been looked at.  Where it is the last one's equal, others
+    // as near may be above both.
+    const unsigned equal = __ballot_sync(kFull, same && j == k - 1);
+    if (equal) {
+      const bool mine = (equal >> (lane & ~(kLanes - 1)) & ((1u << kLanes) - 1)) != 0;
+#pragma unroll 1
+      for (int i = 0; i < vecs && mine && !doubt; ++i) {
+        uint32_t key[4];
+        load_keys(i, key);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (key[c] < last && key[c] >= 256 && (last >> 8) - (key[c] >> 8) <= kNear &&
+              !same_inputs(a, tt, expert_of(last), expert_of(key[c])))
+            doubt = true;
+      }
+      __syncwarp();
+    }
     if (kScored && j < k && own < 256 && masks_differ) doubt = true;  // a masked expert among the chosen
     const unsigned doubts = __ballot_sync(kFull, doubt && live);
     doubt = (doubts >> (lane & ~(kLanes - 1)) & ((1u << kLanes) - 1)) != 0;

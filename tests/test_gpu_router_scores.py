@@ -286,3 +286,22 @@ def test_sum_of_many_small_exponentials(lanes):
             bias[23] = exact[at] + away * 2.0 ** -25
             check(x, 1, "softmax", bias)
             check(x, 2, "softmax", bias, renorm=False)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_equal_neighbours_do_not_hide_a_third(score, dtype):
+    # scores that no key tells apart: the border's two experts have the same logit, a later one a larger
+    zero = torch.zeros(32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(24)
+    for base, more in ((20.0, 0.5), (30.0, 1.0), (0.0, 1e-7), (-50.0, 0.25)):
+        x = torch.full((64, 32), base, device="cuda")
+        x[:, 31] = 5.0 if base < 5.0 else 100.0  # the largest, for what is relative to it
+        at = torch.randint(3, 31, (64, 2), generator=g, device="cuda")
+        x.scatter_(1, at, base + more)
+        x = x.to(getattr(torch, dtype))
+        for k in (1, 2, 3, 4, 8):
+            for bias in (None, zero, zero - 0.75):
+                check(x, k, score, bias)
+            check(x, k, score, None, 4, 2)
+            check(x, k, score, zero, 4, 3)
