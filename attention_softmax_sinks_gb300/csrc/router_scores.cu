@@ -293,7 +293,8 @@ __device__ __noinline__ Wide exact_value(const RouterScoresArgs& a, long long t,
   return wide_sum(kSigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - top) / sum, bias_of(a, e));
 }
 
-// The token's largest logit and, for scores by softmax, the sum below it.
+// The token's largest logit and, for scores by softmax, the sum below it (0 and 1 where every logit is
+// -inf, so that the scores are 0).
 template <bool kSigmoid>
 __device__ __forceinline__ void exact_sum(const RouterScoresArgs& a, long long t, bool scored, double& top, double& sum) {
   const int lane = threadIdx.x & 31;
@@ -304,6 +305,7 @@ __device__ __forceinline__ void exact_sum(const RouterScoresArgs& a, long long t
   for (int e = lane; e < a.num_experts; e += 32) most = fmaxf(most, load_logit(a, t, e));
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(kFull, most, off));
+  if (most == kNegInf) return;
   top = most;
   sum = 0.0;
 #pragma unroll 2

@@ -81,9 +81,11 @@ sa_status moe_router(const void* x, const void* w_router, const void* bias, int 
  *
  *  logits        fp32 (is_fp32 != 0) or bf16 [num_tokens, num_experts], row-major, at least
  *                aligned to their elements (four logits at a time where rows are aligned to that);
- *                -inf takes an expert out, NaN not allowed (the experts of such a row are
- *                some in range)
- *  bias          fp32 [num_experts] or NULL; -inf puts an expert behind all others
+ *                -inf is a score of 0, behind all others where there is no bias (a row of nothing
+ *                but -inf has scores of 0 by softmax as well); NaN not allowed, nor +inf with softmax (the
+ *                experts of such a row are some in range)
+ *  bias          fp32 [num_experts] or NULL; -inf (as NaN) puts an expert behind all others, +inf
+ *                before them; +inf and -inf in one merit count as -inf
  *  topk_idx, topk_weight, expert_counts: as for moe_router_topk_softmax
  *  1 <= num_experts <= 256, 1 <= num_groups <= 32 dividing num_experts, 1 <= top_groups <=
  *  num_groups, 1 <= top_k <= min(8, experts of top_groups groups), scale finite

@@ -305,3 +305,35 @@ def test_equal_neighbours_do_not_hide_a_third(score, dtype):
                 check(x, k, score, bias)
             check(x, k, score, None, 4, 2)
             check(x, k, score, zero, 4, 3)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_rows_whose_mask_leaves_nothing(score):
+    # every logit -inf: the scores are 0 and the biases decide, also where they are nearly the same
+    import attention_softmax_sinks_gb300 as sa
+    g = torch.Generator(device="cuda").manual_seed(25)
+    x = torch.randn(6, 64, generator=g, device="cuda")
+    x[::2] = -INF
+    order = torch.randperm(64, generator=g, device="cuda").float()
+    for step in (2.0 ** -25, 2.0 ** -22, 2.0 ** -10):
+        bias = 0.25 + order * step
+        for k, groups, keep in ((8, 1, 1), (3, 1, 1), (6, 8, 3), (8, 32, 5)):
+            idx, w = sa.moe_router_scores(x, k, score=score, bias=bias, num_groups=groups, top_groups=keep)
+            ri, _ = reference(x[::2], k, "sigmoid", bias, groups, keep, True, 1.0)  # whose score of -inf is 0
+            assert torch.equal(idx[::2].long(), ri)
+            assert bool((w[::2] == 0).all())
+            ri, rw = reference(x[1::2], k, score, bias, groups, keep, True, 1.0)
+            assert torch.equal(idx[1::2].long(), ri)
+
+
+def test_infinite_logits_by_sigmoid():
+    x, bias = make(300, 64, bias=0.1, seed=26)
+    x[:, 40] = INF
+    x[1::3, 50:] = INF
+    x[2::3, :30] = -INF
+    for b in (None, bias):
+        for k in (1, 3, 8):
+            check(x, k, "sigmoid", b)
+        check(x, 6, "sigmoid", b, 8, 3)
+        check(x[:, :32].contiguous(), 5, "sigmoid", None if b is None else b[:32].contiguous(), 32, 7)
+    check(x.to(torch.bfloat16), 8, "sigmoid")
