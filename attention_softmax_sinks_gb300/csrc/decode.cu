@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     for (int w = 0; w < kWarps; ++w) M = fmaxf(M, mg->m[w][hh]);
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     float den = 0.0f;
-    if (M != kNegInf) {
+    if (kPlan != 0 || M != kNegInf) {  // (with a plan also where no score was a number: NaN shows)
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float mw = mg->m[w][hh];
@@ -573,7 +573,8 @@ __global__ void __launch_bounds__(kWarps * 32)
       continue;
     }
     const float inv = den > 0.0f ? 1.0f / den : 0.0f;
-    const float lse = den > 0.0f ? (M + lg2(den)) * kLn2 : kNegInf;
+    float lse = den > 0.0f ? (M + lg2(den)) * kLn2 : kNegInf;
+    if (kShared && den != den) lse = den;  // for the merge, which lets NaN through
     const int head = kvh * G + hh;
     if (!kShared && a.num_splits == 1) {
       uint16_t* out = static_cast<uint16_t*>(a.out) +

@@ -707,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  __uint_as_float(u[3]) * inv);
             }
           }
-          a.partial_lse[out] = d > 0.0f ? (m + lg2(d)) * kLn2 : kNegInf;
+          a.partial_lse[out] = d > 0.0f ? (m + lg2(d)) * kLn2 : d == d ? kNegInf : d;  // NaN stays NaN
           if (seg.last && (t == 0 || !seg.turns)) {  // slots that nothing goes into
             float* lse = a.partial_lse + static_cast<size_t>(seq) * slot_rows * a.hq + head;
             for (int e = seg.turns ? 2 * seg.slot + 2 : seg.slot + 1; e < a.plan.shared_splits; ++e) lse[static_cast<size_t>(e) * a.hq] = kNegInf;
@@ -733,7 +733,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Adds a row's slots up: lse = ln sum e^lse_s, out = sum e^(lse_s - lse) o_s.  Sixteen lanes per row,
-// four dimensions each; a slot without weight (lse = -inf) is not read.
+// four dimensions each; an empty slot (lse = -inf) is not read.  A slot whose scores were not all numbers
+// (lse = NaN) makes the output NaN, and one whose weight vanishes is multiplied all the same: an infinite
+// value in it shows, as in the decode of a sequence by itself.  The lse of a NaN row is -inf, as there.
 constexpr int kMergeThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kPosInf = __builtin_huge_valf();
@@ -751,7 +753,7 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Merge
   const float4* o = reinterpret_cast<const float4*>(a.partial_o + (b * S * a.heads + h) * kHeadDim) + lane;
   const unsigned half = 0xffffu << (threadIdx.x & 16);
   // Sixteen slots' values are asked for before any weight is known, so that a row of up to sixteen
-  // costs one way to L2 (a slot that was not written holds anything: it is not multiplied).
+  // costs one way to L2 (a slot that was not written holds anything, and is not multiplied).
   float4 v[16];
   auto ask = [&](int s0) {
 #pragma unroll
@@ -767,14 +769,15 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Merge
   float z = 0.0f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int s0 = 0; s0 < S; s0 += 16) {
-    // this lane's slot's weight: the largest term exactly 1, -inf exactly 0
+    // this lane's slot's weight: the largest term exactly 1;
     const float l = s0 == 0 ? first : s0 + lane < S ? lse[static_cast<long long>(s0 + lane) * a.heads] : kNegInf;
-    const float w = l == kNegInf ? 0.0f : l == most ? 1.0f : most == kPosInf ? 0.0f : ex2((l - most) * kLog2e);
+    // an empty slot has weight -1 here.
+    const float w = l == kNegInf ? -1.0f : l == most ? 1.0f : l != l ? l : most == kPosInf ? 0.0f : ex2((l - most) * kLog2e);
     if (s0 > 0) ask(s0);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const float wi = __shfl_sync(half, w, (threadIdx.x & 16) + i);  // (0 behind the last slot)
-      if (wi != 0.0f) {
+      const float wi = __shfl_sync(half, w, (threadIdx.x & 16) + i);  // (-1 behind the last slot)
+      if (!(wi < 0.0f)) {
         z += wi;
         acc.x = fmaf(wi, v[i].x, acc.x);
         acc.y = fmaf(wi, v[i].y, acc.y);
@@ -788,7 +791,7 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Merge
   pk.x = pack_bf16x2(acc.x * inv, acc.y * inv);
   pk.y = pack_bf16x2(acc.z * inv, acc.w * inv);
   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * kHeadDim + 4 * lane) = pk;
-  if (a.lse && lane == 0) a.lse[row] = most == kPosInf ? kPosInf : z > 0.0f ? most + lg2(z) * kLn2 : kNegInf;
+  if (a.lse && lane == 0) a.lse[row] = !(z > 0.0f) ? kNegInf : most == kPosInf ? kPosInf : most + lg2(z) * kLn2;
 }
 
 }  // namespace

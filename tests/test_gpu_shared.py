@@ -296,3 +296,66 @@ def test_any_number_of_slots(groups, hq, hkv):
     for slots in (1, 2, 3, 4, 5, 6, 7, 8, 11, 14, 15, 20, 39, 64):
         ws = (torch.full((n, slots + 1, hq, DIM), NAN, device="cuda"), torch.full((n, slots + 1, hq), NAN, device="cuda"))
         check(a, *call(a, splits=(slots, 1), workspace=ws))
+
+
+@pytest.mark.parametrize("splits", [(3, 2), (1, 1), (6, 1), (0, 1)])
+@pytest.mark.parametrize("place", ["query", "shared key", "own key", "shared value", "own value", "only key"])
+@pytest.mark.parametrize("sink", [0.5, -INF])
+def test_what_is_not_finite_shows(splits, place, sink):
+    # as in sink_attn_decode: whatever a head attends to is in its result, in every plan
+    import attention_softmax_sinks_gb300 as sa
+    a = make([(4, 20), (2, 3), (1, 0)], [1, 20, 1, 40, 5, 60, 30], 16, 2)
+    for x in (a["paged_k"], a["paged_v"]):
+        x.copy_(torch.nan_to_num(x))
+    a["sinks"].fill_(sink)
+    table, hit = a["page_table"], torch.zeros(7, 16, dtype=torch.bool, device="cuda")
+    if place == "query":
+        a["q"][2, 11, 5] = NAN
+        a["q"][6, 1, 7] = NAN
+        hit[2, 11] = hit[6, 1] = True
+    elif place == "shared key":
+        a["paged_k"][table[0, 17].long(), 1, 3, 9] = NAN
+        hit[:4, 8:] = True
+    elif place == "own key":  # the second of a sequence's own pages, the only token of another's
+        a["paged_k"][table[1, 21].long(), 0, 2, 0] = NAN
+        a["paged_k"][table[2, 20].long(), 0, 0, 0] = NAN
+        hit[1:3, :8] = True
+    elif place == "shared value":
+        a["paged_v"][table[4, 1].long(), 0, 15, :] = NAN
+        hit[4:6, :8] = True
+    elif place == "own value":
+        a["paged_v"][table[6, 0].long(), 1, 0, :] = INF
+        hit[6, 8:] = True
+    else:  # every shared key
+        a["paged_k"][table[4, :3].long()] = NAN
+        hit[4:6] = True
+    sa.sink_attn_device_status(True)
+    out, lse = sa.sink_attn_decode_shared(**a, splits=splits)
+    o, l = sa.sink_attn_decode(a["q"], a["paged_k"], a["paged_v"], table, a["kv_lens"], a["sinks"], SCALE)
+    torch.cuda.synchronize()
+    assert sa.sink_attn_device_status(True) == 0
+    assert torch.equal(~torch.isfinite(out).all(2), hit) and torch.equal(~torch.isfinite(out).any(2), hit)
+    if not (place == "query" and sink == -INF):  # (nothing but that there: no weight at all)
+        assert torch.equal(torch.isfinite(out), torch.isfinite(o)) and torch.equal(torch.isfinite(lse), torch.isfinite(l))
+    ro, _, mag = reference({**a, "q": torch.where(hit[:, :, None], 0.0, a["q"])})
+    good = ~hit
+    bound = 2.0 ** -8 * (ro.abs() + mag) + 2.0 ** -13 * mag + 1e-30
+    assert bool(((out.double() - ro).abs() <= bound)[good].all())
+
+
+@pytest.mark.parametrize("splits", [(3, 2), (1, 1), (0, 1)])
+def test_a_value_without_weight_that_is_infinite(splits):
+    # a slot whose weight vanishes beside another's is multiplied all the same
+    import attention_softmax_sinks_gb300 as sa
+    a = make([(2, 20)], [5, 3], 8, 1)
+    for x in (a["paged_k"], a["paged_v"]):
+        x.copy_(torch.nan_to_num(x))
+    a["q"].fill_(1.0)
+    table = a["page_table"]
+    a["paged_k"][table[:, 20].long()] = 40.0   # own scores 320
+    a["paged_k"][table[0, :20].long()] = 0.0   # shared ones 0
+    a["paged_v"][table[0, 3].long(), 0, 2, 8:] = INF
+    out, _ = sa.sink_attn_decode_shared(**a, splits=splits)
+    o, _ = sa.sink_attn_decode(a["q"], a["paged_k"], a["paged_v"], table, a["kv_lens"], a["sinks"], SCALE)
+    assert not bool(torch.isfinite(out[:, :, 8:]).any()) and bool(torch.isfinite(out[:, :, :8]).all())
+    assert torch.equal(torch.isfinite(out), torch.isfinite(o))
