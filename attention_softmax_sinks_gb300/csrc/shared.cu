@@ -325,10 +325,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   sum_work(a, sm, 0, blockIdx.x == 0);
   const int units = sm.units, most1 = sm.most[1], most = max(sm.most[0], most1);
   const bool aligned = slots > 1 && 4 * units <= grid;
-  int each = slots == 1 ? most : 0, quantum;
+  int each = 0, quantum;
   bool turns = false;
-  if (each) {
-    sum_work(a, sm, each, false);
+  if (slots == 1) {
+    each = most;
+    if (each > 0) sum_work(a, sm, each, false);
     quantum = each * ((units + grid - 1) / grid);
   } else {
     const int cover = aligned ? (sm.total - units + grid - units - 1) / (grid - units) : (sm.total + grid - 1) / grid;

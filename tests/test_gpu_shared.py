@@ -359,3 +359,11 @@ def test_a_value_without_weight_that_is_infinite(splits):
     o, _ = sa.sink_attn_decode(a["q"], a["paged_k"], a["paged_v"], table, a["kv_lens"], a["sinks"], SCALE)
     assert not bool(torch.isfinite(out[:, :, 8:]).any()) and bool(torch.isfinite(out[:, :, :8]).all())
     assert torch.equal(torch.isfinite(out), torch.isfinite(o))
+
+
+@pytest.mark.parametrize("own", [1, 4])
+def test_nothing_shared_and_one_slot(own):
+    for groups in ([(5, 0)], [(2, 0), (0, 0), (3, 0)]):
+        a = make(groups, [1, 16, 17, 100, 33], 16, 2)
+        check(a, *call(a, splits=(1, own)))
+        check(a, *call({**a, "max_shared_pages": 3}, splits=(1, own)))
