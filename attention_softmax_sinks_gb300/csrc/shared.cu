@@ -109,8 +109,8 @@ struct __align__(1024) SharedSmem {
   int total;                   // tiles of keys of all units
   int units;
   int most[2];                 // of one unit: of one row tile in two slots, others
-  int warp_sum[kThreads / 32];
-  int warp_units[kThreads / 32];
+  unsigned warp_sum[kThreads / 32];
+  unsigned warp_units[kThreads / 32];
   int warp_most[2][kThreads / 32];
   int chunk[kMaxChunks];       // work before each kThreads groups
   Segment seg[kSegments];      // parts of this CTA's run, in turn; n_kv = 0: its end
@@ -156,14 +156,15 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint64_t
   }
 }
 
-// Sequences and shared pages of group g; no rows when they break the declared bounds.
+// Sequences and shared pages of group g; no rows (0, or -1 where the offsets go back) when they
+// break the declared bounds.
 __device__ __forceinline__ bool group_bounds(const SharedArgs& a, int g, int& first, int& count, int& pages) {
   first = __ldg(a.plan.group_offsets + g);
   const int end = __ldg(a.plan.group_offsets + g + 1);
   pages = __ldg(a.plan.shared_pages + g);
   const bool good = first >= 0 && end >= first && end <= a.batch && pages >= 0 && pages <= a.plan.max_shared_pages &&
                     (g > 0 || first == 0) && (g + 1 < a.plan.num_groups || end == a.batch);
-  count = good ? end - first : 0;
+  count = good ? end - first : end < first ? -1 : 0;
   return good;
 }
 
@@ -182,14 +183,20 @@ __device__ __forceinline__ int group_work(const SharedArgs& a, int count, int pa
 }
 
 // Sums up the groups' work, kThreads groups at a time: sm.total, sm.units, sm.most, sm.chunk.  All threads.
+// Offsets that go back somewhere can count a sequence many times, each group for itself within its
+// bounds.  Then there is no work: the sums, and places in them, would pass 32 bits (without, the
+// limit that the call checks holds), and the batch's size would not bound the time.
 __device__ __forceinline__ void sum_work(const SharedArgs& a, SharedSmem& sm, int each, bool report) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int before = 0, units = 0, most[2] = {0, 0};
+  unsigned before = 0, units = 0;
+  int most[2] = {0, 0};
+  bool ascend = true;
   for (int g0 = 0; g0 < a.plan.num_groups; g0 += kThreads) {
     const int g = g0 + static_cast<int>(threadIdx.x);
-    int n = 0, u = 0, tiles[2] = {0, 0};
+    unsigned n = 0, u = 0;
+    int count = 0, tiles[2] = {0, 0};
     if (g < a.plan.num_groups) {
-      int first, count, pages, len;
+      int first, pages, len;
       if (!group_bounds(a, g, first, count, pages) && report) raise_status(a.status, kStatusBadLen);
       n = group_work(a, count, pages, each, len);
       u = n > 0 ? n / len : 0;
@@ -204,7 +211,7 @@ __device__ __forceinline__ void sum_work(const SharedArgs& a, SharedSmem& sm, in
       tiles[0] = max(tiles[0], __shfl_xor_sync(0xffffffffu, tiles[0], off));
       tiles[1] = max(tiles[1], __shfl_xor_sync(0xffffffffu, tiles[1], off));
     }
-    __syncthreads();  // the last round's sums have been read
+    if (__syncthreads_or(count < 0)) ascend = false;  // (the last round's sums have been read)
     if (lane == 0) {
       sm.warp_sum[warp] = n;
       sm.warp_units[warp] = u;
@@ -221,10 +228,10 @@ __device__ __forceinline__ void sum_work(const SharedArgs& a, SharedSmem& sm, in
     }
   }
   if (threadIdx.x == 0) {
-    sm.total = before;
-    sm.units = units;
-    sm.most[0] = most[0];
-    sm.most[1] = most[1];
+    sm.total = ascend ? before : 0;
+    sm.units = ascend ? units : 0;
+    sm.most[0] = ascend ? most[0] : 0;
+    sm.most[1] = ascend ? most[1] : 0;
   }
   __syncthreads();
 }

@@ -160,7 +160,7 @@ sa_status sink_attn_decode(const void* q, const void* paged_k, const void* paged
  *               the caller's workspace, overwritten.  Calls that overlap on the GPU, captured
  *               graphs among them, need workspaces of their own.
  * A plan that breaks its bounds sets SA_ERR_BOUNDS in the device status word, and the results
- * of the sequences it concerns are undefined; keys of a page id outside [0, num_pages) read as
+ * of the sequences it concerns are undefined (all of them where group_offsets go back); keys of a page id outside [0, num_pages) read as
  * zeros (shared) or are skipped (own, or with shared_splits 0).  What the last page holds behind
  * kv_lens is never used, finite or not.  A query, key or value that is not finite shows in the
  * result of the heads that attend to it, whatever the split counts.

@@ -367,3 +367,19 @@ def test_nothing_shared_and_one_slot(own):
         a = make(groups, [1, 16, 17, 100, 33], 16, 2)
         check(a, *call(a, splits=(1, own)))
         check(a, *call({**a, "max_shared_pages": 3}, splits=(1, own)))
+
+
+@pytest.mark.parametrize("splits", [(3, 1), (1, 1), (0, 1)])
+@pytest.mark.parametrize("times", [2, 40, 4000])
+def test_offsets_that_go_back(splits, times):
+    # every second group is the whole batch, within its own bounds: reported, and not worked through
+    import attention_softmax_sinks_gb300 as sa
+    a = make([(9, 4)], [1 + i for i in range(9)], 16, 2)
+    want = call(a, splits=splits)
+    offsets = torch.tensor([0, 9], device="cuda", dtype=torch.int32).repeat(times)
+    bad = {**a, "group_offsets": offsets, "shared_pages": torch.full((2 * times - 1,), 4, device="cuda", dtype=torch.int32)}
+    sa.sink_attn_decode_shared(**bad, splits=splits)
+    torch.cuda.synchronize()
+    assert sa.sink_attn_device_status(True) == 5
+    got = call(a, splits=splits)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
