@@ -68,8 +68,12 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
+// The key of an expert with a bias of +inf (as a 24-bit key: all ones).
+constexpr uint32_t kPinned = 0xffffffffu;
+
 // 24 bits of fixed point of what is ordered, 1 .. 2^24 - 1; 0 for what is not a number and for a
-// masked expert (conversion to unsigned saturates).  bias_key: 1 + the bias's part.
+// masked expert, kPinned for one with a bias of +inf (conversion to unsigned saturates).  bias_key:
+// 1 + the bias's part.
 template <bool kSigmoid, bool kScored>
 __device__ __forceinline__ uint32_t fixed_point(float x, float ref, float unit, float soft_unit, float bias_key) {
   if constexpr (!kScored) return __float2uint_rn(fmaxf((x - ref + 32.0f) * 524287.0f, 0.0f) + 1.0f);
@@ -388,10 +392,10 @@ __device__ __noinline__ void choose_among_all(const RouterScoresArgs& a, WarpScr
   __syncwarp();
 }
 
+// (not NaN)
 __device__ __forceinline__ float warp_min(float v) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v = fminf(v, __shfl_xor_sync(kFull, v, off));
-  return v;
+  auto swap = [](int b) { return b ^ (b >> 31 & 0x7fffffff); };  // sorts like the float, and back
+  return __int_as_float(swap(__reduce_min_sync(kFull, swap(__float_as_int(v)))));
 }
 __device__ __forceinline__ float warp_max(float v) { return -warp_min(-v); }
 
@@ -636,8 +640,8 @@ __global__ void __launch_bounds__(kBlock, 3) router_scores_kernel(const RouterSc
   __shared__ int hist[256];
   __shared__ __align__(16) float bias_key[256];  // 1 + the bias's part of a key
   __shared__ float key_unit;                     // keys per unit of score
-  __shared__ bool masks_differ;                  // masked experts have an order of their own
-  __shared__ bool keyless;                       // biases too far apart for keys, or +inf: every token in fp64
+  __shared__ int bias_kind;                      // 1: masked experts have an order of their own
+                                                 // 2: biases too far apart for keys, every token in fp64
   __shared__ long long doubtful[kMaxDoubtful];   // tokens left for the end
   __shared__ int num_doubtful;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -691,28 +695,24 @@ __global__ void __launch_bounds__(kBlock, 3) router_scores_kernel(const RouterSc
       for (int i = 0; i < 8; ++i) b[i] = lane + 32 * i < E ? bias_of(a, lane + 32 * i) : __int_as_float(0x7fffffff);
       bias_range(b, grouped ? max(k, 2 * a.top_groups) : k, lo, hi);
       const float unit = kKeyRange / (1.0f + (hi - lo));
-      bool differ = false, pinned = false;
+      bool differ = false;
       // b - lo first: what is rounded is small beside the range
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const bool in = b[i] >= lo;  // (not a NaN, which counts as -inf)
         bias_key[lane + 32 * i] = in ? (b[i] - lo) * unit + 1.0f : -4e7f;
         if (b[i] < lo && b[i] != kNegInf) differ = true;
-        if (b[i] == -kNegInf) pinned = true;
       }
       differ = __any_sync(kFull, differ);
-      pinned = __any_sync(kFull, pinned);
       if (lane == 0) {
         key_unit = unit;
-        masks_differ = differ;
-        keyless = pinned || !(hi - lo <= 1e30f);
+        bias_kind = (differ ? 1 : 0) | (hi - lo <= 1e30f ? 0 : 2);
       }
     }
-  } else if (threadIdx.x == 0) {
-    masks_differ = keyless = false;
   }
   __syncthreads();
   const float unit = kScored ? key_unit : 0.0f;
+  const bool masks_differ = kScored && (bias_kind & 1), keyless = kScored && (bias_kind & 2);
   for (; p < passes; p += warps) {
     const long long t = p * kTokens + tok, tt = token_of(p);
     const bool live = t < a.num_tokens;  // the lanes of a token agree
@@ -752,7 +752,7 @@ __global__ void __launch_bounds__(kBlock, 3) router_scores_kernel(const RouterSc
     }
     if (p + warps < passes) load(token_of(p + warps));
     auto expert_of = [](uint32_t full_key) { return 255 - static_cast<int>(full_key & 255u); };
-    bool doubt = kScored && keyless;  // some comparison is not certain
+    bool doubt = keyless;  // some comparison is not certain
     unsigned kept = kFull;
     // ---- groups
     if (grouped) {
@@ -786,7 +786,11 @@ __global__ void __launch_bounds__(kBlock, 3) router_scores_kernel(const RouterSc
 #pragma unroll 1
             for (int i = 0; i < size; ++i) take(from[i]);
           }
-          merit[n] = size > 1 && second != 0 ? first + second : size > 1 ? 0 : first;  // 0: masked, or one left
+          merit[n] = first;  // 0: masked, or one left
+          if (size > 1) {
+            merit[n] = second == 0 ? 0 : first == kPinned ? kPinned : first + second;
+            if (second == 0 && first == kPinned) doubt = true;
+          }
         }
       }
       // a group is kept if fewer than top_groups come before it
@@ -822,8 +826,8 @@ __global__ void __launch_bounds__(kBlock, 3) router_scores_kernel(const RouterSc
         last_kept = min(last_kept, __shfl_xor_sync(kFull, last_kept, off));
         first_dropped = max(first_dropped, __shfl_xor_sync(kFull, first_dropped, off));
       }
-      // a tie in merit as well; of 0 only if the masks make a difference
-      doubt |= last_kept - first_dropped <= 2 * kNear && (last_kept != 0 || masks_differ);
+      // a tie in merit as well; not of +inf, and of 0 only if the masks make a difference
+      doubt |= last_kept - first_dropped <= 2 * kNear && last_kept != kPinned && (last_kept != 0 || masks_differ);
       if (size % 4 == 0) {  // the kept groups' first experts, in order
 #pragma unroll
         for (int n = 0; n < kMine; ++n) {
@@ -917,21 +921,30 @@ __global__ void __launch_bounds__(kBlock, 3) router_scores_kernel(const RouterSc
 #pragma unroll
     for (int r = 0; r < K; ++r)
       if (j == r) own = best[r];
-    const bool near = j < k && below >= 256 && (own >> 8) - (below >> 8) <= kNear;
+    constexpr uint32_t kDistance = kScored ? kNear : 0;
+    const bool near = j < k && below >= 256 && (own >> 8) - (below >> 8) <= kDistance && below >> 8 != kPinned >> 8;
     const bool same = near && same_inputs(a, tt, expert, expert_of(below));
     if (near && !same) doubt = true;
     // At the border only the first behind it has been looked at.  Where it is the last one's equal, others
     // as near may be above both.
     const unsigned equal = __ballot_sync(kFull, same && j == k - 1);
     if (equal) {
-      const bool mine = (equal >> (lane & ~(kLanes - 1)) & ((1u << kLanes) - 1)) != 0;
+      bool mine = (equal >> (lane & ~(kLanes - 1)) & ((1u << kLanes) - 1)) != 0;
+      if (!kFp32 && mine && a.bias == nullptr) {
+        // Equal logits are common in bf16, where another logit is |x| 2^-8 away at least: mostly more than
+        // the 31 steps of keys (4 for logits) within which it could be one of those (32768 x 256 in bf16, no
+        // bias: 18.6 us, 22.9 if every token with equals at its border looks)
+        const float x = fabsf(load_logit(a, tt, expert_of(last))), q = static_cast<float>(last >> 8);
+        if (kScored ? (kSigmoid ? x >= 0x1p-8f && x <= 8.0f : x <= 64.0f && q * x >= 16384.0f) : x >= 0x1p-8f && q > 1.0f)
+          mine = false;
+      }
 #pragma unroll 1
       for (int i = 0; i < vecs && mine && !doubt; ++i) {
         uint32_t key[4];
         load_keys(i, key);
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          if (key[c] < last && key[c] >= 256 && (last >> 8) - (key[c] >> 8) <= kNear &&
+          if (key[c] < last && key[c] >= 256 && (last >> 8) - (key[c] >> 8) <= kDistance &&
               !same_inputs(a, tt, expert_of(last), expert_of(key[c])))
             doubt = true;
       }

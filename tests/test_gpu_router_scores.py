@@ -337,3 +337,27 @@ def test_infinite_logits_by_sigmoid():
         check(x, 6, "sigmoid", b, 8, 3)
         check(x[:, :32].contiguous(), 5, "sigmoid", None if b is None else b[:32].contiguous(), 32, 7)
     check(x.to(torch.bfloat16), 8, "sigmoid")
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("mask", [torch.finfo(torch.float32).min, -1e9, -1e3])
+def test_pinned_and_masked_experts_in_one_group(score, mask):
+    # +inf and a finite mask make a merit of +inf, as +inf and any other bias
+    x, bias = make(200, 64, bias=0.1, seed=27)
+    e = torch.arange(64, device="cuda")
+    bias = torch.where((e // 4 % 4 == 1) & (e % 4 != 2), mask, bias)
+    bias[[0, 6, 22, 33, 34]] = INF
+    for groups in (16, 8, 32):
+        for keep in (1, 2, 3, 5, 7):
+            check(x, 2, score, bias, groups, keep)
+            check(x, min(8, 64 // groups * keep), score, bias, groups, keep)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,keep", [(1, 1), (8, 4)])
+@pytest.mark.parametrize("std", [0.002, 1.5, 12.0])
+def test_many_equal_logits_in_bf16(score, groups, keep, std):
+    x, b = make(20000, 256, "bfloat16", 0.05, std=std, seed=8)
+    for bias in (None, b, b.to(torch.bfloat16).float() * 0.0):
+        for k in (1, 8):
+            check(x, k, score, bias, groups, keep)
