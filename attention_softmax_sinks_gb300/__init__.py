@@ -347,7 +347,8 @@ def sink_attn_decode_shared(q, paged_k, paged_v, page_table, kv_lens, sinks, gro
     q [B, Hq, 64] bf16, paged_k/v [P, Hkv, 16, 64] bf16, page_table [B, max_pages] int32,
     kv_lens [B] int32 (whole sequences), sinks [Hq] fp32.  group_offsets [G + 1] int32: group g
     is sequences [group_offsets[g], group_offsets[g + 1]); shared_pages [G] int32: the pages that
-    begin the page tables of all its sequences, at most max_shared_pages.
+    begin the page tables of all its sequences, at most max_shared_pages (best near the longest of them;
+    the page table may be as wide as the model's context).
     splits: (shared, own) along the keys, default sink_attn_decode_shared_splits; (0, 1): every
     sequence reads all its pages for itself, in one launch.  workspace: (partial_o [B, shared + own,
     Hq, 64], partial_lse [B, shared + own, Hq]) fp32, allocated when not given, not used for (0, 1).  Returns (out [B, Hq, 64] bf16, lse [B, Hq] fp32 or None)."""

@@ -440,14 +440,15 @@ void sink_attn_decode_shared_splits(int batch, int num_groups, int num_qo_heads,
       max_pages > 0) {
     if (num_sms <= 0) num_sms = 152;
     // Few pages: every sequence by itself, one launch, if that is estimated to be faster.  By itself:
-    // 5.5 us and, for 1000 pages of 8 KV heads, 4.5, or 9 where more than 8 sequences read the same
-    // ones (5 if they are short, too); together: three launches and the run along the prompt, whose
-    // groups follow one another.  (us by itself / together, 64/8 heads, 64 tokens of their own: 4
+    // 5.5 us and, for 1000 shared pages of 8 KV heads, 4.5, or 9 where more than 8 sequences read the
+    // same ones (5 if they are short, too); together: three launches and the run along the prompt, whose
+    // groups follow one another.  The own pages are read in both, and what the page table has room for
+    // says nothing of them.  (us by itself / together, 64/8 heads, 64 tokens of their own: 4
     // sequences that share 2048 tokens 8.3 / 11.9, 4096 tokens 10.5 / 12.8, 8192 tokens 14.8 / 14.5;
     // 16 that share 256 tokens 6.1 / 11.8, 1024 tokens 15.4 / 12.3; 64 in 4 groups 256 tokens 7.5 /
     // 13.5, 1024 tokens 30 / 17.6; 4 in 4 groups 16384 tokens 22 / 35.)
-    const double kpages = 1e-3 / 8 * batch * num_kv_heads * max_pages;
-    const double alone = 5.5 + kpages * (batch <= 8LL * num_groups ? 4.5 : max_pages < 32 ? 5.0 : 9.0);
+    const double kpages = 1e-3 / 8 * batch * num_kv_heads * max_shared_pages;
+    const double alone = 5.5 + kpages * (batch <= 8LL * num_groups ? 4.5 : max_shared_pages < 32 ? 5.0 : 9.0);
     const double side = num_groups * (num_kv_heads / 8.0);
     const double together = 10.5 + (batch < 64 ? 0.07 * batch : 4.5) + 6.5e-3 * max_shared_pages * (side > 1.0 ? side : 1.0);
     if (alone < together) {

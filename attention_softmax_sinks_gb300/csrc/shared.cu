@@ -816,11 +816,17 @@ int shared_ctas(int batch, int num_groups, int group, int hkv, int max_shared_pa
                 long long own_ctas, int sms) {
   // SM time (us) of the shared part, if every group's prompt is the longest: 1.28 for a tile of keys
   // of two row tiles, 0.75 of one.  Of the own parts, if they are half as long as the page table has
-  // room for: three CTAs of 3 us and 35 KB per us beside one another.
+  // room for, but of 48 pages at most: three CTAs of 3 us and 35 KB per us beside one another.  A table
+  // may be as wide as the model's context, for a step captured once; SMs left to own parts that
+  // are not there cost a factor, too few of them little, as own parts run where the shared part has ended
+  // (64 sequences that share 32768 tokens, 1024 of their own: 56.5 us with a table of 2108 pages and 57.4 with
+  // 8192, without the limit 383; 32 sequences of 32/8 heads in 2 groups on 11200 tokens, own parts
+  // to 3000: 41.6 us, 35.3 without).
   const bool one = static_cast<long long>(batch) * group <= static_cast<long long>(kBlockQ) * num_groups;
   const double tiles = static_cast<double>(shared_row_tiles(batch, num_groups, group)) * hkv * key_tiles_of(max_shared_pages);
   const double work = tiles * (one ? 0.75 : 1.28);
-  const double own_bytes = 0.5 * (max_pages - max_shared_pages) * kPageSize * 256.0 * hkv * batch;
+  const int own_pages = max_pages - max_shared_pages;
+  const double own_bytes = 0.5 * (own_pages < 96 ? own_pages : 96) * kPageSize * 256.0 * hkv * batch;
   const double cta = 3.0 + own_bytes / own_ctas / 35e3;
   const double own = own_ctas * cta / 3.0;
   // x SMs for the shared part: what the own parts have left at its end then has all SMs

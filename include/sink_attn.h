@@ -176,7 +176,9 @@ sa_status sink_attn_decode_shared(const void* q, const void* paged_k, const void
                                   cudaStream_t stream);
 
 /* Host-only helper: split counts for sink_attn_decode_shared from what the host knows of the
- * batch (bounds: max_shared_pages, and max_pages of whole sequences); 0 and 1 for few pages.
+ * batch (bounds: max_shared_pages, and max_pages of whole sequences); 0 and 1 for few shared pages.
+ * max_shared_pages should be near the longest prompt of the batch: the counts, and what the call
+ * gives to either part, go by it.  max_pages may be as wide as the model's context.
  * num_sms 0: 152.  No CUDA call. */
 void sink_attn_decode_shared_splits(int batch, int num_groups, int num_qo_heads, int num_kv_heads,
                                     int max_shared_pages, int max_pages, int num_sms,

@@ -383,3 +383,22 @@ def test_offsets_that_go_back(splits, times):
     assert sa.sink_attn_device_status(True) == 5
     got = call(a, splits=splits)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("groups", [[(4, 128)], [(30, 200), (1, 0), (9, 77)], [(5, 3)]])
+def test_a_table_as_wide_as_the_context(groups):
+    # captured once, replayed with other lengths
+    import attention_softmax_sinks_gb300 as sa
+    n = sum(c for c, _ in groups)
+    a = make(groups, [40 + 11 * i % 60 for i in range(n)], 64, 8, extra_width=8000)
+    check(a, *call(a))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out, lse = sa.sink_attn_decode_shared(**a)
+    for less in (20, 3, 15):
+        a["kv_lens"] -= less
+        a["q"].copy_(a["q"].flip(1))
+        g.replay()
+        torch.cuda.synchronize()
+        assert sa.sink_attn_device_status(True) == 0
+        check(a, out, lse)

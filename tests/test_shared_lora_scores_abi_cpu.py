@@ -72,6 +72,22 @@ def test_splits_of_shared_prompts():
     assert f(4, 1, 64, 8, 16, 20) == (0, 1) and f(64, 1, 64, 8, 2048, 2112)[0] > 0
 
 
+def test_splits_go_by_the_prompts_and_not_by_the_tables_width():
+    import attention_softmax_sinks_gb300 as sa
+    f = sa.sink_attn_decode_shared_splits
+    for batch in (1, 4, 16, 37, 64, 512):
+        for groups in (1, 5, 8):
+            for hq, hkv in ((64, 8), (40, 8), (28, 4), (16, 1)):
+                for shared in (1, 16, 128, 501, 2048):
+                    tight = f(batch, groups, hq, hkv, shared, shared + 96)
+                    for width in (shared + 100, 4096, 8192, 65536):
+                        wide = f(batch, groups, hq, hkv, shared, width)
+                        assert wide[0] == tight[0] and wide[1] >= tight[1]
+                    # few of their own: SMs are moved between the parts, a slot or two with them
+                    assert (f(batch, groups, hq, hkv, shared, shared + 4)[0] == 0) == (tight[0] == 0)
+    assert f(4, 1, 64, 8, 128, 8192) == (0, 1)
+
+
 def _lora(lib, **kw):
     a = dict(x=FAKE, w=FAKE, bias=FAKE, a=FAKE, b=FAKE, scale=FAKE, idx=FAKE, m=5, n=640, k=256, rank=16, adapters=3,
              ws=FAKE, out=FAKE)
