@@ -24,7 +24,8 @@
 //    which run ahead of the product; B_i comes by TMA in boxes of 16 ranks.  So any mix of
 //    adapters in a tile is right, and a tile of one adapter costs R more columns of K.
 //    Zeros do not keep out an infinity or NaN of another request's B_i: an element that comes out
-//    not finite is computed once more by itself, from its own operands only.
+//    not finite is computed once more by itself, from its own operands only, unless its row has a
+//    NaN of its own.
 //    Many tokens: pairs of CTAs (cta_group::2, 256 tokens), which stage half of W's columns each.
 //    Few tiles: clusters of 2, 4 or 8 CTAs share one tile's K and adapters and add their accumulators
 //    up through each other's shared memory.  What bounds them is not W's way from memory but the
@@ -714,38 +715,100 @@ __device__ __forceinline__ void seed_bias(uint32_t taddr, const uint16_t* bias, 
   }
 }
 
-// Element (m, n) by itself, from the operands of token m alone: for elements that an adapter of
-// another token in the tile made not finite (0 times infinity).
-__device__ __noinline__ float single_element(const LoraArgs& a, int m, int n) {
-  auto dot8 = [](const uint16_t* p, const uint16_t* q, float sum) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p)), v = __ldg(reinterpret_cast<const uint4*>(q));
-    const uint32_t us[4] = {u.x, u.y, u.z, u.w}, vs[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ bool bf16_nan(uint32_t pair) {  // one of two
+  return (pair & 0x7FFFu) > 0x7F80u || (pair & 0x7FFF0000u) > 0x7F800000u;
+}
+
+// Part (of 32 lanes) of x[m] W^T for columns n .. n + kCols - 1 of W, and of t B^T behind it.
+template <int kCols, typename St>
+__device__ __forceinline__ void row_products(const LoraArgs& a, const uint16_t* x, int id, int n, St&& st, float (&sum)[kCols]) {
+  const int lane = threadIdx.x & 31;
+  const uint16_t* w = a.w + static_cast<long long>(n) * a.K;
+#pragma unroll kCols == 1 ? 4 : 1
+  for (int k = 8 * lane; k < a.K; k += 256) {
+    const uint4 xv = __ldg(reinterpret_cast<const uint4*>(x + k));
+    const uint32_t xs[4] = {xv.x, xv.y, xv.z, xv.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      sum = fmaf(__uint_as_float(us[i] << 16), __uint_as_float(vs[i] << 16), sum);
-      sum = fmaf(__uint_as_float(us[i] & 0xFFFF0000u), __uint_as_float(vs[i] & 0xFFFF0000u), sum);
-    }
-    return sum;
-  };
-  float sum = a.bias ? __uint_as_float(static_cast<uint32_t>(__ldg(a.bias + n)) << 16) : 0.0f;
-  for (int k = 0; k < a.K; k += 8)
-    sum = dot8(a.x + static_cast<long long>(m) * a.K + k, a.w + static_cast<long long>(n) * a.K + k, sum);
-  const int id = __ldg(a.adapter + m);
-  if (id >= 0 && id < a.num_adapters) {
-    const uint16_t* b = a.lora_b + (static_cast<long long>(id) * a.N + n) * a.R;
-    for (int r = 0; r < a.R; ++r) {
-      uint32_t st;  // as the tensor core gets it
-      if (a.t) {
-        st = __ldcg(a.t + static_cast<long long>(m) * a.R + r);
-      } else {
-        float v = 0.0f;
-        for (int s = 0; s < a.splits; ++s) v += __ldcg(a.t_parts + (static_cast<long long>(s) * a.M + m) * a.R + r);
-        st = pack_bf16x2(v, 0.0f);
+    for (int i = 0; i < kCols; ++i) {
+      const uint4 wv = __ldg(reinterpret_cast<const uint4*>(w + static_cast<long long>(i) * a.K + k));
+      const uint32_t ws[4] = {wv.x, wv.y, wv.z, wv.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sum[i] = fmaf(__uint_as_float(xs[j] << 16), __uint_as_float(ws[j] << 16), sum[i]);
+        sum[i] = fmaf(__uint_as_float(xs[j] & 0xFFFF0000u), __uint_as_float(ws[j] & 0xFFFF0000u), sum[i]);
       }
-      sum = fmaf(__uint_as_float(st << 16), __uint_as_float(static_cast<uint32_t>(__ldg(b + r)) << 16), sum);
     }
   }
-  return sum;
+  if (id >= 0) {
+    const uint16_t* b = a.lora_b + (static_cast<long long>(id) * a.N + n) * a.R;
+    for (int r = lane; r < a.R; r += 32) {
+      const float t = __uint_as_float(st(r) << 16);
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) sum[i] = fmaf(t, __uint_as_float(static_cast<uint32_t>(__ldg(b + i * a.R + r)) << 16), sum[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kCols; ++i)
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], off);
+}
+
+// Outputs that are not finite once more, each from the operands of its own token alone: an adapter of
+// another token in the tile may have made them so (0 times infinity).  By a whole warp, whose lane i
+// has stored row row0 + i; bit c of its `odd`: columns n0 + 8 c .. + 7 are not all finite.  A row with a NaN
+// of its own is NaN throughout already and stays: a batch may be padded with such rows (4096 -> 2880, 333
+// tokens, one of them NaN: as without; a lane by itself for each element, 5.9 ms).  An adapter with a NaN
+// in one output feature costs the others' rows a column: 2880 -> 5120, 64 tokens, 0.15 ms.
+__device__ __noinline__ void repair_rows(const LoraArgs& a, unsigned odd, int row0, int n0) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();  // the other lanes' stores are visible
+  for (unsigned rows = __ballot_sync(0xffffffffu, odd != 0); rows; rows &= rows - 1) {
+    const int i = __ffs(rows) - 1, m = row0 + i;
+    const uint16_t* x = a.x + static_cast<long long>(m) * a.K;
+    int id = __ldg(a.adapter + m);
+    if (id >= a.num_adapters) id = -1;
+    auto st = [&](int r) -> uint32_t {  // as the tensor core gets it
+      if (a.t) return __ldcg(a.t + static_cast<long long>(m) * a.R + r);
+      float v = 0.0f;
+      for (int s = 0; s < a.splits; ++s) v += __ldcg(a.t_parts + (static_cast<long long>(s) * a.M + m) * a.R + r);
+      return pack_bf16x2(v, 0.0f) & 0xFFFFu;
+    };
+    bool looked = false;
+    for (unsigned blocks = __shfl_sync(0xffffffffu, odd, i); blocks; blocks &= blocks - 1) {
+      const int n = n0 + 8 * (__ffs(blocks) - 1);
+      uint16_t* out = a.out + static_cast<long long>(m) * a.N + n;
+      const uint32_t now = lane < 8 ? *reinterpret_cast<const volatile uint16_t*>(out + lane) : 0;
+      const unsigned which = __ballot_sync(0xffffffffu, (now & 0x7F80u) == 0x7F80u);
+      if (!looked && __ballot_sync(0xffffffffu, bf16_nan(now)) == 0xFFu) {
+        bool nan = false;
+        for (int k = 8 * lane; k < a.K; k += 256) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(x + k));
+          nan |= bf16_nan(v.x) || bf16_nan(v.y) || bf16_nan(v.z) || bf16_nan(v.w);
+        }
+        if (id >= 0)
+          for (int r = lane; r < a.R; r += 32) nan |= bf16_nan(st(r));
+        if (__any_sync(0xffffffffu, nan)) break;
+        looked = true;
+      }
+      float mine = 0.0f;
+      if (which == 0) continue;
+      if ((which & (which - 1)) == 0) {  // one column
+        float sum[1] = {};
+        row_products(a, x, id, n + __ffs(which) - 1, st, sum);
+        mine = sum[0];
+      } else {
+        float sum[8] = {};
+        row_products(a, x, id, n, st, sum);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          if (lane == c) mine = sum[c];
+      }
+      if (which >> lane & 1) {
+        if (a.bias) mine += __uint_as_float(static_cast<uint32_t>(__ldg(a.bias + n + lane)) << 16);
+        out[lane] = static_cast<uint16_t>(pack_bf16x2(mine, 0.0f) & 0xFFFFu);
+      }
+    }
+  }
 }
 
 // A ring stage holds `sub` blocks of 64 values of K: small tiles' blocks are a few KB, and a stage's
@@ -763,20 +826,14 @@ __host__ __device__ constexpr int stage_count(int mode, int box_rows, int wrows)
   return n > kMaxStages ? kMaxStages : n;
 }
 // Accumulators r of row m, columns n .. n + 7, to the output (where n < N; N is a multiple of 8).
-__device__ __forceinline__ void store8(const LoraArgs& a, int m, int n, const float (&r)[8]) {
+// Is one of them not finite: a bit for the block of columns (the c-th of a tile, of eight).
+__device__ __forceinline__ unsigned store8(const LoraArgs& a, int m, int n, int c, const float (&r)[8]) {
   float odd = 0.0f;  // NaN if some element is not finite
 #pragma unroll
   for (int v = 0; v < 8; ++v) odd = fmaf(r[v], 0.0f, odd);
-  float f[8];
-#pragma unroll
-  for (int v = 0; v < 8; ++v) f[v] = r[v];
-  if (odd != 0.0f) {
-#pragma unroll
-    for (int v = 0; v < 8; ++v)
-      if (!(fabsf(f[v]) <= 3.402823466e38f)) f[v] = single_element(a, m, n + v);
-  }
   *reinterpret_cast<uint4*>(a.out + static_cast<long long>(m) * a.N + n) =
-      make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+      make_uint4(pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3]), pack_bf16x2(r[4], r[5]), pack_bf16x2(r[6], r[7]));
+  return odd != 0.0f ? 1u << c : 0u;
 }
 
 __host__ __device__ constexpr int acc_columns(int bn) { return (bn + 31) / 32 * 32; }
@@ -784,6 +841,7 @@ __host__ __device__ constexpr int t_bufs(int bn) {
   const int n = (static_cast<int>(kTmemCols) - 2 * acc_columns(bn)) / kTCols;
   return n > kMaxTBufs ? kMaxTBufs : n;
 }
+static_assert(kMaxBlockN / 8 <= 32, "a bit for eight columns");
 static_assert(t_bufs(kMaxBlockN) >= 2, "two buffers of T behind the accumulators");
 
 // RC: chunks of 16 ranks (a rank in between counts as the next size: the boxes behind R read zeros).
@@ -1097,6 +1155,7 @@ __global__ void __launch_bounds__(kThreads, kMode == kModePair || RC > 4 ? 1 : 2
       tc_fence_after();
       if constexpr (kSplit) break;  // the one tile: added up below
       const uint32_t acc = lane_base + b * acc_stride;
+      unsigned odd = 0;
       if (m0 + 32 * q < a.M) {  // some row of this warp exists
 #pragma unroll 1
         for (int c = 0; c < bn; c += 16) {
@@ -1108,7 +1167,7 @@ __global__ void __launch_bounds__(kThreads, kMode == kModePair || RC > 4 ? 1 : 2
             float f[8];
 #pragma unroll
             for (int v = 0; v < 8; ++v) f[v] = __uint_as_float(r[h + v]);
-            if (row < a.M && n0 + c + h < a.N) store8(a, row, n0 + c + h, f);
+            if (row < a.M && n0 + c + h < a.N) odd |= store8(a, row, n0 + c + h, (c + h) / 8, f);
           }
         }
       }
@@ -1118,6 +1177,7 @@ __global__ void __launch_bounds__(kThreads, kMode == kModePair || RC > 4 ? 1 : 2
       tc_fence_before();
       __syncwarp();
       if (lane == 0) pair_arrive<kPair>(acc_empty0 + 8 * b);
+      if (__any_sync(0xffffffffu, odd != 0)) repair_rows(a, odd, m0 + 32 * q, n0);
     }
   }
 
@@ -1152,7 +1212,8 @@ __global__ void __launch_bounds__(kThreads, kMode == kModePair || RC > 4 ? 1 : 2
     }
     __syncwarp();
     cluster_sync();
-    if (warp_live && !*abort_flag) {
+    if (warp_live && !__any_sync(0xffffffffu, *abort_flag != 0)) {
+      unsigned odd = 0;
 #pragma unroll 1
       for (int c = part * cw + 8 * half; c < min((part + 1) * cw, bn); c += 16) {
         uint32_t v[8];
@@ -1181,9 +1242,10 @@ __global__ void __launch_bounds__(kThreads, kMode == kModePair || RC > 4 ? 1 : 2
             sum[6] += hi.z;
             sum[7] += hi.w;
           }
-          store8(a, row, n0 + c, sum);
+          odd |= store8(a, row, n0 + c, c / 8, sum);
         }
       }
+      if (__any_sync(0xffffffffu, odd != 0)) repair_rows(a, odd, mt * kBM + 32 * q, n0);
     }
   }
   tc_fence_before();

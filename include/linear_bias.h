@@ -48,7 +48,9 @@ sa_status linear_bias(const void* x, const void* w, const void* bias, int m, int
  *
  * and without the last term where adapter_idx[m] is negative.  x A^T is summed in fp32, times
  * s_a rounded once to bf16 for the second product; everything adds up in the fp32 accumulator
- * that starts from the bias, and the result rounds once to bf16.
+ * that starts from the bias, and the result rounds once to bf16.  Rows stand alone: a NaN or an infinity
+ * in one token's x or adapter does not reach others (outputs of theirs that it would have reached
+ * are computed once more, which takes longer the more of them there are).
  *
  *  x, w, bias, out, m, n, k: as for linear_bias
  *  lora_a       bf16 [num_adapters, rank, k], lora_b bf16 [num_adapters, n, rank], 16-byte

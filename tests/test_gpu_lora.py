@@ -187,3 +187,30 @@ def test_repeated_calls_and_graph_replay():
     check(a, out)
     check({**a, "x": out[:, :512].contiguous()}, out2)
     assert sa.sink_attn_device_status(True) == 0
+
+
+@pytest.mark.parametrize("name", ["one token", "rank 24", "rank 128", "runs", "decode, 64 tokens", "clusters, odd sizes",
+                                  "clusters, two row blocks", "pairs, mixed", "pairs, rank 128", "pairs, rank 24"])
+def test_rows_and_adapters_that_are_not_finite(name):
+    # rows of NaN (what pads a batch), infinite ones, adapters with a NaN in either factor: each row as by itself
+    m, k, n, r, l, idx = CASES[name]
+    a = make(m, k, n, r, l, idx, seed=len(name))
+    inf = float("inf")
+    if m > 1:
+        a["x"][0] = NAN
+        a["adapter_idx"][0] = -1
+        a["x"][m // 2, k // 3] = NAN
+        a["x"][m // 3, 5] = inf
+        a["x"][-1, 0], a["x"][-1, 1] = inf, -inf
+    used = sorted(set(a["adapter_idx"].tolist()) - {-1})
+    a["lora_b"][used[0], 7, 3] = NAN
+    a["lora_b"][used[-1], n - 1, 0] = inf
+    if len(used) > 2:
+        a["lora_b"][used[1]] = NAN
+        a["lora_a"][used[2], 1, 2] = NAN
+    out = call(a).double()
+    ref, bound = reference(a)
+    good = torch.isfinite(ref)
+    assert torch.equal(torch.isnan(out), torch.isnan(ref))
+    assert torch.equal(torch.isfinite(out), good) and torch.equal(out[torch.isinf(ref)], ref[torch.isinf(ref)])
+    assert bool(((out - ref).abs() <= bound)[good].all())
