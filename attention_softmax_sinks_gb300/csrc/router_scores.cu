@@ -86,6 +86,36 @@ __device__ __forceinline__ float weight_of(float x, float ref, float inv_sum) {
   return kSigmoid ? 1.0f / (1.0f + expf(-x)) : expf(x - ref) * inv_sum;
 }
 
+// The chosen experts' scores (of logits x, a token's on kLanes neighbouring lanes; -inf behind the
+// k-th) and their sum, for the weights.  Renormalised weights keep their ratios where scores fall below
+// fp32's range, as a bias or groups can choose experts far below the largest: there they are taken
+// relative to the largest chosen one, s_i / s_m = e^(x_i - x_m) (1 + e^x_m) / (1 + e^x_i) by sigmoid, without
+// the fraction by softmax.  (A sum of 1/2 or more leaves nothing above 2^-126 out.)
+struct Chosen {
+  float score, sum;
+};
+template <bool kSigmoid>
+__device__ __noinline__ Chosen vanishing_scores(float x, Chosen c) {
+  float top = x;
+#pragma unroll
+  for (int off = 1; off < kLanes; off <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+  float r = expf(x - top);
+  if (kSigmoid) r *= (1.0f + expf(top)) / (1.0f + expf(x));
+  float sum = r;
+#pragma unroll
+  for (int off = 1; off < kLanes; off <<= 1) sum += __shfl_xor_sync(kFull, sum, off);
+  return c.sum < 0.5f && top > kNegInf ? Chosen{r, sum} : c;
+}
+template <bool kSigmoid>
+__device__ __forceinline__ Chosen chosen_scores(float x, float ref, float inv_sum, bool renormalize) {
+  Chosen c;
+  c.score = c.sum = weight_of<kSigmoid>(x, ref, inv_sum);
+#pragma unroll
+  for (int off = 1; off < kLanes; off <<= 1) c.sum += __shfl_xor_sync(kFull, c.sum, off);
+  if (renormalize && __any_sync(kFull, x > kNegInf && c.score < 0x1p-100f && c.sum < 0.5f)) c = vanishing_scores<kSigmoid>(x, c);
+  return c;
+}
+
 // sum exp(x - ref), added in pairs: a term is rounded log2(N) times.
 template <int N>
 __device__ __forceinline__ float exp_sum(const float* x, float ref) {
@@ -623,11 +653,8 @@ __device__ __noinline__ void settle(const RouterScoresArgs& a, WarpScratch& ws, 
 #pragma unroll
   for (int r = 0; r < 8; ++r)
     if (lane == r) expert = picked[r];
-  float mine = lane < k ? weight_of<kSigmoid>(load_logit(a, t, expert), ref, inv_sum) : 0.0f;
-  float sum = mine;
-#pragma unroll
-  for (int off = 1; off < kLanes; off <<= 1) sum += __shfl_xor_sync(kFull, sum, off);
-  if (lane < k) write_choice(a, hist, t, lane, expert, mine, sum);
+  const Chosen c = chosen_scores<kSigmoid>(lane < k ? load_logit(a, t, expert) : kNegInf, ref, inv_sum, a.renormalize);
+  if (lane < k) write_choice(a, hist, t, lane, expert, c.score, c.sum);
   __syncwarp();
 }
 
@@ -954,11 +981,8 @@ __global__ void __launch_bounds__(kBlock, 3) router_scores_kernel(const RouterSc
     const unsigned doubts = __ballot_sync(kFull, doubt && live);
     doubt = (doubts >> (lane & ~(kLanes - 1)) & ((1u << kLanes) - 1)) != 0;
     // ---- weights
-    const float mine = j < k ? weight_of<kSigmoid>(load_logit(a, tt, expert), ref, inv_sum) : 0.0f;
-    float sum = mine;
-#pragma unroll
-    for (int off = 1; off < kLanes; off <<= 1) sum += __shfl_xor_sync(kFull, sum, off);
-    if (live && !doubt && j < k) write_choice(a, hist, t, j, expert, mine, sum);
+    const Chosen c = chosen_scores<kSigmoid>(j < k ? load_logit(a, tt, expert) : kNegInf, ref, inv_sum, a.renormalize);
+    if (live && !doubt && j < k) write_choice(a, hist, t, j, expert, c.score, c.sum);
     __syncwarp();  // the keys have been read
     if (doubt && live && j == 0) {  // left for the end: in the list, or marked where it is full
       const int at = atomicAdd(&num_doubtful, 1);

@@ -72,7 +72,7 @@ sa_status moe_router(const void* x, const void* w_router, const void* bias, int 
  *     groups of num_experts / num_groups consecutive experts: the merit of a group is the sum of
  *     its two largest v (of one expert: its v); the top_groups groups of largest merit are kept
  *     S   = the top_k experts of the kept groups with the largest v, largest first
- *     w_r = scale * s_S[r]  (/ sum_r' s_S[r'] with renormalize; 0 where that sum is 0)
+ *     w_r = scale * s_S[r]  (/ sum_r' s_S[r'] with renormalize; 0 where every chosen score is 0)
  *
  * The choice is that of exact arithmetic on the logits and biases as given, equal values in
  * favour of the lower index; without a bias it is the logits' own order (within the groups kept).

@@ -361,3 +361,23 @@ def test_many_equal_logits_in_bf16(score, groups, keep, std):
     for bias in (None, b, b.to(torch.bfloat16).float() * 0.0):
         for k in (1, 8):
             check(x, k, score, bias, groups, keep)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_chosen_scores_that_vanish_in_fp32(score, dtype):
+    # a bias chooses experts far below the largest: their weights add up to scale all the same
+    x, _ = make(300, 64, dtype, std=3.0, seed=28)
+    bias = torch.zeros(64, device="cuda")
+    bias[8:] = -2.0
+    bias[3] = -1.5
+    x[:, 8:] += 60
+    for below in (0.0, 40.0, 90.0, 130.0, 300.0):
+        y = x.clone()
+        y[:, :8] -= below
+        y[::7, 2:8] = -INF
+        y[5, :8] = -INF
+        for k, groups, keep in ((4, 1, 1), (8, 1, 1), (3, 8, 1), (8, 16, 3)):
+            check(y, k, score, bias, groups, keep, scale=2.5)
+            check(y, k, score, bias, groups, keep, renorm=False)
+    check((x - 500).clamp(max=-100), 8, score)
