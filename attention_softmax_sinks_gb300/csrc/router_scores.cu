@@ -9,23 +9,28 @@
 // values in favour of the lower index:
 //  - Eight lanes per token; lane j holds experts 4 (j + 8 i) + c.  What is ordered becomes a
 //    32-bit key: 24 bits of fixed point and 255 - expert.  The fixed point holds s + bias over its
-//    range; without bias and groups x - max x in [-32, 0] (scores and logits have the same order).
+//    range, which leaves masked experts out (bias_range; their key is 0), and all ones for a bias of +inf;
+//    without bias and groups x - max x in [-32, 0] (scores and logits have the same order).
 //    Keys sort with one min and one max per comparison: sorting networks per lane, then three
 //    rounds of merging between lanes.  (A lane's keys differ from each other without j, which is
 //    added to the few that leave the lane.)
 //  - A key is off by a few units from what it stands for.  Where the last group kept and the first
 //    dropped, or two neighbours among the chosen, or the last chosen and the first not chosen are
-//    closer than that, and not equal in logit and bias (nor, behind an equal one not chosen, any
-//    other as close), the experts within reach of that border
-//    are compared once more, a lane for each: scores by sigmoid in pairs of fp32, and where that
-//    does not settle it, or by softmax, in fp64 (one token in a thousand of 256 experts in 8 groups
-//    with logits in 32 bits); more than 32 of them by a walk over all experts in fp64.
+//    closer than that, and not equal in logit and bias (or, behind an equal one not chosen, any other
+//    is as close), the experts within reach of that border are compared once more, a lane for
+//    each: scores by sigmoid in pairs of fp32, and where that does not settle it, or by softmax, in
+//    fp64 (one token in a thousand of 256 experts in 8 groups with logits in 32 bits); more than 32 of
+//    them by a walk over all experts in fp64.
 //
-// What bounds it: at many tokens the instructions, some 1600 for four tokens of 256 experts, and
-// behind them the latency of the doubtful tokens, not the logits' way from memory: 32768 tokens of
-// 256 experts in fp32, 8 of them from 4 of 8 groups, take 30.8 us, 22 of them without the doubtful
-// ones, 5.2 for the bytes alone (33.5 with all of the doubtful in fp64; with 32 lanes per token 90).
-// At few tokens the latency of a launch and one pass: 64 tokens 5.9 us.
+// What bounds it: at many tokens the instructions, some 1700 for four tokens of 256 experts (issue slots
+// are taken 56% of the time while an SM works), and behind them the latency of the doubtful tokens and
+// the last, partial round, not the logits' way from memory: 32768 tokens of 256 experts in fp32, 8 of
+// them from 4 of 8 groups, by sigmoid take 29.7 us, 5.2 for the bytes alone (with 32 lanes per token 90); in
+// bf16 35.4, as more of them are near one another.  By softmax 47: more scores are small and near, and
+// the doubtful go to fp64; without bias and groups, where keys hold logits, 24.6, and 20.2 in bf16.
+// Masked experts (1 in 16 by -inf, the least fp32 number or -1e4): 31 and 47.
+// At few tokens the latency of a launch and one pass: 64 tokens 6.1 us; 25.6 with a token that has more
+// than 32 experts near its border.
 #include <cstdint>
 
 #include "ptx.cuh"

@@ -35,14 +35,16 @@
 // Slots that a unit does not use get lse = -inf and are not read by the merge; those of sequences
 // that share nothing are marked by the own parts' kernel.
 //
-// What bounds it: the softmax's issue slots and exponentials.  A tile of 128 keys and two row tiles
-// takes 1.28 us of an SM, 0.68 of which the tensor core needs (64 sequences of 64/8 heads that
-// share 32768 tokens, with 500 of their own each: 56.5 us, of which 46 are this kernel on 128 SMs
-// beside the own parts on the others; each sequence by itself would read 64 times as much, 4.3 GB).
+// What bounds it: the chain of a tile's steps (scores, maximum, exponentials, P, product), one row tile's
+// beside the other's.  A tile of 128 keys and two row tiles takes 1.28 us of an SM, 0.68 of which the
+// tensor core needs; while an SM works, issue slots are taken 40% of the time, the exponentials' pipe
+// 39%, the tensor core 39%: none is near its limit (64 sequences of 64/8 heads that share 32768 tokens,
+// with 500 of their own each: 57.5 us, of which 46 are this kernel on 128 SMs beside the own parts on
+// the others; each sequence by itself would read 64 times as much, 4.3 GB).
 // A batch whose own parts are longer than its prompts is bound by memory: 512 sequences in 8 groups,
-// 1.1 GB, take 204 us, 5.5 TB/s.  Few short prompts are bound by latency: 4 sequences that share 2048
+// 1.1 GB, take 203 us, 5.5 TB/s.  Few short prompts are bound by latency: 4 sequences that share 2048
 // tokens 11.9 us, of which 2.6 go by before the first part begins and 2.5 in the merge; such batches
-// are left to one launch that reads every sequence's pages (8.4 us).
+// are left to one launch that reads every sequence's pages (8.1 us).
 // Kept out, as slower: units of up to 64 rows twice in a tile, each copy with half of a tile's keys
 // (4 x 2048 13.1 us, 37 in 5 groups 31.5); all SMs for both kernels (37 sequences in 5 groups 33 us against 29), units dealt
 // out whole (211 us against 203 for 512 sequences), every role walking along the run for itself (its

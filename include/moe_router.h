@@ -78,6 +78,10 @@ sa_status moe_router(const void* x, const void* w_router, const void* bias, int 
  * favour of the lower index; without a bias it is the logits' own order (within the groups kept).
  * (Scores are known to about 2^-52 here: values that differ by less are ordered as they round.)
  * The weights are computed in fp32 and stored as bf16.
+ * Tokens whose experts are near one another in v take longer; so do biases of many sizes, which leave
+ * less room to the scores (a mask, as -inf, -1e4 or the least fp32 number for some experts, does not,
+ * where as many experts are left as are chosen; 32768 tokens of 256 experts: 30 to 50 us, 1.5 ms with
+ * nothing but tokens that are compared in fp64 throughout).
  *
  *  logits        fp32 (is_fp32 != 0) or bf16 [num_tokens, num_experts], row-major, at least
  *                aligned to their elements (four logits at a time where rows are aligned to that);
