@@ -1350,7 +1350,9 @@ void lora_plan(LoraArgs& a, int sms) {
   // least two steps; else: a step of K for each of a CTA's eight warps, up to 4 parts.
   int pair_splits = 1;
   while (pair_splits < 8 && 2 * pair_splits * a.tiles_m <= sms && 4 * pair_splits <= k_blocks) pair_splits *= 2;
-  // As blocks of K: ranks of half the adapters that a tile of tokens can have.
+  // As blocks of K: ranks of half the adapters that a tile of tokens can have.  (The host knows the resident
+  // ones only: where 2 of 1000 are present, 64 tokens 2880 -> 5120 of rank 16 take 14.7 us instead of 13.8
+  // with 2 resident, 1000 tokens of rank 64 38.2 instead of 33.0.)
   const int most = a.M < kBM ? a.M : kBM;
   const int adapter_blocks = ((a.num_adapters < most ? a.num_adapters : most) * ((a.R + 15) / 16) + 7) / 8;
   // Estimated cycles of tiles of bn columns, by single CTAs, by pairs or by clusters that share K; the
